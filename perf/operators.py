@@ -261,6 +261,11 @@ def _plain_extend(s, q, k, v):
     return [out[valid].bfloat16(), s["pool"]]
 
 
+def _pow2(e):
+    """2^e in 64 bits, put together from its bits: library powers may be off in the last one."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
 def _quantise(x):
     """Codes in [-127, 127] and scale exponents (scale 2^(s - 127)) of blocks of 32 along the last
     axis: the smallest power of two that keeps the largest code at 127 or less, at least 2^-127; a
@@ -270,15 +275,14 @@ def _quantise(x):
     fine = torch.isfinite(top)
     e = torch.frexp(torch.where(fine, top, 1.0))[1] - 7  # top / 2^e is in [64, 128)
     e = torch.where(top == 0, -127, e).clamp(min=-127)
-    e = e + (torch.round(torch.ldexp(torch.where(fine, top, 1.0), -e)) > 127).to(e.dtype)
-    codes = torch.round(torch.ldexp(x, -e[..., None])).to(torch.int8)
-    codes = torch.where(fine[..., None], codes, torch.zeros_like(codes))
+    e = e + (torch.round(torch.where(fine, top, 1.0) * _pow2(-e)) > 127).to(e.dtype)
+    codes = torch.where(fine[..., None], torch.round(x * _pow2(-e)[..., None]), 0.0).to(torch.int8)
     return codes.flatten(-2), torch.where(fine, e + 127, 255).to(torch.uint8)
 
 
 def _restore(codes, scales):
     x = codes.reshape(*codes.shape[:-1], codes.shape[-1] // 32, 32).double()
-    x = torch.ldexp(x, scales.int()[..., None] - 127)
+    x = x * _pow2(scales.int() - 127)[..., None]
     return torch.where(scales[..., None] == 255, math.nan, x).float().flatten(-2)
 
 
@@ -287,15 +291,16 @@ def exact(case, seed):
     s = prepare(case, seed)
     idx = s["idx"].long()
     if case["op"] in ("pack", "unpack"):
-        at, one = s["sidx"].long(), torch.ones((), dtype=torch.float64, device=DEV)
+        at = s["sidx"].long()
+        powers = torch.tensor([2.0 ** e for e in range(-200, 201)], dtype=torch.float64, device=DEV)
         if case["op"] == "unpack":
-            scale = torch.ldexp(one, s["scales"][at].int() - 127).repeat_interleave(32, -1)
+            scale = powers[s["scales"][at].long() - 127 + 200].repeat_interleave(32, -1)
             to = s["pool"].double()
             to[idx] = s["codes"][at].double() * scale
             return to
         to = s["back"].double()
         x = s["pool"][idx].double().unflatten(-1, (D // 32, 32))
-        step = torch.ldexp(one, (torch.floor(torch.log2(x.abs().amax(-1, keepdim=True))) - 6).int())
+        step = powers[torch.floor(torch.log2(x.abs().amax(-1, keepdim=True))).long() - 6 + 200]
         step = torch.where(torch.round(x.abs().amax(-1, keepdim=True) / step) > 127, 2 * step, step)
         to[idx] = (torch.round(x / step) * step).flatten(-2)
         return to
