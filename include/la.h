@@ -342,6 +342,92 @@ la_status la_commit_accepted(const float *inter_states, const int32_t *accept_id
                              int N, int H, int D, la_stream stream);
 
 /*
+ * Gated delta rule -- the linear attention whose update removes what the state already holds for a
+ * key before it writes the new value.  It has no counterpart on the page, whose seg_la it sits next
+ * to: the same pool, slots, packed tokens, flags, streams and errors, so that a model of both kinds
+ * of layers serves from one pool layout.  Per request and value head h, with key head
+ * j = h / (H / Hk), S (D x D, rows k, columns v):
+ *     S <- e^{g_t[h]} S;   u_t = beta_t[h] (v_t[h] - S^T k_t[j]);   S <- S + outer(k_t[j], u_t);
+ *     o_t[h] = (q_t[j] @ S) * D^-0.5
+ * Arguments shared by the three calls:
+ *   q, k          device, bf16 rows of Hk * D elements (head j at columns [j*D, (j+1)*D))
+ *   v             device, bf16 rows of H * D elements
+ *   q_row_stride, k_row_stride, v_row_stride
+ *                 elements from one token's row to the next (0: packed), so that q, k and v may be
+ *                 column ranges of one projection's output; multiples of 8, at least the row's
+ *                 width (LA_ERR_INVALID otherwise; ignored for a single row)
+ *   g             device, fp32 [tokens][H]: the log of the decay, at most 0 (-inf empties the state)
+ *   beta          device, fp32 [tokens][H]: the writing strength, usually in (0, 1)
+ *   state_pool    device, fp32 [num_slots][H][D][D]
+ *   out           device, bf16 [tokens][H*D], packed
+ *   H, Hk         value heads and key heads; H must be a multiple of Hk (LA_ERR_INVALID otherwise)
+ *   qk_l2norm     nonzero: q and k are first divided by sqrt(sum of squares of the head + 1e-6)
+ * A positive g or keys with beta |k|^2 > 2 let a state grow without bound, as the formula says;
+ * nothing is clamped.  All other conventions (alignment, preconditions, device-detected faults,
+ * B = 0) are the ones at the top of this file.  None of the calls needs scratch.
+ */
+
+/*
+ * la_delta_extend -- packed varlen gated delta rule over the pool: for each request, from its slot's
+ * state (prefix_mask[b] nonzero) or from zero, over rows [cu_seqlens[b], cu_seqlens[b+1]), final
+ * state written to its slot (for zero-length requests too).  state_idx, cu_seqlens, prefix_mask,
+ * max_seqlen, B, T as for la_extend; rows of out that belong to no request are left as they were.
+ */
+la_status la_delta_extend(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, int64_t q_row_stride,
+                          int64_t k_row_stride, int64_t v_row_stride, const float *g,
+                          const float *beta, float *state_pool, int num_slots,
+                          const int32_t *state_idx, const int32_t *cu_seqlens,
+                          const uint8_t *prefix_mask, la_bf16 *out, int B, int T, int H, int Hk,
+                          int D, int max_seqlen, int qk_l2norm, la_stream stream);
+
+/*
+ * la_delta_decode -- one token per request (row b of q, k, v, g, beta and out), states updated in
+ * place; fp32 throughout, out rounded to bf16 once.
+ */
+la_status la_delta_decode(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, int64_t q_row_stride,
+                          int64_t k_row_stride, int64_t v_row_stride, const float *g,
+                          const float *beta, float *state_pool, int num_slots,
+                          const int32_t *state_idx, la_bf16 *out, int B, int H, int Hk, int D,
+                          int qk_l2norm, la_stream stream);
+
+/*
+ * la_delta_verify_chain -- N draft tokens per request (rows b*N .. b*N+N-1) as a chain: outputs, and
+ * the state after each token into inter_states, fp32 [B][N][H][D][D].  The pool is only read;
+ * la_commit_accepted moves the accepted token's state into the slot.
+ */
+la_status la_delta_verify_chain(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v,
+                                int64_t q_row_stride, int64_t k_row_stride, int64_t v_row_stride,
+                                const float *g, const float *beta, const float *state_pool,
+                                int num_slots, const int32_t *state_idx, float *inter_states,
+                                la_bf16 *out, int B, int N, int H, int Hk, int D, int qk_l2norm,
+                                la_stream stream);
+
+/*
+ * Packed state store -- pool slots kept at a quarter of their size, for prefix states that wait to be
+ * used again (the snapshots of la_extend_ex, the states of finished or preempted requests).  A row of
+ * a state is D / 32 blocks of 32 values along v; a block is 32 int8 codes in [-127, 127] and one
+ * scale byte s, and stands for code * 2^(s - 127).  s is the smallest for which no code exceeds 127,
+ * at least 0, so a code is the value over a power of two, rounded to the nearest integer (ties to
+ * even): a restored value is off by at most half of 2^(s - 127), at most 1/127 of the block's largest
+ * magnitude, and packing a restored state gives it back bit for bit (-0 comes back as 0).  s is at
+ * most 248 there, so that every code stands for a finite value: magnitudes above 127.5 * 2^121 are held
+ * at code 127.  A block that holds an infinity or a NaN has s = 255 and codes 0, and is restored as NaN.
+ *   codes      device, int8 [entries][H][D][D], 16-byte aligned
+ *   scales     device, uint8 [entries][H][D][D/32], 4-byte aligned
+ *   store_idx  device, int32 [B], each in [0, entries): the entry of request b
+ *   state_idx  device, int32 [B]: its pool slot
+ * Preconditions: the indices of what a call writes (store_idx for pack, state_idx for unpack) are
+ * distinct; those of what it reads may repeat (one packed prefix for several requests).  A slot or an
+ * entry out of range skips that request and is reported by la_poll_error as LA_ERR_DEVICE_INPUT.
+ */
+la_status la_pack_states(const float *state_pool, int num_slots, const int32_t *state_idx,
+                         int8_t *codes, uint8_t *scales, int entries, const int32_t *store_idx, int B,
+                         int H, int D, la_stream stream);
+la_status la_unpack_states(const int8_t *codes, const uint8_t *scales, int entries,
+                           const int32_t *store_idx, float *state_pool, int num_slots,
+                           const int32_t *state_idx, int B, int H, int D, la_stream stream);
+
+/*
  * la_poll_error -- synchronise `stream` and then the whole current device (every stream on it),
  * then read and clear the device's error word.  The word is shared by all of the library's
  * kernels on the device, whatever stream they run on, so the device-wide synchronisation makes

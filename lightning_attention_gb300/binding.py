@@ -27,7 +27,8 @@ STATUS = {0: "LA_OK", 1: "LA_ERR_INVALID", 2: "LA_ERR_UNSUPPORTED", 3: "LA_ERR_C
 EXPORTS = ("la_slopes", "la_extend", "la_extend_ex", "la_extend_workspace_size", "la_decode",
            "la_verify_chain", "la_verify_tree", "la_commit_accepted", "la_poll_error", "la_status_string",
            "la_set_wait_limit", "la_set_column_split", "la_set_persistent", "la_set_balanced", "la_extend_noalloc", "la_extend_gqa",
-           "la_extend_gqa_workspace_size", "la_decode_gqa")
+           "la_extend_gqa_workspace_size", "la_decode_gqa", "la_delta_extend", "la_delta_decode",
+           "la_delta_verify_chain", "la_pack_states", "la_unpack_states")
 
 
 class LAError(RuntimeError):
@@ -93,6 +94,19 @@ def load():
         lib.la_extend_gqa_workspace_size.restype = ip
         lib.la_decode_gqa.argtypes = [vp, vp, vp, vp, vp, ip, vp, vp, ip, ip, ip, ip, vp]
         lib.la_decode_gqa.restype = ip
+        lib.la_delta_extend.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, vp, ip, vp, vp, vp, vp, ip,
+                                        ip, ip, ip, ip, ip, ip, vp]
+        lib.la_delta_extend.restype = ip
+        lib.la_delta_decode.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, vp, ip, vp, vp, ip, ip, ip,
+                                        ip, ip, vp]
+        lib.la_delta_decode.restype = ip
+        lib.la_delta_verify_chain.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, vp, ip, vp, vp, vp,
+                                              ip, ip, ip, ip, ip, ip, vp]
+        lib.la_delta_verify_chain.restype = ip
+        lib.la_pack_states.argtypes = [vp, ip, vp, vp, vp, ip, vp, ip, ip, ip, vp]
+        lib.la_pack_states.restype = ip
+        lib.la_unpack_states.argtypes = [vp, vp, ip, vp, vp, ip, vp, ip, ip, ip, vp]
+        lib.la_unpack_states.restype = ip
         _lib = lib
         return lib
 
@@ -479,3 +493,150 @@ def decode_gqa(q, k, v, slopes_, state_pool, state_idx, out=None):
                                   _stream_handle(dev))
     _check("la_decode_gqa", st)
     return out
+
+
+def _need_rows(t, name: str, device, rows: int, width: int) -> int:
+    """Row stride (in elements) of a bf16 [rows, width] tensor whose rows are contiguous but may lie
+    further apart, as the columns of a wider projection do."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if tuple(t.shape) != (rows, width):
+        raise ValueError(f"{name} must have shape {(rows, width)}, got {tuple(t.shape)}")
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} rows must be contiguous")
+    if rows <= 1:
+        return width
+    if t.stride(0) < width or t.stride(0) % 8 != 0:
+        raise ValueError(f"{name} rows must lie a multiple of 8 elements, at least {width}, apart; "
+                         f"got {t.stride(0)}")
+    return t.stride(0)
+
+
+def _need_pool(state_pool, dev):
+    if not isinstance(state_pool, torch.Tensor) or state_pool.dim() != 4:
+        raise TypeError("state_pool must be an fp32 [S, H, D, D] tensor")
+    _need(state_pool, "state_pool", torch.float32, dev, tuple(state_pool.shape[:3]) + (state_pool.shape[2],))
+    return state_pool.shape[:3]
+
+
+def _delta_args(q, k, v, g, beta, state_pool, state_idx, out, tokens: int | None):
+    """Checks shared by the delta calls: (tokens, B, H, Hk, D, row strides, out)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 2:
+        raise TypeError("q must be a bf16 [tokens, Hk*D] tensor")
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError(f"q must be on a CUDA device, got {dev}")
+    _, H, D = _need_pool(state_pool, dev)
+    if not isinstance(state_idx, torch.Tensor) or state_idx.dim() != 1:
+        raise TypeError("state_idx must be an int32 [B] tensor")
+    B = state_idx.shape[0]
+    rows = q.shape[0] if tokens is None else B * tokens
+    if D < 1 or q.shape[1] % D != 0:
+        raise ValueError(f"q must have a multiple of {D} columns, got {q.shape[1]}")
+    Hk = q.shape[1] // D
+    strides = (_need_rows(q, "q", dev, rows, Hk * D), _need_rows(k, "k", dev, rows, Hk * D),
+               _need_rows(v, "v", dev, rows, H * D))
+    _need(g, "g", torch.float32, dev, (rows, H))
+    _need(beta, "beta", torch.float32, dev, (rows, H))
+    _need(state_idx, "state_idx", torch.int32, dev, (B,))
+    if out is None:
+        out = torch.empty((rows, H * D), dtype=torch.bfloat16, device=dev)
+    _need(out, "out", torch.bfloat16, dev, (rows, H * D))
+    return rows, B, H, Hk, D, strides, out
+
+
+def delta_extend(q, k, v, g, beta, state_pool, state_idx, cu_seqlens, prefix_mask, out=None,
+                 max_seqlen: int | None = None, qk_l2norm: bool = False):
+    """Packed varlen gated delta rule (la_delta_extend).  q, k: bf16 [T, Hk*D]; v: bf16 [T, H*D]
+    (rows may be strided: column ranges of one projection); g (log decay) and beta: fp32 [T, H];
+    state_pool fp32 [S, H, D, D] updated in place; returns out bf16 [T, H*D].  Value head h reads key
+    head h // (H / Hk); qk_l2norm divides q and k by their head's 2-norm first."""
+    T, B, H, Hk, D, rs, out = _delta_args(q, k, v, g, beta, state_pool, state_idx, out, None)
+    dev = q.device
+    _need(cu_seqlens, "cu_seqlens", torch.int32, dev, (B + 1,))
+    _need(prefix_mask, "prefix_mask", torch.uint8, dev, (B,))
+    if max_seqlen is None:
+        max_seqlen = T
+    with _on(dev):
+        st = load().la_delta_extend(_ptr(q), _ptr(k), _ptr(v), *rs, _ptr(g), _ptr(beta),
+                                    _ptr(state_pool), state_pool.shape[0], _ptr(state_idx),
+                                    _ptr(cu_seqlens), _ptr(prefix_mask), _ptr(out), B, T, H, Hk, D,
+                                    int(max_seqlen), int(bool(qk_l2norm)), _stream_handle(dev))
+    _check("la_delta_extend", st)
+    return out
+
+
+def delta_decode(q, k, v, g, beta, state_pool, state_idx, out=None, qk_l2norm: bool = False):
+    """One-token gated delta rule (la_delta_decode): q, k bf16 [B, Hk*D]; v bf16 [B, H*D]; g, beta
+    fp32 [B, H]; pool updated in place; returns out bf16 [B, H*D]."""
+    _, B, H, Hk, D, rs, out = _delta_args(q, k, v, g, beta, state_pool, state_idx, out, 1)
+    dev = q.device
+    with _on(dev):
+        st = load().la_delta_decode(_ptr(q), _ptr(k), _ptr(v), *rs, _ptr(g), _ptr(beta),
+                                    _ptr(state_pool), state_pool.shape[0], _ptr(state_idx), _ptr(out),
+                                    B, H, Hk, D, int(bool(qk_l2norm)), _stream_handle(dev))
+    _check("la_delta_decode", st)
+    return out
+
+
+def delta_verify_chain(q, k, v, g, beta, state_pool, state_idx, N: int, inter_states=None, out=None,
+                       qk_l2norm: bool = False):
+    """Chain verify under the gated delta rule (la_delta_verify_chain).  q, k: bf16 [B*N, Hk*D]; v:
+    bf16 [B*N, H*D]; g, beta: fp32 [B*N, H]; returns (out, inter_states) with inter_states fp32
+    [B, N, H, D, D], as commit_accepted takes them; the pool is not modified."""
+    if N < 1:
+        raise ValueError(f"N must be at least 1, got {N}")
+    _, B, H, Hk, D, rs, out = _delta_args(q, k, v, g, beta, state_pool, state_idx, out, int(N))
+    dev = q.device
+    if inter_states is None:
+        inter_states = torch.empty((B, N, H, D, D), dtype=torch.float32, device=dev)
+    _need(inter_states, "inter_states", torch.float32, dev, (B, N, H, D, D))
+    with _on(dev):
+        st = load().la_delta_verify_chain(_ptr(q), _ptr(k), _ptr(v), *rs, _ptr(g), _ptr(beta),
+                                          _ptr(state_pool), state_pool.shape[0], _ptr(state_idx),
+                                          _ptr(inter_states), _ptr(out), B, int(N), H, Hk, D,
+                                          int(bool(qk_l2norm)), _stream_handle(dev))
+    _check("la_delta_verify_chain", st)
+    return out, inter_states
+
+
+def _pack_args(state_pool, state_idx, codes, scales, store_idx):
+    if not isinstance(state_pool, torch.Tensor):
+        raise TypeError("state_pool must be an fp32 [S, H, D, D] tensor")
+    dev = state_pool.device
+    if dev.type != "cuda":
+        raise ValueError(f"state_pool must be on a CUDA device, got {dev}")
+    num_slots, H, D = _need_pool(state_pool, dev)
+    if not isinstance(state_idx, torch.Tensor) or not isinstance(codes, torch.Tensor):
+        raise TypeError("state_idx and codes must be torch.Tensors")
+    if state_idx.dim() != 1 or codes.dim() != 4:
+        raise ValueError("state_idx must have shape [B] and codes [E, H, D, D]")
+    B, E = state_idx.shape[0], codes.shape[0]
+    _need(state_idx, "state_idx", torch.int32, dev, (B,))
+    _need(store_idx, "store_idx", torch.int32, dev, (B,))
+    _need(codes, "codes", torch.int8, dev, (E, H, D, D))
+    _need(scales, "scales", torch.uint8, dev, (E, H, D, D // 32))
+    return dev, num_slots, E, B, H, D
+
+
+def pack_states(state_pool, state_idx, codes, scales, store_idx) -> None:
+    """Pack pool slots into the 8-bit state store (la_pack_states): slot state_idx[b] into entry
+    store_idx[b] of codes (int8 [E, H, D, D]) and scales (uint8 [E, H, D, D // 32])."""
+    dev, num_slots, E, B, H, D = _pack_args(state_pool, state_idx, codes, scales, store_idx)
+    with _on(dev):
+        st = load().la_pack_states(_ptr(state_pool), num_slots, _ptr(state_idx), _ptr(codes),
+                                   _ptr(scales), E, _ptr(store_idx), B, H, D, _stream_handle(dev))
+    _check("la_pack_states", st)
+
+
+def unpack_states(codes, scales, store_idx, state_pool, state_idx) -> None:
+    """Restore entries of the 8-bit state store into pool slots (la_unpack_states)."""
+    dev, num_slots, E, B, H, D = _pack_args(state_pool, state_idx, codes, scales, store_idx)
+    with _on(dev):
+        st = load().la_unpack_states(_ptr(codes), _ptr(scales), E, _ptr(store_idx), _ptr(state_pool),
+                                     num_slots, _ptr(state_idx), B, H, D, _stream_handle(dev))
+    _check("la_unpack_states", st)

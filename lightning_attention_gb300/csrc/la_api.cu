@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "la.h"
+#include "la_delta.h"
 #include "la_extend_bal.h"
 #include "la_internal.h"
 
@@ -523,6 +524,184 @@ la_status la_extend_workspace_size(int B, int T, int H, int D, int max_seqlen, s
     if (st != LA_OK) return st;
     *bytes = (size_t)(scr.full + scr.order + scr.recs + scr.bal);
     return LA_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Row stride of a token row of `width` elements: 0 means packed; rows may not overlap and start on
+// 16-byte boundaries.  The stride of a single row does not matter.
+bool row_stride_ok(int64_t *rs, long long rows, long long width) {
+    if (*rs == 0 || (rows <= 1 && *rs > 0)) *rs = width;
+    return *rs >= width && *rs % 8 == 0;
+}
+
+// The checks and the marshalling that the delta entry points share.  `tokens` is their number of
+// token rows; work == false: nothing to launch.
+la_status delta_params(la::DeltaParams *p, bool *work, const la_bf16 *q, const la_bf16 *k,
+                       const la_bf16 *v, int64_t q_rs, int64_t k_rs, int64_t v_rs, const float *g,
+                       const float *beta, const float *state_pool, int num_slots,
+                       const int32_t *state_idx, la_bf16 *out, int B, long long tokens, int H,
+                       int Hk, int D, int qk_l2norm) {
+    *work = false;
+    if (B < 0 || tokens < 0 || H < 1 || Hk < 1 || H % Hk != 0 || D < 1 || num_slots < 1)
+        return LA_ERR_INVALID;
+    if (D != la::kHeadDim) return LA_ERR_UNSUPPORTED;
+    if (tokens > 0x7fffffffLL) return LA_ERR_INVALID;
+    if (!row_stride_ok(&q_rs, tokens, (long long)Hk * D) ||
+        !row_stride_ok(&k_rs, tokens, (long long)Hk * D) ||
+        !row_stride_ok(&v_rs, tokens, (long long)H * D))
+        return LA_ERR_INVALID;
+    const long long widest = std::max<long long>(std::max<long long>(q_rs, k_rs), v_rs);
+    if (widest >= (1ll << 38) || tokens * widest >= (1ll << 40)) return LA_ERR_UNSUPPORTED;
+    // the grids have B * H CTAs, or four times as many
+    if ((long long)B * H > 0x1fffffffLL) return LA_ERR_UNSUPPORTED;
+    if (B == 0) return LA_OK;
+    if (!state_pool || !state_idx) return LA_ERR_INVALID;
+    if (tokens > 0 && (!q || !k || !v || !g || !beta || !out)) return LA_ERR_INVALID;
+    if (!aligned16(state_pool) || !aligned4(state_idx)) return LA_ERR_INVALID;
+    if (tokens > 0 && (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) ||
+                       !aligned4(g) || !aligned4(beta)))
+        return LA_ERR_INVALID;
+    *p = la::DeltaParams{};
+    p->q = reinterpret_cast<const __nv_bfloat16 *>(q);
+    p->k = reinterpret_cast<const __nv_bfloat16 *>(k);
+    p->v = reinterpret_cast<const __nv_bfloat16 *>(v);
+    p->q_rs = q_rs;
+    p->k_rs = k_rs;
+    p->v_rs = v_rs;
+    p->g = g;
+    p->beta = beta;
+    p->pool = const_cast<float *>(state_pool);
+    p->state_idx = state_idx;
+    p->out = reinterpret_cast<__nv_bfloat16 *>(out);
+    p->B = B;
+    p->T = (int)tokens;
+    p->H = H;
+    p->Hk = Hk;
+    p->N = 1;
+    p->group = H / Hk;
+    p->num_slots = num_slots;
+    p->l2norm = qk_l2norm != 0;
+    const unsigned long long us = g_wait_limit.load();
+    p->wait_limit_ns = (us == 0 ? kDefaultWaitLimitUs : us) * 1000ull;
+    *work = true;
+    return LA_OK;
+}
+
+la_status pack_params(la::PackParams *p, bool *work, const float *state_pool, int num_slots,
+                      const int32_t *state_idx, const int8_t *codes, const uint8_t *scales,
+                      int entries, const int32_t *store_idx, int B, int H, int D) {
+    *work = false;
+    if (B < 0 || H < 1 || D < 1 || num_slots < 1 || entries < 1) return LA_ERR_INVALID;
+    if (D != la::kHeadDim) return LA_ERR_UNSUPPORTED;
+    if ((long long)B * H > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
+    if (B == 0) return LA_OK;
+    if (!state_pool || !state_idx || !codes || !scales || !store_idx) return LA_ERR_INVALID;
+    if (!aligned16(state_pool) || !aligned16(codes) || !aligned4(scales) || !aligned4(state_idx) ||
+        !aligned4(store_idx))
+        return LA_ERR_INVALID;
+    *p = la::PackParams{};
+    p->pool = const_cast<float *>(state_pool);
+    p->state_idx = state_idx;
+    p->codes = const_cast<int8_t *>(codes);
+    p->scales = const_cast<uint8_t *>(scales);
+    p->store_idx = store_idx;
+    p->B = B;
+    p->H = H;
+    p->num_slots = num_slots;
+    p->entries = entries;
+    const la_status st = error_word_ptr(&p->err);
+    if (st != LA_OK) return st;
+    *work = true;
+    return LA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+la_status la_delta_extend(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, int64_t q_row_stride,
+                          int64_t k_row_stride, int64_t v_row_stride, const float *g,
+                          const float *beta, float *state_pool, int num_slots,
+                          const int32_t *state_idx, const int32_t *cu_seqlens,
+                          const uint8_t *prefix_mask, la_bf16 *out, int B, int T, int H, int Hk,
+                          int D, int max_seqlen, int qk_l2norm, la_stream stream) {
+    la::DeltaParams p;
+    bool work;
+    if (max_seqlen < 0) return LA_ERR_INVALID;
+    la_status st = delta_params(&p, &work, q, k, v, q_row_stride, k_row_stride, v_row_stride, g, beta,
+                                state_pool, num_slots, state_idx, out, B, T, H, Hk, D, qk_l2norm);
+    if (st != LA_OK || !work) return st;
+    if (!cu_seqlens || !prefix_mask || !aligned4(cu_seqlens)) return LA_ERR_INVALID;
+    p.cu_seqlens = cu_seqlens;
+    p.prefix_mask = prefix_mask;
+    p.max_seqlen = max_seqlen;
+    int sms = 0;
+    if ((st = error_word_ptr(&p.err)) != LA_OK || (st = num_sms(&sms)) != LA_OK) return st;
+    return launch_status(la::launch_delta_recurrent(la::DELTA_EXTEND, p, sms,
+                                                    static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_delta_decode(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, int64_t q_row_stride,
+                          int64_t k_row_stride, int64_t v_row_stride, const float *g,
+                          const float *beta, float *state_pool, int num_slots,
+                          const int32_t *state_idx, la_bf16 *out, int B, int H, int Hk, int D,
+                          int qk_l2norm, la_stream stream) {
+    la::DeltaParams p;
+    bool work;
+    la_status st = delta_params(&p, &work, q, k, v, q_row_stride, k_row_stride, v_row_stride, g, beta,
+                                state_pool, num_slots, state_idx, out, B, B, H, Hk, D, qk_l2norm);
+    if (st != LA_OK || !work) return st;
+    int sms = 0;
+    if ((st = error_word_ptr(&p.err)) != LA_OK || (st = num_sms(&sms)) != LA_OK) return st;
+    return launch_status(la::launch_delta_recurrent(la::DELTA_DECODE, p, sms,
+                                                    static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_delta_verify_chain(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v,
+                                int64_t q_row_stride, int64_t k_row_stride, int64_t v_row_stride,
+                                const float *g, const float *beta, const float *state_pool,
+                                int num_slots, const int32_t *state_idx, float *inter_states,
+                                la_bf16 *out, int B, int N, int H, int Hk, int D, int qk_l2norm,
+                                la_stream stream) {
+    la::DeltaParams p;
+    bool work;
+    if (N < 1) return LA_ERR_INVALID;
+    la_status st = delta_params(&p, &work, q, k, v, q_row_stride, k_row_stride, v_row_stride, g, beta,
+                                state_pool, num_slots, state_idx, out, B, (long long)B * N, H, Hk, D,
+                                qk_l2norm);
+    if (st != LA_OK || !work) return st;
+    if (!inter_states || !aligned16(inter_states)) return LA_ERR_INVALID;
+    p.N = N;
+    p.inter = inter_states;
+    int sms = 0;
+    if ((st = error_word_ptr(&p.err)) != LA_OK || (st = num_sms(&sms)) != LA_OK) return st;
+    return launch_status(la::launch_delta_recurrent(la::DELTA_VERIFY, p, sms,
+                                                    static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_pack_states(const float *state_pool, int num_slots, const int32_t *state_idx,
+                         int8_t *codes, uint8_t *scales, int entries, const int32_t *store_idx, int B,
+                         int H, int D, la_stream stream) {
+    la::PackParams p;
+    bool work;
+    const la_status st = pack_params(&p, &work, state_pool, num_slots, state_idx, codes, scales,
+                                     entries, store_idx, B, H, D);
+    if (st != LA_OK || !work) return st;
+    return launch_status(la::launch_pack_states(p, static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_unpack_states(const int8_t *codes, const uint8_t *scales, int entries,
+                           const int32_t *store_idx, float *state_pool, int num_slots,
+                           const int32_t *state_idx, int B, int H, int D, la_stream stream) {
+    la::PackParams p;
+    bool work;
+    const la_status st = pack_params(&p, &work, state_pool, num_slots, state_idx, codes, scales,
+                                     entries, store_idx, B, H, D);
+    if (st != LA_OK || !work) return st;
+    return launch_status(la::launch_unpack_states(p, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
