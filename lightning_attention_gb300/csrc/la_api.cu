@@ -640,8 +640,7 @@ la_status la_delta_extend(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, 
     p.max_seqlen = max_seqlen;
     int sms = 0;
     if ((st = error_word_ptr(&p.err)) != LA_OK || (st = num_sms(&sms)) != LA_OK) return st;
-    return launch_status(la::launch_delta_recurrent(la::DELTA_EXTEND, p, sms,
-                                                    static_cast<cudaStream_t>(stream)));
+    return launch_status(la::launch_delta_extend(p, sms, static_cast<cudaStream_t>(stream)));
 }
 
 la_status la_delta_decode(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, int64_t q_row_stride,
