@@ -364,7 +364,7 @@ la_status la_commit_accepted(const float *inter_states, const int32_t *accept_id
  *   qk_l2norm     nonzero: q and k are first divided by sqrt(sum of squares of the head + 1e-6)
  * A positive g or keys with beta |k|^2 > 2 let a state grow without bound, as the formula says;
  * nothing is clamped.  All other conventions (alignment, preconditions, device-detected faults,
- * B = 0) are the ones at the top of this file.  None of the calls needs scratch.
+ * B = 0) are the ones at the top of this file.
  */
 
 /*
@@ -372,13 +372,29 @@ la_status la_commit_accepted(const float *inter_states, const int32_t *accept_id
  * state (prefix_mask[b] nonzero) or from zero, over rows [cu_seqlens[b], cu_seqlens[b+1]), final
  * state written to its slot (for zero-length requests too).  state_idx, cu_seqlens, prefix_mask,
  * max_seqlen, B, T as for la_extend; rows of out that belong to no request are left as they were.
+ *   workspace        device scratch, 16-byte aligned, of at least la_delta_extend_workspace_size()
+ *                    bytes (LA_ERR_INVALID otherwise; may be NULL when T = 0): about half of what q, k,
+ *                    v and out take together.  Contents do not matter on entry and are garbage on exit;
+ *                    calls that share one must not overlap on the GPU.
+ * Two launches: one forms, for every chunk of 64 tokens at once, what depends on no state; the other runs
+ * the chunks of each (request, head) in turn.  Numerics: bf16 products with fp32 accumulation; each
+ * operand the kernels compute is a bf16 pair hi + lo (off by at most 2^-16); states are kept and updated
+ * in fp32; out is rounded to bf16 once.  A NaN or an infinity in a request's inputs may reach all of that
+ * request's outputs and its state, and nothing of any other request.
  */
 la_status la_delta_extend(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, int64_t q_row_stride,
                           int64_t k_row_stride, int64_t v_row_stride, const float *g,
                           const float *beta, float *state_pool, int num_slots,
                           const int32_t *state_idx, const int32_t *cu_seqlens,
                           const uint8_t *prefix_mask, la_bf16 *out, int B, int T, int H, int Hk,
-                          int D, int max_seqlen, int qk_l2norm, la_stream stream);
+                          int D, int max_seqlen, int qk_l2norm, void *workspace,
+                          size_t workspace_bytes, la_stream stream);
+
+/*
+ * la_delta_extend_workspace_size -- bytes of device scratch la_delta_extend needs for a batch of B
+ * requests and T tokens.  Host only.  LA_ERR_INVALID for bad sizes or bytes == NULL.
+ */
+la_status la_delta_extend_workspace_size(int B, int T, int H, int D, size_t *bytes);
 
 /*
  * la_delta_decode -- one token per request (row b of q, k, v, g, beta and out), states updated in

@@ -27,7 +27,8 @@ STATUS = {0: "LA_OK", 1: "LA_ERR_INVALID", 2: "LA_ERR_UNSUPPORTED", 3: "LA_ERR_C
 EXPORTS = ("la_slopes", "la_extend", "la_extend_ex", "la_extend_workspace_size", "la_decode",
            "la_verify_chain", "la_verify_tree", "la_commit_accepted", "la_poll_error", "la_status_string",
            "la_set_wait_limit", "la_set_column_split", "la_set_persistent", "la_set_balanced", "la_extend_noalloc", "la_extend_gqa",
-           "la_extend_gqa_workspace_size", "la_decode_gqa", "la_delta_extend", "la_delta_decode",
+           "la_extend_gqa_workspace_size", "la_decode_gqa", "la_delta_extend",
+           "la_delta_extend_workspace_size", "la_delta_decode",
            "la_delta_verify_chain", "la_pack_states", "la_unpack_states")
 
 
@@ -95,8 +96,10 @@ def load():
         lib.la_decode_gqa.argtypes = [vp, vp, vp, vp, vp, ip, vp, vp, ip, ip, ip, ip, vp]
         lib.la_decode_gqa.restype = ip
         lib.la_delta_extend.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, vp, ip, vp, vp, vp, vp, ip,
-                                        ip, ip, ip, ip, ip, ip, vp]
+                                        ip, ip, ip, ip, ip, ip, vp, sz, vp]
         lib.la_delta_extend.restype = ip
+        lib.la_delta_extend_workspace_size.argtypes = [ip, ip, ip, ip, ctypes.POINTER(sz)]
+        lib.la_delta_extend_workspace_size.restype = ip
         lib.la_delta_decode.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, vp, ip, vp, vp, ip, ip, ip,
                                         ip, ip, vp]
         lib.la_delta_decode.restype = ip
@@ -549,8 +552,16 @@ def _delta_args(q, k, v, g, beta, state_pool, state_idx, out, tokens: int | None
     return rows, B, H, Hk, D, strides, out
 
 
+def delta_extend_workspace_size(B: int, T: int, H: int, D: int) -> int:
+    """Bytes of scratch la_delta_extend needs for a batch of B requests and T tokens."""
+    n = ctypes.c_size_t(0)
+    _check("la_delta_extend_workspace_size",
+           load().la_delta_extend_workspace_size(B, T, H, D, ctypes.byref(n)))
+    return int(n.value)
+
+
 def delta_extend(q, k, v, g, beta, state_pool, state_idx, cu_seqlens, prefix_mask, out=None,
-                 max_seqlen: int | None = None, qk_l2norm: bool = False):
+                 max_seqlen: int | None = None, qk_l2norm: bool = False, workspace=None):
     """Packed varlen gated delta rule (la_delta_extend).  q, k: bf16 [T, Hk*D]; v: bf16 [T, H*D]
     (rows may be strided: column ranges of one projection); g (log decay) and beta: fp32 [T, H];
     state_pool fp32 [S, H, D, D] updated in place; returns out bf16 [T, H*D].  Value head h reads key
@@ -561,11 +572,15 @@ def delta_extend(q, k, v, g, beta, state_pool, state_idx, cu_seqlens, prefix_mas
     _need(prefix_mask, "prefix_mask", torch.uint8, dev, (B,))
     if max_seqlen is None:
         max_seqlen = T
+    if workspace is None:
+        workspace = torch.empty(delta_extend_workspace_size(B, T, H, D), dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", torch.uint8, dev)
     with _on(dev):
         st = load().la_delta_extend(_ptr(q), _ptr(k), _ptr(v), *rs, _ptr(g), _ptr(beta),
                                     _ptr(state_pool), state_pool.shape[0], _ptr(state_idx),
                                     _ptr(cu_seqlens), _ptr(prefix_mask), _ptr(out), B, T, H, Hk, D,
-                                    int(max_seqlen), int(bool(qk_l2norm)), _stream_handle(dev))
+                                    int(max_seqlen), int(bool(qk_l2norm)), _ptr(workspace),
+                                    workspace.numel(), _stream_handle(dev))
     _check("la_delta_extend", st)
     return out
 

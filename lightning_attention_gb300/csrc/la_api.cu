@@ -555,8 +555,8 @@ la_status delta_params(la::DeltaParams *p, bool *work, const la_bf16 *q, const l
         return LA_ERR_INVALID;
     const long long widest = std::max<long long>(std::max<long long>(q_rs, k_rs), v_rs);
     if (widest >= (1ll << 38) || tokens * widest >= (1ll << 40)) return LA_ERR_UNSUPPORTED;
-    // the grids have B * H CTAs, or four times as many
-    if ((long long)B * H > 0x1fffffffLL) return LA_ERR_UNSUPPORTED;
+    // the grids have B * H CTAs, four times as many, or one per chunk and head
+    if ((long long)B * H > 0x1fffffffLL || (tokens / 64 + B) * H > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
     if (B == 0) return LA_OK;
     if (!state_pool || !state_idx) return LA_ERR_INVALID;
     if (tokens > 0 && (!q || !k || !v || !g || !beta || !out)) return LA_ERR_INVALID;
@@ -627,7 +627,8 @@ la_status la_delta_extend(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, 
                           const float *beta, float *state_pool, int num_slots,
                           const int32_t *state_idx, const int32_t *cu_seqlens,
                           const uint8_t *prefix_mask, la_bf16 *out, int B, int T, int H, int Hk,
-                          int D, int max_seqlen, int qk_l2norm, la_stream stream) {
+                          int D, int max_seqlen, int qk_l2norm, void *workspace,
+                          size_t workspace_bytes, la_stream stream) {
     la::DeltaParams p;
     bool work;
     if (max_seqlen < 0) return LA_ERR_INVALID;
@@ -635,12 +636,21 @@ la_status la_delta_extend(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, 
                                 state_pool, num_slots, state_idx, out, B, T, H, Hk, D, qk_l2norm);
     if (st != LA_OK || !work) return st;
     if (!cu_seqlens || !prefix_mask || !aligned4(cu_seqlens)) return LA_ERR_INVALID;
+    const unsigned long long need = la::delta_scratch_bytes(B, T, H);
+    if (need > 0 && (!workspace || !aligned16(workspace) || (unsigned long long)workspace_bytes < need))
+        return LA_ERR_INVALID;
     p.cu_seqlens = cu_seqlens;
     p.prefix_mask = prefix_mask;
     p.max_seqlen = max_seqlen;
-    int sms = 0;
-    if ((st = error_word_ptr(&p.err)) != LA_OK || (st = num_sms(&sms)) != LA_OK) return st;
-    return launch_status(la::launch_delta_extend(p, sms, static_cast<cudaStream_t>(stream)));
+    if ((st = error_word_ptr(&p.err)) != LA_OK) return st;
+    return launch_status(la::launch_delta_extend(p, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_delta_extend_workspace_size(int B, int T, int H, int D, size_t *bytes) {
+    if (B < 0 || T < 0 || H < 1 || D < 1 || bytes == nullptr) return LA_ERR_INVALID;
+    if (D != la::kHeadDim) return LA_ERR_UNSUPPORTED;
+    *bytes = (size_t)la::delta_scratch_bytes(B, T, H);
+    return LA_OK;
 }
 
 la_status la_delta_decode(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, int64_t q_row_stride,

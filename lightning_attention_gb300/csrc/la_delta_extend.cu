@@ -1,5 +1,5 @@
 // la_delta_extend.cu -- chunked gated delta rule on the 5th-generation tensor cores, one CTA per
-// (request, value head) or per half of its value columns.
+// (request, value head).
 //
 // Per request and head, token by token: S <- e^{g} S; u = beta (v - S^T k); S <- S + k u^T;
 // o = D^-0.5 S^T q (q, k divided by their 2-norms first if asked).  Over a chunk of C = 64 tokens with
@@ -15,27 +15,32 @@
 // Every exponent is formed as a difference of sums that are exact in fixed point, so that steep
 // decays lose nothing; factors are at most 1.
 //
-// Stacked operands.  K and Q of a chunk share one [128][128] tile, interleaved by 16 rows (rows 32 a ..
-// + 15: tokens 16 a .. of K, the next 16 the same tokens of Q), so that every product has M = 128: an
-// M = 64 or N = 64 tcgen05.mma costs about what the full one does.  One product of the tile with its own
-// transpose gives K K^T, Q K^T and, on its diagonal, the squared norms; [T'; P T] is stacked the same
-// way, so that T' R and P T R are one product, and the output needs no product after U.
+// Two kernels.  T and P T of a chunk depend on nothing before it, so a first kernel forms them for all
+// chunks at once (delta_t_kernel, a CTA of four warps per chunk and head), with the chunk's coefficients,
+// into the workspace; the second runs the chain over the chunks, one CTA per (request, head)
+// (delta_extend_kernel).  One kernel with T warps beside the chain took 393 us on 8 requests of 512-4096
+// tokens x 16 heads: while tcgen05.mma instructions stream, warp-level MMAs are starved and a shared-memory
+// load takes about 280 cycles, so T (11,000 cycles a chunk) held the chain up.
 //
-// Precision.  Products run in bf16 with fp32 accumulation.  K, Q are used as loaded; the operands that
-// are computed (S, R, T', P T, U) are bf16 pairs hi + lo, off by at most 2^-16 and about a sixth of that
-// in the mean; U takes R itself in fp32 and only T' R through pairs; the state stays in fp32
-// registers and is never accumulated in tensor memory.
+// The chain is computed transposed: lanes of tensor memory are the 128 value columns.
+//   X^T = S^T [K; Q]^T,   [U; O']^T = R^T [T'; P T]^T,   dS^T = U^T K
+// so the three operands that it computes (S, R, U) are the A operands, which a tcgen05.mma takes from
+// tensor memory: a warp converts its lanes where they lie, without a trip through shared memory, and the
+// B operands (the stacked [K; Q] tile, the stacked [T'; P T] tile, K) come in by TMA ahead of the chain.
+// The stacking keeps every product at M = N = 128 (65 cycles an instruction; one of N = 64 takes 45-50).
+// P T makes the output a product with R, so nothing of it waits for U.
 //
-// Roles (512 threads, one CTA per SM):
-//   warps 0-3   T: per chunk the gate sums and norms, A and P from tensor memory, T by blocks of 16
-//               (diagonal blocks by substitution in fp32, the others with warp-level MMAs from bf16
-//               pairs), P T; a chunk ahead of the rest.
-//   warps 4-11  E: the state (32 k rows x 64 v columns a warp) and the passes R, U, O and S.
-//   warp 12     TMA producer; warp 13 tensor-memory owner and MMA issuer;
-//   warp 14     zeroes the tile rows past the end of the request's last chunk (they hold the next
-//               request's tokens, and 0 x NaN is NaN).
-// Per chunk the chain is X -> R -> T' R -> U -> K^T U -> S; the product for the next chunk's T runs under
-// R, the output pass under K^T U.
+// Precision.  Products run in bf16 with fp32 accumulation.  K and Q are used as loaded; the operands
+// that are computed (S, R, T', P T, U) are bf16 pairs hi + lo, off by at most 2^-16 and about a sixth of
+// that in the mean; U takes R itself in fp32 and only T' R through pairs; the state stays in fp32
+// registers and is never accumulated in tensor memory (which does not round to nearest).
+//
+// Roles of the chain kernel (352 threads, one CTA per SM):
+//   warps 0-7   E: the state (32 v rows x 64 k columns a warp) and the passes R, U, O and S;
+//   warp 8      TMA producer; warp 9 tensor-memory owner and MMA issuer;
+//   warp 10     zeroes the K rows past the end of the request's last chunk (they hold the next
+//               request's keys, and 0 x NaN is NaN).
+// Per chunk the chain is X -> R -> T' R -> U -> U^T K -> S; the output pass runs under U^T K.
 //
 // Every wait is an mbarrier wait with a deadline; one that runs out sets the error word and an abort flag
 // that ends every role, then the CTA waits for its copies and MMAs, frees tensor memory and exits.
@@ -54,60 +59,64 @@ namespace {
 using namespace sm100;
 
 constexpr int C = 64;  // tokens of a chunk
-constexpr int kTWarps = 4, kEWarps = 8;
-constexpr int kProducerWarp = 12, kMmaWarp = 13, kFixWarp = 14;
-constexpr int kThreads = 512;
-// registers per thread of the roles: 64 + 128 + 2 x 160 = 4 x 128, the launch's share
-constexpr int kRegsT = 128, kRegsE = 160, kRegsRest = 64;
-static_assert(kRegsT + 2 * kRegsE + kRegsRest <= 512, "register split");
+constexpr int kEWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kFixWarp = 10;
+constexpr int kThreads = 352;
+constexpr int kTThreads = 128;
 constexpr float kScale = 0.08838834764831845f;  // 128^-0.5
 
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t TM_X = 0, TM_Y = 128, TM_A = 256, TM_D = 384;
+// The operands S, R and U are kept per k-step (16 values of the contraction) as 8 columns of hi parts,
+// two to a column, and 8 of lo parts.  X: [K | Q] tokens, R replaces the K part 16 tokens by 16; Y:
+// [U | O'], U likewise.
+constexpr uint32_t TM_S = 0, TM_X = 128, TM_Y = 256, TM_D = 384;
 
-// Shared memory, from a 1024-byte aligned base.  Operand tiles are 128-byte-swizzled blocks of 64
-// columns; the blocks of [128]-row tiles lie 16 KiB apart, those of [64]-row tiles 8 KiB.
-constexpr uint32_t OFF_KQ = 0;                     // 2 stages x [128][128]
-constexpr uint32_t OFF_V = OFF_KQ + 2 * 32768;     // [64][128]
-constexpr uint32_t OFF_SHI = OFF_V + 16384;        // [128][128] hi, lo
-constexpr uint32_t OFF_SLO = OFF_SHI + 32768;
-constexpr uint32_t OFF_RHI = OFF_SLO + 32768;      // [64][128] hi, lo: R, then U
-constexpr uint32_t OFF_RLO = OFF_RHI + 16384;
-constexpr uint32_t OFF_THI = OFF_RLO + 16384;      // [128][64] hi, lo: T' and P T, interleaved
-constexpr uint32_t OFF_TLO = OFF_THI + 16384;
-// 16 x 16 blocks of the inversion, as two panels of 8 columns x 16 rows x 16 bytes: the blocks of A
-// below the diagonal (hi, lo), the diagonal blocks of T (hi, lo), and A's diagonal blocks in fp32,
-// transposed
-constexpr uint32_t OFF_AB = OFF_TLO + 16384;       // 6 x (512 hi + 512 lo)
-constexpr uint32_t OFF_TD = OFF_AB + 6 * 1024;     // 4 x (512 hi + 512 lo)
-constexpr uint32_t OFF_AD = OFF_TD + 4 * 1024;     // 4 x 1024
-constexpr uint32_t OFF_TOK = OFF_AD + 4 * 1024;    // per token: ghi, glo, rk, beta rk, scale rq
-constexpr uint32_t OFF_COEF = OFF_TOK + 5 * 256;   // 2 x per token: beta, beta gamma rk, lam rk, out
-constexpr uint32_t OFF_BAR = OFF_COEF + 2 * 1024;
-constexpr uint32_t SZ_BAR = 320;
+// What the first kernel leaves per chunk and head: the operand tile [64 T' rows; 64 P T rows][64] as its hi
+// and its lo parts, in the layout the MMA reads, then the coefficients: beta, -beta gamma rk, lam rk and
+// scale gamma rq per token, gamma_C.
+constexpr uint32_t SZ_T = 16384;
+constexpr uint32_t SZ_COEF = 4 * 256 + 16;
+constexpr uint32_t SZ_SLOT = 2 * SZ_T + SZ_COEF;
+// Chunk slots of a batch: request b's start at floor(cu_seqlens[b] / C) + b, far enough from the next
+// request's for its ceil(length / C) chunks.
+__host__ __device__ inline long long chunk_slots(long long T, long long B) { return T / C + B; }
+
+// Shared memory of the chain kernel, from a 1024-byte aligned base.
+constexpr int kStages = 3;
+constexpr uint32_t SZ_KQ = 32768;                          // [64 K rows; 64 Q rows][128], swizzled
+constexpr uint32_t OFF_KQ = 0;
+constexpr uint32_t OFF_V = OFF_KQ + kStages * SZ_KQ;       // 2 x [64][128], rows of 256 bytes
+constexpr uint32_t OFF_T = OFF_V + 2 * 16384;              // 2 x a slot's tile, hi and lo
+constexpr uint32_t OFF_COEF = OFF_T + 4 * SZ_T;            // 2 x a slot's coefficients
+constexpr uint32_t OFF_BAR = OFF_COEF + 2 * SZ_COEF;
+constexpr uint32_t SZ_BAR = 256;
 constexpr uint32_t kSmemBytes = OFF_BAR + SZ_BAR + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 struct Bars {
-    uint64_t kq_full[2], kq_empty[2];
-    uint64_t v_full;
+    uint64_t kq_full[kStages], kq_empty[kStages];
+    uint64_t v_full[2], t_full[2];
+    uint64_t y_done[2];    // the product with T's tile done: tile and V buffer free
+    uint64_t c_free[2];    // E warps: the chunk's coefficients read (8)
     uint64_t kq_last;      // producer: the last chunk's loads are issued
-    uint64_t kq_fixed;     // warp 14: rows past the end of the last chunk zeroed
-    uint64_t a_full;       // A = [K; Q] [K; Q]^T done
-    uint64_t a_free;       // T warps: A read (4)
-    uint64_t t_sync[3];    // among the T warps (4)
-    uint64_t coef[2];      // T warps: the chunk's coefficients written (4); two, as the T warps may
-                           // be a chunk ahead of a reader
-    uint64_t t_ready;      // T warps: T', P T written (4)
+    uint64_t kq_fixed;     // warp 10: rows past the end of the last chunk zeroed
     uint64_t x_full, y_full, d_full;
     uint64_t r_ready, u_ready, s_ready, o_free;  // E warps (8)
     uint64_t drain;
-    float gend[2];         // e^{G_C} of the chunk
     uint32_t tmem_base;
     int abort_flag;
     int request;
 };
 static_assert(sizeof(Bars) <= SZ_BAR, "barrier block");
+
+// Shared memory of the T kernel.  16 x 16 blocks of the inversion are two panels of 8 columns x 16 rows x
+// 16 bytes: the blocks of A below the diagonal (hi, lo) and the diagonal blocks of T (hi, lo; before that
+// A's in fp32, transposed).  T' takes the place of K and Q once every block is formed.
+constexpr uint32_t TK_KQ = 0;                              // [64 K rows; 64 Q rows][128]; T' hi, lo
+constexpr uint32_t TK_P = 32768;                           // [64][64] hi, lo: P, then P T
+constexpr uint32_t TK_AB = TK_P + 16384;                   // 6 x (512 hi + 512 lo)
+constexpr uint32_t TK_TD = TK_AB + 6 * 1024;               // 4 x (512 hi + 512 lo)
+constexpr uint32_t TK_TOK = TK_TD + 4 * 1024;              // per token: ghi, glo, rk, beta rk, scale rq
+constexpr uint32_t kTSmemBytes = TK_TOK + 5 * 256 + 1024;
 
 constexpr uint64_t kDrainLimitNs = 2000000000ull;
 
@@ -140,11 +149,44 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
     if (lane == 0) mbar_arrive(bar);
 }
 
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo) {
-    hi = pack_bf16x2(x0, x1);
-    lo = pack_bf16x2(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xffff0000u));
+// Two fp32 values in one 64-bit register, for the packed fp32 instructions.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
 }
-
+__device__ __forceinline__ uint64_t f2u(uint32_t a, uint32_t b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// bf16 pairs of two values: hi = bf16(x), lo = bf16(x - hi), the first value in the low halves.
+__device__ __forceinline__ void split2(uint64_t x, uint32_t &hi, uint32_t &lo) {
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+    hi = pack_bf16x2(a, b);
+    const uint64_t d = fma2(f2u(hi << 16, hi & 0xffff0000u), f2(-1.f, -1.f), x);
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
+    lo = pack_bf16x2(a, b);
+}
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo) {
+    split2(f2(x0, x1), hi, lo);
+}
 // A 16 x 16 accumulator (two 16 x 8 fragments) as the bf16 pair of an A operand.
 __device__ __forceinline__ void split_frag(const float (&c)[8], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
     split2(c[0], c[1], hi[0], lo[0]);
@@ -179,151 +221,236 @@ __device__ __forceinline__ long long gate_fixed(float g) {
 }
 constexpr float kFixedStep = 9.094947017729282379e-13f;  // 2^-40
 
-__device__ void t_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx &cx, uint32_t tbase,
-                       int a, int lane, size_t t0, int n, int h, int nchunks) {
-    float *tok = reinterpret_cast<float *>(sm + OFF_TOK);
+// Address of a 16 x 16 block's row for ldmatrix in a 128-byte-swizzled tile: row rho, 16-byte piece kc.
+__device__ __forceinline__ uint32_t sw_row(uint32_t tile, int rho, int kc) {
+    return tile + (uint32_t)rho * 128u + ((uint32_t)(kc ^ (rho & 7)) << 4);
+}
+
+// acc += X_rows Y_rows^T over the 128 columns of a [K; Q] tile: rows ra .. + 15 against rows rb .. + 15;
+// a second row block ra2 shares the loads of rb's fragments.
+template <bool kTwo>
+__device__ __forceinline__ void dot_rows(float (&acc)[8], float (&acc2)[8], uint32_t tile, int ra, int ra2,
+                                         int rb, int lane) {
+    const int mrow = lane & 7, midx = lane >> 3;
+    const int ar = (midx & 1) * 8 + mrow, ak = midx >> 1;   // A operand: matrices (k half, row half)
+    const int br = (midx >> 1) * 8 + mrow, bk = midx & 1;   // B operand: matrices (n half, k half)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    if (kTwo) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc2[e] = 0.f;
+    }
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+        const uint32_t blk = tile + (ks >> 2) * 16384u;
+        const int kc = (ks & 3) * 2;
+        uint32_t fa[4], fb[4];
+        ldsm4(sw_row(blk, rb + br, kc + bk), fb);
+        ldsm4(sw_row(blk, ra + ar, kc + ak), fa);
+        mma_16816(acc, fa, fb[0], fb[1]);
+        mma_16816(acc + 4, fa, fb[2], fb[3]);
+        if (kTwo) {
+            ldsm4(sw_row(blk, ra2 + ar, kc + ak), fa);
+            mma_16816(acc2, fa, fb[0], fb[1]);
+            mma_16816(acc2 + 4, fa, fb[2], fb[3]);
+        }
+    }
+}
+
+// T', P T and the coefficients of one chunk and head (blockIdx.x = slot * H + head).
+__global__ void __launch_bounds__(kTThreads) delta_t_kernel(const DeltaParams p, uint8_t *ws) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int w = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_trigger();
+    const int slot = (int)(blockIdx.x / (unsigned)p.H);
+    const int h = (int)(blockIdx.x - (unsigned)slot * (unsigned)p.H);
+
+    // The slot's request: the last b with floor(cu_seqlens[b] / C) + b <= slot, 32 candidates at a time.
+    // (Requests that are out of order or too long are skipped by the chain kernel; whatever is found for
+    // them is checked before it is used.)
+    int b = 0;
+    {
+        int step = 1;
+        while (step * 32 < p.B) step *= 32;
+        int lo = 0;
+        for (; step > 0; step /= 32) {
+            const int cand = lo + lane * step;
+            const bool in = cand < p.B && (p.cu_seqlens[cand] >> 6) + cand <= slot;
+            const uint32_t m = __ballot_sync(0xffffffffu, in);
+            if (m == 0) return;
+            lo += (31 - __clz(m)) * step;
+        }
+        b = lo;
+    }
+    const int t_req0 = p.cu_seqlens[b], t_req1 = p.cu_seqlens[b + 1];
+    if (t_req0 < 0 || t_req1 < t_req0 || t_req1 > p.T) return;
+    const int c = slot - (t_req0 >> 6) - b;
+    const int r = t_req1 - t_req0 - c * C;  // tokens from this chunk on
+    if (c < 0 || r <= 0) return;
+    const size_t t0 = (size_t)t_req0 + (size_t)c * C;
+
+    float *tok = reinterpret_cast<float *>(sm + TK_TOK);
     float *ghi = tok, *glo = tok + 64, *rk = tok + 128, *brk = tok + 192, *qs = tok + 256;
-    const uint32_t ab = smem_u32(sm + OFF_AB), td = smem_u32(sm + OFF_TD);
-    const uint32_t thi = smem_u32(sm + OFF_THI);
-    float *ad = reinterpret_cast<float *>(sm + OFF_AD) + a * 256;
+    uint8_t *abp = sm + TK_AB, *tdp = sm + TK_TD, *tp = sm + TK_KQ, *pp = sm + TK_P;
+    const uint32_t ab = smem_u32(abp), td = smem_u32(tdp), kq = smem_u32(sm + TK_KQ), tt = kq;
+    const uint32_t pt = smem_u32(pp);
+    float *ad = reinterpret_cast<float *>(tdp + w * 1024);
+    uint8_t *slot_out = ws + (size_t)blockIdx.x * SZ_SLOT;
+    float *cf = reinterpret_cast<float *>(slot_out + 2 * SZ_T);
     const int row = lane >> 2, cp = (lane & 3) * 2;  // fragment row, column pair
     const int mrow = lane & 7, midx = lane >> 3;     // ldmatrix: row, matrix
-    // operand blocks: matrices (panel, row half); the same for transposed A and for [n][k] B
     const uint32_t off_p = (uint32_t)((midx & 1) * 256 + (midx >> 1) * 128 + mrow * 16);
-    const uint32_t lane_k = tbase + TM_A + ((uint32_t)(a * 32) << 16);
+    const int i16 = 16 * w + (lane & 15);            // this warp's tokens, twice
 
-    const float *gp = p.g + (t0 * p.H + h), *bp = p.beta + (t0 * p.H + h);
-    float gn0 = 0.f, gn1 = 0.f, bn = 0.f;
-    auto fetch = [&](int c) {  // gates of tokens lane and lane + 32, beta of this warp's token
-        const int r = n - c * C;
-        const size_t at = (size_t)c * C;
-        gn0 = lane < r ? gp[(at + lane) * p.H] : 0.f;
-        gn1 = lane + 32 < r ? gp[(at + lane + 32) * p.H] : 0.f;
-        const int i = 16 * a + (lane & 15);
-        bn = i < r ? bp[(at + i) * p.H] : 0.f;
-    };
-    if (nchunks > 0) fetch(0);
-
-    for (int c = 0; c < nchunks; ++c) {
-        const uint32_t par = c & 1;
-        // running sums of the gates: every warp forms all 64
-        long long x0 = gate_fixed(gn0), x1 = gate_fixed(gn1);
-        // a NaN has no fixed-point form: it is passed on through beta
-        const uint32_t bad = a < 2 ? __ballot_sync(0xffffffffu, gn0 != gn0)
-                                   : __ballot_sync(0xffffffffu, gn1 != gn1);
-        const float beta =
-            (bad >> (16 * (a & 1) + (lane & 15))) & 1u ? __uint_as_float(0x7fffffffu) : bn;
+    // K and Q into swizzled tiles; rows past the request's end read as zero
+    {
+        const __nv_bfloat16 *kp = p.k + t0 * p.k_rs + (size_t)(h / p.group) * kHeadDim;
+        const __nv_bfloat16 *qp = p.q + t0 * p.q_rs + (size_t)(h / p.group) * kHeadDim;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long y0 = __shfl_up_sync(0xffffffffu, x0, d);
-            const long long y1 = __shfl_up_sync(0xffffffffu, x1, d);
-            if (lane >= d) {
-                x0 += y0;
-                x1 += y1;
-            }
+        for (int x = 0; x < 16; ++x) {
+            const int rho = x * 8 + (int)(threadIdx.x >> 4), piece = threadIdx.x & 15;
+            const int i = rho & 63;
+            const __nv_bfloat16 *src = (rho < 64 ? kp + (size_t)i * p.k_rs : qp + (size_t)i * p.q_rs) + piece * 8;
+            cp_async16(sw_row(kq + (piece >> 3) * 16384u, rho, piece & 7), i < r ? (const void *)src : kp,
+                       i < r ? 16u : 0u);
         }
-        x1 += __shfl_sync(0xffffffffu, x0, 31);
-        const long long xend = __shfl_sync(0xffffffffu, x1, 31);
-        // this warp's tokens 16 a + (lane % 16)
-        const long long xi =
-            __shfl_sync(0xffffffffu, a < 2 ? x0 : x1, 16 * (a & 1) + (lane & 15));
-        if (c + 1 < nchunks) fetch(c + 1);
-
-        if (!warp_wait(&bars->a_full, par, cx)) return;
-        tc_fence_after();
-        {
-            // squared norms: K's in lanes 0-15, Q's in lanes 16-31, of tokens 16 a + lane % 16
-            uint32_t dg[32];
-            tmem_ld32(lane_k + (uint32_t)(a * 32), dg);
-            tmem_ld_wait_regs(dg);
-            float nn = 0.f;
+        cp_async_commit();
+    }
+    // running sums of the gates: every warp forms all 64
+    const float *gp = p.g + (t0 * p.H + h);
+    const float gn0 = lane < r ? gp[(size_t)lane * p.H] : 0.f;
+    const float gn1 = lane + 32 < r ? gp[(size_t)(lane + 32) * p.H] : 0.f;
+    const float bn = i16 < r ? p.beta[(t0 + i16) * p.H + h] : 0.f;
+    long long x0 = gate_fixed(gn0), x1 = gate_fixed(gn1);
+    // a NaN has no fixed-point form: it is passed on through beta
+    const uint32_t bad =
+        w < 2 ? __ballot_sync(0xffffffffu, gn0 != gn0) : __ballot_sync(0xffffffffu, gn1 != gn1);
+    const float beta = (bad >> (i16 & 31)) & 1u ? __uint_as_float(0x7fffffffu) : bn;
 #pragma unroll
-            for (int x = 0; x < 32; ++x) nn = lane == x ? __uint_as_float(dg[x]) : nn;
-            const float inv = p.l2norm ? 1.f / sqrtf(nn + kDeltaEps) : 1.f;
-            const int i = 16 * a + (lane & 15);
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long y0 = __shfl_up_sync(0xffffffffu, x0, d);
+        const long long y1 = __shfl_up_sync(0xffffffffu, x1, d);
+        if (lane >= d) {
+            x0 += y0;
+            x1 += y1;
+        }
+    }
+    x1 += __shfl_sync(0xffffffffu, x0, 31);
+    const long long xend = __shfl_sync(0xffffffffu, x1, 31);
+    const long long xi = __shfl_sync(0xffffffffu, w < 2 ? x0 : x1, i16 & 31);
+    // the blocks of P and P T above the diagonal are zero (those of T' follow below)
+    for (int x = threadIdx.x; x < 16384 / 16; x += kTThreads)
+        reinterpret_cast<uint4 *>(pp)[x] = make_uint4(0u, 0u, 0u, 0u);
+    cp_async_wait_all();
+    __syncthreads();
+
+        // ---- K K^T and Q K^T of the diagonal block; norms
+        float kk[8], qk[8];
+        dot_rows<true>(kk, qk, kq, 16 * w, 64 + 16 * w, 16 * w, lane);
+        float nk = 1.f, nq = 1.f;  // squared norms of token i16
+        if (p.l2norm) {
+            float qq[8], none[8];
+            dot_rows<false>(qq, none, kq, 64 + 16 * w, 0, 64 + 16 * w, lane);
+            // element (i, i) of a fragment block: rows 0-7 in lane 4 i + i / 2, rows 8-15 likewise
+            const int src = 4 * (lane & 7) + ((lane & 7) >> 1);
+            const float k0 = __shfl_sync(0xffffffffu, row & 1 ? kk[1] : kk[0], src);
+            const float k1 = __shfl_sync(0xffffffffu, row & 1 ? kk[7] : kk[6], src);
+            const float q0 = __shfl_sync(0xffffffffu, row & 1 ? qq[1] : qq[0], src);
+            const float q1 = __shfl_sync(0xffffffffu, row & 1 ? qq[7] : qq[6], src);
+            nk = (lane & 8 ? k1 : k0) + kDeltaEps;
+            nq = (lane & 8 ? q1 : q0) + kDeltaEps;
+        }
+        {
+            const float inv = 1.f / sqrtf(lane < 16 ? nk : nq);
             const float gam = ex2((float)xi * kFixedStep);
-            float *cf = reinterpret_cast<float *>(sm + OFF_COEF + par * 1024);
             if (lane < 16) {
                 const float hi = (float)xi;
-                ghi[i] = hi * kFixedStep;
-                glo[i] = (float)(xi - __float2ll_rn(hi)) * kFixedStep;
-                rk[i] = inv;
-                brk[i] = beta * inv;
-                cf[i] = beta;
-                cf[64 + i] = beta * gam * inv;
-                cf[128 + i] = ex2((float)(xend - xi) * kFixedStep) * inv;
+                ghi[i16] = hi * kFixedStep;
+                glo[i16] = (float)(xi - __float2ll_rn(hi)) * kFixedStep;
+                rk[i16] = inv;
+                brk[i16] = beta * inv;
+                cf[i16] = beta;
+                cf[64 + i16] = -beta * gam * inv;
+                cf[128 + i16] = ex2((float)(xend - xi) * kFixedStep) * inv;
             } else {
-                qs[i] = kScale * inv;
-                cf[192 + i] = kScale * gam * inv;
+                qs[i16] = kScale * inv;
+                cf[192 + i16] = kScale * gam * inv;
             }
-            if (a == 0 && lane == 0) bars->gend[par] = ex2((float)xend * kFixedStep);
+            if (w == 0 && lane == 0) cf[256] = ex2((float)xend * kFixedStep);
         }
-        warp_arrive(&bars->t_sync[0], lane);
-        if (!warp_wait(&bars->t_sync[0], par, cx)) return;
-        if (lane == 0) mbar_arrive(&bars->coef[par]);
+        __syncthreads();
 
-        // ---- A and P of row block a
-        uint32_t ph[4][4], pl[4][4];
-        {
+        // ---- scaled blocks: A to scratch, P into the tile's lower half.  Warp w takes diagonal block
+        // w; the blocks below the diagonal go (2,0) (3,0) | (1,0) | (2,1) (3,1) | (3,2).
+#pragma unroll 1
+        for (int x = 0; x < 3; ++x) {
+            int a = w, b = w;
+            if (x > 0) {
+                if (x == 2 && (w & 1)) break;
+                a = w == 0 ? 1 + x : w == 1 ? 1 : w == 2 ? 1 + x : 3;
+                b = w == 0 ? 0 : w == 1 ? 0 : w == 2 ? 1 : 2;
+                dot_rows<true>(kk, qk, kq, 16 * a, 64 + 16 * a, 16 * b, lane);
+            }
             const int i0 = 16 * a + row, i1 = i0 + 8;
             const float gh0 = ghi[i0], gh1 = ghi[i1], gl0 = glo[i0], gl1 = glo[i1];
             const float ai0 = brk[i0], ai1 = brk[i1], qi0 = qs[i0], qi1 = qs[i1];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                if (b > a) break;
-                uint32_t kk[8], qk[8];
-                tmem_ld16x256_pair_wait(lane_k + (uint32_t)(b * 32),
-                                        lane_k + (16u << 16) + (uint32_t)(b * 32), kk, qk);
-                float pv[8];
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const int j = 16 * b + 8 * hf + cp;
-                    const float2 gh = *reinterpret_cast<const float2 *>(ghi + j);
-                    const float2 gl = *reinterpret_cast<const float2 *>(glo + j);
-                    const float2 rj = *reinterpret_cast<const float2 *>(rk + j);
-                    const float e00 = ex2((gh0 - gh.x) + (gl0 - gl.x)) * rj.x;
-                    const float e01 = ex2((gh0 - gh.y) + (gl0 - gl.y)) * rj.y;
-                    const float e10 = ex2((gh1 - gh.x) + (gl1 - gl.x)) * rj.x;
-                    const float e11 = ex2((gh1 - gh.y) + (gl1 - gl.y)) * rj.y;
-                    float a00 = __uint_as_float(kk[4 * hf]) * (e00 * ai0);
-                    float a01 = __uint_as_float(kk[4 * hf + 1]) * (e01 * ai0);
-                    float a10 = __uint_as_float(kk[4 * hf + 2]) * (e10 * ai1);
-                    float a11 = __uint_as_float(kk[4 * hf + 3]) * (e11 * ai1);
-                    pv[4 * hf] = __uint_as_float(qk[4 * hf]) * (e00 * qi0);
-                    pv[4 * hf + 1] = __uint_as_float(qk[4 * hf + 1]) * (e01 * qi0);
-                    pv[4 * hf + 2] = __uint_as_float(qk[4 * hf + 2]) * (e10 * qi1);
-                    pv[4 * hf + 3] = __uint_as_float(qk[4 * hf + 3]) * (e11 * qi1);
-                    if (b == a) {
-                        if (j > i0) pv[4 * hf] = 0.f;
-                        if (j + 1 > i0) pv[4 * hf + 1] = 0.f;
-                        if (j > i1) pv[4 * hf + 2] = 0.f;
-                        if (j + 1 > i1) pv[4 * hf + 3] = 0.f;
-                        const int m = 8 * hf + cp;
-                        ad[m * 16 + row] = j < i0 ? a00 : 0.f;
-                        ad[(m + 1) * 16 + row] = j + 1 < i0 ? a01 : 0.f;
-                        ad[m * 16 + row + 8] = j < i1 ? a10 : 0.f;
-                        ad[(m + 1) * 16 + row + 8] = j + 1 < i1 ? a11 : 0.f;
-                    } else {
-                        uint32_t h0, l0, h1, l1;
-                        split2(a00, a01, h0, l0);
-                        split2(a10, a11, h1, l1);
-                        uint8_t *blk = sm + OFF_AB + (a * (a - 1) / 2 + b) * 1024 + hf * 256 +
-                                       row * 16 + cp * 2;
-                        *reinterpret_cast<uint32_t *>(blk) = h0;
-                        *reinterpret_cast<uint32_t *>(blk + 128) = h1;
-                        *reinterpret_cast<uint32_t *>(blk + 512) = l0;
-                        *reinterpret_cast<uint32_t *>(blk + 640) = l1;
-                    }
+            for (int hf = 0; hf < 2; ++hf) {
+                const int j = 16 * b + 8 * hf + cp;
+                const float2 gh = *reinterpret_cast<const float2 *>(ghi + j);
+                const float2 gl = *reinterpret_cast<const float2 *>(glo + j);
+                const float2 rj = *reinterpret_cast<const float2 *>(rk + j);
+                const float e00 = ex2((gh0 - gh.x) + (gl0 - gl.x)) * rj.x;
+                const float e01 = ex2((gh0 - gh.y) + (gl0 - gl.y)) * rj.y;
+                const float e10 = ex2((gh1 - gh.x) + (gl1 - gl.x)) * rj.x;
+                const float e11 = ex2((gh1 - gh.y) + (gl1 - gl.y)) * rj.y;
+                float a00 = kk[4 * hf] * (e00 * ai0);
+                float a01 = kk[4 * hf + 1] * (e01 * ai0);
+                float a10 = kk[4 * hf + 2] * (e10 * ai1);
+                float a11 = kk[4 * hf + 3] * (e11 * ai1);
+                float p00 = qk[4 * hf] * (e00 * qi0);
+                float p01 = qk[4 * hf + 1] * (e01 * qi0);
+                float p10 = qk[4 * hf + 2] * (e10 * qi1);
+                float p11 = qk[4 * hf + 3] * (e11 * qi1);
+                if (a == b) {
+                    if (j > i0) p00 = 0.f;
+                    if (j + 1 > i0) p01 = 0.f;
+                    if (j > i1) p10 = 0.f;
+                    if (j + 1 > i1) p11 = 0.f;
+                    const int m = 8 * hf + cp;
+                    ad[m * 16 + row] = j < i0 ? a00 : 0.f;
+                    ad[(m + 1) * 16 + row] = j + 1 < i0 ? a01 : 0.f;
+                    ad[m * 16 + row + 8] = j < i1 ? a10 : 0.f;
+                    ad[(m + 1) * 16 + row + 8] = j + 1 < i1 ? a11 : 0.f;
+                } else {
+                    uint32_t h0, l0, h1, l1;
+                    split2(a00, a01, h0, l0);
+                    split2(a10, a11, h1, l1);
+                    uint8_t *blk = abp + (a * (a - 1) / 2 + b) * 1024 + hf * 256 + row * 16 + cp * 2;
+                    *reinterpret_cast<uint32_t *>(blk) = h0;
+                    *reinterpret_cast<uint32_t *>(blk + 128) = h1;
+                    *reinterpret_cast<uint32_t *>(blk + 512) = l0;
+                    *reinterpret_cast<uint32_t *>(blk + 640) = l1;
                 }
-                split_frag(pv, ph[b], pl[b]);
+                uint32_t h0, l0, h1, l1;
+                split2(p00, p01, h0, l0);
+                split2(p10, p11, h1, l1);
+                const int rho = 16 * a + row;  // and rho + 8: the same rho % 8
+                uint8_t *dst = pp + rho * 128 + (((2 * b + hf) ^ (rho & 7)) << 4) + cp * 2;
+                *reinterpret_cast<uint32_t *>(dst) = h0;
+                *reinterpret_cast<uint32_t *>(dst + 1024) = h1;
+                *reinterpret_cast<uint32_t *>(dst + 8192) = l0;
+                *reinterpret_cast<uint32_t *>(dst + 8192 + 1024) = l1;
             }
         }
-        tc_fence_before();
-        warp_arrive(&bars->a_free, lane);
+        __syncwarp();
 
         // ---- the diagonal block of T: column j = lane % 16 by substitution
-        float x[16];
         {
+            float x[16];
             const int j = lane & 15;
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] = i == j ? 1.f : 0.f;
@@ -338,67 +465,64 @@ __device__ void t_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
                     if (4 * v4 + 3 > m) x[4 * v4 + 3] = fmaf(-f.w, x[m], x[4 * v4 + 3]);
                 }
             }
-            // lanes 0-15 keep the hi parts, lanes 16-31 the lo parts
-            uint8_t *dst = sm + OFF_TD + a * 1024 + (lane >> 4) * 512 + (j >> 3) * 256 + (j & 7) * 2;
+            __syncthreads();  // A's diagonal blocks and K, Q are read: T's blocks and T' take their place
+            // the blocks of T' above the diagonal are zero
+            for (int z = lane; z < 256; z += 32) {  // (part, piece, row)
+                const int rho = 16 * w + (z & 15), kc = (z >> 4) & 7;
+                if (kc >= 2 * w + 2)
+                    *reinterpret_cast<uint4 *>(tp + (z >> 7) * 8192 + rho * 128 + ((kc ^ (rho & 7)) << 4)) =
+                        make_uint4(0u, 0u, 0u, 0u);
+            }
+            // lanes 0-15 keep the hi parts, lanes 16-31 the lo parts; the operand tile holds T' = T - I
+            uint8_t *dst = tdp + w * 1024 + (lane >> 4) * 512 + (j >> 3) * 256 + (j & 7) * 2;
+            uint8_t *tile = tp + (lane >> 4) * 8192 + (j & 7) * 2;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const __nv_bfloat16 hi = __float2bfloat16_rn(x[i]);
                 const __nv_bfloat16 lo = __float2bfloat16_rn(x[i] - __bfloat162float(hi));
-                *reinterpret_cast<__nv_bfloat16 *>(dst + i * 16) = lane < 16 ? hi : lo;
+                const __nv_bfloat16 part = lane < 16 ? hi : lo;
+                *reinterpret_cast<__nv_bfloat16 *>(dst + i * 16) = part;
+                const int rho = 16 * w + i;
+                *reinterpret_cast<__nv_bfloat16 *>(tile + rho * 128 +
+                                                   (((2 * w + (j >> 3)) ^ (rho & 7)) << 4)) =
+                    i > j ? part : __float2bfloat16_rn(0.f);
             }
         }
-        warp_arrive(&bars->t_sync[1], lane);
-        // the previous chunk's product with [T'; P T] is done with the tile
-        if (c > 0 && !warp_wait(&bars->y_full, (c - 1) & 1, cx)) return;
-        {
-            const int j = lane & 15;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int rho = 32 * a + i;
-                const float v = i > j ? x[i] : 0.f;
-                const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-                const __nv_bfloat16 lo = __float2bfloat16_rn(v - __bfloat162float(hi));
-                *reinterpret_cast<__nv_bfloat16 *>(sm + (lane < 16 ? OFF_THI : OFF_TLO) + rho * 128 +
-                                                   (((2 * a + (j >> 3)) ^ (rho & 7)) << 4) +
-                                                   (j & 7) * 2) = lane < 16 ? hi : lo;
-            }
-        }
-        if (!warp_wait(&bars->t_sync[1], par, cx)) return;
+        __syncthreads();  // all diagonal blocks
 
-        // ---- column block b = a of T below the diagonal, as its transpose:
+        // ---- column block b = w of T below the diagonal, as its transpose:
         // T_rb^T = -(sum_{b <= m < r} T_mb^T A_rm^T) T_rr^T
         {
-            const int b = a;
+            const int b = w;
             uint32_t yh[3][4], yl[3][4];
             ldsm4_t(td + b * 1024 + off_p, yh[0]);
             ldsm4_t(td + b * 1024 + 512 + off_p, yl[0]);
 #pragma unroll
             for (int dr = 1; dr < 4; ++dr) {
-                const int r = b + dr;
-                if (r > 3) break;
+                const int rr = b + dr;
+                if (rr > 3) break;
                 float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                uint32_t bh[4], bl[4];
 #pragma unroll
                 for (int dm = 0; dm < dr; ++dm) {
-                    uint32_t bh[4], bl[4];
-                    const uint32_t blk = ab + (r * (r - 1) / 2 + b + dm) * 1024 + off_p;
+                    const uint32_t blk = ab + (rr * (rr - 1) / 2 + b + dm) * 1024 + off_p;
                     ldsm4(blk, bh);
                     ldsm4(blk + 512, bl);
                     prod16(acc, yh[dm], yl[dm], bh, bl);
                 }
-                uint32_t zh[4], zl[4], bh[4], bl[4];
+                uint32_t zh[4], zl[4];
                 split_frag(acc, zh, zl);
                 float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                ldsm4(td + r * 1024 + off_p, bh);
-                ldsm4(td + r * 1024 + 512 + off_p, bl);
+                ldsm4(td + rr * 1024 + off_p, bh);
+                ldsm4(td + rr * 1024 + 512 + off_p, bl);
                 prod16(t, zh, zl, bh, bl);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) t[e] = -t[e];
                 split_frag(t, zh, zl);
                 // matrices (j half, i half) -> rows i of the tile, columns 16 b + j
-                const int rho = 32 * r + 8 * (midx >> 1) + mrow;
-                const uint32_t at = thi + rho * 128 + (((2 * b + (midx & 1)) ^ (rho & 7)) << 4);
+                const uint32_t at = sw_row(tt, 16 * rr + 8 * (midx >> 1) + mrow, 2 * b + (midx & 1));
                 stsm4_t(at, zh);
-                stsm4_t(at + (OFF_TLO - OFF_THI), zl);
+                stsm4_t(at + 8192, zl);
                 if (dr < 3) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -408,326 +532,303 @@ __device__ void t_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
                 }
             }
         }
-        warp_arrive(&bars->t_sync[2], lane);
-        if (!warp_wait(&bars->t_sync[2], par, cx)) return;
+        __syncthreads();  // T'
 
-        // ---- row block a of P T
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            if (b > a) break;
-            float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int m = b; m < 4; ++m) {
-                if (m > a) break;
-                uint32_t bh[4], bl[4];
-                const int k = (midx & 1) * 8 + mrow, nh = midx >> 1;
-                if (m == b) {
-                    const uint32_t at = td + b * 1024 + nh * 256 + k * 16;
-                    ldsm4_t(at, bh);
-                    ldsm4_t(at + 512, bl);
-                } else {
-                    const int rho = 32 * m + k;
-                    const uint32_t at = thi + rho * 128 + (((2 * b + nh) ^ (rho & 7)) << 4);
-                    ldsm4_t(at, bh);
-                    ldsm4_t(at + (OFF_TLO - OFF_THI), bl);
+        // ---- row block a = w of P T, over P: block b needs P's blocks b and later
+        {
+            const int a = w;
+#pragma unroll 1
+            for (int b = 0; b <= a; ++b) {
+                float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                for (int m = b; m <= a; ++m) {
+                    uint32_t fh[4], fl[4], bh[4], bl[4];
+                    const uint32_t pa =
+                        sw_row(pt, 16 * a + (midx & 1) * 8 + mrow, 2 * m + (midx >> 1));
+                    ldsm4(pa, fh);
+                    ldsm4(pa + 8192, fl);
+                    const int k = (midx & 1) * 8 + mrow, nh = midx >> 1;
+                    if (m == b) {
+                        const uint32_t at = td + b * 1024 + nh * 256 + k * 16;
+                        ldsm4_t(at, bh);
+                        ldsm4_t(at + 512, bl);
+                    } else {
+                        const uint32_t at = sw_row(tt, 16 * m + k, 2 * b + nh);
+                        ldsm4_t(at, bh);
+                        ldsm4_t(at + 8192, bl);
+                    }
+                    prod16(acc, fh, fl, bh, bl);
                 }
-                prod16(acc, ph[m], pl[m], bh, bl);
-            }
+                __syncwarp();
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                uint32_t h0, l0, h1, l1;
-                split2(acc[4 * hf], acc[4 * hf + 1], h0, l0);
-                split2(acc[4 * hf + 2], acc[4 * hf + 3], h1, l1);
-                const int rho = 32 * a + 16 + row;  // and rho + 8: the same rho % 8
-                uint8_t *dst =
-                    sm + OFF_THI + rho * 128 + (((2 * b + hf) ^ (rho & 7)) << 4) + cp * 2;
-                *reinterpret_cast<uint32_t *>(dst) = h0;
-                *reinterpret_cast<uint32_t *>(dst + 1024) = h1;
-                *reinterpret_cast<uint32_t *>(dst + (OFF_TLO - OFF_THI)) = l0;
-                *reinterpret_cast<uint32_t *>(dst + (OFF_TLO - OFF_THI) + 1024) = l1;
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t h0, l0, h1, l1;
+                    split2(acc[4 * hf], acc[4 * hf + 1], h0, l0);
+                    split2(acc[4 * hf + 2], acc[4 * hf + 3], h1, l1);
+                    const int rho = 16 * a + row;
+                    uint8_t *dst = pp + rho * 128 + (((2 * b + hf) ^ (rho & 7)) << 4) + cp * 2;
+                    *reinterpret_cast<uint32_t *>(dst) = h0;
+                    *reinterpret_cast<uint32_t *>(dst + 1024) = h1;
+                    *reinterpret_cast<uint32_t *>(dst + 8192) = l0;
+                    *reinterpret_cast<uint32_t *>(dst + 8192 + 1024) = l1;
+                }
+                __syncwarp();
             }
         }
-        fence_proxy_async_smem();
-        warp_arrive(&bars->t_ready, lane);
+
+    // the tile to the workspace: [T' hi; P T hi], [T' lo; P T lo]
+    __syncthreads();
+    fence_proxy_async_smem();
+    if (threadIdx.x == 0) {
+        bulk_store(slot_out, tp, 8192);
+        bulk_store(slot_out + 8192, pp, 8192);
+        bulk_store(slot_out + SZ_T, tp + 8192, 8192);
+        bulk_store(slot_out + SZ_T + 8192, pp + 8192, 8192);
+        bulk_commit_group();
+        bulk_wait_group0();
     }
 }
 
 // ------------------------------------------------------------------------------------------------
-// E warps: quarter q of the lanes, half hf of the CTA's NV value columns.
+// E warps: lanes are value columns v = 32 q + lane; half hf of the chunk's tokens and of the k columns.
 
-// A thread's fragment rows (tokens 16 q + lane / 4 and + 8) of its CW columns into the [64][NV] tiles.
-template <int CW>
-__device__ __forceinline__ void store_rows_split(uint8_t *sm, int i0, int sw, int col0, int cp,
-                                                 const float (&x)[CW / 2]) {
+// Eight pairs (one k-step of an operand) as 8 columns of hi parts and 8 of lo parts.
+__device__ __forceinline__ void put_pairs(uint32_t t, const uint64_t *x) {
+    uint32_t hi[8], lo[8];
 #pragma unroll
-    for (int j = 0; j < CW / 8; ++j) {
-        const int col = col0 + 8 * j;
-        const uint32_t off = (uint32_t)(col >> 6) * 8192u + (uint32_t)i0 * 128u +
-                             (((uint32_t)((col & 63) >> 3) ^ (uint32_t)sw) << 4) + (uint32_t)cp * 2u;
-        uint32_t h0, l0, h1, l1;
-        split2(x[4 * j], x[4 * j + 1], h0, l0);
-        split2(x[4 * j + 2], x[4 * j + 3], h1, l1);
-        *reinterpret_cast<uint32_t *>(sm + OFF_RHI + off) = h0;
-        *reinterpret_cast<uint32_t *>(sm + OFF_RLO + off) = l0;
-        *reinterpret_cast<uint32_t *>(sm + OFF_RHI + off + 1024) = h1;
-        *reinterpret_cast<uint32_t *>(sm + OFF_RLO + off + 1024) = l1;
-    }
+    for (int e = 0; e < 8; ++e) split2(x[e], hi[e], lo[e]);
+    tmem_st8(t, hi);
+    tmem_st8(t + 8u, lo);
 }
 
-// The thread's row of the state (CW columns from col0) as a bf16 pair into the operand tiles.
-template <int CW>
-__device__ __forceinline__ void store_state_split(uint8_t *sm, int row, int col0, const float (&S)[CW]) {
-#pragma unroll
-    for (int k = 0; k < CW / 8; ++k) {
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) split2(S[8 * k + 2 * e], S[8 * k + 2 * e + 1], hi[e], lo[e]);
-        const int col = col0 + 8 * k;
-        const uint32_t off = (uint32_t)(col >> 6) * 16384u + (uint32_t)row * 128u +
-                             ((uint32_t)(((col & 63) >> 3) ^ (row & 7)) << 4);
-        *reinterpret_cast<uint4 *>(sm + OFF_SHI + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4 *>(sm + OFF_SLO + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    }
-}
-
-template <int NV>
 __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx &cx, uint32_t tbase, int q,
-                       int hf, int lane, size_t t0, int n, int h, int c0, int slot, bool prefix,
-                       int nchunks) {
-    constexpr int CW = NV / 2;
-    const int col0 = hf * CW;                // of the CTA's NV columns
-    const int srow = 32 * q + lane;          // state row
-    const int sw = lane >> 2;                // token row % 8 of both fragment rows
-    const int i0 = 16 * q + sw, i1 = i0 + 8; // tokens of the chunk
-    const int cp = (lane & 3) * 2;
-    const uint32_t lanes = (uint32_t)(32 * q) << 16;
-    float *gs = p.pool + (((size_t)slot * p.H + h) * kHeadDim + srow) * kHeadDim + c0 + col0;
+                       int hf, int lane, size_t t0, int n, int h, int slot, bool prefix, int nchunks) {
+    const int v = 32 * q + lane;
+    const int tok0 = 32 * hf;  // tokens tok0 .. + 31 of the chunk
+    const uint32_t lanes = tbase + ((uint32_t)(32 * q) << 16);
+    const uint32_t ts = lanes + TM_S + 64u * hf;
+    const uint32_t tx = lanes + TM_X + 32u * hf, ty = lanes + TM_Y + 32u * hf, td = lanes + TM_D + 64u * hf;
+    float *gs = p.pool + (((size_t)slot * p.H + h) * kHeadDim + 64 * hf) * kHeadDim + v;
 
-    float S[CW];
+    uint64_t S[32];  // S[64 hf + 2 x, 64 hf + 2 x + 1][v]
     if (prefix) {
 #pragma unroll
-        for (int x = 0; x < CW / 4; ++x) {
-            const float4 f = reinterpret_cast<const float4 *>(gs)[x];
-            S[4 * x] = f.x;
-            S[4 * x + 1] = f.y;
-            S[4 * x + 2] = f.z;
-            S[4 * x + 3] = f.w;
-        }
+        for (int x = 0; x < 32; ++x) S[x] = f2(gs[2 * x * kHeadDim], gs[(2 * x + 1) * kHeadDim]);
     } else {
 #pragma unroll
-        for (int x = 0; x < CW; ++x) S[x] = 0.f;
+        for (int x = 0; x < 32; ++x) S[x] = 0ull;
     }
     if (nchunks > 0) {
-        store_state_split<CW>(sm, srow, col0, S);
-        fence_proxy_async_smem();
+#pragma unroll
+        for (int x = 0; x < 4; ++x) put_pairs(ts + 16u * x, S + 8 * x);
+        tmem_st_wait();
+        tc_fence_before();
         warp_arrive(&bars->s_ready, lane);
     }
 
     bool ok = true;
     for (int c = 0; c < nchunks; ++c) {
-        const uint32_t par = c & 1;
+        const uint32_t par = c & 1, ph = (c >> 1) & 1;
         const int r = n - c * C;  // tokens from this chunk on
-        const float *cf = reinterpret_cast<const float *>(sm + OFF_COEF + par * 1024);
+        const float *cf = reinterpret_cast<const float *>(sm + OFF_COEF + par * SZ_COEF) + tok0;
         // ---- R = beta V - (beta gamma rk) X^K
-        if (!(ok = warp_wait(&bars->coef[par], (c >> 1) & 1, cx))) break;
-        const float b0 = cf[i0], b1 = cf[i1], bx0 = cf[64 + i0], bx1 = cf[64 + i1];
-        if (!(ok = warp_wait(&bars->v_full, par, cx))) break;
+        if (!(ok = warp_wait(&bars->t_full[par], ph, cx))) break;
+        if (!(ok = warp_wait(&bars->v_full[par], ph, cx))) break;
         if (!(ok = warp_wait(&bars->x_full, par, cx))) break;
         tc_fence_after();
-        float R[CW / 2];
+        uint64_t R[16];
         {
-            uint32_t w[CW / 2];
-            tmem_ld16x256_wait(tbase + lanes + TM_X + (uint32_t)col0, w);
+            const uint8_t *vp = sm + OFF_V + par * 16384 + tok0 * 256 + v * 2;
+            uint32_t w[2][16];
+            tmem_ld16(tx, w[0]);
 #pragma unroll
-            for (int j = 0; j < CW / 8; ++j) {
-                const int col = col0 + 8 * j;
-                const uint8_t *v = sm + OFF_V + (col >> 6) * 8192 + i0 * 128 +
-                                   ((((col & 63) >> 3) ^ sw) << 4) + cp * 2;
-                const uint32_t v0 = *reinterpret_cast<const uint32_t *>(v);
-                const uint32_t v1 = *reinterpret_cast<const uint32_t *>(v + 1024);
-                R[4 * j] = fmaf(-bx0, __uint_as_float(w[4 * j]), b0 * __uint_as_float(v0 << 16));
-                R[4 * j + 1] =
-                    fmaf(-bx0, __uint_as_float(w[4 * j + 1]), b0 * __uint_as_float(v0 & 0xffff0000u));
-                R[4 * j + 2] = fmaf(-bx1, __uint_as_float(w[4 * j + 2]), b1 * __uint_as_float(v1 << 16));
-                R[4 * j + 3] =
-                    fmaf(-bx1, __uint_as_float(w[4 * j + 3]), b1 * __uint_as_float(v1 & 0xffff0000u));
+            for (int y = 0; y < 2; ++y) {
+                tmem_ld_wait_regs(w[y]);
+                if (y == 0) tmem_ld16(tx + 16u, w[1]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int t4 = 4 * y + x;  // four tokens
+                    const float4 b = *reinterpret_cast<const float4 *>(cf + 4 * t4);
+                    const float4 bx = *reinterpret_cast<const float4 *>(cf + 64 + 4 * t4);
+                    uint32_t vv[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        vv[e] = (uint32_t)*reinterpret_cast<const uint16_t *>(vp + (4 * t4 + e) * 256) << 16;
+                    R[2 * t4] = fma2(f2(bx.x, bx.y), f2u(w[y][4 * x], w[y][4 * x + 1]),
+                                     mul2(f2(b.x, b.y), f2u(vv[0], vv[1])));
+                    R[2 * t4 + 1] = fma2(f2(bx.z, bx.w), f2u(w[y][4 * x + 2], w[y][4 * x + 3]),
+                                         mul2(f2(b.z, b.w), f2u(vv[2], vv[3])));
+                }
+                if (r < C) {  // rows past the end hold other requests' values
+#pragma unroll
+                    for (int x = 8 * y; x < 8 * y + 8; ++x) {
+                        if (tok0 + 2 * x >= r) R[x] = 0ull;
+                        else if (tok0 + 2 * x + 1 >= r) R[x] &= 0xffffffffull;
+                    }
+                }
+                put_pairs(tx + 16u * y, R + 8 * y);
             }
         }
-        if (r < C) {  // rows past the end hold other requests' values
-#pragma unroll
-            for (int j = 0; j < CW / 8; ++j) {
-                if (i0 >= r) R[4 * j] = R[4 * j + 1] = 0.f;
-                if (i1 >= r) R[4 * j + 2] = R[4 * j + 3] = 0.f;
-            }
-        }
-        store_rows_split<CW>(sm, i0, sw, col0, cp, R);
-        fence_proxy_async_smem();
+        tmem_st_wait();
         tc_fence_before();
         warp_arrive(&bars->r_ready, lane);
 
         // ---- U = R + T' R, scaled for the state update
-        const float u0 = cf[128 + i0], u1 = cf[128 + i1];
         if (!(ok = warp_wait(&bars->y_full, par, cx))) break;
         tc_fence_after();
         {
-            uint32_t w[CW / 2];
-            tmem_ld16x256_wait(tbase + lanes + TM_Y + (uint32_t)col0, w);
+            uint32_t w[2][16];
+            tmem_ld16(ty, w[0]);
 #pragma unroll
-            for (int j = 0; j < CW / 8; ++j) {
-                R[4 * j] = (R[4 * j] + __uint_as_float(w[4 * j])) * u0;
-                R[4 * j + 1] = (R[4 * j + 1] + __uint_as_float(w[4 * j + 1])) * u0;
-                R[4 * j + 2] = (R[4 * j + 2] + __uint_as_float(w[4 * j + 2])) * u1;
-                R[4 * j + 3] = (R[4 * j + 3] + __uint_as_float(w[4 * j + 3])) * u1;
+            for (int y = 0; y < 2; ++y) {
+                tmem_ld_wait_regs(w[y]);
+                if (y == 0) tmem_ld16(ty + 16u, w[1]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int t4 = 4 * y + x;
+                    const float4 u = *reinterpret_cast<const float4 *>(cf + 128 + 4 * t4);
+                    R[2 * t4] = mul2(f2(u.x, u.y), add2(R[2 * t4], f2u(w[y][4 * x], w[y][4 * x + 1])));
+                    R[2 * t4 + 1] =
+                        mul2(f2(u.z, u.w), add2(R[2 * t4 + 1], f2u(w[y][4 * x + 2], w[y][4 * x + 3])));
+                }
+                put_pairs(ty + 16u * y, R + 8 * y);
             }
         }
-        store_rows_split<CW>(sm, i0, sw, col0, cp, R);
-        fence_proxy_async_smem();
+        tmem_st_wait();
+        tc_fence_before();
         warp_arrive(&bars->u_ready, lane);
 
-        // ---- o = (scale gamma rq) X^Q + P T R
+        // ---- o = (scale gamma rq) X^Q + P T R; neighbouring lanes exchange halves, so that each
+        // stores two value columns of one token
         {
-            const float co0 = cf[192 + i0], co1 = cf[192 + i1];
-            uint32_t w[CW / 2], y[CW / 2];
-            tmem_ld16x256_wait(tbase + lanes + (16u << 16) + TM_X + (uint32_t)col0, w);
-            tmem_ld16x256_wait(tbase + lanes + (16u << 16) + TM_Y + (uint32_t)col0, y);
-            tc_fence_before();
-            warp_arrive(&bars->o_free, lane);
-            const size_t tok = t0 + (size_t)c * C;
-            __nv_bfloat16 *o0 = p.out + ((tok + i0) * p.H + h) * kHeadDim + c0 + col0;
-            __nv_bfloat16 *o1 = p.out + ((tok + i1) * p.H + h) * kHeadDim + c0 + col0;
-            const int t4 = lane & 3;
+            const size_t tok = t0 + (size_t)c * C + tok0 + (lane & 1);
+            __nv_bfloat16 *op = p.out + (tok * p.H + h) * kHeadDim + (v & ~1);
+            const size_t two = (size_t)p.H * kHeadDim * 2;
+            const int left = r - tok0 - (lane & 1);
 #pragma unroll
-            for (int j4 = 0; j4 < CW / 32; ++j4) {
-                // the thread's column pairs of four 8-column fragments, for its two rows; a 4 x 4
-                // transpose among the row's four lanes leaves lane t4 with fragment t4's 8 columns
-                uint32_t o[2][4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int at = 16 * j4 + 4 * e;
-                    o[0][e] = pack_bf16x2(fmaf(co0, __uint_as_float(w[at]), __uint_as_float(y[at])),
-                                          fmaf(co0, __uint_as_float(w[at + 1]), __uint_as_float(y[at + 1])));
-                    o[1][e] =
-                        pack_bf16x2(fmaf(co1, __uint_as_float(w[at + 2]), __uint_as_float(y[at + 2])),
-                                    fmaf(co1, __uint_as_float(w[at + 3]), __uint_as_float(y[at + 3])));
+            for (int z = 0; z < 2; ++z) {
+                uint32_t w[16], y[16];
+                tmem_ld16(tx + 64u + 16u * z, w);
+                tmem_ld16(ty + 64u + 16u * z, y);
+                tmem_ld_wait_regs(w);
+                tmem_ld_wait_regs(y);
+                if (z == 1) {
+                    tc_fence_before();
+                    warp_arrive(&bars->o_free, lane);
                 }
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    uint32_t(&v)[4] = o[x];
-                    const bool lo2 = t4 < 2;
-                    const uint32_t ra = __shfl_xor_sync(0xffffffffu, lo2 ? v[2] : v[0], 2);
-                    const uint32_t rb = __shfl_xor_sync(0xffffffffu, lo2 ? v[3] : v[1], 2);
-                    if (lo2) { v[2] = ra; v[3] = rb; } else { v[0] = ra; v[1] = rb; }
-                    const bool even = (t4 & 1) == 0;
-                    const uint32_t rc = __shfl_xor_sync(0xffffffffu, even ? v[1] : v[0], 1);
-                    const uint32_t rd = __shfl_xor_sync(0xffffffffu, even ? v[3] : v[2], 1);
-                    if (even) { v[1] = rc; v[3] = rd; } else { v[0] = rc; v[2] = rd; }
-                    const int i = x ? i1 : i0;
-                    if (i < r)
-                        *reinterpret_cast<uint4 *>((x ? o1 : o0) + 32 * j4 + 8 * t4) =
-                            make_uint4(v[0], v[1], v[2], v[3]);
+                for (int x = 0; x < 4; ++x) {
+                    const float4 o = *reinterpret_cast<const float4 *>(cf + 192 + 16 * z + 4 * x);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int at = 4 * x + 2 * e;
+                        float za, zb;
+                        asm("mov.b64 {%0, %1}, %2;"
+                            : "=f"(za), "=f"(zb)
+                            : "l"(fma2(e ? f2(o.z, o.w) : f2(o.x, o.y), f2u(w[at], w[at + 1]),
+                                       f2u(y[at], y[at + 1]))));
+                        const uint32_t mine = pack_bf16x2(za, zb);  // tokens at, at + 1
+                        const uint32_t theirs = __shfl_xor_sync(0xffffffffu, mine, 1);
+                        // even lanes: the first token of (v, v + 1); odd lanes: the second of (v - 1, v)
+                        const uint32_t word = (lane & 1) ? __byte_perm(theirs, mine, 0x7632)
+                                                         : __byte_perm(mine, theirs, 0x5410);
+                        if (16 * z + at < left)
+                            *reinterpret_cast<uint32_t *>(op + (8 * z + (at >> 1)) * two) = word;
+                    }
                 }
             }
         }
 
         // ---- S = gamma_C S + K^T U
-        const float ge = bars->gend[par];
+        const float ge = cf[256 - tok0];
+        warp_arrive(&bars->c_free[par], lane);
         if (!(ok = warp_wait(&bars->d_full, par, cx))) break;
         tc_fence_after();
+        {
+            const uint64_t ge2 = f2(ge, ge);
+            uint32_t w[2][16];
+            tmem_ld16(td, w[0]);
 #pragma unroll
-        for (int x = 0; x < CW / 32; ++x) {
-            uint32_t w[32];
-            tmem_ld32(tbase + lanes + TM_D + (uint32_t)(col0 + 32 * x), w);
-            tmem_ld_wait_regs(w);
+            for (int x = 0; x < 4; ++x) {
+                uint32_t(&d)[16] = w[x & 1];
+                tmem_ld_wait_regs(d);
+                if (x < 3) tmem_ld16(td + 16u * (x + 1), w[(x + 1) & 1]);
 #pragma unroll
-            for (int y = 0; y < 32; ++y) S[32 * x + y] = fmaf(ge, S[32 * x + y], __uint_as_float(w[y]));
+                for (int e = 0; e < 8; ++e)
+                    S[8 * x + e] = fma2(ge2, S[8 * x + e], f2u(d[2 * e], d[2 * e + 1]));
+                if (c + 1 < nchunks) put_pairs(ts + 16u * x, S + 8 * x);
+            }
         }
         if (c + 1 < nchunks) {
-            store_state_split<CW>(sm, srow, col0, S);
-            fence_proxy_async_smem();
+            tmem_st_wait();
             tc_fence_before();
             warp_arrive(&bars->s_ready, lane);
         }
     }
     if (ok && !(prefix && nchunks == 0)) {
 #pragma unroll
-        for (int x = 0; x < CW / 4; ++x)
-            reinterpret_cast<float4 *>(gs)[x] =
-                make_float4(S[4 * x], S[4 * x + 1], S[4 * x + 2], S[4 * x + 3]);
+        for (int x = 0; x < 32; ++x) {
+            float a, b;
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(S[x]));
+            gs[2 * x * kHeadDim] = a;
+            gs[(2 * x + 1) * kHeadDim] = b;
+        }
     }
 }
 
 // ------------------------------------------------------------------------------------------------
 // MMA issuer (one thread)
-template <int NV>
 __device__ void mma_role(Bars *bars, uint32_t tbase, uint32_t s_base, int nchunks, bool ragged, Ctx cx) {
-    const uint32_t idA = idesc_bf16_f32(128, 128, false, false);
-    const uint32_t idX = idesc_bf16_f32(128, NV, false, true);
-    const uint32_t idD = idesc_bf16_f32(128, NV, true, true);
-    // All operands have the same high descriptor word (8-row groups 1024 bytes apart, 128-byte
-    // swizzle), so only low words are kept: start address and leading-dimension offset.
+    const uint32_t id = idesc_bf16_f32(128, 128, false, false);
+    const uint32_t idD = idesc_bf16_f32(128, 128, false, true);
+    // All B operands have the same high descriptor word (8-row groups 1024 bytes apart, 128-byte
+    // swizzle); the low word holds the start address and the leading-dimension offset.
     const uint64_t high = sdesc_sw128(0, 0, 1024);
-    auto low = [&](uint32_t off, uint32_t lbo) { return ((s_base + off) >> 4) | ((lbo >> 4) << 16); };
-    auto mma = [&](uint32_t d, uint32_t da, uint32_t db, uint32_t id, uint32_t acc) {
-        mma_bf16(tbase + d, high | da, high | db, id, acc);
+    auto mma = [&](uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+        mma_f16_tmem_a(tbase + d, tbase + a, high | b, idesc, acc);
     };
-    const uint32_t dKQ = low(OFF_KQ, 16);      // K-major
-    const uint32_t dKt = low(OFF_KQ, 16384);   // M-major (k dimensions)
-    const uint32_t dSh = low(OFF_SHI, 16384), dSl = low(OFF_SLO, 16384);
-    const uint32_t dTh = low(OFF_THI, 16), dTl = low(OFF_TLO, 16);
-    const uint32_t dRh = low(OFF_RHI, 8192), dRl = low(OFF_RLO, 8192);
-    constexpr uint32_t stage = 32768 >> 4;
-    auto kofs = [](int kk) { return (uint32_t)((kk >> 2) * 1024 + (kk & 3) * 2); };
-
-    auto issue_a = [&](int c) -> bool {
-        const int st = c & 1;
-        if (!wait_bar(&bars->kq_full[st], (c >> 1) & 1, cx)) return false;
-        if (ragged && c == nchunks - 1 && !wait_bar(&bars->kq_fixed, 0, cx)) return false;
-        if (c > 0 && !wait_bar(&bars->a_free, (c - 1) & 1, cx)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-            mma(TM_A, dKQ + st * stage + kofs(kk), dKQ + st * stage + kofs(kk), idA, kk > 0);
-        mma_commit(&bars->a_full);
-        return true;
-    };
-    bool ok = nchunks > 0 ? issue_a(0) : true;
-    for (int c = 0; c < nchunks && ok; ++c) {
-        const int st = c & 1;
-        const uint32_t par = c & 1;
-        ok = wait_bar(&bars->s_ready, par, cx) && (c == 0 || wait_bar(&bars->o_free, (c - 1) & 1, cx));
+    bool ok = true;
+    int st = 0;
+    uint32_t stp = 0;
+    for (int c = 0; c < nchunks; ++c) {
+        const uint32_t par = c & 1, ph = (c >> 1) & 1;
+        ok = wait_bar(&bars->kq_full[st], stp, cx) && wait_bar(&bars->s_ready, par, cx) &&
+             (c == 0 || wait_bar(&bars->o_free, (c - 1) & 1, cx));
         if (!ok) break;
         tc_fence_after();
+        const uint32_t kq = (s_base + OFF_KQ + st * SZ_KQ) >> 4;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-            mma(TM_X, dKQ + st * stage + kofs(kk), dSh + kk * 128, idX, kk > 0);
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-            mma(TM_X, dKQ + st * stage + kofs(kk), dSl + kk * 128, idX, 1);
+            for (int kk = 0; kk < 8; ++kk)
+                mma(TM_X, TM_S + 16u * kk + 8u * x, kq + ((kk >> 2) * 1024 + (kk & 3) * 2) + (1u << 16), id,
+                    x + kk > 0);
         mma_commit(&bars->x_full);
-        if (c + 1 < nchunks && !(ok = issue_a(c + 1))) break;
-        if (!(ok = wait_bar(&bars->t_ready, par, cx) && wait_bar(&bars->r_ready, par, cx))) break;
+        if (!(ok = wait_bar(&bars->t_full[par], ph, cx) && wait_bar(&bars->r_ready, par, cx))) break;
         tc_fence_after();
+        const uint32_t tt = (s_base + OFF_T + par * 2 * SZ_T) >> 4;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-            mma(TM_Y, dTh + kk * 2, dRh + kk * 128, idX, kk > 0);
+        for (int x = 0; x < 3; ++x)  // R_hi T_hi, R_lo T_hi, R_hi T_lo
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-            mma(TM_Y, dTh + kk * 2, dRl + kk * 128, idX, 1);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-            mma(TM_Y, dTl + kk * 2, dRh + kk * 128, idX, 1);
+            for (int kk = 0; kk < 4; ++kk)
+                mma(TM_Y, TM_X + 16u * kk + (x == 1 ? 8u : 0u),
+                    tt + (x == 2 ? SZ_T >> 4 : 0u) + kk * 2 + (1u << 16), id, x + kk > 0);
         mma_commit(&bars->y_full);
+        mma_commit(&bars->y_done[par]);
+        if (ragged && c == nchunks - 1 && !(ok = wait_bar(&bars->kq_fixed, 0, cx))) break;
         if (!(ok = wait_bar(&bars->u_ready, par, cx))) break;
         tc_fence_after();
-        // 16 tokens of K a step: rows 32 kk .. 32 kk + 15 of the interleaved tile
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-            mma(TM_D, dKt + st * stage + kk * 256, dRh + kk * 128, idD, kk > 0);
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-            mma(TM_D, dKt + st * stage + kk * 256, dRl + kk * 128, idD, 1);
+            for (int kk = 0; kk < 4; ++kk)
+                mma(TM_D, TM_Y + 16u * kk + 8u * x, kq + kk * 128 + ((16384u >> 4) << 16), idD, x + kk > 0);
         mma_commit(&bars->d_full);
         mma_commit(&bars->kq_empty[st]);
+        if (++st == kStages) {
+            st = 0;
+            stp ^= 1;
+        }
     }
     // every issued MMA must finish before tensor memory is freed
     mma_commit(&bars->drain);
@@ -737,46 +838,48 @@ __device__ void mma_role(Bars *bars, uint32_t tbase, uint32_t s_base, int nchunk
     wait_bar(&bars->drain, 0, cx);
 }
 
-template <int NV>
 __device__ void producer_role(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, Bars *bars,
-                              uint8_t *sm, int t0, int nchunks, int xq, int xv, Ctx cx) {
+                              uint8_t *sm, const uint8_t *slots, size_t slot_step, int t0, int nchunks,
+                              int xq, int xv, Ctx cx) {
     int kq = 0, vv = 0;
     for (int c = 0; c < nchunks; ++c) {
-        const int st = c & 1;
-        if (c >= 2 && !wait_bar(&bars->kq_empty[st], ((c >> 1) - 1) & 1, cx)) break;
-        uint8_t *dst = sm + OFF_KQ + st * 32768;
-        mbar_arrive_expect_tx(&bars->kq_full[st], 32768);
+        const int st = c % kStages, g = c & 1;
+        if (c >= kStages && !wait_bar(&bars->kq_empty[st], (c / kStages - 1) & 1, cx)) break;
+        uint8_t *dst = sm + OFF_KQ + st * SZ_KQ;
         const int y = t0 + c * C;
+        mbar_arrive_expect_tx(&bars->kq_full[st], SZ_KQ);
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                tma_load_2d(dst + x * 16384 + a * 4096, &tk, &bars->kq_full[st], xq + 64 * x, y + 16 * a);
-                tma_load_2d(dst + x * 16384 + a * 4096 + 2048, &tq, &bars->kq_full[st], xq + 64 * x,
-                            y + 16 * a);
-            }
+        for (int x = 0; x < 2; ++x) {
+            tma_load_2d(dst + x * 16384, &tk, &bars->kq_full[st], xq + 64 * x, y);
+            tma_load_2d(dst + x * 16384 + 8192, &tq, &bars->kq_full[st], xq + 64 * x, y);
         }
         kq = c + 1;
         if (kq == nchunks) mbar_arrive(&bars->kq_last);
-        if (c >= 1 && !wait_bar(&bars->r_ready, (c - 1) & 1, cx)) break;
-        mbar_arrive_expect_tx(&bars->v_full, NV * C * 2);
-#pragma unroll
-        for (int x = 0; x < NV / 64; ++x)
-            tma_load_2d(sm + OFF_V + x * 8192, &tv, &bars->v_full, xv + 64 * x, y);
+        if (c >= 2 && (!wait_bar(&bars->y_done[g], ((c >> 1) - 1) & 1, cx) ||
+                       !wait_bar(&bars->c_free[g], ((c >> 1) - 1) & 1, cx)))
+            break;
+        mbar_arrive_expect_tx(&bars->t_full[g], SZ_SLOT);
+        bulk_load(sm + OFF_T + g * 2 * SZ_T, slots + c * slot_step, 2 * SZ_T, &bars->t_full[g]);
+        bulk_load(sm + OFF_COEF + g * SZ_COEF, slots + c * slot_step + 2 * SZ_T, SZ_COEF, &bars->t_full[g]);
+        mbar_arrive_expect_tx(&bars->v_full[g], 16384);
+        tma_load_2d(sm + OFF_V + g * 16384, &tv, &bars->v_full[g], xv, y);
         vv = c + 1;
     }
     // copies still in flight must land before the shared memory goes away
     int dummy = 0;
     cx.abort_flag = &dummy;
     cx.limit = kDrainLimitNs;
-    for (int c = kq >= 2 ? kq - 2 : 0; c < kq; ++c) wait_bar(&bars->kq_full[c & 1], (c >> 1) & 1, cx);
-    if (vv > 0) wait_bar(&bars->v_full, (vv - 1) & 1, cx);
+    for (int c = kq >= kStages ? kq - kStages : 0; c < kq; ++c)
+        wait_bar(&bars->kq_full[c % kStages], (c / kStages) & 1, cx);
+    for (int c = vv >= 2 ? vv - 2 : 0; c < vv; ++c) {
+        wait_bar(&bars->t_full[c & 1], (c >> 1) & 1, cx);
+        wait_bar(&bars->v_full[c & 1], (c >> 1) & 1, cx);
+    }
 }
 
-template <int NV>
 __global__ void __launch_bounds__(kThreads, 1)
     delta_extend_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                        const __grid_constant__ CUtensorMap tv, const DeltaParams p) {
+                        const __grid_constant__ CUtensorMap tv, const DeltaParams p, const uint8_t *ws) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Bars *bars = reinterpret_cast<Bars *>(sm + OFF_BAR);
@@ -784,10 +887,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
-    constexpr int kParts = kHeadDim / NV;
-    const int part = (int)blockIdx.x % kParts;
-    const int h = ((int)blockIdx.x / kParts) % p.H;
-    const int want = (int)blockIdx.x / kParts / p.H;
+    const int h = (int)blockIdx.x % p.H;
+    const int want = (int)blockIdx.x / p.H;
 
     // Longest request first for batches that the CTA can rank itself: CTAs are issued in index
     // order, so long requests do not finish last.
@@ -825,18 +926,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool ragged = n % C != 0;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             mbar_init(&bars->kq_full[s], 1);
             mbar_init(&bars->kq_empty[s], 1);
-            mbar_init(&bars->coef[s], kTWarps);
         }
-        mbar_init(&bars->v_full, 1);
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(&bars->v_full[g], 1);
+            mbar_init(&bars->t_full[g], 1);
+            mbar_init(&bars->y_done[g], 1);
+            mbar_init(&bars->c_free[g], kEWarps);
+        }
         mbar_init(&bars->kq_last, 1);
         mbar_init(&bars->kq_fixed, 1);
-        mbar_init(&bars->a_full, 1);
-        mbar_init(&bars->a_free, kTWarps);
-        for (int s = 0; s < 3; ++s) mbar_init(&bars->t_sync[s], kTWarps);
-        mbar_init(&bars->t_ready, kTWarps);
         mbar_init(&bars->x_full, 1);
         mbar_init(&bars->y_full, 1);
         mbar_init(&bars->d_full, 1);
@@ -857,49 +958,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tk);
         tma_prefetch_desc(&tv);
     }
-    // the blocks of [T'; P T] above the diagonal stay zero
-    for (int x = threadIdx.x; x < 32768 / 16; x += kThreads)
-        reinterpret_cast<uint4 *>(sm + OFF_THI)[x] = make_uint4(0u, 0u, 0u, 0u);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = bars->tmem_base;
     const Ctx cx{p.wait_limit_ns, &bars->abort_flag, p.err};
-    const int c0 = part * NV;
 
-    if (warp < kTWarps) {
-        reg_dec<kRegsT>();
-        t_role(p, sm, bars, cx, tbase, warp, lane, (size_t)t_req0, n, h, nchunks);
-    } else if (warp < kTWarps + kEWarps) {
-        reg_inc<kRegsE>();
-        e_role<NV>(p, sm, bars, cx, tbase, warp & 3, (warp - kTWarps) >> 2, lane, (size_t)t_req0, n, h, c0,
-                   slot, p.prefix_mask[b] != 0, nchunks);
-    } else {
-        reg_dec<kRegsRest>();
-        if (warp == kProducerWarp) {
-            if (lane == 0)
-                producer_role<NV>(tq, tk, tv, bars, sm, t_req0, nchunks, (h / p.group) * kHeadDim,
-                                  h * kHeadDim + c0, cx);
-        } else if (warp == kMmaWarp) {
-            if (lane == 0) mma_role<NV>(bars, tbase, smem_u32(sm), nchunks, ragged, cx);
-        } else if (warp == kFixWarp && ragged) {
-            const int c = nchunks - 1;
-            if (warp_wait(&bars->kq_last, 0, cx) &&
-                warp_wait(&bars->kq_full[c & 1], (c >> 1) & 1, cx)) {
-                uint8_t *tile = sm + OFF_KQ + (c & 1) * 32768;
-                // (token, K or Q, column block, 16-byte piece)
-                for (int x = (n - c * C) * 32 + lane; x < C * 32; x += 32) {
-                    const int i = x >> 5;
-                    const int rho = 32 * (i >> 4) + (i & 15) + ((x >> 4) & 1) * 16;
-                    *reinterpret_cast<uint4 *>(tile + ((x >> 3) & 1) * 16384 + rho * 128 + (x & 7) * 16) =
-                        make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();
-                warp_arrive(&bars->kq_fixed, lane);
-            }
+    if (warp < kEWarps) {
+        e_role(p, sm, bars, cx, tbase, warp & 3, warp >> 2, lane, (size_t)t_req0, n, h, slot,
+               p.prefix_mask[b] != 0, nchunks);
+    } else if (warp == kProducerWarp) {
+        if (lane == 0)
+            producer_role(tq, tk, tv, bars, sm, ws + ((size_t)((t_req0 >> 6) + b) * p.H + h) * SZ_SLOT,
+                          (size_t)p.H * SZ_SLOT, t_req0, nchunks, (h / p.group) * kHeadDim, h * kHeadDim, cx);
+    } else if (warp == kMmaWarp) {
+        if (lane == 0) mma_role(bars, tbase, smem_u32(sm), nchunks, ragged, cx);
+    } else if (warp == kFixWarp && ragged) {
+        const int c = nchunks - 1, st = c % kStages;
+        if (warp_wait(&bars->kq_last, 0, cx) && warp_wait(&bars->kq_full[st], (c / kStages) & 1, cx)) {
+            uint8_t *tile = sm + OFF_KQ + st * SZ_KQ;
+            for (int x = (n - c * C) * 16 + lane; x < C * 16; x += 32)  // (token, column block, piece)
+                *reinterpret_cast<uint4 *>(tile + ((x >> 3) & 1) * 16384 + (x >> 4) * 128 + (x & 7) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            warp_arrive(&bars->kq_fixed, lane);
         }
-        __syncwarp();
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) {
@@ -908,18 +993,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int NV>
-cudaError_t launch_nv(const DeltaParams &p, cudaStream_t stream) {
-    const long long ctas = (long long)p.B * p.H * (kHeadDim / NV);
-    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+}  // namespace
+
+unsigned long long delta_scratch_bytes(long long B, long long T, long long H) {
+    return T > 0 && B > 0 ? (unsigned long long)chunk_slots(T, B) * (unsigned long long)H * SZ_SLOT : 0ull;
+}
+
+cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, cudaStream_t stream) {
+    const long long ctas = (long long)p.B * p.H;
+    if (ctas <= 0) return cudaSuccess;
+    const long long t_ctas = p.T > 0 ? chunk_slots(p.T, p.B) * p.H : 0;
+    if (ctas > 0x7fffffffLL || t_ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     CUtensorMap tq, tk, tv;
     memset(&tq, 0, sizeof(tq));
     memset(&tk, 0, sizeof(tk));
     memset(&tv, 0, sizeof(tv));
     if (p.T > 0 &&
-        (!make_rows_map(&tq, p.q, p.T, (long long)p.Hk * kHeadDim, p.q_rs, 16) ||
-         !make_rows_map(&tk, p.k, p.T, (long long)p.Hk * kHeadDim, p.k_rs, 16) ||
-         !make_rows_map(&tv, p.v, p.T, (long long)p.H * kHeadDim, p.v_rs, C)))
+        (!make_rows_map(&tq, p.q, p.T, (long long)p.Hk * kHeadDim, p.q_rs, 64, C, true) ||
+         !make_rows_map(&tk, p.k, p.T, (long long)p.Hk * kHeadDim, p.k_rs, 64, C, true) ||
+         !make_rows_map(&tv, p.v, p.T, (long long)p.H * kHeadDim, p.v_rs, kHeadDim, C, false)))
         return cudaErrorInvalidValue;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -930,23 +1022,21 @@ cudaError_t launch_nv(const DeltaParams &p, cudaStream_t stream) {
         std::lock_guard<std::mutex> lock(mu);
         if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
         if (!configured[dev]) {
-            e = cudaFuncSetAttribute(delta_extend_kernel<NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            e = cudaFuncSetAttribute(delta_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      kSmemBytes);
+            if (e != cudaSuccess) return e;
+            e = cudaFuncSetAttribute(delta_t_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTSmemBytes);
             if (e != cudaSuccess) return e;
             configured[dev] = true;
         }
     }
-    return launch_pdl(delta_extend_kernel<NV>, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, tq,
-                      tk, tv, p);
-}
-
-}  // namespace
-
-cudaError_t launch_delta_extend(const DeltaParams &p, int num_sms, cudaStream_t stream) {
-    if (p.B <= 0) return cudaSuccess;
-    // two CTAs per head while that still is one wave
-    if ((long long)p.B * p.H * 2 <= num_sms) return launch_nv<64>(p, stream);
-    return launch_nv<128>(p, stream);
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    if (t_ctas > 0) {
+        e = launch_pdl(delta_t_kernel, dim3((unsigned)t_ctas), dim3(kTThreads), kTSmemBytes, stream, p, w);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(delta_extend_kernel, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, tq, tk,
+                      tv, p, (const uint8_t *)w);
 }
 
 }  // namespace la

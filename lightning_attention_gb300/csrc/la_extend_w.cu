@@ -482,22 +482,23 @@ EncodeTiledFn encode_fn() {
 }  // namespace
 
 bool make_rows_map(CUtensorMap *m, const void *ptr, int rows, long long width, long long row_stride,
-                   int box_rows) {
+                   int box_cols, int box_rows, bool swizzle) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)row_stride * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
     const cuuint32_t es[2] = {1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box,
-               es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
            CUDA_SUCCESS;
 }
 
 // [T][H*128] bf16, box of 64 columns x C rows, 128-byte swizzle; rows past T read as zero.
 bool make_token_map_full(CUtensorMap *m, const void *ptr, int T, int H) {
-    return make_rows_map(m, ptr, T, (long long)H * kHeadDim, (long long)H * kHeadDim, C);
+    return make_rows_map(m, ptr, T, (long long)H * kHeadDim, (long long)H * kHeadDim, 64, C, true);
 }
 
 cudaError_t launch_extend_wide(const ExtendParams &p, cudaStream_t stream) {

@@ -178,10 +178,10 @@ cudaError_t launch_extend_wide(const ExtendParams &p, cudaStream_t stream);  // 
 // [T][H*128] bf16 TMA map, box of 64 columns x 128 rows, 128-byte swizzle; rows past T read as
 // zero (la_extend_w.cu).
 bool make_token_map_full(CUtensorMap *m, const void *ptr, int T, int H);
-// [rows][width] bf16 with row_stride elements between rows, box of 64 columns x box_rows rows,
-// 128-byte swizzle; rows past the last read as zero (la_extend_w.cu).
+// [rows][width] bf16 with row_stride elements between rows, box of box_cols columns x box_rows rows, with
+// the 128-byte swizzle (64 columns) or without; rows past the last read as zero (la_extend_w.cu).
 bool make_rows_map(CUtensorMap *m, const void *ptr, int rows, long long width, long long row_stride,
-                   int box_rows);
+                   int box_cols, int box_rows, bool swizzle);
 // The pre-pass of a split or grouped extend: the workspace copy of each initial state, and the
 // block states of split requests (la_extend_seg.cu).  Launched when p.seg_len > 0 or p.group > 1.
 cudaError_t launch_block_states(const ExtendParams &p, cudaStream_t stream);

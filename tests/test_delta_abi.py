@@ -19,8 +19,9 @@ def lib():
 
 
 def extend(lib, q=OK, k=OK, v=OK, rs=(0, 0, 0), g=OK, beta=OK, pool=OK, slots=4, idx=OK, cu=OK, pm=OK,
-           out=OK, B=1, T=8, H=2, Hk=1, D=128, ms=8):
-    return lib.la_delta_extend(q, k, v, *rs, g, beta, pool, slots, idx, cu, pm, out, B, T, H, Hk, D, ms, 0, N)
+           out=OK, B=1, T=8, H=2, Hk=1, D=128, ms=8, ws=OK, nbytes=1 << 30):
+    return lib.la_delta_extend(q, k, v, *rs, g, beta, pool, slots, idx, cu, pm, out, B, T, H, Hk, D, ms, 0, ws,
+                               nbytes, N)
 
 
 def decode(lib, q=OK, k=OK, v=OK, rs=(0, 0, 0), g=OK, beta=OK, pool=OK, slots=4, idx=OK, out=OK, B=2, H=2,
@@ -72,6 +73,8 @@ def test_null_and_misaligned_pointers(lib):
             assert call(lib, **{name: BAD4}) == 1, (call, name)
             assert call(lib, **{name: N}) == 1, (call, name)
     assert extend(lib, pm=N) == 1
+    assert extend(lib, ws=N) == 1 and extend(lib, ws=BAD16) == 1
+    assert extend(lib, nbytes=la.delta_extend_workspace_size(1, 8, 2, 128) - 1) == 1
     for call in (pack, unpack):
         for name, bad in (("pool", BAD16), ("codes", BAD16), ("scales", BAD4), ("idx", BAD4), ("sidx", BAD4)):
             assert call(lib, **{name: bad}) == 1, (call, name)
@@ -89,6 +92,23 @@ def _cpu(rows=4, Hk=1, H=2):
     bf = lambda w: torch.zeros(rows, w, dtype=torch.bfloat16)  # noqa: E731
     return (bf(Hk * 128), bf(Hk * 128), bf(H * 128), torch.zeros(rows, H), torch.zeros(rows, H),
             torch.zeros(3, H, 128, 128), torch.zeros(rows, dtype=torch.int32))
+
+
+def test_workspace_size(lib):
+    nb = ctypes.c_size_t(7)
+    size = lib.la_delta_extend_workspace_size
+    assert size(1, 1, 1, 64, ctypes.byref(nb)) == 2
+    assert size(-1, 1, 1, 128, ctypes.byref(nb)) == 1 and size(1, -1, 1, 128, ctypes.byref(nb)) == 1
+    assert size(1, 1, 0, 128, ctypes.byref(nb)) == 1 and size(1, 1, 1, 128, None) == 1
+    assert size(0, 0, 1, 128, ctypes.byref(nb)) == 0 and nb.value == 0
+    one = la.delta_extend_workspace_size(1, 64, 1, 128)
+    assert one > 0 and la.delta_extend_workspace_size(3, 1000, 4, 128) % 16 == 0
+    # enough slots for every way to cut T tokens into B requests
+    for lens in ([1, 1, 1], [64, 64, 64], [63, 65, 1], [0, 0, 129], [128, 127, 2]):
+        base = [sum(lens[:b]) // 64 + b for b in range(3)]
+        chunks = [-(-n // 64) for n in lens]
+        ends = [x + y for x, y in zip(base, chunks)]
+        assert all(e <= s for e, s in zip(ends, base[1:] + [sum(lens) // 64 + 3]))
 
 
 def test_binding_refuses_before_the_library():
