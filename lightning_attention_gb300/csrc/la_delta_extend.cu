@@ -108,12 +108,12 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= SZ_BAR, "barrier block");
 
-// Shared memory of the T kernel.  16 x 16 blocks of the inversion are two panels of 8 columns x 16 rows x
-// 16 bytes: the blocks of A below the diagonal (hi, lo) and the diagonal blocks of T (hi, lo; before that
-// A's in fp32, transposed).  T' takes the place of K and Q once every block is formed.
-constexpr uint32_t TK_KQ = 0;                              // [64 K rows; 64 Q rows][128]; T' hi, lo
-constexpr uint32_t TK_P = 32768;                           // [64][64] hi, lo: P, then P T
-constexpr uint32_t TK_AB = TK_P + 16384;                   // 6 x (512 hi + 512 lo)
+// Shared memory of the T kernel (five CTAs per SM).  16 x 16 blocks of the inversion are two panels of 8
+// columns x 16 rows x 16 bytes: the blocks of A below the diagonal (hi, lo) and the diagonal blocks of T
+// (hi, lo; before that A's, transposed, and T's in fp32).  T' and P T take the place of K and Q.
+constexpr uint32_t TK_KQ = 0;                              // [64 K rows; 64 Q rows][128]
+constexpr uint32_t TK_T = 0, TK_P = 16384;                 // [64][64] hi, lo each: T'; P, then P T
+constexpr uint32_t TK_AB = 32768;                          // 6 x (512 hi + 512 lo)
 constexpr uint32_t TK_TD = TK_AB + 6 * 1024;               // 4 x (512 hi + 512 lo)
 constexpr uint32_t TK_TOK = TK_TD + 4 * 1024;              // per token: ghi, glo, rk, beta rk, scale rq
 constexpr uint32_t kTSmemBytes = TK_TOK + 5 * 256 + 1024;
@@ -226,39 +226,116 @@ __device__ __forceinline__ uint32_t sw_row(uint32_t tile, int rho, int kc) {
     return tile + (uint32_t)rho * 128u + ((uint32_t)(kc ^ (rho & 7)) << 4);
 }
 
-// acc += X_rows Y_rows^T over the 128 columns of a [K; Q] tile: rows ra .. + 15 against rows rb .. + 15;
-// a second row block ra2 shares the loads of rb's fragments.
+// acc = X_rows Y_rows^T over the 128 columns of the [K; Q] tile: rows ra .. + 15 against rows rb .. + 15;
+// with kTwo, acc2 the same for rows ra2 .. + 15, which share the loads of rb's fragments.  The tile starts
+// on a 1024-byte boundary and row blocks on multiples of 16, so the swizzle is an exclusive or of a lane's
+// address with the piece.
 template <bool kTwo>
-__device__ __forceinline__ void dot_rows(float (&acc)[8], float (&acc2)[8], uint32_t tile, int ra, int ra2,
-                                         int rb, int lane) {
+__device__ __forceinline__ void dot_rows(float *acc, float *acc2, uint32_t tile, int ra, int ra2, int rb,
+                                         int lane) {
     const int mrow = lane & 7, midx = lane >> 3;
     const int ar = (midx & 1) * 8 + mrow, ak = midx >> 1;   // A operand: matrices (k half, row half)
     const int br = (midx >> 1) * 8 + mrow, bk = midx & 1;   // B operand: matrices (n half, k half)
+    const uint32_t pb = (tile + (uint32_t)(rb + br) * 128u) | (uint32_t)((bk ^ mrow) << 4);
+    const uint32_t pa = (tile + (uint32_t)(ra + ar) * 128u) | (uint32_t)((ak ^ mrow) << 4);
+    const uint32_t pa2 = (tile + (uint32_t)(ra2 + ar) * 128u) | (uint32_t)((ak ^ mrow) << 4);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    if (kTwo) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc2[e] = 0.f;
+    for (int e = 0; e < 8; ++e) {
+        acc[e] = 0.f;
+        if (kTwo) acc2[e] = 0.f;
     }
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
-        const uint32_t blk = tile + (ks >> 2) * 16384u;
-        const int kc = (ks & 3) * 2;
+        const uint32_t piece = (ks & 3) * 32u, blk = (ks >> 2) * 16384u;
         uint32_t fa[4], fb[4];
-        ldsm4(sw_row(blk, rb + br, kc + bk), fb);
-        ldsm4(sw_row(blk, ra + ar, kc + ak), fa);
+        ldsm4((pb ^ piece) + blk, fb);
+        ldsm4((pa ^ piece) + blk, fa);
         mma_16816(acc, fa, fb[0], fb[1]);
         mma_16816(acc + 4, fa, fb[2], fb[3]);
         if (kTwo) {
-            ldsm4(sw_row(blk, ra2 + ar, kc + ak), fa);
+            ldsm4((pa2 ^ piece) + blk, fa);
             mma_16816(acc2, fa, fb[0], fb[1]);
             mma_16816(acc2 + 4, fa, fb[2], fb[3]);
         }
     }
 }
 
+// A fragment block (16 x 16) as a bf16 pair into rows rho0 .. + 15, pieces kc and kc + 1 of a swizzled
+// [64][64] tile, its lo part 8 KiB behind.
+__device__ __forceinline__ void put_block(uint8_t *tile, int rho0, int kc, int row, int cp, const float *x) {
+    const int rho = rho0 + row;  // and rho + 8: the same rho % 8
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+        uint32_t h0, l0, h1, l1;
+        split2(x[4 * hf], x[4 * hf + 1], h0, l0);
+        split2(x[4 * hf + 2], x[4 * hf + 3], h1, l1);
+        uint8_t *dst = tile + rho * 128 + (((kc + hf) ^ (rho & 7)) << 4) + cp * 2;
+        *reinterpret_cast<uint32_t *>(dst) = h0;
+        *reinterpret_cast<uint32_t *>(dst + 1024) = h1;
+        *reinterpret_cast<uint32_t *>(dst + 8192) = l0;
+        *reinterpret_cast<uint32_t *>(dst + 8192 + 1024) = l1;
+    }
+}
+// The same into a scratch block (two panels of 8 columns; lo 512 bytes behind).
+__device__ __forceinline__ void put_panel(uint8_t *blk, int row, int cp, const float *x) {
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+        uint32_t h0, l0, h1, l1;
+        split2(x[4 * hf], x[4 * hf + 1], h0, l0);
+        split2(x[4 * hf + 2], x[4 * hf + 3], h1, l1);
+        uint8_t *dst = blk + hf * 256 + row * 16 + cp * 2;
+        *reinterpret_cast<uint32_t *>(dst) = h0;
+        *reinterpret_cast<uint32_t *>(dst + 128) = h1;
+        *reinterpret_cast<uint32_t *>(dst + 512) = l0;
+        *reinterpret_cast<uint32_t *>(dst + 640) = l1;
+    }
+}
+
+// Per-token factors of the T kernel's blocks.
+struct TokenFactors {
+    const float *ghi, *glo, *rk, *brk, *qs;
+};
+
+// Block (a, b): kk and qk become A's and P's elements (above the diagonal zero, A's diagonal too).
+__device__ __forceinline__ void scale_block(const TokenFactors &f, int a, int b, int row, int cp, float *kk,
+                                            float *qk) {
+    const int i0 = 16 * a + row, i1 = i0 + 8;
+    const float gh0 = f.ghi[i0], gh1 = f.ghi[i1], gl0 = f.glo[i0], gl1 = f.glo[i1];
+    const float ai0 = f.brk[i0], ai1 = f.brk[i1], qi0 = f.qs[i0], qi1 = f.qs[i1];
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+        const int j = 16 * b + 8 * hf + cp;
+        const float2 gh = *reinterpret_cast<const float2 *>(f.ghi + j);
+        const float2 gl = *reinterpret_cast<const float2 *>(f.glo + j);
+        const float2 rj = *reinterpret_cast<const float2 *>(f.rk + j);
+        const float e00 = ex2((gh0 - gh.x) + (gl0 - gl.x)) * rj.x;
+        const float e01 = ex2((gh0 - gh.y) + (gl0 - gl.y)) * rj.y;
+        const float e10 = ex2((gh1 - gh.x) + (gl1 - gl.x)) * rj.x;
+        const float e11 = ex2((gh1 - gh.y) + (gl1 - gl.y)) * rj.y;
+        float *k = kk + 4 * hf, *q = qk + 4 * hf;
+        k[0] *= e00 * ai0;
+        k[1] *= e01 * ai0;
+        k[2] *= e10 * ai1;
+        k[3] *= e11 * ai1;
+        q[0] *= e00 * qi0;
+        q[1] *= e01 * qi0;
+        q[2] *= e10 * qi1;
+        q[3] *= e11 * qi1;
+        if (a == b) {
+            if (j >= i0) k[0] = 0.f;
+            if (j + 1 >= i0) k[1] = 0.f;
+            if (j >= i1) k[2] = 0.f;
+            if (j + 1 >= i1) k[3] = 0.f;
+            if (j > i0) q[0] = 0.f;
+            if (j + 1 > i0) q[1] = 0.f;
+            if (j > i1) q[2] = 0.f;
+            if (j + 1 > i1) q[3] = 0.f;
+        }
+    }
+}
+
 // T', P T and the coefficients of one chunk and head (blockIdx.x = slot * H + head).
-__global__ void __launch_bounds__(kTThreads) delta_t_kernel(const DeltaParams p, uint8_t *ws) {
+__global__ void __launch_bounds__(kTThreads, 5) delta_t_kernel(const DeltaParams p, uint8_t *ws) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int w = threadIdx.x >> 5;
@@ -294,7 +371,7 @@ __global__ void __launch_bounds__(kTThreads) delta_t_kernel(const DeltaParams p,
 
     float *tok = reinterpret_cast<float *>(sm + TK_TOK);
     float *ghi = tok, *glo = tok + 64, *rk = tok + 128, *brk = tok + 192, *qs = tok + 256;
-    uint8_t *abp = sm + TK_AB, *tdp = sm + TK_TD, *tp = sm + TK_KQ, *pp = sm + TK_P;
+    uint8_t *abp = sm + TK_AB, *tdp = sm + TK_TD, *tp = sm + TK_T, *pp = sm + TK_P;
     const uint32_t ab = smem_u32(abp), td = smem_u32(tdp), kq = smem_u32(sm + TK_KQ), tt = kq;
     const uint32_t pt = smem_u32(pp);
     float *ad = reinterpret_cast<float *>(tdp + w * 1024);
@@ -341,240 +418,185 @@ __global__ void __launch_bounds__(kTThreads) delta_t_kernel(const DeltaParams p,
     x1 += __shfl_sync(0xffffffffu, x0, 31);
     const long long xend = __shfl_sync(0xffffffffu, x1, 31);
     const long long xi = __shfl_sync(0xffffffffu, w < 2 ? x0 : x1, i16 & 31);
-    // the blocks of P and P T above the diagonal are zero (those of T' follow below)
-    for (int x = threadIdx.x; x < 16384 / 16; x += kTThreads)
-        reinterpret_cast<uint4 *>(pp)[x] = make_uint4(0u, 0u, 0u, 0u);
     cp_async_wait_all();
     __syncthreads();
 
-        // ---- K K^T and Q K^T of the diagonal block; norms
-        float kk[8], qk[8];
-        dot_rows<true>(kk, qk, kq, 16 * w, 64 + 16 * w, 16 * w, lane);
-        float nk = 1.f, nq = 1.f;  // squared norms of token i16
-        if (p.l2norm) {
-            float qq[8], none[8];
-            dot_rows<false>(qq, none, kq, 64 + 16 * w, 0, 64 + 16 * w, lane);
-            // element (i, i) of a fragment block: rows 0-7 in lane 4 i + i / 2, rows 8-15 likewise
-            const int src = 4 * (lane & 7) + ((lane & 7) >> 1);
-            const float k0 = __shfl_sync(0xffffffffu, row & 1 ? kk[1] : kk[0], src);
-            const float k1 = __shfl_sync(0xffffffffu, row & 1 ? kk[7] : kk[6], src);
-            const float q0 = __shfl_sync(0xffffffffu, row & 1 ? qq[1] : qq[0], src);
-            const float q1 = __shfl_sync(0xffffffffu, row & 1 ? qq[7] : qq[6], src);
-            nk = (lane & 8 ? k1 : k0) + kDeltaEps;
-            nq = (lane & 8 ? q1 : q0) + kDeltaEps;
+    // ---- K K^T and Q K^T of the warp's blocks: the diagonal one (w, w), then (2,0) (3,0) | (1,0) |
+    // (2,1) (3,1) | (3,2); norms from the diagonals of K K^T and Q Q^T
+    const int a1 = w == 0 ? 2 : w == 1 ? 1 : w == 2 ? 2 : 3, b1 = w == 0 ? 0 : w - 1;
+    float kk[3][8], qk[3][8];
+    dot_rows<true>(kk[0], qk[0], kq, 16 * w, 64 + 16 * w, 16 * w, lane);
+    float nk = 1.f, nq = 1.f;  // squared norms of token i16
+    if (p.l2norm) {
+        dot_rows<false>(kk[1], nullptr, kq, 64 + 16 * w, 0, 64 + 16 * w, lane);
+        // element (i, i) of a fragment block: rows 0-7 in lane 4 i + i / 2, rows 8-15 likewise
+        const int src = 4 * (lane & 7) + ((lane & 7) >> 1);
+        const float k0 = __shfl_sync(0xffffffffu, row & 1 ? kk[0][1] : kk[0][0], src);
+        const float k1 = __shfl_sync(0xffffffffu, row & 1 ? kk[0][7] : kk[0][6], src);
+        const float q0 = __shfl_sync(0xffffffffu, row & 1 ? kk[1][1] : kk[1][0], src);
+        const float q1 = __shfl_sync(0xffffffffu, row & 1 ? kk[1][7] : kk[1][6], src);
+        nk = (lane & 8 ? k1 : k0) + kDeltaEps;
+        nq = (lane & 8 ? q1 : q0) + kDeltaEps;
+    }
+    {
+        const float inv = 1.f / sqrtf(lane < 16 ? nk : nq);
+        const float gam = ex2((float)xi * kFixedStep);
+        if (lane < 16) {
+            const float hi = (float)xi;
+            ghi[i16] = hi * kFixedStep;
+            glo[i16] = (float)(xi - __float2ll_rn(hi)) * kFixedStep;
+            rk[i16] = inv;
+            brk[i16] = beta * inv;
+            cf[i16] = beta;
+            cf[64 + i16] = -beta * gam * inv;
+            cf[128 + i16] = ex2((float)(xend - xi) * kFixedStep) * inv;
+        } else {
+            qs[i16] = kScale * inv;
+            cf[192 + i16] = kScale * gam * inv;
         }
-        {
-            const float inv = 1.f / sqrtf(lane < 16 ? nk : nq);
-            const float gam = ex2((float)xi * kFixedStep);
-            if (lane < 16) {
-                const float hi = (float)xi;
-                ghi[i16] = hi * kFixedStep;
-                glo[i16] = (float)(xi - __float2ll_rn(hi)) * kFixedStep;
-                rk[i16] = inv;
-                brk[i16] = beta * inv;
-                cf[i16] = beta;
-                cf[64 + i16] = -beta * gam * inv;
-                cf[128 + i16] = ex2((float)(xend - xi) * kFixedStep) * inv;
-            } else {
-                qs[i16] = kScale * inv;
-                cf[192 + i16] = kScale * gam * inv;
-            }
-            if (w == 0 && lane == 0) cf[256] = ex2((float)xend * kFixedStep);
-        }
-        __syncthreads();
+        if (w == 0 && lane == 0) cf[256] = ex2((float)xend * kFixedStep);
+    }
+    dot_rows<true>(kk[1], qk[1], kq, 16 * a1, 64 + 16 * a1, 16 * b1, lane);
+    if (!(w & 1)) dot_rows<true>(kk[2], qk[2], kq, 48, 64 + 48, 16 * b1, lane);
+    __syncthreads();  // K and Q are read: P and T' take their place
 
-        // ---- scaled blocks: A to scratch, P into the tile's lower half.  Warp w takes diagonal block
-        // w; the blocks below the diagonal go (2,0) (3,0) | (1,0) | (2,1) (3,1) | (3,2).
-#pragma unroll 1
-        for (int x = 0; x < 3; ++x) {
-            int a = w, b = w;
-            if (x > 0) {
-                if (x == 2 && (w & 1)) break;
-                a = w == 0 ? 1 + x : w == 1 ? 1 : w == 2 ? 1 + x : 3;
-                b = w == 0 ? 0 : w == 1 ? 0 : w == 2 ? 1 : 2;
-                dot_rows<true>(kk, qk, kq, 16 * a, 64 + 16 * a, 16 * b, lane);
-            }
-            const int i0 = 16 * a + row, i1 = i0 + 8;
-            const float gh0 = ghi[i0], gh1 = ghi[i1], gl0 = glo[i0], gl1 = glo[i1];
-            const float ai0 = brk[i0], ai1 = brk[i1], qi0 = qs[i0], qi1 = qs[i1];
+    // ---- scaled blocks: A to scratch, P to its tile, whose blocks above the diagonal are zero, as T''s
+    {
+        const TokenFactors f{ghi, glo, rk, brk, qs};
+        scale_block(f, w, w, row, cp, kk[0], qk[0]);
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int j = 16 * b + 8 * hf + cp;
-                const float2 gh = *reinterpret_cast<const float2 *>(ghi + j);
-                const float2 gl = *reinterpret_cast<const float2 *>(glo + j);
-                const float2 rj = *reinterpret_cast<const float2 *>(rk + j);
-                const float e00 = ex2((gh0 - gh.x) + (gl0 - gl.x)) * rj.x;
-                const float e01 = ex2((gh0 - gh.y) + (gl0 - gl.y)) * rj.y;
-                const float e10 = ex2((gh1 - gh.x) + (gl1 - gl.x)) * rj.x;
-                const float e11 = ex2((gh1 - gh.y) + (gl1 - gl.y)) * rj.y;
-                float a00 = kk[4 * hf] * (e00 * ai0);
-                float a01 = kk[4 * hf + 1] * (e01 * ai0);
-                float a10 = kk[4 * hf + 2] * (e10 * ai1);
-                float a11 = kk[4 * hf + 3] * (e11 * ai1);
-                float p00 = qk[4 * hf] * (e00 * qi0);
-                float p01 = qk[4 * hf + 1] * (e01 * qi0);
-                float p10 = qk[4 * hf + 2] * (e10 * qi1);
-                float p11 = qk[4 * hf + 3] * (e11 * qi1);
-                if (a == b) {
-                    if (j > i0) p00 = 0.f;
-                    if (j + 1 > i0) p01 = 0.f;
-                    if (j > i1) p10 = 0.f;
-                    if (j + 1 > i1) p11 = 0.f;
-                    const int m = 8 * hf + cp;
-                    ad[m * 16 + row] = j < i0 ? a00 : 0.f;
-                    ad[(m + 1) * 16 + row] = j + 1 < i0 ? a01 : 0.f;
-                    ad[m * 16 + row + 8] = j < i1 ? a10 : 0.f;
-                    ad[(m + 1) * 16 + row + 8] = j + 1 < i1 ? a11 : 0.f;
-                } else {
-                    uint32_t h0, l0, h1, l1;
-                    split2(a00, a01, h0, l0);
-                    split2(a10, a11, h1, l1);
-                    uint8_t *blk = abp + (a * (a - 1) / 2 + b) * 1024 + hf * 256 + row * 16 + cp * 2;
-                    *reinterpret_cast<uint32_t *>(blk) = h0;
-                    *reinterpret_cast<uint32_t *>(blk + 128) = h1;
-                    *reinterpret_cast<uint32_t *>(blk + 512) = l0;
-                    *reinterpret_cast<uint32_t *>(blk + 640) = l1;
-                }
-                uint32_t h0, l0, h1, l1;
-                split2(p00, p01, h0, l0);
-                split2(p10, p11, h1, l1);
-                const int rho = 16 * a + row;  // and rho + 8: the same rho % 8
-                uint8_t *dst = pp + rho * 128 + (((2 * b + hf) ^ (rho & 7)) << 4) + cp * 2;
-                *reinterpret_cast<uint32_t *>(dst) = h0;
-                *reinterpret_cast<uint32_t *>(dst + 1024) = h1;
-                *reinterpret_cast<uint32_t *>(dst + 8192) = l0;
-                *reinterpret_cast<uint32_t *>(dst + 8192 + 1024) = l1;
+        for (int e = 0; e < 8; ++e)  // transposed: column m of A's block at ad + 16 m
+            ad[(8 * (e >> 2) + cp + (e & 1)) * 16 + row + 8 * ((e >> 1) & 1)] = kk[0][e];
+        put_block(pp, 16 * w, 2 * w, row, cp, qk[0]);
+        scale_block(f, a1, b1, row, cp, kk[1], qk[1]);
+        put_panel(abp + (a1 * (a1 - 1) / 2 + b1) * 1024, row, cp, kk[1]);
+        put_block(pp, 16 * a1, 2 * b1, row, cp, qk[1]);
+        if (!(w & 1)) {
+            scale_block(f, 3, b1, row, cp, kk[2], qk[2]);
+            put_panel(abp + (3 + b1) * 1024, row, cp, kk[2]);
+            put_block(pp, 48, 2 * b1, row, cp, qk[2]);
+        }
+        for (int z = lane; z < 512; z += 32) {  // (tile, part, piece, row) of row block w
+            const int rho = 16 * w + (z & 15), kc = (z >> 4) & 7;
+            if (kc >= 2 * w + 2)
+                *reinterpret_cast<uint4 *>(sm + (z >> 7) * 8192 + rho * 128 + ((kc ^ (rho & 7)) << 4)) =
+                    make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+    __syncwarp();
+
+    // ---- the diagonal block of T: column j = lane % 16 by substitution
+    {
+        float x[16];
+        const int j = lane & 15;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = i == j ? 1.f : 0.f;
+#pragma unroll
+        for (int m = 0; m < 15; ++m) {
+#pragma unroll
+            for (int v4 = (m + 1) / 4; v4 < 4; ++v4) {
+                const float4 f = *reinterpret_cast<const float4 *>(ad + m * 16 + 4 * v4);
+                if (4 * v4 > m) x[4 * v4] = fmaf(-f.x, x[m], x[4 * v4]);
+                if (4 * v4 + 1 > m) x[4 * v4 + 1] = fmaf(-f.y, x[m], x[4 * v4 + 1]);
+                if (4 * v4 + 2 > m) x[4 * v4 + 2] = fmaf(-f.z, x[m], x[4 * v4 + 2]);
+                if (4 * v4 + 3 > m) x[4 * v4 + 3] = fmaf(-f.w, x[m], x[4 * v4 + 3]);
             }
         }
         __syncwarp();
+        if (lane < 16) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) ad[i * 16 + j] = x[i];
+        }
+        __syncwarp();
+        float t[8];  // the block in fragment layout
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            const float2 f = *reinterpret_cast<const float2 *>(ad + (row + 8 * ((e >> 1) & 1)) * 16 +
+                                                               8 * (e >> 2) + cp);
+            t[e] = f.x;
+            t[e + 1] = f.y;
+        }
+        __syncwarp();
+        put_panel(tdp + w * 1024, row, cp, t);
+        // the operand tile holds T' = T - I
+        if (row == cp) t[0] = t[6] = 0.f;
+        if (row == cp + 1) t[1] = t[7] = 0.f;
+        put_block(tp, 16 * w, 2 * w, row, cp, t);
+    }
+    __syncthreads();  // all blocks of A, all diagonal blocks of T
 
-        // ---- the diagonal block of T: column j = lane % 16 by substitution
-        {
-            float x[16];
-            const int j = lane & 15;
+    // ---- column block b = w of T below the diagonal, as its transpose:
+    // T_rb^T = -(sum_{b <= m < r} T_mb^T A_rm^T) T_rr^T
+    {
+        const int b = w;
+        uint32_t yh[3][4], yl[3][4];
+        ldsm4_t(td + b * 1024 + off_p, yh[0]);
+        ldsm4_t(td + b * 1024 + 512 + off_p, yl[0]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = i == j ? 1.f : 0.f;
+        for (int dr = 1; dr < 4; ++dr) {
+            const int rr = b + dr;
+            if (rr > 3) break;
+            float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            uint32_t bh[4], bl[4];
 #pragma unroll
-            for (int m = 0; m < 15; ++m) {
+            for (int dm = 0; dm < dr; ++dm) {
+                const uint32_t blk = ab + (rr * (rr - 1) / 2 + b + dm) * 1024 + off_p;
+                ldsm4(blk, bh);
+                ldsm4(blk + 512, bl);
+                prod16(acc, yh[dm], yl[dm], bh, bl);
+            }
+            uint32_t zh[4], zl[4];
+            split_frag(acc, zh, zl);
+            float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            ldsm4(td + rr * 1024 + off_p, bh);
+            ldsm4(td + rr * 1024 + 512 + off_p, bl);
+            prod16(t, zh, zl, bh, bl);
 #pragma unroll
-                for (int v4 = (m + 1) / 4; v4 < 4; ++v4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(ad + m * 16 + 4 * v4);
-                    if (4 * v4 > m) x[4 * v4] = fmaf(-f.x, x[m], x[4 * v4]);
-                    if (4 * v4 + 1 > m) x[4 * v4 + 1] = fmaf(-f.y, x[m], x[4 * v4 + 1]);
-                    if (4 * v4 + 2 > m) x[4 * v4 + 2] = fmaf(-f.z, x[m], x[4 * v4 + 2]);
-                    if (4 * v4 + 3 > m) x[4 * v4 + 3] = fmaf(-f.w, x[m], x[4 * v4 + 3]);
+            for (int e = 0; e < 8; ++e) t[e] = -t[e];
+            split_frag(t, zh, zl);
+            // matrices (j half, i half) -> rows i of the tile, columns 16 b + j
+            const uint32_t at = sw_row(tt, 16 * rr + 8 * (midx >> 1) + mrow, 2 * b + (midx & 1));
+            stsm4_t(at, zh);
+            stsm4_t(at + 8192, zl);
+            if (dr < 3) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    yh[dr][e] = zh[e];
+                    yl[dr][e] = zl[e];
                 }
             }
-            __syncthreads();  // A's diagonal blocks and K, Q are read: T's blocks and T' take their place
-            // the blocks of T' above the diagonal are zero
-            for (int z = lane; z < 256; z += 32) {  // (part, piece, row)
-                const int rho = 16 * w + (z & 15), kc = (z >> 4) & 7;
-                if (kc >= 2 * w + 2)
-                    *reinterpret_cast<uint4 *>(tp + (z >> 7) * 8192 + rho * 128 + ((kc ^ (rho & 7)) << 4)) =
-                        make_uint4(0u, 0u, 0u, 0u);
-            }
-            // lanes 0-15 keep the hi parts, lanes 16-31 the lo parts; the operand tile holds T' = T - I
-            uint8_t *dst = tdp + w * 1024 + (lane >> 4) * 512 + (j >> 3) * 256 + (j & 7) * 2;
-            uint8_t *tile = tp + (lane >> 4) * 8192 + (j & 7) * 2;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const __nv_bfloat16 hi = __float2bfloat16_rn(x[i]);
-                const __nv_bfloat16 lo = __float2bfloat16_rn(x[i] - __bfloat162float(hi));
-                const __nv_bfloat16 part = lane < 16 ? hi : lo;
-                *reinterpret_cast<__nv_bfloat16 *>(dst + i * 16) = part;
-                const int rho = 16 * w + i;
-                *reinterpret_cast<__nv_bfloat16 *>(tile + rho * 128 +
-                                                   (((2 * w + (j >> 3)) ^ (rho & 7)) << 4)) =
-                    i > j ? part : __float2bfloat16_rn(0.f);
-            }
         }
-        __syncthreads();  // all diagonal blocks
+    }
+    __syncthreads();  // T'
 
-        // ---- column block b = w of T below the diagonal, as its transpose:
-        // T_rb^T = -(sum_{b <= m < r} T_mb^T A_rm^T) T_rr^T
-        {
-            const int b = w;
-            uint32_t yh[3][4], yl[3][4];
-            ldsm4_t(td + b * 1024 + off_p, yh[0]);
-            ldsm4_t(td + b * 1024 + 512 + off_p, yl[0]);
+    // ---- row block w of P T, over P
+    {
+        uint32_t fh[4][4], fl[4][4];
 #pragma unroll
-            for (int dr = 1; dr < 4; ++dr) {
-                const int rr = b + dr;
-                if (rr > 3) break;
-                float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int m = 0; m < 4; ++m) {
+            if (m > w) break;
+            const uint32_t pa = sw_row(pt, 16 * w + (midx & 1) * 8 + mrow, 2 * m + (midx >> 1));
+            ldsm4(pa, fh[m]);
+            ldsm4(pa + 8192, fl[m]);
+        }
+        __syncwarp();
+        const int k = (midx & 1) * 8 + mrow, nh = midx >> 1;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            if (b > w) break;
+            float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int m = b; m < 4; ++m) {
+                if (m > w) break;
                 uint32_t bh[4], bl[4];
-#pragma unroll
-                for (int dm = 0; dm < dr; ++dm) {
-                    const uint32_t blk = ab + (rr * (rr - 1) / 2 + b + dm) * 1024 + off_p;
-                    ldsm4(blk, bh);
-                    ldsm4(blk + 512, bl);
-                    prod16(acc, yh[dm], yl[dm], bh, bl);
-                }
-                uint32_t zh[4], zl[4];
-                split_frag(acc, zh, zl);
-                float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                ldsm4(td + rr * 1024 + off_p, bh);
-                ldsm4(td + rr * 1024 + 512 + off_p, bl);
-                prod16(t, zh, zl, bh, bl);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) t[e] = -t[e];
-                split_frag(t, zh, zl);
-                // matrices (j half, i half) -> rows i of the tile, columns 16 b + j
-                const uint32_t at = sw_row(tt, 16 * rr + 8 * (midx >> 1) + mrow, 2 * b + (midx & 1));
-                stsm4_t(at, zh);
-                stsm4_t(at + 8192, zl);
-                if (dr < 3) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        yh[dr][e] = zh[e];
-                        yl[dr][e] = zl[e];
-                    }
-                }
+                const uint32_t at = m == b ? td + b * 1024 + nh * 256 + k * 16 : sw_row(tt, 16 * m + k, 2 * b + nh);
+                ldsm4_t(at, bh);
+                ldsm4_t(at + (m == b ? 512 : 8192), bl);
+                prod16(acc, fh[m], fl[m], bh, bl);
             }
+            put_block(pp, 16 * w, 2 * b, row, cp, acc);
         }
-        __syncthreads();  // T'
-
-        // ---- row block a = w of P T, over P: block b needs P's blocks b and later
-        {
-            const int a = w;
-#pragma unroll 1
-            for (int b = 0; b <= a; ++b) {
-                float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-                for (int m = b; m <= a; ++m) {
-                    uint32_t fh[4], fl[4], bh[4], bl[4];
-                    const uint32_t pa =
-                        sw_row(pt, 16 * a + (midx & 1) * 8 + mrow, 2 * m + (midx >> 1));
-                    ldsm4(pa, fh);
-                    ldsm4(pa + 8192, fl);
-                    const int k = (midx & 1) * 8 + mrow, nh = midx >> 1;
-                    if (m == b) {
-                        const uint32_t at = td + b * 1024 + nh * 256 + k * 16;
-                        ldsm4_t(at, bh);
-                        ldsm4_t(at + 512, bl);
-                    } else {
-                        const uint32_t at = sw_row(tt, 16 * m + k, 2 * b + nh);
-                        ldsm4_t(at, bh);
-                        ldsm4_t(at + 8192, bl);
-                    }
-                    prod16(acc, fh, fl, bh, bl);
-                }
-                __syncwarp();
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    uint32_t h0, l0, h1, l1;
-                    split2(acc[4 * hf], acc[4 * hf + 1], h0, l0);
-                    split2(acc[4 * hf + 2], acc[4 * hf + 3], h1, l1);
-                    const int rho = 16 * a + row;
-                    uint8_t *dst = pp + rho * 128 + (((2 * b + hf) ^ (rho & 7)) << 4) + cp * 2;
-                    *reinterpret_cast<uint32_t *>(dst) = h0;
-                    *reinterpret_cast<uint32_t *>(dst + 1024) = h1;
-                    *reinterpret_cast<uint32_t *>(dst + 8192) = l0;
-                    *reinterpret_cast<uint32_t *>(dst + 8192 + 1024) = l1;
-                }
-                __syncwarp();
-            }
-        }
+    }
 
     // the tile to the workspace: [T' hi; P T hi], [T' lo; P T lo]
     __syncthreads();
@@ -599,6 +621,16 @@ __device__ __forceinline__ void put_pairs(uint32_t t, const uint64_t *x) {
     for (int e = 0; e < 8; ++e) split2(x[e], hi[e], lo[e]);
     tmem_st8(t, hi);
     tmem_st8(t + 8u, lo);
+}
+
+// 32 per-token coefficients (the same for all lanes).
+__device__ __forceinline__ void load_pairs(const float *src, uint64_t (&x)[16]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(src + 4 * e);
+        x[2 * e] = f.x;
+        x[2 * e + 1] = f.y;
+    }
 }
 
 __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx &cx, uint32_t tbase, int q,
@@ -631,14 +663,24 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
         const uint32_t par = c & 1, ph = (c >> 1) & 1;
         const int r = n - c * C;  // tokens from this chunk on
         const float *cf = reinterpret_cast<const float *>(sm + OFF_COEF + par * SZ_COEF) + tok0;
-        // ---- R = beta V - (beta gamma rk) X^K
+        // ---- R = beta V - (beta gamma rk) X^K; what needs no X is formed while its product runs
         if (!(ok = warp_wait(&bars->t_full[par], ph, cx))) break;
         if (!(ok = warp_wait(&bars->v_full[par], ph, cx))) break;
-        if (!(ok = warp_wait(&bars->x_full, par, cx))) break;
-        tc_fence_after();
-        uint64_t R[16];
+        uint64_t R[16], f[16];
         {
             const uint8_t *vp = sm + OFF_V + par * 16384 + tok0 * 256 + v * 2;
+            load_pairs(cf, R);
+            load_pairs(cf + 64, f);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+                const uint32_t v0 = *reinterpret_cast<const uint16_t *>(vp + (2 * x) * 256);
+                const uint32_t v1 = *reinterpret_cast<const uint16_t *>(vp + (2 * x + 1) * 256);
+                R[x] = mul2(R[x], f2u(v0 << 16, v1 << 16));
+            }
+        }
+        if (!(ok = warp_wait(&bars->x_full, par, cx))) break;
+        tc_fence_after();
+        {
             uint32_t w[2][16];
             tmem_ld16(tx, w[0]);
 #pragma unroll
@@ -646,19 +688,8 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
                 tmem_ld_wait_regs(w[y]);
                 if (y == 0) tmem_ld16(tx + 16u, w[1]);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int t4 = 4 * y + x;  // four tokens
-                    const float4 b = *reinterpret_cast<const float4 *>(cf + 4 * t4);
-                    const float4 bx = *reinterpret_cast<const float4 *>(cf + 64 + 4 * t4);
-                    uint32_t vv[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        vv[e] = (uint32_t)*reinterpret_cast<const uint16_t *>(vp + (4 * t4 + e) * 256) << 16;
-                    R[2 * t4] = fma2(f2(bx.x, bx.y), f2u(w[y][4 * x], w[y][4 * x + 1]),
-                                     mul2(f2(b.x, b.y), f2u(vv[0], vv[1])));
-                    R[2 * t4 + 1] = fma2(f2(bx.z, bx.w), f2u(w[y][4 * x + 2], w[y][4 * x + 3]),
-                                         mul2(f2(b.z, b.w), f2u(vv[2], vv[3])));
-                }
+                for (int x = 0; x < 8; ++x)
+                    R[8 * y + x] = fma2(f[8 * y + x], f2u(w[y][2 * x], w[y][2 * x + 1]), R[8 * y + x]);
                 if (r < C) {  // rows past the end hold other requests' values
 #pragma unroll
                     for (int x = 8 * y; x < 8 * y + 8; ++x) {
@@ -674,6 +705,7 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
         warp_arrive(&bars->r_ready, lane);
 
         // ---- U = R + T' R, scaled for the state update
+        load_pairs(cf + 128, f);
         if (!(ok = warp_wait(&bars->y_full, par, cx))) break;
         tc_fence_after();
         {
@@ -684,13 +716,9 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
                 tmem_ld_wait_regs(w[y]);
                 if (y == 0) tmem_ld16(ty + 16u, w[1]);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int t4 = 4 * y + x;
-                    const float4 u = *reinterpret_cast<const float4 *>(cf + 128 + 4 * t4);
-                    R[2 * t4] = mul2(f2(u.x, u.y), add2(R[2 * t4], f2u(w[y][4 * x], w[y][4 * x + 1])));
-                    R[2 * t4 + 1] =
-                        mul2(f2(u.z, u.w), add2(R[2 * t4 + 1], f2u(w[y][4 * x + 2], w[y][4 * x + 3])));
-                }
+                for (int x = 0; x < 8; ++x)
+                    R[8 * y + x] =
+                        mul2(f[8 * y + x], add2(R[8 * y + x], f2u(w[y][2 * x], w[y][2 * x + 1])));
                 put_pairs(ty + 16u * y, R + 8 * y);
             }
         }
