@@ -70,12 +70,19 @@ constexpr uint32_t kTmemCols = 512;
 // [U | O'], U likewise.
 constexpr uint32_t TM_S = 0, TM_X = 128, TM_Y = 256, TM_D = 384;
 
-// What the first kernel leaves per chunk and head: the operand tile [64 T' rows; 64 P T rows][64] as its hi
-// and its lo parts, in the layout the MMA reads, then the coefficients: beta, -beta gamma rk, lam rk and
-// scale gamma rq per token, gamma_C.
-constexpr uint32_t SZ_T = 16384;
+// What the first kernel leaves per chunk and head: [T'; P T] as its hi and its lo parts, then the
+// coefficients: beta, -beta gamma rk, lam rk and scale gamma rq per token, gamma_C.  A part is cut by
+// k-steps kk of 16 columns, of which only rows 16 kk .. 63 are not zero: per step first T''s rows, then
+// P T's, 32 bytes each, with the 16-byte pieces of a row swapped where the row's bit 2 is set (the 32-byte
+// swizzle that the MMA reads).
+constexpr uint32_t SZ_PART = 10240;
 constexpr uint32_t SZ_COEF = 4 * 256 + 16;
-constexpr uint32_t SZ_SLOT = 2 * SZ_T + SZ_COEF;
+constexpr uint32_t SZ_SLOT = 2 * SZ_PART + SZ_COEF;
+// Offset within a part of row 0 of T' (pt = 0) or P T (pt = 1) of step kk.
+__host__ __device__ constexpr uint32_t part_ofs(int kk, int pt) {
+    return (uint32_t)(4096 * kk - 512 * kk * (kk - 1) + pt * (2048 - 512 * kk) - 512 * kk);
+}
+static_assert(part_ofs(3, 1) + 64 * 32 == SZ_PART, "part layout");
 // Chunk slots of a batch: request b's start at floor(cu_seqlens[b] / C) + b, far enough from the next
 // request's for its ceil(length / C) chunks.
 __host__ __device__ inline long long chunk_slots(long long T, long long B) { return T / C + B; }
@@ -85,7 +92,9 @@ constexpr int kStages = 3;
 constexpr uint32_t SZ_KQ = 32768;                          // [64 K rows; 64 Q rows][128], swizzled
 constexpr uint32_t OFF_KQ = 0;
 constexpr uint32_t OFF_V = OFF_KQ + kStages * SZ_KQ;       // 2 x [64][128], rows of 256 bytes
-constexpr uint32_t OFF_T = OFF_V + 2 * 16384;              // 2 x a slot's tile, hi and lo
+// 2 x (hi, lo) x 4 k-steps x [64 T' rows; 64 P T rows][16], with the 32-byte swizzle
+constexpr uint32_t SZ_T = 16384;
+constexpr uint32_t OFF_T = OFF_V + 2 * 16384;
 constexpr uint32_t OFF_COEF = OFF_T + 4 * SZ_T;            // 2 x a slot's coefficients
 constexpr uint32_t OFF_BAR = OFF_COEF + 2 * SZ_COEF;
 constexpr uint32_t SZ_BAR = 256;
@@ -110,9 +119,9 @@ static_assert(sizeof(Bars) <= SZ_BAR, "barrier block");
 
 // Shared memory of the T kernel (five CTAs per SM).  16 x 16 blocks of the inversion are two panels of 8
 // columns x 16 rows x 16 bytes: the blocks of A below the diagonal (hi, lo) and the diagonal blocks of T
-// (hi, lo; before that A's, transposed, and T's in fp32).  T' and P T take the place of K and Q.
+// (hi, lo; before that A's, transposed, and T's in fp32).  The slot's two parts take the place of K and Q
+// (P before P T).
 constexpr uint32_t TK_KQ = 0;                              // [64 K rows; 64 Q rows][128]
-constexpr uint32_t TK_T = 0, TK_P = 16384;                 // [64][64] hi, lo each: T'; P, then P T
 constexpr uint32_t TK_AB = 32768;                          // 6 x (512 hi + 512 lo)
 constexpr uint32_t TK_TD = TK_AB + 6 * 1024;               // 4 x (512 hi + 512 lo)
 constexpr uint32_t TK_TOK = TK_TD + 4 * 1024;              // per token: ghi, glo, rk, beta rk, scale rq
@@ -226,54 +235,40 @@ __device__ __forceinline__ uint32_t sw_row(uint32_t tile, int rho, int kc) {
     return tile + (uint32_t)rho * 128u + ((uint32_t)(kc ^ (rho & 7)) << 4);
 }
 
-// acc = X_rows Y_rows^T over the 128 columns of the [K; Q] tile: rows ra .. + 15 against rows rb .. + 15;
-// with kTwo, acc2 the same for rows ra2 .. + 15, which share the loads of rb's fragments.  The tile starts
-// on a 1024-byte boundary and row blocks on multiples of 16, so the swizzle is an exclusive or of a lane's
-// address with the piece.
-template <bool kTwo>
-__device__ __forceinline__ void dot_rows(float *acc, float *acc2, uint32_t tile, int ra, int ra2, int rb,
-                                         int lane) {
-    const int mrow = lane & 7, midx = lane >> 3;
-    const int ar = (midx & 1) * 8 + mrow, ak = midx >> 1;   // A operand: matrices (k half, row half)
-    const int br = (midx >> 1) * 8 + mrow, bk = midx & 1;   // B operand: matrices (n half, k half)
-    const uint32_t pb = (tile + (uint32_t)(rb + br) * 128u) | (uint32_t)((bk ^ mrow) << 4);
-    const uint32_t pa = (tile + (uint32_t)(ra + ar) * 128u) | (uint32_t)((ak ^ mrow) << 4);
-    const uint32_t pa2 = (tile + (uint32_t)(ra2 + ar) * 128u) | (uint32_t)((ak ^ mrow) << 4);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        acc[e] = 0.f;
-        if (kTwo) acc2[e] = 0.f;
-    }
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks) {
-        const uint32_t piece = (ks & 3) * 32u, blk = (ks >> 2) * 16384u;
-        uint32_t fa[4], fb[4];
-        ldsm4((pb ^ piece) + blk, fb);
-        ldsm4((pa ^ piece) + blk, fa);
-        mma_16816(acc, fa, fb[0], fb[1]);
-        mma_16816(acc + 4, fa, fb[2], fb[3]);
-        if (kTwo) {
-            ldsm4((pa2 ^ piece) + blk, fa);
-            mma_16816(acc2, fa, fb[0], fb[1]);
-            mma_16816(acc2 + 4, fa, fb[2], fb[3]);
-        }
-    }
+// The fragments of rows 16 blk .. + 15 of the [K; Q] tile (Q: blk + 4) at k-step ks, as an A operand; as a
+// B operand the same registers are {0, 2} for columns 0-7 and {1, 3} for columns 8-15.  The tile starts on
+// a 1024-byte boundary and row blocks on multiples of 16, so the swizzle is an exclusive or of the lane's
+// address at = kq_lane() with the piece.
+__device__ __forceinline__ uint32_t kq_lane(uint32_t tile, int lane) {
+    const int mrow = lane & 7, midx = lane >> 3;  // matrices (k half, row half)
+    return (tile + (uint32_t)((midx & 1) * 8 + mrow) * 128u) | (uint32_t)(((midx >> 1) ^ mrow) << 4);
+}
+__device__ __forceinline__ void kq_frag(uint32_t at, int blk, int ks, uint32_t (&f)[4]) {
+    ldsm4((at ^ ((ks & 3) * 32u)) + (ks >> 2) * 16384u + blk * 2048u, f);
+}
+// acc (16 x 16) += A B^T of two such fragments.
+__device__ __forceinline__ void dot_frag(float *acc, const uint32_t (&a)[4], const uint32_t (&b)[4]) {
+    mma_16816(acc, a, b[0], b[2]);
+    mma_16816(acc + 4, a, b[1], b[3]);
 }
 
-// A fragment block (16 x 16) as a bf16 pair into rows rho0 .. + 15, pieces kc and kc + 1 of a swizzled
-// [64][64] tile, its lo part 8 KiB behind.
-__device__ __forceinline__ void put_block(uint8_t *tile, int rho0, int kc, int row, int cp, const float *x) {
-    const int rho = rho0 + row;  // and rho + 8: the same rho % 8
+// Address of a row's 16-byte piece kc (0, 1) in a part: row rho of T' or P T, columns of step kk.
+__device__ __forceinline__ uint32_t part_row(uint32_t part, int kk, int pt, int rho, int kc) {
+    return part + part_ofs(kk, pt) + (uint32_t)rho * 32u + ((uint32_t)(kc ^ ((rho >> 2) & 1)) << 4);
+}
+// A fragment block (16 x 16) as a bf16 pair: rows rho0 .. + 15 of step kk.
+__device__ __forceinline__ void put_block(uint8_t *parts, int kk, int pt, int rho0, int row, int cp,
+                                          const float *x) {
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
         uint32_t h0, l0, h1, l1;
         split2(x[4 * hf], x[4 * hf + 1], h0, l0);
         split2(x[4 * hf + 2], x[4 * hf + 3], h1, l1);
-        uint8_t *dst = tile + rho * 128 + (((kc + hf) ^ (rho & 7)) << 4) + cp * 2;
+        uint8_t *dst = parts + part_row(0, kk, pt, rho0 + row, hf) + cp * 2;
         *reinterpret_cast<uint32_t *>(dst) = h0;
-        *reinterpret_cast<uint32_t *>(dst + 1024) = h1;
-        *reinterpret_cast<uint32_t *>(dst + 8192) = l0;
-        *reinterpret_cast<uint32_t *>(dst + 8192 + 1024) = l1;
+        *reinterpret_cast<uint32_t *>(dst + 256) = h1;  // row + 8: the same swizzle
+        *reinterpret_cast<uint32_t *>(dst + SZ_PART) = l0;
+        *reinterpret_cast<uint32_t *>(dst + SZ_PART + 256) = l1;
     }
 }
 // The same into a scratch block (two panels of 8 columns; lo 512 bytes behind).
@@ -371,12 +366,11 @@ __global__ void __launch_bounds__(kTThreads, 5) delta_t_kernel(const DeltaParams
 
     float *tok = reinterpret_cast<float *>(sm + TK_TOK);
     float *ghi = tok, *glo = tok + 64, *rk = tok + 128, *brk = tok + 192, *qs = tok + 256;
-    uint8_t *abp = sm + TK_AB, *tdp = sm + TK_TD, *tp = sm + TK_T, *pp = sm + TK_P;
-    const uint32_t ab = smem_u32(abp), td = smem_u32(tdp), kq = smem_u32(sm + TK_KQ), tt = kq;
-    const uint32_t pt = smem_u32(pp);
+    uint8_t *abp = sm + TK_AB, *tdp = sm + TK_TD;
+    const uint32_t ab = smem_u32(abp), td = smem_u32(tdp), kq = smem_u32(sm + TK_KQ), parts = smem_u32(sm);
     float *ad = reinterpret_cast<float *>(tdp + w * 1024);
     uint8_t *slot_out = ws + (size_t)blockIdx.x * SZ_SLOT;
-    float *cf = reinterpret_cast<float *>(slot_out + 2 * SZ_T);
+    float *cf = reinterpret_cast<float *>(slot_out + 2 * SZ_PART);
     const int row = lane >> 2, cp = (lane & 3) * 2;  // fragment row, column pair
     const int mrow = lane & 7, midx = lane >> 3;     // ldmatrix: row, matrix
     const uint32_t off_p = (uint32_t)((midx & 1) * 256 + (midx >> 1) * 128 + mrow * 16);
@@ -421,20 +415,46 @@ __global__ void __launch_bounds__(kTThreads, 5) delta_t_kernel(const DeltaParams
     cp_async_wait_all();
     __syncthreads();
 
-    // ---- K K^T and Q K^T of the warp's blocks: the diagonal one (w, w), then (2,0) (3,0) | (1,0) |
-    // (2,1) (3,1) | (3,2); norms from the diagonals of K K^T and Q Q^T
-    const int a1 = w == 0 ? 2 : w == 1 ? 1 : w == 2 ? 2 : 3, b1 = w == 0 ? 0 : w - 1;
-    float kk[3][8], qk[3][8];
-    dot_rows<true>(kk[0], qk[0], kq, 16 * w, 64 + 16 * w, 16 * w, lane);
+    // ---- K K^T and Q K^T of the warp's blocks (a, b): the diagonal one (w, w), then (3,0) | (1,0) |
+    // (2,0) (2,1) | (3,1) (3,2), rows of the warp's own fragments but for (3,0), which has its columns;
+    // Q Q^T for the norms
+    const int a1 = w == 0 ? 3 : w, b1 = w == 3 ? 1 : 0, b2 = w - 1;
+    float kk[3][8] = {}, qk[3][8] = {}, qq[8] = {};
+    {
+        const uint32_t at = kq_lane(kq, lane);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+            uint32_t fk[4], fq[4], f[4];
+            kq_frag(at, w, ks, fk);
+            kq_frag(at, 4 + w, ks, fq);
+            dot_frag(kk[0], fk, fk);
+            dot_frag(qk[0], fq, fk);
+            if (p.l2norm) dot_frag(qq, fq, fq);
+            if (w == 0) {
+                kq_frag(at, 3, ks, f);
+                dot_frag(kk[1], f, fk);
+                kq_frag(at, 7, ks, f);
+                dot_frag(qk[1], f, fk);
+            } else {
+                kq_frag(at, b1, ks, f);
+                dot_frag(kk[1], fk, f);
+                dot_frag(qk[1], fq, f);
+            }
+            if (w >= 2) {
+                kq_frag(at, b2, ks, f);
+                dot_frag(kk[2], fk, f);
+                dot_frag(qk[2], fq, f);
+            }
+        }
+    }
     float nk = 1.f, nq = 1.f;  // squared norms of token i16
     if (p.l2norm) {
-        dot_rows<false>(kk[1], nullptr, kq, 64 + 16 * w, 0, 64 + 16 * w, lane);
         // element (i, i) of a fragment block: rows 0-7 in lane 4 i + i / 2, rows 8-15 likewise
         const int src = 4 * (lane & 7) + ((lane & 7) >> 1);
         const float k0 = __shfl_sync(0xffffffffu, row & 1 ? kk[0][1] : kk[0][0], src);
         const float k1 = __shfl_sync(0xffffffffu, row & 1 ? kk[0][7] : kk[0][6], src);
-        const float q0 = __shfl_sync(0xffffffffu, row & 1 ? kk[1][1] : kk[1][0], src);
-        const float q1 = __shfl_sync(0xffffffffu, row & 1 ? kk[1][7] : kk[1][6], src);
+        const float q0 = __shfl_sync(0xffffffffu, row & 1 ? qq[1] : qq[0], src);
+        const float q1 = __shfl_sync(0xffffffffu, row & 1 ? qq[7] : qq[6], src);
         nk = (lane & 8 ? k1 : k0) + kDeltaEps;
         nq = (lane & 8 ? q1 : q0) + kDeltaEps;
     }
@@ -456,31 +476,23 @@ __global__ void __launch_bounds__(kTThreads, 5) delta_t_kernel(const DeltaParams
         }
         if (w == 0 && lane == 0) cf[256] = ex2((float)xend * kFixedStep);
     }
-    dot_rows<true>(kk[1], qk[1], kq, 16 * a1, 64 + 16 * a1, 16 * b1, lane);
-    if (!(w & 1)) dot_rows<true>(kk[2], qk[2], kq, 48, 64 + 48, 16 * b1, lane);
     __syncthreads();  // K and Q are read: P and T' take their place
 
-    // ---- scaled blocks: A to scratch, P to its tile, whose blocks above the diagonal are zero, as T''s
+    // ---- scaled blocks: A to scratch, P to its place
     {
         const TokenFactors f{ghi, glo, rk, brk, qs};
         scale_block(f, w, w, row, cp, kk[0], qk[0]);
 #pragma unroll
         for (int e = 0; e < 8; ++e)  // transposed: column m of A's block at ad + 16 m
             ad[(8 * (e >> 2) + cp + (e & 1)) * 16 + row + 8 * ((e >> 1) & 1)] = kk[0][e];
-        put_block(pp, 16 * w, 2 * w, row, cp, qk[0]);
+        put_block(sm, w, 1, 16 * w, row, cp, qk[0]);
         scale_block(f, a1, b1, row, cp, kk[1], qk[1]);
         put_panel(abp + (a1 * (a1 - 1) / 2 + b1) * 1024, row, cp, kk[1]);
-        put_block(pp, 16 * a1, 2 * b1, row, cp, qk[1]);
-        if (!(w & 1)) {
-            scale_block(f, 3, b1, row, cp, kk[2], qk[2]);
-            put_panel(abp + (3 + b1) * 1024, row, cp, kk[2]);
-            put_block(pp, 48, 2 * b1, row, cp, qk[2]);
-        }
-        for (int z = lane; z < 512; z += 32) {  // (tile, part, piece, row) of row block w
-            const int rho = 16 * w + (z & 15), kc = (z >> 4) & 7;
-            if (kc >= 2 * w + 2)
-                *reinterpret_cast<uint4 *>(sm + (z >> 7) * 8192 + rho * 128 + ((kc ^ (rho & 7)) << 4)) =
-                    make_uint4(0u, 0u, 0u, 0u);
+        put_block(sm, b1, 1, 16 * a1, row, cp, qk[1]);
+        if (w >= 2) {
+            scale_block(f, w, b2, row, cp, kk[2], qk[2]);
+            put_panel(abp + (w * (w - 1) / 2 + b2) * 1024, row, cp, kk[2]);
+            put_block(sm, b2, 1, 16 * w, row, cp, qk[2]);
         }
     }
     __syncwarp();
@@ -521,7 +533,7 @@ __global__ void __launch_bounds__(kTThreads, 5) delta_t_kernel(const DeltaParams
         // the operand tile holds T' = T - I
         if (row == cp) t[0] = t[6] = 0.f;
         if (row == cp + 1) t[1] = t[7] = 0.f;
-        put_block(tp, 16 * w, 2 * w, row, cp, t);
+        put_block(sm, w, 0, 16 * w, row, cp, t);
     }
     __syncthreads();  // all blocks of A, all diagonal blocks of T
 
@@ -555,9 +567,9 @@ __global__ void __launch_bounds__(kTThreads, 5) delta_t_kernel(const DeltaParams
             for (int e = 0; e < 8; ++e) t[e] = -t[e];
             split_frag(t, zh, zl);
             // matrices (j half, i half) -> rows i of the tile, columns 16 b + j
-            const uint32_t at = sw_row(tt, 16 * rr + 8 * (midx >> 1) + mrow, 2 * b + (midx & 1));
+            const uint32_t at = part_row(parts, b, 0, 16 * rr + 8 * (midx >> 1) + mrow, midx & 1);
             stsm4_t(at, zh);
-            stsm4_t(at + 8192, zl);
+            stsm4_t(at + SZ_PART, zl);
             if (dr < 3) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -575,9 +587,9 @@ __global__ void __launch_bounds__(kTThreads, 5) delta_t_kernel(const DeltaParams
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             if (m > w) break;
-            const uint32_t pa = sw_row(pt, 16 * w + (midx & 1) * 8 + mrow, 2 * m + (midx >> 1));
+            const uint32_t pa = part_row(parts, m, 1, 16 * w + (midx & 1) * 8 + mrow, midx >> 1);
             ldsm4(pa, fh[m]);
-            ldsm4(pa + 8192, fl[m]);
+            ldsm4(pa + SZ_PART, fl[m]);
         }
         __syncwarp();
         const int k = (midx & 1) * 8 + mrow, nh = midx >> 1;
@@ -589,23 +601,20 @@ __global__ void __launch_bounds__(kTThreads, 5) delta_t_kernel(const DeltaParams
             for (int m = b; m < 4; ++m) {
                 if (m > w) break;
                 uint32_t bh[4], bl[4];
-                const uint32_t at = m == b ? td + b * 1024 + nh * 256 + k * 16 : sw_row(tt, 16 * m + k, 2 * b + nh);
+                const uint32_t at =
+                    m == b ? td + b * 1024 + nh * 256 + k * 16 : part_row(parts, b, 0, 16 * m + k, nh);
                 ldsm4_t(at, bh);
-                ldsm4_t(at + (m == b ? 512 : 8192), bl);
+                ldsm4_t(at + (m == b ? 512 : SZ_PART), bl);
                 prod16(acc, fh[m], fl[m], bh, bl);
             }
-            put_block(pp, 16 * w, 2 * b, row, cp, acc);
+            put_block(sm, b, 1, 16 * w, row, cp, acc);
         }
     }
 
-    // the tile to the workspace: [T' hi; P T hi], [T' lo; P T lo]
     __syncthreads();
     fence_proxy_async_smem();
     if (threadIdx.x == 0) {
-        bulk_store(slot_out, tp, 8192);
-        bulk_store(slot_out + 8192, pp, 8192);
-        bulk_store(slot_out + SZ_T, tp + 8192, 8192);
-        bulk_store(slot_out + SZ_T + 8192, pp + 8192, 8192);
+        bulk_store(slot_out, sm, 2 * SZ_PART);
         bulk_commit_group();
         bulk_wait_group0();
     }
@@ -809,11 +818,12 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
 __device__ void mma_role(Bars *bars, uint32_t tbase, uint32_t s_base, int nchunks, bool ragged, Ctx cx) {
     const uint32_t id = idesc_bf16_f32(128, 128, false, false);
     const uint32_t idD = idesc_bf16_f32(128, 128, false, true);
-    // All B operands have the same high descriptor word (8-row groups 1024 bytes apart, 128-byte
+    // B operands of one swizzle have the same high descriptor word (8-row groups 1024 bytes apart, 128-byte
     // swizzle); the low word holds the start address and the leading-dimension offset.
     const uint64_t high = sdesc_sw128(0, 0, 1024);
-    auto mma = [&](uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
-        mma_f16_tmem_a(tbase + d, tbase + a, high | b, idesc, acc);
+    const uint64_t high32 = sdesc_sw32(0, 0, 256);  // T's tile: rows of 32 bytes
+    auto mma = [&](uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint64_t hw) {
+        mma_f16_tmem_a(tbase + d, tbase + a, hw | b, idesc, acc);
     };
     bool ok = true;
     int st = 0;
@@ -830,7 +840,7 @@ __device__ void mma_role(Bars *bars, uint32_t tbase, uint32_t s_base, int nchunk
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
                 mma(TM_X, TM_S + 16u * kk + 8u * x, kq + ((kk >> 2) * 1024 + (kk & 3) * 2) + (1u << 16), id,
-                    x + kk > 0);
+                    x + kk > 0, high);
         mma_commit(&bars->x_full);
         if (!(ok = wait_bar(&bars->t_full[par], ph, cx) && wait_bar(&bars->r_ready, par, cx))) break;
         tc_fence_after();
@@ -840,7 +850,7 @@ __device__ void mma_role(Bars *bars, uint32_t tbase, uint32_t s_base, int nchunk
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
                 mma(TM_Y, TM_X + 16u * kk + (x == 1 ? 8u : 0u),
-                    tt + (x == 2 ? SZ_T >> 4 : 0u) + kk * 2 + (1u << 16), id, x + kk > 0);
+                    tt + (x == 2 ? SZ_T >> 4 : 0u) + kk * (4096u >> 4) + (1u << 16), id, x + kk > 0, high32);
         mma_commit(&bars->y_full);
         mma_commit(&bars->y_done[par]);
         if (ragged && c == nchunks - 1 && !(ok = wait_bar(&bars->kq_fixed, 0, cx))) break;
@@ -850,7 +860,8 @@ __device__ void mma_role(Bars *bars, uint32_t tbase, uint32_t s_base, int nchunk
         for (int x = 0; x < 2; ++x)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                mma(TM_D, TM_Y + 16u * kk + 8u * x, kq + kk * 128 + ((16384u >> 4) << 16), idD, x + kk > 0);
+                mma(TM_D, TM_Y + 16u * kk + 8u * x, kq + kk * 128 + ((16384u >> 4) << 16), idD, x + kk > 0,
+                    high);
         mma_commit(&bars->d_full);
         mma_commit(&bars->kq_empty[st]);
         if (++st == kStages) {
@@ -887,8 +898,15 @@ __device__ void producer_role(const CUtensorMap &tq, const CUtensorMap &tk, cons
                        !wait_bar(&bars->c_free[g], ((c >> 1) - 1) & 1, cx)))
             break;
         mbar_arrive_expect_tx(&bars->t_full[g], SZ_SLOT);
-        bulk_load(sm + OFF_T + g * 2 * SZ_T, slots + c * slot_step, 2 * SZ_T, &bars->t_full[g]);
-        bulk_load(sm + OFF_COEF + g * SZ_COEF, slots + c * slot_step + 2 * SZ_T, SZ_COEF, &bars->t_full[g]);
+        const uint8_t *slot = slots + c * slot_step;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {  // (part, step, T' or P T): rows 16 kk .. 63
+            const int kk = (x >> 1) & 3, pt = x & 1;
+            bulk_load(sm + OFF_T + (2 * g + (x >> 3)) * SZ_T + kk * 4096 + pt * 2048 + kk * 512,
+                      slot + (x >> 3) * SZ_PART + part_ofs(kk, pt) + kk * 512, 2048 - kk * 512,
+                      &bars->t_full[g]);
+        }
+        bulk_load(sm + OFF_COEF + g * SZ_COEF, slot + 2 * SZ_PART, SZ_COEF, &bars->t_full[g]);
         mbar_arrive_expect_tx(&bars->v_full[g], 16384);
         tma_load_2d(sm + OFF_V + g * 16384, &tv, &bars->v_full[g], xv, y);
         vv = c + 1;
@@ -986,6 +1004,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tk);
         tma_prefetch_desc(&tv);
     }
+    // the rows of T' and P T before a k-step's columns stay zero
+    for (int x = threadIdx.x; x < (int)(4 * SZ_T / 16); x += kThreads)
+        reinterpret_cast<uint4 *>(sm + OFF_T)[x] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -177,6 +177,12 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t smem_addr, uint32_t lbo
     return d;
 }
 
+// The same for the 32-byte swizzle (atoms of 8 rows x 32 bytes; code 6): 16-byte piece c of row r is stored
+// at position c ^ ((r / 4) % 2).
+__device__ __forceinline__ uint64_t sdesc_sw32(uint32_t smem_addr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+    return (sdesc_sw128(smem_addr, lbo_bytes, sbo_bytes) & ~((uint64_t)7 << 61)) | ((uint64_t)6 << 61);
+}
+
 // D[tmem] (+)= A[smem] * B[smem]; issued by one thread.
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                          uint32_t idesc, uint32_t accumulate) {
