@@ -109,7 +109,8 @@ struct Bars {
     uint64_t kq_last;      // producer: the last chunk's loads are issued
     uint64_t kq_fixed;     // warp 10: rows past the end of the last chunk zeroed
     uint64_t x_full, y_full, d_full;
-    uint64_t r_ready, u_ready, s_ready, o_free;  // E warps (8)
+    // E warps (8): k-steps y and 2 + y of R and U, k-steps y and 4 + y of S in place; X^Q and O' read
+    uint64_t r_ready[2], u_ready[2], s_ready[4], o_free;
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
@@ -623,13 +624,17 @@ __global__ void __launch_bounds__(kTThreads, 5) delta_t_kernel(const DeltaParams
 // ------------------------------------------------------------------------------------------------
 // E warps: lanes are value columns v = 32 q + lane; half hf of the chunk's tokens and of the k columns.
 
-// Eight pairs (one k-step of an operand) as 8 columns of hi parts and 8 of lo parts.
-__device__ __forceinline__ void put_pairs(uint32_t t, const uint64_t *x) {
+// Eight pairs (one k-step of an operand) as 8 columns of hi parts and 8 of lo parts; the MMA issuer may
+// use them once every E warp has arrived.
+__device__ __forceinline__ void put_step(uint32_t t, const uint64_t *x, uint64_t *bar, int lane) {
     uint32_t hi[8], lo[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) split2(x[e], hi[e], lo[e]);
     tmem_st8(t, hi);
     tmem_st8(t + 8u, lo);
+    tmem_st_wait();
+    tc_fence_before();
+    warp_arrive(bar, lane);
 }
 
 // 32 per-token coefficients (the same for all lanes).
@@ -661,10 +666,7 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
     }
     if (nchunks > 0) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) put_pairs(ts + 16u * x, S + 8 * x);
-        tmem_st_wait();
-        tc_fence_before();
-        warp_arrive(&bars->s_ready, lane);
+        for (int x = 0; x < 4; ++x) put_step(ts + 16u * x, S + 8 * x, &bars->s_ready[x], lane);
     }
 
     bool ok = true;
@@ -706,12 +708,9 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
                         else if (tok0 + 2 * x + 1 >= r) R[x] &= 0xffffffffull;
                     }
                 }
-                put_pairs(tx + 16u * y, R + 8 * y);
+                put_step(tx + 16u * y, R + 8 * y, &bars->r_ready[y], lane);
             }
         }
-        tmem_st_wait();
-        tc_fence_before();
-        warp_arrive(&bars->r_ready, lane);
 
         // ---- U = R + T' R, scaled for the state update
         load_pairs(cf + 128, f);
@@ -728,12 +727,9 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
                 for (int x = 0; x < 8; ++x)
                     R[8 * y + x] =
                         mul2(f[8 * y + x], add2(R[8 * y + x], f2u(w[y][2 * x], w[y][2 * x + 1])));
-                put_pairs(ty + 16u * y, R + 8 * y);
+                put_step(ty + 16u * y, R + 8 * y, &bars->u_ready[y], lane);
             }
         }
-        tmem_st_wait();
-        tc_fence_before();
-        warp_arrive(&bars->u_ready, lane);
 
         // ---- o = (scale gamma rq) X^Q + P T R; neighbouring lanes exchange halves, so that each
         // stores two value columns of one token
@@ -793,13 +789,8 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     S[8 * x + e] = fma2(ge2, S[8 * x + e], f2u(d[2 * e], d[2 * e + 1]));
-                if (c + 1 < nchunks) put_pairs(ts + 16u * x, S + 8 * x);
+                if (c + 1 < nchunks) put_step(ts + 16u * x, S + 8 * x, &bars->s_ready[x], lane);
             }
-        }
-        if (c + 1 < nchunks) {
-            tmem_st_wait();
-            tc_fence_before();
-            warp_arrive(&bars->s_ready, lane);
         }
     }
     if (ok && !(prefix && nchunks == 0)) {
@@ -830,38 +821,53 @@ __device__ void mma_role(Bars *bars, uint32_t tbase, uint32_t s_base, int nchunk
     uint32_t stp = 0;
     for (int c = 0; c < nchunks; ++c) {
         const uint32_t par = c & 1, ph = (c >> 1) & 1;
-        ok = wait_bar(&bars->kq_full[st], stp, cx) && wait_bar(&bars->s_ready, par, cx) &&
+        ok = wait_bar(&bars->kq_full[st], stp, cx) &&
              (c == 0 || wait_bar(&bars->o_free, (c - 1) & 1, cx));
         if (!ok) break;
-        tc_fence_after();
         const uint32_t kq = (s_base + OFF_KQ + st * SZ_KQ) >> 4;
+        // a k-step starts as soon as the E warps have put it in place
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int y = 0; y < 4; ++y) {
+            if (!(ok = wait_bar(&bars->s_ready[y], par, cx))) break;
+            tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-                mma(TM_X, TM_S + 16u * kk + 8u * x, kq + ((kk >> 2) * 1024 + (kk & 3) * 2) + (1u << 16), id,
-                    x + kk > 0, high);
+            for (int x = 0; x < 4; ++x) {
+                const int kk = y + 4 * (x >> 1);  // hi, lo of k-steps y and 4 + y
+                mma(TM_X, TM_S + 16u * kk + 8u * (x & 1), kq + ((kk >> 2) * 1024 + (kk & 3) * 2) + (1u << 16),
+                    id, y + x > 0, high);
+            }
+        }
+        if (!ok) break;
         mma_commit(&bars->x_full);
-        if (!(ok = wait_bar(&bars->t_full[par], ph, cx) && wait_bar(&bars->r_ready, par, cx))) break;
-        tc_fence_after();
+        if (!(ok = wait_bar(&bars->t_full[par], ph, cx))) break;
         const uint32_t tt = (s_base + OFF_T + par * 2 * SZ_T) >> 4;
 #pragma unroll
-        for (int x = 0; x < 3; ++x)  // R_hi T_hi, R_lo T_hi, R_hi T_lo
+        for (int y = 0; y < 2; ++y) {
+            if (!(ok = wait_bar(&bars->r_ready[y], par, cx))) break;
+            tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                mma(TM_Y, TM_X + 16u * kk + (x == 1 ? 8u : 0u),
-                    tt + (x == 2 ? SZ_T >> 4 : 0u) + kk * (4096u >> 4) + (1u << 16), id, x + kk > 0, high32);
+            for (int x = 0; x < 6; ++x) {  // R_hi T_hi, R_lo T_hi, R_hi T_lo of k-steps y and 2 + y
+                const int kk = y + 2 * (x / 3), term = x % 3;
+                mma(TM_Y, TM_X + 16u * kk + (term == 1 ? 8u : 0u),
+                    tt + (term == 2 ? SZ_T >> 4 : 0u) + kk * (4096u >> 4) + (1u << 16), id, y + x > 0, high32);
+            }
+        }
+        if (!ok) break;
         mma_commit(&bars->y_full);
         mma_commit(&bars->y_done[par]);
         if (ragged && c == nchunks - 1 && !(ok = wait_bar(&bars->kq_fixed, 0, cx))) break;
-        if (!(ok = wait_bar(&bars->u_ready, par, cx))) break;
-        tc_fence_after();
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int y = 0; y < 2; ++y) {
+            if (!(ok = wait_bar(&bars->u_ready[y], par, cx))) break;
+            tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                mma(TM_D, TM_Y + 16u * kk + 8u * x, kq + kk * 128 + ((16384u >> 4) << 16), idD, x + kk > 0,
+            for (int x = 0; x < 4; ++x) {
+                const int kk = y + 2 * (x >> 1);
+                mma(TM_D, TM_Y + 16u * kk + 8u * (x & 1), kq + kk * 128 + ((16384u >> 4) << 16), idD, y + x > 0,
                     high);
+            }
+        }
+        if (!ok) break;
         mma_commit(&bars->d_full);
         mma_commit(&bars->kq_empty[st]);
         if (++st == kStages) {
@@ -987,9 +993,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&bars->x_full, 1);
         mbar_init(&bars->y_full, 1);
         mbar_init(&bars->d_full, 1);
-        mbar_init(&bars->r_ready, kEWarps);
-        mbar_init(&bars->u_ready, kEWarps);
-        mbar_init(&bars->s_ready, kEWarps);
+        for (int y = 0; y < 2; ++y) {
+            mbar_init(&bars->r_ready[y], kEWarps);
+            mbar_init(&bars->u_ready[y], kEWarps);
+        }
+        for (int y = 0; y < 4; ++y) mbar_init(&bars->s_ready[y], kEWarps);
         mbar_init(&bars->o_free, kEWarps);
         mbar_init(&bars->drain, 1);
         bars->abort_flag = 0;
