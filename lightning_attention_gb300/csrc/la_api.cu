@@ -556,7 +556,7 @@ la_status delta_params(la::DeltaParams *p, bool *work, const la_bf16 *q, const l
     const long long widest = std::max<long long>(std::max<long long>(q_rs, k_rs), v_rs);
     if (widest >= (1ll << 38) || tokens * widest >= (1ll << 40)) return LA_ERR_UNSUPPORTED;
     // the grids have B * H CTAs, four times as many, or one per chunk and head
-    if ((long long)B * H > 0x1fffffffLL || (tokens / 64 + B) * H > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
+    if ((long long)B * H > 0x1fffffffLL || (tokens / 64 + B) * H > 0x7fff0000LL) return LA_ERR_UNSUPPORTED;
     if (B == 0) return LA_OK;
     if (!state_pool || !state_idx) return LA_ERR_INVALID;
     if (tokens > 0 && (!q || !k || !v || !g || !beta || !out)) return LA_ERR_INVALID;
@@ -642,8 +642,9 @@ la_status la_delta_extend(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, 
     p.cu_seqlens = cu_seqlens;
     p.prefix_mask = prefix_mask;
     p.max_seqlen = max_seqlen;
-    if ((st = error_word_ptr(&p.err)) != LA_OK) return st;
-    return launch_status(la::launch_delta_extend(p, workspace, static_cast<cudaStream_t>(stream)));
+    int sms = 0;
+    if ((st = error_word_ptr(&p.err)) != LA_OK || (st = num_sms(&sms)) != LA_OK) return st;
+    return launch_status(la::launch_delta_extend(p, workspace, sms, static_cast<cudaStream_t>(stream)));
 }
 
 la_status la_delta_extend_workspace_size(int B, int T, int H, int D, size_t *bytes) {

@@ -32,7 +32,7 @@ cudaError_t launch_delta_recurrent(DeltaMode mode, const DeltaParams &p, int num
 
 // Chunked extend on the tensor cores (la_delta_extend.cu); ws: delta_scratch_bytes() bytes.
 unsigned long long delta_scratch_bytes(long long B, long long T, long long H);
-cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, cudaStream_t stream);
+cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cudaStream_t stream);
 
 // Packed state store: slot state_idx[b] of the pool <-> entry store_idx[b] of codes and scales.
 struct PackParams {

@@ -42,7 +42,7 @@
 //               request's keys, and 0 x NaN is NaN).
 // Per chunk the chain is X -> R -> T' R -> U -> U^T K -> S; the output pass runs under U^T K.
 //
-// Every wait is an mbarrier wait with a deadline; one that runs out sets the error word and an abort flag
+// Every wait ends: mbarrier waits have a deadline (the named barriers below end with them); one that runs out sets the error word and an abort flag
 // that ends every role, then the CTA waits for its copies and MMAs, frees tensor memory and exits.
 #include <cuda.h>
 #include <string.h>
@@ -62,6 +62,7 @@ constexpr int C = 64;  // tokens of a chunk
 constexpr int kEWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kFixWarp = 10;
 constexpr int kThreads = 352;
 constexpr int kTThreads = 128;
+constexpr int kMaxRanked = 8192;  // requests of a batch that is taken longest first
 constexpr float kScale = 0.08838834764831845f;  // 128^-0.5
 
 constexpr uint32_t kTmemCols = 512;
@@ -109,12 +110,10 @@ struct Bars {
     uint64_t kq_last;      // producer: the last chunk's loads are issued
     uint64_t kq_fixed;     // warp 10: rows past the end of the last chunk zeroed
     uint64_t x_full, y_full, d_full;
-    // E warps (8): k-steps y and 2 + y of R and U, k-steps y and 4 + y of S in place; X^Q and O' read
-    uint64_t r_ready[2], u_ready[2], s_ready[4], o_free;
+    uint64_t o_free;       // E warps (8): X^Q and O' read
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
-    int request;
 };
 static_assert(sizeof(Bars) <= SZ_BAR, "barrier block");
 
@@ -127,6 +126,20 @@ constexpr uint32_t TK_AB = 32768;                          // 6 x (512 hi + 512 
 constexpr uint32_t TK_TD = TK_AB + 6 * 1024;               // 4 x (512 hi + 512 lo)
 constexpr uint32_t TK_TOK = TK_TD + 4 * 1024;              // per token: ghi, glo, rk, beta rk, scale rq
 constexpr uint32_t kTSmemBytes = TK_TOK + 5 * 256 + 1024;
+
+// Named barriers between the E warps, which arrive, and the MMA warp, which waits: k-steps y and 4 + y of S
+// (kBarS + y), y and 2 + y of R and U (kBarR + y, kBarU + y) are in place.  They cost a handover some 30
+// cycles where an mbarrier, polled in shared memory beside streaming MMAs, costs 200.  They have no deadline of
+// their own: the E warps arrive at every one of every chunk, whether their own (bounded) waits succeed or
+// not, so the MMA warp's waits end when theirs do.
+constexpr int kBarS = 1, kBarR = 5, kBarU = 7;
+constexpr int kBarThreads = (kEWarps + 1) * 32;
+__device__ __forceinline__ void bar_arrive(int id) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kBarThreads) : "memory");
+}
+__device__ __forceinline__ void bar_wait(int id) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kBarThreads) : "memory");
+}
 
 constexpr uint64_t kDrainLimitNs = 2000000000ull;
 
@@ -330,16 +343,39 @@ __device__ __forceinline__ void scale_block(const TokenFactors &f, int a, int b,
     }
 }
 
-// T', P T and the coefficients of one chunk and head (blockIdx.x = slot * H + head).
-__global__ void __launch_bounds__(kTThreads, 5) delta_t_kernel(const DeltaParams p, uint8_t *ws) {
+// Request of each rank in decreasing length order (ties by index), kTThreads requests per CTA.
+__device__ void rank_requests(const DeltaParams &p, int block, int32_t *order, int *lens) {
+    const int b = block * kTThreads + (int)threadIdx.x;
+    const int mine = b < p.B ? p.cu_seqlens[b + 1] - p.cu_seqlens[b] : 0;
+    int rank = 0;
+    for (int u0 = 0; u0 < p.B; u0 += kTThreads) {
+        __syncthreads();
+        const int u = u0 + (int)threadIdx.x;
+        lens[threadIdx.x] = u < p.B ? p.cu_seqlens[u + 1] - p.cu_seqlens[u] : 0;
+        __syncthreads();
+        const int m = min(kTThreads, p.B - u0);
+        for (int x = 0; x < m; ++x) rank += (lens[x] > mine) || (lens[x] == mine && u0 + x < b);
+    }
+    if (b < p.B) order[rank] = b;
+}
+
+// T', P T and the coefficients of one chunk and head (blockIdx.x = rank_ctas + slot * H + head); the first
+// rank_ctas CTAs order the requests for the chain kernel.
+__global__ void __launch_bounds__(kTThreads, 5)
+    delta_t_kernel(const DeltaParams p, uint8_t *ws, int32_t *order, int rank_ctas) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int w = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
-    const int slot = (int)(blockIdx.x / (unsigned)p.H);
-    const int h = (int)(blockIdx.x - (unsigned)slot * (unsigned)p.H);
+    if ((int)blockIdx.x < rank_ctas) {
+        rank_requests(p, blockIdx.x, order, reinterpret_cast<int *>(sm));
+        return;
+    }
+    const unsigned item = blockIdx.x - (unsigned)rank_ctas;
+    const int slot = (int)(item / (unsigned)p.H);
+    const int h = (int)(item - (unsigned)slot * (unsigned)p.H);
 
     // The slot's request: the last b with floor(cu_seqlens[b] / C) + b <= slot, 32 candidates at a time.
     // (Requests that are out of order or too long are skipped by the chain kernel; whatever is found for
@@ -370,7 +406,7 @@ __global__ void __launch_bounds__(kTThreads, 5) delta_t_kernel(const DeltaParams
     uint8_t *abp = sm + TK_AB, *tdp = sm + TK_TD;
     const uint32_t ab = smem_u32(abp), td = smem_u32(tdp), kq = smem_u32(sm + TK_KQ), parts = smem_u32(sm);
     float *ad = reinterpret_cast<float *>(tdp + w * 1024);
-    uint8_t *slot_out = ws + (size_t)blockIdx.x * SZ_SLOT;
+    uint8_t *slot_out = ws + (size_t)item * SZ_SLOT;
     float *cf = reinterpret_cast<float *>(slot_out + 2 * SZ_PART);
     const int row = lane >> 2, cp = (lane & 3) * 2;  // fragment row, column pair
     const int mrow = lane & 7, midx = lane >> 3;     // ldmatrix: row, matrix
@@ -626,7 +662,7 @@ __global__ void __launch_bounds__(kTThreads, 5) delta_t_kernel(const DeltaParams
 
 // Eight pairs (one k-step of an operand) as 8 columns of hi parts and 8 of lo parts; the MMA issuer may
 // use them once every E warp has arrived.
-__device__ __forceinline__ void put_step(uint32_t t, const uint64_t *x, uint64_t *bar, int lane) {
+__device__ __forceinline__ void put_step(uint32_t t, const uint64_t *x, int bar) {
     uint32_t hi[8], lo[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) split2(x[e], hi[e], lo[e]);
@@ -634,7 +670,7 @@ __device__ __forceinline__ void put_step(uint32_t t, const uint64_t *x, uint64_t
     tmem_st8(t + 8u, lo);
     tmem_st_wait();
     tc_fence_before();
-    warp_arrive(bar, lane);
+    bar_arrive(bar);
 }
 
 // 32 per-token coefficients (the same for all lanes).
@@ -666,17 +702,35 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
     }
     if (nchunks > 0) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) put_step(ts + 16u * x, S + 8 * x, &bars->s_ready[x], lane);
+        for (int x = 0; x < 4; ++x) put_step(ts + 16u * x, S + 8 * x, kBarS + x);
     }
 
     bool ok = true;
+    // a wait gave up: the named barriers that are left of this chunk, from R's, U's or S's on (waited for,
+    // so that no warp runs a chunk ahead of the others)
+    auto give_up = [&](int from, int c) {
+        ok = false;
+        for (int x = from; x < kBarU + 2; ++x) bar_wait(x);
+        if (c + 1 < nchunks)
+            for (int x = kBarS; x < kBarR; ++x) bar_wait(x);
+    };
     for (int c = 0; c < nchunks; ++c) {
+        if (!ok) {
+            give_up(kBarR, c);
+            continue;
+        }
         const uint32_t par = c & 1, ph = (c >> 1) & 1;
         const int r = n - c * C;  // tokens from this chunk on
         const float *cf = reinterpret_cast<const float *>(sm + OFF_COEF + par * SZ_COEF) + tok0;
         // ---- R = beta V - (beta gamma rk) X^K; what needs no X is formed while its product runs
-        if (!(ok = warp_wait(&bars->t_full[par], ph, cx))) break;
-        if (!(ok = warp_wait(&bars->v_full[par], ph, cx))) break;
+        if (!warp_wait(&bars->t_full[par], ph, cx)) {
+            give_up(kBarR, c);
+            continue;
+        }
+        if (!warp_wait(&bars->v_full[par], ph, cx)) {
+            give_up(kBarR, c);
+            continue;
+        }
         uint64_t R[16], f[16];
         {
             const uint8_t *vp = sm + OFF_V + par * 16384 + tok0 * 256 + v * 2;
@@ -689,7 +743,10 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
                 R[x] = mul2(R[x], f2u(v0 << 16, v1 << 16));
             }
         }
-        if (!(ok = warp_wait(&bars->x_full, par, cx))) break;
+        if (!warp_wait(&bars->x_full, par, cx)) {
+            give_up(kBarR, c);
+            continue;
+        }
         tc_fence_after();
         {
             uint32_t w[2][16];
@@ -708,13 +765,16 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
                         else if (tok0 + 2 * x + 1 >= r) R[x] &= 0xffffffffull;
                     }
                 }
-                put_step(tx + 16u * y, R + 8 * y, &bars->r_ready[y], lane);
+                put_step(tx + 16u * y, R + 8 * y, kBarR + y);
             }
         }
 
         // ---- U = R + T' R, scaled for the state update
         load_pairs(cf + 128, f);
-        if (!(ok = warp_wait(&bars->y_full, par, cx))) break;
+        if (!warp_wait(&bars->y_full, par, cx)) {
+            give_up(kBarU, c);
+            continue;
+        }
         tc_fence_after();
         {
             uint32_t w[2][16];
@@ -727,7 +787,7 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
                 for (int x = 0; x < 8; ++x)
                     R[8 * y + x] =
                         mul2(f[8 * y + x], add2(R[8 * y + x], f2u(w[y][2 * x], w[y][2 * x + 1])));
-                put_step(ty + 16u * y, R + 8 * y, &bars->u_ready[y], lane);
+                put_step(ty + 16u * y, R + 8 * y, kBarU + y);
             }
         }
 
@@ -775,7 +835,10 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
         // ---- S = gamma_C S + K^T U
         const float ge = cf[256 - tok0];
         warp_arrive(&bars->c_free[par], lane);
-        if (!(ok = warp_wait(&bars->d_full, par, cx))) break;
+        if (!warp_wait(&bars->d_full, par, cx)) {
+            give_up(kBarU + 2, c);
+            continue;
+        }
         tc_fence_after();
         {
             const uint64_t ge2 = f2(ge, ge);
@@ -789,7 +852,7 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     S[8 * x + e] = fma2(ge2, S[8 * x + e], f2u(d[2 * e], d[2 * e + 1]));
-                if (c + 1 < nchunks) put_step(ts + 16u * x, S + 8 * x, &bars->s_ready[x], lane);
+                if (c + 1 < nchunks) put_step(ts + 16u * x, S + 8 * x, kBarS + x);
             }
         }
     }
@@ -805,8 +868,9 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
 }
 
 // ------------------------------------------------------------------------------------------------
-// MMA issuer (one thread)
-__device__ void mma_role(Bars *bars, uint32_t tbase, uint32_t s_base, int nchunks, bool ragged, Ctx cx) {
+// MMA issuer (one warp, of which lane 0 issues)
+__device__ void mma_role(Bars *bars, uint32_t tbase, uint32_t s_base, int nchunks, bool ragged, int lane,
+                         Ctx cx) {
     const uint32_t id = idesc_bf16_f32(128, 128, false, false);
     const uint32_t idD = idesc_bf16_f32(128, 128, false, true);
     // B operands of one swizzle have the same high descriptor word (8-row groups 1024 bytes apart, 128-byte
@@ -821,66 +885,79 @@ __device__ void mma_role(Bars *bars, uint32_t tbase, uint32_t s_base, int nchunk
     uint32_t stp = 0;
     for (int c = 0; c < nchunks; ++c) {
         const uint32_t par = c & 1, ph = (c >> 1) & 1;
-        ok = wait_bar(&bars->kq_full[st], stp, cx) &&
-             (c == 0 || wait_bar(&bars->o_free, (c - 1) & 1, cx));
-        if (!ok) break;
+        // once a wait gave up nothing more is issued, but every named barrier is waited for
+        ok = ok && warp_wait(&bars->kq_full[st], stp, cx) &&
+             (c == 0 || warp_wait(&bars->o_free, (c - 1) & 1, cx));
         const uint32_t kq = (s_base + OFF_KQ + st * SZ_KQ) >> 4;
         // a k-step starts as soon as the E warps have put it in place
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-            if (!(ok = wait_bar(&bars->s_ready[y], par, cx))) break;
+            bar_wait(kBarS + y);
             tc_fence_after();
+            if (ok && lane == 0) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int kk = y + 4 * (x >> 1);  // hi, lo of k-steps y and 4 + y
-                mma(TM_X, TM_S + 16u * kk + 8u * (x & 1), kq + ((kk >> 2) * 1024 + (kk & 3) * 2) + (1u << 16),
-                    id, y + x > 0, high);
+                for (int x = 0; x < 4; ++x) {
+                    const int kk = y + 4 * (x >> 1);  // hi, lo of k-steps y and 4 + y
+                    mma(TM_X, TM_S + 16u * kk + 8u * (x & 1),
+                        kq + ((kk >> 2) * 1024 + (kk & 3) * 2) + (1u << 16), id, y + x > 0, high);
+                }
+                if (y == 3) mma_commit(&bars->x_full);
             }
+            __syncwarp();
         }
-        if (!ok) break;
-        mma_commit(&bars->x_full);
-        if (!(ok = wait_bar(&bars->t_full[par], ph, cx))) break;
+        ok = ok && warp_wait(&bars->t_full[par], ph, cx);
         const uint32_t tt = (s_base + OFF_T + par * 2 * SZ_T) >> 4;
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-            if (!(ok = wait_bar(&bars->r_ready[y], par, cx))) break;
+            bar_wait(kBarR + y);
             tc_fence_after();
+            if (ok && lane == 0) {
 #pragma unroll
-            for (int x = 0; x < 6; ++x) {  // R_hi T_hi, R_lo T_hi, R_hi T_lo of k-steps y and 2 + y
-                const int kk = y + 2 * (x / 3), term = x % 3;
-                mma(TM_Y, TM_X + 16u * kk + (term == 1 ? 8u : 0u),
-                    tt + (term == 2 ? SZ_T >> 4 : 0u) + kk * (4096u >> 4) + (1u << 16), id, y + x > 0, high32);
+                for (int x = 0; x < 6; ++x) {  // R_hi T_hi, R_lo T_hi, R_hi T_lo of k-steps y and 2 + y
+                    const int kk = y + 2 * (x / 3), term = x % 3;
+                    mma(TM_Y, TM_X + 16u * kk + (term == 1 ? 8u : 0u),
+                        tt + (term == 2 ? SZ_T >> 4 : 0u) + kk * (4096u >> 4) + (1u << 16), id, y + x > 0,
+                        high32);
+                }
+                if (y == 1) {
+                    mma_commit(&bars->y_full);
+                    mma_commit(&bars->y_done[par]);
+                }
             }
+            __syncwarp();
         }
-        if (!ok) break;
-        mma_commit(&bars->y_full);
-        mma_commit(&bars->y_done[par]);
-        if (ragged && c == nchunks - 1 && !(ok = wait_bar(&bars->kq_fixed, 0, cx))) break;
+        if (ragged && c == nchunks - 1) ok = ok && warp_wait(&bars->kq_fixed, 0, cx);
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-            if (!(ok = wait_bar(&bars->u_ready[y], par, cx))) break;
+            bar_wait(kBarU + y);
             tc_fence_after();
+            if (ok && lane == 0) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int kk = y + 2 * (x >> 1);
-                mma(TM_D, TM_Y + 16u * kk + 8u * (x & 1), kq + kk * 128 + ((16384u >> 4) << 16), idD, y + x > 0,
-                    high);
+                for (int x = 0; x < 4; ++x) {
+                    const int kk = y + 2 * (x >> 1);
+                    mma(TM_D, TM_Y + 16u * kk + 8u * (x & 1), kq + kk * 128 + ((16384u >> 4) << 16), idD,
+                        y + x > 0, high);
+                }
+                if (y == 1) {
+                    mma_commit(&bars->d_full);
+                    mma_commit(&bars->kq_empty[st]);
+                }
             }
+            __syncwarp();
         }
-        if (!ok) break;
-        mma_commit(&bars->d_full);
-        mma_commit(&bars->kq_empty[st]);
         if (++st == kStages) {
             st = 0;
             stp ^= 1;
         }
     }
     // every issued MMA must finish before tensor memory is freed
-    mma_commit(&bars->drain);
-    int dummy = 0;
-    cx.abort_flag = &dummy;
-    cx.limit = kDrainLimitNs;
-    wait_bar(&bars->drain, 0, cx);
+    if (lane == 0) {
+        mma_commit(&bars->drain);
+        int dummy = 0;
+        cx.abort_flag = &dummy;
+        cx.limit = kDrainLimitNs;
+        wait_bar(&bars->drain, 0, cx);
+    }
 }
 
 __device__ void producer_role(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, Bars *bars,
@@ -931,7 +1008,7 @@ __device__ void producer_role(const CUtensorMap &tq, const CUtensorMap &tk, cons
 
 __global__ void __launch_bounds__(kThreads, 1)
     delta_extend_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                        const __grid_constant__ CUtensorMap tv, const DeltaParams p, const uint8_t *ws) {
+                        const __grid_constant__ CUtensorMap tv, const DeltaParams p, const uint8_t *ws, const int32_t *order) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Bars *bars = reinterpret_cast<Bars *>(sm + OFF_BAR);
@@ -942,26 +1019,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int h = (int)blockIdx.x % p.H;
     const int want = (int)blockIdx.x / p.H;
 
-    // Longest request first for batches that the CTA can rank itself: CTAs are issued in index
-    // order, so long requests do not finish last.
-    int b = want;
-    if (p.B > 1 && p.B <= kThreads) {
-        int *lens = reinterpret_cast<int *>(sm);
-        const int t = threadIdx.x;
-        const int mine = t < p.B ? p.cu_seqlens[t + 1] - p.cu_seqlens[t] : 0;
-        lens[t] = mine;
-        __syncthreads();
-        if (t < p.B) {
-            int rank = 0;
-            for (int u = 0; u < p.B; ++u) {
-                const int lu = lens[u];
-                rank += (lu > mine) || (lu == mine && u < t);
-            }
-            if (rank == want) bars->request = t;
-        }
-        __syncthreads();
-        b = bars->request;
-    }
+    // Longest request first where there is more than one wave of CTAs: they are issued in index order, so
+    // long requests do not finish last.
+    const int b = order ? order[want] : want;
 
     const int slot = p.state_idx[b];
     const int t_req0 = p.cu_seqlens[b], t_req1 = p.cu_seqlens[b + 1];
@@ -993,11 +1053,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&bars->x_full, 1);
         mbar_init(&bars->y_full, 1);
         mbar_init(&bars->d_full, 1);
-        for (int y = 0; y < 2; ++y) {
-            mbar_init(&bars->r_ready[y], kEWarps);
-            mbar_init(&bars->u_ready[y], kEWarps);
-        }
-        for (int y = 0; y < 4; ++y) mbar_init(&bars->s_ready[y], kEWarps);
         mbar_init(&bars->o_free, kEWarps);
         mbar_init(&bars->drain, 1);
         bars->abort_flag = 0;
@@ -1030,7 +1085,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             producer_role(tq, tk, tv, bars, sm, ws + ((size_t)((t_req0 >> 6) + b) * p.H + h) * SZ_SLOT,
                           (size_t)p.H * SZ_SLOT, t_req0, nchunks, (h / p.group) * kHeadDim, h * kHeadDim, cx);
     } else if (warp == kMmaWarp) {
-        if (lane == 0) mma_role(bars, tbase, smem_u32(sm), nchunks, ragged, cx);
+        mma_role(bars, tbase, smem_u32(sm), nchunks, ragged, lane, cx);
     } else if (warp == kFixWarp && ragged) {
         const int c = nchunks - 1, st = c % kStages;
         if (warp_wait(&bars->kq_last, 0, cx) && warp_wait(&bars->kq_full[st], (c / kStages) & 1, cx)) {
@@ -1054,14 +1109,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace
 
 unsigned long long delta_scratch_bytes(long long B, long long T, long long H) {
-    return T > 0 && B > 0 ? (unsigned long long)chunk_slots(T, B) * (unsigned long long)H * SZ_SLOT : 0ull;
+    if (T <= 0 || B <= 0) return 0ull;
+    return (unsigned long long)chunk_slots(T, B) * (unsigned long long)H * SZ_SLOT +
+           ((unsigned long long)B * sizeof(int32_t) + 15ull) / 16ull * 16ull;
 }
 
-cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, cudaStream_t stream) {
+cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cudaStream_t stream) {
     const long long ctas = (long long)p.B * p.H;
     if (ctas <= 0) return cudaSuccess;
     const long long t_ctas = p.T > 0 ? chunk_slots(p.T, p.B) * p.H : 0;
-    if (ctas > 0x7fffffffLL || t_ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (ctas > 0x7fffffffLL || t_ctas + kMaxRanked > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     CUtensorMap tq, tk, tv;
     memset(&tq, 0, sizeof(tq));
     memset(&tk, 0, sizeof(tk));
@@ -1089,12 +1146,20 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, cudaStream_t str
         }
     }
     uint8_t *w = static_cast<uint8_t *>(ws);
+    // One wave needs no order; ranking is B comparisons per request.
+    int32_t *order = nullptr;
+    int rank_ctas = 0;
+    if (t_ctas > 0 && p.B > 1 && p.B <= kMaxRanked && ctas > num_sms) {
+        order = reinterpret_cast<int32_t *>(w + t_ctas * SZ_SLOT);
+        rank_ctas = (p.B + kTThreads - 1) / kTThreads;
+    }
     if (t_ctas > 0) {
-        e = launch_pdl(delta_t_kernel, dim3((unsigned)t_ctas), dim3(kTThreads), kTSmemBytes, stream, p, w);
+        e = launch_pdl(delta_t_kernel, dim3((unsigned)(rank_ctas + t_ctas)), dim3(kTThreads), kTSmemBytes,
+                       stream, p, w, order, rank_ctas);
         if (e != cudaSuccess) return e;
     }
     return launch_pdl(delta_extend_kernel, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, tq, tk,
-                      tv, p, (const uint8_t *)w);
+                      tv, p, (const uint8_t *)w, (const int32_t *)order);
 }
 
 }  // namespace la
