@@ -498,9 +498,23 @@ def decode_gqa(q, k, v, slopes_, state_pool, state_idx, out=None):
     return out
 
 
+# The checks below run on every decode call, whose kernel takes a few microseconds: a tensor that is as it
+# should be passes one comparison, any other goes through the checks that name what is wrong.
+def _fits(t, dtype, index: int, shape) -> bool:
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == index and t.is_contiguous())
+
+
+def _need_fast(t, name: str, dtype, dev, shape):
+    if not _fits(t, dtype, dev.index, shape):
+        _need(t, name, dtype, dev, shape)
+
+
 def _need_rows(t, name: str, device, rows: int, width: int) -> int:
     """Row stride (in elements) of a bf16 [rows, width] tensor whose rows are contiguous but may lie
     further apart, as the columns of a wider projection do."""
+    if _fits(t, torch.bfloat16, device.index, (rows, width)):
+        return width
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != torch.bfloat16:
@@ -520,36 +534,39 @@ def _need_rows(t, name: str, device, rows: int, width: int) -> int:
 
 
 def _need_pool(state_pool, dev):
+    """(slots, H, D) of an fp32 [S, H, D, D] pool on dev."""
     if not isinstance(state_pool, torch.Tensor) or state_pool.dim() != 4:
         raise TypeError("state_pool must be an fp32 [S, H, D, D] tensor")
-    _need(state_pool, "state_pool", torch.float32, dev, tuple(state_pool.shape[:3]) + (state_pool.shape[2],))
-    return state_pool.shape[:3]
+    S, H, D, _ = state_pool.shape
+    _need_fast(state_pool, "state_pool", torch.float32, dev, (S, H, D, D))
+    return S, H, D
 
 
 def _delta_args(q, k, v, g, beta, state_pool, state_idx, out, tokens: int | None):
-    """Checks shared by the delta calls: (tokens, B, H, Hk, D, row strides, out)."""
+    """Checks shared by the delta calls: (device, rows, slots, B, H, Hk, D, row strides, out)."""
     if not isinstance(q, torch.Tensor) or q.dim() != 2:
         raise TypeError("q must be a bf16 [tokens, Hk*D] tensor")
     dev = q.device
     if dev.type != "cuda":
         raise ValueError(f"q must be on a CUDA device, got {dev}")
-    _, H, D = _need_pool(state_pool, dev)
+    slots, H, D = _need_pool(state_pool, dev)
     if not isinstance(state_idx, torch.Tensor) or state_idx.dim() != 1:
         raise TypeError("state_idx must be an int32 [B] tensor")
     B = state_idx.shape[0]
-    rows = q.shape[0] if tokens is None else B * tokens
-    if D < 1 or q.shape[1] % D != 0:
-        raise ValueError(f"q must have a multiple of {D} columns, got {q.shape[1]}")
-    Hk = q.shape[1] // D
-    strides = (_need_rows(q, "q", dev, rows, Hk * D), _need_rows(k, "k", dev, rows, Hk * D),
+    q_rows, q_cols = q.shape
+    rows = q_rows if tokens is None else B * tokens
+    if D < 1 or q_cols % D != 0:
+        raise ValueError(f"q must have a multiple of {D} columns, got {q_cols}")
+    strides = (_need_rows(q, "q", dev, rows, q_cols), _need_rows(k, "k", dev, rows, q_cols),
                _need_rows(v, "v", dev, rows, H * D))
-    _need(g, "g", torch.float32, dev, (rows, H))
-    _need(beta, "beta", torch.float32, dev, (rows, H))
-    _need(state_idx, "state_idx", torch.int32, dev, (B,))
+    _need_fast(g, "g", torch.float32, dev, (rows, H))
+    _need_fast(beta, "beta", torch.float32, dev, (rows, H))
+    _need_fast(state_idx, "state_idx", torch.int32, dev, (B,))
     if out is None:
         out = torch.empty((rows, H * D), dtype=torch.bfloat16, device=dev)
-    _need(out, "out", torch.bfloat16, dev, (rows, H * D))
-    return rows, B, H, Hk, D, strides, out
+    else:
+        _need_fast(out, "out", torch.bfloat16, dev, (rows, H * D))
+    return dev, rows, slots, B, H, q_cols // D, D, strides, out
 
 
 def delta_extend_workspace_size(B: int, T: int, H: int, D: int) -> int:
@@ -566,35 +583,34 @@ def delta_extend(q, k, v, g, beta, state_pool, state_idx, cu_seqlens, prefix_mas
     (rows may be strided: column ranges of one projection); g (log decay) and beta: fp32 [T, H];
     state_pool fp32 [S, H, D, D] updated in place; returns out bf16 [T, H*D].  Value head h reads key
     head h // (H / Hk); qk_l2norm divides q and k by their head's 2-norm first."""
-    T, B, H, Hk, D, rs, out = _delta_args(q, k, v, g, beta, state_pool, state_idx, out, None)
-    dev = q.device
-    _need(cu_seqlens, "cu_seqlens", torch.int32, dev, (B + 1,))
-    _need(prefix_mask, "prefix_mask", torch.uint8, dev, (B,))
+    dev, T, slots, B, H, Hk, D, rs, out = _delta_args(q, k, v, g, beta, state_pool, state_idx, out, None)
+    _need_fast(cu_seqlens, "cu_seqlens", torch.int32, dev, (B + 1,))
+    _need_fast(prefix_mask, "prefix_mask", torch.uint8, dev, (B,))
     if max_seqlen is None:
         max_seqlen = T
     if workspace is None:
         workspace = torch.empty(delta_extend_workspace_size(B, T, H, D), dtype=torch.uint8, device=dev)
     _need(workspace, "workspace", torch.uint8, dev)
     with _on(dev):
-        st = load().la_delta_extend(_ptr(q), _ptr(k), _ptr(v), *rs, _ptr(g), _ptr(beta),
-                                    _ptr(state_pool), state_pool.shape[0], _ptr(state_idx),
-                                    _ptr(cu_seqlens), _ptr(prefix_mask), _ptr(out), B, T, H, Hk, D,
-                                    int(max_seqlen), int(bool(qk_l2norm)), _ptr(workspace),
-                                    workspace.numel(), _stream_handle(dev))
-    _check("la_delta_extend", st)
+        st = (_lib or load()).la_delta_extend(
+            _ptr(q), _ptr(k), _ptr(v), *rs, _ptr(g), _ptr(beta), _ptr(state_pool), slots, _ptr(state_idx),
+            _ptr(cu_seqlens), _ptr(prefix_mask), _ptr(out), B, T, H, Hk, D, int(max_seqlen),
+            1 if qk_l2norm else 0, _ptr(workspace), workspace.numel(), _stream_handle(dev))
+    if st:
+        _check("la_delta_extend", st)
     return out
 
 
 def delta_decode(q, k, v, g, beta, state_pool, state_idx, out=None, qk_l2norm: bool = False):
     """One-token gated delta rule (la_delta_decode): q, k bf16 [B, Hk*D]; v bf16 [B, H*D]; g, beta
     fp32 [B, H]; pool updated in place; returns out bf16 [B, H*D]."""
-    _, B, H, Hk, D, rs, out = _delta_args(q, k, v, g, beta, state_pool, state_idx, out, 1)
-    dev = q.device
+    dev, _, slots, B, H, Hk, D, rs, out = _delta_args(q, k, v, g, beta, state_pool, state_idx, out, 1)
     with _on(dev):
-        st = load().la_delta_decode(_ptr(q), _ptr(k), _ptr(v), *rs, _ptr(g), _ptr(beta),
-                                    _ptr(state_pool), state_pool.shape[0], _ptr(state_idx), _ptr(out),
-                                    B, H, Hk, D, int(bool(qk_l2norm)), _stream_handle(dev))
-    _check("la_delta_decode", st)
+        st = (_lib or load()).la_delta_decode(
+            _ptr(q), _ptr(k), _ptr(v), *rs, _ptr(g), _ptr(beta), _ptr(state_pool), slots, _ptr(state_idx),
+            _ptr(out), B, H, Hk, D, 1 if qk_l2norm else 0, _stream_handle(dev))
+    if st:
+        _check("la_delta_decode", st)
     return out
 
 
@@ -605,17 +621,18 @@ def delta_verify_chain(q, k, v, g, beta, state_pool, state_idx, N: int, inter_st
     [B, N, H, D, D], as commit_accepted takes them; the pool is not modified."""
     if N < 1:
         raise ValueError(f"N must be at least 1, got {N}")
-    _, B, H, Hk, D, rs, out = _delta_args(q, k, v, g, beta, state_pool, state_idx, out, int(N))
-    dev = q.device
+    N = int(N)
+    dev, _, slots, B, H, Hk, D, rs, out = _delta_args(q, k, v, g, beta, state_pool, state_idx, out, N)
     if inter_states is None:
         inter_states = torch.empty((B, N, H, D, D), dtype=torch.float32, device=dev)
-    _need(inter_states, "inter_states", torch.float32, dev, (B, N, H, D, D))
+    else:
+        _need_fast(inter_states, "inter_states", torch.float32, dev, (B, N, H, D, D))
     with _on(dev):
-        st = load().la_delta_verify_chain(_ptr(q), _ptr(k), _ptr(v), *rs, _ptr(g), _ptr(beta),
-                                          _ptr(state_pool), state_pool.shape[0], _ptr(state_idx),
-                                          _ptr(inter_states), _ptr(out), B, int(N), H, Hk, D,
-                                          int(bool(qk_l2norm)), _stream_handle(dev))
-    _check("la_delta_verify_chain", st)
+        st = (_lib or load()).la_delta_verify_chain(
+            _ptr(q), _ptr(k), _ptr(v), *rs, _ptr(g), _ptr(beta), _ptr(state_pool), slots, _ptr(state_idx),
+            _ptr(inter_states), _ptr(out), B, N, H, Hk, D, 1 if qk_l2norm else 0, _stream_handle(dev))
+    if st:
+        _check("la_delta_verify_chain", st)
     return out, inter_states
 
 
@@ -631,10 +648,10 @@ def _pack_args(state_pool, state_idx, codes, scales, store_idx):
     if state_idx.dim() != 1 or codes.dim() != 4:
         raise ValueError("state_idx must have shape [B] and codes [E, H, D, D]")
     B, E = state_idx.shape[0], codes.shape[0]
-    _need(state_idx, "state_idx", torch.int32, dev, (B,))
-    _need(store_idx, "store_idx", torch.int32, dev, (B,))
-    _need(codes, "codes", torch.int8, dev, (E, H, D, D))
-    _need(scales, "scales", torch.uint8, dev, (E, H, D, D // 32))
+    _need_fast(state_idx, "state_idx", torch.int32, dev, (B,))
+    _need_fast(store_idx, "store_idx", torch.int32, dev, (B,))
+    _need_fast(codes, "codes", torch.int8, dev, (E, H, D, D))
+    _need_fast(scales, "scales", torch.uint8, dev, (E, H, D, D // 32))
     return dev, num_slots, E, B, H, D
 
 
@@ -643,15 +660,17 @@ def pack_states(state_pool, state_idx, codes, scales, store_idx) -> None:
     store_idx[b] of codes (int8 [E, H, D, D]) and scales (uint8 [E, H, D, D // 32])."""
     dev, num_slots, E, B, H, D = _pack_args(state_pool, state_idx, codes, scales, store_idx)
     with _on(dev):
-        st = load().la_pack_states(_ptr(state_pool), num_slots, _ptr(state_idx), _ptr(codes),
+        st = (_lib or load()).la_pack_states(_ptr(state_pool), num_slots, _ptr(state_idx), _ptr(codes),
                                    _ptr(scales), E, _ptr(store_idx), B, H, D, _stream_handle(dev))
-    _check("la_pack_states", st)
+    if st:
+        _check("la_pack_states", st)
 
 
 def unpack_states(codes, scales, store_idx, state_pool, state_idx) -> None:
     """Restore entries of the 8-bit state store into pool slots (la_unpack_states)."""
     dev, num_slots, E, B, H, D = _pack_args(state_pool, state_idx, codes, scales, store_idx)
     with _on(dev):
-        st = load().la_unpack_states(_ptr(codes), _ptr(scales), E, _ptr(store_idx), _ptr(state_pool),
+        st = (_lib or load()).la_unpack_states(_ptr(codes), _ptr(scales), E, _ptr(store_idx), _ptr(state_pool),
                                      num_slots, _ptr(state_idx), B, H, D, _stream_handle(dev))
-    _check("la_unpack_states", st)
+    if st:
+        _check("la_unpack_states", st)

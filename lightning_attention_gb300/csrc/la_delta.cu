@@ -10,7 +10,10 @@
 // all of them when there are enough (request, head) pairs to fill the GPU, a quarter otherwise.
 // HBM-bound: a state is read once and written once (verify: written once per draft token).
 // Every access is a 16-byte vector of a row, all of a thread's loads are issued before any
-// arithmetic (64 KiB in flight per CTA, 16 KiB at a quarter), one barrier per token.
+// arithmetic (64 KiB in flight per CTA, 16 KiB at a quarter).  A thread's rows are contiguous, so its
+// k and q entries are one or two broadcast vector loads, and the sums that the whole rows need (|k|^2,
+// |q|^2, k.q) are formed over the same rows and meet in the same reduction: one barrier per token.  The
+// next token's entries are loaded before the barrier.
 #include "la_delta.h"
 
 namespace la {
@@ -24,18 +27,45 @@ constexpr float kScale = 0.08838834764831845f;
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-__device__ __forceinline__ float warp_sum(float x) {
+// n consecutive bf16 values (4 or 16) of a row.
+template <int n>
+struct RowVec {
+    uint32_t w[n / 2];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+        if constexpr (n == 4) {
+            const uint2 u = *reinterpret_cast<const uint2 *>(p);
+            w[0] = u.x;
+            w[1] = u.y;
+        } else {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    return x;
+            for (int x = 0; x < n / 8; ++x) {
+                const uint4 u = reinterpret_cast<const uint4 *>(p)[x];
+                w[4 * x] = u.x;
+                w[4 * x + 1] = u.y;
+                w[4 * x + 2] = u.z;
+                w[4 * x + 3] = u.w;
+            }
+        }
+    }
+    __device__ __forceinline__ float operator[](int i) const {
+        return i & 1 ? bf_hi(w[i >> 1]) : bf_lo(w[i >> 1]);
+    }
+};
+
+__device__ __forceinline__ float4 add4(const float4 &a, const float4 &b) {
+    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+__device__ __forceinline__ float4 shfl4(const float4 &a, int d) {
+    return make_float4(__shfl_xor_sync(0xffffffffu, a.x, d), __shfl_xor_sync(0xffffffffu, a.y, d),
+                       __shfl_xor_sync(0xffffffffu, a.z, d), __shfl_xor_sync(0xffffffffu, a.w, d));
 }
 
 template <int MODE, int COLS>
-__global__ void __launch_bounds__(kThreads) delta_recurrent_kernel(const DeltaParams p) {
+__global__ void __launch_bounds__(kThreads, 2) delta_recurrent_kernel(const DeltaParams p) {
     constexpr int kParts = kHeadDim / COLS;
-    constexpr int kLanesPerRow = COLS / 4;              // a lane owns 4 columns
-    constexpr int kRowGroups = kWarps * (32 / kLanesPerRow);
-    constexpr int kRows = kHeadDim / kRowGroups;        // rows of a thread
+    constexpr int kLanesPerRow = COLS / 4;                             // a lane owns 4 columns
+    constexpr int kRows = kHeadDim / (kThreads / kLanesPerRow);        // rows of a thread
+    static_assert(kRows == 16 || kRows == 4, "a thread's rows are whole vectors");
     pdl_wait();
     pdl_trigger();
     const int H = p.H;
@@ -43,16 +73,15 @@ __global__ void __launch_bounds__(kThreads) delta_recurrent_kernel(const DeltaPa
     const int pair = (int)(blockIdx.x / kParts);
     const int b = pair / H;
     const int h = pair - b * H;
-    const int hk = h / p.group;
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int row_group = threadIdx.x / kLanesPerRow;   // rows row_group + kRowGroups r
+    const int row0 = (int)(threadIdx.x / kLanesPerRow) * kRows;
     const int c4 = (lane % kLanesPerRow) * 4;           // column of the CTA's COLS
     const int col = part * COLS + c4;                   // value column
 
     __shared__ __align__(16) float red_x[2][kWarps][COLS];
     __shared__ __align__(16) float red_o[2][kWarps][COLS];
-    __shared__ __align__(16) float sk[2][kHeadDim], sq[2][kHeadDim];
+    __shared__ __align__(16) float4 red_s[2][kWarps];   // sums of k k, q q, k q
 
     const int slot = p.state_idx[b];
     if (slot < 0 || slot >= p.num_slots) {
@@ -60,106 +89,84 @@ __global__ void __launch_bounds__(kThreads) delta_recurrent_kernel(const DeltaPa
         return;
     }
     constexpr size_t kMat = (size_t)kHeadDim * kHeadDim;
-    float *state = p.pool + ((size_t)slot * H + h) * kMat + col;
-
-    size_t t_begin;
-    int n;
-    bool zero = false;
-    if constexpr (MODE == DELTA_EXTEND) {
-        const int t0 = p.cu_seqlens[b], t1 = p.cu_seqlens[b + 1];
-        if (t0 < 0 || t1 < t0 || t1 > p.T || t1 - t0 > p.max_seqlen) {
-            if (threadIdx.x == 0) atomicOr(p.err, ERR_BIT_SEQLENS);
-            return;
-        }
-        t_begin = (size_t)t0;
-        n = t1 - t0;
-        zero = p.prefix_mask[b] == 0;
-    } else {
-        t_begin = (size_t)b * p.N;
-        n = p.N;
-    }
-
+    float *state = p.pool + ((size_t)slot * H + h) * kMat + (size_t)row0 * kHeadDim + col;
     float4 s[kRows];
-    if (zero) {
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) s[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-    } else {
-#pragma unroll
-        for (int r = 0; r < kRows; ++r)
-            s[r] = __ldcs(reinterpret_cast<const float4 *>(
-                state + (size_t)(row_group + r * kRowGroups) * kHeadDim));
-    }
+    for (int r = 0; r < kRows; ++r)
+        s[r] = __ldcs(reinterpret_cast<const float4 *>(state + (size_t)r * kHeadDim));
+
+    const int n = MODE == DELTA_DECODE ? 1 : p.N;
+    const size_t t_begin = (size_t)b * n;
+    const __nv_bfloat16 *kp = p.k + t_begin * p.k_rs + (size_t)(h / p.group) * kHeadDim + row0;
+    const __nv_bfloat16 *qp = p.q + t_begin * p.q_rs + (size_t)(h / p.group) * kHeadDim + row0;
+    const __nv_bfloat16 *vp = p.v + t_begin * p.v_rs + (size_t)h * kHeadDim + col;
+    const float *gp = p.g + t_begin * H + h, *bp = p.beta + t_begin * H + h;
+    RowVec<kRows> kf, qf;
+    RowVec<4> vf;
+    kf.load(kp);
+    qf.load(qp);
+    vf.load(vp);
+    float g = *gp, beta = *bp;
 
     for (int t = 0; t < n; ++t) {
-        const size_t tok = t_begin + t;
-        // Every warp forms the token's three inner products from its own copy of the rows.
-        const uint2 kw = *reinterpret_cast<const uint2 *>(p.k + tok * p.k_rs + hk * kHeadDim + lane * 4);
-        const uint2 qw = *reinterpret_cast<const uint2 *>(p.q + tok * p.q_rs + hk * kHeadDim + lane * 4);
-        const uint2 vv = *reinterpret_cast<const uint2 *>(p.v + tok * p.v_rs + h * kHeadDim + col);
-        const float decay = expf(p.g[tok * H + h]);
-        const float beta = p.beta[tok * H + h];
-        const float k0 = bf_lo(kw.x), k1 = bf_hi(kw.x), k2 = bf_lo(kw.y), k3 = bf_hi(kw.y);
-        const float q0 = bf_lo(qw.x), q1 = bf_hi(qw.x), q2 = bf_lo(qw.y), q3 = bf_hi(qw.y);
         const int buf = t & 1;
-        if (warp == 0) {
-            *reinterpret_cast<float4 *>(&sk[buf][lane * 4]) = make_float4(k0, k1, k2, k3);
-            *reinterpret_cast<float4 *>(&sq[buf][lane * 4]) = make_float4(q0, q1, q2, q3);
-        }
-        float kq = warp_sum(fmaf(k0, q0, fmaf(k1, q1, fmaf(k2, q2, k3 * q3))));
-        float rk = 1.f, rq = 1.f;
-        if (p.l2norm) {
-            rk = 1.f / sqrtf(warp_sum(fmaf(k0, k0, fmaf(k1, k1, fmaf(k2, k2, k3 * k3)))) + kDeltaEps);
-            rq = 1.f / sqrtf(warp_sum(fmaf(q0, q0, fmaf(q1, q1, fmaf(q2, q2, q3 * q3)))) + kDeltaEps);
-            kq *= rk * rq;
-        }
-        __syncthreads();  // k and q staged; the partials of token t - 1 are read
-
-        float kf[kRows];
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), o = x;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), o = x, sum = x;
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
-            kf[r] = sk[buf][row_group + r * kRowGroups];
-            const float qf = sq[buf][row_group + r * kRowGroups];
-            x.x = fmaf(kf[r], s[r].x, x.x);
-            x.y = fmaf(kf[r], s[r].y, x.y);
-            x.z = fmaf(kf[r], s[r].z, x.z);
-            x.w = fmaf(kf[r], s[r].w, x.w);
-            o.x = fmaf(qf, s[r].x, o.x);
-            o.y = fmaf(qf, s[r].y, o.y);
-            o.z = fmaf(qf, s[r].z, o.z);
-            o.w = fmaf(qf, s[r].w, o.w);
+            const float k = kf[r], q = qf[r];
+            x.x = fmaf(k, s[r].x, x.x);
+            x.y = fmaf(k, s[r].y, x.y);
+            x.z = fmaf(k, s[r].z, x.z);
+            x.w = fmaf(k, s[r].w, x.w);
+            o.x = fmaf(q, s[r].x, o.x);
+            o.y = fmaf(q, s[r].y, o.y);
+            o.z = fmaf(q, s[r].z, o.z);
+            o.w = fmaf(q, s[r].w, o.w);
+            sum.x = fmaf(k, k, sum.x);
+            sum.y = fmaf(q, q, sum.y);
+            sum.z = fmaf(k, q, sum.z);
         }
 #pragma unroll
         for (int d = kLanesPerRow; d < 32; d <<= 1) {
-            x.x += __shfl_xor_sync(0xffffffffu, x.x, d);
-            x.y += __shfl_xor_sync(0xffffffffu, x.y, d);
-            x.z += __shfl_xor_sync(0xffffffffu, x.z, d);
-            x.w += __shfl_xor_sync(0xffffffffu, x.w, d);
-            o.x += __shfl_xor_sync(0xffffffffu, o.x, d);
-            o.y += __shfl_xor_sync(0xffffffffu, o.y, d);
-            o.z += __shfl_xor_sync(0xffffffffu, o.z, d);
-            o.w += __shfl_xor_sync(0xffffffffu, o.w, d);
+            x = add4(x, shfl4(x, d));
+            o = add4(o, shfl4(o, d));
+            sum = add4(sum, shfl4(sum, d));
         }
         if (lane < kLanesPerRow) {
             *reinterpret_cast<float4 *>(&red_x[buf][warp][c4]) = x;
             *reinterpret_cast<float4 *>(&red_o[buf][warp][c4]) = o;
         }
-        __syncthreads();
-        float4 sx = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (lane == 0) red_s[buf][warp] = sum;
+        RowVec<kRows> kn, qn;
+        RowVec<4> vn;
+        float gn = 0.f, bn = 0.f;
+        if (MODE == DELTA_VERIFY && t + 1 < n) {
+            const size_t next = (size_t)(t + 1);
+            kn.load(kp + next * p.k_rs);
+            qn.load(qp + next * p.q_rs);
+            vn.load(vp + next * p.v_rs);
+            gn = gp[next * H];
+            bn = bp[next * H];
+        }
+        __syncthreads();  // one per token: buffer t & 1 is rewritten after the barrier of token t + 1
+        float4 sx = make_float4(0.f, 0.f, 0.f, 0.f), ss = sx;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float4 f = *reinterpret_cast<const float4 *>(&red_x[buf][w][c4]);
-            sx.x += f.x;
-            sx.y += f.y;
-            sx.z += f.z;
-            sx.w += f.w;
+            sx = add4(sx, *reinterpret_cast<const float4 *>(&red_x[buf][w][c4]));
+            ss = add4(ss, red_s[buf][w]);
         }
+        const float decay = expf(g);
+        const float rk = p.l2norm ? 1.f / sqrtf(ss.x + kDeltaEps) : 1.f;
+        const float rq = p.l2norm ? 1.f / sqrtf(ss.y + kDeltaEps) : 1.f;
         const float xs = decay * rk;
         float4 u;
-        u.x = beta * (bf_lo(vv.x) - xs * sx.x);
-        u.y = beta * (bf_hi(vv.x) - xs * sx.y);
-        u.z = beta * (bf_lo(vv.y) - xs * sx.z);
-        u.w = beta * (bf_hi(vv.y) - xs * sx.w);
+        u.x = beta * (vf[0] - xs * sx.x);
+        u.y = beta * (vf[1] - xs * sx.y);
+        u.z = beta * (vf[2] - xs * sx.z);
+        u.w = beta * (vf[3] - xs * sx.w);
+        float *dst = MODE == DELTA_VERIFY
+                         ? p.inter + (((size_t)b * n + t) * H + h) * kMat + (size_t)row0 * kHeadDim + col
+                         : state;
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
             const float kr = kf[r] * rk;
@@ -167,42 +174,30 @@ __global__ void __launch_bounds__(kThreads) delta_recurrent_kernel(const DeltaPa
             s[r].y = fmaf(kr, u.y, s[r].y * decay);
             s[r].z = fmaf(kr, u.z, s[r].z * decay);
             s[r].w = fmaf(kr, u.w, s[r].w * decay);
-        }
-        if constexpr (MODE == DELTA_VERIFY) {
-            float *dst = p.inter + (((size_t)b * p.N + t) * H + h) * kMat + col;
-#pragma unroll
-            for (int r = 0; r < kRows; ++r)
-                __stcs(reinterpret_cast<float4 *>(
-                           dst + (size_t)(row_group + r * kRowGroups) * kHeadDim),
-                       s[r]);
+            __stcs(reinterpret_cast<float4 *>(dst + (size_t)r * kHeadDim), s[r]);
         }
         if (threadIdx.x < kLanesPerRow) {
             float4 so = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float4 f = *reinterpret_cast<const float4 *>(&red_o[buf][w][c4]);
-                so.x += f.x;
-                so.y += f.y;
-                so.z += f.z;
-                so.w += f.w;
-            }
-            const float os = decay * rq;
-            const __nv_bfloat162 a =
-                __floats2bfloat162_rn(fmaf(kq, u.x, os * so.x) * kScale, fmaf(kq, u.y, os * so.y) * kScale);
-            const __nv_bfloat162 c =
-                __floats2bfloat162_rn(fmaf(kq, u.z, os * so.z) * kScale, fmaf(kq, u.w, os * so.w) * kScale);
+            for (int w = 0; w < kWarps; ++w)
+                so = add4(so, *reinterpret_cast<const float4 *>(&red_o[buf][w][c4]));
+            const float os = decay * rq, kq = ss.z * rk * rq;
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(fmaf(kq, u.x, os * so.x) * kScale,
+                                                            fmaf(kq, u.y, os * so.y) * kScale);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(fmaf(kq, u.z, os * so.z) * kScale,
+                                                            fmaf(kq, u.w, os * so.w) * kScale);
             uint2 w2;
-            w2.x = *reinterpret_cast<const uint32_t *>(&a);
-            w2.y = *reinterpret_cast<const uint32_t *>(&c);
-            *reinterpret_cast<uint2 *>(p.out + (tok * H + h) * kHeadDim + col) = w2;
+            w2.x = *reinterpret_cast<const uint32_t *>(&lo);
+            w2.y = *reinterpret_cast<const uint32_t *>(&hi);
+            *reinterpret_cast<uint2 *>(p.out + ((t_begin + t) * H + h) * kHeadDim + col) = w2;
         }
-    }
-
-    if constexpr (MODE != DELTA_VERIFY) {
-#pragma unroll
-        for (int r = 0; r < kRows; ++r)
-            __stcs(reinterpret_cast<float4 *>(state + (size_t)(row_group + r * kRowGroups) * kHeadDim),
-                   s[r]);
+        if (MODE == DELTA_VERIFY) {
+            kf = kn;
+            qf = qn;
+            vf = vn;
+            g = gn;
+            beta = bn;
+        }
     }
 }
 
@@ -226,7 +221,6 @@ cudaError_t launch_delta_recurrent(DeltaMode mode, const DeltaParams &p, int num
     switch (mode) {
         case DELTA_DECODE: return launch_mode<DELTA_DECODE>(p, num_sms, stream);
         case DELTA_VERIFY: return launch_mode<DELTA_VERIFY>(p, num_sms, stream);
-        case DELTA_EXTEND: return launch_mode<DELTA_EXTEND>(p, num_sms, stream);
     }
     return cudaErrorInvalidValue;
 }

@@ -25,7 +25,7 @@ struct DeltaParams {
 };
 constexpr float kDeltaEps = 1e-6f;
 
-enum DeltaMode : int { DELTA_DECODE = 0, DELTA_VERIFY = 1, DELTA_EXTEND = 2 };
+enum DeltaMode : int { DELTA_DECODE = 0, DELTA_VERIFY = 1 };
 // Token-serial kernels: the state stays in registers from the first token to the last.
 cudaError_t launch_delta_recurrent(DeltaMode mode, const DeltaParams &p, int num_sms,
                                    cudaStream_t stream);
