@@ -244,11 +244,6 @@ __device__ __forceinline__ long long gate_fixed(float g) {
 }
 constexpr float kFixedStep = 9.094947017729282379e-13f;  // 2^-40
 
-// Address of a 16 x 16 block's row for ldmatrix in a 128-byte-swizzled tile: row rho, 16-byte piece kc.
-__device__ __forceinline__ uint32_t sw_row(uint32_t tile, int rho, int kc) {
-    return tile + (uint32_t)rho * 128u + ((uint32_t)(kc ^ (rho & 7)) << 4);
-}
-
 // The fragments of rows 16 blk .. + 15 of the [K; Q] tile (Q: blk + 4) at k-step ks, as an A operand; as a
 // B operand the same registers are {0, 2} for columns 0-7 and {1, 3} for columns 8-15.  The tile starts on
 // a 1024-byte boundary and row blocks on multiples of 16, so the swizzle is an exclusive or of the lane's
@@ -362,8 +357,10 @@ __device__ void rank_requests(const DeltaParams &p, int block, int32_t *order, i
 // T', P T and the coefficients of one chunk and head (blockIdx.x = rank_ctas + slot * H + head); the first
 // rank_ctas CTAs order the requests for the chain kernel.
 __global__ void __launch_bounds__(kTThreads, 5)
-    delta_t_kernel(const DeltaParams p, uint8_t *ws, int32_t *order, int rank_ctas) {
+    delta_t_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                   const DeltaParams p, uint8_t *ws, int32_t *order, int rank_ctas) {
     extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t kq_full;
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int w = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -413,44 +410,63 @@ __global__ void __launch_bounds__(kTThreads, 5)
     const uint32_t off_p = (uint32_t)((midx & 1) * 256 + (midx >> 1) * 128 + mrow * 16);
     const int i16 = 16 * w + (lane & 15);            // this warp's tokens, twice
 
-    // K and Q into swizzled tiles; rows past the request's end read as zero
-    {
-        const __nv_bfloat16 *kp = p.k + t0 * p.k_rs + (size_t)(h / p.group) * kHeadDim;
-        const __nv_bfloat16 *qp = p.q + t0 * p.q_rs + (size_t)(h / p.group) * kHeadDim;
+    // K and Q into swizzled tiles
+    if (threadIdx.x == 0) {
+        mbar_init(&kq_full, 1);
+        fence_mbar_init();
+        mbar_arrive_expect_tx(&kq_full, SZ_KQ);
+        const int x = (h / p.group) * kHeadDim;
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-            const int rho = x * 8 + (int)(threadIdx.x >> 4), piece = threadIdx.x & 15;
-            const int i = rho & 63;
-            const __nv_bfloat16 *src = (rho < 64 ? kp + (size_t)i * p.k_rs : qp + (size_t)i * p.q_rs) + piece * 8;
-            cp_async16(sw_row(kq + (piece >> 3) * 16384u, rho, piece & 7), i < r ? (const void *)src : kp,
-                       i < r ? 16u : 0u);
-        }
-        cp_async_commit();
-    }
-    // running sums of the gates: every warp forms all 64
-    const float *gp = p.g + (t0 * p.H + h);
-    const float gn0 = lane < r ? gp[(size_t)lane * p.H] : 0.f;
-    const float gn1 = lane + 32 < r ? gp[(size_t)(lane + 32) * p.H] : 0.f;
-    const float bn = i16 < r ? p.beta[(t0 + i16) * p.H + h] : 0.f;
-    long long x0 = gate_fixed(gn0), x1 = gate_fixed(gn1);
-    // a NaN has no fixed-point form: it is passed on through beta
-    const uint32_t bad =
-        w < 2 ? __ballot_sync(0xffffffffu, gn0 != gn0) : __ballot_sync(0xffffffffu, gn1 != gn1);
-    const float beta = (bad >> (i16 & 31)) & 1u ? __uint_as_float(0x7fffffffu) : bn;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const long long y0 = __shfl_up_sync(0xffffffffu, x0, d);
-        const long long y1 = __shfl_up_sync(0xffffffffu, x1, d);
-        if (lane >= d) {
-            x0 += y0;
-            x1 += y1;
+        for (int y = 0; y < 2; ++y) {
+            tma_load_2d(sm + y * 16384, &tk, &kq_full, x + 64 * y, (int)t0);
+            tma_load_2d(sm + y * 16384 + 8192, &tq, &kq_full, x + 64 * y, (int)t0);
         }
     }
-    x1 += __shfl_sync(0xffffffffu, x0, 31);
-    const long long xend = __shfl_sync(0xffffffffu, x1, 31);
-    const long long xi = __shfl_sync(0xffffffffu, w < 2 ? x0 : x1, i16 & 31);
-    cp_async_wait_all();
+    // running sums of the gates, by warp 0, in the place of A's blocks; a NaN has no fixed-point form and
+    // is passed on through beta
+    long long *sums = reinterpret_cast<long long *>(abp);
+    uint32_t *nans = reinterpret_cast<uint32_t *>(sums + C);
+    if (w == 0) {
+        const float *gp = p.g + (t0 * p.H + h);
+        const float gn0 = lane < r ? gp[(size_t)lane * p.H] : 0.f;
+        const float gn1 = lane + 32 < r ? gp[(size_t)(lane + 32) * p.H] : 0.f;
+        long long x0 = gate_fixed(gn0), x1 = gate_fixed(gn1);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long y0 = __shfl_up_sync(0xffffffffu, x0, d);
+            const long long y1 = __shfl_up_sync(0xffffffffu, x1, d);
+            if (lane >= d) {
+                x0 += y0;
+                x1 += y1;
+            }
+        }
+        x1 += __shfl_sync(0xffffffffu, x0, 31);
+        sums[lane] = x0;
+        sums[lane + 32] = x1;
+        const uint32_t bad0 = __ballot_sync(0xffffffffu, gn0 != gn0);
+        const uint32_t bad1 = __ballot_sync(0xffffffffu, gn1 != gn1);
+        if (lane == 0) {
+            nans[0] = bad0;
+            nans[1] = bad1;
+        }
+    }
+    float beta = i16 < r ? p.beta[(t0 + i16) * p.H + h] : 0.f;
     __syncthreads();
+    const long long xi = sums[i16], xend = sums[C - 1];
+    if ((nans[i16 >> 5] >> (i16 & 31)) & 1u) beta = __uint_as_float(0x7fffffffu);
+    if (!mbar_wait(&kq_full, 0, p.wait_limit_ns)) {
+        // the copies are waited for once more before the CTA's shared memory goes away
+        if (threadIdx.x == 0) atomicOr(p.err, ERR_BIT_TIMEOUT);
+        mbar_wait(&kq_full, 0, kDrainLimitNs);
+        return;
+    }
+    if (r < C) {
+        // rows past the end hold the next request's tokens, and 0 x NaN is NaN: zero them
+        for (int x = r * 32 + (int)threadIdx.x; x < C * 32; x += kTThreads)  // (token, K or Q, block, piece)
+            *reinterpret_cast<uint4 *>(sm + ((x >> 3) & 1) * 16384 + ((x >> 5) + ((x >> 4) & 1) * 64) * 128 +
+                                       (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        __syncthreads();
+    }
 
     // ---- K K^T and Q K^T of the warp's blocks (a, b): the diagonal one (w, w), then (3,0) | (1,0) |
     // (2,0) (2,1) | (3,1) (3,2), rows of the warp's own fragments but for (3,0), which has its columns;
@@ -1155,7 +1171,7 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
     }
     if (t_ctas > 0) {
         e = launch_pdl(delta_t_kernel, dim3((unsigned)(rank_ctas + t_ctas)), dim3(kTThreads), kTSmemBytes,
-                       stream, p, w, order, rank_ctas);
+                       stream, tq, tk, p, w, order, rank_ctas);
         if (e != cudaSuccess) return e;
     }
     return launch_pdl(delta_extend_kernel, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, tq, tk,
