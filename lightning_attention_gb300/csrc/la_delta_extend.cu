@@ -12,8 +12,8 @@
 //   P_ij  = D^-0.5 rq_i rk_j e^{G_i - G_j} (q_i . k_j)             j <= i, else 0
 //   o_i   = D^-0.5 gamma_i rq_i X^Q_i + (P U)_i,   P U = (P T) R
 //   S     <- gamma_C S + K^T diag(e^{G_C - G_j} rk_j) U
-// Every exponent is formed as a difference of sums that are exact in fixed point, so that steep
-// decays lose nothing; factors are at most 1.
+// Every exponent is formed as a difference of sums that are kept as fp32 pairs, so that steep decays lose
+// nothing; factors are at most 1.
 //
 // Two kernels.  T and P T of a chunk depend on nothing before it, so a first kernel forms them for all
 // chunks at once (delta_t_kernel, a CTA of four warps per chunk and head), with the chunk's coefficients,
@@ -218,31 +218,40 @@ __device__ __forceinline__ void split_frag(const float (&c)[8], uint32_t (&hi)[4
     split2(c[6], c[7], hi[3], lo[3]);
 }
 
-// acc += A B with A and B bf16 pairs (the product of the two lo parts, 2^-16, is left out).
-__device__ __forceinline__ void prod16(float (&acc)[8], const uint32_t (&ah)[4], const uint32_t (&al)[4],
-                                       const uint32_t (&bh)[4], const uint32_t (&bl)[4]) {
+// acc + cross += A B with A and B bf16 pairs (the product of the two lo parts, 2^-16, is left out): two
+// sums, so that fewer MMAs wait for one another.
+__device__ __forceinline__ void prod16(float (&acc)[8], float (&cross)[8], const uint32_t (&ah)[4],
+                                       const uint32_t (&al)[4], const uint32_t (&bh)[4],
+                                       const uint32_t (&bl)[4]) {
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
         mma_16816(acc + 4 * n, ah, bh[2 * n], bh[2 * n + 1]);
-        mma_16816(acc + 4 * n, ah, bl[2 * n], bl[2 * n + 1]);
-        mma_16816(acc + 4 * n, al, bh[2 * n], bh[2 * n + 1]);
+        mma_16816(cross + 4 * n, ah, bl[2 * n], bl[2 * n + 1]);
+        mma_16816(cross + 4 * n, al, bh[2 * n], bh[2 * n + 1]);
     }
 }
 
 // ------------------------------------------------------------------------------------------------
 // T warps
 
-// 2^40 log2(e) g as a fixed-point number, -1e4 standing for everything below (e^-1e4 is 0 in fp32,
-// and the sums of a chunk stay finite), 1e4 for everything above.
-__device__ __forceinline__ long long gate_fixed(float g) {
-    constexpr float kHi = 1.44269502162933349609f;   // log2(e) in fp32
-    constexpr float kLo = 1.92596299112661746887e-8f;  // the rest
-    g = g < -1e4f ? -1e4f : g > 1e4f ? 1e4f : g;
-    const float p = g * kHi;
-    const float e = fmaf(g, kHi, -p) + g * kLo;
-    return __float2ll_rn(p * 1099511627776.f) + __float2ll_rn(e * 1099511627776.f);
+// A sum as hi + lo, lo the part that hi's rounding lost: sums of a chunk's gates keep about 2^-45.
+struct Sum2 {
+    float hi, lo;
+};
+__device__ __forceinline__ Sum2 add_sums(const Sum2 &a, const Sum2 &b) {
+    const float s = a.hi + b.hi, bb = s - a.hi;
+    const float lo = ((a.hi - (s - bb)) + (b.hi - bb)) + (a.lo + b.lo);
+    const float hi = s + lo;
+    return {hi, lo - (hi - s)};
 }
-constexpr float kFixedStep = 9.094947017729282379e-13f;  // 2^-40
+// log2(e) g, -1e4 standing for every g below (e^-1e4 is 0 in fp32, and the sums stay finite).
+__device__ __forceinline__ Sum2 gate_log2(float g) {
+    constexpr float kHi = 1.44269502162933349609f;     // log2(e) in fp32
+    constexpr float kLo = 1.92596299112661746887e-8f;  // the rest
+    g = g < -1e4f ? -1e4f : g;
+    const float p = g * kHi;
+    return {p, fmaf(g, kHi, -p) + g * kLo};
+}
 
 // The fragments of rows 16 blk .. + 15 of the [K; Q] tile (Q: blk + 4) at k-step ks, as an A operand; as a
 // B operand the same registers are {0, 2} for columns 0-7 and {1, 3} for columns 8-15.  The tile starts on
@@ -422,38 +431,28 @@ __global__ void __launch_bounds__(kTThreads, 5)
             tma_load_2d(sm + y * 16384 + 8192, &tq, &kq_full, x + 64 * y, (int)t0);
         }
     }
-    // running sums of the gates, by warp 0, in the place of A's blocks; a NaN has no fixed-point form and
-    // is passed on through beta
-    long long *sums = reinterpret_cast<long long *>(abp);
-    uint32_t *nans = reinterpret_cast<uint32_t *>(sums + C);
+    const float beta = i16 < r ? p.beta[(t0 + i16) * p.H + h] : 0.f;
+    // running sums of the gates, by warp 0
     if (w == 0) {
         const float *gp = p.g + (t0 * p.H + h);
-        const float gn0 = lane < r ? gp[(size_t)lane * p.H] : 0.f;
-        const float gn1 = lane + 32 < r ? gp[(size_t)(lane + 32) * p.H] : 0.f;
-        long long x0 = gate_fixed(gn0), x1 = gate_fixed(gn1);
+        Sum2 x0 = gate_log2(lane < r ? gp[(size_t)lane * p.H] : 0.f);
+        Sum2 x1 = gate_log2(lane + 32 < r ? gp[(size_t)(lane + 32) * p.H] : 0.f);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const long long y0 = __shfl_up_sync(0xffffffffu, x0, d);
-            const long long y1 = __shfl_up_sync(0xffffffffu, x1, d);
+            const Sum2 y0{__shfl_up_sync(0xffffffffu, x0.hi, d), __shfl_up_sync(0xffffffffu, x0.lo, d)};
+            const Sum2 y1{__shfl_up_sync(0xffffffffu, x1.hi, d), __shfl_up_sync(0xffffffffu, x1.lo, d)};
             if (lane >= d) {
-                x0 += y0;
-                x1 += y1;
+                x0 = add_sums(x0, y0);
+                x1 = add_sums(x1, y1);
             }
         }
-        x1 += __shfl_sync(0xffffffffu, x0, 31);
-        sums[lane] = x0;
-        sums[lane + 32] = x1;
-        const uint32_t bad0 = __ballot_sync(0xffffffffu, gn0 != gn0);
-        const uint32_t bad1 = __ballot_sync(0xffffffffu, gn1 != gn1);
-        if (lane == 0) {
-            nans[0] = bad0;
-            nans[1] = bad1;
-        }
+        x1 = add_sums(x1, {__shfl_sync(0xffffffffu, x0.hi, 31), __shfl_sync(0xffffffffu, x0.lo, 31)});
+        ghi[lane] = x0.hi;
+        glo[lane] = x0.lo;
+        ghi[lane + 32] = x1.hi;
+        glo[lane + 32] = x1.lo;
     }
-    float beta = i16 < r ? p.beta[(t0 + i16) * p.H + h] : 0.f;
     __syncthreads();
-    const long long xi = sums[i16], xend = sums[C - 1];
-    if ((nans[i16 >> 5] >> (i16 & 31)) & 1u) beta = __uint_as_float(0x7fffffffu);
     if (!mbar_wait(&kq_full, 0, p.wait_limit_ns)) {
         // the copies are waited for once more before the CTA's shared memory goes away
         if (threadIdx.x == 0) atomicOr(p.err, ERR_BIT_TIMEOUT);
@@ -512,22 +511,20 @@ __global__ void __launch_bounds__(kTThreads, 5)
         nq = (lane & 8 ? q1 : q0) + kDeltaEps;
     }
     {
-        const float inv = 1.f / sqrtf(lane < 16 ? nk : nq);
-        const float gam = ex2((float)xi * kFixedStep);
+        const float inv = p.l2norm ? rsqrtf(lane < 16 ? nk : nq) : 1.f;
+        const float gh = ghi[i16], gl = glo[i16];
+        const float gam = ex2(gh + gl);
         if (lane < 16) {
-            const float hi = (float)xi;
-            ghi[i16] = hi * kFixedStep;
-            glo[i16] = (float)(xi - __float2ll_rn(hi)) * kFixedStep;
             rk[i16] = inv;
             brk[i16] = beta * inv;
             cf[i16] = beta;
             cf[64 + i16] = -beta * gam * inv;
-            cf[128 + i16] = ex2((float)(xend - xi) * kFixedStep) * inv;
+            cf[128 + i16] = ex2((ghi[C - 1] - gh) + (glo[C - 1] - gl)) * inv;
         } else {
             qs[i16] = kScale * inv;
             cf[192 + i16] = kScale * gam * inv;
         }
-        if (w == 0 && lane == 0) cf[256] = ex2((float)xend * kFixedStep);
+        if (w == 0 && lane == 0) cf[256] = ex2(ghi[C - 1] + glo[C - 1]);
     }
     __syncthreads();  // K and Q are read: P and T' take their place
 
@@ -601,23 +598,25 @@ __global__ void __launch_bounds__(kTThreads, 5)
         for (int dr = 1; dr < 4; ++dr) {
             const int rr = b + dr;
             if (rr > 3) break;
-            float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            float acc[8] = {}, cross[8] = {};
             uint32_t bh[4], bl[4];
 #pragma unroll
             for (int dm = 0; dm < dr; ++dm) {
                 const uint32_t blk = ab + (rr * (rr - 1) / 2 + b + dm) * 1024 + off_p;
                 ldsm4(blk, bh);
                 ldsm4(blk + 512, bl);
-                prod16(acc, yh[dm], yl[dm], bh, bl);
+                prod16(acc, cross, yh[dm], yl[dm], bh, bl);
             }
             uint32_t zh[4], zl[4];
+            float t[8] = {}, tc[8] = {};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] += cross[e];
             split_frag(acc, zh, zl);
-            float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             ldsm4(td + rr * 1024 + off_p, bh);
             ldsm4(td + rr * 1024 + 512 + off_p, bl);
-            prod16(t, zh, zl, bh, bl);
+            prod16(t, tc, zh, zl, bh, bl);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) t[e] = -t[e];
+            for (int e = 0; e < 8; ++e) t[e] = -t[e] - tc[e];
             split_frag(t, zh, zl);
             // matrices (j half, i half) -> rows i of the tile, columns 16 b + j
             const uint32_t at = part_row(parts, b, 0, 16 * rr + 8 * (midx >> 1) + mrow, midx & 1);
@@ -632,35 +631,50 @@ __global__ void __launch_bounds__(kTThreads, 5)
             }
         }
     }
-    __syncthreads();  // T'
-
-    // ---- row block w of P T, over P
+    // ---- P T over P, five products a warp: blocks (3,0) (0,0) | (3,1) (1,0) | (2,0) (2,1) | (3,2) (1,1)
+    // (2,2) (3,3).  Every block of P is in its readers' registers before one is overwritten.
     {
-        uint32_t fh[4][4], fl[4][4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            if (m > w) break;
-            const uint32_t pa = part_row(parts, m, 1, 16 * w + (midx & 1) * 8 + mrow, midx >> 1);
-            ldsm4(pa, fh[m]);
-            ldsm4(pa + SZ_PART, fl[m]);
-        }
-        __syncwarp();
         const int k = (midx & 1) * 8 + mrow, nh = midx >> 1;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            if (b > w) break;
-            float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int m = b; m < 4; ++m) {
-                if (m > w) break;
-                uint32_t bh[4], bl[4];
-                const uint32_t at =
-                    m == b ? td + b * 1024 + nh * 256 + k * 16 : part_row(parts, b, 0, 16 * m + k, nh);
-                ldsm4_t(at, bh);
-                ldsm4_t(at + (m == b ? 512 : SZ_PART), bl);
-                prod16(acc, fh[m], fl[m], bh, bl);
+        const uint32_t pa_off = (uint32_t)((midx & 1) * 8 + mrow), kc = (uint32_t)(midx >> 1);
+        uint32_t fh[5][4], fl[5][4];
+        // the i-th product of the warp: P block (a, m) times T block (m, b)
+        auto which = [&](int i, int &a, int &m, int &b) {
+            if (w == 0) {
+                a = i < 4 ? 3 : 0, m = i < 4 ? i : 0, b = 0;
+            } else if (w == 1) {
+                a = i < 3 ? 3 : 1, m = i < 3 ? 1 + i : i - 3, b = i < 3 ? 1 : 0;
+            } else if (w == 2) {
+                a = 2, m = i < 3 ? i : i - 2, b = i < 3 ? 0 : 1;
+            } else {
+                a = i < 2 ? 3 : i - 1, m = i < 2 ? 2 + i : i - 1, b = i < 2 ? 2 : i - 1;
             }
-            put_block(sm, b, 1, 16 * w, row, cp, acc);
+        };
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+            int a, m, b;
+            which(i, a, m, b);
+            const uint32_t pa = part_row(parts, m, 1, 16 * a + pa_off, kc);
+            ldsm4(pa, fh[i]);
+            ldsm4(pa + SZ_PART, fl[i]);
+        }
+        __syncthreads();  // T' is written, P is read
+        float acc[8] = {}, cross[8] = {};
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+            int a, m, b;
+            which(i, a, m, b);
+            uint32_t bh[4], bl[4];
+            const uint32_t at = m == b ? td + b * 1024 + nh * 256 + k * 16 : part_row(parts, b, 0, 16 * m + k, nh);
+            ldsm4_t(at, bh);
+            ldsm4_t(at + (m == b ? 512 : SZ_PART), bl);
+            prod16(acc, cross, fh[i], fl[i], bh, bl);
+            if (m == a) {  // the block's last product
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] += cross[e];
+                put_block(sm, b, 1, 16 * a, row, cp, acc);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] = cross[e] = 0.f;
+            }
         }
     }
 
