@@ -898,7 +898,28 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
 }
 
 // ------------------------------------------------------------------------------------------------
-// MMA issuer (one warp, of which lane 0 issues)
+// MMA issuer: one warp, of which lane 0 issues.  The warp stays together and only the instruction itself is
+// predicated, so that its operands are formed by the uniform datapath: with a branch around them each MMA
+// took some 110 cycles to issue, longer than to run.
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t lead, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_u32(bar)),
+        "r"(lead)
+        : "memory");
+}
 __device__ void mma_role(Bars *bars, uint32_t tbase, uint32_t s_base, int nchunks, bool ragged, int lane,
                          Ctx cx) {
     const uint32_t id = idesc_bf16_f32(128, 128, false, false);
@@ -907,8 +928,9 @@ __device__ void mma_role(Bars *bars, uint32_t tbase, uint32_t s_base, int nchunk
     // swizzle); the low word holds the start address and the leading-dimension offset.
     const uint64_t high = sdesc_sw128(0, 0, 1024);
     const uint64_t high32 = sdesc_sw32(0, 0, 256);  // T's tile: rows of 32 bytes
+    uint32_t lead = lane == 0;  // 0 in every lane once a wait gave up
     auto mma = [&](uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint64_t hw) {
-        mma_f16_tmem_a(tbase + d, tbase + a, hw | b, idesc, acc);
+        mma_ts(lead, tbase + d, tbase + a, hw | b, idesc, acc);
     };
     bool ok = true;
     int st = 0;
@@ -918,62 +940,58 @@ __device__ void mma_role(Bars *bars, uint32_t tbase, uint32_t s_base, int nchunk
         // once a wait gave up nothing more is issued, but every named barrier is waited for
         ok = ok && warp_wait(&bars->kq_full[st], stp, cx) &&
              (c == 0 || warp_wait(&bars->o_free, (c - 1) & 1, cx));
+        if (!ok) lead = 0;
         const uint32_t kq = (s_base + OFF_KQ + st * SZ_KQ) >> 4;
         // a k-step starts as soon as the E warps have put it in place
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
             bar_wait(kBarS + y);
             tc_fence_after();
-            if (ok && lane == 0) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int kk = y + 4 * (x >> 1);  // hi, lo of k-steps y and 4 + y
-                    mma(TM_X, TM_S + 16u * kk + 8u * (x & 1),
-                        kq + ((kk >> 2) * 1024 + (kk & 3) * 2) + (1u << 16), id, y + x > 0, high);
-                }
-                if (y == 3) mma_commit(&bars->x_full);
+            for (int x = 0; x < 4; ++x) {
+                const int kk = y + 4 * (x >> 1);  // hi, lo of k-steps y and 4 + y
+                mma(TM_X, TM_S + 16u * kk + 8u * (x & 1),
+                    kq + ((kk >> 2) * 1024 + (kk & 3) * 2) + (1u << 16), id, y + x > 0, high);
             }
-            __syncwarp();
+            if (y == 3) commit_if(lead, &bars->x_full);
         }
         ok = ok && warp_wait(&bars->t_full[par], ph, cx);
+        if (!ok) lead = 0;
         const uint32_t tt = (s_base + OFF_T + par * 2 * SZ_T) >> 4;
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
             bar_wait(kBarR + y);
             tc_fence_after();
-            if (ok && lane == 0) {
 #pragma unroll
-                for (int x = 0; x < 6; ++x) {  // R_hi T_hi, R_lo T_hi, R_hi T_lo of k-steps y and 2 + y
-                    const int kk = y + 2 * (x / 3), term = x % 3;
-                    mma(TM_Y, TM_X + 16u * kk + (term == 1 ? 8u : 0u),
-                        tt + (term == 2 ? SZ_T >> 4 : 0u) + kk * (4096u >> 4) + (1u << 16), id, y + x > 0,
-                        high32);
-                }
-                if (y == 1) {
-                    mma_commit(&bars->y_full);
-                    mma_commit(&bars->y_done[par]);
-                }
+            for (int x = 0; x < 6; ++x) {  // R_hi T_hi, R_lo T_hi, R_hi T_lo of k-steps y and 2 + y
+                const int kk = y + 2 * (x / 3), term = x % 3;
+                mma(TM_Y, TM_X + 16u * kk + (term == 1 ? 8u : 0u),
+                    tt + (term == 2 ? SZ_T >> 4 : 0u) + kk * (4096u >> 4) + (1u << 16), id, y + x > 0,
+                    high32);
             }
-            __syncwarp();
+            if (y == 1) {
+                commit_if(lead, &bars->y_full);
+                commit_if(lead, &bars->y_done[par]);
+            }
         }
-        if (ragged && c == nchunks - 1) ok = ok && warp_wait(&bars->kq_fixed, 0, cx);
+        if (ragged && c == nchunks - 1) {
+            ok = ok && warp_wait(&bars->kq_fixed, 0, cx);
+            if (!ok) lead = 0;
+        }
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
             bar_wait(kBarU + y);
             tc_fence_after();
-            if (ok && lane == 0) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int kk = y + 2 * (x >> 1);
-                    mma(TM_D, TM_Y + 16u * kk + 8u * (x & 1), kq + kk * 128 + ((16384u >> 4) << 16), idD,
-                        y + x > 0, high);
-                }
-                if (y == 1) {
-                    mma_commit(&bars->d_full);
-                    mma_commit(&bars->kq_empty[st]);
-                }
+            for (int x = 0; x < 4; ++x) {
+                const int kk = y + 2 * (x >> 1);
+                mma(TM_D, TM_Y + 16u * kk + 8u * (x & 1), kq + kk * 128 + ((16384u >> 4) << 16), idD,
+                    y + x > 0, high);
             }
-            __syncwarp();
+            if (y == 1) {
+                commit_if(lead, &bars->d_full);
+                commit_if(lead, &bars->kq_empty[st]);
+            }
         }
         if (++st == kStages) {
             st = 0;
@@ -1042,7 +1060,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Bars *bars = reinterpret_cast<Bars *>(sm + OFF_BAR);
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
@@ -1104,7 +1122,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tbase = bars->tmem_base;
+    // the same in every lane, for the uniform datapath
+    const uint32_t tbase = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
     const Ctx cx{p.wait_limit_ns, &bars->abort_flag, p.err};
 
     if (warp < kEWarps) {
