@@ -67,23 +67,21 @@ constexpr float kScale = 0.08838834764831845f;  // 128^-0.5
 
 constexpr uint32_t kTmemCols = 512;
 // The operands S, R and U are kept per k-step (16 values of the contraction) as 8 columns of hi parts,
-// two to a column, and 8 of lo parts.  X: [K | Q] tokens, R replaces the K part 16 tokens by 16; Y:
-// [U | O'], U likewise.
+// two to a column, and 8 of lo parts.  X: [K | Q] tokens, R replaces the K part 16 tokens by 16; Y: per 16
+// tokens [U | O'], U likewise.
 constexpr uint32_t TM_S = 0, TM_X = 128, TM_Y = 256, TM_D = 384;
 
-// What the first kernel leaves per chunk and head: [T'; P T] as its hi and its lo parts, then the
-// coefficients: beta, -beta gamma rk, lam rk and scale gamma rq per token, gamma_C.  A part is cut by
-// k-steps kk of 16 columns, of which only rows 16 kk .. 63 are not zero: per step first T''s rows, then
-// P T's, 32 bytes each, with the 16-byte pieces of a row swapped where the row's bit 2 is set (the 32-byte
-// swizzle that the MMA reads).
+// What the first kernel leaves per chunk and head: T' and P T as their hi and their lo parts, then the
+// coefficients: beta, -beta gamma rk, lam rk and scale gamma rq per token, gamma_C.  T' and P T are stacked
+// by blocks of 16 rows (T' of tokens 16 a .., then P T of them, a = 0 .. 3), and a part is cut by k-steps kk
+// of 16 columns, of which only the row blocks a >= kk are not zero: 128 - 32 kk rows of 32 bytes, with the
+// 16-byte pieces of a row swapped where the row's bit 2 is set (the 32-byte swizzle that the MMA reads).
 constexpr uint32_t SZ_PART = 10240;
 constexpr uint32_t SZ_COEF = 4 * 256 + 16;
 constexpr uint32_t SZ_SLOT = 2 * SZ_PART + SZ_COEF;
-// Offset within a part of row 0 of T' (pt = 0) or P T (pt = 1) of step kk.
-__host__ __device__ constexpr uint32_t part_ofs(int kk, int pt) {
-    return (uint32_t)(4096 * kk - 512 * kk * (kk - 1) + pt * (2048 - 512 * kk) - 512 * kk);
-}
-static_assert(part_ofs(3, 1) + 64 * 32 == SZ_PART, "part layout");
+// Offset within a part of step kk.
+__host__ __device__ constexpr uint32_t part_ofs(int kk) { return (uint32_t)(4096 * kk - 512 * kk * (kk - 1)); }
+static_assert(part_ofs(4) == SZ_PART, "part layout");
 // Chunk slots of a batch: request b's start at floor(cu_seqlens[b] / C) + b, far enough from the next
 // request's for its ceil(length / C) chunks.
 __host__ __device__ inline long long chunk_slots(long long T, long long B) { return T / C + B; }
@@ -93,11 +91,10 @@ constexpr int kStages = 3;
 constexpr uint32_t SZ_KQ = 32768;                          // [64 K rows; 64 Q rows][128], swizzled
 constexpr uint32_t OFF_KQ = 0;
 constexpr uint32_t OFF_V = OFF_KQ + kStages * SZ_KQ;       // 2 x [64][128], rows of 256 bytes
-// 2 x (hi, lo) x 4 k-steps x [64 T' rows; 64 P T rows][16], with the 32-byte swizzle
-constexpr uint32_t SZ_T = 16384;
-constexpr uint32_t OFF_T = OFF_V + 2 * 16384;
-constexpr uint32_t OFF_COEF = OFF_T + 4 * SZ_T;            // 2 x a slot's coefficients
-constexpr uint32_t OFF_BAR = OFF_COEF + 2 * SZ_COEF;
+constexpr uint32_t OFF_T = OFF_V + 2 * 16384;              // 2 x a slot
+constexpr uint32_t SZ_T = (SZ_SLOT + 255) / 256 * 256;     // whole swizzle atoms
+constexpr uint32_t OFF_COEF = OFF_T + 2 * SZ_PART;         // a slot's coefficients
+constexpr uint32_t OFF_BAR = OFF_T + 2 * SZ_T;
 constexpr uint32_t SZ_BAR = 256;
 constexpr uint32_t kSmemBytes = OFF_BAR + SZ_BAR + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -270,9 +267,10 @@ __device__ __forceinline__ void dot_frag(float *acc, const uint32_t (&a)[4], con
     mma_16816(acc + 4, a, b[1], b[3]);
 }
 
-// Address of a row's 16-byte piece kc (0, 1) in a part: row rho of T' or P T, columns of step kk.
+// Address of a row's 16-byte piece kc (0, 1) in a part: row rho of T' (pt = 0) or P T (1), columns of step kk.
 __device__ __forceinline__ uint32_t part_row(uint32_t part, int kk, int pt, int rho, int kc) {
-    return part + part_ofs(kk, pt) + (uint32_t)rho * 32u + ((uint32_t)(kc ^ ((rho >> 2) & 1)) << 4);
+    return part + part_ofs(kk) + (uint32_t)(rho + 16 * ((rho >> 4) + pt) - 32 * kk) * 32u +
+           ((uint32_t)(kc ^ ((rho >> 2) & 1)) << 4);
 }
 // A fragment block (16 x 16) as a bf16 pair: rows rho0 .. + 15 of step kk.
 __device__ __forceinline__ void put_block(uint8_t *parts, int kk, int pt, int rho0, int row, int cp,
@@ -719,7 +717,7 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
     const int tok0 = 32 * hf;  // tokens tok0 .. + 31 of the chunk
     const uint32_t lanes = tbase + ((uint32_t)(32 * q) << 16);
     const uint32_t ts = lanes + TM_S + 64u * hf;
-    const uint32_t tx = lanes + TM_X + 32u * hf, ty = lanes + TM_Y + 32u * hf, td = lanes + TM_D + 64u * hf;
+    const uint32_t tx = lanes + TM_X + 32u * hf, ty = lanes + TM_Y + 64u * hf, td = lanes + TM_D + 64u * hf;
     float *gs = p.pool + (((size_t)slot * p.H + h) * kHeadDim + 64 * hf) * kHeadDim + v;
 
     uint64_t S[32];  // S[64 hf + 2 x, 64 hf + 2 x + 1][v]
@@ -751,7 +749,7 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
         }
         const uint32_t par = c & 1, ph = (c >> 1) & 1;
         const int r = n - c * C;  // tokens from this chunk on
-        const float *cf = reinterpret_cast<const float *>(sm + OFF_COEF + par * SZ_COEF) + tok0;
+        const float *cf = reinterpret_cast<const float *>(sm + OFF_COEF + par * SZ_T) + tok0;
         // ---- R = beta V - (beta gamma rk) X^K; what needs no X is formed while its product runs
         if (!warp_wait(&bars->t_full[par], ph, cx)) {
             give_up(kBarR, c);
@@ -812,12 +810,12 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 tmem_ld_wait_regs(w[y]);
-                if (y == 0) tmem_ld16(ty + 16u, w[1]);
+                if (y == 0) tmem_ld16(ty + 32u, w[1]);
 #pragma unroll
                 for (int x = 0; x < 8; ++x)
                     R[8 * y + x] =
                         mul2(f[8 * y + x], add2(R[8 * y + x], f2u(w[y][2 * x], w[y][2 * x + 1])));
-                put_step(ty + 16u * y, R + 8 * y, kBarU + y);
+                put_step(ty + 32u * y, R + 8 * y, kBarU + y);
             }
         }
 
@@ -832,7 +830,7 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
             for (int z = 0; z < 2; ++z) {
                 uint32_t w[16], y[16];
                 tmem_ld16(tx + 64u + 16u * z, w);
-                tmem_ld16(ty + 64u + 16u * z, y);
+                tmem_ld16(ty + 16u + 32u * z, y);
                 tmem_ld_wait_regs(w);
                 tmem_ld_wait_regs(y);
                 if (z == 1) {
@@ -957,17 +955,18 @@ __device__ void mma_role(Bars *bars, uint32_t tbase, uint32_t s_base, int nchunk
         }
         ok = ok && warp_wait(&bars->t_full[par], ph, cx);
         if (!ok) lead = 0;
-        const uint32_t tt = (s_base + OFF_T + par * 2 * SZ_T) >> 4;
+        const uint32_t tt = (s_base + OFF_T + par * SZ_T) >> 4;
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
             bar_wait(kBarR + y);
             tc_fence_after();
 #pragma unroll
-            for (int x = 0; x < 6; ++x) {  // R_hi T_hi, R_lo T_hi, R_hi T_lo of k-steps y and 2 + y
+            for (int x = 0; x < 6; ++x) {  // R_hi T_hi, R_lo T_hi, R_hi T_lo of k-steps y and 2 + y,
+                                           // for the rows that are not zero
                 const int kk = y + 2 * (x / 3), term = x % 3;
-                mma(TM_Y, TM_X + 16u * kk + (term == 1 ? 8u : 0u),
-                    tt + (term == 2 ? SZ_T >> 4 : 0u) + kk * (4096u >> 4) + (1u << 16), id, y + x > 0,
-                    high32);
+                mma(TM_Y + 32u * kk, TM_X + 16u * kk + (term == 1 ? 8u : 0u),
+                    tt + (term == 2 ? SZ_PART >> 4 : 0u) + (part_ofs(kk) >> 4) + (1u << 16),
+                    idesc_bf16_f32(128, 128 - 32 * kk, false, false), y + x > 0, high32);
             }
             if (y == 1) {
                 commit_if(lead, &bars->y_full);
@@ -985,7 +984,7 @@ __device__ void mma_role(Bars *bars, uint32_t tbase, uint32_t s_base, int nchunk
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int kk = y + 2 * (x >> 1);
-                mma(TM_D, TM_Y + 16u * kk + 8u * (x & 1), kq + kk * 128 + ((16384u >> 4) << 16), idD,
+                mma(TM_D, TM_Y + 32u * kk + 8u * (x & 1), kq + kk * 128 + ((16384u >> 4) << 16), idD,
                     y + x > 0, high);
             }
             if (y == 1) {
@@ -1029,15 +1028,7 @@ __device__ void producer_role(const CUtensorMap &tq, const CUtensorMap &tk, cons
                        !wait_bar(&bars->c_free[g], ((c >> 1) - 1) & 1, cx)))
             break;
         mbar_arrive_expect_tx(&bars->t_full[g], SZ_SLOT);
-        const uint8_t *slot = slots + c * slot_step;
-#pragma unroll
-        for (int x = 0; x < 16; ++x) {  // (part, step, T' or P T): rows 16 kk .. 63
-            const int kk = (x >> 1) & 3, pt = x & 1;
-            bulk_load(sm + OFF_T + (2 * g + (x >> 3)) * SZ_T + kk * 4096 + pt * 2048 + kk * 512,
-                      slot + (x >> 3) * SZ_PART + part_ofs(kk, pt) + kk * 512, 2048 - kk * 512,
-                      &bars->t_full[g]);
-        }
-        bulk_load(sm + OFF_COEF + g * SZ_COEF, slot + 2 * SZ_PART, SZ_COEF, &bars->t_full[g]);
+        bulk_load(sm + OFF_T + g * SZ_T, slots + c * slot_step, SZ_SLOT, &bars->t_full[g]);
         mbar_arrive_expect_tx(&bars->v_full[g], 16384);
         tma_load_2d(sm + OFF_V + g * 16384, &tv, &bars->v_full[g], xv, y);
         vv = c + 1;
@@ -1115,10 +1106,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tk);
         tma_prefetch_desc(&tv);
     }
-    // the rows of T' and P T before a k-step's columns stay zero
-    for (int x = threadIdx.x; x < (int)(4 * SZ_T / 16); x += kThreads)
-        reinterpret_cast<uint4 *>(sm + OFF_T)[x] = make_uint4(0u, 0u, 0u, 0u);
-    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
