@@ -19,8 +19,8 @@
 // chunks at once (delta_t_kernel, a CTA of four warps per chunk and head), with the chunk's coefficients,
 // into the workspace; the second runs the chain over the chunks, one CTA per (request, head)
 // (delta_extend_kernel).  One kernel with T warps beside the chain took 393 us on 8 requests of 512-4096
-// tokens x 16 heads: while tcgen05.mma instructions stream, warp-level MMAs are starved and a shared-memory
-// load takes about 280 cycles, so T (11,000 cycles a chunk) held the chain up.
+// tokens x 16 heads: while tcgen05.mma instructions stream, warp-level MMAs are starved (four take 1,764
+// cycles in place of 79), so T held the chain up.
 //
 // The chain is computed transposed: lanes of tensor memory are the 128 value columns.
 //   X^T = S^T [K; Q]^T,   [U; O']^T = R^T [T'; P T]^T,   dS^T = U^T K
@@ -35,15 +35,16 @@
 // that in the mean; U takes R itself in fp32 and only T' R through pairs; the state stays in fp32
 // registers and is never accumulated in tensor memory (which does not round to nearest).
 //
-// Roles of the chain kernel (352 threads, one CTA per SM):
+// Roles of the chain kernel (384 threads, one CTA per SM):
 //   warps 0-7   E: the state (32 v rows x 64 k columns a warp) and the passes R, U, O and S;
 //   warp 8      TMA producer; warp 9 tensor-memory owner and MMA issuer;
 //   warp 10     zeroes the K rows past the end of the request's last chunk (they hold the next
 //               request's keys, and 0 x NaN is NaN).
 // Per chunk the chain is X -> R -> T' R -> U -> U^T K -> S; the output pass runs under U^T K.
 //
-// Every wait ends: mbarrier waits have a deadline (the named barriers below end with them); one that runs out sets the error word and an abort flag
-// that ends every role, then the CTA waits for its copies and MMAs, frees tensor memory and exits.
+// Every wait ends: mbarrier waits have a deadline (the named barriers below end with them); one that runs out
+// sets the error word and an abort flag that ends every role, then the CTA waits for its copies and MMAs,
+// frees tensor memory and exits.
 #include <cuda.h>
 #include <string.h>
 
@@ -60,7 +61,10 @@ using namespace sm100;
 
 constexpr int C = 64;  // tokens of a chunk
 constexpr int kEWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kFixWarp = 10;
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
+// registers per thread of the warp groups: 2 x 184 (E) + 136 = 3 x 168, the launch's share
+constexpr int kRegsE = 184, kRegsRest = 136;
+static_assert(2 * kRegsE + kRegsRest <= 3 * 168, "register split");
 constexpr int kTThreads = 128;
 constexpr int kMaxRanked = 8192;  // requests of a batch that is taken longest first
 constexpr float kScale = 0.08838834764831845f;  // 128^-0.5
@@ -125,8 +129,8 @@ constexpr uint32_t TK_TOK = TK_TD + 4 * 1024;              // per token: ghi, gl
 constexpr uint32_t kTSmemBytes = TK_TOK + 5 * 256 + 1024;
 
 // Named barriers between the E warps, which arrive, and the MMA warp, which waits: k-steps y and 4 + y of S
-// (kBarS + y), y and 2 + y of R and U (kBarR + y, kBarU + y) are in place.  They cost a handover some 30
-// cycles where an mbarrier, polled in shared memory beside streaming MMAs, costs 200.  They have no deadline of
+// (kBarS + y), y and 2 + y of R and U (kBarR + y, kBarU + y) are in place.  A test of an
+// mbarrier takes about 113 cycles when eight warps poll, a named barrier about 30.  They have no deadline of
 // their own: the E warps arrive at every one of every chunk, whether their own (bounded) waits succeed or
 // not, so the MMA warp's waits end when theirs do.
 constexpr int kBarS = 1, kBarR = 5, kBarU = 7;
@@ -369,7 +373,7 @@ __global__ void __launch_bounds__(kTThreads, 5)
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t kq_full;
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const int w = threadIdx.x >> 5;
+    const int w = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);  // uniform, so its branches are too
     const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
@@ -1113,6 +1117,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tbase = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
     const Ctx cx{p.wait_limit_ns, &bars->abort_flag, p.err};
 
+    if (warp < kEWarps)
+        reg_inc<kRegsE>();
+    else
+        reg_dec<kRegsRest>();
     if (warp < kEWarps) {
         e_role(p, sm, bars, cx, tbase, warp & 3, warp >> 2, lane, (size_t)t_req0, n, h, slot,
                p.prefix_mask[b] != 0, nchunks);
