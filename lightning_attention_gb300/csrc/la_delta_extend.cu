@@ -1,5 +1,5 @@
 // la_delta_extend.cu -- chunked gated delta rule on the 5th-generation tensor cores, one CTA per
-// (request, value head).
+// (request, value head), or several where there are few.
 //
 // Per request and head, token by token: S <- e^{g} S; u = beta (v - S^T k); S <- S + k u^T;
 // o = D^-0.5 S^T q (q, k divided by their 2-norms first if asked).  Over a chunk of C = 64 tokens with
@@ -18,9 +18,10 @@
 // Two kernels.  T and P T of a chunk depend on nothing before it, so a first kernel forms them for all
 // chunks at once (delta_t_kernel, a CTA of four warps per chunk and head), with the chunk's coefficients,
 // into the workspace; the second runs the chain over the chunks, one CTA per (request, head)
-// (delta_extend_kernel).  One kernel with T warps beside the chain took 393 us on 8 requests of 512-4096
-// tokens x 16 heads: while tcgen05.mma instructions stream, warp-level MMAs are starved (four take 1,764
-// cycles in place of 79), so T held the chain up.
+// (delta_extend_kernel; a long request among few is split, see Split).  One kernel with T warps beside the
+// chain took 393 us on 8 requests of 512-4096 tokens x 16 heads, the two take 220: while tcgen05.mma
+// instructions stream, warp-level MMAs are starved (four take 1,764 cycles in place of 79), so T held the
+// chain up.
 //
 // The chain is computed transposed: lanes of tensor memory are the 128 value columns.
 //   X^T = S^T [K; Q]^T,   [U; O']^T = R^T [T'; P T]^T,   dS^T = U^T K
@@ -690,6 +691,48 @@ __global__ void __launch_bounds__(kTThreads, 5)
 }
 
 // ------------------------------------------------------------------------------------------------
+// Split of a long request.  With few (request, head) pairs the chain leaves SMs idle, and a segment of it
+// can be run without its start state: its chunks take S to M S + N, N being the segment's result from
+// S = 0 and M its result from the identity with V = 0, which are two more chains of the same kernel.  So the
+// chain is cut into segs segments, the first ratio times as long as the others:
+//   pass 1   segment 0 as usual; N and M of segments 1 .. segs - 2, side by side with it;
+//   join     the segments' start states, S_1 from pass 1, S_{g+1} = M_g S_g + N_g in fp32;
+//   pass 2   segments 1 .. segs - 1 from their start states, side by side.
+// Rounding in a segment is amplified by the segments after it as the chain's own is.
+// Measured whole / split, us, T kernel included, l2norm, one request: 8 heads: 1,024 tokens 47.5 / 45.8,
+// 2,048: 84.6 / 66.5, 16,384: 626 / 199; 32 heads: 1,024: 52.7 / 61.9, 1,536: 75.3 / 73.7, 16,384:
+// 703 / 438; 76 heads: 2,560: 145 / 149, 4,096: 222 / 212, 16,384: 836 / 720.
+struct Split {
+    int segs, ratio;
+    int pass;       // 0: not split
+    float *starts;  // [chains][segs - 1][D][D]: S_g at g - 1 (N_{g-1} before the join)
+    float *trans;   // [chains][segs - 2][D][D]: M_g at g - 1
+};
+constexpr int kMaxSegs = 16;
+constexpr int kSplitSMs = 152;       // chains that run side by side
+constexpr int kSplitMinChunks = 20;  // shorter requests are not split
+// What the join and two more launches cost, and a segment in the join, in chunks of the chain.
+constexpr double kSplitCost = 5., kJoinCost = 1.;
+constexpr double kSplitGain = .95;  // a split has to promise this much
+constexpr size_t kMat = (size_t)kHeadDim * kHeadDim;
+// Chunks of segments 1, 2 ..; the last segment that has any.
+__host__ __device__ inline int split_base(const Split &s, int nchunks) {
+    return (nchunks + s.ratio + s.segs - 2) / (s.ratio + s.segs - 1);
+}
+__host__ __device__ inline int split_last(const Split &s, int nchunks) {
+    const int base = split_base(s, nchunks), rest = nchunks - s.ratio * base;
+    return rest > 0 ? 1 + (rest - 1) / base : 0;
+}
+
+// Where a CTA's chain starts and ends, and whether it writes outputs.
+struct Ends {
+    const float *from;  // null: zero, or the identity for a transition
+    float *to;          // null: not kept
+    bool transition;    // V counts as zero
+    bool emit;
+};
+
+// ------------------------------------------------------------------------------------------------
 // E warps: lanes are value columns v = 32 q + lane; half hf of the chunk's tokens and of the k columns.
 
 // Eight pairs (one k-step of an operand) as 8 columns of hi parts and 8 of lo parts; the MMA issuer may
@@ -715,22 +758,28 @@ __device__ __forceinline__ void load_pairs(const float *src, uint64_t (&x)[16]) 
     }
 }
 
+template <bool SPLIT>
 __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx &cx, uint32_t tbase, int q,
-                       int hf, int lane, size_t t0, int n, int h, int slot, bool prefix, int nchunks) {
+                       int hf, int lane, size_t t0, int n, int h, const Ends &ends, int nchunks) {
     const int v = 32 * q + lane;
     const int tok0 = 32 * hf;  // tokens tok0 .. + 31 of the chunk
     const uint32_t lanes = tbase + ((uint32_t)(32 * q) << 16);
     const uint32_t ts = lanes + TM_S + 64u * hf;
     const uint32_t tx = lanes + TM_X + 32u * hf, ty = lanes + TM_Y + 64u * hf, td = lanes + TM_D + 64u * hf;
-    float *gs = p.pool + (((size_t)slot * p.H + h) * kHeadDim + 64 * hf) * kHeadDim + v;
+    const int at = 64 * hf * kHeadDim + v;
+    const bool transition = SPLIT && ends.transition, emit = !SPLIT || ends.emit;
 
     uint64_t S[32];  // S[64 hf + 2 x, 64 hf + 2 x + 1][v]
-    if (prefix) {
+    if (ends.from) {
+        const float *gs = ends.from + at;
 #pragma unroll
         for (int x = 0; x < 32; ++x) S[x] = f2(gs[2 * x * kHeadDim], gs[(2 * x + 1) * kHeadDim]);
     } else {
 #pragma unroll
-        for (int x = 0; x < 32; ++x) S[x] = 0ull;
+        for (int x = 0; x < 32; ++x) {
+            const int d = transition ? v - 64 * hf - 2 * x : -1;
+            S[x] = f2(d == 0 ? 1.f : 0.f, d == 1 ? 1.f : 0.f);
+        }
     }
     if (nchunks > 0) {
 #pragma unroll
@@ -772,7 +821,7 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
             for (int x = 0; x < 16; ++x) {
                 const uint32_t v0 = *reinterpret_cast<const uint16_t *>(vp + (2 * x) * 256);
                 const uint32_t v1 = *reinterpret_cast<const uint16_t *>(vp + (2 * x + 1) * 256);
-                R[x] = mul2(R[x], f2u(v0 << 16, v1 << 16));
+                R[x] = transition ? 0ull : mul2(R[x], f2u(v0 << 16, v1 << 16));
             }
         }
         if (!warp_wait(&bars->x_full, par, cx)) {
@@ -825,7 +874,9 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
 
         // ---- o = (scale gamma rq) X^Q + P T R; neighbouring lanes exchange halves, so that each
         // stores two value columns of one token
-        {
+        if (!emit) {
+            warp_arrive(&bars->o_free, lane);
+        } else {
             const size_t tok = t0 + (size_t)c * C + tok0 + (lane & 1);
             __nv_bfloat16 *op = p.out + (tok * p.H + h) * kHeadDim + (v & ~1);
             const size_t two = (size_t)p.H * kHeadDim * 2;
@@ -888,7 +939,8 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
             }
         }
     }
-    if (ok && !(prefix && nchunks == 0)) {
+    if (ok && ends.to) {
+        float *gs = ends.to + at;
 #pragma unroll
         for (int x = 0; x < 32; ++x) {
             float a, b;
@@ -1049,9 +1101,11 @@ __device__ void producer_role(const CUtensorMap &tq, const CUtensorMap &tk, cons
     }
 }
 
+template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     delta_extend_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                        const __grid_constant__ CUtensorMap tv, const DeltaParams p, const uint8_t *ws, const int32_t *order) {
+                        const __grid_constant__ CUtensorMap tv, const DeltaParams p, const uint8_t *ws,
+                        const int32_t *order, const Split split) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Bars *bars = reinterpret_cast<Bars *>(sm + OFF_BAR);
@@ -1059,8 +1113,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
-    const int h = (int)blockIdx.x % p.H;
-    const int want = (int)blockIdx.x / p.H;
+    const int chains = p.B * p.H;
+    const int chain = (int)blockIdx.x % chains, job = (int)blockIdx.x / chains;
+    const int h = chain % p.H;
+    const int want = chain / p.H;
 
     // Longest request first where there is more than one wave of CTAs: they are issued in index order, so
     // long requests do not finish last.
@@ -1076,9 +1132,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (threadIdx.x == 0) atomicOr(p.err, ERR_BIT_SEQLENS);
         return;
     }
-    const int n = t_req1 - t_req0;
-    const int nchunks = (n + C - 1) / C;
+    int n = t_req1 - t_req0, c0 = 0;  // tokens and first chunk of this CTA
+    int nchunks = (n + C - 1) / C;
+    float *state = p.pool + ((size_t)slot * p.H + h) * kMat;
+    Ends ends{p.prefix_mask[b] ? state : nullptr, p.prefix_mask[b] && n == 0 ? nullptr : state, false, true};
+    if (SPLIT) {
+        const int base = split_base(split, nchunks), last = split_last(split, nchunks);
+        float *starts = split.starts + (size_t)chain * (split.segs - 1) * kMat;
+        int seg = 0;
+        if (split.pass == 2) {
+            seg = 1 + job;
+            if (seg > last) return;
+            ends.from = starts + (seg - 1) * kMat;
+            if (seg < last) ends.to = nullptr;
+        } else if (job > 0) {
+            seg = 1 + ((job - 1) >> 1);
+            if (seg >= last) return;
+            ends.from = nullptr;
+            ends.transition = job & 1;
+            ends.to = ends.transition
+                          ? split.trans + ((size_t)chain * (split.segs - 2) + seg - 1) * kMat
+                          : starts + seg * kMat;
+            ends.emit = false;
+        } else if (last > 0) {
+            ends.to = starts;
+        }
+        c0 = seg ? (split.ratio + seg - 1) * base : 0;
+        n -= c0 * C;
+        nchunks -= c0;
+        if (seg < last) {
+            nchunks = seg ? base : split.ratio * base;
+            n = nchunks * C;
+        }
+    }
     const bool ragged = n % C != 0;
+    const int t_seg = t_req0 + c0 * C;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -1122,12 +1210,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     else
         reg_dec<kRegsRest>();
     if (warp < kEWarps) {
-        e_role(p, sm, bars, cx, tbase, warp & 3, warp >> 2, lane, (size_t)t_req0, n, h, slot,
-               p.prefix_mask[b] != 0, nchunks);
+        e_role<SPLIT>(p, sm, bars, cx, tbase, warp & 3, warp >> 2, lane, (size_t)t_seg, n, h, ends, nchunks);
     } else if (warp == kProducerWarp) {
         if (lane == 0)
-            producer_role(tq, tk, tv, bars, sm, ws + ((size_t)((t_req0 >> 6) + b) * p.H + h) * SZ_SLOT,
-                          (size_t)p.H * SZ_SLOT, t_req0, nchunks, (h / p.group) * kHeadDim, h * kHeadDim, cx);
+            producer_role(tq, tk, tv, bars, sm,
+                          ws + ((size_t)((t_req0 >> 6) + b + c0) * p.H + h) * SZ_SLOT,
+                          (size_t)p.H * SZ_SLOT, t_seg, nchunks, (h / p.group) * kHeadDim, h * kHeadDim, cx);
     } else if (warp == kMmaWarp) {
         mma_role(bars, tbase, smem_u32(sm), nchunks, ragged, lane, cx);
     } else if (warp == kFixWarp && ragged) {
@@ -1150,12 +1238,120 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// The join: a CTA of 256 threads takes kJoinCols columns of one chain's states through all segments.
+// 128 x 128 x kJoinCols fp32 products a segment, 4 x 4 of them a thread, so that a shared-memory load feeds
+// eight; M is fetched one segment ahead (64 KB, from L2).
+constexpr int kJoinCols = 32, kJoinThreads = 256;
+constexpr int kJoinPitch = kHeadDim + 4;
+constexpr uint32_t kJoinSmem = (2 * kHeadDim * kJoinPitch + 2 * kHeadDim * kJoinCols) * sizeof(float);
+__device__ __forceinline__ void fetch_mat(float *dst, const float *src) {
+    for (int x = threadIdx.x; x < (int)kMat / 4; x += kJoinThreads)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         smem_u32(dst + (x >> 5) * kJoinPitch + (x & 31) * 4)),
+                     "l"(src + 4 * x)
+                     : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+__global__ void __launch_bounds__(kJoinThreads)
+    delta_join_kernel(const DeltaParams p, const Split split) {
+    extern __shared__ __align__(16) float join_smem[];
+    float *ms = join_smem, *ss = join_smem + 2 * kHeadDim * kJoinPitch;
+    pdl_wait();
+    pdl_trigger();
+    constexpr int kParts = kHeadDim / kJoinCols;
+    const int chain = (int)blockIdx.x / kParts, v0 = (int)blockIdx.x % kParts * kJoinCols;
+    const int b = chain / p.H;
+    const int n = p.cu_seqlens[b + 1] - p.cu_seqlens[b];
+    if (p.cu_seqlens[b] < 0 || n <= 0 || p.cu_seqlens[b + 1] > p.T || n > p.max_seqlen) return;
+    const int last = split_last(split, (n + C - 1) / C);
+    if (last < 2) return;
+    float *starts = split.starts + (size_t)chain * (split.segs - 1) * kMat + v0;
+    const float *trans = split.trans + (size_t)chain * (split.segs - 2) * kMat;
+    fetch_mat(ms, trans);
+    // rows k0 + 32 i and columns v .. v + 3 of a thread
+    const int v = threadIdx.x % (kJoinCols / 4) * 4, k0 = threadIdx.x / (kJoinCols / 4);
+    starts += v;
+    ss += v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<float4 *>(ss + (k0 + 32 * i) * kJoinCols) =
+            *reinterpret_cast<const float4 *>(starts + (k0 + 32 * i) * kHeadDim);
+    for (int g = 1; g < last; ++g) {
+        const float *m = ms + ((g - 1) & 1) * kHeadDim * kJoinPitch + k0 * kJoinPitch;
+        const float *s = ss + ((g - 1) & 1) * kHeadDim * kJoinCols;
+        float *next = starts + g * kMat;
+        float4 acc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = *reinterpret_cast<const float4 *>(next + (k0 + 32 * i) * kHeadDim);
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();  // M_g and S_g are there, and all are done with the other buffers
+        if (g + 1 < last) fetch_mat(ms + (g & 1) * kHeadDim * kJoinPitch, trans + g * kMat);
+#pragma unroll 4
+        for (int j = 0; j < kHeadDim; j += 4) {
+            float4 f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = *reinterpret_cast<const float4 *>(m + 32 * i * kJoinPitch + j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 x = *reinterpret_cast<const float4 *>(s + (j + e) * kJoinCols);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float y = e == 0 ? f[i].x : e == 1 ? f[i].y : e == 2 ? f[i].z : f[i].w;
+                    acc[i].x = fmaf(y, x.x, acc[i].x);
+                    acc[i].y = fmaf(y, x.y, acc[i].y);
+                    acc[i].z = fmaf(y, x.z, acc[i].z);
+                    acc[i].w = fmaf(y, x.w, acc[i].w);
+                }
+            }
+        }
+        float *keep = ss + (g & 1) * kHeadDim * kJoinCols;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            *reinterpret_cast<float4 *>(keep + (k0 + 32 * i) * kJoinCols) = acc[i];
+            *reinterpret_cast<float4 *>(next + (k0 + 32 * i) * kHeadDim) = acc[i];
+        }
+    }
+}
+
+// Matrices of a split: at most two per chain that runs in pass 2, (segs - 1) chains <= kSplitSMs.
+unsigned long long split_mats(long long chains, long long chunks) {
+    if (chunks < kSplitMinChunks || 2 * chains > kSplitSMs) return 0ull;
+    const long long most = chains * (2 * kMaxSegs - 3);
+    return (unsigned long long)(most < 2 * kSplitSMs ? most : 2 * kSplitSMs);
+}
+// The split whose longest way through both passes is shortest, in chunks: a pass 1 with ratio of the
+// short chains one after another beside a segment 0, then a segment of pass 2, and what the join and its
+// launches cost.
+Split plan_split(long long chains, long long chunks) {
+    Split s{1, 1, 0, nullptr, nullptr};
+    if (split_mats(chains, chunks) == 0) return s;
+    double best = kSplitGain * (double)chunks;
+    for (int ratio = 1; ratio <= 2; ++ratio)
+        for (int segs = 3; segs <= kMaxSegs && (segs - 1) * chains <= kSplitSMs; ++segs) {
+            if (2 * (segs - 2) * chains > ratio * (kSplitSMs - chains)) continue;
+            const Split t{segs, ratio, 1, nullptr, nullptr};
+            const double cost = (ratio + 1) * split_base(t, (int)chunks) + kSplitCost + kJoinCost * segs;
+            if (cost < best) {
+                best = cost;
+                s = t;
+            }
+        }
+    return s;
+}
+// Bytes of the slots, of the order, of a split's matrices.
+unsigned long long slots_bytes(long long B, long long T, long long H) {
+    return ((unsigned long long)chunk_slots(T, B) * (unsigned long long)H * SZ_SLOT);
+}
+unsigned long long order_bytes(long long B) {
+    return ((unsigned long long)B * sizeof(int32_t) + 15ull) / 16ull * 16ull;
+}
+
 }  // namespace
 
 unsigned long long delta_scratch_bytes(long long B, long long T, long long H) {
     if (T <= 0 || B <= 0) return 0ull;
-    return (unsigned long long)chunk_slots(T, B) * (unsigned long long)H * SZ_SLOT +
-           ((unsigned long long)B * sizeof(int32_t) + 15ull) / 16ull * 16ull;
+    return slots_bytes(B, T, H) + order_bytes(B) +
+           split_mats(B * H, (T + C - 1) / C) * (kMat * sizeof(float));
 }
 
 cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cudaStream_t stream) {
@@ -1181,10 +1377,16 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
         std::lock_guard<std::mutex> lock(mu);
         if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
         if (!configured[dev]) {
-            e = cudaFuncSetAttribute(delta_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            e = cudaFuncSetAttribute(delta_extend_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kSmemBytes);
+            if (e != cudaSuccess) return e;
+            e = cudaFuncSetAttribute(delta_extend_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      kSmemBytes);
             if (e != cudaSuccess) return e;
             e = cudaFuncSetAttribute(delta_t_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTSmemBytes);
+            if (e != cudaSuccess) return e;
+            e = cudaFuncSetAttribute(delta_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kJoinSmem);
             if (e != cudaSuccess) return e;
             configured[dev] = true;
         }
@@ -1194,7 +1396,7 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
     int32_t *order = nullptr;
     int rank_ctas = 0;
     if (t_ctas > 0 && p.B > 1 && p.B <= kMaxRanked && ctas > num_sms) {
-        order = reinterpret_cast<int32_t *>(w + t_ctas * SZ_SLOT);
+        order = reinterpret_cast<int32_t *>(w + slots_bytes(p.B, p.T, p.H));
         rank_ctas = (p.B + kTThreads - 1) / kTThreads;
     }
     if (t_ctas > 0) {
@@ -1202,8 +1404,21 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
                        stream, tq, tk, p, w, order, rank_ctas);
         if (e != cudaSuccess) return e;
     }
-    return launch_pdl(delta_extend_kernel, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, tq, tk,
-                      tv, p, (const uint8_t *)w, (const int32_t *)order);
+    Split split = plan_split(ctas, ((long long)(p.max_seqlen < p.T ? p.max_seqlen : p.T) + C - 1) / C);
+    if (split.pass == 0)
+        return launch_pdl(delta_extend_kernel<false>, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, tq,
+                          tk, tv, p, (const uint8_t *)w, (const int32_t *)order, split);
+    split.starts = reinterpret_cast<float *>(w + slots_bytes(p.B, p.T, p.H) + order_bytes(p.B));
+    split.trans = split.starts + (size_t)ctas * (split.segs - 1) * kMat;
+    e = launch_pdl(delta_extend_kernel<true>, dim3((unsigned)(ctas * (2 * split.segs - 3))), dim3(kThreads),
+                   kSmemBytes, stream, tq, tk, tv, p, (const uint8_t *)w, (const int32_t *)order, split);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(delta_join_kernel, dim3((unsigned)(ctas * (kHeadDim / kJoinCols))), dim3(kJoinThreads),
+                   kJoinSmem, stream, p, split);
+    if (e != cudaSuccess) return e;
+    split.pass = 2;
+    return launch_pdl(delta_extend_kernel<true>, dim3((unsigned)(ctas * (split.segs - 1))), dim3(kThreads),
+                      kSmemBytes, stream, tq, tk, tv, p, (const uint8_t *)w, (const int32_t *)order, split);
 }
 
 }  // namespace la

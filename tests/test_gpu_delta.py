@@ -18,7 +18,7 @@ def _to(*ts):
 
 
 def check_extend(lens, Hk, H, l2=True, gate="model", seed=0, prefix=None, gap=0, tail=0, spread=1.0,
-                 wide=False, max_seqlen=None):
+                 wide=False, max_seqlen=None, tol=TOL_EXTEND):
     """One extend call; `gap` rows before and `tail` rows behind the requests hold NaN inputs."""
     B, n = len(lens), sum(lens)
     T = gap + n + tail
@@ -46,8 +46,8 @@ def check_extend(lens, Hk, H, l2=True, gate="model", seed=0, prefix=None, gap=0,
         S0 = f64(pool0[int(idx[b])]) if prefix[b] else np.zeros((H, D, D))
         o, S, norms = run_states(q[r], k[r], v[r], g[r], beta[r], S0, Hk, H, l2)
         what = f"request {b} of {lens}"
-        check_out(f64(out[r]), o, q[r], np.broadcast_to(norms, (lens[b], H)), TOL_EXTEND, Hk, H, l2, what)
-        check_states(f64(pool[int(idx[b])]), S, TOL_EXTEND, what)
+        check_out(f64(out[r]), o, q[r], np.broadcast_to(norms, (lens[b], H)), tol, Hk, H, l2, what)
+        check_states(f64(pool[int(idx[b])]), S, tol, what)
         if lens[b] == 0:
             assert torch.equal(pool[int(idx[b])].cpu(), torch.from_numpy(S).float())
     free = [s for s in range(B + 3) if s not in idx.tolist()]
@@ -115,6 +115,40 @@ def test_extend_long():
 def test_extend_many_requests():
     r = np.random.default_rng(12)
     check_extend([int(x) for x in r.integers(0, 140, 90)], 1, 2, seed=12)
+
+
+@pytest.mark.parametrize("lens,Hk,H,l2,gate,max_seqlen", [
+    ([2500], 1, 2, True, "model", None),
+    ([2048], 1, 1, True, "none", None),
+    ([2085, 0, 5, 700, 2048, 64, 130], 1, 2, True, "model", None),
+    ([40, 2300], 1, 3, False, "none", 1 << 30),
+    ([2111], 5, 20, True, "reset", None),  # segment 0 twice as long as the others
+    ([900, 700], 1, 1, True, "model", 2100),  # taken as long, and every request is shorter
+])
+def test_extend_split(lens, Hk, H, l2, gate, max_seqlen):
+    """Few long requests: the chain in segments.  A state is M S + N, with M and N each within the
+    extend's tolerance."""
+    check_extend(lens, Hk, H, l2=l2, gate=gate, max_seqlen=max_seqlen, seed=21, gap=3, tail=600,
+                 prefix=[(b + 1) % 2 for b in range(len(lens))], tol=2 * TOL_EXTEND)
+
+
+def test_extend_split_nan_stays_behind():
+    """NaN inputs late in a split request leave the outputs before them as they were."""
+    n, H = 2600, 2
+    q, k, v, g, beta = _to(*inputs(n, 1, H, 22))
+    idx = torch.tensor([1], dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    mask = torch.ones(1, dtype=torch.uint8, device=DEV)
+    outs = []
+    for bad in (False, True):
+        if bad:
+            k[2000] = float("nan")
+        pool = torch.full((3, H, D, D), 0.01, device=DEV)
+        outs.append(la.delta_extend(q, k, v, g, beta, pool, idx, cu, mask, qk_l2norm=True))
+    la.poll_error()
+    assert torch.equal(outs[0][:1984], outs[1][:1984])  # 1984: the chunk of token 2000
+    assert outs[1][2000:].isnan().all()
+    assert pool[1].isnan().all() and (pool[[0, 2]] == 0.01).all()
 
 
 def test_extend_in_two_calls_equals_one():
