@@ -373,13 +373,18 @@ la_status la_commit_accepted(const float *inter_states, const int32_t *accept_id
  * state written to its slot (for zero-length requests too).  state_idx, cu_seqlens, prefix_mask,
  * max_seqlen, B, T as for la_extend; rows of out that belong to no request are left as they were.
  *   workspace        device scratch, 16-byte aligned, of at least la_delta_extend_workspace_size()
- *                    bytes (LA_ERR_INVALID otherwise; may be NULL when T = 0): about half of what q, k,
- *                    v and out take together.  Contents do not matter on entry and are garbage on exit;
- *                    calls that share one must not overlap on the GPU.
- * Two launches: one forms, for every chunk of 64 tokens at once, what depends on no state; the other runs
- * the chunks of each (request, head) in turn.  Numerics: bf16 products with fp32 accumulation; each
- * operand the kernels compute is a bf16 pair hi + lo (off by at most 2^-16); states are kept and updated
- * in fp32; out is rounded to bf16 once.  A NaN or an infinity in a request's inputs may reach all of that
+ *                    bytes (LA_ERR_INVALID otherwise; may be NULL when T = 0): 21,520 bytes per value
+ *                    head and 64 tokens (a third of what q, k, v and out take at Hk = H), and up to
+ *                    20 MB more where B * H <= 76.  Contents do not matter on entry and are garbage on
+ *                    exit; calls that share one must not overlap on the GPU.
+ * A first launch forms, for every chunk of 64 tokens at once, what depends on no state; a second runs the
+ * chunks of each (request, head) in turn.  Where B * H <= 76 and max_seqlen (T, if that is less) is large
+ * enough (from about 1,300 tokens at B * H = 8, from about 2,600 at 76) the chunks run as segments side by
+ * side, in four launches, with the same results up to rounding: so pass max_seqlen no larger than it is.
+ * A call in which cu_seqlens decreases somewhere skips the requests concerned and reports them, but the
+ * results of its other requests are then unspecified too.  Numerics: bf16 products with fp32 accumulation; each
+ * operand the kernels compute is a bf16 pair hi + lo (off by at most 2^-16); states are kept, updated and
+ * joined in fp32; out is rounded to bf16 once.  A NaN or an infinity in a request's inputs may reach all of that
  * request's outputs and its state, and nothing of any other request.
  */
 la_status la_delta_extend(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, int64_t q_row_stride,

@@ -456,7 +456,8 @@ __global__ void __launch_bounds__(kTThreads, 5)
         glo[lane + 32] = x1.lo;
     }
     __syncthreads();
-    if (!mbar_wait(&kq_full, 0, p.wait_limit_ns)) {
+    // the CTA goes on only if every thread's wait succeeded
+    if (!__syncthreads_and(mbar_wait(&kq_full, 0, p.wait_limit_ns))) {
         // the copies are waited for once more before the CTA's shared memory goes away
         if (threadIdx.x == 0) atomicOr(p.err, ERR_BIT_TIMEOUT);
         mbar_wait(&kq_full, 0, kDrainLimitNs);
