@@ -38,10 +38,15 @@
 //
 // Roles of the chain kernel (384 threads, one CTA per SM):
 //   warps 0-7   E: the state (32 v rows x 64 k columns a warp) and the passes R, U, O and S;
-//   warp 8      TMA producer; warp 9 tensor-memory owner and MMA issuer;
+//   warp 8      finds the items (below) and issues their loads; warp 9 tensor-memory owner and MMA issuer;
 //   warp 10     zeroes the K rows past the end of the request's last chunk (they hold the next
 //               request's keys, and 0 x NaN is NaN).
-// Per chunk the chain is X -> R -> T' R -> U -> U^T K -> S; the output pass runs under U^T K.
+// Per chunk the chain is X -> R -> T' R -> U -> U^T K -> S; the output pass runs under U^T K.  A chunk takes
+// about 2.4 us: 36 MMAs of 45-65 cycles are half of it, the passes between them (wait, tensor memory to
+// registers, pair split, back, barrier) the other half; no two of them overlap along the chain, and a second
+// chain on the SM has room neither in tensor memory (512 columns) nor in shared memory (171 KB).
+// More items than SMs: a CTA per SM takes several in turn (387 us of chain on 256 requests of 32-512 tokens x
+// 16 heads, where a CTA per item took 437), and warp 8 runs ahead of the item that is worked on.
 //
 // Every wait ends: mbarrier waits have a deadline (the named barriers below end with them); one that runs out
 // sets the error word and an abort flag that ends every role, then the CTA waits for its copies and MMAs,
@@ -63,7 +68,8 @@ using namespace sm100;
 constexpr int C = 64;  // tokens of a chunk
 constexpr int kEWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kFixWarp = 10;
 constexpr int kThreads = 384;
-// registers per thread of the warp groups: 2 x 184 (E) + 136 = 3 x 168, the launch's share
+// Registers per thread of the warp groups: 2 x 184 (E) + 136 = 3 x 168, the launch's share.  (E at 200: the
+// same times; at 216: 678 us in place of 663 on the batch above.)
 constexpr int kRegsE = 184, kRegsRest = 136;
 static_assert(2 * kRegsE + kRegsRest <= 3 * 168, "register split");
 constexpr int kTThreads = 128;
@@ -100,22 +106,34 @@ constexpr uint32_t OFF_T = OFF_V + 2 * 16384;              // 2 x a slot
 constexpr uint32_t SZ_T = (SZ_SLOT + 255) / 256 * 256;     // whole swizzle atoms
 constexpr uint32_t OFF_COEF = OFF_T + 2 * SZ_PART;         // a slot's coefficients
 constexpr uint32_t OFF_BAR = OFF_T + 2 * SZ_T;
-constexpr uint32_t SZ_BAR = 256;
+constexpr uint32_t SZ_BAR = 512;
 constexpr uint32_t kSmemBytes = OFF_BAR + SZ_BAR + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
+// What a CTA's roles need of the item (a chain, or a segment of one) they are on.
+struct Item {
+    const float *from;  // the start state; null: zero, or the identity for a transition
+    float *to;          // where the end state goes; null: not kept
+    int t0, n, h;       // first token, tokens, value head
+};
+constexpr int kItems = 4;
+
 struct Bars {
-    uint64_t kq_full[kStages], kq_empty[kStages];
+    uint64_t kq_full[kStages];
+    uint64_t kq_empty[kStages];  // the chunk's products done; warp 10 past it (2)
+    uint64_t kq_ready[kStages];  // warp 10: K rows past the request's end zeroed
     uint64_t v_full[2], t_full[2];
     uint64_t y_done[2];    // the product with T's tile done: tile and V buffer free
     uint64_t c_free[2];    // E warps: the chunk's coefficients read (8)
-    uint64_t kq_last;      // producer: the last chunk's loads are issued
-    uint64_t kq_fixed;     // warp 10: rows past the end of the last chunk zeroed
+    uint64_t item_full[kItems];
+    uint64_t item_empty[kItems];  // read by the E warps, the MMA warp and warp 10 (10)
     uint64_t x_full, y_full, d_full;
     uint64_t o_free;       // E warps (8): X^Q and O' read
     uint64_t drain;
+    Item items[kItems];
     uint32_t tmem_base;
     int abort_flag;
+    int go[2];             // the MMA warp's word to the E warps: on to the next item
 };
 static_assert(sizeof(Bars) <= SZ_BAR, "barrier block");
 
@@ -133,8 +151,9 @@ constexpr uint32_t kTSmemBytes = TK_TOK + 5 * 256 + 1024;
 // (kBarS + y), y and 2 + y of R and U (kBarR + y, kBarU + y) are in place.  A test of an
 // mbarrier takes about 113 cycles when eight warps poll, a named barrier about 30.  They have no deadline of
 // their own: the E warps arrive at every one of every chunk, whether their own (bounded) waits succeed or
-// not, so the MMA warp's waits end when theirs do.
-constexpr int kBarS = 1, kBarR = 5, kBarU = 7;
+// not, so the MMA warp's waits end when theirs do.  At kBarItem all of them meet before an item: the MMA warp,
+// which waits (with a deadline) for the item, says there whether it is still to be run.
+constexpr int kBarS = 1, kBarR = 5, kBarU = 7, kBarItem = 9;
 constexpr int kBarThreads = (kEWarps + 1) * 32;
 __device__ __forceinline__ void bar_arrive(int id) {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kBarThreads) : "memory");
@@ -144,6 +163,7 @@ __device__ __forceinline__ void bar_wait(int id) {
 }
 
 constexpr uint64_t kDrainLimitNs = 2000000000ull;
+constexpr uint64_t kTryNs = 10000;
 
 struct Ctx {
     uint64_t limit;
@@ -151,12 +171,28 @@ struct Ctx {
     unsigned int *err;
 };
 
+// A try may suspend the thread for some 4 us; under a limit below that warps 8 and 10, whose waits are the
+// longest, test without being suspended (TEST).
+template <bool TEST>
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity, const Ctx &cx) {
+    if (!TEST || cx.limit >= kTryNs) return mbar_try_wait(bar, parity);
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+template <bool TEST = false>
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const Ctx &cx) {
     const uint32_t a = smem_u32(bar);
-    if (mbar_try_wait(a, parity)) return true;
+    if (try_wait<TEST>(a, parity, cx)) return true;
     const uint64_t t0 = globaltimer_ns();
     while (true) {
-        if (mbar_try_wait(a, parity)) return true;
+        if (try_wait<TEST>(a, parity, cx)) return true;
         if (*cx.abort_flag) return false;
         if (globaltimer_ns() - t0 > cx.limit) {
             *cx.abort_flag = 1;
@@ -166,8 +202,9 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const C
     }
 }
 // All lanes wait; the warp goes on only if every lane's wait succeeded.
+template <bool TEST = false>
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const Ctx &cx) {
-    return __all_sync(0xffffffffu, wait_bar(bar, parity, cx));
+    return __all_sync(0xffffffffu, wait_bar<TEST>(bar, parity, cx));
 }
 __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
     __syncwarp();
@@ -725,13 +762,16 @@ __host__ __device__ inline int split_last(const Split &s, int nchunks) {
     return rest > 0 ? 1 + (rest - 1) / base : 0;
 }
 
-// Where a CTA's chain starts and ends, and whether it writes outputs.
-struct Ends {
-    const float *from;  // null: zero, or the identity for a transition
-    float *to;          // null: not kept
-    bool transition;    // V counts as zero
-    bool emit;
+// The job of a CTA (one item each): segment, whether it is a transition, whether outputs are written.
+struct Job {
+    int seg;
+    bool transition, emit;
 };
+__device__ __forceinline__ Job split_job(const DeltaParams &p, const Split &s) {
+    const int job = (int)blockIdx.x / (p.B * p.H);
+    if (s.pass == 2) return {1 + job, false, true};
+    return {(job + 1) >> 1, (job & 1) != 0, job == 0};
+}
 
 // ------------------------------------------------------------------------------------------------
 // E warps: lanes are value columns v = 32 q + lane; half hf of the chunk's tokens and of the k columns.
@@ -761,193 +801,207 @@ __device__ __forceinline__ void load_pairs(const float *src, uint64_t (&x)[16]) 
 
 template <bool SPLIT>
 __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx &cx, uint32_t tbase, int q,
-                       int hf, int lane, size_t t0, int n, int h, const Ends &ends, int nchunks) {
+                       int hf, int lane, int items, const Split &split) {
     const int v = 32 * q + lane;
     const int tok0 = 32 * hf;  // tokens tok0 .. + 31 of the chunk
     const uint32_t lanes = tbase + ((uint32_t)(32 * q) << 16);
     const uint32_t ts = lanes + TM_S + 64u * hf;
     const uint32_t tx = lanes + TM_X + 32u * hf, ty = lanes + TM_Y + 64u * hf, td = lanes + TM_D + 64u * hf;
     const int at = 64 * hf * kHeadDim + v;
-    const bool transition = SPLIT && ends.transition, emit = !SPLIT || ends.emit;
-
-    uint64_t S[32];  // S[64 hf + 2 x, 64 hf + 2 x + 1][v]
-    if (ends.from) {
-        const float *gs = ends.from + at;
-#pragma unroll
-        for (int x = 0; x < 32; ++x) S[x] = f2(gs[2 * x * kHeadDim], gs[(2 * x + 1) * kHeadDim]);
-    } else {
-#pragma unroll
-        for (int x = 0; x < 32; ++x) {
-            const int d = transition ? v - 64 * hf - 2 * x : -1;
-            S[x] = f2(d == 0 ? 1.f : 0.f, d == 1 ? 1.f : 0.f);
-        }
-    }
-    if (nchunks > 0) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) put_step(ts + 16u * x, S + 8 * x, kBarS + x);
-    }
-
     bool ok = true;
-    // a wait gave up: the named barriers that are left of this chunk, from R's, U's or S's on (waited for,
-    // so that no warp runs a chunk ahead of the others)
-    auto give_up = [&](int from, int c) {
-        ok = false;
-        for (int x = from; x < kBarU + 2; ++x) bar_wait(x);
-        if (c + 1 < nchunks)
-            for (int x = kBarS; x < kBarR; ++x) bar_wait(x);
-    };
-    for (int c = 0; c < nchunks; ++c) {
-        if (!ok) {
-            give_up(kBarR, c);
-            continue;
-        }
-        const uint32_t par = c & 1, ph = (c >> 1) & 1;
-        const int r = n - c * C;  // tokens from this chunk on
-        const float *cf = reinterpret_cast<const float *>(sm + OFF_COEF + par * SZ_T) + tok0;
-        // ---- R = beta V - (beta gamma rk) X^K; what needs no X is formed while its product runs
-        if (!warp_wait(&bars->t_full[par], ph, cx)) {
-            give_up(kBarR, c);
-            continue;
-        }
-        if (!warp_wait(&bars->v_full[par], ph, cx)) {
-            give_up(kBarR, c);
-            continue;
-        }
-        uint64_t R[16], f[16];
-        {
-            const uint8_t *vp = sm + OFF_V + par * 16384 + tok0 * 256 + v * 2;
-            load_pairs(cf, R);
-            load_pairs(cf + 64, f);
+    int cc = 0;  // chunks of the items before
+    for (int k = 0; k < items; ++k) {
+        bar_wait(kBarItem);
+        if (!*(volatile int *)&bars->go[k & 1]) break;
+        const Item item = bars->items[k % kItems];
+        warp_arrive(&bars->item_empty[k % kItems], lane);
+        const int n = item.n, h = item.h, nchunks = (n + C - 1) / C;
+        const size_t t0 = (size_t)item.t0;
+        const bool transition = SPLIT && split_job(p, split).transition;
+        const bool emit = !SPLIT || split_job(p, split).emit;
+        // a transition's V as zero (a choice between values makes its loads wait behind a branch: 975 us in
+        // place of 840 for 32,768 tokens)
+        const uint32_t vmask = transition ? 0u : 0xffffffffu;
+
+        uint64_t S[32];  // S[64 hf + 2 x, 64 hf + 2 x + 1][v]
+        if (item.from) {
+            const float *gs = item.from + at;
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-                const uint32_t v0 = *reinterpret_cast<const uint16_t *>(vp + (2 * x) * 256);
-                const uint32_t v1 = *reinterpret_cast<const uint16_t *>(vp + (2 * x + 1) * 256);
-                R[x] = transition ? 0ull : mul2(R[x], f2u(v0 << 16, v1 << 16));
+            for (int x = 0; x < 32; ++x) S[x] = f2(gs[2 * x * kHeadDim], gs[(2 * x + 1) * kHeadDim]);
+        } else {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+                const int d = transition ? v - 64 * hf - 2 * x : -1;
+                S[x] = f2(d == 0 ? 1.f : 0.f, d == 1 ? 1.f : 0.f);
             }
         }
-        if (!warp_wait(&bars->x_full, par, cx)) {
-            give_up(kBarR, c);
-            continue;
+        if (nchunks > 0) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) put_step(ts + 16u * x, S + 8 * x, kBarS + x);
         }
-        tc_fence_after();
-        {
-            uint32_t w[2][16];
-            tmem_ld16(tx, w[0]);
+
+        // a wait gave up: the named barriers that are left of this chunk, from R's, U's or S's on (waited for,
+        // so that no warp runs a chunk ahead of the others)
+        auto give_up = [&](int from, int c) {
+            ok = false;
+            for (int x = from; x < kBarU + 2; ++x) bar_wait(x);
+            if (c + 1 < nchunks)
+                for (int x = kBarS; x < kBarR; ++x) bar_wait(x);
+        };
+        for (int c = 0; c < nchunks; ++c) {
+            if (!ok) {
+                give_up(kBarR, c);
+                continue;
+            }
+            const uint32_t par = (cc + c) & 1, ph = ((cc + c) >> 1) & 1;
+            const int r = n - c * C;  // tokens from this chunk on
+            const float *cf = reinterpret_cast<const float *>(sm + OFF_COEF + par * SZ_T) + tok0;
+            // ---- R = beta V - (beta gamma rk) X^K; what needs no X is formed while its product runs
+            if (!warp_wait(&bars->t_full[par], ph, cx)) {
+                give_up(kBarR, c);
+                continue;
+            }
+            if (!warp_wait(&bars->v_full[par], ph, cx)) {
+                give_up(kBarR, c);
+                continue;
+            }
+            uint64_t R[16], f[16];
+            {
+                const uint8_t *vp = sm + OFF_V + par * 16384 + tok0 * 256 + v * 2;
+                load_pairs(cf, R);
+                load_pairs(cf + 64, f);
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                tmem_ld_wait_regs(w[y]);
-                if (y == 0) tmem_ld16(tx + 16u, w[1]);
+                for (int x = 0; x < 16; ++x) {
+                    const uint32_t v0 = *reinterpret_cast<const uint16_t *>(vp + (2 * x) * 256);
+                    const uint32_t v1 = *reinterpret_cast<const uint16_t *>(vp + (2 * x + 1) * 256);
+                    R[x] = mul2(R[x], f2u((v0 << 16) & vmask, (v1 << 16) & vmask));
+                }
+            }
+            if (!warp_wait(&bars->x_full, par, cx)) {
+                give_up(kBarR, c);
+                continue;
+            }
+            tc_fence_after();
+            {
+                uint32_t w[2][16];
+                tmem_ld16(tx, w[0]);
 #pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    R[8 * y + x] = fma2(f[8 * y + x], f2u(w[y][2 * x], w[y][2 * x + 1]), R[8 * y + x]);
-                if (r < C) {  // rows past the end hold other requests' values
+                for (int y = 0; y < 2; ++y) {
+                    tmem_ld_wait_regs(w[y]);
+                    if (y == 0) tmem_ld16(tx + 16u, w[1]);
 #pragma unroll
-                    for (int x = 8 * y; x < 8 * y + 8; ++x) {
-                        if (tok0 + 2 * x >= r) R[x] = 0ull;
-                        else if (tok0 + 2 * x + 1 >= r) R[x] &= 0xffffffffull;
+                    for (int x = 0; x < 8; ++x)
+                        R[8 * y + x] = fma2(f[8 * y + x], f2u(w[y][2 * x], w[y][2 * x + 1]), R[8 * y + x]);
+                    if (r < C) {  // rows past the end hold other requests' values
+#pragma unroll
+                        for (int x = 8 * y; x < 8 * y + 8; ++x) {
+                            if (tok0 + 2 * x >= r) R[x] = 0ull;
+                            else if (tok0 + 2 * x + 1 >= r) R[x] &= 0xffffffffull;
+                        }
+                    }
+                    put_step(tx + 16u * y, R + 8 * y, kBarR + y);
+                }
+            }
+
+            // ---- U = R + T' R, scaled for the state update
+            load_pairs(cf + 128, f);
+            if (!warp_wait(&bars->y_full, par, cx)) {
+                give_up(kBarU, c);
+                continue;
+            }
+            tc_fence_after();
+            {
+                uint32_t w[2][16];
+                tmem_ld16(ty, w[0]);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    tmem_ld_wait_regs(w[y]);
+                    if (y == 0) tmem_ld16(ty + 32u, w[1]);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        R[8 * y + x] =
+                            mul2(f[8 * y + x], add2(R[8 * y + x], f2u(w[y][2 * x], w[y][2 * x + 1])));
+                    put_step(ty + 32u * y, R + 8 * y, kBarU + y);
+                }
+            }
+
+            // ---- o = (scale gamma rq) X^Q + P T R; neighbouring lanes exchange halves, so that each
+            // stores two value columns of one token
+            if (!emit) {
+                warp_arrive(&bars->o_free, lane);
+            } else {
+                const size_t tok = t0 + (size_t)c * C + tok0 + (lane & 1);
+                __nv_bfloat16 *op = p.out + (tok * p.H + h) * kHeadDim + (v & ~1);
+                const size_t two = (size_t)p.H * kHeadDim * 2;
+                const int left = r - tok0 - (lane & 1);
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    uint32_t w[16], y[16];
+                    tmem_ld16(tx + 64u + 16u * z, w);
+                    tmem_ld16(ty + 16u + 32u * z, y);
+                    tmem_ld_wait_regs(w);
+                    tmem_ld_wait_regs(y);
+                    if (z == 1) {
+                        tc_fence_before();
+                        warp_arrive(&bars->o_free, lane);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float4 o = *reinterpret_cast<const float4 *>(cf + 192 + 16 * z + 4 * x);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int at = 4 * x + 2 * e;
+                            float za, zb;
+                            asm("mov.b64 {%0, %1}, %2;"
+                                : "=f"(za), "=f"(zb)
+                                : "l"(fma2(e ? f2(o.z, o.w) : f2(o.x, o.y), f2u(w[at], w[at + 1]),
+                                           f2u(y[at], y[at + 1]))));
+                            const uint32_t mine = pack_bf16x2(za, zb);  // tokens at, at + 1
+                            const uint32_t theirs = __shfl_xor_sync(0xffffffffu, mine, 1);
+                            // even lanes: the first token of (v, v + 1); odd lanes: the second of (v - 1, v)
+                            const uint32_t word = (lane & 1) ? __byte_perm(theirs, mine, 0x7632)
+                                                             : __byte_perm(mine, theirs, 0x5410);
+                            if (16 * z + at < left)
+                                *reinterpret_cast<uint32_t *>(op + (8 * z + (at >> 1)) * two) = word;
+                        }
                     }
                 }
-                put_step(tx + 16u * y, R + 8 * y, kBarR + y);
             }
-        }
 
-        // ---- U = R + T' R, scaled for the state update
-        load_pairs(cf + 128, f);
-        if (!warp_wait(&bars->y_full, par, cx)) {
-            give_up(kBarU, c);
-            continue;
-        }
-        tc_fence_after();
-        {
-            uint32_t w[2][16];
-            tmem_ld16(ty, w[0]);
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                tmem_ld_wait_regs(w[y]);
-                if (y == 0) tmem_ld16(ty + 32u, w[1]);
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    R[8 * y + x] =
-                        mul2(f[8 * y + x], add2(R[8 * y + x], f2u(w[y][2 * x], w[y][2 * x + 1])));
-                put_step(ty + 32u * y, R + 8 * y, kBarU + y);
+            // ---- S = gamma_C S + K^T U
+            const float ge = cf[256 - tok0];
+            warp_arrive(&bars->c_free[par], lane);
+            if (!warp_wait(&bars->d_full, par, cx)) {
+                give_up(kBarU + 2, c);
+                continue;
             }
-        }
-
-        // ---- o = (scale gamma rq) X^Q + P T R; neighbouring lanes exchange halves, so that each
-        // stores two value columns of one token
-        if (!emit) {
-            warp_arrive(&bars->o_free, lane);
-        } else {
-            const size_t tok = t0 + (size_t)c * C + tok0 + (lane & 1);
-            __nv_bfloat16 *op = p.out + (tok * p.H + h) * kHeadDim + (v & ~1);
-            const size_t two = (size_t)p.H * kHeadDim * 2;
-            const int left = r - tok0 - (lane & 1);
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-                uint32_t w[16], y[16];
-                tmem_ld16(tx + 64u + 16u * z, w);
-                tmem_ld16(ty + 16u + 32u * z, y);
-                tmem_ld_wait_regs(w);
-                tmem_ld_wait_regs(y);
-                if (z == 1) {
-                    tc_fence_before();
-                    warp_arrive(&bars->o_free, lane);
-                }
+            tc_fence_after();
+            {
+                const uint64_t ge2 = f2(ge, ge);
+                uint32_t w[2][16];
+                tmem_ld16(td, w[0]);
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const float4 o = *reinterpret_cast<const float4 *>(cf + 192 + 16 * z + 4 * x);
+                    uint32_t(&d)[16] = w[x & 1];
+                    tmem_ld_wait_regs(d);
+                    if (x < 3) tmem_ld16(td + 16u * (x + 1), w[(x + 1) & 1]);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int at = 4 * x + 2 * e;
-                        float za, zb;
-                        asm("mov.b64 {%0, %1}, %2;"
-                            : "=f"(za), "=f"(zb)
-                            : "l"(fma2(e ? f2(o.z, o.w) : f2(o.x, o.y), f2u(w[at], w[at + 1]),
-                                       f2u(y[at], y[at + 1]))));
-                        const uint32_t mine = pack_bf16x2(za, zb);  // tokens at, at + 1
-                        const uint32_t theirs = __shfl_xor_sync(0xffffffffu, mine, 1);
-                        // even lanes: the first token of (v, v + 1); odd lanes: the second of (v - 1, v)
-                        const uint32_t word = (lane & 1) ? __byte_perm(theirs, mine, 0x7632)
-                                                         : __byte_perm(mine, theirs, 0x5410);
-                        if (16 * z + at < left)
-                            *reinterpret_cast<uint32_t *>(op + (8 * z + (at >> 1)) * two) = word;
-                    }
+                    for (int e = 0; e < 8; ++e)
+                        S[8 * x + e] = fma2(ge2, S[8 * x + e], f2u(d[2 * e], d[2 * e + 1]));
+                    if (c + 1 < nchunks) put_step(ts + 16u * x, S + 8 * x, kBarS + x);
                 }
             }
         }
-
-        // ---- S = gamma_C S + K^T U
-        const float ge = cf[256 - tok0];
-        warp_arrive(&bars->c_free[par], lane);
-        if (!warp_wait(&bars->d_full, par, cx)) {
-            give_up(kBarU + 2, c);
-            continue;
-        }
-        tc_fence_after();
-        {
-            const uint64_t ge2 = f2(ge, ge);
-            uint32_t w[2][16];
-            tmem_ld16(td, w[0]);
+        cc += nchunks;
+        if (ok && item.to) {
+            float *gs = item.to + at;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                uint32_t(&d)[16] = w[x & 1];
-                tmem_ld_wait_regs(d);
-                if (x < 3) tmem_ld16(td + 16u * (x + 1), w[(x + 1) & 1]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    S[8 * x + e] = fma2(ge2, S[8 * x + e], f2u(d[2 * e], d[2 * e + 1]));
-                if (c + 1 < nchunks) put_step(ts + 16u * x, S + 8 * x, kBarS + x);
+            for (int x = 0; x < 32; ++x) {
+                float a, b;
+                asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(S[x]));
+                gs[2 * x * kHeadDim] = a;
+                gs[(2 * x + 1) * kHeadDim] = b;
             }
-        }
-    }
-    if (ok && ends.to) {
-        float *gs = ends.to + at;
-#pragma unroll
-        for (int x = 0; x < 32; ++x) {
-            float a, b;
-            asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(S[x]));
-            gs[2 * x * kHeadDim] = a;
-            gs[(2 * x + 1) * kHeadDim] = b;
         }
     }
 }
@@ -975,8 +1029,7 @@ __device__ __forceinline__ void commit_if(uint32_t lead, uint64_t *bar) {
         "r"(lead)
         : "memory");
 }
-__device__ void mma_role(Bars *bars, uint32_t tbase, uint32_t s_base, int nchunks, bool ragged, int lane,
-                         Ctx cx) {
+__device__ void mma_role(Bars *bars, uint32_t tbase, uint32_t s_base, int items, int lane, Ctx cx) {
     const uint32_t id = idesc_bf16_f32(128, 128, false, false);
     const uint32_t idD = idesc_bf16_f32(128, 128, false, true);
     // B operands of one swizzle have the same high descriptor word (8-row groups 1024 bytes apart, 128-byte
@@ -988,71 +1041,82 @@ __device__ void mma_role(Bars *bars, uint32_t tbase, uint32_t s_base, int nchunk
         mma_ts(lead, tbase + d, tbase + a, hw | b, idesc, acc);
     };
     bool ok = true;
-    int st = 0;
+    int st = 0, cc = 0;  // cc: chunks of the items before
     uint32_t stp = 0;
-    for (int c = 0; c < nchunks; ++c) {
-        const uint32_t par = c & 1, ph = (c >> 1) & 1;
-        // once a wait gave up nothing more is issued, but every named barrier is waited for
-        ok = ok && warp_wait(&bars->kq_full[st], stp, cx) &&
-             (c == 0 || warp_wait(&bars->o_free, (c - 1) & 1, cx));
-        if (!ok) lead = 0;
-        const uint32_t kq = (s_base + OFF_KQ + st * SZ_KQ) >> 4;
-        // a k-step starts as soon as the E warps have put it in place
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            bar_wait(kBarS + y);
-            tc_fence_after();
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int kk = y + 4 * (x >> 1);  // hi, lo of k-steps y and 4 + y
-                mma(TM_X, TM_S + 16u * kk + 8u * (x & 1),
-                    kq + ((kk >> 2) * 1024 + (kk & 3) * 2) + (1u << 16), id, y + x > 0, high);
-            }
-            if (y == 3) commit_if(lead, &bars->x_full);
-        }
-        ok = ok && warp_wait(&bars->t_full[par], ph, cx);
-        if (!ok) lead = 0;
-        const uint32_t tt = (s_base + OFF_T + par * SZ_T) >> 4;
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            bar_wait(kBarR + y);
-            tc_fence_after();
-#pragma unroll
-            for (int x = 0; x < 6; ++x) {  // R_hi T_hi, R_lo T_hi, R_hi T_lo of k-steps y and 2 + y,
-                                           // for the rows that are not zero
-                const int kk = y + 2 * (x / 3), term = x % 3;
-                mma(TM_Y + 32u * kk, TM_X + 16u * kk + (term == 1 ? 8u : 0u),
-                    tt + (term == 2 ? SZ_PART >> 4 : 0u) + (part_ofs(kk) >> 4) + (1u << 16),
-                    idesc_bf16_f32(128, 128 - 32 * kk, false, false), y + x > 0, high32);
-            }
-            if (y == 1) {
-                commit_if(lead, &bars->y_full);
-                commit_if(lead, &bars->y_done[par]);
-            }
-        }
-        if (ragged && c == nchunks - 1) {
-            ok = ok && warp_wait(&bars->kq_fixed, 0, cx);
+    for (int k = 0; k < items; ++k) {
+        ok = ok && warp_wait(&bars->item_full[k % kItems], (k / kItems) & 1, cx);
+        const bool go = __shfl_sync(0xffffffffu, (int)(ok && !*cx.abort_flag), 0);
+        if (lane == 0) bars->go[k & 1] = go;
+        __syncwarp();
+        bar_wait(kBarItem);
+        if (!go) break;
+        const int n = bars->items[k % kItems].n, nchunks = (n + C - 1) / C;
+        warp_arrive(&bars->item_empty[k % kItems], lane);
+        for (int c = 0; c < nchunks; ++c) {
+            const uint32_t par = (cc + c) & 1, ph = ((cc + c) >> 1) & 1;
+            // once a wait gave up nothing more is issued, but every named barrier is waited for
+            ok = ok && warp_wait(&bars->kq_full[st], stp, cx) &&
+                 (cc + c == 0 || warp_wait(&bars->o_free, (cc + c - 1) & 1, cx));
             if (!ok) lead = 0;
-        }
+            const uint32_t kq = (s_base + OFF_KQ + st * SZ_KQ) >> 4;
+            // a k-step starts as soon as the E warps have put it in place
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            bar_wait(kBarU + y);
-            tc_fence_after();
+            for (int y = 0; y < 4; ++y) {
+                bar_wait(kBarS + y);
+                tc_fence_after();
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int kk = y + 2 * (x >> 1);
-                mma(TM_D, TM_Y + 32u * kk + 8u * (x & 1), kq + kk * 128 + ((16384u >> 4) << 16), idD,
-                    y + x > 0, high);
+                for (int x = 0; x < 4; ++x) {
+                    const int kk = y + 4 * (x >> 1);  // hi, lo of k-steps y and 4 + y
+                    mma(TM_X, TM_S + 16u * kk + 8u * (x & 1),
+                        kq + ((kk >> 2) * 1024 + (kk & 3) * 2) + (1u << 16), id, y + x > 0, high);
+                }
+                if (y == 3) commit_if(lead, &bars->x_full);
             }
-            if (y == 1) {
-                commit_if(lead, &bars->d_full);
-                commit_if(lead, &bars->kq_empty[st]);
+            ok = ok && warp_wait(&bars->t_full[par], ph, cx);
+            if (!ok) lead = 0;
+            const uint32_t tt = (s_base + OFF_T + par * SZ_T) >> 4;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                bar_wait(kBarR + y);
+                tc_fence_after();
+#pragma unroll
+                for (int x = 0; x < 6; ++x) {  // R_hi T_hi, R_lo T_hi, R_hi T_lo of k-steps y and 2 + y,
+                                               // for the rows that are not zero
+                    const int kk = y + 2 * (x / 3), term = x % 3;
+                    mma(TM_Y + 32u * kk, TM_X + 16u * kk + (term == 1 ? 8u : 0u),
+                        tt + (term == 2 ? SZ_PART >> 4 : 0u) + (part_ofs(kk) >> 4) + (1u << 16),
+                        idesc_bf16_f32(128, 128 - 32 * kk, false, false), y + x > 0, high32);
+                }
+                if (y == 1) {
+                    commit_if(lead, &bars->y_full);
+                    commit_if(lead, &bars->y_done[par]);
+                }
+            }
+            if (n - c * C < C) {
+                ok = ok && warp_wait(&bars->kq_ready[st], stp, cx);
+                if (!ok) lead = 0;
+            }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                bar_wait(kBarU + y);
+                tc_fence_after();
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int kk = y + 2 * (x >> 1);
+                    mma(TM_D, TM_Y + 32u * kk + 8u * (x & 1), kq + kk * 128 + ((16384u >> 4) << 16), idD,
+                        y + x > 0, high);
+                }
+                if (y == 1) {
+                    commit_if(lead, &bars->d_full);
+                    commit_if(lead, &bars->kq_empty[st]);
+                }
+            }
+            if (++st == kStages) {
+                st = 0;
+                stp ^= 1;
             }
         }
-        if (++st == kStages) {
-            st = 0;
-            stp ^= 1;
-        }
+        cc += nchunks;
     }
     // every issued MMA must finish before tensor memory is freed
     if (lane == 0) {
@@ -1064,31 +1128,102 @@ __device__ void mma_role(Bars *bars, uint32_t tbase, uint32_t s_base, int nchunk
     }
 }
 
+// Item k of a CTA: rows of gridDim.x items, taken from the left and the right in turn (they come longest
+// first, so that the CTAs' sums stay close).
+__device__ __forceinline__ int item_at(int k) {
+    return k * (int)gridDim.x + (int)((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+__device__ __forceinline__ int item_count(int all) {
+    const int rows = all / (int)gridDim.x;
+    return rows + (item_at(rows) < all);
+}
+
+template <bool SPLIT>
+__device__ __forceinline__ Item find_item(const DeltaParams &p, const int32_t *order, const Split &split,
+                                          int which, int &slot0) {
+    Item item{nullptr, nullptr, 0, 0, 0};
+    const int chains = p.B * p.H;
+    const int chain = SPLIT ? which % chains : which;
+    const int h = chain % p.H, want = chain / p.H;
+    // Longest request first where there is more than one row of items.
+    const int b = order ? order[want] : want;
+    item.h = h;
+    const int slot = p.state_idx[b];
+    const int t_req0 = p.cu_seqlens[b], t_req1 = p.cu_seqlens[b + 1];
+    const bool prefix = p.prefix_mask[b];
+    if (slot < 0 || slot >= p.num_slots) {
+        atomicOr(p.err, ERR_BIT_SLOT_RANGE);
+        return item;
+    }
+    if (t_req0 < 0 || t_req1 < t_req0 || t_req1 > p.T || t_req1 - t_req0 > p.max_seqlen) {
+        atomicOr(p.err, ERR_BIT_SEQLENS);
+        return item;
+    }
+    int n = t_req1 - t_req0, c0 = 0;  // tokens, first chunk
+    float *state = p.pool + ((size_t)slot * p.H + h) * kMat;
+    if (prefix) item.from = state;
+    if (!prefix || n > 0) item.to = state;
+    if (SPLIT) {
+        const int nchunks = (n + C - 1) / C;
+        const int base = split_base(split, nchunks), last = split_last(split, nchunks);
+        float *starts = split.starts + (size_t)chain * (split.segs - 1) * kMat;
+        const Job job = split_job(p, split);
+        const int seg = job.seg;
+        // no such segment, or one whose end state nothing needs
+        if (seg > last || (seg == last && !job.emit)) return Item{nullptr, nullptr, 0, 0, 0};
+        if (seg > 0) item.from = split.pass == 2 ? starts + (seg - 1) * kMat : nullptr;
+        if (job.transition)
+            item.to = split.trans + ((size_t)chain * (split.segs - 2) + seg - 1) * kMat;
+        else if (seg < last)
+            item.to = split.pass == 2 ? nullptr : starts + seg * kMat;
+        c0 = seg ? (split.ratio + seg - 1) * base : 0;
+        n = seg < last ? (seg ? base : split.ratio * base) * C : n - c0 * C;
+    }
+    item.t0 = t_req0 + c0 * C;
+    item.n = n;
+    slot0 = (t_req0 >> 6) + b + c0;
+    return item;
+}
+
+template <bool SPLIT>
 __device__ void producer_role(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, Bars *bars,
-                              uint8_t *sm, const uint8_t *slots, size_t slot_step, int t0, int nchunks,
-                              int xq, int xv, Ctx cx) {
-    int kq = 0, vv = 0;
-    for (int c = 0; c < nchunks; ++c) {
-        const int st = c % kStages, g = c & 1;
-        if (c >= kStages && !wait_bar(&bars->kq_empty[st], (c / kStages - 1) & 1, cx)) break;
-        uint8_t *dst = sm + OFF_KQ + st * SZ_KQ;
-        const int y = t0 + c * C;
-        mbar_arrive_expect_tx(&bars->kq_full[st], SZ_KQ);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            tma_load_2d(dst + x * 16384, &tk, &bars->kq_full[st], xq + 64 * x, y);
-            tma_load_2d(dst + x * 16384 + 8192, &tq, &bars->kq_full[st], xq + 64 * x, y);
+                              uint8_t *sm, const DeltaParams &p, const uint8_t *ws, const int32_t *order,
+                              const Split &split, int items, Item item, int slot0, Ctx cx) {
+    int kq = 0, vv = 0;  // chunks whose K and Q, whose T and V are on the way
+    const size_t slot_step = (size_t)p.H * SZ_SLOT;
+    bool ok = true;
+    for (int k = 0; ok && k < items; ++k) {
+        if (k > 0) {
+            item = find_item<SPLIT>(p, order, split, item_at(k), slot0);
+            if (item.from && item.n > 0) bulk_prefetch(item.from, kMat * sizeof(float));
+            if (k >= kItems && !wait_bar<true>(&bars->item_empty[k % kItems], (k / kItems - 1) & 1, cx)) break;
         }
-        kq = c + 1;
-        if (kq == nchunks) mbar_arrive(&bars->kq_last);
-        if (c >= 2 && (!wait_bar(&bars->y_done[g], ((c >> 1) - 1) & 1, cx) ||
-                       !wait_bar(&bars->c_free[g], ((c >> 1) - 1) & 1, cx)))
-            break;
-        mbar_arrive_expect_tx(&bars->t_full[g], SZ_SLOT);
-        bulk_load(sm + OFF_T + g * SZ_T, slots + c * slot_step, SZ_SLOT, &bars->t_full[g]);
-        mbar_arrive_expect_tx(&bars->v_full[g], 16384);
-        tma_load_2d(sm + OFF_V + g * 16384, &tv, &bars->v_full[g], xv, y);
-        vv = c + 1;
+        bars->items[k % kItems] = item;
+        mbar_arrive(&bars->item_full[k % kItems]);
+        const int nchunks = (item.n + C - 1) / C;
+        const uint8_t *slots = ws + ((size_t)slot0 * p.H + item.h) * SZ_SLOT;
+        const int xq = (item.h / p.group) * kHeadDim, xv = item.h * kHeadDim;
+        for (int c = 0; c < nchunks; ++c) {
+            const int st = kq % kStages, g = kq & 1;
+            if (kq >= kStages && !(ok = wait_bar<true>(&bars->kq_empty[st], (kq / kStages - 1) & 1, cx))) break;
+            uint8_t *dst = sm + OFF_KQ + st * SZ_KQ;
+            const int y = item.t0 + c * C;
+            mbar_arrive_expect_tx(&bars->kq_full[st], SZ_KQ);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                tma_load_2d(dst + x * 16384, &tk, &bars->kq_full[st], xq + 64 * x, y);
+                tma_load_2d(dst + x * 16384 + 8192, &tq, &bars->kq_full[st], xq + 64 * x, y);
+            }
+            ++kq;
+            if (vv >= 2 && !(ok = wait_bar<true>(&bars->y_done[g], ((vv >> 1) - 1) & 1, cx) &&
+                                  wait_bar<true>(&bars->c_free[g], ((vv >> 1) - 1) & 1, cx)))
+                break;
+            mbar_arrive_expect_tx(&bars->t_full[g], SZ_SLOT);
+            bulk_load(sm + OFF_T + g * SZ_T, slots + c * slot_step, SZ_SLOT, &bars->t_full[g]);
+            mbar_arrive_expect_tx(&bars->v_full[g], 16384);
+            tma_load_2d(sm + OFF_V + g * 16384, &tv, &bars->v_full[g], xv, y);
+            ++vv;
+        }
     }
     // copies still in flight must land before the shared memory goes away
     int dummy = 0;
@@ -1102,77 +1237,50 @@ __device__ void producer_role(const CUtensorMap &tq, const CUtensorMap &tk, cons
     }
 }
 
+// Warp 10: rows of the request's last K tile past its end are zeroed.
+__device__ void fix_role(Bars *bars, uint8_t *sm, int items, int lane, const Ctx &cx) {
+    int st = 0;
+    uint32_t stp = 0;
+    for (int k = 0; k < items; ++k) {
+        if (!warp_wait<true>(&bars->item_full[k % kItems], (k / kItems) & 1, cx)) return;
+        const int n = bars->items[k % kItems].n;
+        warp_arrive(&bars->item_empty[k % kItems], lane);
+        for (int left = n; left > 0; left -= C) {
+            if (!warp_wait<true>(&bars->kq_full[st], stp, cx)) return;
+            if (left < C) {
+                uint8_t *tile = sm + OFF_KQ + st * SZ_KQ;
+                for (int x = left * 16 + lane; x < C * 16; x += 32)  // (token, column block, piece)
+                    *reinterpret_cast<uint4 *>(tile + ((x >> 3) & 1) * 16384 + (x >> 4) * 128 +
+                                               (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+            }
+            warp_arrive(&bars->kq_ready[st], lane);
+            warp_arrive(&bars->kq_empty[st], lane);
+            if (++st == kStages) {
+                st = 0;
+                stp ^= 1;
+            }
+        }
+    }
+}
+
+// Items: the chains (SPLIT: the jobs of a pass), one CTA each, or a CTA per SM that takes several in turn,
+// its loads running ahead into the next item.
 template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     delta_extend_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                         const __grid_constant__ CUtensorMap tv, const DeltaParams p, const uint8_t *ws,
-                        const int32_t *order, const Split split) {
+                        const int32_t *order, const Split split, int all_items) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Bars *bars = reinterpret_cast<Bars *>(sm + OFF_BAR);
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31;
-    pdl_wait();
-    pdl_trigger();
-    const int chains = p.B * p.H;
-    const int chain = (int)blockIdx.x % chains, job = (int)blockIdx.x / chains;
-    const int h = chain % p.H;
-    const int want = chain / p.H;
-
-    // Longest request first where there is more than one wave of CTAs: they are issued in index order, so
-    // long requests do not finish last.
-    const int b = order ? order[want] : want;
-
-    const int slot = p.state_idx[b];
-    const int t_req0 = p.cu_seqlens[b], t_req1 = p.cu_seqlens[b + 1];
-    if (slot < 0 || slot >= p.num_slots) {
-        if (threadIdx.x == 0) atomicOr(p.err, ERR_BIT_SLOT_RANGE);
-        return;
-    }
-    if (t_req0 < 0 || t_req1 < t_req0 || t_req1 > p.T || t_req1 - t_req0 > p.max_seqlen) {
-        if (threadIdx.x == 0) atomicOr(p.err, ERR_BIT_SEQLENS);
-        return;
-    }
-    int n = t_req1 - t_req0, c0 = 0;  // tokens and first chunk of this CTA
-    int nchunks = (n + C - 1) / C;
-    float *state = p.pool + ((size_t)slot * p.H + h) * kMat;
-    Ends ends{p.prefix_mask[b] ? state : nullptr, p.prefix_mask[b] && n == 0 ? nullptr : state, false, true};
-    if (SPLIT) {
-        const int base = split_base(split, nchunks), last = split_last(split, nchunks);
-        float *starts = split.starts + (size_t)chain * (split.segs - 1) * kMat;
-        int seg = 0;
-        if (split.pass == 2) {
-            seg = 1 + job;
-            if (seg > last) return;
-            ends.from = starts + (seg - 1) * kMat;
-            if (seg < last) ends.to = nullptr;
-        } else if (job > 0) {
-            seg = 1 + ((job - 1) >> 1);
-            if (seg >= last) return;
-            ends.from = nullptr;
-            ends.transition = job & 1;
-            ends.to = ends.transition
-                          ? split.trans + ((size_t)chain * (split.segs - 2) + seg - 1) * kMat
-                          : starts + seg * kMat;
-            ends.emit = false;
-        } else if (last > 0) {
-            ends.to = starts;
-        }
-        c0 = seg ? (split.ratio + seg - 1) * base : 0;
-        n -= c0 * C;
-        nchunks -= c0;
-        if (seg < last) {
-            nchunks = seg ? base : split.ratio * base;
-            n = nchunks * C;
-        }
-    }
-    const bool ragged = n % C != 0;
-    const int t_seg = t_req0 + c0 * C;
-
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&bars->kq_full[s], 1);
-            mbar_init(&bars->kq_empty[s], 1);
+            mbar_init(&bars->kq_empty[s], 2);
+            mbar_init(&bars->kq_ready[s], 1);
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(&bars->v_full[g], 1);
@@ -1180,8 +1288,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars->y_done[g], 1);
             mbar_init(&bars->c_free[g], kEWarps);
         }
-        mbar_init(&bars->kq_last, 1);
-        mbar_init(&bars->kq_fixed, 1);
+        for (int k = 0; k < kItems; ++k) {
+            mbar_init(&bars->item_full[k], 1);
+            mbar_init(&bars->item_empty[k], kEWarps + 2);
+        }
         mbar_init(&bars->x_full, 1);
         mbar_init(&bars->y_full, 1);
         mbar_init(&bars->d_full, 1);
@@ -1190,14 +1300,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         bars->abort_flag = 0;
         fence_mbar_init();
     }
+    pdl_wait();
+    pdl_trigger();
+    const int items = item_count(all_items);
+    Item first{};
+    int slot0 = 0;
     if (warp == kMmaWarp) {
         tmem_alloc(&bars->tmem_base, kTmemCols);
         tmem_relinquish();
-    }
-    if (warp == kProducerWarp && lane == 0 && nchunks > 0) {
+    } else if (warp == kProducerWarp && lane == 0) {
         tma_prefetch_desc(&tq);
         tma_prefetch_desc(&tk);
         tma_prefetch_desc(&tv);
+        first = find_item<SPLIT>(p, order, split, item_at(0), slot0);
     }
     tc_fence_before();
     __syncthreads();
@@ -1211,24 +1326,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     else
         reg_dec<kRegsRest>();
     if (warp < kEWarps) {
-        e_role<SPLIT>(p, sm, bars, cx, tbase, warp & 3, warp >> 2, lane, (size_t)t_seg, n, h, ends, nchunks);
+        e_role<SPLIT>(p, sm, bars, cx, tbase, warp & 3, warp >> 2, lane, items, split);
     } else if (warp == kProducerWarp) {
         if (lane == 0)
-            producer_role(tq, tk, tv, bars, sm,
-                          ws + ((size_t)((t_req0 >> 6) + b + c0) * p.H + h) * SZ_SLOT,
-                          (size_t)p.H * SZ_SLOT, t_seg, nchunks, (h / p.group) * kHeadDim, h * kHeadDim, cx);
+            producer_role<SPLIT>(tq, tk, tv, bars, sm, p, ws, order, split, items, first, slot0, cx);
     } else if (warp == kMmaWarp) {
-        mma_role(bars, tbase, smem_u32(sm), nchunks, ragged, lane, cx);
-    } else if (warp == kFixWarp && ragged) {
-        const int c = nchunks - 1, st = c % kStages;
-        if (warp_wait(&bars->kq_last, 0, cx) && warp_wait(&bars->kq_full[st], (c / kStages) & 1, cx)) {
-            uint8_t *tile = sm + OFF_KQ + st * SZ_KQ;
-            for (int x = (n - c * C) * 16 + lane; x < C * 16; x += 32)  // (token, column block, piece)
-                *reinterpret_cast<uint4 *>(tile + ((x >> 3) & 1) * 16384 + (x >> 4) * 128 + (x & 7) * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async_smem();
-            warp_arrive(&bars->kq_fixed, lane);
-        }
+        mma_role(bars, tbase, smem_u32(sm), items, lane, cx);
+    } else if (warp == kFixWarp) {
+        fix_role(bars, sm, items, lane, cx);
     }
     __syncwarp();
     tc_fence_before();
@@ -1359,7 +1464,8 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
     const long long ctas = (long long)p.B * p.H;
     if (ctas <= 0) return cudaSuccess;
     const long long t_ctas = p.T > 0 ? chunk_slots(p.T, p.B) * p.H : 0;
-    if (ctas > 0x7fffffffLL || t_ctas + kMaxRanked > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (ctas + num_sms > 0x7fffffffLL || t_ctas + kMaxRanked > 0x7fffffffLL)
+        return cudaErrorInvalidConfiguration;
     CUtensorMap tq, tk, tv;
     memset(&tq, 0, sizeof(tq));
     memset(&tk, 0, sizeof(tk));
@@ -1407,19 +1513,22 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
     }
     Split split = plan_split(ctas, ((long long)(p.max_seqlen < p.T ? p.max_seqlen : p.T) + C - 1) / C);
     if (split.pass == 0)
-        return launch_pdl(delta_extend_kernel<false>, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, tq,
-                          tk, tv, p, (const uint8_t *)w, (const int32_t *)order, split);
+        return launch_pdl(delta_extend_kernel<false>, dim3((unsigned)(ctas < num_sms ? ctas : num_sms)),
+                          dim3(kThreads), kSmemBytes, stream, tq, tk, tv, p, (const uint8_t *)w,
+                          (const int32_t *)order, split, (int)ctas);
     split.starts = reinterpret_cast<float *>(w + slots_bytes(p.B, p.T, p.H) + order_bytes(p.B));
     split.trans = split.starts + (size_t)ctas * (split.segs - 1) * kMat;
     e = launch_pdl(delta_extend_kernel<true>, dim3((unsigned)(ctas * (2 * split.segs - 3))), dim3(kThreads),
-                   kSmemBytes, stream, tq, tk, tv, p, (const uint8_t *)w, (const int32_t *)order, split);
+                   kSmemBytes, stream, tq, tk, tv, p, (const uint8_t *)w, (const int32_t *)order, split,
+                   (int)(ctas * (2 * split.segs - 3)));
     if (e != cudaSuccess) return e;
     e = launch_pdl(delta_join_kernel, dim3((unsigned)(ctas * (kHeadDim / kJoinCols))), dim3(kJoinThreads),
                    kJoinSmem, stream, p, split);
     if (e != cudaSuccess) return e;
     split.pass = 2;
     return launch_pdl(delta_extend_kernel<true>, dim3((unsigned)(ctas * (split.segs - 1))), dim3(kThreads),
-                      kSmemBytes, stream, tq, tk, tv, p, (const uint8_t *)w, (const int32_t *)order, split);
+                      kSmemBytes, stream, tq, tk, tv, p, (const uint8_t *)w, (const int32_t *)order, split,
+                      (int)(ctas * (split.segs - 1)));
 }
 
 }  // namespace la
