@@ -117,6 +117,9 @@ struct Item {
     int t0, n, h;       // first token, tokens, value head
 };
 constexpr int kItems = 4;
+// The kernel's kinds: several items a CTA; one (without the loop over items in the E warps' code, which costs
+// the chunk loop 2%); one that is a segment.
+enum Kind : int { MANY, ONE, SEGMENT };
 
 struct Bars {
     uint64_t kq_full[kStages];
@@ -799,9 +802,10 @@ __device__ __forceinline__ void load_pairs(const float *src, uint64_t (&x)[16]) 
     }
 }
 
-template <bool SPLIT>
+template <Kind KIND>
 __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx &cx, uint32_t tbase, int q,
                        int hf, int lane, int items, const Split &split) {
+    constexpr bool SPLIT = KIND == SEGMENT;
     const int v = 32 * q + lane;
     const int tok0 = 32 * hf;  // tokens tok0 .. + 31 of the chunk
     const uint32_t lanes = tbase + ((uint32_t)(32 * q) << 16);
@@ -810,7 +814,7 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
     const int at = 64 * hf * kHeadDim + v;
     bool ok = true;
     int cc = 0;  // chunks of the items before
-    for (int k = 0; k < items; ++k) {
+    for (int k = 0; k < (KIND == MANY ? items : 1); ++k) {
         bar_wait(kBarItem);
         if (!*(volatile int *)&bars->go[k & 1]) break;
         const Item item = bars->items[k % kItems];
@@ -1138,9 +1142,10 @@ __device__ __forceinline__ int item_count(int all) {
     return rows + (item_at(rows) < all);
 }
 
-template <bool SPLIT>
+template <Kind KIND>
 __device__ __forceinline__ Item find_item(const DeltaParams &p, const int32_t *order, const Split &split,
                                           int which, int &slot0) {
+    constexpr bool SPLIT = KIND == SEGMENT;
     Item item{nullptr, nullptr, 0, 0, 0};
     const int chains = p.B * p.H;
     const int chain = SPLIT ? which % chains : which;
@@ -1185,7 +1190,7 @@ __device__ __forceinline__ Item find_item(const DeltaParams &p, const int32_t *o
     return item;
 }
 
-template <bool SPLIT>
+template <Kind KIND>
 __device__ void producer_role(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, Bars *bars,
                               uint8_t *sm, const DeltaParams &p, const uint8_t *ws, const int32_t *order,
                               const Split &split, int items, Item item, int slot0, Ctx cx) {
@@ -1194,7 +1199,7 @@ __device__ void producer_role(const CUtensorMap &tq, const CUtensorMap &tk, cons
     bool ok = true;
     for (int k = 0; ok && k < items; ++k) {
         if (k > 0) {
-            item = find_item<SPLIT>(p, order, split, item_at(k), slot0);
+            item = find_item<KIND>(p, order, split, item_at(k), slot0);
             if (item.from && item.n > 0) bulk_prefetch(item.from, kMat * sizeof(float));
             if (k >= kItems && !wait_bar<true>(&bars->item_empty[k % kItems], (k / kItems - 1) & 1, cx)) break;
         }
@@ -1264,9 +1269,9 @@ __device__ void fix_role(Bars *bars, uint8_t *sm, int items, int lane, const Ctx
     }
 }
 
-// Items: the chains (SPLIT: the jobs of a pass), one CTA each, or a CTA per SM that takes several in turn,
+// Items: the chains (SEGMENT: the jobs of a pass), one CTA each, or a CTA per SM that takes several in turn,
 // its loads running ahead into the next item.
-template <bool SPLIT>
+template <Kind KIND>
 __global__ void __launch_bounds__(kThreads, 1)
     delta_extend_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                         const __grid_constant__ CUtensorMap tv, const DeltaParams p, const uint8_t *ws,
@@ -1312,7 +1317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tq);
         tma_prefetch_desc(&tk);
         tma_prefetch_desc(&tv);
-        first = find_item<SPLIT>(p, order, split, item_at(0), slot0);
+        first = find_item<KIND>(p, order, split, item_at(0), slot0);
     }
     tc_fence_before();
     __syncthreads();
@@ -1326,10 +1331,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     else
         reg_dec<kRegsRest>();
     if (warp < kEWarps) {
-        e_role<SPLIT>(p, sm, bars, cx, tbase, warp & 3, warp >> 2, lane, items, split);
+        e_role<KIND>(p, sm, bars, cx, tbase, warp & 3, warp >> 2, lane, items, split);
     } else if (warp == kProducerWarp) {
         if (lane == 0)
-            producer_role<SPLIT>(tq, tk, tv, bars, sm, p, ws, order, split, items, first, slot0, cx);
+            producer_role<KIND>(tq, tk, tv, bars, sm, p, ws, order, split, items, first, slot0, cx);
     } else if (warp == kMmaWarp) {
         mma_role(bars, tbase, smem_u32(sm), items, lane, cx);
     } else if (warp == kFixWarp) {
@@ -1484,12 +1489,10 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
         std::lock_guard<std::mutex> lock(mu);
         if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
         if (!configured[dev]) {
-            e = cudaFuncSetAttribute(delta_extend_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     kSmemBytes);
-            if (e != cudaSuccess) return e;
-            e = cudaFuncSetAttribute(delta_extend_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     kSmemBytes);
-            if (e != cudaSuccess) return e;
+            for (auto *kernel : {delta_extend_kernel<MANY>, delta_extend_kernel<ONE>, delta_extend_kernel<SEGMENT>}) {
+                e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+                if (e != cudaSuccess) return e;
+            }
             e = cudaFuncSetAttribute(delta_t_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTSmemBytes);
             if (e != cudaSuccess) return e;
             e = cudaFuncSetAttribute(delta_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1513,12 +1516,12 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
     }
     Split split = plan_split(ctas, ((long long)(p.max_seqlen < p.T ? p.max_seqlen : p.T) + C - 1) / C);
     if (split.pass == 0)
-        return launch_pdl(delta_extend_kernel<false>, dim3((unsigned)(ctas < num_sms ? ctas : num_sms)),
-                          dim3(kThreads), kSmemBytes, stream, tq, tk, tv, p, (const uint8_t *)w,
-                          (const int32_t *)order, split, (int)ctas);
+        return launch_pdl(ctas > num_sms ? delta_extend_kernel<MANY> : delta_extend_kernel<ONE>,
+                          dim3((unsigned)(ctas < num_sms ? ctas : num_sms)), dim3(kThreads), kSmemBytes,
+                          stream, tq, tk, tv, p, (const uint8_t *)w, (const int32_t *)order, split, (int)ctas);
     split.starts = reinterpret_cast<float *>(w + slots_bytes(p.B, p.T, p.H) + order_bytes(p.B));
     split.trans = split.starts + (size_t)ctas * (split.segs - 1) * kMat;
-    e = launch_pdl(delta_extend_kernel<true>, dim3((unsigned)(ctas * (2 * split.segs - 3))), dim3(kThreads),
+    e = launch_pdl(delta_extend_kernel<SEGMENT>, dim3((unsigned)(ctas * (2 * split.segs - 3))), dim3(kThreads),
                    kSmemBytes, stream, tq, tk, tv, p, (const uint8_t *)w, (const int32_t *)order, split,
                    (int)(ctas * (2 * split.segs - 3)));
     if (e != cudaSuccess) return e;
@@ -1526,7 +1529,7 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
                    kJoinSmem, stream, p, split);
     if (e != cudaSuccess) return e;
     split.pass = 2;
-    return launch_pdl(delta_extend_kernel<true>, dim3((unsigned)(ctas * (split.segs - 1))), dim3(kThreads),
+    return launch_pdl(delta_extend_kernel<SEGMENT>, dim3((unsigned)(ctas * (split.segs - 1))), dim3(kThreads),
                       kSmemBytes, stream, tq, tk, tv, p, (const uint8_t *)w, (const int32_t *)order, split,
                       (int)(ctas * (split.segs - 1)));
 }
