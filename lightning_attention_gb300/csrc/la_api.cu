@@ -537,6 +537,11 @@ bool row_stride_ok(int64_t *rs, long long rows, long long width) {
     return *rs >= width && *rs % 8 == 0;
 }
 
+// The grids have B * H CTAs, four times as many, or one per chunk and head.
+bool delta_grid_ok(long long B, long long tokens, long long H) {
+    return B * H <= 0x1fffffffLL && (tokens / 64 + B) * H <= 0x7fff0000LL;
+}
+
 // The checks and the marshalling that the delta entry points share.  `tokens` is their number of
 // token rows; work == false: nothing to launch.
 la_status delta_params(la::DeltaParams *p, bool *work, const la_bf16 *q, const la_bf16 *k,
@@ -555,8 +560,7 @@ la_status delta_params(la::DeltaParams *p, bool *work, const la_bf16 *q, const l
         return LA_ERR_INVALID;
     const long long widest = std::max<long long>(std::max<long long>(q_rs, k_rs), v_rs);
     if (widest >= (1ll << 38) || tokens * widest >= (1ll << 40)) return LA_ERR_UNSUPPORTED;
-    // the grids have B * H CTAs, four times as many, or one per chunk and head
-    if ((long long)B * H > 0x1fffffffLL || (tokens / 64 + B) * H > 0x7fff0000LL) return LA_ERR_UNSUPPORTED;
+    if (!delta_grid_ok(B, tokens, H)) return LA_ERR_UNSUPPORTED;
     if (B == 0) return LA_OK;
     if (!state_pool || !state_idx) return LA_ERR_INVALID;
     if (tokens > 0 && (!q || !k || !v || !g || !beta || !out)) return LA_ERR_INVALID;
@@ -649,7 +653,7 @@ la_status la_delta_extend(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, 
 
 la_status la_delta_extend_workspace_size(int B, int T, int H, int D, size_t *bytes) {
     if (B < 0 || T < 0 || H < 1 || D < 1 || bytes == nullptr) return LA_ERR_INVALID;
-    if (D != la::kHeadDim) return LA_ERR_UNSUPPORTED;
+    if (D != la::kHeadDim || !delta_grid_ok(B, T, H)) return LA_ERR_UNSUPPORTED;
     *bytes = (size_t)la::delta_scratch_bytes(B, T, H);
     return LA_OK;
 }

@@ -727,8 +727,8 @@ __global__ void __launch_bounds__(kTThreads, 5)
         }
     }
 
-    __syncthreads();
     fence_proxy_async_smem();
+    __syncthreads();
     if (threadIdx.x == 0) {
         bulk_store(slot_out, sm, 2 * SZ_PART);
         bulk_commit_group();
@@ -1319,9 +1319,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(&bars->tmem_base, kTmemCols);
         tmem_relinquish();
     } else if (warp == kProducerWarp && lane == 0) {
-        tma_prefetch_desc(&tq);
-        tma_prefetch_desc(&tk);
-        tma_prefetch_desc(&tv);
+        if (p.T > 0) {
+            tma_prefetch_desc(&tq);
+            tma_prefetch_desc(&tk);
+            tma_prefetch_desc(&tv);
+        }
         first = find_item<KIND>(p, order, split, item_at(0), slot0);
     }
     tc_fence_before();

@@ -29,7 +29,8 @@ def _mask(n, value=0):
     return torch.full((n,), value, dtype=torch.uint8, device=DEV)
 
 
-@pytest.mark.parametrize("lens,H,must", [([1000, 300], 2, True), ([3000], 2, True), ([40] * 100, 2, False)])
+@pytest.mark.parametrize("lens,H,must", [([1000, 300], 2, True), ([3000], 2, True),
+                                          ([700] * 80, 2, True), ([40] * 100, 2, False)])
 def test_waits_that_run_out(lens, H, must):
     """Calls under a 1 us wait limit are reported as LA_ERR_TIMEOUT; the next call is as ever.  A try
     of a wait may itself be suspended for a few microseconds, so that the waits of a request of one
