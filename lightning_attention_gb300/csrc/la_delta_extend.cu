@@ -142,12 +142,13 @@ static_assert(sizeof(Bars) <= SZ_BAR, "barrier block");
 
 // Shared memory of the T kernel (five CTAs per SM).  16 x 16 blocks of the inversion are two panels of 8
 // columns x 16 rows x 16 bytes: the blocks of A below the diagonal (hi, lo) and the diagonal blocks of T
-// (hi, lo; before that A's, transposed, and T's in fp32).  The slot's two parts take the place of K and Q
-// (P before P T).
+// (hi, lo; before that A's, transposed, and T's in fp32).  The slot's two parts (P before P T) and the blocks
+// take the place of K and Q.  (Six CTAs fit, at 80 registers: 227 us in place of 222 on the mixed batch.)
 constexpr uint32_t TK_KQ = 0;                              // [64 K rows; 64 Q rows][128]
-constexpr uint32_t TK_AB = 32768;                          // 6 x (512 hi + 512 lo)
+constexpr uint32_t TK_AB = 2 * SZ_PART;                          // 6 x (512 hi + 512 lo)
 constexpr uint32_t TK_TD = TK_AB + 6 * 1024;               // 4 x (512 hi + 512 lo)
-constexpr uint32_t TK_TOK = TK_TD + 4 * 1024;              // per token: ghi, glo, rk, beta rk, scale rq
+constexpr uint32_t TK_TOK = TK_KQ + SZ_KQ;             // per token: ghi, glo, rk, beta rk, scale rq
+static_assert(TK_TD + 4 * 1024 <= SZ_KQ, "blocks in place of K and Q");
 constexpr uint32_t kTSmemBytes = TK_TOK + 5 * 256 + 1024;
 
 // Named barriers between the E warps, which arrive, and the MMA warp, which waits: k-steps y and 4 + y of S
@@ -412,7 +413,7 @@ __device__ void rank_requests(const DeltaParams &p, int block, int32_t *order, i
 // block of I + A by substitution, a lane per column, then the blocks below by T_ab = -T_aa sum A_am T_mb.
 // Measured: 66 us on 8 requests of 512-4096 tokens x 16 heads, 254 us on 256 of 32-512; 40-50 % of DRAM and half
 // of the issue slots.  Bound by the latency of the dependent small products and the barriers between them, at
-// the 20 warps per SM that registers (95) and shared memory (45 KB) allow.
+// the 20 warps per SM that its 95 registers allow.
 __global__ void __launch_bounds__(kTThreads, 5)
     delta_t_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const DeltaParams p, uint8_t *ws, int32_t *order, int rank_ctas) {
