@@ -45,8 +45,9 @@
 // about 2.4 us: 36 MMAs of 45-65 cycles are half of it, the passes between them (wait, tensor memory to
 // registers, pair split, back, barrier) the other half; no two of them overlap along the chain, and a second
 // chain on the SM has room neither in tensor memory (512 columns) nor in shared memory (171 KB).
-// More items than SMs: a CTA per SM takes several in turn (387 us of chain on 256 requests of 32-512 tokens x
-// 16 heads, where a CTA per item took 437), and warp 8 runs ahead of the item that is worked on.
+// More items than SMs: a CTA per SM takes several in turn, longest first, each from a common count, and warp 8
+// runs ahead of the item that is worked on.  256 requests of 32-512 tokens x 16 heads: 636 us; items dealt out
+// in turn 655, a CTA per item 703.
 //
 // Every wait ends: mbarrier waits have a deadline (the named barriers below end with them); one that runs out
 // sets the error word and an abort flag that ends every role, then the CTA waits for its copies and MMAs,
@@ -69,7 +70,7 @@ constexpr int C = 64;  // tokens of a chunk
 constexpr int kEWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kFixWarp = 10;
 constexpr int kThreads = 384;
 // Registers per thread of the warp groups: 2 x 184 (E) + 136 = 3 x 168, the launch's share.  (E at 200: the
-// same times; at 216: 678 us in place of 663 on the batch above.)
+// same times; at 216 2% more on the batch above.)
 constexpr int kRegsE = 184, kRegsRest = 136;
 static_assert(2 * kRegsE + kRegsRest <= 3 * 168, "register split");
 constexpr int kTThreads = 128;
@@ -115,11 +116,13 @@ struct Item {
     const float *from;  // the start state; null: zero, or the identity for a transition
     float *to;          // where the end state goes; null: not kept
     int t0, n, h;       // first token, tokens, value head
+    int transition;     // PLANNED: V counts as zero
+    int emit;           // PLANNED: outputs are written
 };
 constexpr int kItems = 4;
 // The kernel's kinds: several items a CTA; one (without the loop over items in the E warps' code, which costs
-// the chunk loop 2%); one that is a segment.
-enum Kind : int { MANY, ONE, SEGMENT };
+// the chunk loop 2%); one that is a segment; several that are segments of a plan.
+enum Kind : int { MANY, ONE, SEGMENT, PLANNED };
 
 struct Bars {
     uint64_t kq_full[kStages];
@@ -391,6 +394,168 @@ __device__ __forceinline__ void scale_block(const TokenFactors &f, int a, int b,
     }
 }
 
+// ------------------------------------------------------------------------------------------------
+// Split of a long request.  With few (request, head) pairs the chain leaves SMs idle, and a segment of it
+// can be run without its start state: its chunks take S to M S + N, N being the segment's result from
+// S = 0 and M its result from the identity with V = 0, which are two more chains of the same kernel.  So the
+// chain is cut into segs segments, the first ratio times as long as the others:
+//   pass 1   segment 0 as usual; N and M of segments 1 .. segs - 2, side by side with it;
+//   join     the segments' start states, S_1 from pass 1, S_{g+1} = M_g S_g + N_g in fp32;
+//   pass 2   segments 1 .. segs - 1 from their start states, side by side.
+// Rounding in a segment is amplified by the segments after it as the chain's own is.
+// Measured whole / split, us, T kernel included, l2norm, one request: 8 heads: 1,024 tokens 47.5 / 45.8,
+// 2,048: 84.6 / 66.5, 16,384: 626 / 199; 32 heads: 1,024: 52.7 / 61.9, 1,536: 75.3 / 73.7, 16,384:
+// 703 / 438; 76 heads: 2,560: 145 / 149, 4,096: 222 / 212, 16,384: 836 / 720.
+struct Split {
+    int segs, ratio;
+    int pass;       // 0: not split
+    float *starts;  // [chains][segs - 1][D][D]: S_g at g - 1 (N_{g-1} before the join)
+    float *trans;   // [chains][segs - 2][D][D]: M_g at g - 1
+    const int32_t *plan;  // PLANNED: what follows; starts holds all of the plan's matrices
+};
+constexpr int kMaxSegs = 16;
+constexpr int kSplitSMs = 152;       // chains that run side by side
+constexpr int kSplitMinChunks = 20;  // shorter requests are not split
+// What the join and two more launches cost, and a segment in the join, in chunks of the chain.
+constexpr double kSplitCost = 5., kJoinCost = 1.;
+constexpr float kItemCost = 1.2f;  // of an item beside its chunks, in chunks
+constexpr double kSplitGain = .95;  // a split has to promise this much
+constexpr size_t kMat = (size_t)kHeadDim * kHeadDim;
+// Chunks of segments 1, 2 ..; the last segment that has any.
+__host__ __device__ inline int split_base(const Split &s, int nchunks) {
+    return (nchunks + s.ratio + s.segs - 2) / (s.ratio + s.segs - 1);
+}
+__host__ __device__ inline int split_last(const Split &s, int nchunks) {
+    const int base = split_base(s, nchunks), rest = nchunks - s.ratio * base;
+    return rest > 0 ? 1 + (rest - 1) / base : 0;
+}
+
+// The job of a CTA (one item each): segment, whether it is a transition, whether outputs are written.
+struct Job {
+    int seg;
+    bool transition, emit;
+};
+__device__ __forceinline__ Job split_job(const DeltaParams &p, const Split &s) {
+    const int job = (int)blockIdx.x / (p.B * p.H);
+    if (s.pass == 2) return {1 + job, false, true};
+    return {(job + 1) >> 1, (job & 1) != 0, job == 0};
+}
+
+// Plan of a batch whose longest request is much longer than its share of the SMs (which the host judges by
+// max_seqlen and T; the lengths are on the device).  The same two passes, but with one cut for all requests:
+// segment 0 is a request's first a chunks, the next are b chunks each, so that short requests end in pass 1 as
+// they are.  A CTA of the first kernel tries 128 pairs (a, b) and lists the segments of both passes longest
+// first; an entry stands for its request's H heads.
+constexpr int kMaxPlanned = 512;  // requests
+constexpr int kPlanMats = 512;    // matrices (start states and transitions, all heads)
+constexpr int kPlanA = 0, kPlanB = 1, kPlanFirst = 2, kPlanSecond = 3, kPlanJoins = 4, kPlanStarts = 5;
+constexpr int kPlanTaken1 = 6, kPlanTaken2 = 7;  // items taken in a pass, beyond each CTA's first
+constexpr int kPlanList1 = 16;                                  // entries of pass 1
+constexpr int kPlanList2 = kPlanList1 + kMaxPlanned + kPlanMats;  // of pass 2
+constexpr int kPlanJoin = kPlanList2 + kPlanMats;               // requests with a join
+constexpr int kPlanS = kPlanJoin + kMaxPlanned;                 // start states before a request's
+constexpr int kPlanT = kPlanS + kMaxPlanned;                    // transitions before a request's
+constexpr int kPlanInts = kPlanT + kMaxPlanned;
+constexpr size_t kPlanBytes = kPlanInts * sizeof(int32_t);
+static_assert(kPlanBytes % 16 == 0, "matrices are 16-byte aligned");
+constexpr int kPlanTrans = 1 << 30;
+__device__ __forceinline__ int plan_entry(int request, int seg) { return request | seg << 10; }
+__host__ __device__ inline int segments_after(int nchunks, int a, int b) {
+    return nchunks > a ? (nchunks - a + b - 1) / b : 0;
+}
+__device__ __forceinline__ bool request_ok(const DeltaParams &p, int t0, int t1) {
+    return t0 >= 0 && t1 >= t0 && t1 <= p.T && t1 - t0 <= p.max_seqlen;
+}
+__device__ void plan_requests(const DeltaParams &p, int32_t *plan, int *sm) {
+    int *len = sm, *last = sm + kMaxPlanned;
+    __shared__ int most;
+    __shared__ unsigned long long best;
+    if (threadIdx.x == 0) {
+        most = 0;
+        best = ~0ull;
+    }
+    __syncthreads();
+    for (int r = threadIdx.x; r < p.B; r += kTThreads) {
+        const int t0 = p.cu_seqlens[r], t1 = p.cu_seqlens[r + 1];
+        len[r] = request_ok(p, t0, t1) ? (t1 - t0 + C - 1) / C : 0;
+        atomicMax(&most, len[r]);
+    }
+    __syncthreads();
+    auto cut_a = [&](int t) { return max(1, (most * ((t >> 3) + 1) + 15) / 16); };
+    auto cut_b = [&](int t) { return max(1, (cut_a(t) * ((t & 7) + 1) + 7) / 8); };
+    {
+        const int a = cut_a(threadIdx.x), b = cut_b(threadIdx.x);
+        int w1 = 0, w2 = 0, mats = 0, trans = 0, deepest = 0, tail = 0;
+        for (int r = 0; r < p.B; ++r) {
+            w1 += min(len[r], a);
+            const int l = segments_after(len[r], a, b);
+            if (l > 0) {
+                w1 += 2 * (l - 1) * b;
+                w2 += len[r] - a;
+                mats += 2 * l - 1;
+                trans += l - 1;
+                deepest = max(deepest, l);
+                tail = max(tail, min(b, len[r] - a));
+            }
+        }
+        // the longest segment of a pass, or the SMs' share of all, items' own cost and uneven ends included
+        const float share = 1.1f * (float)p.H / (float)kSplitSMs;
+        float cost = fmaxf((float)min(a, most), share * ((float)w1 + kItemCost * (float)(p.B + 2 * trans)));
+        if (deepest > 0) {
+            cost += fmaxf((float)tail, share * ((float)w2 + kItemCost * (float)(mats - trans))) +
+                    (float)kSplitCost + 2.f * (float)kJoinCost * (float)deepest;
+            cost *= 1.f / (float)kSplitGain;
+            if (mats > kPlanMats / p.H) cost = 3e38f;
+        }
+        atomicMin(&best, (unsigned long long)__float_as_uint(cost) << 32 | threadIdx.x);
+    }
+    __syncthreads();
+    const int won = (int)(best & 0xffffffffu);
+    const int a = cut_a(won), b = cut_b(won);
+    for (int r = threadIdx.x; r < p.B; r += kTThreads) last[r] = segments_after(len[r], a, b);
+    __syncthreads();
+    for (int r = threadIdx.x; r < p.B; r += kTThreads) {
+        const int first = min(len[r], a), mine = last[r];
+        const int tail = len[r] - a - (mine - 1) * b;  // chunks of the last segment
+        int rank1 = 0, rank2 = 0, whole = 0, starts = 0, trans = 0, joins = 0, all_trans = 0;
+        for (int u = 0; u < p.B; ++u) {
+            const int f = min(len[u], a), l = last[u], before = u < r;
+            rank1 += f > first || (f == first && before);
+            whole += f >= b;
+            all_trans += max(l - 1, 0);
+            if (before) {
+                starts += l;
+                trans += max(l - 1, 0);
+                joins += l > 1;
+            }
+            const int x = len[u] - a - (l - 1) * b;
+            rank2 += l > 0 && (x > tail || (x == tail && before));
+        }
+        plan[kPlanS + r] = starts;
+        plan[kPlanT + r] = trans;
+        if (mine > 1) plan[kPlanJoin + joins] = r;
+        // N and M of a segment stand behind the first segments that are as long
+        plan[kPlanList1 + rank1 + (first < b ? 2 * all_trans : 0)] = plan_entry(r, 0);
+        for (int g = 1; g < mine; ++g) {
+            plan[kPlanList1 + whole + 2 * (trans + g - 1)] = plan_entry(r, g);
+            plan[kPlanList1 + whole + 2 * (trans + g - 1) + 1] = plan_entry(r, g) | kPlanTrans;
+            plan[kPlanList2 + trans + g - 1] = plan_entry(r, g);
+        }
+        if (mine > 0) plan[kPlanList2 + all_trans + rank2] = plan_entry(r, mine);
+        if (r == p.B - 1) {
+            plan[kPlanTaken1] = plan[kPlanTaken2] = 0;
+            plan[kPlanA] = a;
+            plan[kPlanB] = b;
+            plan[kPlanFirst] = p.B + 2 * all_trans;
+            plan[kPlanSecond] = starts + mine;
+            plan[kPlanJoins] = joins + (mine > 1);
+            plan[kPlanStarts] = starts + mine;
+        }
+    }
+}
+
+// The order of a batch, and behind it a count.
+__host__ __device__ inline int order_ints(int B) { return (B + 1 + 3) / 4 * 4; }
 // Request of each rank in decreasing length order (ties by index), kTThreads requests per CTA.
 __device__ void rank_requests(const DeltaParams &p, int block, int32_t *order, int *lens) {
     const int b = block * kTThreads + (int)threadIdx.x;
@@ -405,18 +570,19 @@ __device__ void rank_requests(const DeltaParams &p, int block, int32_t *order, i
         for (int x = 0; x < m; ++x) rank += (lens[x] > mine) || (lens[x] == mine && u0 + x < b);
     }
     if (b < p.B) order[rank] = b;
+    if (b == 0) order[order_ints(p.B) - 1] = 0;  // items taken beyond each CTA's first
 }
 
 // T', P T and the coefficients of one chunk and head (blockIdx.x = rank_ctas + slot * H + head); the first
-// rank_ctas CTAs order the requests for the chain kernel.  Warp w has the 16 rows 16 w .. of everything: the
-// 16 x 16 blocks of K K^T and Q K^T (mma.sync: a block is too small for tcgen05), the inverse of its diagonal
+// rank_ctas CTAs order the requests for the chain kernel, or plan its segments.  Warp w has the 16 rows 16 w ..
+// of everything: the 16 x 16 blocks of K K^T and Q K^T (mma.sync: a block is too small for tcgen05), the inverse of its diagonal
 // block of I + A by substitution, a lane per column, then the blocks below by T_ab = -T_aa sum A_am T_mb.
 // Measured: 66 us on 8 requests of 512-4096 tokens x 16 heads, 254 us on 256 of 32-512; 40-50 % of DRAM and half
 // of the issue slots.  Bound by the latency of the dependent small products and the barriers between them, at
 // the 20 warps per SM that its 95 registers allow.
 __global__ void __launch_bounds__(kTThreads, 5)
     delta_t_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                   const DeltaParams p, uint8_t *ws, int32_t *order, int rank_ctas) {
+                   const DeltaParams p, uint8_t *ws, int32_t *order, int32_t *plan, int rank_ctas) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t kq_full;
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -425,7 +591,10 @@ __global__ void __launch_bounds__(kTThreads, 5)
     pdl_wait();
     pdl_trigger();
     if ((int)blockIdx.x < rank_ctas) {
-        rank_requests(p, blockIdx.x, order, reinterpret_cast<int *>(sm));
+        if (plan)
+            plan_requests(p, plan, reinterpret_cast<int *>(sm));
+        else
+            rank_requests(p, blockIdx.x, order, reinterpret_cast<int *>(sm));
         return;
     }
     const unsigned item = blockIdx.x - (unsigned)rank_ctas;
@@ -738,51 +907,6 @@ __global__ void __launch_bounds__(kTThreads, 5)
 }
 
 // ------------------------------------------------------------------------------------------------
-// Split of a long request.  With few (request, head) pairs the chain leaves SMs idle, and a segment of it
-// can be run without its start state: its chunks take S to M S + N, N being the segment's result from
-// S = 0 and M its result from the identity with V = 0, which are two more chains of the same kernel.  So the
-// chain is cut into segs segments, the first ratio times as long as the others:
-//   pass 1   segment 0 as usual; N and M of segments 1 .. segs - 2, side by side with it;
-//   join     the segments' start states, S_1 from pass 1, S_{g+1} = M_g S_g + N_g in fp32;
-//   pass 2   segments 1 .. segs - 1 from their start states, side by side.
-// Rounding in a segment is amplified by the segments after it as the chain's own is.
-// Measured whole / split, us, T kernel included, l2norm, one request: 8 heads: 1,024 tokens 47.5 / 45.8,
-// 2,048: 84.6 / 66.5, 16,384: 626 / 199; 32 heads: 1,024: 52.7 / 61.9, 1,536: 75.3 / 73.7, 16,384:
-// 703 / 438; 76 heads: 2,560: 145 / 149, 4,096: 222 / 212, 16,384: 836 / 720.
-struct Split {
-    int segs, ratio;
-    int pass;       // 0: not split
-    float *starts;  // [chains][segs - 1][D][D]: S_g at g - 1 (N_{g-1} before the join)
-    float *trans;   // [chains][segs - 2][D][D]: M_g at g - 1
-};
-constexpr int kMaxSegs = 16;
-constexpr int kSplitSMs = 152;       // chains that run side by side
-constexpr int kSplitMinChunks = 20;  // shorter requests are not split
-// What the join and two more launches cost, and a segment in the join, in chunks of the chain.
-constexpr double kSplitCost = 5., kJoinCost = 1.;
-constexpr double kSplitGain = .95;  // a split has to promise this much
-constexpr size_t kMat = (size_t)kHeadDim * kHeadDim;
-// Chunks of segments 1, 2 ..; the last segment that has any.
-__host__ __device__ inline int split_base(const Split &s, int nchunks) {
-    return (nchunks + s.ratio + s.segs - 2) / (s.ratio + s.segs - 1);
-}
-__host__ __device__ inline int split_last(const Split &s, int nchunks) {
-    const int base = split_base(s, nchunks), rest = nchunks - s.ratio * base;
-    return rest > 0 ? 1 + (rest - 1) / base : 0;
-}
-
-// The job of a CTA (one item each): segment, whether it is a transition, whether outputs are written.
-struct Job {
-    int seg;
-    bool transition, emit;
-};
-__device__ __forceinline__ Job split_job(const DeltaParams &p, const Split &s) {
-    const int job = (int)blockIdx.x / (p.B * p.H);
-    if (s.pass == 2) return {1 + job, false, true};
-    return {(job + 1) >> 1, (job & 1) != 0, job == 0};
-}
-
-// ------------------------------------------------------------------------------------------------
 // E warps: lanes are value columns v = 32 q + lane; half hf of the chunk's tokens and of the k columns.
 
 // Eight pairs (one k-step of an operand) as 8 columns of hi parts and 8 of lo parts; the MMA issuer may
@@ -820,15 +944,16 @@ __device__ void e_role(const DeltaParams &p, uint8_t *sm, Bars *bars, const Ctx 
     const int at = 64 * hf * kHeadDim + v;
     bool ok = true;
     int cc = 0;  // chunks of the items before
-    for (int k = 0; k < (KIND == MANY ? items : 1); ++k) {
+    for (int k = 0; k < (KIND == MANY || KIND == PLANNED ? items : 1); ++k) {
         bar_wait(kBarItem);
         if (!*(volatile int *)&bars->go[k & 1]) break;
         const Item item = bars->items[k % kItems];
         warp_arrive(&bars->item_empty[k % kItems], lane);
         const int n = item.n, h = item.h, nchunks = (n + C - 1) / C;
         const size_t t0 = (size_t)item.t0;
-        const bool transition = SPLIT && split_job(p, split).transition;
-        const bool emit = !SPLIT || split_job(p, split).emit;
+        const bool transition =
+            KIND == PLANNED ? item.transition != 0 : SPLIT && split_job(p, split).transition;
+        const bool emit = KIND == PLANNED ? item.emit != 0 : !SPLIT || split_job(p, split).emit;
         // a transition's V as zero (a choice between values makes its loads wait behind a branch: 975 us in
         // place of 840 for 32,768 tokens)
         const uint32_t vmask = transition ? 0u : 0xffffffffu;
@@ -1055,7 +1180,8 @@ __device__ void mma_role(Bars *bars, uint32_t tbase, uint32_t s_base, int items,
     uint32_t stp = 0;
     for (int k = 0; k < items; ++k) {
         ok = ok && warp_wait(&bars->item_full[k % kItems], (k / kItems) & 1, cx);
-        const bool go = __shfl_sync(0xffffffffu, (int)(ok && !*cx.abort_flag), 0);
+        const bool go =
+            __shfl_sync(0xffffffffu, (int)(ok && !*cx.abort_flag && bars->items[k % kItems].n >= 0), 0);
         if (lane == 0) bars->go[k & 1] = go;
         __syncwarp();
         bar_wait(kBarItem);
@@ -1138,8 +1264,8 @@ __device__ void mma_role(Bars *bars, uint32_t tbase, uint32_t s_base, int items,
     }
 }
 
-// Item k of a CTA: rows of gridDim.x items, taken from the left and the right in turn (they come longest
-// first, so that the CTAs' sums stay close).
+// Item k of a CTA where none are counted out: rows of gridDim.x items, taken from the left and the right in
+// turn.
 __device__ __forceinline__ int item_at(int k) {
     return k * (int)gridDim.x + (int)((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
@@ -1152,12 +1278,14 @@ template <Kind KIND>
 __device__ __forceinline__ Item find_item(const DeltaParams &p, const int32_t *order, const Split &split,
                                           int which, int &slot0) {
     constexpr bool SPLIT = KIND == SEGMENT;
-    Item item{nullptr, nullptr, 0, 0, 0};
+    Item item{nullptr, nullptr, 0, 0, 0, 0, 1};
     const int chains = p.B * p.H;
     const int chain = SPLIT ? which % chains : which;
     const int h = chain % p.H, want = chain / p.H;
+    const int32_t *plan = split.plan;
+    const int entry = KIND == PLANNED ? plan[(split.pass == 2 ? kPlanList2 : kPlanList1) + want] : 0;
     // Longest request first where there is more than one row of items.
-    const int b = order ? order[want] : want;
+    const int b = KIND == PLANNED ? entry & 1023 : order ? order[want] : want;
     item.h = h;
     const int slot = p.state_idx[b];
     const int t_req0 = p.cu_seqlens[b], t_req1 = p.cu_seqlens[b + 1];
@@ -1166,7 +1294,7 @@ __device__ __forceinline__ Item find_item(const DeltaParams &p, const int32_t *o
         atomicOr(p.err, ERR_BIT_SLOT_RANGE);
         return item;
     }
-    if (t_req0 < 0 || t_req1 < t_req0 || t_req1 > p.T || t_req1 - t_req0 > p.max_seqlen) {
+    if (!request_ok(p, t_req0, t_req1)) {
         atomicOr(p.err, ERR_BIT_SEQLENS);
         return item;
     }
@@ -1181,7 +1309,7 @@ __device__ __forceinline__ Item find_item(const DeltaParams &p, const int32_t *o
         const Job job = split_job(p, split);
         const int seg = job.seg;
         // no such segment, or one whose end state nothing needs
-        if (seg > last || (seg == last && !job.emit)) return Item{nullptr, nullptr, 0, 0, 0};
+        if (seg > last || (seg == last && !job.emit)) return Item{nullptr, nullptr, 0, 0, 0, 0, 0};
         if (seg > 0) item.from = split.pass == 2 ? starts + (seg - 1) * kMat : nullptr;
         if (job.transition)
             item.to = split.trans + ((size_t)chain * (split.segs - 2) + seg - 1) * kMat;
@@ -1189,6 +1317,23 @@ __device__ __forceinline__ Item find_item(const DeltaParams &p, const int32_t *o
             item.to = split.pass == 2 ? nullptr : starts + seg * kMat;
         c0 = seg ? (split.ratio + seg - 1) * base : 0;
         n = seg < last ? (seg ? base : split.ratio * base) * C : n - c0 * C;
+    }
+    if (KIND == PLANNED) {
+        const int nchunks = (n + C - 1) / C, a = plan[kPlanA], len = plan[kPlanB];
+        const int seg = (entry >> 10) & 1023, last = segments_after(nchunks, a, len);
+        // start state g of head h; the transitions stand behind all start states
+        auto mat = [&](int x) { return split.starts + ((size_t)x * p.H + h) * kMat; };
+        auto start = [&](int g) { return mat(plan[kPlanS + b] + g - 1); };
+        const bool second = split.pass == 2;
+        item.transition = (entry & kPlanTrans) != 0;
+        item.emit = second || seg == 0;
+        if (seg > 0) item.from = second ? start(seg) : nullptr;
+        if (item.transition)
+            item.to = mat(plan[kPlanStarts] + plan[kPlanT + b] + seg - 1);
+        else if (seg < last)
+            item.to = second ? nullptr : start(seg + 1);
+        c0 = seg ? a + (seg - 1) * len : 0;
+        n = seg < last ? (seg ? len : a) * C : n - c0 * C;
     }
     item.t0 = t_req0 + c0 * C;
     item.n = n;
@@ -1199,19 +1344,28 @@ __device__ __forceinline__ Item find_item(const DeltaParams &p, const int32_t *o
 template <Kind KIND>
 __device__ void producer_role(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, Bars *bars,
                               uint8_t *sm, const DeltaParams &p, const uint8_t *ws, const int32_t *order,
-                              const Split &split, int items, Item item, int slot0, Ctx cx) {
+                              const Split &split, int32_t *taken, int all, int items, Item item, int slot0,
+                              Ctx cx) {
     int kq = 0, vv = 0;  // chunks whose K and Q, whose T and V are on the way
     const size_t slot_step = (size_t)p.H * SZ_SLOT;
     bool ok = true;
     for (int k = 0; ok && k < items; ++k) {
         if (k > 0) {
-            item = find_item<KIND>(p, order, split, item_at(k), slot0);
+            // items come longest first, and the next one goes to the CTA that is ready for it first
+            const int which = taken ? (int)gridDim.x + atomicAdd(taken, 1) : item_at(k);
+            if (which >= all) {
+                item.n = -1;  // no more
+                item.from = nullptr;
+                items = k;
+            } else {
+                item = find_item<KIND>(p, order, split, which, slot0);
+            }
             if (item.from && item.n > 0) bulk_prefetch(item.from, kMat * sizeof(float));
             if (k >= kItems && !wait_bar<true>(&bars->item_empty[k % kItems], (k / kItems - 1) & 1, cx)) break;
         }
         bars->items[k % kItems] = item;
         mbar_arrive(&bars->item_full[k % kItems]);
-        const int nchunks = (item.n + C - 1) / C;
+        const int nchunks = item.n > 0 ? (item.n + C - 1) / C : 0;
         const uint8_t *slots = ws + ((size_t)slot0 * p.H + item.h) * SZ_SLOT;
         const int xq = (item.h / p.group) * kHeadDim, xv = item.h * kHeadDim;
         for (int c = 0; c < nchunks; ++c) {
@@ -1255,6 +1409,7 @@ __device__ void fix_role(Bars *bars, uint8_t *sm, int items, int lane, const Ctx
     for (int k = 0; k < items; ++k) {
         if (!warp_wait<true>(&bars->item_full[k % kItems], (k / kItems) & 1, cx)) return;
         const int n = bars->items[k % kItems].n;
+        if (n < 0) return;
         warp_arrive(&bars->item_empty[k % kItems], lane);
         for (int left = n; left > 0; left -= C) {
             if (!warp_wait<true>(&bars->kq_full[st], stp, cx)) return;
@@ -1281,7 +1436,7 @@ template <Kind KIND>
 __global__ void __launch_bounds__(kThreads, 1)
     delta_extend_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                         const __grid_constant__ CUtensorMap tv, const DeltaParams p, const uint8_t *ws,
-                        const int32_t *order, const Split split, int all_items) {
+                        const int32_t *order, const Split split, int32_t *taken, int all_items) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Bars *bars = reinterpret_cast<Bars *>(sm + OFF_BAR);
@@ -1313,7 +1468,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     pdl_wait();
     pdl_trigger();
-    const int items = item_count(all_items);
+    if (KIND == PLANNED) all_items = split.plan[split.pass == 2 ? kPlanSecond : kPlanFirst] * p.H;
+    if (KIND == PLANNED && (int)blockIdx.x >= all_items) return;
+    const int items = taken ? 0x7fffffff : item_count(all_items);
     Item first{};
     int slot0 = 0;
     if (warp == kMmaWarp) {
@@ -1342,7 +1499,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         e_role<KIND>(p, sm, bars, cx, tbase, warp & 3, warp >> 2, lane, items, split);
     } else if (warp == kProducerWarp) {
         if (lane == 0)
-            producer_role<KIND>(tq, tk, tv, bars, sm, p, ws, order, split, items, first, slot0, cx);
+            producer_role<KIND>(tq, tk, tv, bars, sm, p, ws, order, split, taken, all_items, items, first,
+                                slot0, cx);
     } else if (warp == kMmaWarp) {
         mma_role(bars, tbase, smem_u32(sm), items, lane, cx);
     } else if (warp == kFixWarp) {
@@ -1359,8 +1517,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // The join: a CTA of 256 threads takes kJoinCols columns of one chain's states through all segments.
 // 128 x 128 x kJoinCols fp32 products a segment, 4 x 4 of them a thread, so that a shared-memory load feeds
-// eight; M is fetched one segment ahead (64 KB, from L2).
+// eight; M (64 KB, from L2) and N are fetched one segment ahead.  About 5 us a segment, bound by those loads
+// (512 threads of half as many products each: 6).
 constexpr int kJoinCols = 32, kJoinThreads = 256;
+constexpr int kJoinRows = kHeadDim * kJoinCols / 4 / kJoinThreads;  // of a thread, kJoinStep apart
+constexpr int kJoinStep = kHeadDim / kJoinRows;
 constexpr int kJoinPitch = kHeadDim + 4;
 constexpr uint32_t kJoinSmem = (2 * kHeadDim * kJoinPitch + 2 * kHeadDim * kJoinCols) * sizeof(float);
 __device__ __forceinline__ void fetch_mat(float *dst, const float *src) {
@@ -1371,6 +1532,67 @@ __device__ __forceinline__ void fetch_mat(float *dst, const float *src) {
                      : "memory");
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
+// starts: S_1, N_1, .. of one chain, trans: M_1, .., step values apart.
+__device__ __forceinline__ void join_chain(float *starts, const float *trans, size_t step, int last, float *ms,
+                                           float *ss) {
+    if (last < 2) return;
+    fetch_mat(ms, trans);
+    // rows k0 + kJoinStep i and columns v .. v + 3 of a thread
+    const int v = threadIdx.x % (kJoinCols / 4) * 4, k0 = threadIdx.x / (kJoinCols / 4);
+    starts += v;
+    ss += v;
+#pragma unroll
+    for (int i = 0; i < kJoinRows; ++i)
+        *reinterpret_cast<float4 *>(ss + (k0 + kJoinStep * i) * kJoinCols) =
+            *reinterpret_cast<const float4 *>(starts + (k0 + kJoinStep * i) * kHeadDim);
+    float4 acc[kJoinRows];
+    auto fetch_n = [&](int g) {
+#pragma unroll
+        for (int i = 0; i < kJoinRows; ++i)
+            acc[i] = *reinterpret_cast<const float4 *>(starts + g * step + (k0 + kJoinStep * i) * kHeadDim);
+    };
+    float4 sum[kJoinRows];
+    fetch_n(1);
+    for (int g = 1; g < last; ++g) {
+        const float *m = ms + ((g - 1) & 1) * kHeadDim * kJoinPitch + k0 * kJoinPitch;
+        const float *s = ss + ((g - 1) & 1) * kHeadDim * kJoinCols;
+        float *next = starts + g * step;
+#pragma unroll
+        for (int i = 0; i < kJoinRows; ++i) sum[i] = acc[i];
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();  // M_g and S_g are there, and all are done with the other buffers
+        if (g + 1 < last) {
+            fetch_mat(ms + (g & 1) * kHeadDim * kJoinPitch, trans + g * step);
+            fetch_n(g + 1);
+        }
+#pragma unroll 4
+        for (int j = 0; j < kHeadDim; j += 4) {
+            float4 f[kJoinRows];
+#pragma unroll
+            for (int i = 0; i < kJoinRows; ++i)
+                f[i] = *reinterpret_cast<const float4 *>(m + kJoinStep * i * kJoinPitch + j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 x = *reinterpret_cast<const float4 *>(s + (j + e) * kJoinCols);
+#pragma unroll
+                for (int i = 0; i < kJoinRows; ++i) {
+                    const float y = e == 0 ? f[i].x : e == 1 ? f[i].y : e == 2 ? f[i].z : f[i].w;
+                    sum[i].x = fmaf(y, x.x, sum[i].x);
+                    sum[i].y = fmaf(y, x.y, sum[i].y);
+                    sum[i].z = fmaf(y, x.z, sum[i].z);
+                    sum[i].w = fmaf(y, x.w, sum[i].w);
+                }
+            }
+        }
+        float *keep = ss + (g & 1) * kHeadDim * kJoinCols;
+#pragma unroll
+        for (int i = 0; i < kJoinRows; ++i) {
+            *reinterpret_cast<float4 *>(keep + (k0 + kJoinStep * i) * kJoinCols) = sum[i];
+            *reinterpret_cast<float4 *>(next + (k0 + kJoinStep * i) * kHeadDim) = sum[i];
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kJoinThreads)
     delta_join_kernel(const DeltaParams p, const Split split) {
     extern __shared__ __align__(16) float join_smem[];
@@ -1378,57 +1600,24 @@ __global__ void __launch_bounds__(kJoinThreads)
     pdl_wait();
     pdl_trigger();
     constexpr int kParts = kHeadDim / kJoinCols;
-    const int chain = (int)blockIdx.x / kParts, v0 = (int)blockIdx.x % kParts * kJoinCols;
-    const int b = chain / p.H;
-    const int n = p.cu_seqlens[b + 1] - p.cu_seqlens[b];
-    if (p.cu_seqlens[b] < 0 || n <= 0 || p.cu_seqlens[b + 1] > p.T || n > p.max_seqlen) return;
-    const int last = split_last(split, (n + C - 1) / C);
-    if (last < 2) return;
-    float *starts = split.starts + (size_t)chain * (split.segs - 1) * kMat + v0;
-    const float *trans = split.trans + (size_t)chain * (split.segs - 2) * kMat;
-    fetch_mat(ms, trans);
-    // rows k0 + 32 i and columns v .. v + 3 of a thread
-    const int v = threadIdx.x % (kJoinCols / 4) * 4, k0 = threadIdx.x / (kJoinCols / 4);
-    starts += v;
-    ss += v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<float4 *>(ss + (k0 + 32 * i) * kJoinCols) =
-            *reinterpret_cast<const float4 *>(starts + (k0 + 32 * i) * kHeadDim);
-    for (int g = 1; g < last; ++g) {
-        const float *m = ms + ((g - 1) & 1) * kHeadDim * kJoinPitch + k0 * kJoinPitch;
-        const float *s = ss + ((g - 1) & 1) * kHeadDim * kJoinCols;
-        float *next = starts + g * kMat;
-        float4 acc[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = *reinterpret_cast<const float4 *>(next + (k0 + 32 * i) * kHeadDim);
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncthreads();  // M_g and S_g are there, and all are done with the other buffers
-        if (g + 1 < last) fetch_mat(ms + (g & 1) * kHeadDim * kJoinPitch, trans + g * kMat);
-#pragma unroll 4
-        for (int j = 0; j < kHeadDim; j += 4) {
-            float4 f[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = *reinterpret_cast<const float4 *>(m + 32 * i * kJoinPitch + j);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float4 x = *reinterpret_cast<const float4 *>(s + (j + e) * kJoinCols);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float y = e == 0 ? f[i].x : e == 1 ? f[i].y : e == 2 ? f[i].z : f[i].w;
-                    acc[i].x = fmaf(y, x.x, acc[i].x);
-                    acc[i].y = fmaf(y, x.y, acc[i].y);
-                    acc[i].z = fmaf(y, x.z, acc[i].z);
-                    acc[i].w = fmaf(y, x.w, acc[i].w);
-                }
-            }
+    const int32_t *plan = split.plan;
+    const int all = (plan ? plan[kPlanJoins] : p.B) * p.H * kParts;
+    for (int x = blockIdx.x; x < all; x += gridDim.x) {
+        const int chain = x / kParts, v0 = x % kParts * kJoinCols;
+        const int h = chain % p.H, b = plan ? plan[kPlanJoin + chain / p.H] : chain / p.H;
+        const int t0 = p.cu_seqlens[b], t1 = p.cu_seqlens[b + 1];
+        if (!request_ok(p, t0, t1)) continue;
+        const int nchunks = (t1 - t0 + C - 1) / C;
+        if (plan) {
+            join_chain(split.starts + ((size_t)plan[kPlanS + b] * p.H + h) * kMat + v0,
+                       split.starts + ((size_t)(plan[kPlanStarts] + plan[kPlanT + b]) * p.H + h) * kMat,
+                       p.H * kMat, segments_after(nchunks, plan[kPlanA], plan[kPlanB]), ms, ss);
+        } else {
+            join_chain(split.starts + (size_t)chain * (split.segs - 1) * kMat + v0,
+                       split.trans + (size_t)chain * (split.segs - 2) * kMat, kMat, split_last(split, nchunks),
+                       ms, ss);
         }
-        float *keep = ss + (g & 1) * kHeadDim * kJoinCols;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            *reinterpret_cast<float4 *>(keep + (k0 + 32 * i) * kJoinCols) = acc[i];
-            *reinterpret_cast<float4 *>(next + (k0 + 32 * i) * kHeadDim) = acc[i];
-        }
+        __syncthreads();  // the buffers are free
     }
 }
 
@@ -1442,13 +1631,13 @@ unsigned long long split_mats(long long chains, long long chunks) {
 // short chains one after another beside a segment 0, then a segment of pass 2, and what the join and its
 // launches cost.
 Split plan_split(long long chains, long long chunks) {
-    Split s{1, 1, 0, nullptr, nullptr};
+    Split s{1, 1, 0, nullptr, nullptr, nullptr};
     if (split_mats(chains, chunks) == 0) return s;
     double best = kSplitGain * (double)chunks;
     for (int ratio = 1; ratio <= 2; ++ratio)
         for (int segs = 3; segs <= kMaxSegs && (segs - 1) * chains <= kSplitSMs; ++segs) {
             if (2 * (segs - 2) * chains > ratio * (kSplitSMs - chains)) continue;
-            const Split t{segs, ratio, 1, nullptr, nullptr};
+            const Split t{segs, ratio, 1, nullptr, nullptr, nullptr};
             const double cost = (ratio + 1) * split_base(t, (int)chunks) + kSplitCost + kJoinCost * segs;
             if (cost < best) {
                 best = cost;
@@ -1457,20 +1646,31 @@ Split plan_split(long long chains, long long chunks) {
         }
     return s;
 }
+// Whether a batch gets a plan: more chains than a split takes, and a longest request (of `longest` chunks) of
+// at least twice the SMs' even share of all chunks, 8 added to it.  At 16 heads, without / with, us: 16,384
+// tokens among 63 x 256: 707 / 426; 8192, 4096, 6 x 500: 352 / 227; 4096 among 7 x 1024 (2.4 times): 193 / 169,
+// among 7 x 1536 (2.0): 204 / 201; eight of 512-4096 (1.7): 218 / 212 and 218 / 229; twelve of 256-4096 (1.1):
+// 221 / 232.
+bool planned(long long B, long long H, long long chunks, long long longest) {
+    return 2 * B * H > kSplitSMs && B >= 2 && B <= kMaxPlanned && H <= kPlanMats && longest >= kSplitMinChunks &&
+           longest * kSplitSMs >= 2 * (H * chunks + 8 * kSplitSMs);
+}
 // Bytes of the slots, of the order, of a split's matrices.
 unsigned long long slots_bytes(long long B, long long T, long long H) {
     return ((unsigned long long)chunk_slots(T, B) * (unsigned long long)H * SZ_SLOT);
 }
 unsigned long long order_bytes(long long B) {
-    return ((unsigned long long)B * sizeof(int32_t) + 15ull) / 16ull * 16ull;
+    return (unsigned long long)order_ints((int)B) * sizeof(int32_t);
 }
 
 }  // namespace
 
 unsigned long long delta_scratch_bytes(long long B, long long T, long long H) {
     if (T <= 0 || B <= 0) return 0ull;
-    return slots_bytes(B, T, H) + order_bytes(B) +
-           split_mats(B * H, (T + C - 1) / C) * (kMat * sizeof(float));
+    const long long chunks = (T + C - 1) / C;
+    const unsigned long long mat = kMat * sizeof(float);
+    return slots_bytes(B, T, H) + order_bytes(B) + split_mats(B * H, chunks) * mat +
+           (planned(B, H, chunks, chunks) ? kPlanBytes + kPlanMats * mat : 0ull);
 }
 
 cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cudaStream_t stream) {
@@ -1497,7 +1697,8 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
         std::lock_guard<std::mutex> lock(mu);
         if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
         if (!configured[dev]) {
-            for (auto *kernel : {delta_extend_kernel<MANY>, delta_extend_kernel<ONE>, delta_extend_kernel<SEGMENT>}) {
+            for (auto *kernel : {delta_extend_kernel<MANY>, delta_extend_kernel<ONE>, delta_extend_kernel<SEGMENT>,
+                                 delta_extend_kernel<PLANNED>}) {
                 e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
                 if (e != cudaSuccess) return e;
             }
@@ -1511,27 +1712,49 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
     }
     uint8_t *w = static_cast<uint8_t *>(ws);
     // One wave needs no order; ranking is B comparisons per request.
-    int32_t *order = nullptr;
+    int32_t *order = nullptr, *plan = nullptr;
     int rank_ctas = 0;
-    if (t_ctas > 0 && p.B > 1 && p.B <= kMaxRanked && ctas > num_sms) {
+    const long long chunks = ((long long)p.T + C - 1) / C;
+    const long long longest = ((long long)(p.max_seqlen < p.T ? p.max_seqlen : p.T) + C - 1) / C;
+    if (planned(p.B, p.H, chunks, longest)) {
+        plan = reinterpret_cast<int32_t *>(w + slots_bytes(p.B, p.T, p.H) + order_bytes(p.B));
+        rank_ctas = 1;
+    } else if (t_ctas > 0 && p.B > 1 && p.B <= kMaxRanked && ctas > num_sms) {
         order = reinterpret_cast<int32_t *>(w + slots_bytes(p.B, p.T, p.H));
         rank_ctas = (p.B + kTThreads - 1) / kTThreads;
     }
     if (t_ctas > 0) {
         e = launch_pdl(delta_t_kernel, dim3((unsigned)(rank_ctas + t_ctas)), dim3(kTThreads), kTSmemBytes,
-                       stream, tq, tk, p, w, order, rank_ctas);
+                       stream, tq, tk, p, w, order, plan, rank_ctas);
         if (e != cudaSuccess) return e;
     }
-    Split split = plan_split(ctas, ((long long)(p.max_seqlen < p.T ? p.max_seqlen : p.T) + C - 1) / C);
+    Split split = plan_split(ctas, longest);
+    if (plan) {
+        split.plan = plan;
+        split.starts = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(plan) + kPlanBytes);
+        for (split.pass = 1; split.pass <= 2; ++split.pass) {
+            if (split.pass == 2) {
+                e = launch_pdl(delta_join_kernel, dim3((unsigned)num_sms), dim3(kJoinThreads), kJoinSmem,
+                               stream, p, split);
+                if (e != cudaSuccess) return e;
+            }
+            e = launch_pdl(delta_extend_kernel<PLANNED>, dim3((unsigned)num_sms), dim3(kThreads), kSmemBytes,
+                           stream, tq, tk, tv, p, (const uint8_t *)w, (const int32_t *)nullptr, split,
+                           plan + (split.pass == 2 ? kPlanTaken2 : kPlanTaken1), 0);
+            if (e != cudaSuccess) return e;
+        }
+        return cudaSuccess;
+    }
     if (split.pass == 0)
         return launch_pdl(ctas > num_sms ? delta_extend_kernel<MANY> : delta_extend_kernel<ONE>,
                           dim3((unsigned)(ctas < num_sms ? ctas : num_sms)), dim3(kThreads), kSmemBytes,
-                          stream, tq, tk, tv, p, (const uint8_t *)w, (const int32_t *)order, split, (int)ctas);
+                          stream, tq, tk, tv, p, (const uint8_t *)w, (const int32_t *)order, split,
+                          order ? order + order_ints(p.B) - 1 : (int32_t *)nullptr, (int)ctas);
     split.starts = reinterpret_cast<float *>(w + slots_bytes(p.B, p.T, p.H) + order_bytes(p.B));
     split.trans = split.starts + (size_t)ctas * (split.segs - 1) * kMat;
     e = launch_pdl(delta_extend_kernel<SEGMENT>, dim3((unsigned)(ctas * (2 * split.segs - 3))), dim3(kThreads),
                    kSmemBytes, stream, tq, tk, tv, p, (const uint8_t *)w, (const int32_t *)order, split,
-                   (int)(ctas * (2 * split.segs - 3)));
+                   (int32_t *)nullptr, (int)(ctas * (2 * split.segs - 3)));
     if (e != cudaSuccess) return e;
     e = launch_pdl(delta_join_kernel, dim3((unsigned)(ctas * (kHeadDim / kJoinCols))), dim3(kJoinThreads),
                    kJoinSmem, stream, p, split);
@@ -1539,7 +1762,7 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
     split.pass = 2;
     return launch_pdl(delta_extend_kernel<SEGMENT>, dim3((unsigned)(ctas * (split.segs - 1))), dim3(kThreads),
                       kSmemBytes, stream, tq, tk, tv, p, (const uint8_t *)w, (const int32_t *)order, split,
-                      (int)(ctas * (split.segs - 1)));
+                      (int32_t *)nullptr, (int)(ctas * (split.segs - 1)));
 }
 
 }  // namespace la

@@ -30,7 +30,8 @@ def _mask(n, value=0):
 
 
 @pytest.mark.parametrize("lens,H,must", [([1000, 300], 2, True), ([3000], 2, True),
-                                          ([700] * 80, 2, True), ([40] * 100, 2, False)])
+                                          ([700] * 80, 2, True), ([40] * 100, 2, False),
+                                          ([3000] + [64] * 40, 2, True)])
 def test_waits_that_run_out(lens, H, must):
     """Calls under a 1 us wait limit are reported as LA_ERR_TIMEOUT; the next call is as ever.  A try
     of a wait may itself be suspended for a few microseconds, so that the waits of a request of one
@@ -228,6 +229,51 @@ def test_large_batches(B):
         check_out(f64(out[x]), o, d[0][x], np.broadcast_to(norms, (lens[b], H)), TOL_EXTEND, 1, H, True, str(b))
         check_states(f64(pool[b]), S, TOL_EXTEND, str(b))
     assert torch.isfinite(pool).all() and torch.isfinite(out).all()
+
+
+def test_faults_in_a_planned_batch():
+    """A long request among many short ones; some with a slot out of range or longer than max_seqlen
+    are skipped and reported, and the others are as without them."""
+    lens, H = [64] * 39 + [2400] + [100] * 10, 2
+    B = len(lens)
+    d = _to(*inputs(sum(lens), 1, H, 42))
+    slots = list(range(B))
+    want = []
+    for bad, most in (([], 2400), ([0, 39, 45], 2400), ([], 2399)):
+        pool = torch.full((B, H, D, D), 0.01, device=DEV)
+        out = torch.full((sum(lens), H * D), 7.0, dtype=torch.bfloat16, device=DEV)
+        la.delta_extend(*d, pool, _i32([B if b in bad else slots[b] for b in range(B)]), _cu(lens),
+                        _mask(B, 1), out=out, max_seqlen=most, qk_l2norm=True)
+        skipped = bad if most == 2400 else [39]
+        if skipped:
+            with pytest.raises(la.LAError) as e:
+                la.poll_error()
+            assert e.value.status == 5
+        la.poll_error()
+        if not want:
+            want = [out, pool]
+        cu = np.cumsum([0] + lens)
+        for b in range(B):
+            r = slice(int(cu[b]), int(cu[b + 1]))
+            if b in skipped:
+                assert (out[r] == 7.0).all() and (pool[b] == 0.01).all()
+            elif lens[b] < 1000 or most == 2400:
+                same = torch.equal(out[r], want[0][r]) and torch.equal(pool[b], want[1][b])
+                assert same, f"request {b}, bad {bad}"
+
+
+def test_planned_calls_are_bit_equal():
+    lens, H = [33] * 60 + [1900, 2300], 2
+    B = len(lens)
+    d = _to(*inputs(sum(lens), 1, H, 43))
+    got = []
+    for _ in range(3):
+        pool = torch.zeros(B, H, D, D, device=DEV)
+        got.append((la.delta_extend(*d, pool, _i32(list(range(B))), _cu(lens), _mask(B), max_seqlen=2300,
+                                    qk_l2norm=True), pool))
+    la.poll_error()
+    for o, p in got[1:]:
+        assert torch.equal(o, got[0][0]) and torch.equal(p, got[0][1])
 
 
 def test_nan_gates_stay_within_their_request():
