@@ -375,15 +375,15 @@ la_status la_commit_accepted(const float *inter_states, const int32_t *accept_id
  * max_seqlen, B, T as for la_extend; rows of out that belong to no request are left as they were.
  *   workspace        device scratch, 16-byte aligned, of at least la_delta_extend_workspace_size()
  *                    bytes (LA_ERR_INVALID otherwise; may be NULL when T = 0): 21,520 bytes per value
- *                    head and 64 tokens (a third of what q, k, v and out take at Hk = H), and from 1,217
- *                    tokens on up to 20 MB more where B * H <= 76, 34 MB more where it is above and B
- *                    at most 512.  Contents do not matter on entry and are garbage on exit; calls that
+ *                    head and 64 tokens (a third of what q, k, v and out take at Hk = H), and up to
+ *                    20 MB more where B * H <= 76 (from 1,217 tokens on), 34 MB more where it is above
+ *                    and B at most 128 (from 1,985).  Contents do not matter on entry and are garbage on exit; calls that
  *                    share one must not overlap on the GPU.
  * A first launch forms, for every chunk of 64 tokens at once, what depends on no state; a second runs the
  * chunks of each (request, head) in turn.  Long requests run as segments side by side, in four launches,
- * with the same results up to rounding: where B * H <= 76 from about 1,300 tokens at B * H = 8 and from about
- * 2,600 at 76, and above that where max_seqlen is far longer than the SMs' share of T * H.  Both go by
- * max_seqlen (or T, if that is less), so pass it no larger than it is.
+ * with the same results up to rounding: where B * H <= 76 from about 1,300 tokens at B * H = 8 and from
+ * about 2,600 at 76, and above that (B <= 128) where max_seqlen is far longer than the SMs' share of T * H.
+ * Both go by max_seqlen (or T, if that is less), so pass it no larger than it is.
  * A call in which cu_seqlens decreases somewhere skips the requests concerned and reports them, but the
  * results of its other requests are then unspecified too.  Numerics: bf16 products with fp32 accumulation; each
  * operand the kernels compute is a bf16 pair hi + lo (off by at most 2^-16); states are kept, updated and

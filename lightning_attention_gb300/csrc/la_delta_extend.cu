@@ -406,6 +406,9 @@ __device__ __forceinline__ void scale_block(const TokenFactors &f, int a, int b,
 // Measured whole / split, us, T kernel included, l2norm, one request: 8 heads: 1,024 tokens 47.5 / 45.8,
 // 2,048: 84.6 / 66.5, 16,384: 626 / 199; 32 heads: 1,024: 52.7 / 61.9, 1,536: 75.3 / 73.7, 16,384:
 // 703 / 438; 76 heads: 2,560: 145 / 149, 4,096: 222 / 212, 16,384: 836 / 720.
+constexpr int kMaxSegs = 16;
+constexpr int kSplitSMs = 152;       // chains that run side by side
+constexpr int kSplitMinChunks = 20;  // shorter requests are not split
 struct Split {
     int segs, ratio;
     int pass;       // 0: not split
@@ -413,16 +416,15 @@ struct Split {
     float *trans;   // [chains][segs - 2][D][D]: M_g at g - 1
     const int32_t *plan;  // PLANNED: what follows; starts holds all of the plan's matrices
 };
-constexpr int kMaxSegs = 16;
-constexpr int kSplitSMs = 152;       // chains that run side by side
-constexpr int kSplitMinChunks = 20;  // shorter requests are not split
 // What the join and two more launches cost, and a segment in the join, in chunks of the chain.
 constexpr double kSplitCost = 5., kJoinCost = 1.;
 constexpr float kItemCost = 1.2f;  // of an item beside its chunks, in chunks
 constexpr double kSplitGain = .95;  // a split has to promise this much
 constexpr size_t kMat = (size_t)kHeadDim * kHeadDim;
-// Chunks of segments 1, 2 ..; the last segment that has any.
+// Chunks of segments 1, 2 ..; the last segment that has any.  A short request beside long ones (or under a
+// max_seqlen that none comes near) stays whole.
 __host__ __device__ inline int split_base(const Split &s, int nchunks) {
+    if (nchunks < kSplitMinChunks) return nchunks;
     return (nchunks + s.ratio + s.segs - 2) / (s.ratio + s.segs - 1);
 }
 __host__ __device__ inline int split_last(const Split &s, int nchunks) {
@@ -446,7 +448,11 @@ __device__ __forceinline__ Job split_job(const DeltaParams &p, const Split &s) {
 // segment 0 is a request's first a chunks, the next are b chunks each, so that short requests end in pass 1 as
 // they are.  A CTA of the first kernel tries 128 pairs (a, b) and lists the segments of both passes longest
 // first; an entry stands for its request's H heads.
-constexpr int kMaxPlanned = 512;  // requests
+// Requests: planning is a pass over all of them per pair, which 512 short ones made 50 us longer than T takes.
+constexpr int kMaxPlanned = 128;
+// Longest request: one of 1500 tokens among 127 of 64, 4 heads, takes 83 us with a plan and 76 without; of 2000
+// 78 and 93.
+constexpr int kPlanMinChunks = 32;
 constexpr int kPlanMats = 512;    // matrices (start states and transitions, all heads)
 constexpr int kPlanA = 0, kPlanB = 1, kPlanFirst = 2, kPlanSecond = 3, kPlanJoins = 4, kPlanStarts = 5;
 constexpr int kPlanTaken1 = 6, kPlanTaken2 = 7;  // items taken in a pass, beyond each CTA's first
@@ -1652,7 +1658,7 @@ Split plan_split(long long chains, long long chunks) {
 // among 7 x 1536 (2.0): 204 / 201; eight of 512-4096 (1.7): 218 / 212 and 218 / 229; twelve of 256-4096 (1.1):
 // 221 / 232.
 bool planned(long long B, long long H, long long chunks, long long longest) {
-    return 2 * B * H > kSplitSMs && B >= 2 && B <= kMaxPlanned && H <= kPlanMats && longest >= kSplitMinChunks &&
+    return 2 * B * H > kSplitSMs && B >= 2 && B <= kMaxPlanned && H <= kPlanMats && longest >= kPlanMinChunks &&
            longest * kSplitSMs >= 2 * (H * chunks + 8 * kSplitSMs);
 }
 // Bytes of the slots, of the order, of a split's matrices.

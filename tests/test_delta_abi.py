@@ -114,10 +114,10 @@ def test_workspace_size(lib):
     assert la.delta_extend_workspace_size(2, 1216, 4, 128) == slots(2, 1216, 4)
     assert la.delta_extend_workspace_size(2, 8192, 4, 128) == slots(2, 8192, 4) + 8 * 29 * 65536
     assert la.delta_extend_workspace_size(2, 8192, 38, 128) == slots(2, 8192, 38) + 304 * 65536
-    # a plan for up to 512 requests of which one may be far longer than the others
-    assert la.delta_extend_workspace_size(7, 8192, 11, 128) == slots(7, 8192, 11) + 12352 + 512 * 65536
-    assert la.delta_extend_workspace_size(7, 1216, 11, 128) == slots(7, 1216, 11)
-    assert la.delta_extend_workspace_size(513, 8192, 11, 128) == slots(513, 8192, 11)
+    # a plan for up to 128 requests of which one may be far longer than the others
+    assert la.delta_extend_workspace_size(7, 8192, 11, 128) == slots(7, 8192, 11) + 6208 + 512 * 65536
+    assert la.delta_extend_workspace_size(7, 1984, 11, 128) == slots(7, 1984, 11)
+    assert la.delta_extend_workspace_size(129, 8192, 11, 128) == slots(129, 8192, 11)
     assert la.delta_extend_workspace_size(7, 8192, 512, 128) == slots(7, 8192, 512)
     # more (chunk, head) pairs than a grid has CTAs
     assert size(1, 2 ** 31 - 1, 65, 128, ctypes.byref(nb)) == 2

@@ -124,6 +124,7 @@ def test_extend_many_requests():
     ([40, 2300], 1, 3, False, "none", 1 << 30),
     ([2111], 5, 20, True, "reset", None),  # segment 0 twice as long as the others
     ([900, 700], 1, 1, True, "model", 2100),  # taken as long, and every request is shorter
+    ([1300, 900, 1279], 1, 2, True, "model", 3400),
     # one cut for all requests, planned on the device: one long among short ones, two, a mixed batch,
     # none that is worth a cut, one in very many
     ([41] * 20 + [3000] + [64, 0, 1] * 7, 1, 2, True, "model", None),
@@ -131,7 +132,8 @@ def test_extend_many_requests():
     ([1500, 3, 0, 200, 700, 1400], 4, 16, True, "model", None),
     ([64, 0, 2500, 100, 65, 40], 4, 16, True, "model", None),
     ([100] * 77, 1, 1, True, "reset", 7700),
-    ([17] * 300 + [2000] + [9] * 211, 1, 1, True, "model", None),
+    ([17] * 60 + [2000] + [9] * 67, 1, 1, True, "model", None),
+    ([17] * 300 + [2000] + [9] * 211, 1, 1, True, "model", None),  # too many for a plan
 ])
 def test_extend_split(lens, Hk, H, l2, gate, max_seqlen):
     """Few long requests: the chain in segments.  A state is M S + N, with M and N each within the
