@@ -361,7 +361,8 @@ la_status la_commit_accepted(const float *inter_states, const int32_t *accept_id
  *   state_pool    device, fp32 [num_slots][H][D][D]
  *   out           device, bf16 [tokens][H*D], packed
  *   H, Hk         value heads and key heads; H must be a multiple of Hk (LA_ERR_INVALID otherwise)
- *   qk_l2norm     nonzero: q and k are first divided by sqrt(sum of squares of the head + 1e-6)
+ *   qk_l2norm     nonzero: q and k are first divided by sqrt(sum of squares of the head + 1e-6); the
+ *                 products are formed before the division, in fp32, so norms up to about 1e18 fit
  * A positive g or keys with beta |k|^2 > 2 let a state grow without bound, as the formula says;
  * nothing is clamped, and what overflows fp32 may leave NaN anywhere in that request.  All other
  * conventions (alignment, preconditions, device-detected faults, B = 0) are the ones at the top of this

@@ -301,6 +301,32 @@ def test_nan_gates_stay_within_their_request():
     assert torch.isfinite(o[0]).all() and o[1].isnan().all() and torch.isfinite(pool[0]).all()
 
 
+@pytest.mark.parametrize("lens,bad", [([70] * 120, range(0, 120, 3)), ([64] * 30 + [2600] + [90] * 30, [30, 7]),
+                                      ([2600, 130], [0])])
+def test_nan_requests_among_others(lens, bad):
+    """Many waves, a planned batch and a split one: requests full of NaN leave the others bit for bit."""
+    H, B = 2, len(lens)
+    cu = np.cumsum([0] + lens)
+    outs, pools = [], []
+    for poison in (False, True):
+        d = inputs(sum(lens), 1, H, 44)
+        if poison:
+            for b in bad:
+                for x in d:
+                    x[cu[b]:cu[b + 1]] = float("nan")
+        pool = torch.full((B, H, D, D), 0.02, device=DEV)
+        outs.append(la.delta_extend(*_to(*d), pool, _i32(list(range(B))), _cu(lens), _mask(B, 1),
+                                    max_seqlen=max(lens), qk_l2norm=True))
+        pools.append(pool)
+    la.poll_error()
+    for b in range(B):
+        r = slice(int(cu[b]), int(cu[b + 1]))
+        if b in bad:
+            assert outs[1][r].isnan().all() and pools[1][b].isnan().all()
+        else:
+            assert torch.equal(outs[0][r], outs[1][r]) and torch.equal(pools[0][b], pools[1][b]), b
+
+
 def test_keys_nearly_the_same():
     """Keys within 8 degrees of one another, beta near 1, no decay: every token rewrites what the last
     one wrote.  A chunk's errors of u = v - S^T k then add up along one direction: 64 tokens, each of
