@@ -380,8 +380,9 @@ la_status la_commit_accepted(const float *inter_states, const int32_t *accept_id
  *                    20 MB more where B * H <= 76 (from 1,217 tokens on), 34 MB more where it is above
  *                    and B at most 128 (from 1,985).  Contents do not matter on entry and are garbage on exit; calls that
  *                    share one must not overlap on the GPU.
- * A first launch forms, for every chunk of 64 tokens at once, what depends on no state; a second runs the
- * chunks of each (request, head) in turn.  Long requests run as segments side by side, in four launches,
+ * Where max_seqlen (T, if that is less) is at most 6 the tokens are taken one by one, in fp32, in one
+ * launch.  Otherwise a first launch forms, for every chunk of 64 tokens at once, what depends on no
+ * state, and a second runs the chunks of each (request, head) in turn.  Long requests run as segments side by side, in four launches,
  * with the same results up to rounding: where B * H <= 76 from about 1,300 tokens at B * H = 8 and from
  * about 2,600 at 76, and above that (B <= 128) where max_seqlen is far longer than the SMs' share of T * H.
  * Both go by max_seqlen (or T, if that is less), so pass it no larger than it is.

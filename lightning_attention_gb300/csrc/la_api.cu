@@ -648,6 +648,10 @@ la_status la_delta_extend(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, 
     p.max_seqlen = max_seqlen;
     int sms = 0;
     if ((st = error_word_ptr(&p.err)) != LA_OK || (st = num_sms(&sms)) != LA_OK) return st;
+    // a few tokens a request: token by token, without chunks
+    if (std::min(max_seqlen, T) <= la::kSerialTokens)
+        return launch_status(la::launch_delta_recurrent(la::DELTA_SERIAL, p, sms,
+                                                        static_cast<cudaStream_t>(stream)));
     return launch_status(la::launch_delta_extend(p, workspace, sms, static_cast<cudaStream_t>(stream)));
 }
 

@@ -1,4 +1,4 @@
-// la_delta.cu -- token-serial gated delta rule: one-token decode, chain verify.
+// la_delta.cu -- token-serial gated delta rule: one-token decode, chain verify, extend of a few tokens.
 //
 // Per request and value head h, with key head h / (H / Hk), from the state S (rows: k, columns: v):
 //   S <- e^{g} S;  u = beta (v - S^T k);  S <- S + k u^T;  o = D^-0.5 S^T q.
@@ -94,13 +94,34 @@ __global__ void __launch_bounds__(kThreads, 2) delta_recurrent_kernel(const Delt
     }
     constexpr size_t kMat = (size_t)kHeadDim * kHeadDim;
     float *state = p.pool + ((size_t)slot * H + h) * kMat + (size_t)row0 * kHeadDim + col;
+    int n = MODE == DELTA_DECODE ? 1 : p.N;
+    size_t t_begin = (size_t)b * n;
+    bool prefix = true;
+    if (MODE == DELTA_SERIAL) {
+        const int t0 = p.cu_seqlens[b], t1 = p.cu_seqlens[b + 1];
+        if (t0 < 0 || t1 < t0 || t1 > p.T || t1 - t0 > p.max_seqlen) {
+            if (threadIdx.x == 0) atomicOr(p.err, ERR_BIT_SEQLENS);
+            return;
+        }
+        n = t1 - t0;
+        t_begin = (size_t)t0;
+        prefix = p.prefix_mask[b] != 0;
+        if (n == 0 && prefix) return;
+    }
     float4 s[kRows];
+    if (prefix) {
 #pragma unroll
-    for (int r = 0; r < kRows; ++r)
-        s[r] = __ldcs(reinterpret_cast<const float4 *>(state + (size_t)r * kHeadDim));
-
-    const int n = MODE == DELTA_DECODE ? 1 : p.N;
-    const size_t t_begin = (size_t)b * n;
+        for (int r = 0; r < kRows; ++r)
+            s[r] = __ldcs(reinterpret_cast<const float4 *>(state + (size_t)r * kHeadDim));
+    } else {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) s[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (MODE == DELTA_SERIAL && n == 0) {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) __stcs(reinterpret_cast<float4 *>(state + (size_t)r * kHeadDim), s[r]);
+        return;
+    }
     const __nv_bfloat16 *kp = p.k + t_begin * p.k_rs + (size_t)(h / p.group) * kHeadDim + row0;
     const __nv_bfloat16 *qp = p.q + t_begin * p.q_rs + (size_t)(h / p.group) * kHeadDim + row0;
     const __nv_bfloat16 *vp = p.v + t_begin * p.v_rs + (size_t)h * kHeadDim + col;
@@ -144,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 2) delta_recurrent_kernel(const Delt
         RowVec<kRows> kn, qn;
         RowVec<4> vn;
         float gn = 0.f, bn = 0.f;
-        if (MODE == DELTA_VERIFY && t + 1 < n) {
+        if (MODE != DELTA_DECODE && t + 1 < n) {
             const size_t next = (size_t)(t + 1);
             kn.load(kp + next * p.k_rs);
             qn.load(qp + next * p.q_rs);
@@ -178,7 +199,8 @@ __global__ void __launch_bounds__(kThreads, 2) delta_recurrent_kernel(const Delt
             s[r].y = fmaf(kr, u.y, s[r].y * decay);
             s[r].z = fmaf(kr, u.z, s[r].z * decay);
             s[r].w = fmaf(kr, u.w, s[r].w * decay);
-            __stcs(reinterpret_cast<float4 *>(dst + (size_t)r * kHeadDim), s[r]);
+            if (MODE != DELTA_SERIAL || t + 1 == n)
+                __stcs(reinterpret_cast<float4 *>(dst + (size_t)r * kHeadDim), s[r]);
         }
         if (threadIdx.x < kLanesPerRow) {
             float4 so = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -195,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 2) delta_recurrent_kernel(const Delt
             w2.y = *reinterpret_cast<const uint32_t *>(&hi);
             *reinterpret_cast<uint2 *>(p.out + ((t_begin + t) * H + h) * kHeadDim + col) = w2;
         }
-        if (MODE == DELTA_VERIFY) {
+        if (MODE != DELTA_DECODE) {
             kf = kn;
             qf = qn;
             vf = vn;
@@ -227,6 +249,7 @@ cudaError_t launch_delta_recurrent(DeltaMode mode, const DeltaParams &p, int num
     switch (mode) {
         case DELTA_DECODE: return launch_mode<DELTA_DECODE>(p, num_sms, stream);
         case DELTA_VERIFY: return launch_mode<DELTA_VERIFY>(p, num_sms, stream);
+        case DELTA_SERIAL: return launch_mode<DELTA_SERIAL>(p, num_sms, stream);
     }
     return cudaErrorInvalidValue;
 }

@@ -25,8 +25,13 @@ struct DeltaParams {
 };
 constexpr float kDeltaEps = 1e-6f;
 
-enum DeltaMode : int { DELTA_DECODE = 0, DELTA_VERIFY = 1 };
-// Token-serial kernels: the state stays in registers from the first token to the last.
+enum DeltaMode : int { DELTA_DECODE = 0, DELTA_VERIFY = 1, DELTA_SERIAL = 2 };
+// Token-serial kernels: the state stays in registers from the first token to the last.  DELTA_SERIAL: an
+// extend of at most kSerialTokens tokens a request.  Token by token / by chunks, us, every request of n tokens
+// with a prefix state: 8 (request, head) pairs n = 1: 2.8 / 12.9, 4: 4.9 / 12.8, 8: 7.9 / 12.8, 12: 10.9 /
+// 12.9, 16: 13.8 / 12.8; 256 pairs n = 8: 20 / 26, 12: 27 / 26; 4,096 pairs n = 1: 86 / 198, 4: 150 / 199,
+// 8: 242 / 201.
+constexpr int kSerialTokens = 6;
 cudaError_t launch_delta_recurrent(DeltaMode mode, const DeltaParams &p, int num_sms,
                                    cudaStream_t stream);
 

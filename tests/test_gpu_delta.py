@@ -62,6 +62,14 @@ def test_extend_lengths(n, prefix):
     check_extend([n], 1, 1, prefix=[prefix], seed=n)
 
 
+@pytest.mark.parametrize("lens", [[1, 2, 0, 3], [6, 5], [1] * 40, [6] * 170])
+@pytest.mark.parametrize("max_seqlen", [None, 64])
+def test_extend_few_tokens(lens, max_seqlen):
+    # token by token, and by chunks where max_seqlen allows for more
+    check_extend(lens, 1, 2, max_seqlen=max_seqlen, seed=len(lens), gap=2, tail=70)
+    check_extend(lens, 2, 2, l2=False, gate="reset", max_seqlen=max_seqlen, seed=len(lens))
+
+
 @pytest.mark.parametrize("Hk,H", [(1, 1), (1, 3), (2, 4), (4, 4), (3, 6)])
 @pytest.mark.parametrize("l2", [True, False])
 def test_extend_heads(Hk, H, l2):
@@ -261,7 +269,9 @@ def test_device_faults_are_reported_and_skipped():
     i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
     for idx, cu, ms in ((i32(0, 4), i32(0, 10, 30), 30), (i32(-1, 2), i32(0, 10, 30), 30),
                         (i32(0, 1), i32(0, 31, 30), 31), (i32(0, 1), i32(0, 10, 31), 30),
-                        (i32(0, 1), i32(0, 10, 30), 19)):
+                        (i32(0, 1), i32(0, 10, 30), 19),
+                        (i32(0, 4), i32(0, 3, 6), 3), (i32(0, 1), i32(0, 3, 2), 3),
+                        (i32(0, 1), i32(0, 2, 6), 3), (i32(0, 1), i32(28, 30, 31), 3)):
         la.delta_extend(q, k, v, g, beta, pool, idx, cu, one, max_seqlen=ms, qk_l2norm=True)
         with pytest.raises(la.LAError) as e:
             la.poll_error()
