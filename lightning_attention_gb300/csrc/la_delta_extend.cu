@@ -581,11 +581,14 @@ __device__ void rank_requests(const DeltaParams &p, int block, int32_t *order, i
 
 // T', P T and the coefficients of one chunk and head (blockIdx.x = rank_ctas + slot * H + head); the first
 // rank_ctas CTAs order the requests for the chain kernel, or plan its segments.  Warp w has the 16 rows 16 w ..
-// of everything: the 16 x 16 blocks of K K^T and Q K^T (mma.sync: a block is too small for tcgen05), the inverse of its diagonal
-// block of I + A by substitution, a lane per column, then the blocks below by T_ab = -T_aa sum A_am T_mb.
+// of everything: the 16 x 16 blocks of K K^T and Q K^T (mma.sync: a block is too small for tcgen05), the inverse
+// of its diagonal block of I + A by substitution, a lane per column, then the blocks below by T_ab = -T_aa
+// sum A_am T_mb.
 // Measured: 66 us on 8 requests of 512-4096 tokens x 16 heads, 254 us on 256 of 32-512; 40-50 % of DRAM and half
 // of the issue slots.  Bound by the latency of the dependent small products and the barriers between them, at
-// the 20 warps per SM that its 95 registers allow.
+// the 20 warps per SM that its 95 registers allow.  PLAN is a variant of its own, as its code slows the rest down
+// by 4%.
+template <bool PLAN>
 __global__ void __launch_bounds__(kTThreads, 5)
     delta_t_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const DeltaParams p, uint8_t *ws, int32_t *order, int32_t *plan, int rank_ctas) {
@@ -597,7 +600,7 @@ __global__ void __launch_bounds__(kTThreads, 5)
     pdl_wait();
     pdl_trigger();
     if ((int)blockIdx.x < rank_ctas) {
-        if (plan)
+        if (PLAN)
             plan_requests(p, plan, reinterpret_cast<int *>(sm));
         else
             rank_requests(p, blockIdx.x, order, reinterpret_cast<int *>(sm));
@@ -1523,8 +1526,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // The join: a CTA of 256 threads takes kJoinCols columns of one chain's states through all segments.
 // 128 x 128 x kJoinCols fp32 products a segment, 4 x 4 of them a thread, so that a shared-memory load feeds
-// eight; M (64 KB, from L2) and N are fetched one segment ahead.  About 5 us a segment, bound by those loads
-// (512 threads of half as many products each: 6).
+// eight; M is fetched one segment ahead (64 KB, from L2).  About 5 us a segment, bound by the shared-memory
+// loads (512 threads of half as many products each: 6).
 constexpr int kJoinCols = 32, kJoinThreads = 256;
 constexpr int kJoinRows = kHeadDim * kJoinCols / 4 / kJoinThreads;  // of a thread, kJoinStep apart
 constexpr int kJoinStep = kHeadDim / kJoinRows;
@@ -1551,26 +1554,17 @@ __device__ __forceinline__ void join_chain(float *starts, const float *trans, si
     for (int i = 0; i < kJoinRows; ++i)
         *reinterpret_cast<float4 *>(ss + (k0 + kJoinStep * i) * kJoinCols) =
             *reinterpret_cast<const float4 *>(starts + (k0 + kJoinStep * i) * kHeadDim);
-    float4 acc[kJoinRows];
-    auto fetch_n = [&](int g) {
-#pragma unroll
-        for (int i = 0; i < kJoinRows; ++i)
-            acc[i] = *reinterpret_cast<const float4 *>(starts + g * step + (k0 + kJoinStep * i) * kHeadDim);
-    };
-    float4 sum[kJoinRows];
-    fetch_n(1);
     for (int g = 1; g < last; ++g) {
         const float *m = ms + ((g - 1) & 1) * kHeadDim * kJoinPitch + k0 * kJoinPitch;
         const float *s = ss + ((g - 1) & 1) * kHeadDim * kJoinCols;
         float *next = starts + g * step;
+        float4 sum[kJoinRows];
 #pragma unroll
-        for (int i = 0; i < kJoinRows; ++i) sum[i] = acc[i];
+        for (int i = 0; i < kJoinRows; ++i)
+            sum[i] = *reinterpret_cast<const float4 *>(next + (k0 + kJoinStep * i) * kHeadDim);
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();  // M_g and S_g are there, and all are done with the other buffers
-        if (g + 1 < last) {
-            fetch_mat(ms + (g & 1) * kHeadDim * kJoinPitch, trans + g * step);
-            fetch_n(g + 1);
-        }
+        if (g + 1 < last) fetch_mat(ms + (g & 1) * kHeadDim * kJoinPitch, trans + g * step);
 #pragma unroll 4
         for (int j = 0; j < kHeadDim; j += 4) {
             float4 f[kJoinRows];
@@ -1708,8 +1702,10 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
                 e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
                 if (e != cudaSuccess) return e;
             }
-            e = cudaFuncSetAttribute(delta_t_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTSmemBytes);
-            if (e != cudaSuccess) return e;
+            for (auto *kernel : {delta_t_kernel<false>, delta_t_kernel<true>}) {
+                e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTSmemBytes);
+                if (e != cudaSuccess) return e;
+            }
             e = cudaFuncSetAttribute(delta_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      kJoinSmem);
             if (e != cudaSuccess) return e;
@@ -1730,7 +1726,7 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
         rank_ctas = (p.B + kTThreads - 1) / kTThreads;
     }
     if (t_ctas > 0) {
-        e = launch_pdl(delta_t_kernel, dim3((unsigned)(rank_ctas + t_ctas)), dim3(kTThreads), kTSmemBytes,
+        e = launch_pdl(plan ? delta_t_kernel<true> : delta_t_kernel<false>, dim3((unsigned)(rank_ctas + t_ctas)), dim3(kTThreads), kTSmemBytes,
                        stream, tq, tk, p, w, order, plan, rank_ctas);
         if (e != cudaSuccess) return e;
     }
