@@ -1524,17 +1524,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// The join: a CTA of 256 threads takes kJoinCols columns of one chain's states through all segments.
-// 128 x 128 x kJoinCols fp32 products a segment, 4 x 4 of them a thread, so that a shared-memory load feeds
-// eight; M is fetched one segment ahead (64 KB, from L2).  About 5 us a segment, bound by the shared-memory
-// loads (512 threads of half as many products each: 6).
-constexpr int kJoinCols = 32, kJoinThreads = 256;
-constexpr int kJoinRows = kHeadDim * kJoinCols / 4 / kJoinThreads;  // of a thread, kJoinStep apart
-constexpr int kJoinStep = kHeadDim / kJoinRows;
+// The join: a CTA takes COLS columns of one chain's states through all segments, 128 x 128 x COLS fp32 products
+// a segment, 4 x 4 of them a thread (8 COLS threads); M is fetched one segment ahead (64 KB, from L2).  Bound by
+// the latency of its shared-memory loads, so with few chains the columns go to more CTAs, of which an SM holds
+// one: one request of 16,384 tokens with 32 / 16 columns, 8 heads 202 / 190 us, 16 heads 285 / 273, 32 heads
+// (more CTAs than SMs at 16 columns) 445 / 449.
 constexpr int kJoinPitch = kHeadDim + 4;
-constexpr uint32_t kJoinSmem = (2 * kHeadDim * kJoinPitch + 2 * kHeadDim * kJoinCols) * sizeof(float);
+constexpr uint32_t join_smem_bytes(int cols) {
+    return (2 * kHeadDim * kJoinPitch + 2 * kHeadDim * cols) * sizeof(float);
+}
+template <int COLS>
 __device__ __forceinline__ void fetch_mat(float *dst, const float *src) {
-    for (int x = threadIdx.x; x < (int)kMat / 4; x += kJoinThreads)
+    for (int x = threadIdx.x; x < (int)kMat / 4; x += 8 * COLS)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                          smem_u32(dst + (x >> 5) * kJoinPitch + (x & 31) * 4)),
                      "l"(src + 4 * x)
@@ -1542,40 +1543,41 @@ __device__ __forceinline__ void fetch_mat(float *dst, const float *src) {
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
 // starts: S_1, N_1, .. of one chain, trans: M_1, .., step values apart.
+template <int COLS>
 __device__ __forceinline__ void join_chain(float *starts, const float *trans, size_t step, int last, float *ms,
                                            float *ss) {
     if (last < 2) return;
-    fetch_mat(ms, trans);
-    // rows k0 + kJoinStep i and columns v .. v + 3 of a thread
-    const int v = threadIdx.x % (kJoinCols / 4) * 4, k0 = threadIdx.x / (kJoinCols / 4);
+    fetch_mat<COLS>(ms, trans);
+    // rows k0 + 32 i and columns v .. v + 3 of a thread
+    const int v = threadIdx.x % (COLS / 4) * 4, k0 = threadIdx.x / (COLS / 4);
     starts += v;
     ss += v;
 #pragma unroll
-    for (int i = 0; i < kJoinRows; ++i)
-        *reinterpret_cast<float4 *>(ss + (k0 + kJoinStep * i) * kJoinCols) =
-            *reinterpret_cast<const float4 *>(starts + (k0 + kJoinStep * i) * kHeadDim);
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<float4 *>(ss + (k0 + 32 * i) * COLS) =
+            *reinterpret_cast<const float4 *>(starts + (k0 + 32 * i) * kHeadDim);
     for (int g = 1; g < last; ++g) {
         const float *m = ms + ((g - 1) & 1) * kHeadDim * kJoinPitch + k0 * kJoinPitch;
-        const float *s = ss + ((g - 1) & 1) * kHeadDim * kJoinCols;
+        const float *s = ss + ((g - 1) & 1) * kHeadDim * COLS;
         float *next = starts + g * step;
-        float4 sum[kJoinRows];
+        float4 sum[4];
 #pragma unroll
-        for (int i = 0; i < kJoinRows; ++i)
-            sum[i] = *reinterpret_cast<const float4 *>(next + (k0 + kJoinStep * i) * kHeadDim);
+        for (int i = 0; i < 4; ++i)
+            sum[i] = *reinterpret_cast<const float4 *>(next + (k0 + 32 * i) * kHeadDim);
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();  // M_g and S_g are there, and all are done with the other buffers
-        if (g + 1 < last) fetch_mat(ms + (g & 1) * kHeadDim * kJoinPitch, trans + g * step);
+        if (g + 1 < last) fetch_mat<COLS>(ms + (g & 1) * kHeadDim * kJoinPitch, trans + g * step);
 #pragma unroll 4
         for (int j = 0; j < kHeadDim; j += 4) {
-            float4 f[kJoinRows];
+            float4 f[4];
 #pragma unroll
-            for (int i = 0; i < kJoinRows; ++i)
-                f[i] = *reinterpret_cast<const float4 *>(m + kJoinStep * i * kJoinPitch + j);
+            for (int i = 0; i < 4; ++i)
+                f[i] = *reinterpret_cast<const float4 *>(m + 32 * i * kJoinPitch + j);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float4 x = *reinterpret_cast<const float4 *>(s + (j + e) * kJoinCols);
+                const float4 x = *reinterpret_cast<const float4 *>(s + (j + e) * COLS);
 #pragma unroll
-                for (int i = 0; i < kJoinRows; ++i) {
+                for (int i = 0; i < 4; ++i) {
                     const float y = e == 0 ? f[i].x : e == 1 ? f[i].y : e == 2 ? f[i].z : f[i].w;
                     sum[i].x = fmaf(y, x.x, sum[i].x);
                     sum[i].y = fmaf(y, x.y, sum[i].y);
@@ -1584,36 +1586,37 @@ __device__ __forceinline__ void join_chain(float *starts, const float *trans, si
                 }
             }
         }
-        float *keep = ss + (g & 1) * kHeadDim * kJoinCols;
+        float *keep = ss + (g & 1) * kHeadDim * COLS;
 #pragma unroll
-        for (int i = 0; i < kJoinRows; ++i) {
-            *reinterpret_cast<float4 *>(keep + (k0 + kJoinStep * i) * kJoinCols) = sum[i];
-            *reinterpret_cast<float4 *>(next + (k0 + kJoinStep * i) * kHeadDim) = sum[i];
+        for (int i = 0; i < 4; ++i) {
+            *reinterpret_cast<float4 *>(keep + (k0 + 32 * i) * COLS) = sum[i];
+            *reinterpret_cast<float4 *>(next + (k0 + 32 * i) * kHeadDim) = sum[i];
         }
     }
 }
 
-__global__ void __launch_bounds__(kJoinThreads)
+template <int COLS>
+__global__ void __launch_bounds__(8 * COLS)
     delta_join_kernel(const DeltaParams p, const Split split) {
     extern __shared__ __align__(16) float join_smem[];
     float *ms = join_smem, *ss = join_smem + 2 * kHeadDim * kJoinPitch;
     pdl_wait();
     pdl_trigger();
-    constexpr int kParts = kHeadDim / kJoinCols;
+    constexpr int kParts = kHeadDim / COLS;
     const int32_t *plan = split.plan;
     const int all = (plan ? plan[kPlanJoins] : p.B) * p.H * kParts;
     for (int x = blockIdx.x; x < all; x += gridDim.x) {
-        const int chain = x / kParts, v0 = x % kParts * kJoinCols;
+        const int chain = x / kParts, v0 = x % kParts * COLS;
         const int h = chain % p.H, b = plan ? plan[kPlanJoin + chain / p.H] : chain / p.H;
         const int t0 = p.cu_seqlens[b], t1 = p.cu_seqlens[b + 1];
         if (!request_ok(p, t0, t1)) continue;
         const int nchunks = (t1 - t0 + C - 1) / C;
         if (plan) {
-            join_chain(split.starts + ((size_t)plan[kPlanS + b] * p.H + h) * kMat + v0,
+            join_chain<COLS>(split.starts + ((size_t)plan[kPlanS + b] * p.H + h) * kMat + v0,
                        split.starts + ((size_t)(plan[kPlanStarts] + plan[kPlanT + b]) * p.H + h) * kMat,
                        p.H * kMat, segments_after(nchunks, plan[kPlanA], plan[kPlanB]), ms, ss);
         } else {
-            join_chain(split.starts + (size_t)chain * (split.segs - 1) * kMat + v0,
+            join_chain<COLS>(split.starts + (size_t)chain * (split.segs - 1) * kMat + v0,
                        split.trans + (size_t)chain * (split.segs - 2) * kMat, kMat, split_last(split, nchunks),
                        ms, ss);
         }
@@ -1621,6 +1624,10 @@ __global__ void __launch_bounds__(kJoinThreads)
     }
 }
 
+using JoinKernel = void (*)(const DeltaParams, const Split);
+JoinKernel join_kernel(int cols) {
+    return cols == 8 ? delta_join_kernel<8> : cols == 16 ? delta_join_kernel<16> : delta_join_kernel<32>;
+}
 // Matrices of a split: at most two per chain that runs in pass 2, (segs - 1) chains <= kSplitSMs.
 unsigned long long split_mats(long long chains, long long chunks) {
     if (chunks < kSplitMinChunks || 2 * chains > kSplitSMs) return 0ull;
@@ -1706,9 +1713,11 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
                 e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTSmemBytes);
                 if (e != cudaSuccess) return e;
             }
-            e = cudaFuncSetAttribute(delta_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     kJoinSmem);
-            if (e != cudaSuccess) return e;
+            for (const int cols : {8, 16, 32}) {
+                e = cudaFuncSetAttribute(join_kernel(cols), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)join_smem_bytes(cols));
+                if (e != cudaSuccess) return e;
+            }
             configured[dev] = true;
         }
     }
@@ -1736,7 +1745,7 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
         split.starts = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(plan) + kPlanBytes);
         for (split.pass = 1; split.pass <= 2; ++split.pass) {
             if (split.pass == 2) {
-                e = launch_pdl(delta_join_kernel, dim3((unsigned)num_sms), dim3(kJoinThreads), kJoinSmem,
+                e = launch_pdl(join_kernel(16), dim3((unsigned)num_sms), dim3(8 * 16), join_smem_bytes(16),
                                stream, p, split);
                 if (e != cudaSuccess) return e;
             }
@@ -1758,8 +1767,10 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
                    kSmemBytes, stream, tq, tk, tv, p, (const uint8_t *)w, (const int32_t *)order, split,
                    (int32_t *)nullptr, (int)(ctas * (2 * split.segs - 3)));
     if (e != cudaSuccess) return e;
-    e = launch_pdl(delta_join_kernel, dim3((unsigned)(ctas * (kHeadDim / kJoinCols))), dim3(kJoinThreads),
-                   kJoinSmem, stream, p, split);
+    int cols = 32;
+    while (cols > 8 && ctas * (kHeadDim / cols) * 2 <= num_sms) cols /= 2;
+    e = launch_pdl(join_kernel(cols), dim3((unsigned)(ctas * (kHeadDim / cols))), dim3(8 * cols),
+                   join_smem_bytes(cols), stream, p, split);
     if (e != cudaSuccess) return e;
     split.pass = 2;
     return launch_pdl(delta_extend_kernel<SEGMENT>, dim3((unsigned)(ctas * (split.segs - 1))), dim3(kThreads),
