@@ -403,10 +403,10 @@ __device__ __forceinline__ void scale_block(const TokenFactors &f, int a, int b,
 //   join     the segments' start states, S_1 from pass 1, S_{g+1} = M_g S_g + N_g in fp32;
 //   pass 2   segments 1 .. segs - 1 from their start states, side by side.
 // Rounding in a segment is amplified by the segments after it as the chain's own is.
-// Measured whole / split, us, T kernel included, l2norm, one request: 8 heads: 1,024 tokens 47.5 / 45.8,
-// 2,048: 84.6 / 66.5, 16,384: 626 / 199; 32 heads: 1,024: 52.7 / 61.9, 1,536: 75.3 / 73.7, 16,384:
-// 703 / 438; 76 heads: 2,560: 145 / 149, 4,096: 222 / 212, 16,384: 836 / 720.
-constexpr int kMaxSegs = 16;
+// Measured whole / split, us, T kernel included, l2norm, one request: 8 heads: 1,280 tokens 57 / 50, 2,048:
+// 84.6 / 60.5, 16,384: 626 / 190; 32 heads: 1,024: 52.7 / 61.9, 1,536: 75.3 / 73.7, 16,384: 703 / 445;
+// 76 heads: 2,560: 145 / 149, 4,096: 222 / 212, 16,384: 836 / 720.
+constexpr int kMaxSegs = 32;
 constexpr int kSplitSMs = 152;       // chains that run side by side
 constexpr int kSplitMinChunks = 20;  // shorter requests are not split
 struct Split {

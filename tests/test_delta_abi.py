@@ -112,7 +112,7 @@ def test_workspace_size(lib):
     # segments of long requests take room where there are few chains, and only there
     slots = lambda B, T, H: (T // 64 + B) * H * 21520 + (4 * B + 4 + 15) // 16 * 16  # noqa: E731
     assert la.delta_extend_workspace_size(2, 1216, 4, 128) == slots(2, 1216, 4)
-    assert la.delta_extend_workspace_size(2, 8192, 4, 128) == slots(2, 8192, 4) + 8 * 29 * 65536
+    assert la.delta_extend_workspace_size(1, 8192, 3, 128) == slots(1, 8192, 3) + 3 * 61 * 65536
     assert la.delta_extend_workspace_size(2, 8192, 38, 128) == slots(2, 8192, 38) + 304 * 65536
     # a plan for up to 128 requests of which one may be far longer than the others
     assert la.delta_extend_workspace_size(7, 8192, 11, 128) == slots(7, 8192, 11) + 6208 + 512 * 65536

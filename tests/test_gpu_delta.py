@@ -128,6 +128,7 @@ def test_extend_many_requests():
 @pytest.mark.parametrize("lens,Hk,H,l2,gate,max_seqlen", [
     ([2500], 1, 2, True, "model", None),
     ([2048], 1, 1, True, "none", None),
+    ([10000], 1, 1, True, "model", None),  # many segments
     ([2085, 0, 5, 700, 2048, 64, 130], 1, 2, True, "model", None),
     ([40, 2300], 1, 3, False, "none", 1 << 30),
     ([2111], 5, 20, True, "reset", None),  # segment 0 twice as long as the others
@@ -148,6 +149,32 @@ def test_extend_split(lens, Hk, H, l2, gate, max_seqlen):
     extend's tolerance."""
     check_extend(lens, Hk, H, l2=l2, gate=gate, max_seqlen=max_seqlen, seed=21, gap=3, tail=600,
                  prefix=[(b + 1) % 2 for b in range(len(lens))], tol=2 * TOL_EXTEND)
+
+
+@pytest.mark.parametrize("n,H", [(20000, 1), (33333, 2), (30000, 24)])
+def test_extend_split_equals_shorter_calls(n, H):
+    """A long request in as many segments as there are against calls of 1,216 tokens, which are not
+    split: each within the extend's tolerance of the formula, the split one within twice that."""
+    q, k, v, g, beta = _to(*inputs(n, 1, H, 23))
+    idx = torch.tensor([1], dtype=torch.int32, device=DEV)
+    outs, pools = [], []
+    for step in (n, 1216):
+        pool = torch.full((3, H, D, D), SENTINEL, device=DEV)
+        o = []
+        for a in range(0, n, step):
+            b = min(n, a + step)
+            o.append(la.delta_extend(q[a:b], k[a:b], v[a:b], g[a:b], beta[a:b], pool, idx,
+                                     torch.tensor([0, b - a], dtype=torch.int32, device=DEV),
+                                     torch.tensor([int(a > 0)], dtype=torch.uint8, device=DEV), qk_l2norm=True))
+        outs.append(torch.cat(o))
+        pools.append(pool)
+    la.poll_error()
+    check_states(f64(pools[0][1]), f64(pools[1][1]), 3 * TOL_EXTEND, "split")
+    # a state holds about one value per key direction, a norm of sqrt(128) |v| = 128; each output is
+    # rounded once, and before that off by 3 x 2^-16 x 128 x 128^-0.5 at most
+    assert pools[1][1].norm(dim=(1, 2)).max() < 128
+    assert torch.allclose(outs[0].float(), outs[1].float(), rtol=2.0 ** -7, atol=5.2e-4)
+    assert (pools[0][[0, 2]] == SENTINEL).all()
 
 
 def test_extend_split_nan_stays_behind():
