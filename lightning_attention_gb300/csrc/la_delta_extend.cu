@@ -148,9 +148,9 @@ static_assert(sizeof(Bars) <= SZ_BAR, "barrier block");
 // (hi, lo; before that A's, transposed, and T's in fp32).  The slot's two parts (P before P T) and the blocks
 // take the place of K and Q.  (Six CTAs fit, at 80 registers: 227 us in place of 222 on the mixed batch.)
 constexpr uint32_t TK_KQ = 0;                              // [64 K rows; 64 Q rows][128]
-constexpr uint32_t TK_AB = 2 * SZ_PART;                          // 6 x (512 hi + 512 lo)
+constexpr uint32_t TK_AB = 2 * SZ_PART;                    // 6 x (512 hi + 512 lo)
 constexpr uint32_t TK_TD = TK_AB + 6 * 1024;               // 4 x (512 hi + 512 lo)
-constexpr uint32_t TK_TOK = TK_KQ + SZ_KQ;             // per token: ghi, glo, rk, beta rk, scale rq
+constexpr uint32_t TK_TOK = TK_KQ + SZ_KQ;                 // per token: ghi, glo, rk, beta rk, scale rq
 static_assert(TK_TD + 4 * 1024 <= SZ_KQ, "blocks in place of K and Q");
 constexpr uint32_t kTSmemBytes = TK_TOK + 5 * 256 + 1024;
 
@@ -170,7 +170,7 @@ __device__ __forceinline__ void bar_wait(int id) {
 }
 
 constexpr uint64_t kDrainLimitNs = 2000000000ull;
-constexpr uint64_t kTryNs = 10000;
+constexpr uint64_t kTryNs = 10000;  // above a suspended try
 
 struct Ctx {
     uint64_t limit;
@@ -178,7 +178,7 @@ struct Ctx {
     unsigned int *err;
 };
 
-// A try may suspend the thread for some 4 us; under a limit below that warps 8 and 10, whose waits are the
+// A try may suspend the thread for some 4 us; under a limit near that warps 8 and 10, whose waits are the
 // longest, test without being suspended (TEST).
 template <bool TEST>
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity, const Ctx &cx) {
@@ -1704,8 +1704,8 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
         std::lock_guard<std::mutex> lock(mu);
         if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
         if (!configured[dev]) {
-            for (auto *kernel : {delta_extend_kernel<MANY>, delta_extend_kernel<ONE>, delta_extend_kernel<SEGMENT>,
-                                 delta_extend_kernel<PLANNED>}) {
+            for (auto *kernel : {delta_extend_kernel<MANY>, delta_extend_kernel<ONE>,
+                                 delta_extend_kernel<SEGMENT>, delta_extend_kernel<PLANNED>}) {
                 e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
                 if (e != cudaSuccess) return e;
             }
@@ -1735,8 +1735,9 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
         rank_ctas = (p.B + kTThreads - 1) / kTThreads;
     }
     if (t_ctas > 0) {
-        e = launch_pdl(plan ? delta_t_kernel<true> : delta_t_kernel<false>, dim3((unsigned)(rank_ctas + t_ctas)), dim3(kTThreads), kTSmemBytes,
-                       stream, tq, tk, p, w, order, plan, rank_ctas);
+        e = launch_pdl(plan ? delta_t_kernel<true> : delta_t_kernel<false>,
+                       dim3((unsigned)(rank_ctas + t_ctas)), dim3(kTThreads), kTSmemBytes, stream, tq, tk, p, w,
+                       order, plan, rank_ctas);
         if (e != cudaSuccess) return e;
     }
     Split split = plan_split(ctas, longest);
