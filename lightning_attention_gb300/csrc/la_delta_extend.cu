@@ -58,6 +58,7 @@
 #include <mutex>
 
 #include "la_delta.h"
+#include "la_delta_plan.h"
 #include "la_sm100.cuh"
 
 namespace la {
@@ -66,7 +67,7 @@ namespace {
 
 using namespace sm100;
 
-constexpr int C = 64;  // tokens of a chunk
+constexpr int C = kDeltaChunk;
 constexpr int kEWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kFixWarp = 10;
 constexpr int kThreads = 384;
 // Registers per thread of the warp groups: 2 x 184 (E) + 136 = 3 x 168, the launch's share.  (E at 200: the
@@ -74,7 +75,6 @@ constexpr int kThreads = 384;
 constexpr int kRegsE = 184, kRegsRest = 136;
 static_assert(2 * kRegsE + kRegsRest <= 3 * 168, "register split");
 constexpr int kTThreads = 128;
-constexpr int kMaxRanked = 8192;  // requests of a batch that is taken longest first
 constexpr float kScale = 0.08838834764831845f;  // 128^-0.5
 
 constexpr uint32_t kTmemCols = 512;
@@ -406,31 +406,14 @@ __device__ __forceinline__ void scale_block(const TokenFactors &f, int a, int b,
 // Measured whole / split, us, T kernel included, l2norm, one request: 8 heads: 1,280 tokens 57 / 50, 2,048:
 // 84.6 / 60.5, 16,384: 626 / 190; 32 heads: 1,024: 52.7 / 61.9, 1,536: 75.3 / 73.7, 16,384: 703 / 445;
 // 76 heads: 2,560: 145 / 149, 4,096: 222 / 212, 16,384: 836 / 720.
-constexpr int kMaxSegs = 32;
-constexpr int kSplitSMs = 152;       // chains that run side by side
-constexpr int kSplitMinChunks = 20;  // shorter requests are not split
-struct Split {
-    int segs, ratio;
+struct Split : Cut {
     int pass;       // 0: not split
     float *starts;  // [chains][segs - 1][D][D]: S_g at g - 1 (N_{g-1} before the join)
     float *trans;   // [chains][segs - 2][D][D]: M_g at g - 1
     const int32_t *plan;  // PLANNED: what follows; starts holds all of the plan's matrices
 };
-// What the join and two more launches cost, and a segment in the join, in chunks of the chain.
-constexpr double kSplitCost = 5., kJoinCost = 1.;
 constexpr float kItemCost = 1.2f;  // of an item beside its chunks, in chunks
-constexpr double kSplitGain = .95;  // a split has to promise this much
 constexpr size_t kMat = (size_t)kHeadDim * kHeadDim;
-// Chunks of segments 1, 2 ..; the last segment that has any.  A short request beside long ones (or under a
-// max_seqlen that none comes near) stays whole.
-__host__ __device__ inline int split_base(const Split &s, int nchunks) {
-    if (nchunks < kSplitMinChunks) return nchunks;
-    return (nchunks + s.ratio + s.segs - 2) / (s.ratio + s.segs - 1);
-}
-__host__ __device__ inline int split_last(const Split &s, int nchunks) {
-    const int base = split_base(s, nchunks), rest = nchunks - s.ratio * base;
-    return rest > 0 ? 1 + (rest - 1) / base : 0;
-}
 
 // The job of a CTA (one item each): segment, whether it is a transition, whether outputs are written.
 struct Job {
@@ -448,12 +431,6 @@ __device__ __forceinline__ Job split_job(const DeltaParams &p, const Split &s) {
 // segment 0 is a request's first a chunks, the next are b chunks each, so that short requests end in pass 1 as
 // they are.  A CTA of the first kernel tries 128 pairs (a, b) and lists the segments of both passes longest
 // first; an entry stands for its request's H heads.
-// Requests: planning is a pass over all of them per pair, which 512 short ones made 50 us longer than T takes.
-constexpr int kMaxPlanned = 128;
-// Longest request: one of 1500 tokens among 127 of 64, 4 heads, takes 83 us with a plan and 76 without; of 2000
-// 78 and 93.
-constexpr int kPlanMinChunks = 32;
-constexpr int kPlanMats = 512;    // matrices (start states and transitions, all heads)
 constexpr int kPlanA = 0, kPlanB = 1, kPlanFirst = 2, kPlanSecond = 3, kPlanJoins = 4, kPlanStarts = 5;
 constexpr int kPlanTaken1 = 6, kPlanTaken2 = 7;  // items taken in a pass, beyond each CTA's first
 constexpr int kPlanList1 = 16;                                  // entries of pass 1
@@ -1294,7 +1271,7 @@ __device__ __forceinline__ Item find_item(const DeltaParams &p, const int32_t *o
     const int32_t *plan = split.plan;
     const int entry = KIND == PLANNED ? plan[(split.pass == 2 ? kPlanList2 : kPlanList1) + want] : 0;
     // Longest request first where there is more than one row of items.
-    const int b = KIND == PLANNED ? entry & 1023 : order ? order[want] : want;
+    const int b = KIND == PLANNED ? entry & 1023 : !SPLIT && order ? order[want] : want;
     item.h = h;
     const int slot = p.state_idx[b];
     const int t_req0 = p.cu_seqlens[b], t_req1 = p.cu_seqlens[b + 1];
@@ -1628,40 +1605,6 @@ using JoinKernel = void (*)(const DeltaParams, const Split);
 JoinKernel join_kernel(int cols) {
     return cols == 8 ? delta_join_kernel<8> : cols == 16 ? delta_join_kernel<16> : delta_join_kernel<32>;
 }
-// Matrices of a split: at most two per chain that runs in pass 2, (segs - 1) chains <= kSplitSMs.
-unsigned long long split_mats(long long chains, long long chunks) {
-    if (chunks < kSplitMinChunks || 2 * chains > kSplitSMs) return 0ull;
-    const long long most = chains * (2 * kMaxSegs - 3);
-    return (unsigned long long)(most < 2 * kSplitSMs ? most : 2 * kSplitSMs);
-}
-// The split whose longest way through both passes is shortest, in chunks: a pass 1 with ratio of the
-// short chains one after another beside a segment 0, then a segment of pass 2, and what the join and its
-// launches cost.
-Split plan_split(long long chains, long long chunks) {
-    Split s{1, 1, 0, nullptr, nullptr, nullptr};
-    if (split_mats(chains, chunks) == 0) return s;
-    double best = kSplitGain * (double)chunks;
-    for (int ratio = 1; ratio <= 2; ++ratio)
-        for (int segs = 3; segs <= kMaxSegs && (segs - 1) * chains <= kSplitSMs; ++segs) {
-            if (2 * (segs - 2) * chains > ratio * (kSplitSMs - chains)) continue;
-            const Split t{segs, ratio, 1, nullptr, nullptr, nullptr};
-            const double cost = (ratio + 1) * split_base(t, (int)chunks) + kSplitCost + kJoinCost * segs;
-            if (cost < best) {
-                best = cost;
-                s = t;
-            }
-        }
-    return s;
-}
-// Whether a batch gets a plan: more chains than a split takes, and a longest request (of `longest` chunks) of
-// at least twice the SMs' even share of all chunks, 8 added to it.  At 16 heads, without / with, us: 16,384
-// tokens among 63 x 256: 707 / 426; 8192, 4096, 6 x 500: 352 / 227; 4096 among 7 x 1024 (2.4 times): 193 / 169,
-// among 7 x 1536 (2.0): 204 / 201; eight of 512-4096 (1.7): 218 / 212 and 218 / 229; twelve of 256-4096 (1.1):
-// 221 / 232.
-bool planned(long long B, long long H, long long chunks, long long longest) {
-    return 2 * B * H > kSplitSMs && B >= 2 && B <= kMaxPlanned && H <= kPlanMats && longest >= kPlanMinChunks &&
-           longest * kSplitSMs >= 2 * (H * chunks + 8 * kSplitSMs);
-}
 // Bytes of the slots, of the order, of a split's matrices.
 unsigned long long slots_bytes(long long B, long long T, long long H) {
     return ((unsigned long long)chunk_slots(T, B) * (unsigned long long)H * SZ_SLOT);
@@ -1722,15 +1665,13 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
         }
     }
     uint8_t *w = static_cast<uint8_t *>(ws);
-    // One wave needs no order; ranking is B comparisons per request.
     int32_t *order = nullptr, *plan = nullptr;
     int rank_ctas = 0;
-    const long long chunks = ((long long)p.T + C - 1) / C;
-    const long long longest = ((long long)(p.max_seqlen < p.T ? p.max_seqlen : p.T) + C - 1) / C;
-    if (planned(p.B, p.H, chunks, longest)) {
+    const Schedule how = make_schedule(p.B, p.T, p.H, p.max_seqlen, num_sms);
+    if (how.planned) {
         plan = reinterpret_cast<int32_t *>(w + slots_bytes(p.B, p.T, p.H) + order_bytes(p.B));
         rank_ctas = 1;
-    } else if (t_ctas > 0 && p.B > 1 && p.B <= kMaxRanked && ctas > num_sms) {
+    } else if (how.ranked) {
         order = reinterpret_cast<int32_t *>(w + slots_bytes(p.B, p.T, p.H));
         rank_ctas = (p.B + kTThreads - 1) / kTThreads;
     }
@@ -1740,7 +1681,7 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
                        order, plan, rank_ctas);
         if (e != cudaSuccess) return e;
     }
-    Split split = plan_split(ctas, longest);
+    Split split{how.cut, 0, nullptr, nullptr, nullptr};
     if (plan) {
         split.plan = plan;
         split.starts = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(plan) + kPlanBytes);
@@ -1757,15 +1698,16 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
         }
         return cudaSuccess;
     }
-    if (split.pass == 0)
+    if (split.segs == 1)
         return launch_pdl(ctas > num_sms ? delta_extend_kernel<MANY> : delta_extend_kernel<ONE>,
                           dim3((unsigned)(ctas < num_sms ? ctas : num_sms)), dim3(kThreads), kSmemBytes,
                           stream, tq, tk, tv, p, (const uint8_t *)w, (const int32_t *)order, split,
                           order ? order + order_ints(p.B) - 1 : (int32_t *)nullptr, (int)ctas);
     split.starts = reinterpret_cast<float *>(w + slots_bytes(p.B, p.T, p.H) + order_bytes(p.B));
     split.trans = split.starts + (size_t)ctas * (split.segs - 1) * kMat;
+    split.pass = 1;
     e = launch_pdl(delta_extend_kernel<SEGMENT>, dim3((unsigned)(ctas * (2 * split.segs - 3))), dim3(kThreads),
-                   kSmemBytes, stream, tq, tk, tv, p, (const uint8_t *)w, (const int32_t *)order, split,
+                   kSmemBytes, stream, tq, tk, tv, p, (const uint8_t *)w, (const int32_t *)nullptr, split,
                    (int32_t *)nullptr, (int)(ctas * (2 * split.segs - 3)));
     if (e != cudaSuccess) return e;
     int cols = 32;
@@ -1775,7 +1717,7 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
     if (e != cudaSuccess) return e;
     split.pass = 2;
     return launch_pdl(delta_extend_kernel<SEGMENT>, dim3((unsigned)(ctas * (split.segs - 1))), dim3(kThreads),
-                      kSmemBytes, stream, tq, tk, tv, p, (const uint8_t *)w, (const int32_t *)order, split,
+                      kSmemBytes, stream, tq, tk, tv, p, (const uint8_t *)w, (const int32_t *)nullptr, split,
                       (int32_t *)nullptr, (int)(ctas * (split.segs - 1)));
 }
 
