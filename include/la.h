@@ -386,9 +386,9 @@ la_status la_commit_accepted(const float *inter_states, const int32_t *accept_id
  * with the same results up to rounding: where B * H <= 76 from about 1,300 tokens at B * H = 8 and from
  * about 2,600 at 76, and above that (B <= 128) where max_seqlen is far longer than the SMs' share of T * H.
  * Both go by max_seqlen (or T, if that is less), so pass it no larger than it is.
- * A call in which cu_seqlens decreases somewhere skips the requests concerned and reports them, but the
- * results of its other requests are then unspecified too.  Numerics: bf16 products with fp32 accumulation; each
- * operand the kernels compute is a bf16 pair hi + lo (off by at most 2^-16); states are kept, updated and
+ * Where cu_seqlens decreases somewhere, a call that goes token by token skips the requests concerned, and
+ * one that goes by chunks its whole batch (nothing is written); both report it.
+ * Numerics: bf16 products with fp32 accumulation; each operand the kernels compute is a bf16 pair hi + lo (off by at most 2^-16); states are kept, updated and
  * joined in fp32; out is rounded to bf16 once.  A NaN or an infinity in a request's inputs may reach all of that
  * request's outputs and its state, and nothing of any other request.
  */

@@ -91,6 +91,10 @@ constexpr uint32_t TM_S = 0, TM_X = 128, TM_Y = 256, TM_D = 384;
 constexpr uint32_t SZ_PART = 10240;
 constexpr uint32_t SZ_COEF = 4 * 256 + 16;
 constexpr uint32_t SZ_SLOT = 2 * SZ_PART + SZ_COEF;
+// The words behind gamma_C are spare; the first one of the workspace's first slot says whether cu_seqlens
+// decreases somewhere.
+constexpr uint32_t OFF_DISORDER = 2 * SZ_PART + 4 * 257;
+static_assert(OFF_DISORDER + 4 <= SZ_SLOT, "a spare word");
 // Offset within a part of step kk.
 __host__ __device__ constexpr uint32_t part_ofs(int kk) { return (uint32_t)(4096 * kk - 512 * kk * (kk - 1)); }
 static_assert(part_ofs(4) == SZ_PART, "part layout");
@@ -556,8 +560,18 @@ __device__ void rank_requests(const DeltaParams &p, int block, int32_t *order, i
     if (b == 0) order[order_ints(p.B) - 1] = 0;  // items taken beyond each CTA's first
 }
 
-// T', P T and the coefficients of one chunk and head (blockIdx.x = rank_ctas + slot * H + head); the first
-// rank_ctas CTAs order the requests for the chain kernel, or plan its segments.  Warp w has the 16 rows 16 w ..
+// Whether cu_seqlens decreases somewhere.  Chunk slots of different requests may then be the same, and a slot's
+// request is not found by search, so that the chain kernel skips the whole batch.
+__device__ void check_order(const DeltaParams &p, uint8_t *ws) {
+    int less = 0;
+    for (int r = threadIdx.x; r < p.B; r += kTThreads) less |= p.cu_seqlens[r + 1] < p.cu_seqlens[r];
+    less = __syncthreads_or(less);
+    if (threadIdx.x == 0) *reinterpret_cast<int *>(ws + OFF_DISORDER) = less;
+}
+
+// T', P T and the coefficients of one chunk and head (blockIdx.x = first_ctas + slot * H + head); of the
+// first_ctas CTAs the first checks cu_seqlens, and they order the requests for the chain kernel, or plan its
+// segments.  Warp w has the 16 rows 16 w ..
 // of everything: the 16 x 16 blocks of K K^T and Q K^T (mma.sync: a block is too small for tcgen05), the inverse
 // of its diagonal block of I + A by substitution, a lane per column, then the blocks below by T_ab = -T_aa
 // sum A_am T_mb.
@@ -568,7 +582,7 @@ __device__ void rank_requests(const DeltaParams &p, int block, int32_t *order, i
 template <bool PLAN>
 __global__ void __launch_bounds__(kTThreads, 5)
     delta_t_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                   const DeltaParams p, uint8_t *ws, int32_t *order, int32_t *plan, int rank_ctas) {
+                   const DeltaParams p, uint8_t *ws, int32_t *order, int32_t *plan, int first_ctas) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t kq_full;
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -576,20 +590,21 @@ __global__ void __launch_bounds__(kTThreads, 5)
     const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
-    if ((int)blockIdx.x < rank_ctas) {
+    if ((int)blockIdx.x < first_ctas) {
+        if (blockIdx.x == 0) check_order(p, ws);
         if (PLAN)
             plan_requests(p, plan, reinterpret_cast<int *>(sm));
-        else
+        else if (order)
             rank_requests(p, blockIdx.x, order, reinterpret_cast<int *>(sm));
         return;
     }
-    const unsigned item = blockIdx.x - (unsigned)rank_ctas;
+    const unsigned item = blockIdx.x - (unsigned)first_ctas;
     const int slot = (int)(item / (unsigned)p.H);
     const int h = (int)(item - (unsigned)slot * (unsigned)p.H);
 
     // The slot's request: the last b with floor(cu_seqlens[b] / C) + b <= slot, 32 candidates at a time.
-    // (Requests that are out of order or too long are skipped by the chain kernel; whatever is found for
-    // them is checked before it is used.)
+    // (A batch that is out of order and requests that are too long are skipped by the chain kernel; whatever is
+    // found for them is checked before it is used.)
     int b = 0;
     {
         int step = 1;
@@ -1261,8 +1276,8 @@ __device__ __forceinline__ int item_count(int all) {
 }
 
 template <Kind KIND>
-__device__ __forceinline__ Item find_item(const DeltaParams &p, const int32_t *order, const Split &split,
-                                          int which, int &slot0) {
+__device__ __forceinline__ Item find_item(const DeltaParams &p, const uint8_t *ws, const int32_t *order,
+                                          const Split &split, int which, int &slot0) {
     constexpr bool SPLIT = KIND == SEGMENT;
     Item item{nullptr, nullptr, 0, 0, 0, 0, 1};
     const int chains = p.B * p.H;
@@ -1276,11 +1291,12 @@ __device__ __forceinline__ Item find_item(const DeltaParams &p, const int32_t *o
     const int slot = p.state_idx[b];
     const int t_req0 = p.cu_seqlens[b], t_req1 = p.cu_seqlens[b + 1];
     const bool prefix = p.prefix_mask[b];
+    const bool disorder = *reinterpret_cast<const int *>(ws + OFF_DISORDER) != 0;
     if (slot < 0 || slot >= p.num_slots) {
         atomicOr(p.err, ERR_BIT_SLOT_RANGE);
         return item;
     }
-    if (!request_ok(p, t_req0, t_req1)) {
+    if (disorder || !request_ok(p, t_req0, t_req1)) {
         atomicOr(p.err, ERR_BIT_SEQLENS);
         return item;
     }
@@ -1344,7 +1360,7 @@ __device__ void producer_role(const CUtensorMap &tq, const CUtensorMap &tk, cons
                 item.from = nullptr;
                 items = k;
             } else {
-                item = find_item<KIND>(p, order, split, which, slot0);
+                item = find_item<KIND>(p, ws, order, split, which, slot0);
             }
             if (item.from && item.n > 0) bulk_prefetch(item.from, kMat * sizeof(float));
             if (k >= kItems && !wait_bar<true>(&bars->item_empty[k % kItems], (k / kItems - 1) & 1, cx)) break;
@@ -1468,7 +1484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_prefetch_desc(&tk);
             tma_prefetch_desc(&tv);
         }
-        first = find_item<KIND>(p, order, split, item_at(0), slot0);
+        first = find_item<KIND>(p, ws, order, split, item_at(0), slot0);
     }
     tc_fence_before();
     __syncthreads();
@@ -1666,19 +1682,18 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
     }
     uint8_t *w = static_cast<uint8_t *>(ws);
     int32_t *order = nullptr, *plan = nullptr;
-    int rank_ctas = 0;
+    int first_ctas = 1;
     const Schedule how = make_schedule(p.B, p.T, p.H, p.max_seqlen, num_sms);
     if (how.planned) {
         plan = reinterpret_cast<int32_t *>(w + slots_bytes(p.B, p.T, p.H) + order_bytes(p.B));
-        rank_ctas = 1;
     } else if (how.ranked) {
         order = reinterpret_cast<int32_t *>(w + slots_bytes(p.B, p.T, p.H));
-        rank_ctas = (p.B + kTThreads - 1) / kTThreads;
+        first_ctas = (p.B + kTThreads - 1) / kTThreads;
     }
     if (t_ctas > 0) {
         e = launch_pdl(plan ? delta_t_kernel<true> : delta_t_kernel<false>,
-                       dim3((unsigned)(rank_ctas + t_ctas)), dim3(kTThreads), kTSmemBytes, stream, tq, tk, p, w,
-                       order, plan, rank_ctas);
+                       dim3((unsigned)(first_ctas + t_ctas)), dim3(kTThreads), kTSmemBytes, stream, tq, tk, p, w,
+                       order, plan, first_ctas);
         if (e != cudaSuccess) return e;
     }
     Split split{how.cut, 0, nullptr, nullptr, nullptr};
