@@ -375,11 +375,9 @@ la_status la_commit_accepted(const float *inter_states, const int32_t *accept_id
  * state written to its slot (for zero-length requests too).  state_idx, cu_seqlens, prefix_mask,
  * max_seqlen, B, T as for la_extend; rows of out that belong to no request are left as they were.
  *   workspace        device scratch, 16-byte aligned, of at least la_delta_extend_workspace_size()
- *                    bytes (LA_ERR_INVALID otherwise; may be NULL when T = 0): 21,520 bytes per value
- *                    head and 64 tokens (a third of what q, k, v and out take at Hk = H), and up to
- *                    20 MB more where B * H <= 76 (from 1,217 tokens on), 34 MB more where it is above
- *                    and B at most 128 (from 1,985).  Contents do not matter on entry and are garbage on exit; calls that
- *                    share one must not overlap on the GPU.
+ *                    bytes (LA_ERR_INVALID otherwise; none is needed, and NULL will do, where
+ *                    max_seqlen or T is at most 6).  Contents do not matter on entry and are garbage
+ *                    on exit; calls that share one must not overlap on the GPU.
  * Where max_seqlen (T, if that is less) is at most 6 the tokens are taken one by one, in fp32, in one
  * launch.  Otherwise a first launch forms, for every chunk of 64 tokens at once, what depends on no
  * state, and a second runs the chunks of each (request, head) in turn.  Long requests run as segments side by side, in four launches,
@@ -402,7 +400,11 @@ la_status la_delta_extend(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, 
 
 /*
  * la_delta_extend_workspace_size -- bytes of device scratch la_delta_extend needs for a batch of B
- * requests and T tokens.  Host only.  LA_ERR_INVALID for bad sizes or bytes == NULL.
+ * requests and T tokens by chunks, whatever their lengths: 21,520 bytes for each of T / 64 + B chunks
+ * (every request may end inside one) of each value head -- a third of what q, k, v and out take at
+ * Hk = H for long requests, and about 21 KB a request and head for short ones, however few their tokens --
+ * and up to 20 MB more where B * H <= 76 (from 1,217 tokens on), 34 MB more where it is above and B
+ * between 2 and 128 (from 1,985).  Host only.  LA_ERR_INVALID for bad sizes or bytes == NULL.
  */
 la_status la_delta_extend_workspace_size(int B, int T, int H, int D, size_t *bytes);
 

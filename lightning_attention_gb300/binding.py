@@ -570,7 +570,8 @@ def _delta_args(q, k, v, g, beta, state_pool, state_idx, out, tokens: int | None
 
 
 def delta_extend_workspace_size(B: int, T: int, H: int, D: int) -> int:
-    """Bytes of scratch la_delta_extend needs for a batch of B requests and T tokens."""
+    """Bytes of scratch la_delta_extend needs for a batch of B requests and T tokens, more than 6 in some request:
+    21,520 per value head for each of T / 64 + B chunks, and room for segments of long requests."""
     n = ctypes.c_size_t(0)
     _check("la_delta_extend_workspace_size",
            load().la_delta_extend_workspace_size(B, T, H, D, ctypes.byref(n)))
@@ -582,14 +583,20 @@ def delta_extend(q, k, v, g, beta, state_pool, state_idx, cu_seqlens, prefix_mas
     """Packed varlen gated delta rule (la_delta_extend).  q, k: bf16 [T, Hk*D]; v: bf16 [T, H*D]
     (rows may be strided: column ranges of one projection); g (log decay) and beta: fp32 [T, H];
     state_pool fp32 [S, H, D, D] updated in place; returns out bf16 [T, H*D].  Value head h reads key
-    head h // (H / Hk); qk_l2norm divides q and k by their head's 2-norm first."""
+    head h // (H / Hk); qk_l2norm divides q and k by their head's 2-norm first.
+
+    workspace: uint8 scratch of at least delta_extend_workspace_size() bytes; allocated on the current stream
+    where it is not given (none for max_seqlen up to 6).  Under CUDA-graph capture it then lives in the graph's
+    pool; pass one to share it between graphs that do not overlap."""
     dev, T, slots, B, H, Hk, D, rs, out = _delta_args(q, k, v, g, beta, state_pool, state_idx, out, None)
     _need_fast(cu_seqlens, "cu_seqlens", torch.int32, dev, (B + 1,))
     _need_fast(prefix_mask, "prefix_mask", torch.uint8, dev, (B,))
     if max_seqlen is None:
         max_seqlen = T
     if workspace is None:
-        workspace = torch.empty(delta_extend_workspace_size(B, T, H, D), dtype=torch.uint8, device=dev)
+        # la_delta_extend takes at most 6 tokens a request one by one, without scratch
+        nbytes = 0 if min(max_seqlen, T) <= 6 else delta_extend_workspace_size(B, T, H, D)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _need(workspace, "workspace", torch.uint8, dev)
     with _on(dev):
         st = (_lib or load()).la_delta_extend(

@@ -640,7 +640,9 @@ la_status la_delta_extend(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, 
                                 state_pool, num_slots, state_idx, out, B, T, H, Hk, D, qk_l2norm);
     if (st != LA_OK || !work) return st;
     if (!cu_seqlens || !prefix_mask || !aligned4(cu_seqlens)) return LA_ERR_INVALID;
-    const unsigned long long need = la::delta_scratch_bytes(B, T, H);
+    // a few tokens a request: token by token, without chunks
+    const bool serial = std::min(max_seqlen, T) <= la::kSerialTokens;
+    const unsigned long long need = serial ? 0ull : la::delta_scratch_bytes(B, T, H);
     if (need > 0 && (!workspace || !aligned16(workspace) || (unsigned long long)workspace_bytes < need))
         return LA_ERR_INVALID;
     p.cu_seqlens = cu_seqlens;
@@ -648,8 +650,7 @@ la_status la_delta_extend(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, 
     p.max_seqlen = max_seqlen;
     int sms = 0;
     if ((st = error_word_ptr(&p.err)) != LA_OK || (st = num_sms(&sms)) != LA_OK) return st;
-    // a few tokens a request: token by token, without chunks
-    if (std::min(max_seqlen, T) <= la::kSerialTokens)
+    if (serial)
         return launch_status(la::launch_delta_recurrent(la::DELTA_SERIAL, p, sms,
                                                         static_cast<cudaStream_t>(stream)));
     return launch_status(la::launch_delta_extend(p, workspace, sms, static_cast<cudaStream_t>(stream)));
