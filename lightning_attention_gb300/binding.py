@@ -585,6 +585,12 @@ def delta_extend(q, k, v, g, beta, state_pool, state_idx, cu_seqlens, prefix_mas
     state_pool fp32 [S, H, D, D] updated in place; returns out bf16 [T, H*D].  Value head h reads key
     head h // (H / Hk); qk_l2norm divides q and k by their head's 2-norm first.
 
+    max_seqlen: an upper bound on the requests' lengths, which picks the schedule; T where it is not given,
+    since the lengths are on the device.  Pass the longest length: under T a batch of a few tokens a request
+    is taken by chunks (256 requests of one token, 16 heads: 198 us in place of 86), and more than 76
+    (request, head) pairs of 2 to 128 requests run as a skewed batch does from about 2,000 tokens on, a few
+    percent slower where the batch is not skewed.
+
     workspace: uint8 scratch of at least delta_extend_workspace_size() bytes; allocated on the current stream
     where it is not given (none for max_seqlen up to 6).  Under CUDA-graph capture it then lives in the graph's
     pool; pass one to share it between graphs that do not overlap."""
