@@ -533,7 +533,7 @@ namespace {
 // Row stride of a token row of `width` elements: 0 means packed; rows may not overlap and start on
 // 16-byte boundaries.  The stride of a single row does not matter.
 bool row_stride_ok(int64_t *rs, long long rows, long long width) {
-    if (*rs == 0 || (rows <= 1 && *rs > 0)) *rs = width;
+    if (*rs == 0 || rows <= 1) *rs = width;
     return *rs >= width && *rs % 8 == 0;
 }
 
