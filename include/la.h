@@ -436,10 +436,11 @@ la_status la_delta_verify_chain(const la_bf16 *q, const la_bf16 *k, const la_bf1
  * a state is D / 32 blocks of 32 values along v; a block is 32 int8 codes in [-127, 127] and one
  * scale byte s, and stands for code * 2^(s - 127).  s is the smallest for which no code exceeds 127,
  * at least 0, so a code is the value over a power of two, rounded to the nearest integer (ties to
- * even): a restored value is off by at most half of 2^(s - 127), at most 1/127 of the block's largest
- * magnitude, and packing a restored state gives it back bit for bit (-0 comes back as 0).  s is at
- * most 248 there, so that every code stands for a finite value: magnitudes above 127.5 * 2^121 are held
- * at code 127.  A block that holds an infinity or a NaN has s = 255 and codes 0, and is restored as NaN.
+ * even): a restored value is off by at most half of 2^(s - 127), which is at most 1/127 of the block's
+ * largest magnitude where s > 0; where s = 0 (no magnitude of 127.5 * 2^-127 or more) it is 2^-128, and
+ * magnitudes up to that become 0.  Packing a restored state gives it back bit for bit (-0 comes back as
+ * 0).  s is at most 248 there, so that every code stands for a finite value: magnitudes above
+ * 127.5 * 2^121 are held at code 127, off by less than 2^121, 1/127 of them.  A block that holds an infinity or a NaN has s = 255 and codes 0, and is restored as NaN.
  *   codes      device, int8 [entries][H][D][D], 16-byte aligned
  *   scales     device, uint8 [entries][H][D][D/32], 4-byte aligned
  *   store_idx  device, int32 [B], each in [0, entries): the entry of request b

@@ -5,7 +5,8 @@
 // 2^-127, for which the block's largest code stays at 127 or less.  Scaling by a power of two is
 // exact, so a code is the value divided by the scale, rounded once to the nearest integer (ties to
 // even): a restored value is off by at most half a scale, at most 1/127 of the block's largest
-// magnitude.  (Only magnitudes above 127.5 * 2^121 are held at 127 of the largest scale instead.)
+// magnitude where s > 0; where s = 0 that half is 2^-128, whatever the magnitudes.  (Only magnitudes above
+// 127.5 * 2^121 are held at 127 of the largest scale instead.)
 // s = 255 marks a block that held an infinity or a NaN; it is restored as NaN.
 //
 // Both directions are copies bound by HBM (64 KiB of fp32 against 16.5 KiB packed): one CTA of 256
