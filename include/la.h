@@ -380,10 +380,12 @@ la_status la_commit_accepted(const float *inter_states, const int32_t *accept_id
  *                    on exit; calls that share one must not overlap on the GPU.
  * Where max_seqlen (T, if that is less) is at most 6 the tokens are taken one by one, in fp32, in one
  * launch.  Otherwise a first launch forms, for every chunk of 64 tokens at once, what depends on no
- * state, and a second runs the chunks of each (request, head) in turn.  Long requests run as segments side by side, in four launches,
- * with the same results up to rounding: where B * H <= 76 from about 1,300 tokens at B * H = 8 and from
- * about 2,600 at 76, and above that (B <= 128) where max_seqlen is far longer than the SMs' share of T * H.
- * Both go by max_seqlen (or T, if that is less), so pass it no larger than it is.
+ * state, and a second runs the chunks of each (request, head) in turn.  Long requests run as segments
+ * side by side, in four launches, with the same results up to rounding: where B * H <= 76 from 1,217 tokens
+ * on (B * H up to 16), 1,473 (at 32), 2,753 (from 51 to 76; a few lengths up to 400 tokens above these stay
+ * whole), and where B * H is above that and B between 2 and 128, where max_seqlen is at least 1,985 and far
+ * longer than the SMs' share of T * H.  Both go by max_seqlen (or T, if that is less), so pass it no larger
+ * than it is.
  * Where cu_seqlens decreases somewhere, a call that goes token by token skips the requests concerned, and
  * one that goes by chunks its whole batch (nothing is written); both report it.
  * Numerics: bf16 products with fp32 accumulation; each operand the kernels compute is a bf16 pair hi + lo (off by at most 2^-16); states are kept, updated and

@@ -59,3 +59,25 @@ def test_a_split_batch_is_never_ranked(plan, sms):
                 if s["segs"] == 1 and not s["planned"]:
                     assert s["ranked"] == (B > 1 and B * H > sms), (B, H, longest, s)
     assert split > 40
+
+
+@pytest.mark.parametrize("chains,first", [(1, 1217), (8, 1217), (16, 1217), (32, 1473), (51, 2753), (76, 2753)])
+def test_onset_of_a_split(plan, chains, first):
+    """From which length on a request is cut into segments, as the header states it: only lengths within 400
+    tokens above the first stay whole."""
+    segs = lambda n: plan(1, n, chains)["segs"]  # noqa: E731
+    assert all(segs(n) == 1 for n in range(1, first, 7)) and segs(first - 1) == 1
+    assert segs(first) > 1
+    assert all(segs(n) > 1 for n in range(first + 400, 40000, 61))
+    assert plan(77, 40000, 1, 1217)["segs"] == 1 and plan(1, 40000, 77)["segs"] == 1
+
+
+def test_onset_of_a_plan(plan):
+    """A skewed batch of more than 76 pairs and 2 to 128 requests is planned from 1,985 tokens on."""
+    assert not plan(100, 1984 + 99, 1, 1984)["planned"] and plan(100, 1985 + 99, 1, 1985)["planned"]
+    assert not plan(129, 4000, 1, 3000)["planned"] and plan(128, 4000, 1, 3000)["planned"]
+    assert not plan(1, 40000, 128)["planned"] and not plan(2, 40000, 38)["planned"]
+    # at least twice the SMs' share of all chunks, 8 added to it
+    for rest in range(0, 60000, 500):
+        s = plan(100, 4096 + rest, 4, 4096)
+        assert s["planned"] == (64 * 152 >= 2 * (4 * ((4096 + rest + 63) // 64) + 8 * 152)), rest
