@@ -230,8 +230,6 @@ __global__ void __launch_bounds__(kThreads, 2) delta_recurrent_kernel(const Delt
 template <int MODE>
 cudaError_t launch_mode(const DeltaParams &p, int num_sms, cudaStream_t stream) {
     const long long pairs = (long long)p.B * p.H;
-    if (pairs <= 0) return cudaSuccess;
-    if (pairs * 4 > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     // A quarter of the columns per CTA while all of those CTAs are on the SMs at once (two each).  Quarters /
     // whole rows, us: decode of 8 pairs 2.2 / 3.5, 64: 4.1 / 4.6, 76: 4.2 / 4.7, 96: 6.1 / 5.1, 304:
     // 13.2 / 8.7; verify of 5 tokens 6.3 / 11.1, 9.1 / 12.1, 9.3 / 12.2, 14.5 / 12.6, 32.9 / 22.1.

@@ -3,6 +3,7 @@
 
 #include "la_internal.h"
 
+// The entry points have checked all sizes: B and H are at least 1, and the grids fit.
 namespace la {
 
 // Per request and value head h, with key head h / group:
@@ -35,7 +36,8 @@ constexpr int kSerialTokens = 6;
 cudaError_t launch_delta_recurrent(DeltaMode mode, const DeltaParams &p, int num_sms,
                                    cudaStream_t stream);
 
-// Chunked extend on the tensor cores (la_delta_extend.cu); ws: delta_scratch_bytes() bytes.
+// Chunked extend on the tensor cores (la_delta_extend.cu), of B > 0 requests and T > kSerialTokens tokens; ws:
+// delta_scratch_bytes() bytes.
 unsigned long long delta_scratch_bytes(long long B, long long T, long long H);
 cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cudaStream_t stream);
 

@@ -53,7 +53,6 @@
 // sets the error word and an abort flag that ends every role, then the CTA waits for its copies and MMAs,
 // frees tensor memory and exits.
 #include <cuda.h>
-#include <string.h>
 
 #include <mutex>
 
@@ -1479,11 +1478,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(&bars->tmem_base, kTmemCols);
         tmem_relinquish();
     } else if (warp == kProducerWarp && lane == 0) {
-        if (p.T > 0) {
-            tma_prefetch_desc(&tq);
-            tma_prefetch_desc(&tk);
-            tma_prefetch_desc(&tv);
-        }
+        tma_prefetch_desc(&tq);
+        tma_prefetch_desc(&tk);
+        tma_prefetch_desc(&tv);
         first = find_item<KIND>(p, ws, order, split, item_at(0), slot0);
     }
     tc_fence_before();
@@ -1641,18 +1638,11 @@ unsigned long long delta_scratch_bytes(long long B, long long T, long long H) {
 
 cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cudaStream_t stream) {
     const long long ctas = (long long)p.B * p.H;
-    if (ctas <= 0) return cudaSuccess;
-    const long long t_ctas = p.T > 0 ? chunk_slots(p.T, p.B) * p.H : 0;
-    if (ctas + num_sms > 0x7fffffffLL || t_ctas + kMaxRanked > 0x7fffffffLL)
-        return cudaErrorInvalidConfiguration;
+    const long long t_ctas = chunk_slots(p.T, p.B) * p.H;
     CUtensorMap tq, tk, tv;
-    memset(&tq, 0, sizeof(tq));
-    memset(&tk, 0, sizeof(tk));
-    memset(&tv, 0, sizeof(tv));
-    if (p.T > 0 &&
-        (!make_rows_map(&tq, p.q, p.T, (long long)p.Hk * kHeadDim, p.q_rs, 64, C, true) ||
-         !make_rows_map(&tk, p.k, p.T, (long long)p.Hk * kHeadDim, p.k_rs, 64, C, true) ||
-         !make_rows_map(&tv, p.v, p.T, (long long)p.H * kHeadDim, p.v_rs, kHeadDim, C, false)))
+    if (!make_rows_map(&tq, p.q, p.T, (long long)p.Hk * kHeadDim, p.q_rs, 64, C, true) ||
+        !make_rows_map(&tk, p.k, p.T, (long long)p.Hk * kHeadDim, p.k_rs, 64, C, true) ||
+        !make_rows_map(&tv, p.v, p.T, (long long)p.H * kHeadDim, p.v_rs, kHeadDim, C, false))
         return cudaErrorInvalidValue;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1690,12 +1680,9 @@ cudaError_t launch_delta_extend(const DeltaParams &p, void *ws, int num_sms, cud
         order = reinterpret_cast<int32_t *>(w + slots_bytes(p.B, p.T, p.H));
         first_ctas = (p.B + kTThreads - 1) / kTThreads;
     }
-    if (t_ctas > 0) {
-        e = launch_pdl(plan ? delta_t_kernel<true> : delta_t_kernel<false>,
-                       dim3((unsigned)(first_ctas + t_ctas)), dim3(kTThreads), kTSmemBytes, stream, tq, tk, p, w,
-                       order, plan, first_ctas);
-        if (e != cudaSuccess) return e;
-    }
+    e = launch_pdl(plan ? delta_t_kernel<true> : delta_t_kernel<false>, dim3((unsigned)(first_ctas + t_ctas)),
+                   dim3(kTThreads), kTSmemBytes, stream, tq, tk, p, w, order, plan, first_ctas);
+    if (e != cudaSuccess) return e;
     Split split{how.cut, 0, nullptr, nullptr, nullptr};
     if (plan) {
         split.plan = plan;

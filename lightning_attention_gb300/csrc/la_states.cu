@@ -127,15 +127,11 @@ __global__ void __launch_bounds__(kThreads) unpack_states_kernel(const PackParam
 
 cudaError_t launch_pack_states(const PackParams &p, cudaStream_t stream) {
     const long long blocks = (long long)p.B * p.H;
-    if (blocks <= 0) return cudaSuccess;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     return launch_pdl(pack_states_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, p);
 }
 
 cudaError_t launch_unpack_states(const PackParams &p, cudaStream_t stream) {
     const long long blocks = (long long)p.B * p.H;
-    if (blocks <= 0) return cudaSuccess;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     return launch_pdl(unpack_states_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, p);
 }
 
