@@ -33,8 +33,13 @@
 //
 // Precision.  Products run in bf16 with fp32 accumulation.  K and Q are used as loaded; the operands
 // that are computed (S, R, T', P T, U) are bf16 pairs hi + lo, off by at most 2^-16 and about a sixth of
-// that in the mean; U takes R itself in fp32 and only T' R through pairs; the state stays in fp32
-// registers and is never accumulated in tensor memory (which does not round to nearest).
+// that in the mean; U takes R itself in fp32 and only T' R through pairs; products of two pairs leave out that
+// of the lo parts, but for those of the inverse; the state stays in fp32 registers and is never accumulated in
+// tensor memory (which does not round to nearest).  Decays come from ex2.approx (off by 2^-22) and norms from
+// rsqrtf (2 units in the last place), both far below the pairs.  A third part per operand would bring the state's
+// error from 3e-6 of its norm to fp32's and add half to the chain's MMAs, for bits that the bf16 outputs do not
+// show.  Where a chunk's sums cancel (keys nearly the same, beta |k|^2 near 2, no decay) the pairs' errors show
+// more: 1.2e-4 of the norm at keys within 8 degrees.
 //
 // Roles of the chain kernel (384 threads, one CTA per SM):
 //   warps 0-7   E: the state (32 v rows x 64 k columns a warp) and the passes R, U, O and S;
@@ -267,14 +272,16 @@ __device__ __forceinline__ void split_frag(const float (&c)[8], uint32_t (&hi)[4
     split2(c[6], c[7], hi[3], lo[3]);
 }
 
-// acc + cross += A B with A and B bf16 pairs (the product of the two lo parts, 2^-16, is left out): two
-// sums, so that fewer MMAs wait for one another.
+// acc + cross += A B with A and B bf16 pairs: two sums, so that fewer MMAs wait for one another.  The product of
+// the two lo parts (2^-16 at most) is formed where LO says so.
+template <bool LO>
 __device__ __forceinline__ void prod16(float (&acc)[8], float (&cross)[8], const uint32_t (&ah)[4],
                                        const uint32_t (&al)[4], const uint32_t (&bh)[4],
                                        const uint32_t (&bl)[4]) {
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
         mma_16816(acc + 4 * n, ah, bh[2 * n], bh[2 * n + 1]);
+        if (LO) mma_16816(cross + 4 * n, al, bl[2 * n], bl[2 * n + 1]);
         mma_16816(cross + 4 * n, ah, bl[2 * n], bl[2 * n + 1]);
         mma_16816(cross + 4 * n, al, bh[2 * n], bh[2 * n + 1]);
     }
@@ -807,7 +814,11 @@ __global__ void __launch_bounds__(kTThreads, 5)
     __syncthreads();  // all blocks of A, all diagonal blocks of T
 
     // ---- column block b = w of T below the diagonal, as its transpose:
-    // T_rb^T = -(sum_{b <= m < r} T_mb^T A_rm^T) T_rr^T
+    // T_rb^T = -(sum_{b <= m < r} T_mb^T A_rm^T) T_rr^T.
+    // With the products of the lo parts: where keys are nearly the same those do not average out, and T multiplies
+    // A's error from both sides.  At beta near 2 and keys within 8 degrees the state's error is 1.2e-4 of its norm
+    // with them and 6.1e-4 without, at beta near 1 1.8e-5 and 2.1e-5 (256 requests of 32-512 tokens: 640.7 us with,
+    // 637.9 without).  P T goes without them, as its errors reach one output and no state.
     {
         const int b = w;
         uint32_t yh[3][4], yl[3][4];
@@ -824,7 +835,7 @@ __global__ void __launch_bounds__(kTThreads, 5)
                 const uint32_t blk = ab + (rr * (rr - 1) / 2 + b + dm) * 1024 + off_p;
                 ldsm4(blk, bh);
                 ldsm4(blk + 512, bl);
-                prod16(acc, cross, yh[dm], yl[dm], bh, bl);
+                prod16<true>(acc, cross, yh[dm], yl[dm], bh, bl);
             }
             uint32_t zh[4], zl[4];
             float t[8] = {}, tc[8] = {};
@@ -833,7 +844,7 @@ __global__ void __launch_bounds__(kTThreads, 5)
             split_frag(acc, zh, zl);
             ldsm4(td + rr * 1024 + off_p, bh);
             ldsm4(td + rr * 1024 + 512 + off_p, bl);
-            prod16(t, tc, zh, zl, bh, bl);
+            prod16<true>(t, tc, zh, zl, bh, bl);
 #pragma unroll
             for (int e = 0; e < 8; ++e) t[e] = -t[e] - tc[e];
             split_frag(t, zh, zl);
@@ -886,7 +897,7 @@ __global__ void __launch_bounds__(kTThreads, 5)
             const uint32_t at = m == b ? td + b * 1024 + nh * 256 + k * 16 : part_row(parts, b, 0, 16 * m + k, nh);
             ldsm4_t(at, bh);
             ldsm4_t(at + (m == b ? 512 : SZ_PART), bl);
-            prod16(acc, cross, fh[i], fl[i], bh, bl);
+            prod16<false>(acc, cross, fh[i], fl[i], bh, bl);
             if (m == a) {  // the block's last product
 #pragma unroll
                 for (int e = 0; e < 8; ++e) acc[e] += cross[e];
