@@ -388,11 +388,12 @@ la_status la_commit_accepted(const float *inter_states, const int32_t *accept_id
  * than it is.
  * Where cu_seqlens decreases somewhere, a call that goes token by token skips the requests concerned, and
  * one that goes by chunks its whole batch (nothing is written); both report it.
- * Numerics: bf16 products with fp32 accumulation; each operand the kernels compute is a bf16 pair hi + lo (off by at most 2^-16); states are kept, updated and
- * joined in fp32; out is rounded to bf16 once.  A state's error is some 3e-6 of its norm (the token by token
- * form's 1.5e-7); where nearly the same key is written again and again with beta |k|^2 near 2 and no decay,
- * so that a chunk's sums cancel, up to 1.2e-4.  A NaN or an infinity in a request's inputs may reach all of that
- * request's outputs and its state, and nothing of any other request.
+ * Numerics: bf16 products with fp32 accumulation; each operand the kernels compute is a bf16 pair
+ * hi + lo (off by at most 2^-16; below 1e-30 in magnitude by more); states are kept, updated and joined in
+ * fp32; out is rounded to bf16 once.  A state's error is some 3e-6 of its norm (token by token 1.5e-7);
+ * where nearly the same key is written again and again with beta |k|^2 near 2 and no decay, so that a
+ * chunk's sums cancel, some 1e-4.  A NaN or an infinity in a request's inputs may reach all of that request's
+ * outputs and its state, and nothing of any other request.
  */
 la_status la_delta_extend(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, int64_t q_row_stride,
                           int64_t k_row_stride, int64_t v_row_stride, const float *g,
