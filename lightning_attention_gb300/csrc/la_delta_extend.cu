@@ -28,7 +28,8 @@
 // so the three operands that it computes (S, R, U) are the A operands, which a tcgen05.mma takes from
 // tensor memory: a warp converts its lanes where they lie, without a trip through shared memory, and the
 // B operands (the stacked [K; Q] tile, the stacked [T'; P T] tile, K) come in by TMA ahead of the chain.
-// The stacking keeps every product at M = N = 128 (65 cycles an instruction; one of N = 64 takes 45-50).
+// The stacking keeps the products with S and U at M = N = 128 (65 cycles an instruction; one of N = 64 takes
+// 45-50); the one with R leaves out the rows of T' and P T that are zero, so its k-steps have N = 128, 96, 64, 32.
 // P T makes the output a product with R, so nothing of it waits for U.
 //
 // Precision.  Products run in bf16 with fp32 accumulation.  K and Q are used as loaded; the operands
@@ -47,12 +48,12 @@
 //   warp 10     zeroes the K rows past the end of the request's last chunk (they hold the next
 //               request's keys, and 0 x NaN is NaN).
 // Per chunk the chain is X -> R -> T' R -> U -> U^T K -> S; the output pass runs under U^T K.  A chunk takes
-// about 2.4 us: 36 MMAs of 45-65 cycles are half of it, the passes between them (wait, tensor memory to
+// about 2.4 us: 36 MMAs, 24 of 65 cycles and 12 of 65 down to 45 or less, are half of it, the passes between them (wait, tensor memory to
 // registers, pair split, back, barrier) the other half; no two of them overlap along the chain, and a second
 // chain on the SM has room neither in tensor memory (512 columns) nor in shared memory (171 KB).
 // More items than SMs: a CTA per SM takes several in turn, longest first, each from a common count, and warp 8
-// runs ahead of the item that is worked on.  256 requests of 32-512 tokens x 16 heads: 636 us; items dealt out
-// in turn 655, a CTA per item 703.
+// runs ahead of the item that is worked on.  256 requests of 32-512 tokens x 16 heads: 641 us; items dealt out
+// in turn 19 more, a CTA per item 67 more.
 //
 // Every wait ends: mbarrier waits have a deadline (the named barriers below end with them); one that runs out
 // sets the error word and an abort flag that ends every role, then the CTA waits for its copies and MMAs,
@@ -581,7 +582,7 @@ __device__ void check_order(const DeltaParams &p, uint8_t *ws) {
 // of everything: the 16 x 16 blocks of K K^T and Q K^T (mma.sync: a block is too small for tcgen05), the inverse
 // of its diagonal block of I + A by substitution, a lane per column, then the blocks below by T_ab = -T_aa
 // sum A_am T_mb.
-// Measured: 66 us on 8 requests of 512-4096 tokens x 16 heads, 254 us on 256 of 32-512; 40-50 % of DRAM and half
+// Measured: 68 us on 8 requests of 512-4096 tokens x 16 heads, 260 us on 256 of 32-512; 40-50 % of DRAM and half
 // of the issue slots.  Bound by the latency of the dependent small products and the barriers between them, at
 // the 20 warps per SM that its 95 registers allow.  PLAN is a variant of its own, as its code slows the rest down
 // by 4%.

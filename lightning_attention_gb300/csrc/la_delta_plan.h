@@ -18,7 +18,7 @@ struct Cut {
     int segs, ratio;
 };
 constexpr int kMaxSegs = 32;
-constexpr int kSplitSMs = 152;       // chains that run side by side
+constexpr int kSplitSMs = 152;       // SMs of a GB300: chains that run side by side (fewer SMs: the same, in waves)
 constexpr int kSplitMinChunks = 20;  // shorter requests are not split
 // What the join and two more launches cost, and a segment in the join, in chunks of the chain.
 constexpr double kSplitCost = 5., kJoinCost = 1.;
