@@ -445,7 +445,8 @@ la_status la_delta_verify_chain(const la_bf16 *q, const la_bf16 *k, const la_bf1
  * largest magnitude where s > 0; where s = 0 (no magnitude of 127.5 * 2^-127 or more) it is 2^-128, and
  * magnitudes up to that become 0.  Packing a restored state gives it back bit for bit (-0 comes back as
  * 0).  s is at most 248 there, so that every code stands for a finite value: magnitudes above
- * 127.5 * 2^121 are held at code 127, off by less than 2^121, 1/127 of them.  A block that holds an infinity or a NaN has s = 255 and codes 0, and is restored as NaN.
+ * 127.5 * 2^121 are held at code 127, off by less than 2^121, 1/127 of them.  A block that holds an
+ * infinity or a NaN has s = 255 and codes 0, and is restored as NaN.
  *   codes      device, int8 [entries][H][D][D], 16-byte aligned
  *   scales     device, uint8 [entries][H][D][D/32], 4-byte aligned
  *   store_idx  device, int32 [B], each in [0, entries): the entry of request b

@@ -37,9 +37,10 @@
 // that in the mean; U takes R itself in fp32 and only T' R through pairs; products of two pairs leave out that
 // of the lo parts, but for those of the inverse; the state stays in fp32 registers and is never accumulated in
 // tensor memory (which does not round to nearest).  Decays come from ex2.approx (off by 2^-22) and norms from
-// rsqrtf (2 units in the last place), both far below the pairs.  A third part per operand would bring the state's
-// error from 3e-6 of its norm to fp32's and add half to the chain's MMAs, for bits that the bf16 outputs do not
-// show.  Where a chunk's sums cancel (keys nearly the same, beta |k|^2 near 2, no decay) the pairs' errors show
+// rsqrtf (2 units in the last place), both far below the pairs.  The state is off by 3.2e-6 of its norm, of which U's
+// pair is 2.8e-6: a third part of U leaves 1.6e-6 and takes the mixed batch above from 218.5 to 230.8 us, one request
+// of 32,768 tokens x 32 heads from 840 to 895; third parts of S, R and U and a finer inverse would be needed for less
+// than 1e-6, at half again the chain's MMAs.  The outputs are rounded to bf16, 1.7e-3, and show none of it.  Where a chunk's sums cancel (keys nearly the same, beta |k|^2 near 2, no decay) the pairs' errors show
 // more: 1.2e-4 of the norm at keys within 8 degrees.
 //
 // Roles of the chain kernel (384 threads, one CTA per SM):
@@ -48,9 +49,9 @@
 //   warp 10     zeroes the K rows past the end of the request's last chunk (they hold the next
 //               request's keys, and 0 x NaN is NaN).
 // Per chunk the chain is X -> R -> T' R -> U -> U^T K -> S; the output pass runs under U^T K.  A chunk takes
-// about 2.4 us: 36 MMAs, 24 of 65 cycles and 12 of 65 down to 45 or less, are half of it, the passes between them (wait, tensor memory to
-// registers, pair split, back, barrier) the other half; no two of them overlap along the chain, and a second
-// chain on the SM has room neither in tensor memory (512 columns) nor in shared memory (171 KB).
+// about 2.4 us: 36 MMAs, 24 of 65 cycles and 12 of 65 down to 45 or less, are half of it, the passes between them
+// (wait, tensor memory to registers, pair split, back, barrier) the other half; no two of them overlap along the
+// chain, and a second chain on the SM has room neither in tensor memory (512 columns) nor in shared memory (171 KB).
 // More items than SMs: a CTA per SM takes several in turn, longest first, each from a common count, and warp 8
 // runs ahead of the item that is worked on.  256 requests of 32-512 tokens x 16 heads: 641 us; items dealt out
 // in turn 19 more, a CTA per item 67 more.
