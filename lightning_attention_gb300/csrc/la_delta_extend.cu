@@ -40,8 +40,9 @@
 // rsqrtf (2 units in the last place), both far below the pairs.  The state is off by 3.2e-6 of its norm, of which U's
 // pair is 2.8e-6: a third part of U leaves 1.6e-6 and takes the mixed batch above from 218.5 to 230.8 us, one request
 // of 32,768 tokens x 32 heads from 840 to 895; third parts of S, R and U and a finer inverse would be needed for less
-// than 1e-6, at half again the chain's MMAs.  The outputs are rounded to bf16, 1.7e-3, and show none of it.  Where a chunk's sums cancel (keys nearly the same, beta |k|^2 near 2, no decay) the pairs' errors show
-// more: 1.2e-4 of the norm at keys within 8 degrees.
+// than 1e-6, at half again the chain's MMAs.  The outputs are rounded to bf16, 1.7e-3, and show none of it.
+// Where a chunk's sums cancel (keys nearly the same, beta |k|^2 near 2, no decay) the pairs' errors show more: 1.2e-4
+// of the norm at keys within 8 degrees.
 //
 // Roles of the chain kernel (384 threads, one CTA per SM):
 //   warps 0-7   E: the state (32 v rows x 64 k columns a warp) and the passes R, U, O and S;
