@@ -62,7 +62,8 @@ typedef enum {
     LA_ERR_TIMEOUT = 4,      /* a bounded device wait ran out (reported by la_poll_error) */
     LA_ERR_DEVICE_INPUT = 5  /* the device found an index out of range: a slot, cu_seqlens, a
                                 request longer than max_seqlen, a tree parent, an accept or a
-                                track entry (reported by la_poll_error) */
+                                track entry, a page, a cache row, a kv_lens entry (reported by
+                                la_poll_error) */
 } la_status;
 
 typedef uint16_t la_bf16; /* bfloat16 bit pattern */
@@ -463,13 +464,176 @@ la_status la_unpack_states(const int8_t *codes, const uint8_t *scales, int entri
                            const int32_t *state_idx, int B, int H, int D, la_stream stream);
 
 /*
+ * Softmax attention over a paged key/value cache -- the layers that hybrid models put between their linear
+ * ones.  Like the gated delta rule they have no counterpart on the page; tokens, streams, errors and capture are
+ * those of the calls above, so that both kinds of layers run from one batch description.
+ *
+ * The cache: bf16 pages [num_pages][Hkv][page_size][D] of keys, and the same of values; position j of request b
+ * is row j % page_size of page page_table[b][j / page_size].  Arguments shared by the calls:
+ *   k_pages, v_pages  device, 16-byte aligned
+ *   page_stride   elements from one page to the next in both (0: Hkv * page_size * D, packed), a multiple of 8, at
+ *                 least that, so that keys and values may lie in turn in one array
+ *   page_size     16, 32, 64 or 128 (LA_ERR_UNSUPPORTED otherwise)
+ *   page_table    device, int32 [B][max_pages]; entries past a request's last page are not read.  max_pages *
+ *                 page_size is at most 2^30 (LA_ERR_UNSUPPORTED)
+ *   kv_lens       device, int32 [B]: the positions that request b has in the cache, the call's own tokens among
+ *                 them as the last ones (la_kv_store put them there before)
+ *   q, out        device, bf16 rows of H * D elements, 16-byte aligned; q rows q_row_stride elements apart (0:
+ *                 packed; a multiple of 8, at least H * D; ignored for a single row), out packed
+ *   H, Hkv        query heads and kv heads; query head h reads kv head h / (H / Hkv).  H must be a multiple of Hkv
+ *                 (LA_ERR_INVALID), H / Hkv at most 128 (LA_ERR_UNSUPPORTED)
+ *   scale         factor on the scores q . k, finite and positive (LA_ERR_INVALID otherwise); usually D^-0.5
+ * Rows of pages behind a request's positions, and pages that no table names, may hold anything.  Requests may share
+ * pages that no call writes.  A kv_lens entry that is negative, larger than max_pages * page_size, or smaller than the
+ * call's tokens skips its request (its rows of out are left as they were); a page outside [0, num_pages) reads as
+ * zeros, and the rows of its request are undefined; la_poll_error reports both as LA_ERR_DEVICE_INPUT.  A NaN or an infinity in
+ * q reaches its own row and head; one in a request's keys or values may reach all of that request's rows, and nothing
+ * of any other request.  Scores (times scale) beyond fp32 are not supported.
+ */
+
+/* la_rope_scaling -- how the frequencies of rotary positions are stretched for long contexts. */
+typedef enum {
+    LA_ROPE_PLAIN = 0,  /* f_i = base^(-2i / rot_dim) */
+    LA_ROPE_LINEAR = 1, /* f_i / factor: positions are interpolated */
+    LA_ROPE_NTK = 2,    /* base * factor^(rot_dim / (rot_dim - 2)) in place of base */
+    LA_ROPE_YARN = 3    /* f_i / factor where a pair turns less than beta_slow times over orig_len positions, f_i
+                           where it turns more than beta_fast times, a linear ramp over i between (YaRN, Peng et
+                           al. 2023); rotated values times 0.1 ln(factor) + 1 */
+} la_rope_scaling;
+
+/*
+ * la_rope_freqs -- the inverse frequencies of rotary positions (host only, no device work), in double precision.
+ *   rot_dim        rotated values of a head, even, >= 2
+ *   base           > 1, finite (usually 10000)
+ *   factor         >= 1, finite; not read for LA_ROPE_PLAIN
+ *   orig_len, beta_fast, beta_slow   LA_ROPE_YARN only: >= 1, and beta_fast > beta_slow > 0 (usually 32 and 1)
+ *   host_inv_freq  host buffer of rot_dim / 2 doubles, written
+ *   host_mscale    host float, written: the factor on rotated values that la_rope and la_kv_store take
+ * LA_ERR_INVALID for anything else.
+ */
+la_status la_rope_freqs(int rot_dim, double base, la_rope_scaling scaling, double factor, int orig_len,
+                        double beta_fast, double beta_slow, double *host_inv_freq, float *host_mscale);
+
+/*
+ * la_rope -- rotary positions on q and k, before la_extend, la_delta_extend or any other call of theirs: with a = position *
+ * inv_freq[i], pair i of a head becomes
+ *     (x, y) -> mscale * (x cos a - y sin a, x sin a + y cos a),  i = 0 .. rot_dim / 2 - 1
+ * where pair i is columns (i, i + rot_dim / 2) of the head (interleaved == 0) or (2i, 2i + 1) (nonzero); columns from
+ * rot_dim on are copied.
+ *   q, k          device, bf16 rows of H * D and Hkv * D elements, 16-byte aligned, their strides as in the delta calls
+ *   positions     device, int32 [T], any values
+ *   inv_freq      device, fp64 [rot_dim / 2], radians per position (8-byte aligned; not read for rot_dim 0)
+ *   rot_dim       0 .. D, a multiple of 16 (LA_ERR_UNSUPPORTED otherwise)
+ *   q_out, k_out  device, bf16 rows, their strides in q_out_row_stride and k_out_row_stride (0: packed); each may be its input
+ *                 (same pointer and stride), and must not overlap anything else the call reads
+ * Numerics: angles are reduced to one turn in integers, off by some 1e-7 whatever the position; the rotation is in
+ * fp32, rounded to bf16 once.
+ */
+la_status la_rope(const la_bf16 *q, const la_bf16 *k, int64_t q_row_stride, int64_t k_row_stride,
+                  const int32_t *positions, const double *inv_freq, int rot_dim, int interleaved, float mscale,
+                  la_bf16 *q_out, la_bf16 *k_out, int64_t q_out_row_stride, int64_t k_out_row_stride, int T, int H,
+                  int Hkv, int D, la_stream stream);
+
+/*
+ * la_kv_store -- la_rope of q into q_out and of k into pages of the cache, v beside it.
+ *   v             device, bf16 rows of Hkv * D elements
+ *   loc           device, int32 [T]: token t's row of the cache, page * page_size + row; -1: its k and v are not stored
+ *                 (its q is rotated all the same)
+ * The loc entries of one call other than -1 must be distinct.  An entry outside [-1, num_pages * page_size) is treated as -1 and
+ * reported by la_poll_error as LA_ERR_DEVICE_INPUT.  A token's position and its place in the cache need not agree: drafts of a
+ * tree have the position of their depth and a row each.
+ */
+la_status la_kv_store(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, int64_t q_row_stride,
+                      int64_t k_row_stride, int64_t v_row_stride, const int32_t *positions, const double *inv_freq,
+                      int rot_dim, int interleaved, float mscale, la_bf16 *q_out, int64_t q_out_row_stride,
+                      la_bf16 *k_pages, la_bf16 *v_pages, int64_t page_stride, int num_pages, int page_size,
+                      const int32_t *loc, int T, int H, int Hkv, int D, la_stream stream);
+
+/*
+ * la_attn_extend -- causal attention of packed prompts: request b's rows [cu_seqlens[b], cu_seqlens[b+1]) of q are
+ * its last positions in the cache, and each sees the positions at and before its own,
+ *     o_i = sum_{j <= i} e^{scale q_i . k_j} v_j / sum_{j <= i} e^{scale q_i . k_j}
+ * (positions before them: a cached prefix, or earlier chunks of a long prompt).  cu_seqlens, max_seqlen, B, T as for la_extend; rows
+ * of out that belong to no request are left as they were.
+ *   max_kvlen       an upper bound on kv_lens that decides the schedule (any value is right; max_pages * page_size if
+ *                   nothing better is known)
+ *   workspace       device scratch, 16-byte aligned, or NULL.  Where the batch's rows are too few to fill the GPU, the
+ *                   keys of a row are shared out among several CTAs and a second launch joins them; that takes
+ *                   la_attn_extend_workspace_size() bytes.  With NULL or less the call runs without it (same
+ *                   results up to rounding).  Calls that share one must not overlap on the GPU.
+ * Numerics: scores, running references and sums in fp32; weights as bf16 for their product with the values
+ * (2^-9 of each weight, at random), accumulated in fp32; out is rounded to bf16 once.
+ */
+la_status la_attn_extend(const la_bf16 *q, int64_t q_row_stride, const la_bf16 *k_pages, const la_bf16 *v_pages,
+                         int64_t page_stride, int num_pages, int page_size, const int32_t *page_table, int max_pages,
+                         const int32_t *cu_seqlens, const int32_t *kv_lens, la_bf16 *out, int B, int T, int H,
+                         int Hkv, int D, int max_seqlen, int max_kvlen, float scale, void *workspace,
+                         size_t workspace_bytes, la_stream stream);
+
+/*
+ * la_attn_extend_workspace_size -- bytes of scratch la_attn_extend uses for a batch of this shape (0: none).  Host only.
+ */
+la_status la_attn_extend_workspace_size(int B, int T, int H, int Hkv, int D, int max_seqlen, int max_kvlen,
+                                        size_t *bytes);
+
+/*
+ * la_attn_decode -- one token per request (row b of q and out), the request's last position.  A request with kv_lens[b]
+ * 0 (a padded batch) sees nothing: its row is zero.
+ *   workspace       device scratch, 16-byte aligned, of at least la_attn_verify_workspace_size() bytes with N = 1
+ *                   (LA_ERR_INVALID otherwise): the keys are shared out evenly among the SMs, and a second launch
+ *                   joins the requests that several of them shared.  Calls that share one must not overlap on the GPU.
+ * Numerics: as la_attn_extend, with the weights as bf16 pairs hi + lo (2^-16) where at most 64 rows share a kv head's
+ * keys (N * H / Hkv of a block of up to 128), as bf16 above.
+ */
+la_status la_attn_decode(const la_bf16 *q, int64_t q_row_stride, const la_bf16 *k_pages, const la_bf16 *v_pages,
+                         int64_t page_stride, int num_pages, int page_size, const int32_t *page_table, int max_pages,
+                         const int32_t *kv_lens, la_bf16 *out, int B, int H, int Hkv, int D, float scale,
+                         void *workspace, size_t workspace_bytes, la_stream stream);
+
+/*
+ * la_attn_verify_tree -- N draft tokens per request (rows b*N .. b*N+N-1 of q and out), its last N positions: draft t sees the
+ * positions before all drafts, the drafts on its path (parents, as for la_verify_tree: each in [-1, t-1], -1 the context)
+ * and itself.  Nothing is written to the cache; la_kv_commit keeps the accepted path.  N is at most 128
+ * (LA_ERR_UNSUPPORTED).  A request with a parent outside [-1, t-1] is skipped (its rows are left as they were) and
+ * la_poll_error reports LA_ERR_DEVICE_INPUT.  Workspace, empty requests and numerics as for la_attn_decode.
+ */
+la_status la_attn_verify_tree(const la_bf16 *q, int64_t q_row_stride, const la_bf16 *k_pages, const la_bf16 *v_pages,
+                              int64_t page_stride, int num_pages, int page_size, const int32_t *page_table,
+                              int max_pages, const int32_t *kv_lens, const int32_t *parents, la_bf16 *out, int B,
+                              int N, int H, int Hkv, int D, float scale, void *workspace, size_t workspace_bytes,
+                              la_stream stream);
+
+/*
+ * la_attn_verify_workspace_size -- bytes of scratch la_attn_decode (N = 1) and la_attn_verify_tree need, whatever the
+ * batch.  Host only.
+ */
+la_status la_attn_verify_workspace_size(int N, int H, int Hkv, int D, size_t *bytes);
+
+/*
+ * la_kv_commit -- after la_attn_verify_tree, the counterpart of la_commit_accepted: the keys and values of the drafts on the path to draft
+ * accept_idx[b] (-1: none) move to the positions right behind the context, kv_lens[b] - N, in path order, and
+ * new_lens[b] is the length of what is kept, kv_lens[b] - N + (drafts on the path).  Rows behind it are what they
+ * happen to be.
+ *   accept_idx      device, int32 [B], each in [-1, N-1]
+ *   new_lens        device, int32 [B], written; may be kv_lens
+ * The pages of the N drafts' positions must belong to one request.  A request with kv_lens[b] 0 is left alone (new_lens[b]
+ * 0).  An index out of range, a parent on the path outside [-1, t-1], a bad page of the path or a length that does
+ * not fit skips the request (nothing of it is written) and is reported by la_poll_error.
+ */
+la_status la_kv_commit(la_bf16 *k_pages, la_bf16 *v_pages, int64_t page_stride, int num_pages, int page_size,
+                       const int32_t *page_table, int max_pages, const int32_t *kv_lens, const int32_t *parents,
+                       const int32_t *accept_idx, int32_t *new_lens, int B, int N, int Hkv, int D,
+                       la_stream stream);
+
+/*
  * la_poll_error -- synchronise `stream` and then the whole current device (every stream on it),
  * then read and clear the device's error word.  The word is shared by all of the library's
  * kernels on the device, whatever stream they run on, so the device-wide synchronisation makes
  * sure that a fault recorded by a kernel still running on another stream is neither missed nor
  * reported by a later poll.  Returns LA_ERR_TIMEOUT if a bounded device wait ran out,
  * LA_ERR_DEVICE_INPUT if a kernel found a slot index out of range, inconsistent cu_seqlens, a
- * request longer than max_seqlen, a tree parent, commit index or track entry out of range,
+ * request longer than max_seqlen, a tree parent, commit index, track entry, page, cache row or
+ * kv_lens entry out of range,
  * LA_ERR_CUDA if a CUDA error is pending, else LA_OK.  This is the one call that blocks the host
  * (and it cannot be captured in a CUDA graph).
  */

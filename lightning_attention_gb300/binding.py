@@ -29,7 +29,9 @@ EXPORTS = ("la_slopes", "la_extend", "la_extend_ex", "la_extend_workspace_size",
            "la_set_wait_limit", "la_set_column_split", "la_set_persistent", "la_set_balanced", "la_extend_noalloc", "la_extend_gqa",
            "la_extend_gqa_workspace_size", "la_decode_gqa", "la_delta_extend",
            "la_delta_extend_workspace_size", "la_delta_decode",
-           "la_delta_verify_chain", "la_pack_states", "la_unpack_states")
+           "la_delta_verify_chain", "la_pack_states", "la_unpack_states", "la_rope_freqs", "la_rope",
+           "la_kv_store", "la_attn_extend", "la_attn_extend_workspace_size", "la_attn_decode",
+           "la_attn_verify_tree", "la_attn_verify_workspace_size", "la_kv_commit")
 
 
 class LAError(RuntimeError):
@@ -110,6 +112,21 @@ def load():
         lib.la_pack_states.restype = ip
         lib.la_unpack_states.argtypes = [vp, vp, ip, vp, vp, ip, vp, ip, ip, ip, vp]
         lib.la_unpack_states.restype = ip
+        f32, f64, dp = ctypes.c_float, ctypes.c_double, ctypes.POINTER(ctypes.c_double)
+        cache = [vp, vp, i64, ip, ip]  # k_pages, v_pages, page_stride, num_pages, page_size
+        for name, args in (
+                ("la_rope_freqs", [ip, f64, ip, f64, ip, f64, f64, dp, fp]),
+                ("la_rope", [vp, vp, i64, i64, vp, vp, ip, ip, f32, vp, vp, i64, i64, ip, ip, ip, ip, vp]),
+                ("la_kv_store", [vp, vp, vp, i64, i64, i64, vp, vp, ip, ip, f32, vp, i64] + cache +
+                 [vp, ip, ip, ip, ip, vp]),
+                ("la_attn_extend", [vp, i64] + cache + [vp, ip, vp, vp, vp, ip, ip, ip, ip, ip, ip, ip, f32, vp, sz, vp]),
+                ("la_attn_extend_workspace_size", [ip] * 7 + [ctypes.POINTER(sz)]),
+                ("la_attn_decode", [vp, i64] + cache + [vp, ip, vp, vp, ip, ip, ip, ip, f32, vp, sz, vp]),
+                ("la_attn_verify_tree", [vp, i64] + cache + [vp, ip, vp, vp, vp, ip, ip, ip, ip, ip, f32, vp, sz, vp]),
+                ("la_attn_verify_workspace_size", [ip] * 4 + [ctypes.POINTER(sz)]),
+                ("la_kv_commit", cache + [vp, ip, vp, vp, vp, vp, ip, ip, ip, ip, vp])):
+            getattr(lib, name).argtypes = args
+            getattr(lib, name).restype = ip
         _lib = lib
         return lib
 
@@ -687,3 +704,252 @@ def unpack_states(codes, scales, store_idx, state_pool, state_idx) -> None:
                                      num_slots, _ptr(state_idx), B, H, D, _stream_handle(dev))
     if st:
         _check("la_unpack_states", st)
+
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, orig_len: int = 0,
+               beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """Inverse frequencies of rotary positions (la_rope_freqs): (float64 [rot_dim / 2] on the CPU, mscale).  scaling:
+    "none", "linear", "ntk" or "yarn" (which needs orig_len, the length that the model was trained on)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+    buf = (ctypes.c_double * max(rot_dim // 2, 1))()
+    mscale = ctypes.c_float(0.0)
+    _check("la_rope_freqs", load().la_rope_freqs(rot_dim, base, ROPE_SCALINGS[scaling], factor, orig_len, beta_fast,
+                                                 beta_slow, buf, ctypes.byref(mscale)))
+    return torch.tensor(list(buf), dtype=torch.float64), mscale.value
+
+
+_HEAD_DIM = 128
+
+
+def _need_heads(t, name: str) -> int:
+    """Heads of a bf16 [tokens, heads * 128] tensor on a CUDA device."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise TypeError(f"{name} must be a bf16 [tokens, heads * {_HEAD_DIM}] tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a CUDA device, got {t.device}")
+    if t.shape[1] < _HEAD_DIM or t.shape[1] % _HEAD_DIM != 0:
+        raise ValueError(f"{name} must have a multiple of {_HEAD_DIM} columns, got {t.shape[1]}")
+    return t.shape[1] // _HEAD_DIM
+
+
+def _need_pages(k_pages, v_pages, dev):
+    """(pages, kv heads, rows of a page, page stride) of a cache: bf16 [pages, Hkv, P, 128], pages whole, the
+    same distance apart in both."""
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise TypeError(f"k_pages must be a bf16 [pages, Hkv, P, {_HEAD_DIM}] tensor")
+    E, Hkv, P, D = k_pages.shape
+    if D != _HEAD_DIM or E < 1 or Hkv < 1 or P < 1:
+        raise ValueError(f"k_pages must have shape [pages, Hkv, P, {_HEAD_DIM}], got {tuple(k_pages.shape)}")
+    page = Hkv * P * D
+    stride = page if E == 1 else k_pages.stride(0)
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype is not torch.bfloat16:
+            raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+        if t.shape != k_pages.shape:
+            raise ValueError(f"{name} must have shape {tuple(k_pages.shape)}, got {tuple(t.shape)}")
+        if not t[0].is_contiguous() or (E > 1 and t.stride(0) != stride):
+            raise ValueError(f"{name} must have contiguous pages, as far apart as those of k_pages")
+    if stride < page or stride % 8 != 0:
+        raise ValueError(f"pages must lie a multiple of 8 elements, at least {page}, apart; got {stride}")
+    return E, Hkv, P, stride
+
+
+def _need_lists(page_table, kv_lens, dev):
+    """(requests, pages of a table row)."""
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise TypeError("page_table must be an int32 [B, max_pages] tensor")
+    B, width = page_table.shape
+    _need_fast(page_table, "page_table", torch.int32, dev, (B, width))
+    _need_fast(kv_lens, "kv_lens", torch.int32, dev, (B,))
+    return B, width
+
+
+def _rope_args(q, k, positions, inv_freq, q_out):
+    H, Hkv = _need_heads(q, "q"), _need_heads(k, "k")
+    dev, T = q.device, q.shape[0]
+    rs = (_need_rows(q, "q", dev, T, H * _HEAD_DIM), _need_rows(k, "k", dev, T, Hkv * _HEAD_DIM))
+    _need_fast(positions, "positions", torch.int32, dev, (T,))
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+        raise TypeError("inv_freq must be a float64 [rot_dim / 2] tensor")
+    _need_fast(inv_freq, "inv_freq", torch.float64, dev, inv_freq.shape)
+    if q_out is None:
+        q_out = torch.empty((T, H * _HEAD_DIM), dtype=torch.bfloat16, device=dev)
+    return dev, T, H, Hkv, rs, q_out, _need_rows(q_out, "q_out", dev, T, H * _HEAD_DIM)
+
+
+def rope(q, k, positions, inv_freq, interleaved: bool = False, mscale: float = 1.0, q_out=None, k_out=None):
+    """Rotary positions (la_rope): q bf16 [T, H*128], k bf16 [T, Hkv*128] (rows may be strided), positions int32 [T],
+    inv_freq float64 [rot_dim / 2] on the device (rope_freqs); the first rot_dim columns of each head are rotated, as
+    pairs (i, i + rot_dim / 2), or (2i, 2i + 1) where interleaved.  Returns (q_out, k_out); q_out=q and k_out=k
+    rotate in place."""
+    dev, T, H, Hkv, rs, q_out, qo = _rope_args(q, k, positions, inv_freq, q_out)
+    if k_out is None:
+        k_out = torch.empty((T, Hkv * _HEAD_DIM), dtype=torch.bfloat16, device=dev)
+    ko = _need_rows(k_out, "k_out", dev, T, Hkv * _HEAD_DIM)
+    with _on(dev):
+        st = (_lib or load()).la_rope(_ptr(q), _ptr(k), *rs, _ptr(positions), _ptr(inv_freq), 2 * inv_freq.shape[0],
+                                      1 if interleaved else 0, mscale, _ptr(q_out), _ptr(k_out), qo, ko, T, H, Hkv,
+                                      _HEAD_DIM, _stream_handle(dev))
+    if st:
+        _check("la_rope", st)
+    return q_out, k_out
+
+
+def kv_store(q, k, v, positions, inv_freq, k_pages, v_pages, loc, interleaved: bool = False, mscale: float = 1.0,
+             q_out=None):
+    """Rotary positions with the rotated keys and the values stored into a paged cache (la_kv_store): k and v of
+    token t go to row loc[t] % P of page loc[t] // P of k_pages and v_pages, bf16 [pages, Hkv, P, 128]; loc int32 [T],
+    -1: not stored.  Returns q_out; the other arguments are rope's."""
+    dev, T, H, Hkv, rs, q_out, qo = _rope_args(q, k, positions, inv_freq, q_out)
+    E, heads, P, stride = _need_pages(k_pages, v_pages, dev)
+    if heads != Hkv:
+        raise ValueError(f"k has {Hkv} heads, k_pages {heads}")
+    v_rs = _need_rows(v, "v", dev, T, Hkv * _HEAD_DIM)
+    _need_fast(loc, "loc", torch.int32, dev, (T,))
+    with _on(dev):
+        st = (_lib or load()).la_kv_store(_ptr(q), _ptr(k), _ptr(v), *rs, v_rs, _ptr(positions), _ptr(inv_freq),
+                                          2 * inv_freq.shape[0], 1 if interleaved else 0, mscale, _ptr(q_out), qo,
+                                          _ptr(k_pages), _ptr(v_pages), stride, E, P, _ptr(loc), T, H, Hkv, _HEAD_DIM,
+                                          _stream_handle(dev))
+    if st:
+        _check("la_kv_store", st)
+    return q_out
+
+
+def _attn_args(q, k_pages, v_pages, page_table, kv_lens, out, scale):
+    H = _need_heads(q, "q")
+    dev, T = q.device, q.shape[0]
+    q_rs = _need_rows(q, "q", dev, T, H * _HEAD_DIM)
+    E, Hkv, P, stride = _need_pages(k_pages, v_pages, dev)
+    B, width = _need_lists(page_table, kv_lens, dev)
+    if out is None:
+        out = torch.empty((T, H * _HEAD_DIM), dtype=torch.bfloat16, device=dev)
+    else:
+        _need_fast(out, "out", torch.bfloat16, dev, (T, H * _HEAD_DIM))
+    cache = (_ptr(k_pages), _ptr(v_pages), stride, E, P, _ptr(page_table), width)
+    return dev, T, H, Hkv, B, q_rs, cache, out, _HEAD_DIM ** -0.5 if scale is None else scale
+
+
+def attn_extend_workspace_size(B: int, T: int, H: int, Hkv: int, D: int, max_seqlen: int, max_kvlen: int) -> int:
+    """Bytes of scratch la_attn_extend uses for a batch of this shape: 0 where its rows fill the GPU."""
+    n = ctypes.c_size_t(0)
+    _check("la_attn_extend_workspace_size",
+           load().la_attn_extend_workspace_size(B, T, H, Hkv, D, max_seqlen, max_kvlen, ctypes.byref(n)))
+    return int(n.value)
+
+
+def attn_extend(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, out=None, max_seqlen: int | None = None,
+                max_kvlen: int | None = None, scale: float | None = None, workspace=None):
+    """Causal attention of packed prompts over a paged cache (la_attn_extend).  q: bf16 [T, H*128] (rows may be
+    strided); k_pages, v_pages: bf16 [pages, Hkv, P, 128]; page_table: int32 [B, max_pages]; cu_seqlens: int32 [B+1];
+    kv_lens: int32 [B], the positions of each request in the cache, its rows of q the last of them; returns out bf16
+    [T, H*128].  scale: 128 ** -0.5 where it is not given.
+
+    max_seqlen, max_kvlen: upper bounds on the requests' new tokens and positions (T, and what a row of the table holds,
+    where they are not given); the second only picks the schedule.  workspace: uint8 scratch of
+    attn_extend_workspace_size() bytes; allocated on the current stream where it is not given."""
+    dev, T, H, Hkv, B, q_rs, cache, out, scale = _attn_args(q, k_pages, v_pages, page_table, kv_lens, out, scale)
+    _need_fast(cu_seqlens, "cu_seqlens", torch.int32, dev, (B + 1,))
+    max_seqlen = T if max_seqlen is None else int(max_seqlen)
+    max_kvlen = cache[4] * cache[6] if max_kvlen is None else int(max_kvlen)
+    if workspace is None:
+        nbytes = 0 if H % Hkv else attn_extend_workspace_size(B, T, H, Hkv, _HEAD_DIM, max_seqlen, max_kvlen)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", torch.uint8, dev)
+    with _on(dev):
+        st = (_lib or load()).la_attn_extend(_ptr(q), q_rs, *cache, _ptr(cu_seqlens), _ptr(kv_lens), _ptr(out), B, T, H,
+                                             Hkv, _HEAD_DIM, max_seqlen, max_kvlen, scale, _ptr(workspace),
+                                             workspace.numel(), _stream_handle(dev))
+    if st:
+        _check("la_attn_extend", st)
+    return out
+
+
+def attn_verify_workspace_size(N: int, H: int, Hkv: int, D: int) -> int:
+    """Bytes of scratch la_attn_decode (N = 1) and la_attn_verify_tree need, whatever the batch."""
+    n = ctypes.c_size_t(0)
+    _check("la_attn_verify_workspace_size", load().la_attn_verify_workspace_size(N, H, Hkv, D, ctypes.byref(n)))
+    return int(n.value)
+
+
+def _verify_workspace(workspace, N: int, H: int, Hkv: int, dev):
+    if workspace is None:
+        nbytes = 0 if H % Hkv else attn_verify_workspace_size(N, H, Hkv, _HEAD_DIM)
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", torch.uint8, dev)
+    return workspace
+
+
+def attn_decode(q, k_pages, v_pages, page_table, kv_lens, out=None, scale: float | None = None, workspace=None):
+    """Attention of one token per request over a paged cache (la_attn_decode): q bf16 [B, H*128], the last of kv_lens[b]
+    positions; returns out bf16 [B, H*128].  The other arguments are attn_extend's; workspace: uint8 scratch of
+    attn_verify_workspace_size(1, ...) bytes."""
+    dev, T, H, Hkv, B, q_rs, cache, out, scale = _attn_args(q, k_pages, v_pages, page_table, kv_lens, out, scale)
+    if T != B:
+        raise ValueError(f"q must have a row per request, {B}, got {T}")
+    workspace = _verify_workspace(workspace, 1, H, Hkv, dev)
+    with _on(dev):
+        st = (_lib or load()).la_attn_decode(_ptr(q), q_rs, *cache, _ptr(kv_lens), _ptr(out), B, H, Hkv, _HEAD_DIM,
+                                             scale, _ptr(workspace), workspace.numel(), _stream_handle(dev))
+    if st:
+        _check("la_attn_decode", st)
+    return out
+
+
+def attn_verify_tree(q, k_pages, v_pages, page_table, kv_lens, parents, N: int, out=None, scale: float | None = None,
+                     workspace=None):
+    """Attention of N drafts per request over a paged cache (la_attn_verify_tree): q bf16 [B*N, H*128], request b's rows
+    its last N of kv_lens[b] positions; parents int32 [B, N], each in [-1, t-1], -1 the context (a chain: t - 1).
+    Returns out bf16 [B*N, H*128]; kv_commit keeps the accepted drafts."""
+    if N < 1:
+        raise ValueError(f"N must be at least 1, got {N}")
+    N = int(N)
+    dev, T, H, Hkv, B, q_rs, cache, out, scale = _attn_args(q, k_pages, v_pages, page_table, kv_lens, out, scale)
+    if T != B * N:
+        raise ValueError(f"q must have {N} rows per request, {B * N}, got {T}")
+    _need_fast(parents, "parents", torch.int32, dev, (B, N))
+    workspace = _verify_workspace(workspace, N, H, Hkv, dev)
+    with _on(dev):
+        st = (_lib or load()).la_attn_verify_tree(_ptr(q), q_rs, *cache, _ptr(kv_lens), _ptr(parents), _ptr(out), B, N, H,
+                                                  Hkv, _HEAD_DIM, scale, _ptr(workspace), workspace.numel(),
+                                                  _stream_handle(dev))
+    if st:
+        _check("la_attn_verify_tree", st)
+    return out
+
+
+def kv_commit(k_pages, v_pages, page_table, kv_lens, parents, accept_idx, new_lens=None):
+    """Keep the accepted drafts of a tree (la_kv_commit): the rows of the drafts on the path to accept_idx[b] (-1: none) move
+    to the positions behind the context, in place in the pages; returns new_lens int32 [B], the lengths of what is
+    kept (new_lens=kv_lens updates those)."""
+    if not isinstance(k_pages, torch.Tensor):
+        raise TypeError(f"k_pages must be a bf16 [pages, Hkv, P, {_HEAD_DIM}] tensor")
+    dev = k_pages.device
+    if dev.type != "cuda":
+        raise ValueError(f"k_pages must be on a CUDA device, got {dev}")
+    E, Hkv, P, stride = _need_pages(k_pages, v_pages, dev)
+    B, width = _need_lists(page_table, kv_lens, dev)
+    if not isinstance(parents, torch.Tensor) or parents.dim() != 2:
+        raise TypeError("parents must be an int32 [B, N] tensor")
+    N = parents.shape[1]
+    _need_fast(parents, "parents", torch.int32, dev, (B, N))
+    _need_fast(accept_idx, "accept_idx", torch.int32, dev, (B,))
+    if new_lens is None:
+        new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+    else:
+        _need_fast(new_lens, "new_lens", torch.int32, dev, (B,))
+    with _on(dev):
+        st = (_lib or load()).la_kv_commit(_ptr(k_pages), _ptr(v_pages), stride, E, P, _ptr(page_table), width,
+                                           _ptr(kv_lens), _ptr(parents), _ptr(accept_idx), _ptr(new_lens), B, N, Hkv,
+                                           _HEAD_DIM, _stream_handle(dev))
+    if st:
+        _check("la_kv_commit", st)
+    return new_lens

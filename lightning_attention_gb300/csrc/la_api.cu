@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "la.h"
+#include "la_attn.h"
 #include "la_delta.h"
 #include "la_extend_bal.h"
 #include "la_internal.h"
@@ -86,7 +87,7 @@ const char *la_status_string(la_status status) {
         case LA_ERR_TIMEOUT: return "LA_ERR_TIMEOUT: a bounded device wait ran out";
         case LA_ERR_DEVICE_INPUT:
             return "LA_ERR_DEVICE_INPUT: a device-side index (slot, cu_seqlens, parent, accept "
-                   "or track entry) was out of range";
+                   "or track entry, page, cache row or kv_lens) was out of range";
     }
     return "LA_ERR_UNKNOWN";
 }
@@ -131,7 +132,7 @@ la_status la_poll_error(la_stream stream) {
     }
     if (word & la::ERR_BIT_TIMEOUT) return LA_ERR_TIMEOUT;
     if (word & (la::ERR_BIT_SLOT_RANGE | la::ERR_BIT_SEQLENS | la::ERR_BIT_PARENTS |
-                la::ERR_BIT_ACCEPT | la::ERR_BIT_TRACK))
+                la::ERR_BIT_ACCEPT | la::ERR_BIT_TRACK | la::ERR_BIT_PAGE))
         return LA_ERR_DEVICE_INPUT;
     return LA_OK;
 }
@@ -721,6 +722,285 @@ la_status la_unpack_states(const int8_t *codes, const uint8_t *scales, int entri
                                      entries, store_idx, B, H, D);
     if (st != LA_OK || !work) return st;
     return launch_status(la::launch_unpack_states(p, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// A cache's checks that need no device.  `lists`: whether the call has a page table and lengths.
+la_status cache_params(la::CacheParams *c, const la_bf16 *k_pages, const la_bf16 *v_pages,
+                       int64_t page_stride, int num_pages, int page_size, const int32_t *page_table,
+                       int max_pages, const int32_t *kv_lens, int Hkv, int D, bool lists) {
+    if (num_pages < 1 || page_size < 1 || Hkv < 1 || D < 1 || (lists && max_pages < 1)) return LA_ERR_INVALID;
+    if (D != la::kHeadDim) return LA_ERR_UNSUPPORTED;
+    if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return LA_ERR_UNSUPPORTED;
+    const long long page = (long long)Hkv * page_size * la::kHeadDim;
+    if (page_stride == 0) page_stride = page;
+    if (page_stride < page || page_stride % 8 != 0) return LA_ERR_INVALID;
+    if (page_stride >= (1ll << 38) || (long long)num_pages * page_stride >= (1ll << 44)) return LA_ERR_UNSUPPORTED;
+    if (lists && (long long)max_pages * page_size > (1ll << 30)) return LA_ERR_UNSUPPORTED;
+    *c = la::CacheParams{};
+    c->k = reinterpret_cast<__nv_bfloat16 *>(const_cast<la_bf16 *>(k_pages));
+    c->v = reinterpret_cast<__nv_bfloat16 *>(const_cast<la_bf16 *>(v_pages));
+    c->page_stride = page_stride;
+    c->page_table = page_table;
+    c->kv_lens = kv_lens;
+    c->num_pages = num_pages;
+    c->page_size = page_size;
+    c->max_pages = max_pages;
+    return LA_OK;
+}
+
+bool cache_pointers_ok(const la::CacheParams &c, bool lists) {
+    if (!c.k || !c.v || !aligned16(c.k) || !aligned16(c.v)) return false;
+    return !lists || (c.page_table && c.kv_lens && aligned4(c.page_table) && aligned4(c.kv_lens));
+}
+
+la_status rope_params(la::RopeParams *p, const la_bf16 *q, const la_bf16 *k, int64_t q_rs, int64_t k_rs,
+                      const int32_t *positions, const double *inv_freq, int rot_dim, int interleaved,
+                      float mscale, la_bf16 *q_out, int64_t qo_rs, int T, int H, int Hkv, int D) {
+    if (T < 0 || H < 1 || Hkv < 1 || D < 1 || rot_dim < 0 || rot_dim > D || !isfinite(mscale))
+        return LA_ERR_INVALID;
+    if (D != la::kHeadDim || rot_dim % 16 != 0) return LA_ERR_UNSUPPORTED;
+    if ((long long)H + 2ll * Hkv > 0x7fff0000LL / la::kHeadDim) return LA_ERR_UNSUPPORTED;
+    if (!row_stride_ok(&q_rs, T, (long long)H * D) || !row_stride_ok(&k_rs, T, (long long)Hkv * D) ||
+        !row_stride_ok(&qo_rs, T, (long long)H * D))
+        return LA_ERR_INVALID;
+    *p = la::RopeParams{};
+    p->q = reinterpret_cast<const __nv_bfloat16 *>(q);
+    p->k = reinterpret_cast<const __nv_bfloat16 *>(k);
+    p->q_rs = q_rs;
+    p->k_rs = k_rs;
+    p->positions = positions;
+    p->inv_freq = inv_freq;
+    p->q_out = reinterpret_cast<__nv_bfloat16 *>(q_out);
+    p->qo_rs = qo_rs;
+    p->mscale = mscale;
+    p->T = T;
+    p->H = H;
+    p->Hkv = Hkv;
+    p->rot = rot_dim;
+    p->interleaved = interleaved != 0;
+    return LA_OK;
+}
+
+bool rope_pointers_ok(const la::RopeParams &p) {
+    if (!p.q || !p.k || !p.q_out || !p.positions || (p.rot > 0 && !p.inv_freq)) return false;
+    return aligned16(p.q) && aligned16(p.k) && aligned16(p.q_out) && aligned4(p.positions) &&
+           (reinterpret_cast<uintptr_t>(p.inv_freq) & 7u) == 0;
+}
+
+// Checks shared by the attention calls, of `tokens` rows; work == false: nothing to launch.
+la_status attn_params(la::AttnParams *p, bool *work, const la_bf16 *q, int64_t q_rs, const la::CacheParams &c,
+                      la_bf16 *out, int B, long long tokens, int H, int Hkv, float scale) {
+    *work = false;
+    if (B < 0 || tokens < 0 || H < 1 || H % Hkv != 0 || !(scale > 0.f) || !isfinite(scale)) return LA_ERR_INVALID;
+    if (tokens > 0x7fffffffLL) return LA_ERR_INVALID;
+    if (H / Hkv > la::kMaxDrafts) return LA_ERR_UNSUPPORTED;
+    if (!row_stride_ok(&q_rs, tokens, (long long)H * la::kHeadDim)) return LA_ERR_INVALID;
+    if (q_rs >= (1ll << 38)) return LA_ERR_UNSUPPORTED;
+    if (B == 0 || tokens == 0) return LA_OK;
+    if (!q || !out || !aligned16(q) || !aligned16(out) || !cache_pointers_ok(c, true)) return LA_ERR_INVALID;
+    *p = la::AttnParams{};
+    p->q = reinterpret_cast<const __nv_bfloat16 *>(q);
+    p->q_rs = q_rs;
+    p->cache = c;
+    p->out = reinterpret_cast<__nv_bfloat16 *>(out);
+    p->scale_log2 = scale * 1.4426950408889634f;
+    p->B = B;
+    p->T = (int)tokens;
+    p->H = H;
+    p->Hkv = Hkv;
+    p->group = H / Hkv;
+    p->N = 1;
+    const unsigned long long us = g_wait_limit.load();
+    p->wait_limit_ns = (us == 0 ? kDefaultWaitLimitUs : us) * 1000ull;
+    *work = true;
+    return LA_OK;
+}
+
+la_status attn_verify(const la_bf16 *q, int64_t q_rs, const la_bf16 *k_pages, const la_bf16 *v_pages,
+                      int64_t page_stride, int num_pages, int page_size, const int32_t *page_table, int max_pages,
+                      const int32_t *kv_lens, const int32_t *parents, bool tree, la_bf16 *out, int B, int N, int H,
+                      int Hkv, int D, float scale, void *workspace, size_t workspace_bytes, la_stream stream) {
+    la::CacheParams c;
+    la::AttnParams p;
+    bool work;
+    la_status st = cache_params(&c, k_pages, v_pages, page_stride, num_pages, page_size, page_table, max_pages,
+                                kv_lens, Hkv, D, true);
+    if (st != LA_OK) return st;
+    if (N < 1) return LA_ERR_INVALID;
+    if (N > la::kMaxDrafts) return LA_ERR_UNSUPPORTED;
+    st = attn_params(&p, &work, q, q_rs, c, out, B, (long long)B * N, H, Hkv, scale);
+    if (st != LA_OK || !work) return st;
+    if (tree && (!parents || !aligned4(parents))) return LA_ERR_INVALID;
+    if ((long long)p.B * Hkv * N > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;  // blocks of the second launch, at most
+    if (!workspace || !aligned16(workspace) ||
+        (unsigned long long)workspace_bytes < la::attn_verify_ws_bytes(N, p.group))
+        return LA_ERR_INVALID;
+    p.parents = tree ? parents : nullptr;
+    p.N = N;
+    p.ws = workspace;
+    if ((st = error_word_ptr(&p.err)) != LA_OK) return st;
+    return launch_status(la::launch_attn_verify(p, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+la_status la_rope_freqs(int rot_dim, double base, la_rope_scaling scaling, double factor, int orig_len,
+                        double beta_fast, double beta_slow, double *host_inv_freq, float *host_mscale) {
+    if (rot_dim < 2 || rot_dim % 2 != 0 || !(base > 1.0) || !isfinite(base) || !host_inv_freq || !host_mscale)
+        return LA_ERR_INVALID;
+    if (scaling < LA_ROPE_PLAIN || scaling > LA_ROPE_YARN) return LA_ERR_INVALID;
+    if (scaling != LA_ROPE_PLAIN && (!(factor >= 1.0) || !isfinite(factor))) return LA_ERR_INVALID;
+    if (scaling == LA_ROPE_YARN &&
+        (orig_len < 1 || !(beta_fast > beta_slow) || !(beta_slow > 0.0) || !isfinite(beta_fast)))
+        return LA_ERR_INVALID;
+    if (scaling == LA_ROPE_NTK && rot_dim > 2) base *= pow(factor, (double)rot_dim / (rot_dim - 2));
+    // the (real) index of the pair that turns `turns` times over the original length
+    auto index_of = [&](double turns) {
+        return rot_dim * log(orig_len / (turns * 6.283185307179586477)) / (2.0 * log(base));
+    };
+    double lo = 0.0, hi = 0.0;
+    if (scaling == LA_ROPE_YARN) {
+        lo = std::max(floor(index_of(beta_fast)), 0.0);
+        hi = std::min(ceil(index_of(beta_slow)), (double)(rot_dim - 1));
+    }
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        double f = pow(base, -2.0 * i / rot_dim);
+        if (scaling == LA_ROPE_LINEAR) f /= factor;
+        if (scaling == LA_ROPE_YARN) {
+            const double ramp = std::min(std::max((i - lo) / std::max(hi - lo, 1e-3), 0.0), 1.0);
+            f = f / factor * ramp + f * (1.0 - ramp);
+        }
+        host_inv_freq[i] = f;
+    }
+    *host_mscale = scaling == LA_ROPE_YARN ? (float)(0.1 * log(factor) + 1.0) : 1.f;
+    return LA_OK;
+}
+
+la_status la_rope(const la_bf16 *q, const la_bf16 *k, int64_t q_row_stride, int64_t k_row_stride,
+                  const int32_t *positions, const double *inv_freq, int rot_dim, int interleaved, float mscale,
+                  la_bf16 *q_out, la_bf16 *k_out, int64_t q_out_row_stride, int64_t k_out_row_stride, int T, int H,
+                  int Hkv, int D, la_stream stream) {
+    la::RopeParams p;
+    const la_status st = rope_params(&p, q, k, q_row_stride, k_row_stride, positions, inv_freq, rot_dim, interleaved,
+                                     mscale, q_out, q_out_row_stride, T, H, Hkv, D);
+    if (st != LA_OK) return st;
+    if (!row_stride_ok(&k_out_row_stride, T, (long long)Hkv * D)) return LA_ERR_INVALID;
+    if (T == 0) return LA_OK;
+    if (!rope_pointers_ok(p) || !k_out || !aligned16(k_out)) return LA_ERR_INVALID;
+    p.k_out = reinterpret_cast<__nv_bfloat16 *>(k_out);
+    p.ko_rs = k_out_row_stride;
+    return launch_status(la::launch_rope(p, static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_kv_store(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, int64_t q_row_stride,
+                      int64_t k_row_stride, int64_t v_row_stride, const int32_t *positions, const double *inv_freq,
+                      int rot_dim, int interleaved, float mscale, la_bf16 *q_out, int64_t q_out_row_stride,
+                      la_bf16 *k_pages, la_bf16 *v_pages, int64_t page_stride, int num_pages, int page_size,
+                      const int32_t *loc, int T, int H, int Hkv, int D, la_stream stream) {
+    la::RopeParams p;
+    la_status st = rope_params(&p, q, k, q_row_stride, k_row_stride, positions, inv_freq, rot_dim, interleaved, mscale,
+                               q_out, q_out_row_stride, T, H, Hkv, D);
+    if (st != LA_OK) return st;
+    st = cache_params(&p.cache, k_pages, v_pages, page_stride, num_pages, page_size, nullptr, 0, nullptr, Hkv, D, false);
+    if (st != LA_OK) return st;
+    if (!row_stride_ok(&v_row_stride, T, (long long)Hkv * D)) return LA_ERR_INVALID;
+    if (T == 0) return LA_OK;
+    if (!rope_pointers_ok(p) || !v || !aligned16(v) || !loc || !aligned4(loc) || !cache_pointers_ok(p.cache, false))
+        return LA_ERR_INVALID;
+    p.v = reinterpret_cast<const __nv_bfloat16 *>(v);
+    p.v_rs = v_row_stride;
+    p.loc = loc;
+    if ((st = error_word_ptr(&p.err)) != LA_OK) return st;
+    return launch_status(la::launch_rope(p, static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_attn_extend_workspace_size(int B, int T, int H, int Hkv, int D, int max_seqlen, int max_kvlen,
+                                        size_t *bytes) {
+    if (B < 0 || T < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || D < 1 || max_seqlen < 0 || max_kvlen < 0 ||
+        bytes == nullptr)
+        return LA_ERR_INVALID;
+    if (D != la::kHeadDim || H / Hkv > la::kMaxDrafts) return LA_ERR_UNSUPPORTED;
+    *bytes = (size_t)la::plan_attn_extend(B, T, H, Hkv, max_seqlen, max_kvlen).ws_bytes;
+    return LA_OK;
+}
+
+la_status la_attn_extend(const la_bf16 *q, int64_t q_row_stride, const la_bf16 *k_pages, const la_bf16 *v_pages,
+                         int64_t page_stride, int num_pages, int page_size, const int32_t *page_table, int max_pages,
+                         const int32_t *cu_seqlens, const int32_t *kv_lens, la_bf16 *out, int B, int T, int H,
+                         int Hkv, int D, int max_seqlen, int max_kvlen, float scale, void *workspace,
+                         size_t workspace_bytes, la_stream stream) {
+    la::CacheParams c;
+    la::AttnParams p;
+    bool work;
+    la_status st = cache_params(&c, k_pages, v_pages, page_stride, num_pages, page_size, page_table, max_pages,
+                                kv_lens, Hkv, D, true);
+    if (st != LA_OK) return st;
+    if (max_seqlen < 0 || max_kvlen < 0) return LA_ERR_INVALID;
+    st = attn_params(&p, &work, q, q_row_stride, c, out, B, T, H, Hkv, scale);
+    if (st != LA_OK || !work) return st;
+    if (!cu_seqlens || !aligned4(cu_seqlens) || !aligned16(workspace)) return LA_ERR_INVALID;
+    la::AttnExtendPlan plan = la::plan_attn_extend(B, T, H, Hkv, max_seqlen, max_kvlen);
+    if (plan.ws_bytes > 0 && (!workspace || (unsigned long long)workspace_bytes < plan.ws_bytes)) plan.nsplit = 1;
+    if (plan.items * plan.nsplit > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
+    p.cu_seqlens = cu_seqlens;
+    p.max_seqlen = max_seqlen;
+    p.ws = workspace;
+    if ((st = error_word_ptr(&p.err)) != LA_OK) return st;
+    return launch_status(la::launch_attn_extend(p, plan, static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_attn_verify_workspace_size(int N, int H, int Hkv, int D, size_t *bytes) {
+    if (N < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || D < 1 || bytes == nullptr) return LA_ERR_INVALID;
+    if (D != la::kHeadDim || N > la::kMaxDrafts || H / Hkv > la::kMaxDrafts) return LA_ERR_UNSUPPORTED;
+    *bytes = (size_t)la::attn_verify_ws_bytes(N, H / Hkv);
+    return LA_OK;
+}
+
+la_status la_attn_decode(const la_bf16 *q, int64_t q_row_stride, const la_bf16 *k_pages, const la_bf16 *v_pages,
+                         int64_t page_stride, int num_pages, int page_size, const int32_t *page_table, int max_pages,
+                         const int32_t *kv_lens, la_bf16 *out, int B, int H, int Hkv, int D, float scale,
+                         void *workspace, size_t workspace_bytes, la_stream stream) {
+    return attn_verify(q, q_row_stride, k_pages, v_pages, page_stride, num_pages, page_size, page_table, max_pages,
+                       kv_lens, nullptr, false, out, B, 1, H, Hkv, D, scale, workspace, workspace_bytes, stream);
+}
+
+la_status la_attn_verify_tree(const la_bf16 *q, int64_t q_row_stride, const la_bf16 *k_pages, const la_bf16 *v_pages,
+                              int64_t page_stride, int num_pages, int page_size, const int32_t *page_table,
+                              int max_pages, const int32_t *kv_lens, const int32_t *parents, la_bf16 *out, int B,
+                              int N, int H, int Hkv, int D, float scale, void *workspace, size_t workspace_bytes,
+                              la_stream stream) {
+    return attn_verify(q, q_row_stride, k_pages, v_pages, page_stride, num_pages, page_size, page_table, max_pages,
+                       kv_lens, parents, true, out, B, N, H, Hkv, D, scale, workspace, workspace_bytes, stream);
+}
+
+la_status la_kv_commit(la_bf16 *k_pages, la_bf16 *v_pages, int64_t page_stride, int num_pages, int page_size,
+                       const int32_t *page_table, int max_pages, const int32_t *kv_lens, const int32_t *parents,
+                       const int32_t *accept_idx, int32_t *new_lens, int B, int N, int Hkv, int D,
+                       la_stream stream) {
+    la::KvCommitParams p = la::KvCommitParams{};
+    la_status st = cache_params(&p.cache, k_pages, v_pages, page_stride, num_pages, page_size, page_table, max_pages,
+                                kv_lens, Hkv, D, true);
+    if (st != LA_OK) return st;
+    if (B < 0 || N < 1) return LA_ERR_INVALID;
+    if (N > la::kMaxDrafts) return LA_ERR_UNSUPPORTED;
+    if (B == 0) return LA_OK;
+    if (!cache_pointers_ok(p.cache, true) || !parents || !accept_idx || !new_lens || !aligned4(parents) ||
+        !aligned4(accept_idx) || !aligned4(new_lens))
+        return LA_ERR_INVALID;
+    p.parents = parents;
+    p.accept_idx = accept_idx;
+    p.new_lens = new_lens;
+    p.B = B;
+    p.N = N;
+    p.Hkv = Hkv;
+    if ((st = error_word_ptr(&p.err)) != LA_OK) return st;
+    return launch_status(la::launch_kv_commit(p, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,136 @@
+// la_attn.cuh -- what the two attention kernels share on the device: loads of key and value tiles
+// through the page table, MMAs issued from a converged warp, waits, packed arithmetic.
+#pragma once
+
+#include "la_attn.h"
+#include "la_sm100.cuh"
+
+namespace la {
+namespace attn {
+
+using namespace sm100;
+
+constexpr int kTileBytes = kKeyTile * kHeadDim * 2;  // a tile of keys or values: two blocks of 64
+constexpr int kHalfBytes = kTileBytes / 2;           // columns, rows of 128 bytes, 128-byte swizzle
+
+// 5D tiled load: coordinates (column, row, block of 64 columns, kv head, page).
+__device__ __forceinline__ void tma_load_5d(void *smem_dst, const void *tmap, uint64_t *bar, int c0,
+                                            int c1, int c2, int c3, int c4) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+        "r"(c4)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void *smem_dst, const void *tmap, uint64_t *bar, int c0,
+                                            int c1, int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+// Lane l < 128 / page_size: the page that holds positions pos .. of request b, pos = tile * 128 + l *
+// page_size; num_pages, whose rows a tiled load fills with zeros, where the request has no such position
+// or the table names a page that does not exist (which is reported).
+__device__ __forceinline__ int page_of(const CacheParams &c, int b, int kv_len, int tile, int lane,
+                                       unsigned int *err) {
+    const long long pos = (long long)tile * kKeyTile + (long long)lane * c.page_size;
+    if (lane >= kKeyTile / c.page_size || pos >= kv_len) return c.num_pages;
+    const int page = c.page_table[(long long)b * c.max_pages + pos / c.page_size];
+    if (page >= 0 && page < c.num_pages) return page;
+    atomicOr(err, ERR_BIT_PAGE);
+    return c.num_pages;
+}
+
+// A whole warp brings one tile in; `page` is page_of's.  Every row of the tile is written.
+__device__ __forceinline__ void load_tile(const CUtensorMap *map, uint8_t *dst, uint64_t *bar, int page,
+                                          int page_size, int head, int lane) {
+    if (lane == 0) mbar_arrive_expect_tx(bar, kTileBytes);
+    __syncwarp();
+    if (lane < kKeyTile / page_size) {
+        uint8_t *at = dst + lane * page_size * 128;
+        tma_load_5d(at, map, bar, 0, 0, 0, head, page);
+        tma_load_5d(at + kHalfBytes, map, bar, 0, 0, 1, head, page);
+    }
+}
+
+// One lane issues (lead != 0 in it alone), the warp stays converged: the operands are formed by the
+// uniform datapath, and an issue takes less than the MMA.
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t lead, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_u32(bar)),
+        "r"(lead)
+        : "memory");
+}
+
+// A bounded wait; the first to give up reports it.
+struct Waiter {
+    uint64_t limit_ns;
+    unsigned int *err;
+    __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const {
+        if (mbar_wait(bar, parity, limit_ns)) return true;
+        atomicOr(err, ERR_BIT_TIMEOUT);
+        return false;
+    }
+};
+
+// Two fp32 values in one register pair.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void f2_get(uint64_t x, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+}  // namespace attn
+
+// TMA maps (host): pages of a cache, boxes of 64 columns x page_size rows; rows of q, boxes of 64 columns
+// x the query heads of a group x `tokens` tokens.
+bool make_pages_map(CUtensorMap *m, const void *pages, const CacheParams &c, int Hkv);
+bool make_query_map(CUtensorMap *m, const void *q, long long rows, int H, long long row_stride, int group,
+                    int tokens);
+
+}  // namespace la

@@ -1,0 +1,702 @@
+// la_attn_verify.cu -- softmax attention of single tokens and of drafted trees over a paged key/value
+// cache.  The N drafts of a request are its last N positions; draft t sees the positions before them, its
+// ancestors and itself:
+//     o_r = sum_j e^{s_rj - m_r} v_j / sum_j e^{s_rj - m_r},   s_rj = scale q_r . k_j
+// for the R = (drafts) x (query heads of a kv head) rows r that share the keys, each key read once.
+//
+// Bound by HBM: 512 bytes a key and kv head.  The work is the sequence of all tiles of 128 keys, request by
+// request and head by head, cut into equal runs, one CTA per SM each: the SMs finish together whatever the
+// lengths.  A run may begin or end inside a (request, head); those leave unnormalised sums, which a second
+// launch joins in a fixed order.
+//
+// With few rows the keys take the 128 lanes of the tensor cores: S^T = K Q^T and O^T += V^T P^T, both with
+// N = R (padded to 16, 32, 64 or 128), K and V as they lie in their pages.  A thread owns a key in the
+// softmax and a column of v in the result.  The reference m_r is that of the first tile and follows only
+// when a score passes it by more than 2^8, so that a tile takes no maximum, one test; the sums of P come from the
+// same product, as the row of a matrix of ones.  P goes into shared memory as bf16 pairs hi + lo (off by at
+// most 2^-16), which the idle tensor cores take at no cost.
+#include <string.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "la_attn.cuh"
+
+namespace la {
+namespace {
+
+using namespace attn;
+
+constexpr int kThreads = 192;  // warps 0-3: softmax, 4: MMAs, 5: loads
+constexpr int kMmaWarp = 4, kLoadWarp = 5;
+constexpr int kBarSoftmax = 1;
+
+// What fits into 227 KB.  With 128 rows P is one bf16 (2^-9 of each weight): the products with the second
+// part would take the tensor cores as long as HBM takes for the tile.
+template <int RP>
+struct Shape {
+    static constexpr int kQBufs = RP <= 64 ? 2 : 1, kPBufs = RP <= 32 ? 2 : 1;
+    static constexpr int kSlots = RP <= 32 ? 5 : 4;       // tiles of keys and values
+    static constexpr int kParts = RP <= 64 ? 2 : 1;       // of P: hi, lo
+    static constexpr uint32_t kQBytes = RP * 256, kPart = kKeyTile * RP * 2, kPBytes = kParts * kPart;
+    static constexpr uint32_t kOffKV = 0;
+    static constexpr uint32_t kOffQ = kOffKV + kSlots * kTileBytes;
+    static constexpr uint32_t kOffP = kOffQ + kQBufs * kQBytes;
+    static constexpr uint32_t kOffOnes = kOffP + kPBufs * kPBytes;
+    static constexpr uint32_t kOffBars = kOffOnes + 4096;
+    // columns of tensor memory: S twice, O, sums
+    static constexpr uint32_t kTmO = 2 * RP, kTmL = 3 * RP, kTmCols = 4 * RP;
+};
+
+template <int RP>
+struct Bars {
+    uint64_t full[5], empty[5];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], p_empty[2], pv_done, o_full, o_free, drain;
+    alignas(16) float neg_m[RP];        // minus the references, in log 2; inf where a row has seen no key
+    alignas(16) float factor[RP];
+    float top[4][RP];
+    uint8_t tok_of[RP];
+    uint32_t below[kMaxDrafts][4];      // below[a] bit t: draft t is a or descends from it
+    long long x0, x1;                   // the CTA's run of tiles
+    int b0;                             // its first request
+    long long rem0;                     // its place among that request's tiles
+    uint32_t tmem_base;
+};
+
+// Tiles of a (request, kv head); 0: no keys, or lengths that do not fit.
+__device__ __forceinline__ int tiles_of(const AttnParams &p, int b) {
+    const int kv = p.cache.kv_lens[b];
+    if (kv < p.N || kv > (long long)p.cache.max_pages * p.cache.page_size) return 0;
+    return (kv + kKeyTile - 1) / kKeyTile;
+}
+
+// Sum of tiles over all requests, and over those before `upto`: one warp, 256 requests at a time.
+__device__ __forceinline__ long long sum_tiles(const AttnParams &p, int upto, long long *head) {
+    const int lane = threadIdx.x & 31;
+    long long all = 0, before = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 256) {
+        int t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = b0 + i * 32 + lane < p.B ? tiles_of(p, b0 + i * 32 + lane) : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            all += t[i];
+            if (b0 + i * 32 + lane < upto) before += t[i];
+        }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, d);
+        before += __shfl_xor_sync(0xffffffffu, before, d);
+    }
+    if (head) *head = before;
+    return all;
+}
+
+// The request whose tiles (times `per`: kv heads and blocks of drafts) hold place x, and the place within it.
+__device__ __forceinline__ void find_place(const AttnParams &p, long long x, int per, int &b, long long &rem) {
+    const int lane = threadIdx.x & 31;
+    long long before = 0;
+    b = 0;
+    rem = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const long long mine = b0 + lane < p.B ? (long long)tiles_of(p, b0 + lane) * per : 0;
+        long long upto = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += y;
+        }
+        upto += before;
+        const unsigned hit = __ballot_sync(0xffffffffu, x >= upto - mine && x < upto);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            b = b0 + src;
+            rem = x - __shfl_sync(0xffffffffu, upto - mine, src);
+            return;
+        }
+        before = __shfl_sync(0xffffffffu, upto, 31);
+    }
+}
+
+// The (request, kv head, block of drafts)s of a CTA's run, in order.
+struct Walk {
+    int b, kvh, rb, tiles, j0, j1, kv_len;
+    long long left;
+    int blocks;
+    __device__ __forceinline__ void start(const AttnParams &p, int blocks_, int b_, long long rem, long long n) {
+        blocks = blocks_;
+        b = b_;
+        left = n;
+        if (n <= 0) return;
+        tiles = tiles_of(p, b);
+        kv_len = p.cache.kv_lens[b];
+        const int item = (int)(rem / tiles);
+        kvh = item / blocks;
+        rb = item - kvh * blocks;
+        j0 = (int)(rem - (long long)item * tiles);
+        j1 = (int)min((long long)tiles, j0 + left);
+    }
+    __device__ __forceinline__ bool done() const { return left <= 0; }
+    __device__ __forceinline__ void next(const AttnParams &p) {
+        left -= j1 - j0;
+        if (left <= 0) return;
+        if (++rb == blocks) {
+            rb = 0;
+            if (++kvh == p.Hkv) {
+                kvh = 0;
+                do {
+                    tiles = tiles_of(p, ++b);  // left > 0: a request with keys follows
+                } while (tiles == 0);
+                kv_len = p.cache.kv_lens[b];
+            }
+        }
+        j0 = 0;
+        j1 = (int)min((long long)tiles, left);
+    }
+};
+
+__device__ __forceinline__ bool softmax_any(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "n"(kBarSoftmax)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void softmax_sync() {
+    asm volatile("barrier.cta.sync %0, 128;" ::"n"(kBarSoftmax) : "memory");
+}
+__device__ __forceinline__ float redux_max(float x) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Which drafts descend from which; false if a parent is out of range.  128 threads.
+template <int RP>
+__device__ bool build_tree(const AttnParams &p, Bars<RP> *bars, int b, int tid) {
+    softmax_sync();  // the last request's table is not read any more
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bars->below[tid][i] = 0;
+    softmax_sync();
+    bool bad = false;
+    if (tid < p.N) {
+        const int32_t *par = p.parents + (long long)b * p.N;
+        int a = tid;
+        while (true) {
+            atomicOr(&bars->below[a][tid >> 5], 1u << (tid & 31));
+            const int up = par[a];
+            if (up == -1) break;
+            if (up < 0 || up >= a) {
+                bad = true;
+                break;
+            }
+            a = up;
+        }
+    }
+    return !softmax_any(bad);
+}
+
+template <int RP>
+__device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint32_t tbase, int warp, int lane,
+                             int blocks, int tok_block, const Waiter &wait) {
+    using S = Shape<RP>;
+    const int tid = warp * 32 + lane;
+    const uint32_t lanes = (uint32_t)warp << 21;
+    const float c = p.scale_log2;
+    // rows without keys: a request of no positions
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        const int kv = p.cache.kv_lens[b];
+        if (kv == 0) {
+            for (int i = tid; i < p.N * p.H * (kHeadDim / 8); i += 128)
+                reinterpret_cast<uint4 *>(p.out + (long long)b * p.N * p.H * kHeadDim)[i] = make_uint4(0, 0, 0, 0);
+        } else if (tiles_of(p, b) == 0 && tid == 0) {
+            atomicOr(p.err, ERR_BIT_PAGE);
+        }
+    }
+    Walk w;
+    w.start(p, blocks, bars->b0, bars->rem0, bars->x1 - bars->x0);
+    int tile = 0, item = 0, tree_of = -1;
+    bool ok = true, sound = true;
+    for (; !w.done(); w.next(p), ++item) {
+        if (p.parents && tree_of != w.b) {
+            sound = build_tree(p, bars, w.b, tid);
+            if (!sound && tid == 0) atomicOr(p.err, ERR_BIT_PARENTS);
+            tree_of = w.b;
+        }
+        const int ctx = w.kv_len - p.N;
+        for (int j = w.j0; j < w.j1; ++j, ++tile) {
+            const int buf = tile & 1, pbuf = tile % S::kPBufs;
+            ok = ok && __all_sync(0xffffffffu, wait(&bars->s_full[buf], (uint32_t)(tile >> 1) & 1));
+            if (tile >= S::kPBufs)
+                ok = ok && __all_sync(0xffffffffu, wait(&bars->p_empty[pbuf],
+                                                        (uint32_t)(tile / S::kPBufs - 1) & 1));
+            tc_fence_after();
+            float s[RP];
+#pragma unroll
+            for (int i = 0; i < RP; i += 16) {
+                uint32_t r[16];
+                tmem_ld16(tbase + lanes + buf * RP + i, r);
+                tmem_ld_wait_regs(r);
+#pragma unroll
+                for (int x = 0; x < 16; ++x) s[i + x] = __uint_as_float(r[x]);
+            }
+            const int pos = j * kKeyTile + tid;
+            if ((j + 1) * kKeyTile > ctx) {  // the tile holds drafts, or ends behind the request
+                const int d = pos - ctx;
+                if (d >= p.N) {
+#pragma unroll
+                    for (int r = 0; r < RP; ++r) s[r] = -INFINITY;
+                } else if (d >= 0 && p.parents) {
+                    uint32_t see[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) see[i] = bars->below[d][i];
+#pragma unroll
+                    for (int r = 0; r < RP; ++r) {
+                        const int t = min(w.rb * tok_block + bars->tok_of[r], kMaxDrafts - 1);
+                        const uint32_t word = t < 64 ? (t < 32 ? see[0] : see[1]) : (t < 96 ? see[2] : see[3]);
+                        if (!((word >> (t & 31)) & 1u)) s[r] = -INFINITY;
+                    }
+                }
+            }
+            // a score far above its row's reference (or the first tile): new references
+            float far = -INFINITY;
+            const bool first = j == w.j0;
+            if (!first) {
+#pragma unroll
+                for (int r = 0; r < RP; r += 4) {
+                    const float4 m = *reinterpret_cast<const float4 *>(&bars->neg_m[r]);
+                    far = fmaxf(far, fmaxf(fmaxf(fmaf(s[r], c, m.x), fmaf(s[r + 1], c, m.y)),
+                                           fmaxf(fmaf(s[r + 2], c, m.z), fmaf(s[r + 3], c, m.w))));
+                }
+            }
+            if (softmax_any(first || far > 8.f || !ok)) {
+#pragma unroll
+                for (int r = 0; r < RP; ++r) {
+                    const float t = redux_max(s[r]);
+                    if (lane == 0) bars->top[warp][r] = t * c;
+                }
+                if (softmax_any(!ok)) {
+                    ok = false;
+                    break;
+                }
+                if (tid < RP) {
+                    float m = first ? -INFINITY : -bars->neg_m[tid];
+                    const float t = fmaxf(fmaxf(bars->top[0][tid], bars->top[1][tid]),
+                                          fmaxf(bars->top[2][tid], bars->top[3][tid]));
+                    float f = 1.f;
+                    if (t > m) {
+                        f = ex2(m - t);
+                        m = t;
+                    }
+                    bars->factor[tid] = f;
+                    bars->neg_m[tid] = -m;
+                }
+                softmax_sync();
+                if (!first) {  // O and the sums, once the last tile is in them
+                    ok = __all_sync(0xffffffffu, wait(&bars->pv_done, (uint32_t)(tile - 1) & 1));
+                    tc_fence_after();
+                    if (ok) {
+#pragma unroll
+                        for (int i = 0; i < 2 * RP; i += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(tbase + lanes + S::kTmO + i, o);
+                            tmem_ld_wait_regs(o);
+#pragma unroll
+                            for (int x = 0; x < 16; ++x)
+                                o[x] = __float_as_uint(__uint_as_float(o[x]) * bars->factor[(i + x) % RP]);
+                            tmem_st16(tbase + lanes + S::kTmO + i, o);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+            }
+            uint8_t *ph = sm + S::kOffP + pbuf * S::kPBytes + tid * 32;
+#pragma unroll
+            for (int g = 0; g < RP / 16; ++g) {
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int x = 0; x < 16; x += 4) {
+                    const float4 m = *reinterpret_cast<const float4 *>(&bars->neg_m[g * 16 + x]);
+                    const float mm[4] = {m.x, m.y, m.z, m.w};
+                    float e[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)  // a row without keys yet: reference inf, weight 0
+                        e[y] = ex2(mm[y] == INFINITY ? -INFINITY : fmaf(s[g * 16 + x + y], c, mm[y]));
+#pragma unroll
+                    for (int y = 0; y < 4; y += 2) {
+                        const uint32_t h = pack_bf16x2(e[y], e[y + 1]);
+                        hi[(x + y) / 2] = h;
+                        lo[(x + y) / 2] = pack_bf16x2(e[y] - __uint_as_float(h << 16),
+                                                      e[y + 1] - __uint_as_float(h & 0xffff0000u));
+                    }
+                }
+                // groups of 16 rows are 4 KB apart, a key's 32 bytes in pieces of 16, swapped in every other four keys
+                const uint32_t turn = ((uint32_t)tid >> 2 & 1u) << 4;
+                uint8_t *at = ph + g * 4096;
+                *reinterpret_cast<uint4 *>(at + turn) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(at + (turn ^ 16u)) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+                if (S::kParts == 2) {
+                    *reinterpret_cast<uint4 *>(at + S::kPart + turn) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    *reinterpret_cast<uint4 *>(at + S::kPart + (turn ^ 16u)) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+                }
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->p_full[pbuf]);
+        }
+        if (!ok) break;
+        // the item's sums; thread tid holds column tid of v
+        ok = __all_sync(0xffffffffu, wait(&bars->o_full, (uint32_t)item & 1));
+        tc_fence_after();
+        const int toks = min(tok_block, p.N - w.rb * tok_block), rows = toks * p.group;
+        const bool whole = w.j0 == 0 && w.j1 == w.tiles;
+        const long long piece = 2ll * blockIdx.x + (w.j0 == 0 ? 1 : 0);
+        float *po = static_cast<float *>(p.ws) + piece * RP * (kHeadDim + 2);
+        if (ok) {
+#pragma unroll
+            for (int i = 0; i < RP; i += 16) {
+                uint32_t o[16], l[16];
+                tmem_ld16(tbase + lanes + S::kTmO + i, o);
+                tmem_ld16(tbase + lanes + S::kTmL + i, l);
+                tmem_ld_wait_regs(o);
+                tmem_ld_wait_regs(l);
+                if (!sound) continue;
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    const int r = i + x;
+                    if (r >= rows) break;
+                    const float ov = __uint_as_float(o[x]), lv = __uint_as_float(l[x]);
+                    if (whole) {
+                        const long long tok = (long long)w.b * p.N + w.rb * tok_block + bars->tok_of[r];
+                        const int head = w.kvh * p.group + r - bars->tok_of[r] * p.group;
+                        p.out[(tok * p.H + head) * kHeadDim + tid] = __float2bfloat16_rn(lv == 0.f ? 0.f : ov / lv);
+                    } else {
+                        po[r * kHeadDim + tid] = ov;
+                        if (tid == 0)
+                            reinterpret_cast<float2 *>(po + RP * kHeadDim)[r] = make_float2(-bars->neg_m[r], lv);
+                    }
+                }
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->o_free);
+        softmax_sync();  // neg_m is read until here
+    }
+}
+
+template <int RP>
+__device__ void mma_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint32_t tbase, int lane, int blocks,
+                         const Waiter &wait) {
+    using S = Shape<RP>;
+    const uint32_t id_s = idesc_bf16_f32(128, RP, false, false);
+    const uint32_t id_o = idesc_bf16_f32(128, RP, true, true);
+    const uint32_t id_l = idesc_bf16_f32(128, RP, false, true);
+    const uint64_t high = sdesc_sw128(0, 0, 1024), high32 = sdesc_sw32(0, 0, 256);
+    const uint32_t kv_base = smem_u32(sm + S::kOffKV) >> 4, q_base = smem_u32(sm + S::kOffQ) >> 4;
+    const uint32_t p_base = smem_u32(sm + S::kOffP) >> 4;
+    const uint32_t ones = (smem_u32(sm + S::kOffOnes) >> 4) + (1u << 16);
+    const uint32_t lead = lane == 0;
+    bool ok = true;
+    auto full = [&](int i) {
+        return __all_sync(0xffffffffu, wait(&bars->full[i % S::kSlots], (uint32_t)(i / S::kSlots) & 1));
+    };
+    // S^T of tile t of item u; with the item's first tile Q has to be there, with its last Q is done with
+    auto scores = [&](int t, int u, bool first, bool last) {
+        if (first) ok = ok && __all_sync(0xffffffffu, wait(&bars->q_full[u % S::kQBufs], (uint32_t)(u / S::kQBufs) & 1));
+        ok = ok && full(2 * t);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t a = kv_base + (uint32_t)(2 * t % S::kSlots) * (kTileBytes >> 4) + (1u << 16);
+        const uint32_t b = q_base + (uint32_t)(u % S::kQBufs) * (S::kQBytes >> 4) + (1u << 16);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            mma_ss(lead, tbase + (t & 1) * RP, high | (a + (k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2),
+                   high | (b + (k >> 2) * (S::kQBytes >> 5) + (k & 3) * 2), id_s, k > 0);
+        commit_if(lead, &bars->s_full[t & 1]);
+        commit_if(lead, &bars->empty[2 * t % S::kSlots]);
+        if (last) commit_if(lead, &bars->q_empty[u % S::kQBufs]);
+    };
+    Walk w;
+    w.start(p, blocks, bars->b0, bars->rem0, bars->x1 - bars->x0);
+    int tile = 0, item = 0;
+    if (!w.done()) scores(0, 0, true, w.j1 - w.j0 == 1);
+    while (!w.done() && ok) {
+        const int j0 = w.j0, j1 = w.j1, kv_len = w.kv_len;
+        const int end = kv_len % p.cache.page_size, last = (kv_len - 1) / kKeyTile;
+        w.next(p);
+        for (int j = j0; j < j1 && ok; ++j, ++tile) {
+            // the next tile's scores run under this one's softmax; its S was read before tile - 1's P was full
+            const bool more = j + 1 < j1;
+            if (more)
+                scores(tile + 1, item, false, j + 2 == j1);
+            else if (!w.done())
+                scores(tile + 1, item + 1, true, w.j1 - w.j0 == 1);
+            const int iv = 2 * tile + 1, pbuf = tile % S::kPBufs;
+            ok = ok && full(iv);
+            if (!ok) break;
+            if (end != 0 && j == last) {  // rows of the last page behind the request's positions: zeros
+                const int r0 = kv_len - j * kKeyTile, r1 = r0 - end + p.cache.page_size;
+                uint8_t *v = sm + S::kOffKV + (iv % S::kSlots) * kTileBytes;
+                for (int r = r0 + (lane >> 4); r < r1; r += 2)
+                    *reinterpret_cast<uint4 *>(v + ((lane >> 3) & 1) * kHalfBytes + r * 128 + (lane & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            ok = __all_sync(0xffffffffu, wait(&bars->p_full[pbuf], (uint32_t)(tile / S::kPBufs) & 1));
+            if (ok && j == j0 && item > 0)  // the last item's sums have been read
+                ok = __all_sync(0xffffffffu, wait(&bars->o_free, (uint32_t)(item - 1) & 1));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t a = kv_base + (uint32_t)(iv % S::kSlots) * (kTileBytes >> 4) + ((uint32_t)(kHalfBytes >> 4) << 16);
+            const uint32_t b = p_base + (uint32_t)pbuf * (S::kPBytes >> 4) + ((4096u >> 4) << 16);
+#pragma unroll
+            for (int x = 0; x < S::kParts; ++x)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t bk = b + x * (S::kPart >> 4) + k * 32;
+                    mma_ss(lead, tbase + S::kTmO, high | (a + k * 128), high32 | bk, id_o, j > j0 || x + k > 0);
+                    mma_ss(lead, tbase + S::kTmL, high32 | ones, high32 | bk, id_l, j > j0 || x + k > 0);
+                }
+            commit_if(lead, &bars->empty[iv % S::kSlots]);
+            commit_if(lead, &bars->p_empty[pbuf]);
+            commit_if(lead, &bars->pv_done);
+            if (!more) commit_if(lead, &bars->o_full);
+        }
+        ++item;
+    }
+    __syncwarp();
+    commit_if(lead, &bars->drain);
+    wait(&bars->drain, 0);
+}
+
+template <int RP>
+__device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUtensorMap *tk, const CUtensorMap *tv,
+                          Bars<RP> *bars, uint8_t *sm, int lane, int blocks, int tok_block, const Waiter &wait) {
+    using S = Shape<RP>;
+    Walk w;
+    w.start(p, blocks, bars->b0, bars->rem0, bars->x1 - bars->x0);
+    const uint32_t box = (uint32_t)(tok_block * p.group) * 128;
+    int i = 0, item = 0, asked = 0;
+    bool ok = true;
+    for (; !w.done() && ok; w.next(p), ++item) {
+        const int qb = item % S::kQBufs;
+        if (item >= S::kQBufs &&
+            !(ok = __all_sync(0xffffffffu, wait(&bars->q_empty[qb], (uint32_t)(item / S::kQBufs - 1) & 1))))
+            break;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&bars->q_full[qb], 2 * box);
+            for (int x = 0; x < 2; ++x)
+                tma_load_4d(sm + S::kOffQ + qb * S::kQBytes + x * (S::kQBytes / 2), tq, &bars->q_full[qb], 0,
+                            w.kvh * p.group, w.b * p.N + w.rb * tok_block, x);
+        }
+        asked = item + 1;
+        int page = page_of(p.cache, w.b, w.kv_len, w.j0, lane, p.err);
+        for (int j = w.j0; j < w.j1 && ok; ++j) {
+            const int next = j + 1 < w.j1 ? page_of(p.cache, w.b, w.kv_len, j + 1, lane, p.err) : 0;
+            for (int kv = 0; kv < 2; ++kv, ++i) {
+                const int slot = i % S::kSlots;
+                if (i >= S::kSlots &&
+                    !(ok = __all_sync(0xffffffffu, wait(&bars->empty[slot], (uint32_t)(i / S::kSlots - 1) & 1))))
+                    break;
+                load_tile(kv ? tv : tk, sm + S::kOffKV + slot * kTileBytes, &bars->full[slot], page,
+                          p.cache.page_size, w.kvh, lane);
+            }
+            page = next;
+        }
+    }
+    // no copy may be in flight when the CTA exits
+    for (int x = i > S::kSlots ? i - S::kSlots : 0; x < i; ++x)
+        wait(&bars->full[x % S::kSlots], (uint32_t)(x / S::kSlots) & 1);
+    for (int x = asked > S::kQBufs ? asked - S::kQBufs : 0; x < asked; ++x)
+        wait(&bars->q_full[x % S::kQBufs], (uint32_t)(x / S::kQBufs) & 1);
+}
+
+template <int RP>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_verify_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                       const __grid_constant__ CUtensorMap tv, const AttnParams p) {
+    using S = Shape<RP>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    Bars<RP> *bars = reinterpret_cast<Bars<RP> *>(sm + S::kOffBars);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tok_block = min(p.N, kMaxDrafts / p.group), blocks = (p.N + tok_block - 1) / tok_block;
+    if (warp < 4) {
+        // rows of Q that no box fills, and the ones
+        for (int i = threadIdx.x; i < (int)(S::kQBufs * S::kQBytes / 16); i += 128)
+            reinterpret_cast<uint4 *>(sm + S::kOffQ)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = threadIdx.x; i < 256; i += 128)
+            reinterpret_cast<uint4 *>(sm + S::kOffOnes)[i] =
+                make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+        for (int r = threadIdx.x; r < RP; r += 128) bars->tok_of[r] = (uint8_t)(r / p.group);
+        fence_proxy_async_smem();
+    } else if (warp == kMmaWarp) {
+        tmem_alloc(&bars->tmem_base, S::kTmCols);
+        tmem_relinquish();
+    } else {
+        if (lane == 0) {
+            for (int i = 0; i < S::kSlots; ++i) {
+                mbar_init(&bars->full[i], 1);
+                mbar_init(&bars->empty[i], 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&bars->q_full[i], 1);
+                mbar_init(&bars->q_empty[i], 1);
+                mbar_init(&bars->s_full[i], 1);
+                mbar_init(&bars->p_full[i], 4);
+                mbar_init(&bars->p_empty[i], 1);
+            }
+            mbar_init(&bars->pv_done, 1);
+            mbar_init(&bars->o_full, 1);
+            mbar_init(&bars->o_free, 4);
+            mbar_init(&bars->drain, 1);
+            fence_mbar_init();
+        }
+        __syncwarp();
+        pdl_wait();
+        const int per = p.Hkv * blocks;
+        const long long all = sum_tiles(p, 0, nullptr) * per;
+        const long long runs = min((long long)gridDim.x, all), c = min((long long)blockIdx.x, runs);
+        const long long x0 = runs ? all * c / runs : 0, x1 = runs && c < runs ? all * (c + 1) / runs : x0;
+        int b = 0;
+        long long rem = 0;
+        if (x1 > x0) find_place(p, x0, per, b, rem);
+        if (lane == 0) {
+            bars->x0 = x0;
+            bars->x1 = x1;
+            bars->b0 = b;
+            bars->rem0 = rem;
+        }
+    }
+    if (warp != kLoadWarp) pdl_wait();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_trigger();
+    const uint32_t tbase = bars->tmem_base;
+    const Waiter wait{p.wait_limit_ns, p.err};
+    if (warp < 4)
+        softmax_role<RP>(p, bars, sm, tbase, warp, lane, blocks, tok_block, wait);
+    else if (warp == kMmaWarp)
+        mma_role<RP>(p, bars, sm, tbase, lane, blocks, wait);
+    else
+        load_role<RP>(p, &tq, &tk, &tv, bars, sm, lane, blocks, tok_block, wait);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) tmem_dealloc(tbase, S::kTmCols);
+}
+
+// The (request, kv head, block of drafts)s that several CTAs shared.  grid: one block of 4 warps per such
+// triple, a warp per row; rp: the padded rows of a partial result; ctas: the grid that left them.
+__global__ void __launch_bounds__(128) attn_verify_join_kernel(const AttnParams p, int rp, int ctas) {
+    pdl_wait();
+    pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tok_block = min(p.N, kMaxDrafts / p.group), blocks = (p.N + tok_block - 1) / tok_block;
+    const int per = p.Hkv * blocks;
+    const int b = blockIdx.x / per, item = blockIdx.x - b * per;
+    const int tiles = tiles_of(p, b);
+    if (tiles == 0) return;
+    long long before;
+    const long long all = sum_tiles(p, b, &before) * per;
+    const long long x0 = before * per + (long long)item * tiles, x1 = x0 + tiles - 1;
+    const long long runs = min((long long)ctas, all);
+    const int c0 = (int)(((x0 + 1) * runs - 1) / all), c1 = (int)(((x1 + 1) * runs - 1) / all);
+    if (c0 == c1) return;
+    if (p.parents) {  // a request with a parent out of range is left as it was
+        bool bad = false;
+        for (int t = lane; t < p.N; t += 32) {
+            const int up = p.parents[(long long)b * p.N + t];
+            bad |= up < -1 || up >= t;
+        }
+        if (__any_sync(0xffffffffu, bad)) return;
+    }
+    const int kvh = item / blocks, rb = item - kvh * blocks;
+    const int rows = min(tok_block, p.N - rb * tok_block) * p.group;
+    const long long stride = (long long)rp * (kHeadDim + 2);
+    const float *ws = static_cast<const float *>(p.ws);
+    for (int r = warp; r < rows; r += 4) {
+        float m = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = c0; c <= c1; ++c) {
+            const float *at = ws + (2ll * c + (c == c0)) * stride;
+            const float2 ml = reinterpret_cast<const float2 *>(at + rp * kHeadDim)[r];
+            const float4 x = reinterpret_cast<const float4 *>(at + r * kHeadDim)[lane];
+            if (ml.x == -INFINITY) continue;  // none of its keys is seen by the row
+            const float top = fmaxf(m, ml.x), f = ex2(m - top), g = ex2(ml.x - top);
+            m = top;
+            l = l * f + ml.y * g;
+            o.x = o.x * f + x.x * g;
+            o.y = o.y * f + x.y * g;
+            o.z = o.z * f + x.z * g;
+            o.w = o.w * f + x.w * g;
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int tok = r / p.group, head = kvh * p.group + r - tok * p.group;
+        const uint2 w = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        reinterpret_cast<uint2 *>(p.out + (((long long)b * p.N + rb * tok_block + tok) * p.H + head) * kHeadDim)[lane] = w;
+    }
+}
+
+template <int RP>
+cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const AttnParams &p,
+                   int ctas, cudaStream_t stream) {
+    constexpr uint32_t smem = Shape<RP>::kOffBars + sizeof(Bars<RP>) + 1024;
+    static_assert(smem <= 227 * 1024, "shared memory");
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static std::mutex mu;
+    static bool configured[64] = {false};
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+        if (!configured[dev]) {
+            e = cudaFuncSetAttribute(attn_verify_kernel<RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+            configured[dev] = true;
+        }
+    }
+    return launch_pdl(attn_verify_kernel<RP>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, tq, tk, tv, p);
+}
+
+int padded_rows(int N, int group) {
+    const int rows = std::min(N, kMaxDrafts / group) * group;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+}
+
+}  // namespace
+
+unsigned long long attn_verify_ws_bytes(int N, int group) {
+    return 2ull * kAttnCtas * padded_rows(N, group) * (kHeadDim + 2) * 4;
+}
+
+cudaError_t launch_attn_verify(const AttnParams &p, cudaStream_t stream) {
+    const int tok_block = std::min(p.N, kMaxDrafts / p.group), blocks = (p.N + tok_block - 1) / tok_block;
+    CUtensorMap tq, tk, tv;
+    if (!make_query_map(&tq, p.q, (long long)p.B * p.N, p.H, p.q_rs, p.group, tok_block) ||
+        !make_pages_map(&tk, p.cache.k, p.cache, p.Hkv) || !make_pages_map(&tv, p.cache.v, p.cache, p.Hkv))
+        return cudaErrorInvalidValue;
+    const int rp = padded_rows(p.N, p.group);
+    cudaError_t e;
+    switch (rp) {
+        case 16: e = launch<16>(tq, tk, tv, p, kAttnCtas, stream); break;
+        case 32: e = launch<32>(tq, tk, tv, p, kAttnCtas, stream); break;
+        case 64: e = launch<64>(tq, tk, tv, p, kAttnCtas, stream); break;
+        default: e = launch<128>(tq, tk, tv, p, kAttnCtas, stream); break;
+    }
+    if (e != cudaSuccess) return e;
+    return launch_pdl(attn_verify_join_kernel, dim3((unsigned)((long long)p.B * p.Hkv * blocks)), dim3(128), 0, stream,
+                      p, rp, kAttnCtas);
+}
+
+}  // namespace la

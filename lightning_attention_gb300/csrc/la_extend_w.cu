@@ -481,19 +481,31 @@ EncodeTiledFn encode_fn() {
 
 }  // namespace
 
-bool make_rows_map(CUtensorMap *m, const void *ptr, int rows, long long width, long long row_stride,
-                   int box_cols, int box_rows, bool swizzle) {
+bool make_bf16_map(CUtensorMap *m, const void *ptr, int rank, const unsigned long long *extent,
+                   const long long *stride, const int *box_extent, bool swizzle) {
     EncodeTiledFn enc = encode_fn();
-    if (!enc) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)row_stride * 2};
-    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
-    const cuuint32_t es[2] = {1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box,
-               es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    if (!enc || rank < 2 || rank > 5) return false;
+    cuuint64_t dims[5], strides[4];
+    cuuint32_t box[5], es[5];
+    for (int i = 0; i < rank; ++i) {
+        dims[i] = extent[i];
+        box[i] = (cuuint32_t)box_extent[i];
+        es[i] = 1;
+        if (i > 0) strides[i - 1] = (cuuint64_t)stride[i] * 2;
+    }
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(ptr), dims,
+               strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
            CUDA_SUCCESS;
+}
+
+bool make_rows_map(CUtensorMap *m, const void *ptr, int rows, long long width, long long row_stride,
+                   int box_cols, int box_rows, bool swizzle) {
+    const unsigned long long extent[2] = {(unsigned long long)width, (unsigned long long)rows};
+    const long long stride[2] = {1, row_stride};
+    const int box[2] = {box_cols, box_rows};
+    return make_bf16_map(m, ptr, 2, extent, stride, box, swizzle);
 }
 
 // [T][H*128] bf16, box of 64 columns x C rows, 128-byte swizzle; rows past T read as zero.

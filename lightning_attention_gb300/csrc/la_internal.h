@@ -68,6 +68,7 @@ enum : unsigned int {
     ERR_BIT_PARENTS = 8u,       // tree-verify parent index outside [-1, t-1]
     ERR_BIT_ACCEPT = 16u,       // commit index outside [-1, N-1]
     ERR_BIT_TRACK = 32u,        // track length outside [-1, n] or bad track slot
+    ERR_BIT_PAGE = 64u,         // page or cache row out of range, kv_lens that do not fit
 };
 
 constexpr int kHeadDim = 128;
@@ -182,6 +183,10 @@ bool make_token_map_full(CUtensorMap *m, const void *ptr, int T, int H);
 // the 128-byte swizzle (64 columns) or without; rows past the last read as zero (la_extend_w.cu).
 bool make_rows_map(CUtensorMap *m, const void *ptr, int rows, long long width, long long row_stride,
                    int box_cols, int box_rows, bool swizzle);
+// A bf16 array of `rank` dimensions (2 to 5), the first contiguous; strides in elements (stride[0] is not
+// read); what lies outside reads as zero (la_extend_w.cu).
+bool make_bf16_map(CUtensorMap *m, const void *ptr, int rank, const unsigned long long *extent,
+                   const long long *stride, const int *box_extent, bool swizzle);
 // The pre-pass of a split or grouped extend: the workspace copy of each initial state, and the
 // block states of split requests (la_extend_seg.cu).  Launched when p.seg_len > 0 or p.group > 1.
 cudaError_t launch_block_states(const ExtendParams &p, cudaStream_t stream);
