@@ -243,75 +243,90 @@ __device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, in
     }
 }
 
+// What feeds an MMA is the same in every lane and known to be (values from shared memory through a shuffle,
+// slots counted instead of divided), so that the uniform datapath forms the operands: otherwise an issue takes 95
+// cycles, longer than the MMA (16,384 tokens, 32 heads on 8: 1750 us).
 __device__ void mma_role(const AttnParams &p, Bars *bars, uint8_t *sm, uint32_t tbase, int lane,
                          const Waiter &wait) {
-    const Item &it = bars->item;
     const uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
     const uint32_t id_o = idesc_bf16_f32(128, 128, false, true);
     const uint64_t high = sdesc_sw128(0, 0, 1024);
-    const uint32_t q_base = smem_u32(sm + kOffQ) >> 4, kv_base = smem_u32(sm + kOffKV) >> 4;
-    const uint32_t lead = lane == 0;
-    auto slot_base = [&](int i) { return kv_base + (uint32_t)(i % kSlots) * (kTileBytes >> 4); };
-    auto full = [&](int i) {
-        return __all_sync(0xffffffffu, wait(&bars->full[i % kSlots], (uint32_t)(i / kSlots) & 1));
-    };
-    auto scores = [&](int stage, int i) {  // S = Q K^T
-        const uint32_t a = q_base + stage * (kTileBytes >> 4) + (1u << 16), b = slot_base(i) + (1u << 16);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const uint32_t at = (k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2;
-            mma_ss(lead, tbase + kTmS + stage * 128, high | (a + at), high | (b + at), id_s, k > 0);
+    const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(sm), 0) >> 4;
+    const uint32_t q_base = base + (kOffQ >> 4), kv_base = base + (kOffKV >> 4);
+    const int j0 = __shfl_sync(0xffffffffu, bars->item.j0, 0), nt = __shfl_sync(0xffffffffu, bars->item.j1, 0) - j0;
+    const int kv_len = __shfl_sync(0xffffffffu, bars->item.kv_len, 0);
+    int slot = 0;  // the next tile to come
+    uint32_t phase = 0;
+    auto full = [&]() { return __all_sync(0xffffffffu, wait(&bars->full[slot], phase)); };
+    auto next = [&]() {
+        if (++slot == kSlots) {
+            slot = 0;
+            phase ^= 1;
         }
-        commit_if(lead, &bars->s_full[stage]);
     };
-    const int nt = it.j1 - it.j0;
-    bool ok = nt > 0 && __all_sync(0xffffffffu, wait(&bars->q_full, 0)) && full(0);
+    auto scores = [&](int stage, int at_slot) {  // S = Q K^T
+        const uint32_t a = q_base + stage * (kTileBytes >> 4) + (1u << 16);
+        const uint32_t b = kv_base + (uint32_t)at_slot * (kTileBytes >> 4) + (1u << 16);
+        if (elect()) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t at = (k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2;
+                mma_bf16(tbase + kTmS + stage * 128, high | (a + at), high | (b + at), id_s, k > 0);
+            }
+            mma_commit(&bars->s_full[stage]);
+            if (stage == 1) mma_commit(&bars->empty[at_slot]);
+        }
+        __syncwarp();
+    };
+    bool ok = nt > 0 && __all_sync(0xffffffffu, wait(&bars->q_full, 0)) && full();
     if (ok) {
         scores(0, 0);
         scores(1, 0);
-        commit_if(lead, &bars->empty[0]);
+        next();
     }
     // rows of the last page behind the request's positions hold anything: zeros for the values
-    const int end = it.kv_len % p.cache.page_size;
+    const int end = kv_len % p.cache.page_size, last = (kv_len - 1) / kKeyTile - j0;
     for (int j = 0; j < nt && ok; ++j) {
-        const int iv = 2 * j + 1, ik = 2 * j + 2;
+        ok = full();
+        const int sv = slot;
+        next();
+        const int sk = slot;
+        if (ok && end != 0 && j == last) {
+            const int r0 = kv_len - (j0 + j) * kKeyTile, r1 = r0 - end + p.cache.page_size;
+            uint8_t *v = sm + kOffKV + sv * kTileBytes;
+            for (int r = r0 + (lane >> 4); r < r1; r += 2)
+                *reinterpret_cast<uint4 *>(v + ((lane >> 3) & 1) * kHalfBytes + r * 128 + (lane & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+        }
+        const bool more = j + 1 < nt;
 #pragma unroll
         for (int stage = 0; stage < 2; ++stage) {
-            if (stage == 0) {
-                ok = full(iv);
-                if (ok && end != 0 && it.j0 + j == (it.kv_len - 1) / kKeyTile) {
-                    const int r0 = it.kv_len - (it.j0 + j) * kKeyTile, r1 = r0 - end + p.cache.page_size;
-                    uint8_t *v = sm + kOffKV + (iv % kSlots) * kTileBytes;
-                    for (int r = r0 + (lane >> 4); r < r1; r += 2) {
-                        uint8_t *at = v + ((lane >> 3) & 1) * kHalfBytes + r * 128 + (lane & 7) * 16;
-                        *reinterpret_cast<uint4 *>(at) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-            }
             ok = ok && __all_sync(0xffffffffu, wait(&bars->p_full[stage], j & 1));
             if (!ok) break;
             tc_fence_after();
-            const uint32_t b = slot_base(iv) + ((uint32_t)(kHalfBytes >> 4) << 16);
+            const uint32_t b = kv_base + (uint32_t)sv * (kTileBytes >> 4) + ((uint32_t)(kHalfBytes >> 4) << 16);
+            if (elect()) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                mma_ts(lead, tbase + kTmO + stage * 128, tbase + kTmS + stage * 128 + k * 8, high | (b + k * 128),
-                       id_o, j > 0 || k > 0);
-            if (stage == 1) commit_if(lead, &bars->empty[iv % kSlots]);
-            if (j + 1 < nt) {
-                if (stage == 0) ok = full(ik);
+                for (int k = 0; k < 8; ++k)
+                    mma_f16_tmem_a(tbase + kTmO + stage * 128, tbase + kTmS + stage * 128 + k * 8,
+                                   high | (b + k * 128), id_o, j > 0 || k > 0);
+                if (stage == 1) mma_commit(&bars->empty[sv]);
+                if (!more) mma_commit(&bars->o_full[stage]);
+            }
+            __syncwarp();
+            if (more) {
+                if (stage == 0) ok = full();
                 if (!ok) break;
-                scores(stage, ik);
-                if (stage == 1) commit_if(lead, &bars->empty[ik % kSlots]);
-            } else {
-                commit_if(lead, &bars->o_full[stage]);
+                scores(stage, sk);
             }
         }
+        if (more) next();
     }
     // everything issued is complete before tensor memory is freed
     __syncwarp();
-    commit_if(lead, &bars->drain);
+    if (elect()) mma_commit(&bars->drain);
     wait(&bars->drain, 0);
 }
 
@@ -353,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Bars *bars = reinterpret_cast<Bars *>(sm + kOffBars);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     pdl_wait();
     if (warp == 0) {
         Item it;
@@ -392,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tbase = bars->tmem_base;
+    const uint32_t tbase = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
     const Waiter wait{p.wait_limit_ns, p.err};
     if (bars->ok) {
         if (warp < kMmaWarp) {

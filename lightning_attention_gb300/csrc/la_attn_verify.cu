@@ -12,8 +12,7 @@
 // With few rows the keys take the 128 lanes of the tensor cores: S^T = K Q^T and O^T += V^T P^T, both with
 // N = R (padded to 16, 32, 64 or 128), K and V as they lie in their pages.  A thread owns a key in the
 // softmax and a column of v in the result.  The reference m_r is that of the first tile and follows only
-// when a score passes it by more than 2^8, so that a tile takes no maximum, one test; the sums of P come from the
-// same product, as the row of a matrix of ones.  P goes into shared memory as bf16 pairs hi + lo (off by at
+// when a score passes it by more than 2^8, so that a tile takes no maximum, one test.  P goes into shared memory as bf16 pairs hi + lo (off by at
 // most 2^-16), which the idle tensor cores take at no cost.
 #include <string.h>
 
@@ -38,12 +37,13 @@ struct Shape {
     static constexpr int kQBufs = RP <= 64 ? 2 : 1, kPBufs = RP <= 32 ? 2 : 1;
     static constexpr int kSlots = RP <= 32 ? 5 : 4;       // tiles of keys and values
     static constexpr int kParts = RP <= 64 ? 2 : 1;       // of P: hi, lo
+    static constexpr bool kOnes = RP > 64;                // sums of P by the tensor cores, not in registers
     static constexpr uint32_t kQBytes = RP * 256, kPart = kKeyTile * RP * 2, kPBytes = kParts * kPart;
     static constexpr uint32_t kOffKV = 0;
     static constexpr uint32_t kOffQ = kOffKV + kSlots * kTileBytes;
     static constexpr uint32_t kOffP = kOffQ + kQBufs * kQBytes;
     static constexpr uint32_t kOffOnes = kOffP + kPBufs * kPBytes;
-    static constexpr uint32_t kOffBars = kOffOnes + 4096;
+    static constexpr uint32_t kOffBars = kOffOnes + (kOnes ? 4096 : 0);
     // columns of tensor memory: S twice, O, sums
     static constexpr uint32_t kTmO = 2 * RP, kTmL = 3 * RP, kTmCols = 4 * RP;
 };
@@ -223,7 +223,12 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
     w.start(p, blocks, bars->b0, bars->rem0, bars->x1 - bars->x0);
     int tile = 0, item = 0, tree_of = -1;
     bool ok = true, sound = true;
+    float sum[S::kOnes ? 1 : RP];  // of this thread's keys
     for (; !w.done(); w.next(p), ++item) {
+        if (!S::kOnes) {
+#pragma unroll
+            for (int r = 0; r < RP; ++r) sum[S::kOnes ? 0 : r] = 0.f;
+        }
         if (p.parents && tree_of != w.b) {
             sound = build_tree(p, bars, w.b, tid);
             if (!sound && tid == 0) atomicOr(p.err, ERR_BIT_PARENTS);
@@ -298,12 +303,16 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
                     bars->neg_m[tid] = -m;
                 }
                 softmax_sync();
+                if (!S::kOnes) {
+#pragma unroll
+                    for (int r = 0; r < RP; ++r) sum[S::kOnes ? 0 : r] *= bars->factor[r];
+                }
                 if (!first) {  // O and the sums, once the last tile is in them
                     ok = __all_sync(0xffffffffu, wait(&bars->pv_done, (uint32_t)(tile - 1) & 1));
                     tc_fence_after();
                     if (ok) {
 #pragma unroll
-                        for (int i = 0; i < 2 * RP; i += 16) {
+                        for (int i = 0; i < (S::kOnes ? 2 : 1) * RP; i += 16) {
                             uint32_t o[16];
                             tmem_ld16(tbase + lanes + S::kTmO + i, o);
                             tmem_ld_wait_regs(o);
@@ -328,6 +337,10 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
 #pragma unroll
                     for (int y = 0; y < 4; ++y)  // a row without keys yet: reference inf, weight 0
                         e[y] = ex2(mm[y] == INFINITY ? -INFINITY : fmaf(s[g * 16 + x + y], c, mm[y]));
+                    if (!S::kOnes) {
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) sum[S::kOnes ? 0 : g * 16 + x + y] += e[y];
+                    }
 #pragma unroll
                     for (int y = 0; y < 4; y += 2) {
                         const uint32_t h = pack_bf16x2(e[y], e[y + 1]);
@@ -352,7 +365,30 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
             if (lane == 0) mbar_arrive(&bars->p_full[pbuf]);
         }
         if (!ok) break;
-        // the item's sums; thread tid holds column tid of v
+        // the item's sums: over the lanes, each step with half the rows, then over the warps
+        if (!S::kOnes) {
+            int row = 0;
+#pragma unroll
+            for (int d = 16, n = RP; d > 0; d >>= 1) {
+                if (n > 1) {
+                    n >>= 1;
+                    const bool up = (lane & d) != 0;
+                    if (up) row += n;
+#pragma unroll
+                    for (int i = 0; i < RP / 2; ++i)
+                        if (i < n) {
+                            const float mine = up ? sum[i + n] : sum[i], other = up ? sum[i] : sum[i + n];
+                            sum[i] = mine + __shfl_xor_sync(0xffffffffu, other, d);
+                        }
+                } else {
+                    sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], d);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < (RP > 32 ? RP / 32 : 1); ++i) bars->top[warp][row + i] = sum[i];
+            softmax_sync();
+        }
+        // thread tid holds column tid of v
         ok = __all_sync(0xffffffffu, wait(&bars->o_full, (uint32_t)item & 1));
         tc_fence_after();
         const int toks = min(tok_block, p.N - w.rb * tok_block), rows = toks * p.group;
@@ -364,9 +400,16 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
             for (int i = 0; i < RP; i += 16) {
                 uint32_t o[16], l[16];
                 tmem_ld16(tbase + lanes + S::kTmO + i, o);
-                tmem_ld16(tbase + lanes + S::kTmL + i, l);
+                if (S::kOnes) tmem_ld16(tbase + lanes + S::kTmL + i, l);
                 tmem_ld_wait_regs(o);
-                tmem_ld_wait_regs(l);
+                if (S::kOnes) {
+                    tmem_ld_wait_regs(l);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 16; ++x)
+                        l[x] = __float_as_uint((bars->top[0][i + x] + bars->top[1][i + x]) +
+                                               (bars->top[2][i + x] + bars->top[3][i + x]));
+                }
                 if (!sound) continue;
 #pragma unroll
                 for (int x = 0; x < 16; ++x) {
@@ -388,10 +431,13 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->o_free);
-        softmax_sync();  // neg_m is read until here
+        softmax_sync();  // neg_m and the sums are read until here
     }
 }
 
+// What feeds an MMA is the same in every lane and known to be (values from shared memory through a shuffle,
+// slots counted instead of divided), so that the uniform datapath forms the operands: otherwise an issue takes 100
+// cycles, several times the MMA (128 requests of 500-8000 positions, 32 heads on 4: 304 us).
 template <int RP>
 __device__ void mma_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint32_t tbase, int lane, int blocks,
                          const Waiter &wait) {
@@ -400,81 +446,110 @@ __device__ void mma_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint3
     const uint32_t id_o = idesc_bf16_f32(128, RP, true, true);
     const uint32_t id_l = idesc_bf16_f32(128, RP, false, true);
     const uint64_t high = sdesc_sw128(0, 0, 1024), high32 = sdesc_sw32(0, 0, 256);
-    const uint32_t kv_base = smem_u32(sm + S::kOffKV) >> 4, q_base = smem_u32(sm + S::kOffQ) >> 4;
-    const uint32_t p_base = smem_u32(sm + S::kOffP) >> 4;
-    const uint32_t ones = (smem_u32(sm + S::kOffOnes) >> 4) + (1u << 16);
-    const uint32_t lead = lane == 0;
+    const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(sm), 0) >> 4;
+    const uint32_t kv_base = base + (S::kOffKV >> 4), q_base = base + (S::kOffQ >> 4);
+    const uint32_t p_base = base + (S::kOffP >> 4), ones = base + (S::kOffOnes >> 4) + (1u << 16);
     bool ok = true;
-    auto full = [&](int i) {
-        return __all_sync(0xffffffffu, wait(&bars->full[i % S::kSlots], (uint32_t)(i / S::kSlots) & 1));
+    int slot = 0, qb = 0, pb = 0;  // the next tile, Q and P to come, and the parities of their barriers
+    uint32_t slot_par = 0, q_par = 0, p_par = 0;
+    uint32_t s_buf = 0;            // of S, for the next scores
+    auto next_slot = [&]() {
+        if (++slot == S::kSlots) {
+            slot = 0;
+            slot_par ^= 1;
+        }
     };
-    // S^T of tile t of item u; with the item's first tile Q has to be there, with its last Q is done with
-    auto scores = [&](int t, int u, bool first, bool last) {
-        if (first) ok = ok && __all_sync(0xffffffffu, wait(&bars->q_full[u % S::kQBufs], (uint32_t)(u / S::kQBufs) & 1));
-        ok = ok && full(2 * t);
+    // S^T of the next tile; with an item's first tile Q has to be there, with its last Q is done with
+    auto scores = [&](bool first, bool last) {
+        if (first) ok = ok && __all_sync(0xffffffffu, wait(&bars->q_full[qb], q_par));
+        ok = ok && __all_sync(0xffffffffu, wait(&bars->full[slot], slot_par));
         if (!ok) return;
         tc_fence_after();
-        const uint32_t a = kv_base + (uint32_t)(2 * t % S::kSlots) * (kTileBytes >> 4) + (1u << 16);
-        const uint32_t b = q_base + (uint32_t)(u % S::kQBufs) * (S::kQBytes >> 4) + (1u << 16);
+        const uint32_t a = kv_base + (uint32_t)slot * (kTileBytes >> 4) + (1u << 16);
+        const uint32_t b = q_base + (uint32_t)qb * (S::kQBytes >> 4) + (1u << 16);
+        if (elect()) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            mma_ss(lead, tbase + (t & 1) * RP, high | (a + (k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2),
-                   high | (b + (k >> 2) * (S::kQBytes >> 5) + (k & 3) * 2), id_s, k > 0);
-        commit_if(lead, &bars->s_full[t & 1]);
-        commit_if(lead, &bars->empty[2 * t % S::kSlots]);
-        if (last) commit_if(lead, &bars->q_empty[u % S::kQBufs]);
+            for (int k = 0; k < 8; ++k)
+                mma_bf16(tbase + s_buf * RP, high | (a + (k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2),
+                         high | (b + (k >> 2) * (S::kQBytes >> 5) + (k & 3) * 2), id_s, k > 0);
+            mma_commit(&bars->s_full[s_buf]);
+            mma_commit(&bars->empty[slot]);
+            if (last) mma_commit(&bars->q_empty[qb]);
+        }
+        __syncwarp();
+        s_buf ^= 1;
+        next_slot();
+        if (last) {
+            if (++qb == S::kQBufs) {
+                qb = 0;
+                q_par ^= 1;
+            }
+        }
     };
     Walk w;
     w.start(p, blocks, bars->b0, bars->rem0, bars->x1 - bars->x0);
-    int tile = 0, item = 0;
-    if (!w.done()) scores(0, 0, true, w.j1 - w.j0 == 1);
+    int item = 0;
+    if (!w.done()) scores(true, w.j1 - w.j0 == 1);
     while (!w.done() && ok) {
-        const int j0 = w.j0, j1 = w.j1, kv_len = w.kv_len;
+        const int j0 = __shfl_sync(0xffffffffu, w.j0, 0), j1 = __shfl_sync(0xffffffffu, w.j1, 0);
+        const int kv_len = __shfl_sync(0xffffffffu, w.kv_len, 0);
         const int end = kv_len % p.cache.page_size, last = (kv_len - 1) / kKeyTile;
         w.next(p);
-        for (int j = j0; j < j1 && ok; ++j, ++tile) {
-            // the next tile's scores run under this one's softmax; its S was read before tile - 1's P was full
+        const bool follows = __shfl_sync(0xffffffffu, (int)!w.done(), 0) != 0;
+        const bool one = __shfl_sync(0xffffffffu, (int)(w.j1 - w.j0 == 1), 0) != 0;
+        for (int j = j0; j < j1 && ok; ++j) {
+            const int sv = slot;  // this tile's values, then the next tile's keys
+            const uint32_t sv_par = slot_par;
+            next_slot();
+            // the next tile's scores run under this one's softmax; its S was read before the P before was full
             const bool more = j + 1 < j1;
             if (more)
-                scores(tile + 1, item, false, j + 2 == j1);
-            else if (!w.done())
-                scores(tile + 1, item + 1, true, w.j1 - w.j0 == 1);
-            const int iv = 2 * tile + 1, pbuf = tile % S::kPBufs;
-            ok = ok && full(iv);
+                scores(false, j + 2 == j1);
+            else if (follows)
+                scores(true, one);
+            ok = ok && __all_sync(0xffffffffu, wait(&bars->full[sv], sv_par));
             if (!ok) break;
             if (end != 0 && j == last) {  // rows of the last page behind the request's positions: zeros
                 const int r0 = kv_len - j * kKeyTile, r1 = r0 - end + p.cache.page_size;
-                uint8_t *v = sm + S::kOffKV + (iv % S::kSlots) * kTileBytes;
+                uint8_t *v = sm + S::kOffKV + sv * kTileBytes;
                 for (int r = r0 + (lane >> 4); r < r1; r += 2)
                     *reinterpret_cast<uint4 *>(v + ((lane >> 3) & 1) * kHalfBytes + r * 128 + (lane & 7) * 16) =
                         make_uint4(0, 0, 0, 0);
                 fence_proxy_async_smem();
                 __syncwarp();
             }
-            ok = __all_sync(0xffffffffu, wait(&bars->p_full[pbuf], (uint32_t)(tile / S::kPBufs) & 1));
+            ok = __all_sync(0xffffffffu, wait(&bars->p_full[pb], p_par));
             if (ok && j == j0 && item > 0)  // the last item's sums have been read
                 ok = __all_sync(0xffffffffu, wait(&bars->o_free, (uint32_t)(item - 1) & 1));
             if (!ok) break;
             tc_fence_after();
-            const uint32_t a = kv_base + (uint32_t)(iv % S::kSlots) * (kTileBytes >> 4) + ((uint32_t)(kHalfBytes >> 4) << 16);
-            const uint32_t b = p_base + (uint32_t)pbuf * (S::kPBytes >> 4) + ((4096u >> 4) << 16);
+            const uint32_t a = kv_base + (uint32_t)sv * (kTileBytes >> 4) + ((uint32_t)(kHalfBytes >> 4) << 16);
+            const uint32_t b = p_base + (uint32_t)pb * (S::kPBytes >> 4) + ((4096u >> 4) << 16);
+            if (elect()) {
 #pragma unroll
-            for (int x = 0; x < S::kParts; ++x)
+                for (int x = 0; x < S::kParts; ++x)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t bk = b + x * (S::kPart >> 4) + k * 32;
-                    mma_ss(lead, tbase + S::kTmO, high | (a + k * 128), high32 | bk, id_o, j > j0 || x + k > 0);
-                    mma_ss(lead, tbase + S::kTmL, high32 | ones, high32 | bk, id_l, j > j0 || x + k > 0);
-                }
-            commit_if(lead, &bars->empty[iv % S::kSlots]);
-            commit_if(lead, &bars->p_empty[pbuf]);
-            commit_if(lead, &bars->pv_done);
-            if (!more) commit_if(lead, &bars->o_full);
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t bk = b + x * (S::kPart >> 4) + k * 32;
+                        mma_bf16(tbase + S::kTmO, high | (a + k * 128), high32 | bk, id_o, j > j0 || x + k > 0);
+                        if (S::kOnes)
+                            mma_bf16(tbase + S::kTmL, high32 | ones, high32 | bk, id_l, j > j0 || x + k > 0);
+                    }
+                mma_commit(&bars->empty[sv]);
+                mma_commit(&bars->p_empty[pb]);
+                mma_commit(&bars->pv_done);
+                if (!more) mma_commit(&bars->o_full);
+            }
+            __syncwarp();
+            if (++pb == S::kPBufs) {
+                pb = 0;
+                p_par ^= 1;
+            }
         }
         ++item;
     }
     __syncwarp();
-    commit_if(lead, &bars->drain);
+    if (elect()) mma_commit(&bars->drain);
     wait(&bars->drain, 0);
 }
 
@@ -528,13 +603,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Bars<RP> *bars = reinterpret_cast<Bars<RP> *>(sm + S::kOffBars);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int tok_block = min(p.N, kMaxDrafts / p.group), blocks = (p.N + tok_block - 1) / tok_block;
     if (warp < 4) {
         // rows of Q that no box fills, and the ones
         for (int i = threadIdx.x; i < (int)(S::kQBufs * S::kQBytes / 16); i += 128)
             reinterpret_cast<uint4 *>(sm + S::kOffQ)[i] = make_uint4(0, 0, 0, 0);
-        for (int i = threadIdx.x; i < 256; i += 128)
+        for (int i = threadIdx.x; S::kOnes && i < 256; i += 128)
             reinterpret_cast<uint4 *>(sm + S::kOffOnes)[i] =
                 make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
         for (int r = threadIdx.x; r < RP; r += 128) bars->tok_of[r] = (uint8_t)(r / p.group);
@@ -582,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     pdl_trigger();
-    const uint32_t tbase = bars->tmem_base;
+    const uint32_t tbase = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
     const Waiter wait{p.wait_limit_ns, p.err};
     if (warp < 4)
         softmax_role<RP>(p, bars, sm, tbase, warp, lane, blocks, tok_block, wait);
