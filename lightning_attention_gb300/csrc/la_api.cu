@@ -945,9 +945,8 @@ la_status la_attn_extend(const la_bf16 *q, int64_t q_row_stride, const la_bf16 *
     st = attn_params(&p, &work, q, q_row_stride, c, out, B, T, H, Hkv, scale);
     if (st != LA_OK || !work) return st;
     if (!cu_seqlens || !aligned4(cu_seqlens) || !aligned16(workspace)) return LA_ERR_INVALID;
-    la::AttnExtendPlan plan = la::plan_attn_extend(B, T, H, Hkv, max_seqlen, max_kvlen);
-    if (plan.ws_bytes > 0 && (!workspace || (unsigned long long)workspace_bytes < plan.ws_bytes)) plan.nsplit = 1;
-    if (plan.items * plan.nsplit > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
+    const la::AttnExtendPlan plan = la::plan_attn_extend(B, T, H, Hkv, max_seqlen, max_kvlen);
+    p.split = plan.split && workspace && (unsigned long long)workspace_bytes >= plan.ws_bytes;
     p.cu_seqlens = cu_seqlens;
     p.max_seqlen = max_seqlen;
     p.ws = workspace;

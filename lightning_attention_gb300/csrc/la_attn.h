@@ -45,13 +45,13 @@ struct AttnParams {
     unsigned int *err;
     float scale_log2;            // scale * log2 e, positive
     int B, T, H, Hkv, group, N, max_seqlen;
-    int nsplit;                  // extend: CTAs that share the keys of one tile of rows
+    int split;                   // extend: whether CTAs may share the keys of a tile of rows
     unsigned long long wait_limit_ns;
 };
 // Prompts: the tokens of a request are its last positions, each sees those at and before it.
 struct AttnExtendPlan {
-    int nsplit;
-    long long items;             // (row tile, kv head) pairs, an upper bound
+    int split;                   // with a workspace of ws_bytes
+    int ctas, whole_ctas;        // grids with and without
     unsigned long long ws_bytes;
 };
 AttnExtendPlan plan_attn_extend(long long B, long long T, int H, int Hkv, long long max_seqlen,

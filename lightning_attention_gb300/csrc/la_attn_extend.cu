@@ -3,18 +3,24 @@
 //     o_i = sum_j e^{s_ij - m_i} v_j / sum_j e^{s_ij - m_i},   s_ij = scale q_i . k_j
 // in one pass over the keys, m_i a running reference.
 //
-// A CTA owns two tiles of up to 128 rows -- consecutive tokens x the query heads of one kv head, so
-// that the heads of a group share its keys -- and goes over tiles of 128 keys.  Per key tile and row
+// An item is two tiles of up to 128 rows -- consecutive tokens x the query heads of one kv head, so
+// that the heads of a group share its keys -- and the tiles of 128 keys that they see.  Per key tile and row
 // tile, S = Q K^T (tcgen05, fp32 in tensor memory), P = exp2(S scale log2 e - m) by one thread per row
 // (bf16, back into S's columns), O += P V (P from tensor memory, V as it lies in its page).  While one
 // tile's softmax runs, the tensor cores work on the other tile:
 //     S0(j) S1(j) | O0 += P0 V, S0(j+1) | O1 += P1 V, S1(j+1) | ...
 // Warps 0-3 and 4-7: softmax of tile 0 and 1; warp 8 issues the MMAs; warp 9 loads (TMA, a box per page).
 //
-// The reference m_i follows the running maximum only when it falls behind by more than 2^8, so that O,
-// which lies in tensor memory, is rarely rescaled: P is at most 2^8 and sums stay far inside fp32.
+// Bound by the tensor cores: 32 MMAs of 64 cycles per item and key tile, 65 measured.  That leaves a row's thread 1024
+// cycles from S to P, so it goes over S once: weights against the reference it has, and the largest of them beside.
+// The reference follows only when a weight passes 2^8 (then, and for an item's first tile, S is read twice, and O,
+// which lies in tensor memory, is rescaled): sums stay far inside fp32.
 // P is rounded to bf16 (2^-9 of each weight, independent errors: as much as out's own rounding), the sums
 // of its values are formed in fp32 before that.
+//
+// Items differ in length by orders of magnitude, so a CTA per SM takes an equal run of the whole batch's work,
+// item by item, and may begin and end inside one; what it leaves of those, unnormalised, a second launch joins in a
+// fixed order.
 #include <string.h>
 
 #include <algorithm>
@@ -31,25 +37,19 @@ constexpr int kRowTile = 128;
 constexpr int kItemRows = 2 * kRowTile;
 constexpr int kSlots = 5;  // tiles of keys and values in shared memory
 constexpr int kThreads = 384;  // warps 10 and 11 wait for the end: registers are shared out by warp groups
-constexpr int kRegsSoftmax = 208, kRegsRest = 80;
+constexpr int kRegsSoftmax = 208, kRegsRest = 88;
 static_assert(2 * kRegsSoftmax + kRegsRest <= 3 * 168, "register split");
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffKV = kOffQ + 2 * kTileBytes;
 constexpr uint32_t kOffBars = kOffKV + kSlots * kTileBytes;
 
-struct Item {
-    int b, kvh, t0, n, kv_len, tok0;  // request, kv head, its first row, tokens, positions, first token
-    int j0, j1;                       // tiles of keys
-    int row_tok;                      // tokens per row tile
-    long long index;                  // of the item, for partial results
-};
-
 struct Bars {
     uint64_t full[kSlots], empty[kSlots];
-    uint64_t q_full, s_full[2], p_full[2], o_full[2], drain;
-    Item item;
-    int ok;
+    uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], o_free[2], drain;
+    long long lo, hi;  // the CTA's run of the batch's work
+    long long first;   // where its first request's begins
+    int b0;            // its first request
     uint32_t tmem_base;
 };
 constexpr uint32_t kSmemBytes = kOffBars + sizeof(Bars) + 1024;
@@ -58,188 +58,303 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 constexpr uint32_t kTmS = 0, kTmO = 256, kTmCols = 512;
 
 // Geometry of request b, and whether it is sound.
-__device__ __forceinline__ bool request_ok(const AttnParams &p, int b, int &t0, int &n, int &kv_len) {
-    t0 = p.cu_seqlens[b];
+struct Request {
+    int t0, n, kv_len;
+};
+__device__ __forceinline__ bool request_of(const AttnParams &p, int b, Request &r) {
+    r.t0 = p.cu_seqlens[b];
     const int t1 = p.cu_seqlens[b + 1];
-    n = t1 - t0;
-    kv_len = p.cache.kv_lens[b];
-    return t0 >= 0 && t1 >= t0 && t1 <= p.T && n <= p.max_seqlen && kv_len >= n &&
-           kv_len <= (long long)p.cache.max_pages * p.cache.page_size;
+    r.n = t1 - r.t0;
+    r.kv_len = p.cache.kv_lens[b];
+    return r.t0 >= 0 && t1 >= r.t0 && t1 <= p.T && r.n <= p.max_seqlen && r.kv_len >= r.n &&
+           r.kv_len <= (long long)p.cache.max_pages * p.cache.page_size;
 }
 
-// The x-th (tile of rows) of the batch, by request and from a request's last tile to its first: one warp.
-// CTA 0 goes over all requests and reports the faulty ones.
-__device__ bool find_tile(const AttnParams &p, int x, int tok_item, bool report, Item &it) {
+// Work of a kv head's first `items` items of a request: the keys that they see and kItemKeys each for what an item
+// costs besides, or one each where items are not cut.
+constexpr int kItemKeys = 256;
+__device__ __forceinline__ long long work_of(const AttnParams &p, const Request &r, long long items) {
+    if (!p.split) return items;
+    const long long tok = 2 * (kRowTile / p.group);
+    return items * (r.kv_len - r.n + kItemKeys) + tok * (items * (items + 1) / 2);
+}
+__device__ __forceinline__ int items_of(const AttnParams &p, const Request &r) {
+    const int tok = 2 * (kRowTile / p.group);
+    return (r.n + tok - 1) / tok;
+}
+
+// Work of the whole batch; with `report` faulty requests, which have none, are reported.  One warp.
+__device__ __forceinline__ long long sum_work(const AttnParams &p, bool report) {
+    long long all = 0;
+    for (int b = threadIdx.x & 31; b < p.B; b += 32) {
+        Request r;
+        if (request_of(p, b, r))
+            all += work_of(p, r, items_of(p, r)) * p.Hkv;
+        else if (report)
+            atomicOr(p.err, ERR_BIT_SEQLENS);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
+    return all;
+}
+
+// The request within whose work place x lies, and where that begins; false behind the last one's.  One warp.
+__device__ __forceinline__ bool find_request(const AttnParams &p, long long x, int &b, long long &first) {
     const int lane = threadIdx.x & 31;
-    int before = 0;
-    bool found = false;
+    long long before = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int b = b0 + lane;
-        int t0 = 0, n = 0, kv_len = 0, tiles = 0;
-        if (b < p.B) {
-            if (request_ok(p, b, t0, n, kv_len))
-                tiles = (n + tok_item - 1) / tok_item;
-            else if (report)
-                atomicOr(p.err, ERR_BIT_SEQLENS);
-        }
-        int upto = tiles;
+        Request r;
+        const long long mine =
+            b0 + lane < p.B && request_of(p, b0 + lane, r) ? work_of(p, r, items_of(p, r)) * p.Hkv : 0;
+        long long upto = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, upto, d);
+            const long long y = __shfl_up_sync(0xffffffffu, upto, d);
             if (lane >= d) upto += y;
         }
         upto += before;
-        const unsigned hit = __ballot_sync(0xffffffffu, x >= upto - tiles && x < upto);
-        if (hit && !found) {
-            found = true;
-            if (hit & (1u << lane)) {
-                it.b = b;
-                it.t0 = t0;
-                it.n = n;
-                it.kv_len = kv_len;
-                it.tok0 = (upto - 1 - x) * tok_item;
-            }
+        const unsigned hit = __ballot_sync(0xffffffffu, x >= upto - mine && x < upto);
+        if (hit) {
             const int src = __ffs(hit) - 1;
-            it.b = __shfl_sync(0xffffffffu, it.b, src);
-            it.t0 = __shfl_sync(0xffffffffu, it.t0, src);
-            it.n = __shfl_sync(0xffffffffu, it.n, src);
-            it.kv_len = __shfl_sync(0xffffffffu, it.kv_len, src);
-            it.tok0 = __shfl_sync(0xffffffffu, it.tok0, src);
+            b = b0 + src;
+            first = __shfl_sync(0xffffffffu, upto - mine, src);
+            return true;
         }
-        if (found && !report) break;
         before = __shfl_sync(0xffffffffu, upto, 31);
     }
-    return found;
+    return false;
+}
+
+// An item: rows of request b from token tok0 on, kv head kvh, its work [at, at + size), its tiles of keys.
+struct Item {
+    Request r;
+    int b, kvh, t, tok0, tiles;
+    long long at, size;
+    // the item whose work holds place x of request b, whose work begins at `first`
+    __device__ __forceinline__ void find(const AttnParams &p, int b_, long long first, long long x) {
+        b = b_;
+        request_of(p, b, r);
+        const int count = items_of(p, r);
+        const long long head = work_of(p, r, count);
+        kvh = (int)((x - first) / head);
+        const long long rem = x - first - kvh * head;
+        int lo = 0, hi = count - 1;
+        while (lo < hi) {  // the last t whose work begins at rem or before
+            const int mid = (lo + hi + 1) >> 1;
+            if (work_of(p, r, mid) <= rem)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        set(p, lo, first + kvh * head + work_of(p, r, lo));
+    }
+    __device__ __forceinline__ void set(const AttnParams &p, int t_, long long at_) {
+        const int tok = 2 * (kRowTile / p.group);
+        t = t_;
+        at = at_;
+        size = work_of(p, r, t + 1) - work_of(p, r, t);
+        tok0 = t * tok;
+        tiles = (r.kv_len - r.n + min(r.n, tok0 + tok) - 1) / kKeyTile + 1;
+    }
+    // the tile at which the work before place x ends
+    __device__ __forceinline__ int cut(long long x) const {
+        return x <= at ? 0 : x >= at + size ? tiles : (int)((x - at) * tiles / size);
+    }
+    // the next one; false behind the last
+    __device__ __forceinline__ bool next(const AttnParams &p) {
+        const long long end = at + size;
+        if (t + 1 < items_of(p, r)) {
+            set(p, t + 1, end);
+            return true;
+        }
+        if (++kvh == p.Hkv) {
+            kvh = 0;
+            do {
+                if (++b >= p.B) return false;
+            } while (!request_of(p, b, r) || r.n == 0);
+        }
+        set(p, 0, end);
+        return true;
+    }
+};
+
+// The items of a CTA's run, those of which it has no tile left out.
+struct Walk {
+    Item it;
+    long long lo, hi;
+    int j0, j1;
+    bool live;
+    __device__ __forceinline__ void start(const AttnParams &p, const Bars *bars) {
+        lo = bars->lo;
+        hi = bars->hi;
+        live = lo < hi;
+        if (!live) return;
+        it.find(p, bars->b0, bars->first, lo);
+        settle(p);
+    }
+    __device__ __forceinline__ void settle(const AttnParams &p) {
+        while (live) {
+            j0 = it.cut(lo);
+            j1 = it.cut(hi);
+            if (j0 < j1) return;
+            advance(p);
+        }
+    }
+    __device__ __forceinline__ void advance(const AttnParams &p) { live = it.next(p) && it.at < hi; }
+    __device__ __forceinline__ void next(const AttnParams &p) {
+        advance(p);
+        settle(p);
+    }
+};
+
+// A row's reference before it has seen a key: any score passes it, and -inf stays -inf against it.
+constexpr float kUnseen = 1e30f;
+
+// One tile of a row: its weights against the reference as bf16 pairs in w, their sums in l (four partial ones), the
+// largest exponent returned.  S comes in four parts of 32 columns, each fetched while the one before is worked on;
+// columns past `last` are not seen.  Scalar arithmetic: a packed fma.f32x2 takes 4.3 cycles a warp, two fma.f32 2.6.
+template <bool kMask>
+__device__ __forceinline__ float weigh(uint32_t ts, int last, float c, float neg_m, uint32_t (&w)[64], float (&l)[4]) {
+    float top[2] = {-INFINITY, -INFINITY};
+    uint32_t s[2][32];
+    tmem_ld32(ts, s[0]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t(&x)[32] = s[i & 1];
+        tmem_ld_wait_regs(x);
+        if (i < 3) tmem_ld32(ts + (i + 1) * 32, s[(i + 1) & 1]);
+#pragma unroll
+        for (int y = 0; y < 16; ++y) {
+            if (kMask) {
+                if (i * 32 + 2 * y > last) x[2 * y] = 0xff800000u;
+                if (i * 32 + 2 * y + 1 > last) x[2 * y + 1] = 0xff800000u;
+            }
+            float lo = fmaf(__uint_as_float(x[2 * y]), c, neg_m), hi = fmaf(__uint_as_float(x[2 * y + 1]), c, neg_m);
+            top[y & 1] = max3(top[y & 1], lo, hi);
+            lo = ex2z(lo);
+            hi = ex2z(hi);
+            l[(2 * y) & 3] += lo;
+            l[(2 * y + 1) & 3] += hi;
+            w[i * 16 + y] = pack_bf16x2(lo, hi);
+        }
+    }
+    return fmaxf(top[0], top[1]);
+}
+
+// The largest score of a row's tile.
+__device__ __forceinline__ float largest(uint32_t ts, int last) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t x[32];
+        tmem_ld32(ts + i * 32, x);
+        tmem_ld_wait_regs(x);
+#pragma unroll
+        for (int y = 0; y < 32; y += 2)
+            top = max3(top, i * 32 + y > last ? -INFINITY : __uint_as_float(x[y]),
+                       i * 32 + y + 1 > last ? -INFINITY : __uint_as_float(x[y + 1]));
+    }
+    return top;
 }
 
 __device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, int stage, int warp, int lane,
                              const Waiter &wait) {
-    const Item &it = bars->item;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // lane quarter, in the address's upper half
     const uint32_t ts = tbase + kTmS + stage * 128 + lanes, to = tbase + kTmO + stage * 128 + lanes;
-    const int row = (warp & 3) * 32 + lane;
-    const int tok = it.tok0 + stage * it.row_tok + row / p.group, head = row % p.group;
-    const bool valid = row < it.row_tok * p.group && tok < it.n;
-    // last position that the row sees; rows that are not written take any
-    const int limit = it.kv_len - it.n + (valid ? tok : it.n - 1);
-    const uint64_t c2 = f2(p.scale_log2, p.scale_log2);
-    float m = -INFINITY;
-    uint64_t l2[4] = {0, 0, 0, 0};
-    bool ok = true;
-    for (int j = it.j0; j < it.j1; ++j) {
-        ok = __all_sync(0xffffffffu, wait(&bars->s_full[stage], (j - it.j0) & 1));
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t s[4][32];
+    const int row = (warp & 3) * 32 + lane, row_tok = kRowTile / p.group;
+    const int tok_of = stage * row_tok + row / p.group, head = row % p.group;
+    const float c = p.scale_log2;
+    uint32_t tile = 0, item = 0;
+    Walk wk;
+    for (wk.start(p, bars); wk.live; wk.next(p), ++item) {
+        const Item &it = wk.it;
+        const int tok = it.tok0 + tok_of;
+        const bool valid = row < row_tok * p.group && tok < it.r.n;
+        // last position that the row sees; rows that are not written take any
+        const int limit = it.r.kv_len - it.r.n + (valid ? tok : it.r.n - 1);
+        float neg_m = kUnseen;
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int j = wk.j0; j < wk.j1; ++j, ++tile) {
+            if (!__all_sync(0xffffffffu, wait(&bars->s_full[stage], tile & 1))) return;
+            tc_fence_after();
+            const int last = limit - j * kKeyTile;  // columns up to this one are seen
+            const bool mask = __any_sync(0xffffffffu, last < kKeyTile - 1);
+            uint32_t w[64];
+            bool behind = j == wk.j0;
+            if (!behind) {
+                float sum[4] = {l4[0], l4[1], l4[2], l4[3]};
+                const float top = mask ? weigh<true>(ts, last, c, neg_m, w, sum)
+                                       : weigh<false>(ts, last, c, neg_m, w, sum);
+                behind = __any_sync(0xffffffffu, top > 8.f);
+                if (!behind) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(ts + i * 32, s[i]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld_wait_regs(s[i]);
-        const int last = limit - j * kKeyTile;  // columns up to this one are seen
-        if (__any_sync(0xffffffffu, last < kKeyTile - 1)) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int x = 0; x < 32; ++x)
-                    if (i * 32 + x > last) s[i][x] = 0xff800000u;
-        }
-        float top[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            top[i] = __uint_as_float(s[i][0]);
-#pragma unroll
-            for (int x = 1; x < 32; ++x) top[i] = fmaxf(top[i], __uint_as_float(s[i][x]));
-        }
-        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
-        const bool behind = mx > m + 8.f;
-        if (__any_sync(0xffffffffu, behind)) {
-            const float f = behind ? ex2(m - mx) : 1.f;  // 0 from the first visible keys on
-            if (behind) m = mx;
-            const uint64_t ff = f2(f, f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) l2[i] = mul2(l2[i], ff);
-            if (j > it.j0) {  // S(j) comes after O += P(j-1) V, which is complete
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t o[32];
-                    tmem_ld32(to + i * 32, o);
-                    tmem_ld_wait_regs(o);
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                    tmem_st32(to + i * 32, o);
+                    for (int i = 0; i < 4; ++i) l4[i] = sum[i];
                 }
             }
-        }
-        const float sub = m == -INFINITY ? 0.f : -m;
-        const uint64_t m2 = f2(sub, sub);
+            if (behind) {
+                const float top = largest(ts, last) * c;
+                float f = 1.f;
+                if (top > 8.f - neg_m) {
+                    f = neg_m == kUnseen ? 0.f : ex2z(-neg_m - top);
+                    neg_m = -top;
+                }
+                if (j > wk.j0) {  // S(j) comes after O += P(j-1) V, which is complete
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t w[16];
+                    for (int i = 0; i < 4; ++i) l4[i] *= f;
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-                const uint64_t a = fma2(f2(__uint_as_float(s[i][2 * x]), __uint_as_float(s[i][2 * x + 1])), c2, m2);
-                float lo, hi;
-                f2_get(a, lo, hi);
-                lo = ex2(lo);
-                hi = ex2(hi);
-                l2[x & 3] = add2(l2[x & 3], f2(lo, hi));
-                w[x] = pack_bf16x2(lo, hi);
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t o[32];
+                        tmem_ld32(to + i * 32, o);
+                        tmem_ld_wait_regs(o);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                        tmem_st32(to + i * 32, o);
+                    }
+                }
+                weigh<true>(ts, last, c, neg_m, w, l4);
             }
-            tmem_st16(ts + i * 16, w);
+            tmem_st32(ts, *reinterpret_cast<const uint32_t(*)[32]>(&w[0]));
+            tmem_st32(ts + 32, *reinterpret_cast<const uint32_t(*)[32]>(&w[32]));
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->p_full[stage]);
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[stage]);
-    }
-    float la, lb, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f2_get(l2[i], la, lb);
-        l += la + lb;
-    }
-    const bool any = it.j1 > it.j0;
-    if (any) ok = ok && __all_sync(0xffffffffu, wait(&bars->o_full[stage], 0));
-    if (!ok) return;
-    tc_fence_after();
-    if (p.nsplit == 1) {
-        const float inv = 1.f / l;
-        __nv_bfloat16 *dst = p.out + ((long long)(it.t0 + tok) * p.H + it.kvh * p.group + head) * kHeadDim;
+        const float l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        if (!__all_sync(0xffffffffu, wait(&bars->o_full[stage], item & 1))) return;
+        tc_fence_after();
+        const bool whole = wk.j0 == 0 && wk.j1 == it.tiles;
+        const float f = whole ? 1.f / l : 1.f;
+        __nv_bfloat16 *dst = p.out + ((long long)(it.r.t0 + tok) * p.H + it.kvh * p.group + head) * kHeadDim;
+        const long long piece = (2ll * blockIdx.x + (wk.j0 == 0)) * kItemRows + stage * kRowTile + row;
+        float *part = static_cast<float *>(p.ws) + piece * (kHeadDim + 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t o[32];
             tmem_ld32(to + i * 32, o);
             tmem_ld_wait_regs(o);
-            if (valid) {
+            if (!valid) continue;
+            if (whole) {
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     uint32_t w[4];
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
-                        w[y] = pack_bf16x2(__uint_as_float(o[8 * x + 2 * y]) * inv,
-                                           __uint_as_float(o[8 * x + 2 * y + 1]) * inv);
+                        w[y] = pack_bf16x2(__uint_as_float(o[8 * x + 2 * y]) * f, __uint_as_float(o[8 * x + 2 * y + 1]) * f);
                     reinterpret_cast<uint4 *>(dst)[4 * i + x] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
+            } else {
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    reinterpret_cast<uint4 *>(part)[8 * i + x] =
+                        make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
             }
         }
-        return;
-    }
-    const long long piece = blockIdx.x, pieces = gridDim.x;
-    float *po = static_cast<float *>(p.ws) + (piece * kItemRows + stage * kRowTile + row) * kHeadDim;
-    float *ml = static_cast<float *>(p.ws) + pieces * kItemRows * kHeadDim +
-                (piece * kItemRows + stage * kRowTile + row) * 2;
-    if (valid) *reinterpret_cast<float2 *>(ml) = make_float2(any ? m : -INFINITY, l);
-    if (!any) return;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t o[32];
-        tmem_ld32(to + i * 32, o);
-        tmem_ld_wait_regs(o);
-        if (valid) {
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-                reinterpret_cast<uint4 *>(po)[8 * i + x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-        }
+        if (valid && !whole)
+            *reinterpret_cast<float2 *>(part + kHeadDim) = make_float2(neg_m == kUnseen ? -INFINITY : -neg_m, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->o_free[stage]);
     }
 }
 
@@ -253,8 +368,6 @@ __device__ void mma_role(const AttnParams &p, Bars *bars, uint8_t *sm, uint32_t 
     const uint64_t high = sdesc_sw128(0, 0, 1024);
     const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(sm), 0) >> 4;
     const uint32_t q_base = base + (kOffQ >> 4), kv_base = base + (kOffKV >> 4);
-    const int j0 = __shfl_sync(0xffffffffu, bars->item.j0, 0), nt = __shfl_sync(0xffffffffu, bars->item.j1, 0) - j0;
-    const int kv_len = __shfl_sync(0xffffffffu, bars->item.kv_len, 0);
     int slot = 0;  // the next tile to come
     uint32_t phase = 0;
     auto full = [&]() { return __all_sync(0xffffffffu, wait(&bars->full[slot], phase)); };
@@ -264,7 +377,8 @@ __device__ void mma_role(const AttnParams &p, Bars *bars, uint8_t *sm, uint32_t 
             phase ^= 1;
         }
     };
-    auto scores = [&](int stage, int at_slot) {  // S = Q K^T
+    // S = Q K^T; with tile 1's the keys are done with, with the item's last Q too
+    auto scores = [&](int stage, int at_slot, bool last) {
         const uint32_t a = q_base + stage * (kTileBytes >> 4) + (1u << 16);
         const uint32_t b = kv_base + (uint32_t)at_slot * (kTileBytes >> 4) + (1u << 16);
         if (elect()) {
@@ -274,55 +388,72 @@ __device__ void mma_role(const AttnParams &p, Bars *bars, uint8_t *sm, uint32_t 
                 mma_bf16(tbase + kTmS + stage * 128, high | (a + at), high | (b + at), id_s, k > 0);
             }
             mma_commit(&bars->s_full[stage]);
-            if (stage == 1) mma_commit(&bars->empty[at_slot]);
+            if (stage == 1) {
+                mma_commit(&bars->empty[at_slot]);
+                if (last) mma_commit(&bars->q_empty);
+            }
         }
         __syncwarp();
     };
-    bool ok = nt > 0 && __all_sync(0xffffffffu, wait(&bars->q_full, 0)) && full();
-    if (ok) {
-        scores(0, 0);
-        scores(1, 0);
+    bool ok = true;
+    uint32_t tile = 0, item = 0;
+    Walk wk;
+    wk.start(p, bars);
+    while (ok && __shfl_sync(0xffffffffu, (int)wk.live, 0)) {
+        const int j0 = __shfl_sync(0xffffffffu, wk.j0, 0), nt = __shfl_sync(0xffffffffu, wk.j1, 0) - j0;
+        const int kv_len = __shfl_sync(0xffffffffu, wk.it.r.kv_len, 0);
+        const int end = __shfl_sync(0xffffffffu, kv_len % p.cache.page_size, 0);
+        wk.next(p);
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, wait(&bars->q_full, item & 1)) && full();
+        if (!ok) break;
+        tc_fence_after();
+        scores(0, slot, nt == 1);
+        scores(1, slot, nt == 1);
         next();
-    }
-    // rows of the last page behind the request's positions hold anything: zeros for the values
-    const int end = kv_len % p.cache.page_size, last = (kv_len - 1) / kKeyTile - j0;
-    for (int j = 0; j < nt && ok; ++j) {
-        ok = full();
-        const int sv = slot;
-        next();
-        const int sk = slot;
-        if (ok && end != 0 && j == last) {
-            const int r0 = kv_len - (j0 + j) * kKeyTile, r1 = r0 - end + p.cache.page_size;
-            uint8_t *v = sm + kOffKV + sv * kTileBytes;
-            for (int r = r0 + (lane >> 4); r < r1; r += 2)
-                *reinterpret_cast<uint4 *>(v + ((lane >> 3) & 1) * kHalfBytes + r * 128 + (lane & 7) * 16) =
-                    make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-            __syncwarp();
-        }
-        const bool more = j + 1 < nt;
-#pragma unroll
-        for (int stage = 0; stage < 2; ++stage) {
-            ok = ok && __all_sync(0xffffffffu, wait(&bars->p_full[stage], j & 1));
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t b = kv_base + (uint32_t)sv * (kTileBytes >> 4) + ((uint32_t)(kHalfBytes >> 4) << 16);
-            if (elect()) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_f16_tmem_a(tbase + kTmO + stage * 128, tbase + kTmS + stage * 128 + k * 8,
-                                   high | (b + k * 128), id_o, j > 0 || k > 0);
-                if (stage == 1) mma_commit(&bars->empty[sv]);
-                if (!more) mma_commit(&bars->o_full[stage]);
+        // rows of the last page behind the request's positions hold anything: zeros for the values
+        const int last = (kv_len - 1) / kKeyTile - j0;
+        for (int j = 0; j < nt && ok; ++j, ++tile) {
+            ok = full();
+            const int sv = slot;
+            next();
+            const int sk = slot;
+            if (ok && end != 0 && j == last) {
+                const int r0 = kv_len - (j0 + j) * kKeyTile, r1 = r0 - end + p.cache.page_size;
+                uint8_t *v = sm + kOffKV + sv * kTileBytes;
+                for (int r = r0 + (lane >> 4); r < r1; r += 2)
+                    *reinterpret_cast<uint4 *>(v + ((lane >> 3) & 1) * kHalfBytes + r * 128 + (lane & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+                __syncwarp();
             }
-            __syncwarp();
-            if (more) {
-                if (stage == 0) ok = full();
+            const bool more = j + 1 < nt;
+#pragma unroll
+            for (int stage = 0; stage < 2; ++stage) {
+                ok = ok && __all_sync(0xffffffffu, wait(&bars->p_full[stage], tile & 1));
+                if (ok && j == 0 && item > 0)  // the last item's O has been read
+                    ok = __all_sync(0xffffffffu, wait(&bars->o_free[stage], (item - 1) & 1));
                 if (!ok) break;
-                scores(stage, sk);
+                tc_fence_after();
+                const uint32_t b = kv_base + (uint32_t)sv * (kTileBytes >> 4) + ((uint32_t)(kHalfBytes >> 4) << 16);
+                if (elect()) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_f16_tmem_a(tbase + kTmO + stage * 128, tbase + kTmS + stage * 128 + k * 8,
+                                       high | (b + k * 128), id_o, j > 0 || k > 0);
+                    if (stage == 1) mma_commit(&bars->empty[sv]);
+                    if (!more) mma_commit(&bars->o_full[stage]);
+                }
+                __syncwarp();
+                if (more) {
+                    if (stage == 0) ok = full();
+                    if (!ok) break;
+                    scores(stage, sk, j + 2 == nt);
+                }
             }
+            if (more) next();
         }
-        if (more) next();
+        ++item;
     }
     // everything issued is complete before tensor memory is freed
     __syncwarp();
@@ -332,33 +463,40 @@ __device__ void mma_role(const AttnParams &p, Bars *bars, uint8_t *sm, uint32_t 
 
 __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUtensorMap *tk,
                           const CUtensorMap *tv, Bars *bars, uint8_t *sm, int lane, const Waiter &wait) {
-    const Item &it = bars->item;
-    const int nt = it.j1 - it.j0;
-    if (nt <= 0) return;
-    const int box = it.row_tok * p.group * 128;  // bytes of a box: 64 columns
-    if (lane == 0) {
-        mbar_arrive_expect_tx(&bars->q_full, 4 * box);
-        for (int x = 0; x < 4; ++x)
-            tma_load_4d(sm + kOffQ + (x >> 1) * kTileBytes + (x & 1) * kHalfBytes, tq, &bars->q_full, 0,
-                        it.kvh * p.group, it.t0 + it.tok0 + (x >> 1) * it.row_tok, x & 1);
-    }
-    int page = page_of(p.cache, it.b, it.kv_len, it.j0, lane, p.err);
+    const int row_tok = kRowTile / p.group;
+    const int box = row_tok * p.group * 128;  // bytes of a box: 64 columns
     int i = 0;
+    uint32_t item = 0, asked = 0;
     bool ok = true;
-    for (int j = it.j0; j < it.j1 && ok; ++j) {
-        const int next = j + 1 < it.j1 ? page_of(p.cache, it.b, it.kv_len, j + 1, lane, p.err) : 0;
-        for (int kv = 0; kv < 2; ++kv, ++i) {
-            const int slot = i % kSlots;
-            if (i >= kSlots &&
-                !(ok = __all_sync(0xffffffffu, wait(&bars->empty[slot], (uint32_t)(i / kSlots - 1) & 1))))
-                break;
-            load_tile(kv ? tv : tk, sm + kOffKV + slot * kTileBytes, &bars->full[slot], page,
-                      p.cache.page_size, it.kvh, lane);
+    Walk wk;
+    for (wk.start(p, bars); wk.live && ok; wk.next(p), ++item) {
+        const Item &it = wk.it;
+        int page = page_of(p.cache, it.b, it.r.kv_len, wk.j0, lane, p.err);
+        if (item > 0 && !(ok = __all_sync(0xffffffffu, wait(&bars->q_empty, (item - 1) & 1)))) break;
+        if (elect()) {
+            mbar_arrive_expect_tx(&bars->q_full, 4 * box);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                tma_load_4d(sm + kOffQ + (x >> 1) * kTileBytes + (x & 1) * kHalfBytes, tq, &bars->q_full, 0,
+                            it.kvh * p.group, it.r.t0 + it.tok0 + (x >> 1) * row_tok, x & 1);
         }
-        page = next;
+        __syncwarp();
+        asked = item + 1;
+        for (int j = wk.j0; j < wk.j1 && ok; ++j) {
+            const int next = j + 1 < wk.j1 ? page_of(p.cache, it.b, it.r.kv_len, j + 1, lane, p.err) : 0;
+            for (int kv = 0; kv < 2; ++kv, ++i) {
+                const int slot = i % kSlots;
+                if (i >= kSlots &&
+                    !(ok = __all_sync(0xffffffffu, wait(&bars->empty[slot], (uint32_t)(i / kSlots - 1) & 1))))
+                    break;
+                load_tile(kv ? tv : tk, sm + kOffKV + slot * kTileBytes, &bars->full[slot], page,
+                          p.cache.page_size, it.kvh, lane);
+            }
+            page = next;
+        }
     }
     // no copy may be in flight when the CTA exits
-    wait(&bars->q_full, 0);
+    if (asked > 0) wait(&bars->q_full, (asked - 1) & 1);
     for (int x = i > kSlots ? i - kSlots : 0; x < i; ++x) wait(&bars->full[x % kSlots], (uint32_t)(x / kSlots) & 1);
 }
 
@@ -369,57 +507,63 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Bars *bars = reinterpret_cast<Bars *>(sm + kOffBars);
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    pdl_wait();
-    if (warp == 0) {
-        Item it;
-        it.row_tok = kRowTile / p.group;
-        const int split = blockIdx.x % p.nsplit;
-        it.index = blockIdx.x / p.nsplit;
-        it.kvh = (int)(it.index % p.Hkv);
-        const bool ok = find_tile(p, (int)(it.index / p.Hkv), 2 * it.row_tok, blockIdx.x == 0, it);
-        if (ok) {
-            const int last = min(it.n, it.tok0 + 2 * it.row_tok) - 1;
-            const int tiles = (it.kv_len - it.n + last) / kKeyTile + 1;
-            it.j0 = (int)((long long)tiles * split / p.nsplit);
-            it.j1 = (int)((long long)tiles * (split + 1) / p.nsplit);
-        }
-        if (lane == 0) {
-            if (ok) bars->item = it;
-            bars->ok = ok;
-        }
-    } else if (warp == kMmaWarp) {
+    if (warp == kMmaWarp) {
         tmem_alloc(&bars->tmem_base, kTmCols);
         tmem_relinquish();
-    } else if (warp == kLoadWarp && lane == 0) {
-        for (int i = 0; i < kSlots; ++i) {
-            mbar_init(&bars->full[i], 1);
-            mbar_init(&bars->empty[i], 1);
+    } else if (warp == kLoadWarp) {
+        if (lane == 0) {
+            for (int i = 0; i < kSlots; ++i) {
+                mbar_init(&bars->full[i], 1);
+                mbar_init(&bars->empty[i], 1);
+            }
+            mbar_init(&bars->q_full, 1);
+            mbar_init(&bars->q_empty, 1);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&bars->s_full[i], 1);
+                mbar_init(&bars->p_full[i], 4);
+                mbar_init(&bars->o_full[i], 1);
+                mbar_init(&bars->o_free[i], 4);
+            }
+            mbar_init(&bars->drain, 1);
+            fence_mbar_init();
         }
-        mbar_init(&bars->q_full, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars->s_full[i], 1);
-            mbar_init(&bars->p_full[i], 4);
-            mbar_init(&bars->o_full[i], 1);
+        __syncwarp();
+        pdl_wait();
+        const long long all = sum_work(p, blockIdx.x == 0);
+        const long long lo = all * blockIdx.x / gridDim.x, hi = all * (blockIdx.x + 1) / gridDim.x;
+        int b = 0;
+        long long first = 0;
+        if (lo < hi) find_request(p, lo, b, first);
+        if (lane == 0) {
+            bars->lo = lo;
+            bars->hi = hi;
+            bars->b0 = b;
+            bars->first = first;
         }
-        mbar_init(&bars->drain, 1);
-        fence_mbar_init();
     }
+    const int rows = kRowTile / p.group * p.group;
+    if (warp < kMmaWarp && rows < kRowTile) {  // rows of Q that no box fills
+        for (int i = threadIdx.x; i < 4 * (kRowTile - rows) * 8; i += kMmaWarp * 32) {
+            const int block = i / ((kRowTile - rows) * 8), at = i - block * (kRowTile - rows) * 8;
+            reinterpret_cast<uint4 *>(sm + kOffQ + block * kHalfBytes + rows * 128)[at] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+    }
+    if (warp != kLoadWarp) pdl_wait();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
     const Waiter wait{p.wait_limit_ns, p.err};
-    if (bars->ok) {
-        if (warp < kMmaWarp) {
-            reg_inc<kRegsSoftmax>();
-            softmax_role(p, bars, tbase, warp >> 2, warp, lane, wait);
-        } else {
-            reg_dec<kRegsRest>();
-            if (warp == kMmaWarp)
-                mma_role(p, bars, sm, tbase, lane, wait);
-            else if (warp == kLoadWarp)
-                load_role(p, &tq, &tk, &tv, bars, sm, lane, wait);
-        }
+    if (warp < kMmaWarp) {
+        reg_inc<kRegsSoftmax>();
+        softmax_role(p, bars, tbase, warp >> 2, warp, lane, wait);
+    } else {
+        reg_dec<kRegsRest>();
+        if (warp == kMmaWarp)
+            mma_role(p, bars, sm, tbase, lane, wait);
+        else if (warp == kLoadWarp)
+            load_role(p, &tq, &tk, &tv, bars, sm, lane, wait);
     }
     pdl_trigger();
     tc_fence_before();
@@ -427,57 +571,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) tmem_dealloc(tbase, kTmCols);
 }
 
-// The partial results of a tile's rows, joined: o = sum_s 2^{m_s - m} O_s / sum_s 2^{m_s - m} l_s.  A warp
-// per row, in a fixed order.
-__global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
+// The items that several CTAs shared, o = sum_c 2^{m_c - m} O_c / sum_c 2^{m_c - m} l_c over their pieces in order.
+// Block x looks at the end of CTA x's run: the first such end inside an item joins it, a warp per row.
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p, int ctas) {
     __shared__ Item item;
     __shared__ int found;
+    __shared__ long long work;
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row_tok = kRowTile / p.group;
-    const long long index = blockIdx.x;
     if (warp == 0) {
+        const long long all = sum_work(p, false);
+        const long long x = all * (blockIdx.x + 1) / ctas;
         Item it;
-        const bool ok = find_tile(p, (int)(index / p.Hkv), 2 * row_tok, false, it);
+        int b;
+        long long first;
+        bool ok = find_request(p, x, b, first);
+        if (ok) {
+            it.find(p, b, first, x);
+            // ends at its start cut nothing; an earlier end inside it joins it
+            ok = x > it.at && all * blockIdx.x / ctas <= it.at;
+        }
         if (lane == 0) {
-            if (ok) item = it;
             found = ok;
+            work = all;
+            if (ok) item = it;
         }
     }
     __syncthreads();
     if (!found) return;
-    const long long pieces = (long long)gridDim.x * p.nsplit;
-    const float *po = static_cast<const float *>(p.ws);
-    const float2 *ml = reinterpret_cast<const float2 *>(po + pieces * kItemRows * kHeadDim);
+    const Item it = item;
+    const int row_tok = kRowTile / p.group;
+    const float *ws = static_cast<const float *>(p.ws);
+    constexpr int kRowFloats = kHeadDim + 4;
     for (int r = blockIdx.y * 8 + warp; r < kItemRows; r += gridDim.y * 8) {
         const int row = r % kRowTile;
-        const int tok = item.tok0 + (r / kRowTile) * row_tok + row / p.group;
-        if (row >= row_tok * p.group || tok >= item.n) continue;
-        // a lane per piece; at most 32 of them
-        const float2 mine = lane < p.nsplit ? ml[(index * p.nsplit + lane) * kItemRows + r]
-                                            : make_float2(-INFINITY, 0.f);
-        float m = mine.x;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const float w = mine.x == -INFINITY ? 0.f : ex2(mine.x - m);
-        float l = w * mine.y;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        const int tok = it.tok0 + (r / kRowTile) * row_tok + row / p.group;
+        if (row >= row_tok * p.group || tok >= it.r.n) continue;
+        float m = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int s = 0; s < p.nsplit; ++s) {
-            const float ws = __shfl_sync(0xffffffffu, w, s);
-            if (ws == 0.f) continue;
-            const float4 x = reinterpret_cast<const float4 *>(po + ((index * p.nsplit + s) * kItemRows + r) * kHeadDim)[lane];
-            o.x += ws * x.x;
-            o.y += ws * x.y;
-            o.z += ws * x.z;
-            o.w += ws * x.w;
+        for (int c = blockIdx.x; c < ctas; ++c) {
+            const long long lo = work * c / ctas, hi = work * (c + 1) / ctas;
+            if (lo >= it.at + it.size) break;
+            const int j0 = it.cut(lo), j1 = it.cut(hi);
+            if (j0 == j1) continue;
+            if (j0 == 0 && j1 == it.tiles) break;  // one CTA had all of it, and has written it
+            const float *at = ws + ((2ll * c + (j0 == 0)) * kItemRows + r) * kRowFloats;
+            const float2 ml = *reinterpret_cast<const float2 *>(at + kHeadDim);
+            const float4 x = reinterpret_cast<const float4 *>(at)[lane];
+            if (ml.x == -INFINITY) continue;  // none of its keys is seen by the row
+            const float top = fmaxf(m, ml.x), f = ex2z(m - top), g = ex2z(ml.x - top);
+            m = top;
+            l = l * f + ml.y * g;
+            o.x = o.x * f + x.x * g;
+            o.y = o.y * f + x.y * g;
+            o.z = o.z * f + x.z * g;
+            o.w = o.w * f + x.w * g;
         }
+        if (l == 0.f) continue;
         const float inv = 1.f / l;
-        const int h = (int)(index % p.Hkv) * p.group + row % p.group;
-        const uint2 w2 = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        reinterpret_cast<uint2 *>(p.out + ((long long)(item.t0 + tok) * p.H + h) * kHeadDim)[lane] = w2;
+        const int h = it.kvh * p.group + row % p.group;
+        const uint2 w = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        reinterpret_cast<uint2 *>(p.out + ((long long)(it.r.t0 + tok) * p.H + h) * kHeadDim)[lane] = w;
     }
 }
 
@@ -499,26 +654,24 @@ bool make_query_map(CUtensorMap *m, const void *q, long long rows, int H, long l
     return make_bf16_map(m, q, 4, extent, stride, box, true);
 }
 
-// One CTA per pair of row tiles and kv head; where that leaves SMs idle, the keys of each are shared out
-// among up to 32 CTAs and a second launch joins their results.
+// Items that see more than two tiles of keys may be cut; otherwise a CTA takes whole ones, in equal numbers.
 AttnExtendPlan plan_attn_extend(long long B, long long T, int H, int Hkv, long long max_seqlen,
                                 long long max_kvlen) {
     const long long tok = 2 * (kRowTile / (H / Hkv));
     const long long longest = std::min(max_seqlen, T);
-    const long long tiles = std::min(T / tok + std::min(B, T), B * ((longest + tok - 1) / tok));
+    const long long items = std::min(T / tok + std::min(B, T), B * ((longest + tok - 1) / tok)) * Hkv;
+    const long long pieces = (std::max(max_kvlen, longest) + 2 * kKeyTile - 1) / (2 * kKeyTile);  // of an item
     AttnExtendPlan plan;
-    plan.items = tiles * Hkv;
-    plan.nsplit = 1;
-    if (plan.items > 0 && plan.items < kAttnCtas) {
-        const long long most = (std::max(max_kvlen, longest) + kKeyTile - 1) / kKeyTile / 4;
-        plan.nsplit = (int)std::max(1ll, std::min({kAttnCtas / plan.items, most, 32ll}));
-    }
-    plan.ws_bytes = plan.nsplit > 1 ? (unsigned long long)plan.items * plan.nsplit * kItemRows * (kHeadDim + 2) * 4 : 0;
+    plan.split = pieces > 1;
+    plan.ctas = (int)std::min<long long>(items * std::min<long long>(pieces, kAttnCtas), kAttnCtas);
+    plan.whole_ctas = (int)std::min<long long>(items, kAttnCtas);
+    plan.ws_bytes = plan.split ? 2ull * plan.ctas * kItemRows * (kHeadDim + 4) * 4 : 0;
     return plan;
 }
 
 cudaError_t launch_attn_extend(const AttnParams &p, const AttnExtendPlan &plan, cudaStream_t stream) {
-    if (plan.items <= 0) return cudaSuccess;
+    const int ctas = p.split ? plan.ctas : plan.whole_ctas;
+    if (ctas <= 0) return cudaSuccess;
     CUtensorMap tq, tk, tv;
     if (!make_query_map(&tq, p.q, p.T, p.H, p.q_rs, p.group, kRowTile / p.group) ||
         !make_pages_map(&tk, p.cache.k, p.cache, p.Hkv) || !make_pages_map(&tv, p.cache.v, p.cache, p.Hkv))
@@ -537,12 +690,9 @@ cudaError_t launch_attn_extend(const AttnParams &p, const AttnExtendPlan &plan, 
             configured[dev] = true;
         }
     }
-    AttnParams pw = p;
-    pw.nsplit = plan.nsplit;
-    e = launch_pdl(attn_extend_kernel, dim3((unsigned)(plan.items * plan.nsplit)), dim3(kThreads), kSmemBytes,
-                   stream, tq, tk, tv, pw);
-    if (e != cudaSuccess || plan.nsplit == 1) return e;
-    return launch_pdl(attn_join_kernel, dim3((unsigned)plan.items, 4), dim3(256), 0, stream, pw);
+    e = launch_pdl(attn_extend_kernel, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, tq, tk, tv, p);
+    if (e != cudaSuccess || !p.split || ctas == 1) return e;
+    return launch_pdl(attn_join_kernel, dim3((unsigned)(ctas - 1), 8), dim3(256), 0, stream, p, ctas);
 }
 
 }  // namespace la

@@ -296,7 +296,7 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
                                           fmaxf(bars->top[2][tid], bars->top[3][tid]));
                     float f = 1.f;
                     if (t > m) {
-                        f = ex2(m - t);
+                        f = ex2z(m - t);
                         m = t;
                     }
                     bars->factor[tid] = f;
@@ -336,7 +336,7 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
                     float e[4];
 #pragma unroll
                     for (int y = 0; y < 4; ++y)  // a row without keys yet: reference inf, weight 0
-                        e[y] = ex2(mm[y] == INFINITY ? -INFINITY : fmaf(s[g * 16 + x + y], c, mm[y]));
+                        e[y] = ex2z(mm[y] == INFINITY ? -INFINITY : fmaf(s[g * 16 + x + y], c, mm[y]));
                     if (!S::kOnes) {
 #pragma unroll
                         for (int y = 0; y < 4; ++y) sum[S::kOnes ? 0 : g * 16 + x + y] += e[y];
@@ -489,12 +489,14 @@ __device__ void mma_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint3
     Walk w;
     w.start(p, blocks, bars->b0, bars->rem0, bars->x1 - bars->x0);
     int item = 0;
-    if (!w.done()) scores(true, w.j1 - w.j0 == 1);
-    while (!w.done() && ok) {
+    bool live = __shfl_sync(0xffffffffu, (int)!w.done(), 0) != 0;
+    if (live) scores(true, __shfl_sync(0xffffffffu, (int)(w.j1 - w.j0 == 1), 0) != 0);
+    while (live && ok) {
         const int j0 = __shfl_sync(0xffffffffu, w.j0, 0), j1 = __shfl_sync(0xffffffffu, w.j1, 0);
         const int kv_len = __shfl_sync(0xffffffffu, w.kv_len, 0);
         const int end = kv_len % p.cache.page_size, last = (kv_len - 1) / kKeyTile;
         w.next(p);
+        __syncwarp();
         const bool follows = __shfl_sync(0xffffffffu, (int)!w.done(), 0) != 0;
         const bool one = __shfl_sync(0xffffffffu, (int)(w.j1 - w.j0 == 1), 0) != 0;
         for (int j = j0; j < j1 && ok; ++j) {
@@ -547,6 +549,7 @@ __device__ void mma_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint3
             }
         }
         ++item;
+        live = follows;
     }
     __syncwarp();
     if (elect()) mma_commit(&bars->drain);
@@ -707,7 +710,7 @@ __global__ void __launch_bounds__(128) attn_verify_join_kernel(const AttnParams 
             const float2 ml = reinterpret_cast<const float2 *>(at + rp * kHeadDim)[r];
             const float4 x = reinterpret_cast<const float4 *>(at + r * kHeadDim)[lane];
             if (ml.x == -INFINITY) continue;  // none of its keys is seen by the row
-            const float top = fmaxf(m, ml.x), f = ex2(m - top), g = ex2(ml.x - top);
+            const float top = fmaxf(m, ml.x), f = ex2z(m - top), g = ex2z(ml.x - top);
             m = top;
             l = l * f + ml.y * g;
             o.x = o.x * f + x.x * g;

@@ -141,9 +141,11 @@ def test_workspaces(lib):
         assert size(*args, ctypes.byref(nb)) == st, args
     assert size(1, 1, 1, 1, 128, 1, 1, None) == 1
     assert la.attn_extend_workspace_size(0, 0, 1, 1, 128, 0, 0) == 0
-    # long prompts fill the GPU; few rows over many keys are split
-    assert la.attn_extend_workspace_size(1, 16384, 32, 8, 128, 16384, 16384) == 0
-    assert la.attn_extend_workspace_size(1, 64, 8, 1, 128, 64, 30000) > 0
+    # pieces of items that see more than 256 keys, two per CTA at most
+    piece = 2 * 256 * 132 * 4
+    assert la.attn_extend_workspace_size(1, 16384, 32, 8, 128, 16384, 16384) == 152 * piece
+    assert la.attn_extend_workspace_size(1, 1, 8, 1, 128, 1, 1000) == 4 * piece
+    assert la.attn_extend_workspace_size(100, 25600, 8, 1, 128, 256, 256) == 0
 
 
 def test_frequencies():

@@ -78,6 +78,14 @@ def test_extend_scores(spread, scale):
     check_extend([300], [100], 2, 1, seed=8, spread=spread, scale=scale)
 
 
+@pytest.mark.parametrize("new,old,H,Hkv", [([1], [4000], 4, 1), ([1, 1, 1], [300, 9000, 0], 4, 2), ([700, 5], [2000, 700], 12, 2),
+                                           ([33] * 40, [0, 500, 129, 1000] * 10, 8, 2), ([3000], [0], 6, 2),
+                                           ([130, 0, 257, 64] * 6, [0, 5, 300, 64] * 6, 16, 4)])
+def test_extend_runs(new, old, H, Hkv):
+    """Batches whose items are cut at the ends of the CTAs' runs, into two pieces and into many."""
+    check_extend(new, old, H, Hkv, P=16, seed=len(new), tail=3)
+
+
 def test_extend_split_and_whole():
     """Few rows over many keys run split; without scratch for that the same call runs whole."""
     new, old = [3, 40], [3000, 1200]
