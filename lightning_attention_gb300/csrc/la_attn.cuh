@@ -32,31 +32,6 @@ __device__ __forceinline__ void tma_load_4d(void *smem_dst, const void *tmap, ui
         : "memory");
 }
 
-// Lane l < 128 / page_size: the page that holds positions pos .. of request b, pos = tile * 128 + l *
-// page_size; num_pages, whose rows a tiled load fills with zeros, where the request has no such position
-// or the table names a page that does not exist (which is reported).
-__device__ __forceinline__ int page_of(const CacheParams &c, int b, int kv_len, int tile, int lane,
-                                       unsigned int *err) {
-    const long long pos = (long long)tile * kKeyTile + (long long)lane * c.page_size;
-    if (lane >= kKeyTile / c.page_size || pos >= kv_len) return c.num_pages;
-    const int page = c.page_table[(long long)b * c.max_pages + pos / c.page_size];
-    if (page >= 0 && page < c.num_pages) return page;
-    atomicOr(err, ERR_BIT_PAGE);
-    return c.num_pages;
-}
-
-// A whole warp brings one tile in; `page` is page_of's.  Every row of the tile is written.
-__device__ __forceinline__ void load_tile(const CUtensorMap *map, uint8_t *dst, uint64_t *bar, int page,
-                                          int page_size, int head, int lane) {
-    if (lane == 0) mbar_arrive_expect_tx(bar, kTileBytes);
-    __syncwarp();
-    if (lane < kKeyTile / page_size) {
-        uint8_t *at = dst + lane * page_size * 128;
-        tma_load_5d(at, map, bar, 0, 0, 0, head, page);
-        tma_load_5d(at + kHalfBytes, map, bar, 0, 0, 1, head, page);
-    }
-}
-
 // One lane of a converged warp, always the same.  MMAs are issued by `if (elect()) { ... }` around a batch of
 // them and its commits: 38 cycles an issue (N = 16) to 62 (N = 128, as long as the MMA takes); with the instruction
 // predicated on lane 0 60 to 80, the operands' uniform registers being loaded for each.
@@ -68,6 +43,40 @@ __device__ __forceinline__ bool elect() {
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(r));
     return r != 0;
+}
+
+// Pages of a tile: lane l < 128 / page_size has the one that holds positions tile * 128 + l * page_size and on.
+// fetch() asks the table ahead of time (a load that nothing waits for), check() takes its word where the pages are
+// needed: num_pages, whose rows a tiled load fills with zeros, where the request has no such position or the
+// table names a page that does not exist (which is reported).
+struct Pages {
+    int raw;
+    bool there;
+    __device__ __forceinline__ void fetch(const CacheParams &c, int b, int kv_len, int tile, int lane) {
+        const long long pos = (long long)tile * kKeyTile + (long long)lane * c.page_size;
+        there = lane < kKeyTile / c.page_size && pos < kv_len;
+        raw = there ? c.page_table[(long long)b * c.max_pages + pos / c.page_size] : 0;
+    }
+    __device__ __forceinline__ int check(const CacheParams &c, unsigned int *err) const {
+        if (!there) return c.num_pages;
+        if (raw >= 0 && raw < c.num_pages) return raw;
+        atomicOr(err, ERR_BIT_PAGE);
+        return c.num_pages;
+    }
+};
+
+// A whole warp brings one tile in; `page`: Pages::check's.  Every row of the tile is written.
+__device__ __forceinline__ void load_tile(const CUtensorMap *map, uint8_t *dst, uint64_t *bar, int page,
+                                          int page_size, int head) {
+    if (elect()) mbar_arrive_expect_tx(bar, kTileBytes);
+    for (int l = 0; l < kKeyTile / page_size; ++l) {
+        const int at = __shfl_sync(0xffffffffu, page, l);
+        if (elect()) {
+            tma_load_5d(dst + l * page_size * 128, map, bar, 0, 0, 0, head, at);
+            tma_load_5d(dst + l * page_size * 128 + kHalfBytes, map, bar, 0, 0, 1, head, at);
+        }
+    }
+    __syncwarp();
 }
 
 // A bounded wait; the first to give up reports it.

@@ -9,10 +9,12 @@
 // (bf16, back into S's columns), O += P V (P from tensor memory, V as it lies in its page).  While one
 // tile's softmax runs, the tensor cores work on the other tile:
 //     S0(j) S1(j) | O0 += P0 V, S0(j+1) | O1 += P1 V, S1(j+1) | ...
-// Warps 0-3 and 4-7: softmax of tile 0 and 1; warp 8 issues the MMAs; warp 9 loads (TMA, a box per page).
+// Warps 0-7 and 8-15: softmax of tile 0 and 1, two threads a row, one for each half of the keys (one thread took
+// 1400 cycles a tile: with the row's MMAs 2850 in place of 2048); warp 16 issues the MMAs; warp 17 works out the
+// items and loads queries and keys, warp 18 the values (TMA, a box per page and half of the columns).
 //
-// Bound by the tensor cores: 32 MMAs of 64 cycles per item and key tile, 65 measured.  That leaves a row's thread 1024
-// cycles from S to P, so it goes over S once: weights against the reference it has, and the largest of them beside.
+// Bound by the tensor cores: 32 MMAs of 64 cycles per item and key tile, 65 measured.  That leaves a row's threads 1024
+// cycles from S to P, so they go over S once: weights against the reference they have, and the largest of them beside.
 // The reference follows only when a weight passes 2^8 (then, and for an item's first tile, S is read twice, and O,
 // which lies in tensor memory, is rescaled): sums stay far inside fp32.
 // P is rounded to bf16 (2^-9 of each weight, independent errors: as much as out's own rounding), the sums
@@ -36,23 +38,31 @@ using namespace attn;
 constexpr int kRowTile = 128;
 constexpr int kItemRows = 2 * kRowTile;
 constexpr int kSlots = 5;  // tiles of keys and values in shared memory
-constexpr int kThreads = 384;  // warps 10 and 11 wait for the end: registers are shared out by warp groups
-constexpr int kRegsSoftmax = 208, kRegsRest = 88;
-static_assert(2 * kRegsSoftmax + kRegsRest <= 3 * 168, "register split");
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kThreads = 640;
+constexpr int kMmaWarp = 16, kLoadWarp = 17, kValueWarp = 18;
+constexpr int kRegsSoftmax = 104, kRegsRest = 64;  // a thread, by warp groups
+static_assert(4 * kRegsSoftmax + kRegsRest <= 5 * 96, "register split");
+constexpr int kItems = 4;  // items ahead
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffKV = kOffQ + 2 * kTileBytes;
 constexpr uint32_t kOffBars = kOffKV + kSlots * kTileBytes;
 
+// What a CTA's warps have to know of an item.
+struct Rec {
+    int b, t0, n, kv_len, kvh, tok0;  // request, its first row, tokens, positions; kv head; first token
+    int j0, j1, whole;             // tiles of keys that the CTA takes (none: the end of its run), all that there are
+};
+
 struct Bars {
     uint64_t full[kSlots], empty[kSlots];
     uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], o_free[2], drain;
-    long long lo, hi;  // the CTA's run of the batch's work
-    long long first;   // where its first request's begins
-    int b0;            // its first request
+    uint64_t item_full[kItems], item_empty[kItems];
+    Rec items[kItems];
+    float swap[2][2][kRowTile];  // between a row's threads: [row tile][half][row]
+    int loads[2];  // of keys and of values, at the end
     uint32_t tmem_base;
 };
-constexpr uint32_t kSmemBytes = kOffBars + sizeof(Bars) + 1024;
+constexpr uint32_t kSmemBytes = kOffBars + sizeof(Bars);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
 constexpr uint32_t kTmS = 0, kTmO = 256, kTmCols = 512;
@@ -184,12 +194,17 @@ struct Walk {
     long long lo, hi;
     int j0, j1;
     bool live;
-    __device__ __forceinline__ void start(const AttnParams &p, const Bars *bars) {
-        lo = bars->lo;
-        hi = bars->hi;
+    // one warp
+    __device__ __forceinline__ void start(const AttnParams &p) {
+        const long long all = sum_work(p, blockIdx.x == 0);
+        lo = all * blockIdx.x / gridDim.x;
+        hi = all * (blockIdx.x + 1) / gridDim.x;
         live = lo < hi;
         if (!live) return;
-        it.find(p, bars->b0, bars->first, lo);
+        int b = 0;
+        long long first = 0;
+        find_request(p, lo, b, first);
+        it.find(p, b, first, lo);
         settle(p);
     }
     __device__ __forceinline__ void settle(const AttnParams &p) {
@@ -210,25 +225,32 @@ struct Walk {
 // A row's reference before it has seen a key: any score passes it, and -inf stays -inf against it.
 constexpr float kUnseen = 1e30f;
 
-// One tile of a row: its weights against the reference as bf16 pairs in w, their sums in l (four partial ones), the
-// largest exponent returned.  S comes in four parts of 32 columns, each fetched while the one before is worked on;
-// columns past `last` are not seen.  Scalar arithmetic: a packed fma.f32x2 takes 4.3 cycles a warp, two fma.f32 2.6.
+// Half a tile of a row: its weights against the reference as bf16 pairs in w, their sums in l (four partial ones),
+// the largest exponent returned.  Columns past `last` are not seen; lo_last and hi_last: its least and largest value in
+// the warp.  Scalar arithmetic: a packed fma.f32x2 takes 4.3 cycles a warp, two fma.f32 2.6.
 template <bool kMask>
-__device__ __forceinline__ float weigh(uint32_t ts, int last, float c, float neg_m, uint32_t (&w)[64], float (&l)[4]) {
+__device__ __forceinline__ float weigh(uint32_t ts, int last, int lo_last, int hi_last, float c, float neg_m,
+                                       uint32_t (&w)[32], float (&l)[4]) {
     float top[2] = {-INFINITY, -INFINITY};
-    uint32_t s[2][32];
-    tmem_ld32(ts, s[0]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t(&x)[32] = s[i & 1];
+    for (int i = 0; i < 2; ++i) {
+        uint32_t x[32];
+        if (kMask && hi_last < i * 32) {
+#pragma unroll
+            for (int y = 0; y < 16; ++y) w[i * 16 + y] = 0;
+            continue;
+        }
+        tmem_ld32(ts + i * 32, x);
         tmem_ld_wait_regs(x);
-        if (i < 3) tmem_ld32(ts + (i + 1) * 32, s[(i + 1) & 1]);
+        if (kMask) {
+            if (lo_last < i * 32 + 31) {
+#pragma unroll
+                for (int y = 0; y < 32; ++y)
+                    if (i * 32 + y > last) x[y] = 0xff800000u;
+            }
+        }
 #pragma unroll
         for (int y = 0; y < 16; ++y) {
-            if (kMask) {
-                if (i * 32 + 2 * y > last) x[2 * y] = 0xff800000u;
-                if (i * 32 + 2 * y + 1 > last) x[2 * y + 1] = 0xff800000u;
-            }
             float lo = fmaf(__uint_as_float(x[2 * y]), c, neg_m), hi = fmaf(__uint_as_float(x[2 * y + 1]), c, neg_m);
             top[y & 1] = max3(top[y & 1], lo, hi);
             lo = ex2z(lo);
@@ -241,68 +263,117 @@ __device__ __forceinline__ float weigh(uint32_t ts, int last, float c, float neg
     return fmaxf(top[0], top[1]);
 }
 
-// The largest score of a row's tile.
-__device__ __forceinline__ float largest(uint32_t ts, int last) {
-    float top = -INFINITY;
+// The largest score of half a row's tile.
+__device__ __forceinline__ float largest(uint32_t ts, int last, int lo_last, int hi_last) {
+    float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
+        if (hi_last < i * 32) continue;
         uint32_t x[32];
         tmem_ld32(ts + i * 32, x);
         tmem_ld_wait_regs(x);
+        if (lo_last < i * 32 + 31) {
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+                if (i * 32 + y > last) x[y] = 0xff800000u;
+        }
 #pragma unroll
         for (int y = 0; y < 32; y += 2)
-            top = max3(top, i * 32 + y > last ? -INFINITY : __uint_as_float(x[y]),
-                       i * 32 + y + 1 > last ? -INFINITY : __uint_as_float(x[y + 1]));
+            top[(y >> 1) & 1] = max3(top[(y >> 1) & 1], __uint_as_float(x[y]), __uint_as_float(x[y + 1]));
     }
-    return top;
+    return fmaxf(top[0], top[1]);
 }
 
-__device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, int stage, int warp, int lane,
-                             const Waiter &wait) {
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // lane quarter, in the address's upper half
-    const uint32_t ts = tbase + kTmS + stage * 128 + lanes, to = tbase + kTmO + stage * 128 + lanes;
-    const int row = (warp & 3) * 32 + lane, row_tok = kRowTile / p.group;
+// The two warps that share 32 rows; whether any of their threads says so.
+__device__ __forceinline__ bool pair_any(int pair, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 64, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "r"(pair + 1)
+        : "memory");
+    return r != 0;
+}
+
+// Four rows' 64 bytes, a lane each in four pieces, to piece `lane % 4` of the four rows: rows of a quad are then
+// stored 64 bytes at a time (16 at a time the stores of an item hold the SM's store path for 4096 cycles).
+__device__ __forceinline__ void quad_transpose(uint4 (&x)[4], int lane) {
+#pragma unroll
+    for (int d = 1; d <= 2; d <<= 1) {
+        const bool up = (lane & d) != 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & d) continue;
+            uint32_t *a = reinterpret_cast<uint32_t *>(&x[i]), *b = reinterpret_cast<uint32_t *>(&x[i + d]);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? a[y] : b[y], d);
+                if (up)
+                    a[y] = got;
+                else
+                    b[y] = got;
+            }
+        }
+    }
+}
+
+__device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, int warp, int lane, const Waiter &wait) {
+    const int stage = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, pair = stage * 4 + quarter;
+    const uint32_t lanes = (uint32_t)quarter << 21;  // in the address's upper half
+    const uint32_t ts = tbase + kTmS + stage * 128 + lanes, to = tbase + kTmO + stage * 128 + half * 64 + lanes;
+    const int row = quarter * 32 + lane, row_tok = kRowTile / p.group;
     const int tok_of = stage * row_tok + row / p.group, head = row % p.group;
     const float c = p.scale_log2;
+    bool ok = true;
     uint32_t tile = 0, item = 0;
-    Walk wk;
-    for (wk.start(p, bars); wk.live; wk.next(p), ++item) {
-        const Item &it = wk.it;
+    for (;; ++item) {
+        ok = ok && __all_sync(0xffffffffu, wait(&bars->item_full[item % kItems], (item / kItems) & 1));
+        Rec it = bars->items[item % kItems];
+        if (pair_any(pair, !ok) || it.j1 <= it.j0) return;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->item_empty[item % kItems]);
         const int tok = it.tok0 + tok_of;
-        const bool valid = row < row_tok * p.group && tok < it.r.n;
+        const bool valid = row < row_tok * p.group && tok < it.n;
         // last position that the row sees; rows that are not written take any
-        const int limit = it.r.kv_len - it.r.n + (valid ? tok : it.r.n - 1);
+        const int limit = it.kv_len - it.n + (valid ? tok : it.n - 1) - half * 64;
+        const int lo_limit = __reduce_min_sync(0xffffffffu, limit), hi_limit = __reduce_max_sync(0xffffffffu, limit);
         float neg_m = kUnseen;
         float l4[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int j = wk.j0; j < wk.j1; ++j, ++tile) {
-            if (!__all_sync(0xffffffffu, wait(&bars->s_full[stage], tile & 1))) return;
+        for (int j = it.j0; j < it.j1; ++j, ++tile) {
+            ok = ok && __all_sync(0xffffffffu, wait(&bars->s_full[stage], tile & 1));
             tc_fence_after();
-            const int last = limit - j * kKeyTile;  // columns up to this one are seen
-            const bool mask = __any_sync(0xffffffffu, last < kKeyTile - 1);
-            uint32_t w[64];
-            bool behind = j == wk.j0;
-            if (!behind) {
+            // of this half's columns up to `last` are seen
+            const int last = limit - j * kKeyTile, lo_last = lo_limit - j * kKeyTile, hi_last = hi_limit - j * kKeyTile;
+            uint32_t w[32];
+            bool behind = true;
+            if (j > it.j0) {
                 float sum[4] = {l4[0], l4[1], l4[2], l4[3]};
-                const float top = mask ? weigh<true>(ts, last, c, neg_m, w, sum)
-                                       : weigh<false>(ts, last, c, neg_m, w, sum);
-                behind = __any_sync(0xffffffffu, top > 8.f);
+                const float top = lo_last < 63 ? weigh<true>(ts + half * 64, last, lo_last, hi_last, c, neg_m, w, sum)
+                                               : weigh<false>(ts + half * 64, last, lo_last, hi_last, c, neg_m, w, sum);
+                behind = pair_any(pair, top > 8.f || !ok);  // S has been read by both from here on
                 if (!behind) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) l4[i] = sum[i];
                 }
             }
             if (behind) {
-                const float top = largest(ts, last) * c;
+                float top = largest(ts + half * 64, last, lo_last, hi_last);
+                bars->swap[stage][half][row] = top;
+                if (pair_any(pair, !ok)) return;
+                top = fmaxf(top, bars->swap[stage][half ^ 1][row]) * c;
                 float f = 1.f;
                 if (top > 8.f - neg_m) {
                     f = neg_m == kUnseen ? 0.f : ex2z(-neg_m - top);
                     neg_m = -top;
                 }
-                if (j > wk.j0) {  // S(j) comes after O += P(j-1) V, which is complete
+                if (j > it.j0) {  // S(j) comes after O += P(j-1) V, which is complete
 #pragma unroll
                     for (int i = 0; i < 4; ++i) l4[i] *= f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 2; ++i) {
                         uint32_t o[32];
                         tmem_ld32(to + i * 32, o);
                         tmem_ld_wait_regs(o);
@@ -311,50 +382,73 @@ __device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, in
                         tmem_st32(to + i * 32, o);
                     }
                 }
-                weigh<true>(ts, last, c, neg_m, w, l4);
+                weigh<true>(ts + half * 64, last, lo_last, hi_last, c, neg_m, w, l4);
+                pair_any(pair, false);
             }
-            tmem_st32(ts, *reinterpret_cast<const uint32_t(*)[32]>(&w[0]));
-            tmem_st32(ts + 32, *reinterpret_cast<const uint32_t(*)[32]>(&w[32]));
+            tmem_st32(ts + half * 32, w);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->p_full[stage]);
         }
-        const float l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
-        if (!__all_sync(0xffffffffu, wait(&bars->o_full[stage], item & 1))) return;
+        float l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        bars->swap[stage][half][row] = l;
+        ok = ok && __all_sync(0xffffffffu, wait(&bars->o_full[stage], item & 1));
+        if (pair_any(pair, !ok)) return;
+        l += bars->swap[stage][half ^ 1][row];
         tc_fence_after();
-        const bool whole = wk.j0 == 0 && wk.j1 == it.tiles;
-        const float f = whole ? 1.f / l : 1.f;
-        __nv_bfloat16 *dst = p.out + ((long long)(it.r.t0 + tok) * p.H + it.kvh * p.group + head) * kHeadDim;
-        const long long piece = (2ll * blockIdx.x + (wk.j0 == 0)) * kItemRows + stage * kRowTile + row;
-        float *part = static_cast<float *>(p.ws) + piece * (kHeadDim + 4);
+        const long long at = ((long long)(it.t0 + tok) * p.H + it.kvh * p.group + head) * kHeadDim + half * 64;
+        if (it.whole) {
+            const float f = 1.f / l;
+            uint4 w[2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t o[32];
-            tmem_ld32(to + i * 32, o);
-            tmem_ld_wait_regs(o);
-            if (!valid) continue;
-            if (whole) {
+            for (int i = 0; i < 2; ++i) {
+                uint32_t o[32];
+                tmem_ld32(to + i * 32, o);
+                tmem_ld_wait_regs(o);
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    uint32_t w[4];
+                    uint32_t y[4];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        w[y] = pack_bf16x2(__uint_as_float(o[8 * x + 2 * y]) * f, __uint_as_float(o[8 * x + 2 * y + 1]) * f);
-                    reinterpret_cast<uint4 *>(dst)[4 * i + x] = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int z = 0; z < 4; ++z)
+                        y[z] = pack_bf16x2(__uint_as_float(o[8 * x + 2 * z]) * f, __uint_as_float(o[8 * x + 2 * z + 1]) * f);
+                    w[i][x] = make_uint4(y[0], y[1], y[2], y[3]);
                 }
-            } else {
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->o_free[stage]);
+            quad_transpose(w[0], lane);
+            quad_transpose(w[1], lane);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int src = (lane & ~3) | k;
+                const long long to_row = __shfl_sync(0xffffffffu, at, src);
+                if (!__shfl_sync(0xffffffffu, (int)valid, src)) continue;
+                uint4 *dst = reinterpret_cast<uint4 *>(p.out + to_row) + (lane & 3);
+                dst[0] = w[0][k];
+                dst[4] = w[1][k];
+            }
+        } else {
+            const long long piece = (2ll * blockIdx.x + (it.j0 == 0)) * kItemRows + stage * kRowTile + row;
+            float *part = static_cast<float *>(p.ws) + piece * (kHeadDim + 4);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t o[32];
+                tmem_ld32(to + i * 32, o);
+                tmem_ld_wait_regs(o);
+                if (!valid) continue;
 #pragma unroll
                 for (int x = 0; x < 8; ++x)
-                    reinterpret_cast<uint4 *>(part)[8 * i + x] =
+                    reinterpret_cast<uint4 *>(part)[half * 16 + 8 * i + x] =
                         make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
             }
+            if (valid && half == 0)
+                *reinterpret_cast<float2 *>(part + kHeadDim) = make_float2(neg_m == kUnseen ? -INFINITY : -neg_m, l);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->o_free[stage]);
         }
-        if (valid && !whole)
-            *reinterpret_cast<float2 *>(part + kHeadDim) = make_float2(neg_m == kUnseen ? -INFINITY : -neg_m, l);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->o_free[stage]);
     }
 }
 
@@ -397,14 +491,16 @@ __device__ void mma_role(const AttnParams &p, Bars *bars, uint8_t *sm, uint32_t 
     };
     bool ok = true;
     uint32_t tile = 0, item = 0;
-    Walk wk;
-    wk.start(p, bars);
-    while (ok && __shfl_sync(0xffffffffu, (int)wk.live, 0)) {
-        const int j0 = __shfl_sync(0xffffffffu, wk.j0, 0), nt = __shfl_sync(0xffffffffu, wk.j1, 0) - j0;
-        const int kv_len = __shfl_sync(0xffffffffu, wk.it.r.kv_len, 0);
-        const int end = __shfl_sync(0xffffffffu, kv_len % p.cache.page_size, 0);
-        wk.next(p);
+    while (true) {
+        ok = __all_sync(0xffffffffu, wait(&bars->item_full[item % kItems], (item / kItems) & 1));
+        if (!ok) break;
+        const Rec &it = bars->items[item % kItems];
+        const int j0 = __shfl_sync(0xffffffffu, it.j0, 0), nt = __shfl_sync(0xffffffffu, it.j1, 0) - j0;
+        const int kv_len = __shfl_sync(0xffffffffu, it.kv_len, 0);
+        const int end = kv_len % p.cache.page_size;
+        if (nt <= 0) break;
         __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->item_empty[item % kItems]);
         ok = __all_sync(0xffffffffu, wait(&bars->q_full, item & 1)) && full();
         if (!ok) break;
         tc_fence_after();
@@ -453,6 +549,7 @@ __device__ void mma_role(const AttnParams &p, Bars *bars, uint8_t *sm, uint32_t 
             }
             if (more) next();
         }
+        if (!ok) break;
         ++item;
     }
     // everything issued is complete before tensor memory is freed
@@ -461,50 +558,119 @@ __device__ void mma_role(const AttnParams &p, Bars *bars, uint8_t *sm, uint32_t 
     wait(&bars->drain, 0);
 }
 
-__device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUtensorMap *tk,
-                          const CUtensorMap *tv, Bars *bars, uint8_t *sm, int lane, const Waiter &wait) {
+// The tiles that a loading warp fills, every other one of the ring: keys and values in turn.
+struct Ring {
+    int slot, count = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ Ring(int first) : slot(first) {}
+    __device__ __forceinline__ bool load(const AttnParams &p, Bars *bars, uint8_t *sm, const CUtensorMap *map, int page,
+                                         int head, const Waiter &wait) {
+        // a slot's first phase is filled at once: the wait for the one before it returns
+        if (!__all_sync(0xffffffffu, wait(&bars->empty[slot], phase ^ 1))) return false;
+        load_tile(map, sm + kOffKV + slot * kTileBytes, &bars->full[slot], page, p.cache.page_size, head);
+        ++count;
+        slot += 2;
+        if (slot >= kSlots) {
+            slot -= kSlots;
+            phase ^= 1;
+        }
+        return true;
+    }
+};
+
+// No copy may be in flight when the CTA exits: the last load into every slot, of those that the two warps made.
+__device__ void drain_ring(Bars *bars, const Waiter &wait) {
+    for (int s = 0; s < kSlots; ++s) {
+        int last = -1;
+        for (int kv = 0; kv < 2; ++kv)  // load n of warp kv is number 2 n + kv of the ring
+            for (int n = max(0, bars->loads[kv] - kSlots); n < bars->loads[kv]; ++n)
+                if ((2 * n + kv) % kSlots == s) last = max(last, 2 * n + kv);
+        if (last >= 0) wait(&bars->full[s], (uint32_t)(last / kSlots) & 1);
+    }
+}
+
+__device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUtensorMap *tk, Bars *bars, uint8_t *sm,
+                          int lane, const Waiter &wait) {
     const int row_tok = kRowTile / p.group;
     const int box = row_tok * p.group * 128;  // bytes of a box: 64 columns
-    int i = 0;
     uint32_t item = 0, asked = 0;
+    Ring ring(0);
     bool ok = true;
-    Walk wk;
-    for (wk.start(p, bars); wk.live && ok; wk.next(p), ++item) {
-        const Item &it = wk.it;
-        int page = page_of(p.cache, it.b, it.r.kv_len, wk.j0, lane, p.err);
-        if (item > 0 && !(ok = __all_sync(0xffffffffu, wait(&bars->q_empty, (item - 1) & 1)))) break;
-        if (elect()) {
-            mbar_arrive_expect_tx(&bars->q_full, 4 * box);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                tma_load_4d(sm + kOffQ + (x >> 1) * kTileBytes + (x & 1) * kHalfBytes, tq, &bars->q_full, 0,
-                            it.kvh * p.group, it.r.t0 + it.tok0 + (x >> 1) * row_tok, x & 1);
+    auto publish = [&](const Rec &r) {
+        if (item >= kItems)
+            ok = ok && __all_sync(0xffffffffu, wait(&bars->item_empty[item % kItems], (item / kItems - 1) & 1));
+        if (ok && lane == 0) {
+            bars->items[item % kItems] = r;
+            mbar_arrive(&bars->item_full[item % kItems]);
         }
         __syncwarp();
-        asked = item + 1;
+    };
+    Walk wk;
+    for (wk.start(p); wk.live && ok; wk.next(p), ++item) {
+        const Item &it = wk.it;
+        Pages pages;
+        pages.fetch(p.cache, it.b, it.r.kv_len, wk.j0, lane);
+        Rec r;
+        r.b = it.b;
+        r.t0 = it.r.t0;
+        r.n = it.r.n;
+        r.kv_len = it.r.kv_len;
+        r.kvh = it.kvh;
+        r.tok0 = it.tok0;
+        r.j0 = wk.j0;
+        r.j1 = wk.j1;
+        r.whole = wk.j0 == 0 && wk.j1 == it.tiles;
+        publish(r);
         for (int j = wk.j0; j < wk.j1 && ok; ++j) {
-            const int next = j + 1 < wk.j1 ? page_of(p.cache, it.b, it.r.kv_len, j + 1, lane, p.err) : 0;
-            for (int kv = 0; kv < 2; ++kv, ++i) {
-                const int slot = i % kSlots;
-                if (i >= kSlots &&
-                    !(ok = __all_sync(0xffffffffu, wait(&bars->empty[slot], (uint32_t)(i / kSlots - 1) & 1))))
-                    break;
-                load_tile(kv ? tv : tk, sm + kOffKV + slot * kTileBytes, &bars->full[slot], page,
-                          p.cache.page_size, it.kvh, lane);
+            const int page = pages.check(p.cache, p.err);
+            if (j + 1 < wk.j1) pages.fetch(p.cache, it.b, it.r.kv_len, j + 1, lane);
+            ok = ring.load(p, bars, sm, tk, page, it.kvh, wait);
+            if (j > wk.j0 || !ok) continue;
+            // the item's first keys do not wait for the end of the last item's queries
+            if (item > 0 && !(ok = __all_sync(0xffffffffu, wait(&bars->q_empty, (item - 1) & 1)))) break;
+            if (elect()) {
+                mbar_arrive_expect_tx(&bars->q_full, 4 * box);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    tma_load_4d(sm + kOffQ + (x >> 1) * kTileBytes + (x & 1) * kHalfBytes, tq, &bars->q_full, 0,
+                                it.kvh * p.group, it.r.t0 + it.tok0 + (x >> 1) * row_tok, x & 1);
             }
-            page = next;
+            __syncwarp();
+            asked = item + 1;
         }
     }
+    Rec none = {};
+    publish(none);
     // no copy may be in flight when the CTA exits
     if (asked > 0) wait(&bars->q_full, (asked - 1) & 1);
-    for (int x = i > kSlots ? i - kSlots : 0; x < i; ++x) wait(&bars->full[x % kSlots], (uint32_t)(x / kSlots) & 1);
+    if (lane == 0) bars->loads[0] = ring.count;
+}
+
+__device__ void value_role(const AttnParams &p, const CUtensorMap *tv, Bars *bars, uint8_t *sm, int lane,
+                           const Waiter &wait) {
+    Ring ring(1);
+    bool ok = true;
+    for (uint32_t item = 0; ok; ++item) {
+        if (!__all_sync(0xffffffffu, wait(&bars->item_full[item % kItems], (item / kItems) & 1))) break;
+        const Rec it = bars->items[item % kItems];
+        if (it.j1 <= it.j0) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->item_empty[item % kItems]);
+        Pages pages;
+        pages.fetch(p.cache, it.b, it.kv_len, it.j0, lane);
+        for (int j = it.j0; j < it.j1 && ok; ++j) {
+            const int page = pages.check(p.cache, p.err);
+            if (j + 1 < it.j1) pages.fetch(p.cache, it.b, it.kv_len, j + 1, lane);
+            ok = ring.load(p, bars, sm, tv, page, it.kvh, wait);
+        }
+    }
+    if (lane == 0) bars->loads[1] = ring.count;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
     attn_extend_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const AttnParams p) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t sm[];  // no room to align it by hand
     Bars *bars = reinterpret_cast<Bars *>(sm + kOffBars);
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (warp == kMmaWarp) {
@@ -520,25 +686,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars->q_empty, 1);
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&bars->s_full[i], 1);
-                mbar_init(&bars->p_full[i], 4);
+                mbar_init(&bars->p_full[i], 8);
                 mbar_init(&bars->o_full[i], 1);
-                mbar_init(&bars->o_free[i], 4);
+                mbar_init(&bars->o_free[i], 8);
+            }
+            for (int i = 0; i < kItems; ++i) {
+                mbar_init(&bars->item_full[i], 1);
+                mbar_init(&bars->item_empty[i], kMmaWarp + 2);
             }
             mbar_init(&bars->drain, 1);
             fence_mbar_init();
-        }
-        __syncwarp();
-        pdl_wait();
-        const long long all = sum_work(p, blockIdx.x == 0);
-        const long long lo = all * blockIdx.x / gridDim.x, hi = all * (blockIdx.x + 1) / gridDim.x;
-        int b = 0;
-        long long first = 0;
-        if (lo < hi) find_request(p, lo, b, first);
-        if (lane == 0) {
-            bars->lo = lo;
-            bars->hi = hi;
-            bars->b0 = b;
-            bars->first = first;
         }
     }
     const int rows = kRowTile / p.group * p.group;
@@ -549,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
     }
-    if (warp != kLoadWarp) pdl_wait();
+    pdl_wait();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -557,18 +714,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Waiter wait{p.wait_limit_ns, p.err};
     if (warp < kMmaWarp) {
         reg_inc<kRegsSoftmax>();
-        softmax_role(p, bars, tbase, warp >> 2, warp, lane, wait);
+        softmax_role(p, bars, tbase, warp, lane, wait);
     } else {
         reg_dec<kRegsRest>();
         if (warp == kMmaWarp)
             mma_role(p, bars, sm, tbase, lane, wait);
         else if (warp == kLoadWarp)
-            load_role(p, &tq, &tk, &tv, bars, sm, lane, wait);
+            load_role(p, &tq, &tk, bars, sm, lane, wait);
+        else if (warp == kValueWarp)
+            value_role(p, &tv, bars, sm, lane, wait);
     }
     pdl_trigger();
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) tmem_dealloc(tbase, kTmCols);
+    if (warp == kLoadWarp) drain_ring(bars, wait);
 }
 
 // The items that several CTAs shared, o = sum_c 2^{m_c - m} O_c / sum_c 2^{m_c - m} l_c over their pieces in order.

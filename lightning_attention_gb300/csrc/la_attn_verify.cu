@@ -26,8 +26,8 @@ namespace {
 
 using namespace attn;
 
-constexpr int kThreads = 192;  // warps 0-3: softmax, 4: MMAs, 5: loads
-constexpr int kMmaWarp = 4, kLoadWarp = 5;
+constexpr int kThreads = 224;  // warps 0-3: softmax, 4: MMAs, 5: loads of queries and keys, 6: of values
+constexpr int kMmaWarp = 4, kLoadWarp = 5, kValueWarp = 6;
 constexpr int kBarSoftmax = 1;
 
 // What fits into 227 KB.  With 128 rows P is one bf16 (2^-9 of each weight): the products with the second
@@ -60,6 +60,7 @@ struct Bars {
     long long x0, x1;                   // the CTA's run of tiles
     int b0;                             // its first request
     long long rem0;                     // its place among that request's tiles
+    int loads[2];                       // of keys and of values, at the end
     uint32_t tmem_base;
 };
 
@@ -556,46 +557,64 @@ __device__ void mma_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint3
     wait(&bars->drain, 0);
 }
 
+// The tiles that a loading warp fills, every other one of the ring: keys (kv 0, with the queries) and values (1).
 template <int RP>
-__device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUtensorMap *tk, const CUtensorMap *tv,
-                          Bars<RP> *bars, uint8_t *sm, int lane, int blocks, int tok_block, const Waiter &wait) {
+__device__ void load_role(const AttnParams &p, int kv, const CUtensorMap *tq, const CUtensorMap *map, Bars<RP> *bars,
+                          uint8_t *sm, int lane, int blocks, int tok_block, const Waiter &wait) {
     using S = Shape<RP>;
     Walk w;
     w.start(p, blocks, bars->b0, bars->rem0, bars->x1 - bars->x0);
     const uint32_t box = (uint32_t)(tok_block * p.group) * 128;
-    int i = 0, item = 0, asked = 0;
+    int slot = kv, count = 0, item = 0, asked = 0;
+    uint32_t phase = 0;
     bool ok = true;
     for (; !w.done() && ok; w.next(p), ++item) {
-        const int qb = item % S::kQBufs;
-        if (item >= S::kQBufs &&
-            !(ok = __all_sync(0xffffffffu, wait(&bars->q_empty[qb], (uint32_t)(item / S::kQBufs - 1) & 1))))
-            break;
-        if (lane == 0) {
-            mbar_arrive_expect_tx(&bars->q_full[qb], 2 * box);
-            for (int x = 0; x < 2; ++x)
-                tma_load_4d(sm + S::kOffQ + qb * S::kQBytes + x * (S::kQBytes / 2), tq, &bars->q_full[qb], 0,
-                            w.kvh * p.group, w.b * p.N + w.rb * tok_block, x);
-        }
-        asked = item + 1;
-        int page = page_of(p.cache, w.b, w.kv_len, w.j0, lane, p.err);
-        for (int j = w.j0; j < w.j1 && ok; ++j) {
-            const int next = j + 1 < w.j1 ? page_of(p.cache, w.b, w.kv_len, j + 1, lane, p.err) : 0;
-            for (int kv = 0; kv < 2; ++kv, ++i) {
-                const int slot = i % S::kSlots;
-                if (i >= S::kSlots &&
-                    !(ok = __all_sync(0xffffffffu, wait(&bars->empty[slot], (uint32_t)(i / S::kSlots - 1) & 1))))
-                    break;
-                load_tile(kv ? tv : tk, sm + S::kOffKV + slot * kTileBytes, &bars->full[slot], page,
-                          p.cache.page_size, w.kvh, lane);
+        Pages pages;
+        pages.fetch(p.cache, w.b, w.kv_len, w.j0, lane);
+        if (kv == 0) {
+            const int qb = item % S::kQBufs;
+            // a buffer's first phase is filled at once: the wait for the one before it returns
+            if (!(ok = __all_sync(0xffffffffu, wait(&bars->q_empty[qb], (uint32_t)(item / S::kQBufs + 1) & 1)))) break;
+            if (elect()) {
+                mbar_arrive_expect_tx(&bars->q_full[qb], 2 * box);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    tma_load_4d(sm + S::kOffQ + qb * S::kQBytes + x * (S::kQBytes / 2), tq, &bars->q_full[qb], 0,
+                                w.kvh * p.group, w.b * p.N + w.rb * tok_block, x);
             }
-            page = next;
+            __syncwarp();
+            asked = item + 1;
+        }
+        for (int j = w.j0; j < w.j1; ++j) {
+            const int page = pages.check(p.cache, p.err);
+            if (j + 1 < w.j1) pages.fetch(p.cache, w.b, w.kv_len, j + 1, lane);
+            if (!(ok = __all_sync(0xffffffffu, wait(&bars->empty[slot], phase ^ 1)))) break;
+            load_tile(map, sm + S::kOffKV + slot * kTileBytes, &bars->full[slot], page, p.cache.page_size, w.kvh);
+            ++count;
+            slot += 2;
+            if (slot >= S::kSlots) {
+                slot -= S::kSlots;
+                phase ^= 1;
+            }
         }
     }
     // no copy may be in flight when the CTA exits
-    for (int x = i > S::kSlots ? i - S::kSlots : 0; x < i; ++x)
-        wait(&bars->full[x % S::kSlots], (uint32_t)(x / S::kSlots) & 1);
     for (int x = asked > S::kQBufs ? asked - S::kQBufs : 0; x < asked; ++x)
         wait(&bars->q_full[x % S::kQBufs], (uint32_t)(x / S::kQBufs) & 1);
+    if (lane == 0) bars->loads[kv] = count;
+}
+
+// The last load into every slot, of those that the two warps made.
+template <int RP>
+__device__ void drain_ring(Bars<RP> *bars, const Waiter &wait) {
+    constexpr int n_slots = Shape<RP>::kSlots;
+    for (int s = 0; s < n_slots; ++s) {
+        int last = -1;
+        for (int kv = 0; kv < 2; ++kv)  // load n of warp kv is number 2 n + kv of the ring
+            for (int n = max(0, bars->loads[kv] - n_slots); n < bars->loads[kv]; ++n)
+                if ((2 * n + kv) % n_slots == s) last = max(last, 2 * n + kv);
+        if (last >= 0) wait(&bars->full[s], (uint32_t)(last / n_slots) & 1);
+    }
 }
 
 template <int RP>
@@ -620,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kMmaWarp) {
         tmem_alloc(&bars->tmem_base, S::kTmCols);
         tmem_relinquish();
-    } else {
+    } else if (warp == kLoadWarp) {
         if (lane == 0) {
             for (int i = 0; i < S::kSlots; ++i) {
                 mbar_init(&bars->full[i], 1);
@@ -667,10 +686,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     else if (warp == kMmaWarp)
         mma_role<RP>(p, bars, sm, tbase, lane, blocks, wait);
     else
-        load_role<RP>(p, &tq, &tk, &tv, bars, sm, lane, blocks, tok_block, wait);
+        load_role<RP>(p, warp == kValueWarp, &tq, warp == kValueWarp ? &tv : &tk, bars, sm, lane, blocks, tok_block, wait);
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) tmem_dealloc(tbase, S::kTmCols);
+    if (warp == kLoadWarp) drain_ring<RP>(bars, wait);
 }
 
 // The (request, kv head, block of drafts)s that several CTAs shared.  grid: one block of 4 warps per such
