@@ -82,7 +82,7 @@ __device__ __forceinline__ bool request_of(const AttnParams &p, int b, Request &
 
 // Work of a kv head's first `items` items of a request: the keys that they see and kItemKeys each for what an item
 // costs besides, or one each where items are not cut.
-constexpr int kItemKeys = 256;
+constexpr int kItemKeys = 400;
 __device__ __forceinline__ long long work_of(const AttnParams &p, const Request &r, long long items) {
     if (!p.split) return items;
     const long long tok = 2 * (kRowTile / p.group);
