@@ -10,8 +10,8 @@
 // launch joins in a fixed order.
 //
 // With few rows the keys take the 128 lanes of the tensor cores: S^T = K Q^T and O^T += V^T P^T, both with
-// N = R (padded to 16, 32, 64 or 128), K and V as they lie in their pages.  A thread owns a key in the
-// softmax and a column of v in the result.  The reference m_r is that of the first tile and follows only
+// N = R (padded to 16, 32, 64 or 128), K and V as they lie in their pages.  Two threads share a key in the
+// softmax, half of the rows each, and a column of v in the result.  The reference m_r is that of the first tile and follows only
 // when a score passes it by more than 2^8, so that a tile takes no maximum, one test.  P goes into shared memory as bf16 pairs hi + lo (off by at
 // most 2^-16), which the idle tensor cores take at no cost.
 #include <string.h>
@@ -26,9 +26,10 @@ namespace {
 
 using namespace attn;
 
-constexpr int kThreads = 224;  // warps 0-3: softmax, 4: MMAs, 5: loads of queries and keys, 6: of values
-constexpr int kMmaWarp = 4, kLoadWarp = 5, kValueWarp = 6;
+constexpr int kThreads = 352;  // warps 0-7: softmax, 8: MMAs, 9: loads of queries and keys, 10: of values
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kValueWarp = 10;
 constexpr int kBarSoftmax = 1;
+constexpr float kUnseen = 1e30f;  // minus the reference of a row that has seen no key: any score passes it, -inf stays
 
 // What fits into 227 KB.  With 128 rows P is one bf16 (2^-9 of each weight): the products with the second
 // part would take the tensor cores as long as HBM takes for the tile.
@@ -52,7 +53,7 @@ template <int RP>
 struct Bars {
     uint64_t full[5], empty[5];
     uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], p_empty[2], pv_done, o_full, o_free, drain;
-    alignas(16) float neg_m[RP];        // minus the references, in log 2; inf where a row has seen no key
+    alignas(16) float neg_m[RP];        // minus the references, in log 2
     alignas(16) float factor[RP];
     float top[4][RP];
     uint8_t tok_of[RP];
@@ -162,7 +163,7 @@ __device__ __forceinline__ bool softmax_any(bool x) {
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+        "barrier.cta.red.or.pred q, %2, 256, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
         : "r"((uint32_t)x), "n"(kBarSoftmax)
@@ -170,7 +171,7 @@ __device__ __forceinline__ bool softmax_any(bool x) {
     return r != 0;
 }
 __device__ __forceinline__ void softmax_sync() {
-    asm volatile("barrier.cta.sync %0, 128;" ::"n"(kBarSoftmax) : "memory");
+    asm volatile("barrier.cta.sync %0, 256;" ::"n"(kBarSoftmax) : "memory");
 }
 __device__ __forceinline__ float redux_max(float x) {
     float r;
@@ -178,12 +179,14 @@ __device__ __forceinline__ float redux_max(float x) {
     return r;
 }
 
-// Which drafts descend from which; false if a parent is out of range.  128 threads.
+// Which drafts descend from which; false if a parent is out of range.  256 threads.
 template <int RP>
 __device__ bool build_tree(const AttnParams &p, Bars<RP> *bars, int b, int tid) {
     softmax_sync();  // the last request's table is not read any more
+    if (tid < kMaxDrafts) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) bars->below[tid][i] = 0;
+        for (int i = 0; i < 4; ++i) bars->below[tid][i] = 0;
+    }
     softmax_sync();
     bool bad = false;
     if (tid < p.N) {
@@ -203,18 +206,56 @@ __device__ bool build_tree(const AttnParams &p, Bars<RP> *bars, int b, int tid) 
     return !softmax_any(bad);
 }
 
+// n (8 or a multiple of 16) columns of tensor memory.
+template <int n>
+__device__ __forceinline__ void tmem_get(uint32_t at, float (&x)[n]) {
+    if (n == 8) {
+        uint32_t r[8];
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+                     "tcgen05.wait::ld.sync.aligned;"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(at)
+                     : "memory");
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i % n] = __uint_as_float(r[i]);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < n / 16 * 16; i += 16) {
+        uint32_t r[16];
+        tmem_ld16(at + i, r);
+        tmem_ld_wait_regs(r);
+#pragma unroll
+        for (int y = 0; y < 16; ++y) x[(i + y) % n] = __uint_as_float(r[y]);
+    }
+}
+template <int n>
+__device__ __forceinline__ void tmem_put(uint32_t at, const float (&x)[n]) {
+#pragma unroll
+    for (int i = 0; i < n; i += 8) {
+        uint32_t r[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) r[y] = __float_as_uint(x[i + y]);
+        tmem_st8(at + i, r);
+    }
+    tmem_st_wait();
+}
+
+// Two threads a key: warps 0-3 have the first half of the rows, warps 4-7 the other.
 template <int RP>
 __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint32_t tbase, int warp, int lane,
                              int blocks, int tok_block, const Waiter &wait) {
     using S = Shape<RP>;
-    const int tid = warp * 32 + lane;
-    const uint32_t lanes = (uint32_t)warp << 21;
+    constexpr int R = RP / 2;  // rows of a thread
+    const int tid = warp * 32 + lane, key = tid & 127, half = warp >> 2;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const int r0 = half * R;
     const float c = p.scale_log2;
     // rows without keys: a request of no positions
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
         const int kv = p.cache.kv_lens[b];
         if (kv == 0) {
-            for (int i = tid; i < p.N * p.H * (kHeadDim / 8); i += 128)
+            for (int i = tid; i < p.N * p.H * (kHeadDim / 8); i += 256)
                 reinterpret_cast<uint4 *>(p.out + (long long)b * p.N * p.H * kHeadDim)[i] = make_uint4(0, 0, 0, 0);
         } else if (tiles_of(p, b) == 0 && tid == 0) {
             atomicOr(p.err, ERR_BIT_PAGE);
@@ -224,11 +265,11 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
     w.start(p, blocks, bars->b0, bars->rem0, bars->x1 - bars->x0);
     int tile = 0, item = 0, tree_of = -1;
     bool ok = true, sound = true;
-    float sum[S::kOnes ? 1 : RP];  // of this thread's keys
+    float sum[S::kOnes ? 1 : R];  // of this thread's key
     for (; !w.done(); w.next(p), ++item) {
         if (!S::kOnes) {
 #pragma unroll
-            for (int r = 0; r < RP; ++r) sum[S::kOnes ? 0 : r] = 0.f;
+            for (int r = 0; r < R; ++r) sum[S::kOnes ? 0 : r] = 0.f;
         }
         if (p.parents && tree_of != w.b) {
             sound = build_tree(p, bars, w.b, tid);
@@ -239,126 +280,113 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
         for (int j = w.j0; j < w.j1; ++j, ++tile) {
             const int buf = tile & 1, pbuf = tile % S::kPBufs;
             ok = ok && __all_sync(0xffffffffu, wait(&bars->s_full[buf], (uint32_t)(tile >> 1) & 1));
-            if (tile >= S::kPBufs)
-                ok = ok && __all_sync(0xffffffffu, wait(&bars->p_empty[pbuf],
-                                                        (uint32_t)(tile / S::kPBufs - 1) & 1));
             tc_fence_after();
-            float s[RP];
-#pragma unroll
-            for (int i = 0; i < RP; i += 16) {
-                uint32_t r[16];
-                tmem_ld16(tbase + lanes + buf * RP + i, r);
-                tmem_ld_wait_regs(r);
-#pragma unroll
-                for (int x = 0; x < 16; ++x) s[i + x] = __uint_as_float(r[x]);
-            }
-            const int pos = j * kKeyTile + tid;
-            if ((j + 1) * kKeyTile > ctx) {  // the tile holds drafts, or ends behind the request
-                const int d = pos - ctx;
+            float s[R];  // the scores, then the exponents
+            auto fetch = [&]() {
+                tmem_get<R>(tbase + lanes + buf * RP + r0, s);
+                if ((j + 1) * kKeyTile <= ctx) return;
+                // the tile holds drafts, or ends behind the request
+                const int d = j * kKeyTile + key - ctx;
                 if (d >= p.N) {
 #pragma unroll
-                    for (int r = 0; r < RP; ++r) s[r] = -INFINITY;
+                    for (int r = 0; r < R; ++r) s[r] = -INFINITY;
                 } else if (d >= 0 && p.parents) {
                     uint32_t see[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) see[i] = bars->below[d][i];
 #pragma unroll
-                    for (int r = 0; r < RP; ++r) {
-                        const int t = min(w.rb * tok_block + bars->tok_of[r], kMaxDrafts - 1);
+                    for (int r = 0; r < R; ++r) {
+                        const int t = min(w.rb * tok_block + bars->tok_of[r0 + r], kMaxDrafts - 1);
                         const uint32_t word = t < 64 ? (t < 32 ? see[0] : see[1]) : (t < 96 ? see[2] : see[3]);
                         if (!((word >> (t & 31)) & 1u)) s[r] = -INFINITY;
                     }
                 }
-            }
-            // a score far above its row's reference (or the first tile): new references
-            float far = -INFINITY;
-            const bool first = j == w.j0;
-            if (!first) {
+            };
+            auto exponents = [&]() {
 #pragma unroll
-                for (int r = 0; r < RP; r += 4) {
-                    const float4 m = *reinterpret_cast<const float4 *>(&bars->neg_m[r]);
-                    far = fmaxf(far, fmaxf(fmaxf(fmaf(s[r], c, m.x), fmaf(s[r + 1], c, m.y)),
-                                           fmaxf(fmaf(s[r + 2], c, m.z), fmaf(s[r + 3], c, m.w))));
+                for (int r = 0; r < R; r += 4) {
+                    const float4 m = *reinterpret_cast<const float4 *>(&bars->neg_m[r0 + r]);
+                    s[r] = fmaf(s[r], c, m.x);
+                    s[r + 1] = fmaf(s[r + 1], c, m.y);
+                    s[r + 2] = fmaf(s[r + 2], c, m.z);
+                    s[r + 3] = fmaf(s[r + 3], c, m.w);
                 }
-            }
-            if (softmax_any(first || far > 8.f || !ok)) {
+            };
+            fetch();
+            // against the rows' references; new ones with the first tile and where one is passed by more than 2^8
+            const bool first = j == w.j0;
+            float far = first ? INFINITY : -INFINITY;
+            if (!first) {
+                exponents();
 #pragma unroll
-                for (int r = 0; r < RP; ++r) {
+                for (int r = 0; r < R; r += 4) far = max3(max3(far, s[r], s[r + 1]), s[r + 2], s[r + 3]);
+            }
+            if (softmax_any(far > 8.f || !ok)) {
+                if (!first) fetch();
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
                     const float t = redux_max(s[r]);
-                    if (lane == 0) bars->top[warp][r] = t * c;
+                    if (lane == 0) bars->top[warp & 3][r0 + r] = t * c;
                 }
                 if (softmax_any(!ok)) {
                     ok = false;
                     break;
                 }
                 if (tid < RP) {
-                    float m = first ? -INFINITY : -bars->neg_m[tid];
+                    const float old = first ? kUnseen : bars->neg_m[tid];
                     const float t = fmaxf(fmaxf(bars->top[0][tid], bars->top[1][tid]),
                                           fmaxf(bars->top[2][tid], bars->top[3][tid]));
-                    float f = 1.f;
-                    if (t > m) {
-                        f = ex2z(m - t);
-                        m = t;
-                    }
-                    bars->factor[tid] = f;
-                    bars->neg_m[tid] = -m;
+                    const bool follow = t > -old;  // never where no key is seen
+                    bars->factor[tid] = !follow ? 1.f : old == kUnseen ? 0.f : ex2z(-old - t);
+                    bars->neg_m[tid] = follow ? -t : old;
                 }
                 softmax_sync();
+                exponents();
                 if (!S::kOnes) {
 #pragma unroll
-                    for (int r = 0; r < RP; ++r) sum[S::kOnes ? 0 : r] *= bars->factor[r];
+                    for (int r = 0; r < R; ++r) sum[S::kOnes ? 0 : r] *= bars->factor[r0 + r];
                 }
                 if (!first) {  // O and the sums, once the last tile is in them
                     ok = __all_sync(0xffffffffu, wait(&bars->pv_done, (uint32_t)(tile - 1) & 1));
                     tc_fence_after();
                     if (ok) {
 #pragma unroll
-                        for (int i = 0; i < (S::kOnes ? 2 : 1) * RP; i += 16) {
-                            uint32_t o[16];
-                            tmem_ld16(tbase + lanes + S::kTmO + i, o);
-                            tmem_ld_wait_regs(o);
+                        for (int x = 0; x < (S::kOnes ? 2 : 1); ++x) {
+                            float o[R];
+                            const uint32_t at = tbase + lanes + (x ? S::kTmL : S::kTmO) + r0;
+                            tmem_get<R>(at, o);
 #pragma unroll
-                            for (int x = 0; x < 16; ++x)
-                                o[x] = __float_as_uint(__uint_as_float(o[x]) * bars->factor[(i + x) % RP]);
-                            tmem_st16(tbase + lanes + S::kTmO + i, o);
+                            for (int r = 0; r < R; ++r) o[r] *= bars->factor[r0 + r];
+                            tmem_put<R>(at, o);
                         }
-                        tmem_st_wait();
                     }
                 }
             }
-            uint8_t *ph = sm + S::kOffP + pbuf * S::kPBytes + tid * 32;
+            if (tile >= S::kPBufs)
+                ok = ok && __all_sync(0xffffffffu, wait(&bars->p_empty[pbuf], (uint32_t)(tile / S::kPBufs - 1) & 1));
+            // groups of 16 rows are 4 KB apart, a key's 32 bytes in pieces of 16, swapped in every other four keys
+            uint8_t *ph = sm + S::kOffP + pbuf * S::kPBytes + key * 32;
+            const uint32_t turn = ((uint32_t)key >> 2 & 1u) << 4;
 #pragma unroll
-            for (int g = 0; g < RP / 16; ++g) {
-                uint32_t hi[8], lo[8];
+            for (int g = 0; g < R; g += 8) {
+                uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int x = 0; x < 16; x += 4) {
-                    const float4 m = *reinterpret_cast<const float4 *>(&bars->neg_m[g * 16 + x]);
-                    const float mm[4] = {m.x, m.y, m.z, m.w};
-                    float e[4];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y)  // a row without keys yet: reference inf, weight 0
-                        e[y] = ex2z(mm[y] == INFINITY ? -INFINITY : fmaf(s[g * 16 + x + y], c, mm[y]));
+                for (int x = 0; x < 8; x += 2) {
+                    const float e0 = ex2z(s[g + x]), e1 = ex2z(s[g + x + 1]);
                     if (!S::kOnes) {
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) sum[S::kOnes ? 0 : g * 16 + x + y] += e[y];
+                        sum[S::kOnes ? 0 : g + x] += e0;
+                        sum[S::kOnes ? 0 : g + x + 1] += e1;
                     }
-#pragma unroll
-                    for (int y = 0; y < 4; y += 2) {
-                        const uint32_t h = pack_bf16x2(e[y], e[y + 1]);
-                        hi[(x + y) / 2] = h;
-                        lo[(x + y) / 2] = pack_bf16x2(e[y] - __uint_as_float(h << 16),
-                                                      e[y + 1] - __uint_as_float(h & 0xffff0000u));
-                    }
+                    const uint32_t h = pack_bf16x2(e0, e1);
+                    hi[x / 2] = h;
+                    if (S::kParts == 2)
+                        lo[x / 2] = pack_bf16x2(e0 - __uint_as_float(h << 16), e1 - __uint_as_float(h & 0xffff0000u));
                 }
-                // groups of 16 rows are 4 KB apart, a key's 32 bytes in pieces of 16, swapped in every other four keys
-                const uint32_t turn = ((uint32_t)tid >> 2 & 1u) << 4;
-                uint8_t *at = ph + g * 4096;
-                *reinterpret_cast<uint4 *>(at + turn) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(at + (turn ^ 16u)) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-                if (S::kParts == 2) {
-                    *reinterpret_cast<uint4 *>(at + S::kPart + turn) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    *reinterpret_cast<uint4 *>(at + S::kPart + (turn ^ 16u)) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
-                }
+                const int row = r0 + g;
+                uint8_t *at = ph + (row >> 4) * 4096 + (turn ^ ((row & 8) ? 16u : 0u));
+                *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                if (S::kParts == 2)
+                    *reinterpret_cast<uint4 *>(at + S::kPart) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
             fence_proxy_async_smem();
             tc_fence_before();
@@ -368,15 +396,15 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
         if (!ok) break;
         // the item's sums: over the lanes, each step with half the rows, then over the warps
         if (!S::kOnes) {
-            int row = 0;
+            int row = r0;
 #pragma unroll
-            for (int d = 16, n = RP; d > 0; d >>= 1) {
+            for (int d = 16, n = R; d > 0; d >>= 1) {
                 if (n > 1) {
                     n >>= 1;
                     const bool up = (lane & d) != 0;
                     if (up) row += n;
 #pragma unroll
-                    for (int i = 0; i < RP / 2; ++i)
+                    for (int i = 0; i < R / 2; ++i)
                         if (i < n) {
                             const float mine = up ? sum[i + n] : sum[i], other = up ? sum[i] : sum[i + n];
                             sum[i] = mine + __shfl_xor_sync(0xffffffffu, other, d);
@@ -385,11 +413,10 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
                     sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], d);
                 }
             }
-#pragma unroll
-            for (int i = 0; i < (RP > 32 ? RP / 32 : 1); ++i) bars->top[warp][row + i] = sum[i];
+            bars->top[warp & 3][row] = sum[0];
             softmax_sync();
         }
-        // thread tid holds column tid of v
+        // this thread holds column `key` of v
         ok = __all_sync(0xffffffffu, wait(&bars->o_full, (uint32_t)item & 1));
         tc_fence_after();
         const int toks = min(tok_block, p.N - w.rb * tok_block), rows = toks * p.group;
@@ -397,41 +424,35 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
         const long long piece = 2ll * blockIdx.x + (w.j0 == 0 ? 1 : 0);
         float *po = static_cast<float *>(p.ws) + piece * RP * (kHeadDim + 2);
         if (ok) {
+            float o[R], l[R];
+            tmem_get<R>(tbase + lanes + S::kTmO + r0, o);
+            if (S::kOnes) tmem_get<R>(tbase + lanes + S::kTmL + r0, l);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->o_free);
+            if (!S::kOnes) {
 #pragma unroll
-            for (int i = 0; i < RP; i += 16) {
-                uint32_t o[16], l[16];
-                tmem_ld16(tbase + lanes + S::kTmO + i, o);
-                if (S::kOnes) tmem_ld16(tbase + lanes + S::kTmL + i, l);
-                tmem_ld_wait_regs(o);
-                if (S::kOnes) {
-                    tmem_ld_wait_regs(l);
+                for (int r = 0; r < R; ++r)
+                    l[r] = (bars->top[0][r0 + r] + bars->top[1][r0 + r]) + (bars->top[2][r0 + r] + bars->top[3][r0 + r]);
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (r0 + r >= rows || !sound) break;
+                const int tok = bars->tok_of[r0 + r];
+                if (whole) {
+                    const int head = w.kvh * p.group + r0 + r - tok * p.group;
+                    p.out[(((long long)w.b * p.N + w.rb * tok_block + tok) * p.H + head) * kHeadDim + key] =
+                        __float2bfloat16_rn(l[r] == 0.f ? 0.f : o[r] / l[r]);
                 } else {
-#pragma unroll
-                    for (int x = 0; x < 16; ++x)
-                        l[x] = __float_as_uint((bars->top[0][i + x] + bars->top[1][i + x]) +
-                                               (bars->top[2][i + x] + bars->top[3][i + x]));
-                }
-                if (!sound) continue;
-#pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    const int r = i + x;
-                    if (r >= rows) break;
-                    const float ov = __uint_as_float(o[x]), lv = __uint_as_float(l[x]);
-                    if (whole) {
-                        const long long tok = (long long)w.b * p.N + w.rb * tok_block + bars->tok_of[r];
-                        const int head = w.kvh * p.group + r - bars->tok_of[r] * p.group;
-                        p.out[(tok * p.H + head) * kHeadDim + tid] = __float2bfloat16_rn(lv == 0.f ? 0.f : ov / lv);
-                    } else {
-                        po[r * kHeadDim + tid] = ov;
-                        if (tid == 0)
-                            reinterpret_cast<float2 *>(po + RP * kHeadDim)[r] = make_float2(-bars->neg_m[r], lv);
+                    po[(r0 + r) * kHeadDim + key] = o[r];
+                    if (key == 0) {
+                        const float m = bars->neg_m[r0 + r];
+                        reinterpret_cast<float2 *>(po + RP * kHeadDim)[r0 + r] =
+                            make_float2(m == kUnseen ? -INFINITY : -m, l[r]);
                     }
                 }
             }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->o_free);
         softmax_sync();  // neg_m and the sums are read until here
     }
 }
@@ -627,14 +648,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     Bars<RP> *bars = reinterpret_cast<Bars<RP> *>(sm + S::kOffBars);
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int tok_block = min(p.N, kMaxDrafts / p.group), blocks = (p.N + tok_block - 1) / tok_block;
-    if (warp < 4) {
+    if (warp < kMmaWarp) {
         // rows of Q that no box fills, and the ones
-        for (int i = threadIdx.x; i < (int)(S::kQBufs * S::kQBytes / 16); i += 128)
+        for (int i = threadIdx.x; i < (int)(S::kQBufs * S::kQBytes / 16); i += 256)
             reinterpret_cast<uint4 *>(sm + S::kOffQ)[i] = make_uint4(0, 0, 0, 0);
-        for (int i = threadIdx.x; S::kOnes && i < 256; i += 128)
+        for (int i = threadIdx.x; S::kOnes && i < 256; i += 256)
             reinterpret_cast<uint4 *>(sm + S::kOffOnes)[i] =
                 make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-        for (int r = threadIdx.x; r < RP; r += 128) bars->tok_of[r] = (uint8_t)(r / p.group);
+        for (int r = threadIdx.x; r < RP; r += 256) bars->tok_of[r] = (uint8_t)(r / p.group);
         fence_proxy_async_smem();
     } else if (warp == kMmaWarp) {
         tmem_alloc(&bars->tmem_base, S::kTmCols);
@@ -649,12 +670,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&bars->q_full[i], 1);
                 mbar_init(&bars->q_empty[i], 1);
                 mbar_init(&bars->s_full[i], 1);
-                mbar_init(&bars->p_full[i], 4);
+                mbar_init(&bars->p_full[i], 8);
                 mbar_init(&bars->p_empty[i], 1);
             }
             mbar_init(&bars->pv_done, 1);
             mbar_init(&bars->o_full, 1);
-            mbar_init(&bars->o_free, 4);
+            mbar_init(&bars->o_free, 8);
             mbar_init(&bars->drain, 1);
             fence_mbar_init();
         }
@@ -681,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_trigger();
     const uint32_t tbase = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
     const Waiter wait{p.wait_limit_ns, p.err};
-    if (warp < 4)
+    if (warp < kMmaWarp)
         softmax_role<RP>(p, bars, sm, tbase, warp, lane, blocks, tok_block, wait);
     else if (warp == kMmaWarp)
         mma_role<RP>(p, bars, sm, tbase, lane, blocks, wait);
