@@ -835,7 +835,6 @@ la_status attn_verify(const la_bf16 *q, int64_t q_rs, const la_bf16 *k_pages, co
     st = attn_params(&p, &work, q, q_rs, c, out, B, (long long)B * N, H, Hkv, scale);
     if (st != LA_OK || !work) return st;
     if (tree && (!parents || !aligned4(parents))) return LA_ERR_INVALID;
-    if ((long long)p.B * Hkv * N > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;  // blocks of the second launch, at most
     if (!workspace || !aligned16(workspace) ||
         (unsigned long long)workspace_bytes < la::attn_verify_ws_bytes(N, p.group))
         return LA_ERR_INVALID;

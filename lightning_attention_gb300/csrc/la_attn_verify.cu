@@ -38,6 +38,7 @@ struct Shape {
     static constexpr int kQBufs = RP <= 64 ? 2 : 1, kPBufs = RP <= 32 ? 2 : 1;
     static constexpr int kSlots = RP <= 32 ? 5 : 4;       // tiles of keys and values
     static constexpr int kParts = RP <= 64 ? 2 : 1;       // of P: hi, lo
+    static constexpr int kExtra = RP <= 32 ? 1 : 2;       // tiles' time that an item takes besides its own
     static constexpr bool kOnes = RP > 64;                // sums of P by the tensor cores, not in registers
     static constexpr uint32_t kQBytes = RP * 256, kPart = kKeyTile * RP * 2, kPBytes = kParts * kPart;
     static constexpr uint32_t kOffKV = 0;
@@ -49,8 +50,16 @@ struct Shape {
     static constexpr uint32_t kTmO = 2 * RP, kTmL = 3 * RP, kTmCols = 4 * RP;
 };
 
+// What a CTA's warps have to know of an item, published by the warp that loads the keys; no tiles: the run's end.
+struct Rec {
+    int b, kvh, rb, kv_len, j0, j1, whole;
+};
+constexpr int kItems = 4;  // items ahead
+
 template <int RP>
 struct Bars {
+    uint64_t item_full[kItems], item_empty[kItems];
+    Rec items[kItems];
     uint64_t full[5], empty[5];
     uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], p_empty[2], pv_done, o_full, o_free, drain;
     alignas(16) float neg_m[RP];        // minus the references, in log 2
@@ -58,9 +67,6 @@ struct Bars {
     float top[4][RP];
     uint8_t tok_of[RP];
     uint32_t below[kMaxDrafts][4];      // below[a] bit t: draft t is a or descends from it
-    long long x0, x1;                   // the CTA's run of tiles
-    int b0;                             // its first request
-    long long rem0;                     // its place among that request's tiles
     int loads[2];                       // of keys and of values, at the end
     uint32_t tmem_base;
 };
@@ -72,37 +78,40 @@ __device__ __forceinline__ int tiles_of(const AttnParams &p, int b) {
     return (kv + kKeyTile - 1) / kKeyTile;
 }
 
-// Sum of tiles over all requests, and over those before `upto`: one warp, 256 requests at a time.
-__device__ __forceinline__ long long sum_tiles(const AttnParams &p, int upto, long long *head) {
+// An item is a (request, kv head, block of drafts); its work is its tiles and `extra` more for its beginning and end.
+__device__ __forceinline__ int work_of(int tiles, int extra) { return tiles ? tiles + extra : 0; }
+// The tile at which the first `done` of an item's work end.
+__device__ __forceinline__ int cut(long long done, int tiles, int extra) {
+    const int work = tiles + extra;
+    return done <= 0 ? 0 : done >= work ? tiles : (int)(done * tiles / work);
+}
+
+// Work of an item of every request, summed: one warp, 256 requests at a time.
+__device__ __forceinline__ long long sum_work(const AttnParams &p, int extra) {
     const int lane = threadIdx.x & 31;
-    long long all = 0, before = 0;
+    long long all = 0;
     for (int b0 = 0; b0 < p.B; b0 += 256) {
         int t[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = b0 + i * 32 + lane < p.B ? tiles_of(p, b0 + i * 32 + lane) : 0;
+        for (int i = 0; i < 8; ++i)
+            t[i] = b0 + i * 32 + lane < p.B ? work_of(tiles_of(p, b0 + i * 32 + lane), extra) : 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            all += t[i];
-            if (b0 + i * 32 + lane < upto) before += t[i];
-        }
+        for (int i = 0; i < 8; ++i) all += t[i];
     }
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        all += __shfl_xor_sync(0xffffffffu, all, d);
-        before += __shfl_xor_sync(0xffffffffu, before, d);
-    }
-    if (head) *head = before;
+    for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
     return all;
 }
 
-// The request whose tiles (times `per`: kv heads and blocks of drafts) hold place x, and the place within it.
-__device__ __forceinline__ void find_place(const AttnParams &p, long long x, int per, int &b, long long &rem) {
+// The request whose `per` items hold place x of the work, and the place where those begin; false behind the last.
+__device__ __forceinline__ bool find_request(const AttnParams &p, int extra, long long x, int per, int &b,
+                                             long long &first) {
     const int lane = threadIdx.x & 31;
     long long before = 0;
     b = 0;
-    rem = 0;
+    first = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const long long mine = b0 + lane < p.B ? (long long)tiles_of(p, b0 + lane) * per : 0;
+        const long long mine = b0 + lane < p.B ? (long long)work_of(tiles_of(p, b0 + lane), extra) * per : 0;
         long long upto = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -114,47 +123,59 @@ __device__ __forceinline__ void find_place(const AttnParams &p, long long x, int
         if (hit) {
             const int src = __ffs(hit) - 1;
             b = b0 + src;
-            rem = x - __shfl_sync(0xffffffffu, upto - mine, src);
-            return;
+            first = __shfl_sync(0xffffffffu, upto - mine, src);
+            return true;
         }
         before = __shfl_sync(0xffffffffu, upto, 31);
     }
+    return false;
 }
 
-// The (request, kv head, block of drafts)s of a CTA's run, in order.
+// The items of a CTA's run, those of which it has no tile left out.
 struct Walk {
-    int b, kvh, rb, tiles, j0, j1, kv_len;
-    long long left;
-    int blocks;
-    __device__ __forceinline__ void start(const AttnParams &p, int blocks_, int b_, long long rem, long long n) {
+    int b, kvh, rb, tiles, j0, j1, kv_len, blocks, extra;
+    long long at, lo, hi;  // where the item begins; the run
+    bool live;
+    __device__ __forceinline__ void start(const AttnParams &p, int extra_, int blocks_, int b_, long long first,
+                                          long long lo_, long long hi_) {
+        extra = extra_;
         blocks = blocks_;
         b = b_;
-        left = n;
-        if (n <= 0) return;
+        lo = lo_;
+        hi = hi_;
+        live = lo < hi;
+        if (!live) return;
         tiles = tiles_of(p, b);
         kv_len = p.cache.kv_lens[b];
-        const int item = (int)(rem / tiles);
+        const int item = (int)((lo - first) / work_of(tiles, extra));
         kvh = item / blocks;
         rb = item - kvh * blocks;
-        j0 = (int)(rem - (long long)item * tiles);
-        j1 = (int)min((long long)tiles, j0 + left);
+        at = first + (long long)item * work_of(tiles, extra);
+        settle(p);
     }
-    __device__ __forceinline__ bool done() const { return left <= 0; }
-    __device__ __forceinline__ void next(const AttnParams &p) {
-        left -= j1 - j0;
-        if (left <= 0) return;
-        if (++rb == blocks) {
-            rb = 0;
-            if (++kvh == p.Hkv) {
-                kvh = 0;
-                do {
-                    tiles = tiles_of(p, ++b);  // left > 0: a request with keys follows
-                } while (tiles == 0);
-                kv_len = p.cache.kv_lens[b];
-            }
+    __device__ __forceinline__ void advance(const AttnParams &p) {
+        at += work_of(tiles, extra);
+        live = at < hi;
+        if (!live || ++rb < blocks) return;
+        rb = 0;
+        if (++kvh < p.Hkv) return;
+        kvh = 0;
+        do {
+            tiles = tiles_of(p, ++b);  // at < hi: a request with keys follows
+        } while (tiles == 0);
+        kv_len = p.cache.kv_lens[b];
+    }
+    __device__ __forceinline__ void settle(const AttnParams &p) {
+        while (live) {
+            j0 = cut(lo - at, tiles, extra);
+            j1 = cut(hi - at, tiles, extra);
+            if (j0 < j1) return;
+            advance(p);
         }
-        j0 = 0;
-        j1 = (int)min((long long)tiles, left);
+    }
+    __device__ __forceinline__ void next(const AttnParams &p) {
+        advance(p);
+        settle(p);
     }
 };
 
@@ -209,7 +230,7 @@ __device__ bool build_tree(const AttnParams &p, Bars<RP> *bars, int b, int tid) 
 // n (8 or a multiple of 16) columns of tensor memory.
 template <int n>
 __device__ __forceinline__ void tmem_get(uint32_t at, float (&x)[n]) {
-    if (n == 8) {
+    if constexpr (n == 8) {
         uint32_t r[8];
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
                      "tcgen05.wait::ld.sync.aligned;"
@@ -217,16 +238,16 @@ __device__ __forceinline__ void tmem_get(uint32_t at, float (&x)[n]) {
                      : "r"(at)
                      : "memory");
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i % n] = __uint_as_float(r[i]);
-        return;
-    }
+        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r[i]);
+    } else {
 #pragma unroll
-    for (int i = 0; i < n / 16 * 16; i += 16) {
-        uint32_t r[16];
-        tmem_ld16(at + i, r);
-        tmem_ld_wait_regs(r);
+        for (int i = 0; i < n; i += 16) {
+            uint32_t r[16];
+            tmem_ld16(at + i, r);
+            tmem_ld_wait_regs(r);
 #pragma unroll
-        for (int y = 0; y < 16; ++y) x[(i + y) % n] = __uint_as_float(r[y]);
+            for (int y = 0; y < 16; ++y) x[i + y] = __uint_as_float(r[y]);
+        }
     }
 }
 template <int n>
@@ -244,7 +265,7 @@ __device__ __forceinline__ void tmem_put(uint32_t at, const float (&x)[n]) {
 // Two threads a key: warps 0-3 have the first half of the rows, warps 4-7 the other.
 template <int RP>
 __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint32_t tbase, int warp, int lane,
-                             int blocks, int tok_block, const Waiter &wait) {
+                             int tok_block, const Waiter &wait) {
     using S = Shape<RP>;
     constexpr int R = RP / 2;  // rows of a thread
     const int tid = warp * 32 + lane, key = tid & 127, half = warp >> 2;
@@ -261,12 +282,15 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
             atomicOr(p.err, ERR_BIT_PAGE);
         }
     }
-    Walk w;
-    w.start(p, blocks, bars->b0, bars->rem0, bars->x1 - bars->x0);
-    int tile = 0, item = 0, tree_of = -1;
+    int tile = 0, tree_of = -1;
     bool ok = true, sound = true;
     float sum[S::kOnes ? 1 : R];  // of this thread's key
-    for (; !w.done(); w.next(p), ++item) {
+    for (int item = 0;; ++item) {
+        ok = ok && __all_sync(0xffffffffu, wait(&bars->item_full[item % kItems], (uint32_t)(item / kItems) & 1));
+        const Rec w = bars->items[item % kItems];
+        if (softmax_any(!ok) || w.j1 <= w.j0) return;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->item_empty[item % kItems]);
         if (!S::kOnes) {
 #pragma unroll
             for (int r = 0; r < R; ++r) sum[S::kOnes ? 0 : r] = 0.f;
@@ -420,7 +444,6 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
         ok = __all_sync(0xffffffffu, wait(&bars->o_full, (uint32_t)item & 1));
         tc_fence_after();
         const int toks = min(tok_block, p.N - w.rb * tok_block), rows = toks * p.group;
-        const bool whole = w.j0 == 0 && w.j1 == w.tiles;
         const long long piece = 2ll * blockIdx.x + (w.j0 == 0 ? 1 : 0);
         float *po = static_cast<float *>(p.ws) + piece * RP * (kHeadDim + 2);
         if (ok) {
@@ -439,7 +462,7 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
             for (int r = 0; r < R; ++r) {
                 if (r0 + r >= rows || !sound) break;
                 const int tok = bars->tok_of[r0 + r];
-                if (whole) {
+                if (w.whole) {
                     const int head = w.kvh * p.group + r0 + r - tok * p.group;
                     p.out[(((long long)w.b * p.N + w.rb * tok_block + tok) * p.H + head) * kHeadDim + key] =
                         __float2bfloat16_rn(l[r] == 0.f ? 0.f : o[r] / l[r]);
@@ -461,7 +484,7 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
 // slots counted instead of divided), so that the uniform datapath forms the operands: otherwise an issue takes 100
 // cycles, several times the MMA (128 requests of 500-8000 positions, 32 heads on 4: 304 us).
 template <int RP>
-__device__ void mma_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint32_t tbase, int lane, int blocks,
+__device__ void mma_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint32_t tbase, int lane,
                          const Waiter &wait) {
     using S = Shape<RP>;
     const uint32_t id_s = idesc_bf16_f32(128, RP, false, false);
@@ -508,33 +531,34 @@ __device__ void mma_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint3
             }
         }
     };
-    Walk w;
-    w.start(p, blocks, bars->b0, bars->rem0, bars->x1 - bars->x0);
-    int item = 0;
-    bool live = __shfl_sync(0xffffffffu, (int)!w.done(), 0) != 0;
-    if (live) scores(true, __shfl_sync(0xffffffffu, (int)(w.j1 - w.j0 == 1), 0) != 0);
-    while (live && ok) {
-        const int j0 = __shfl_sync(0xffffffffu, w.j0, 0), j1 = __shfl_sync(0xffffffffu, w.j1, 0);
-        const int kv_len = __shfl_sync(0xffffffffu, w.kv_len, 0);
-        const int end = kv_len % p.cache.page_size, last = (kv_len - 1) / kKeyTile;
-        w.next(p);
+    int j0 = 0, j1 = 0, kv_len = 0;
+    auto read_item = [&](int x) {  // j1 = j0: there is none
+        ok = ok && __all_sync(0xffffffffu, wait(&bars->item_full[x % kItems], (uint32_t)(x / kItems) & 1));
+        const Rec &it = bars->items[x % kItems];
+        j0 = __shfl_sync(0xffffffffu, it.j0, 0);
+        j1 = ok ? __shfl_sync(0xffffffffu, it.j1, 0) : j0;
+        kv_len = __shfl_sync(0xffffffffu, it.kv_len, 0);
         __syncwarp();
-        const bool follows = __shfl_sync(0xffffffffu, (int)!w.done(), 0) != 0;
-        const bool one = __shfl_sync(0xffffffffu, (int)(w.j1 - w.j0 == 1), 0) != 0;
-        for (int j = j0; j < j1 && ok; ++j) {
+        if (j0 < j1 && lane == 0) mbar_arrive(&bars->item_empty[x % kItems]);
+    };
+    int item = 0;
+    read_item(0);
+    if (j0 < j1) scores(true, j1 - j0 == 1);
+    while (j0 < j1 && ok) {
+        const int from = j0, to = j1;
+        const int end = kv_len % p.cache.page_size, last = (kv_len - 1) / kKeyTile;
+        const int r0 = kv_len - last * kKeyTile, r1 = r0 - end + p.cache.page_size;
+        for (int j = from; j < to && ok; ++j) {
             const int sv = slot;  // this tile's values, then the next tile's keys
             const uint32_t sv_par = slot_par;
             next_slot();
             // the next tile's scores run under this one's softmax; its S was read before the P before was full
-            const bool more = j + 1 < j1;
-            if (more)
-                scores(false, j + 2 == j1);
-            else if (follows)
-                scores(true, one);
+            const bool more = j + 1 < to;
+            if (!more) read_item(item + 1);
+            if (more || j0 < j1) scores(!more, more ? j + 2 == to : j1 - j0 == 1);
             ok = ok && __all_sync(0xffffffffu, wait(&bars->full[sv], sv_par));
             if (!ok) break;
             if (end != 0 && j == last) {  // rows of the last page behind the request's positions: zeros
-                const int r0 = kv_len - j * kKeyTile, r1 = r0 - end + p.cache.page_size;
                 uint8_t *v = sm + S::kOffKV + sv * kTileBytes;
                 for (int r = r0 + (lane >> 4); r < r1; r += 2)
                     *reinterpret_cast<uint4 *>(v + ((lane >> 3) & 1) * kHalfBytes + r * 128 + (lane & 7) * 16) =
@@ -543,7 +567,7 @@ __device__ void mma_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint3
                 __syncwarp();
             }
             ok = __all_sync(0xffffffffu, wait(&bars->p_full[pb], p_par));
-            if (ok && j == j0 && item > 0)  // the last item's sums have been read
+            if (ok && j == from && item > 0)  // the last item's sums have been read
                 ok = __all_sync(0xffffffffu, wait(&bars->o_free, (uint32_t)(item - 1) & 1));
             if (!ok) break;
             tc_fence_after();
@@ -555,9 +579,9 @@ __device__ void mma_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint3
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         const uint32_t bk = b + x * (S::kPart >> 4) + k * 32;
-                        mma_bf16(tbase + S::kTmO, high | (a + k * 128), high32 | bk, id_o, j > j0 || x + k > 0);
+                        mma_bf16(tbase + S::kTmO, high | (a + k * 128), high32 | bk, id_o, j > from || x + k > 0);
                         if (S::kOnes)
-                            mma_bf16(tbase + S::kTmL, high32 | ones, high32 | bk, id_l, j > j0 || x + k > 0);
+                            mma_bf16(tbase + S::kTmL, high32 | ones, high32 | bk, id_l, j > from || x + k > 0);
                     }
                 mma_commit(&bars->empty[sv]);
                 mma_commit(&bars->p_empty[pb]);
@@ -571,58 +595,108 @@ __device__ void mma_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint3
             }
         }
         ++item;
-        live = follows;
     }
     __syncwarp();
     if (elect()) mma_commit(&bars->drain);
     wait(&bars->drain, 0);
 }
 
-// The tiles that a loading warp fills, every other one of the ring: keys (kv 0, with the queries) and values (1).
+// The tiles that a loading warp fills, every other one of the ring: keys (kv 0) and values (1).
 template <int RP>
-__device__ void load_role(const AttnParams &p, int kv, const CUtensorMap *tq, const CUtensorMap *map, Bars<RP> *bars,
+struct Ring {
+    using S = Shape<RP>;
+    int slot, count = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ Ring(int kv) : slot(kv) {}
+    __device__ __forceinline__ bool load(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, const CUtensorMap *map,
+                                         int page, int head, const Waiter &wait) {
+        // a slot's first phase is filled at once: the wait for the one before it returns
+        if (!__all_sync(0xffffffffu, wait(&bars->empty[slot], phase ^ 1))) return false;
+        load_tile(map, sm + S::kOffKV + slot * kTileBytes, &bars->full[slot], page, p.cache.page_size, head);
+        ++count;
+        slot += 2;
+        if (slot >= S::kSlots) {
+            slot -= S::kSlots;
+            phase ^= 1;
+        }
+        return true;
+    }
+};
+
+template <int RP>
+__device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUtensorMap *tk, Bars<RP> *bars,
                           uint8_t *sm, int lane, int blocks, int tok_block, const Waiter &wait) {
     using S = Shape<RP>;
-    Walk w;
-    w.start(p, blocks, bars->b0, bars->rem0, bars->x1 - bars->x0);
+    const int per = p.Hkv * blocks;
+    const long long all = sum_work(p, S::kExtra) * per;
+    const long long runs = max(1ll, min((long long)gridDim.x, all)), c = min((long long)blockIdx.x, runs);
+    const long long lo = all * c / runs, hi = c < runs ? all * (c + 1) / runs : lo;
+    int b = 0;
+    long long first = 0;
+    if (lo < hi) find_request(p, S::kExtra, lo, per, b, first);
     const uint32_t box = (uint32_t)(tok_block * p.group) * 128;
-    int slot = kv, count = 0, item = 0, asked = 0;
-    uint32_t phase = 0;
+    int item = 0, asked = 0;
+    Ring<RP> ring(0);
     bool ok = true;
-    for (; !w.done() && ok; w.next(p), ++item) {
+    auto publish = [&](const Rec &r) {
+        if (item >= kItems)
+            ok = ok && __all_sync(0xffffffffu, wait(&bars->item_empty[item % kItems], (uint32_t)(item / kItems - 1) & 1));
+        if (ok && lane == 0) {
+            bars->items[item % kItems] = r;
+            mbar_arrive(&bars->item_full[item % kItems]);
+        }
+        __syncwarp();
+    };
+    Walk w;
+    for (w.start(p, S::kExtra, blocks, b, first, lo, hi); w.live && ok; w.next(p), ++item) {
         Pages pages;
         pages.fetch(p.cache, w.b, w.kv_len, w.j0, lane);
-        if (kv == 0) {
-            const int qb = item % S::kQBufs;
-            // a buffer's first phase is filled at once: the wait for the one before it returns
-            if (!(ok = __all_sync(0xffffffffu, wait(&bars->q_empty[qb], (uint32_t)(item / S::kQBufs + 1) & 1)))) break;
-            if (elect()) {
-                mbar_arrive_expect_tx(&bars->q_full[qb], 2 * box);
+        publish({w.b, w.kvh, w.rb, w.kv_len, w.j0, w.j1, w.j0 == 0 && w.j1 == w.tiles});
+        const int qb = item % S::kQBufs;
+        // a buffer's first phase is filled at once: the wait for the one before it returns
+        if (!(ok = ok && __all_sync(0xffffffffu, wait(&bars->q_empty[qb], (uint32_t)(item / S::kQBufs + 1) & 1)))) break;
+        if (elect()) {
+            mbar_arrive_expect_tx(&bars->q_full[qb], 2 * box);
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    tma_load_4d(sm + S::kOffQ + qb * S::kQBytes + x * (S::kQBytes / 2), tq, &bars->q_full[qb], 0,
-                                w.kvh * p.group, w.b * p.N + w.rb * tok_block, x);
-            }
-            __syncwarp();
-            asked = item + 1;
+            for (int x = 0; x < 2; ++x)
+                tma_load_4d(sm + S::kOffQ + qb * S::kQBytes + x * (S::kQBytes / 2), tq, &bars->q_full[qb], 0,
+                            w.kvh * p.group, w.b * p.N + w.rb * tok_block, x);
         }
-        for (int j = w.j0; j < w.j1; ++j) {
+        __syncwarp();
+        asked = item + 1;
+        for (int j = w.j0; j < w.j1 && ok; ++j) {
             const int page = pages.check(p.cache, p.err);
             if (j + 1 < w.j1) pages.fetch(p.cache, w.b, w.kv_len, j + 1, lane);
-            if (!(ok = __all_sync(0xffffffffu, wait(&bars->empty[slot], phase ^ 1)))) break;
-            load_tile(map, sm + S::kOffKV + slot * kTileBytes, &bars->full[slot], page, p.cache.page_size, w.kvh);
-            ++count;
-            slot += 2;
-            if (slot >= S::kSlots) {
-                slot -= S::kSlots;
-                phase ^= 1;
-            }
+            ok = ring.load(p, bars, sm, tk, page, w.kvh, wait);
         }
     }
+    publish({});
     // no copy may be in flight when the CTA exits
     for (int x = asked > S::kQBufs ? asked - S::kQBufs : 0; x < asked; ++x)
         wait(&bars->q_full[x % S::kQBufs], (uint32_t)(x / S::kQBufs) & 1);
-    if (lane == 0) bars->loads[kv] = count;
+    if (lane == 0) bars->loads[0] = ring.count;
+}
+
+template <int RP>
+__device__ void value_role(const AttnParams &p, const CUtensorMap *tv, Bars<RP> *bars, uint8_t *sm, int lane,
+                           const Waiter &wait) {
+    Ring<RP> ring(1);
+    bool ok = true;
+    for (int item = 0; ok; ++item) {
+        if (!__all_sync(0xffffffffu, wait(&bars->item_full[item % kItems], (uint32_t)(item / kItems) & 1))) break;
+        const Rec it = bars->items[item % kItems];
+        if (it.j1 <= it.j0) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->item_empty[item % kItems]);
+        Pages pages;
+        pages.fetch(p.cache, it.b, it.kv_len, it.j0, lane);
+        for (int j = it.j0; j < it.j1 && ok; ++j) {
+            const int page = pages.check(p.cache, p.err);
+            if (j + 1 < it.j1) pages.fetch(p.cache, it.b, it.kv_len, j + 1, lane);
+            ok = ring.load(p, bars, sm, tv, page, it.kvh, wait);
+        }
+    }
+    if (lane == 0) bars->loads[1] = ring.count;
 }
 
 // The last load into every slot, of those that the two warps made.
@@ -673,29 +747,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&bars->p_full[i], 8);
                 mbar_init(&bars->p_empty[i], 1);
             }
+            for (int i = 0; i < kItems; ++i) {
+                mbar_init(&bars->item_full[i], 1);
+                mbar_init(&bars->item_empty[i], kMmaWarp + 2);
+            }
             mbar_init(&bars->pv_done, 1);
             mbar_init(&bars->o_full, 1);
             mbar_init(&bars->o_free, 8);
             mbar_init(&bars->drain, 1);
             fence_mbar_init();
         }
-        __syncwarp();
-        pdl_wait();
-        const int per = p.Hkv * blocks;
-        const long long all = sum_tiles(p, 0, nullptr) * per;
-        const long long runs = min((long long)gridDim.x, all), c = min((long long)blockIdx.x, runs);
-        const long long x0 = runs ? all * c / runs : 0, x1 = runs && c < runs ? all * (c + 1) / runs : x0;
-        int b = 0;
-        long long rem = 0;
-        if (x1 > x0) find_place(p, x0, per, b, rem);
-        if (lane == 0) {
-            bars->x0 = x0;
-            bars->x1 = x1;
-            bars->b0 = b;
-            bars->rem0 = rem;
-        }
     }
-    if (warp != kLoadWarp) pdl_wait();
+    pdl_wait();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -703,53 +766,80 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tbase = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
     const Waiter wait{p.wait_limit_ns, p.err};
     if (warp < kMmaWarp)
-        softmax_role<RP>(p, bars, sm, tbase, warp, lane, blocks, tok_block, wait);
+        softmax_role<RP>(p, bars, sm, tbase, warp, lane, tok_block, wait);
     else if (warp == kMmaWarp)
-        mma_role<RP>(p, bars, sm, tbase, lane, blocks, wait);
-    else
-        load_role<RP>(p, warp == kValueWarp, &tq, warp == kValueWarp ? &tv : &tk, bars, sm, lane, blocks, tok_block, wait);
+        mma_role<RP>(p, bars, sm, tbase, lane, wait);
+    else if (warp == kLoadWarp)
+        load_role<RP>(p, &tq, &tk, bars, sm, lane, blocks, tok_block, wait);
+    else if (warp == kValueWarp)
+        value_role<RP>(p, &tv, bars, sm, lane, wait);
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) tmem_dealloc(tbase, S::kTmCols);
     if (warp == kLoadWarp) drain_ring<RP>(bars, wait);
 }
 
-// The (request, kv head, block of drafts)s that several CTAs shared.  grid: one block of 4 warps per such
-// triple, a warp per row; rp: the padded rows of a partial result; ctas: the grid that left them.
-__global__ void __launch_bounds__(128) attn_verify_join_kernel(const AttnParams p, int rp, int ctas) {
+// The items that several CTAs shared.  Block x looks at the end of CTA x's run: the first such end inside an item joins
+// it, a warp per row, in the CTAs' order.  rp: the padded rows of a partial result; ctas: the grid that left them.
+__global__ void __launch_bounds__(256) attn_verify_join_kernel(const AttnParams p, int rp, int extra, int ctas) {
+    __shared__ long long s_at, s_all;
+    __shared__ int s_b, s_item, s_tiles;
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tok_block = min(p.N, kMaxDrafts / p.group), blocks = (p.N + tok_block - 1) / tok_block;
     const int per = p.Hkv * blocks;
-    const int b = blockIdx.x / per, item = blockIdx.x - b * per;
-    const int tiles = tiles_of(p, b);
-    if (tiles == 0) return;
-    long long before;
-    const long long all = sum_tiles(p, b, &before) * per;
-    const long long x0 = before * per + (long long)item * tiles, x1 = x0 + tiles - 1;
-    const long long runs = min((long long)ctas, all);
-    const int c0 = (int)(((x0 + 1) * runs - 1) / all), c1 = (int)(((x1 + 1) * runs - 1) / all);
-    if (c0 == c1) return;
-    if (p.parents) {  // a request with a parent out of range is left as it was
-        bool bad = false;
-        for (int t = lane; t < p.N; t += 32) {
-            const int up = p.parents[(long long)b * p.N + t];
-            bad |= up < -1 || up >= t;
+    if (warp == 0) {
+        const long long all = sum_work(p, extra) * per, runs = min((long long)ctas, all);
+        int b = 0, tiles = 0, item = 0;
+        long long at = 0, first;
+        if (blockIdx.x + 1 < runs) {
+            const long long x = all * (blockIdx.x + 1) / runs;
+            find_request(p, extra, x, per, b, first);
+            tiles = tiles_of(p, b);
+            item = (int)((x - first) / work_of(tiles, extra));
+            at = first + (long long)item * work_of(tiles, extra);
+            // an end at its beginning cut nothing; an earlier one inside it joins it
+            if (x == at || all * blockIdx.x / runs > at) tiles = 0;
         }
-        if (__any_sync(0xffffffffu, bad)) return;
+        if (tiles > 0 && p.parents) {  // a request with a parent out of range is left as it was
+            bool bad = false;
+            for (int t = lane; t < p.N; t += 32) {
+                const int up = p.parents[(long long)b * p.N + t];
+                bad |= up < -1 || up >= t;
+            }
+            if (__any_sync(0xffffffffu, bad)) tiles = 0;
+        }
+        if (lane == 0) {
+            s_at = at;
+            s_all = all;
+            s_b = b;
+            s_item = item;
+            s_tiles = tiles;
+        }
     }
-    const int kvh = item / blocks, rb = item - kvh * blocks;
+    __syncthreads();
+    const int tiles = s_tiles;
+    if (tiles == 0) return;
+    const long long at = s_at, all = s_all, runs = min((long long)ctas, all), work = work_of(tiles, extra);
+    const int b = s_b, kvh = s_item / blocks, rb = s_item - kvh * blocks;
     const int rows = min(tok_block, p.N - rb * tok_block) * p.group;
     const long long stride = (long long)rp * (kHeadDim + 2);
     const float *ws = static_cast<const float *>(p.ws);
-    for (int r = warp; r < rows; r += 4) {
+    for (int r = blockIdx.y * 8 + warp; r < rows; r += gridDim.y * 8) {
         float m = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = c0; c <= c1; ++c) {
-            const float *at = ws + (2ll * c + (c == c0)) * stride;
-            const float2 ml = reinterpret_cast<const float2 *>(at + rp * kHeadDim)[r];
-            const float4 x = reinterpret_cast<const float4 *>(at + r * kHeadDim)[lane];
+        bool whole = false;
+        for (int c = blockIdx.x; c < runs; ++c) {
+            const long long lo = all * c / runs, hi = all * (c + 1) / runs;
+            if (lo >= at + work) break;
+            const int j0 = cut(lo - at, tiles, extra), j1 = cut(hi - at, tiles, extra);
+            if (j0 == j1) continue;
+            whole = j0 == 0 && j1 == tiles;  // one CTA had all of it, and has written it
+            if (whole) break;
+            const float *piece = ws + (2ll * c + (j0 == 0)) * stride;
+            const float2 ml = reinterpret_cast<const float2 *>(piece + rp * kHeadDim)[r];
+            const float4 x = reinterpret_cast<const float4 *>(piece + r * kHeadDim)[lane];
             if (ml.x == -INFINITY) continue;  // none of its keys is seen by the row
             const float top = fmaxf(m, ml.x), f = ex2z(m - top), g = ex2z(ml.x - top);
             m = top;
@@ -759,6 +849,7 @@ __global__ void __launch_bounds__(128) attn_verify_join_kernel(const AttnParams 
             o.z = o.z * f + x.z * g;
             o.w = o.w * f + x.w * g;
         }
+        if (whole) return;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int tok = r / p.group, head = kvh * p.group + r - tok * p.group;
         const uint2 w = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
@@ -768,7 +859,8 @@ __global__ void __launch_bounds__(128) attn_verify_join_kernel(const AttnParams 
 
 template <int RP>
 cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const AttnParams &p,
-                   int ctas, cudaStream_t stream) {
+                   int ctas, int *extra, cudaStream_t stream) {
+    *extra = Shape<RP>::kExtra;
     constexpr uint32_t smem = Shape<RP>::kOffBars + sizeof(Bars<RP>) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory");
     int dev = 0;
@@ -800,22 +892,22 @@ unsigned long long attn_verify_ws_bytes(int N, int group) {
 }
 
 cudaError_t launch_attn_verify(const AttnParams &p, cudaStream_t stream) {
-    const int tok_block = std::min(p.N, kMaxDrafts / p.group), blocks = (p.N + tok_block - 1) / tok_block;
     CUtensorMap tq, tk, tv;
-    if (!make_query_map(&tq, p.q, (long long)p.B * p.N, p.H, p.q_rs, p.group, tok_block) ||
+    if (!make_query_map(&tq, p.q, (long long)p.B * p.N, p.H, p.q_rs, p.group, std::min(p.N, kMaxDrafts / p.group)) ||
         !make_pages_map(&tk, p.cache.k, p.cache, p.Hkv) || !make_pages_map(&tv, p.cache.v, p.cache, p.Hkv))
         return cudaErrorInvalidValue;
     const int rp = padded_rows(p.N, p.group);
     cudaError_t e;
+    int extra;
     switch (rp) {
-        case 16: e = launch<16>(tq, tk, tv, p, kAttnCtas, stream); break;
-        case 32: e = launch<32>(tq, tk, tv, p, kAttnCtas, stream); break;
-        case 64: e = launch<64>(tq, tk, tv, p, kAttnCtas, stream); break;
-        default: e = launch<128>(tq, tk, tv, p, kAttnCtas, stream); break;
+        case 16: e = launch<16>(tq, tk, tv, p, kAttnCtas, &extra, stream); break;
+        case 32: e = launch<32>(tq, tk, tv, p, kAttnCtas, &extra, stream); break;
+        case 64: e = launch<64>(tq, tk, tv, p, kAttnCtas, &extra, stream); break;
+        default: e = launch<128>(tq, tk, tv, p, kAttnCtas, &extra, stream); break;
     }
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_verify_join_kernel, dim3((unsigned)((long long)p.B * p.Hkv * blocks)), dim3(128), 0, stream,
-                      p, rp, kAttnCtas);
+    return launch_pdl(attn_verify_join_kernel, dim3(kAttnCtas - 1, (unsigned)((rp + 31) / 32)), dim3(256), 0, stream, p, rp,
+                      extra, kAttnCtas);
 }
 
 }  // namespace la
