@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -745,6 +746,9 @@ def _need_pages(k_pages, v_pages, dev):
     if D != _HEAD_DIM or E < 1 or Hkv < 1 or P < 1:
         raise ValueError(f"k_pages must have shape [pages, Hkv, P, {_HEAD_DIM}], got {tuple(k_pages.shape)}")
     page = Hkv * P * D
+    if _fits(k_pages, torch.bfloat16, dev.index, (E, Hkv, P, D)) and _fits(v_pages, torch.bfloat16, dev.index,
+                                                                           (E, Hkv, P, D)):
+        return E, Hkv, P, page
     stride = page if E == 1 else k_pages.stride(0)
     for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
         if not isinstance(t, torch.Tensor):
@@ -838,6 +842,7 @@ def _attn_args(q, k_pages, v_pages, page_table, kv_lens, out, scale):
     return dev, T, H, Hkv, B, q_rs, cache, out, _HEAD_DIM ** -0.5 if scale is None else scale
 
 
+@functools.lru_cache(maxsize=1024)
 def attn_extend_workspace_size(B: int, T: int, H: int, Hkv: int, D: int, max_seqlen: int, max_kvlen: int) -> int:
     """Bytes of scratch la_attn_extend uses for a batch of this shape: 0 where its rows fill the GPU."""
     n = ctypes.c_size_t(0)
@@ -873,6 +878,7 @@ def attn_extend(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, out=None, 
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def attn_verify_workspace_size(N: int, H: int, Hkv: int, D: int) -> int:
     """Bytes of scratch la_attn_decode (N = 1) and la_attn_verify_tree need, whatever the batch."""
     n = ctypes.c_size_t(0)

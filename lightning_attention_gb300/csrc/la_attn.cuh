@@ -102,6 +102,71 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
+// A row's partial results joined: o = sum_c 2^{m_c - m} O_c / sum_c 2^{m_c - m} l_c over CTAs c = first .. ctas - 1, a lane
+// per CTA and step, four of their rows in flight; lane l gets columns 4 l .. 4 l + 3.  piece(c, at): whether CTA c has
+// left a result, and where its O row is (m and l follow `to_ml` floats behind it); `behind(c)`: its run and all later ones
+// lie behind the item.  False if no CTA has left any: one had the whole item, and has written it.
+template <class Piece, class Behind>
+__device__ __forceinline__ bool join_row(int first, int ctas, long long to_ml, int lane, uint2 &out, Piece piece,
+                                         Behind behind) {
+    bool any = false;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c0 = first; c0 < ctas; c0 += 32) {
+        const int c = c0 + lane;
+        const bool past = c >= ctas || behind(c);
+        const float *at = nullptr;
+        float2 ml = make_float2(-INFINITY, 0.f);
+        const bool mine = !past && piece(c, at);
+        if (mine) ml = *reinterpret_cast<const float2 *>(at + to_ml);
+        any |= __any_sync(0xffffffffu, mine);
+        float top = ml.x;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        top = fmaxf(top, m);
+        // a piece whose keys the row does not see, and a lane without one, has m = -inf and counts for nothing
+        const float w = ml.x == -INFINITY ? 0.f : ex2z(ml.x - top), f = m == -INFINITY ? 0.f : ex2z(m - top);
+        float add = w * ml.y;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) add += __shfl_xor_sync(0xffffffffu, add, d);
+        m = top;
+        l = l * f + add;
+        o.x *= f;
+        o.y *= f;
+        o.z *= f;
+        o.w *= f;
+        unsigned left = __ballot_sync(0xffffffffu, w > 0.f);
+        while (left) {
+            float4 x[4];
+            float g[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int src = left ? __ffs(left) - 1 : 0;
+                g[k] = __shfl_sync(0xffffffffu, w, src);
+                const float *row = reinterpret_cast<const float *>(
+                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(at), src));
+                x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (left)
+                    x[k] = reinterpret_cast<const float4 *>(row)[lane];
+                else
+                    g[k] = 0.f;
+                left &= left - 1;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                o.x += g[k] * x[k].x;
+                o.y += g[k] * x[k].y;
+                o.z += g[k] * x[k].z;
+                o.w += g[k] * x[k].w;
+            }
+        }
+        if (__any_sync(0xffffffffu, past)) break;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    out = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    return any;
+}
+
 }  // namespace attn
 
 // TMA maps (host): pages of a cache, boxes of 64 columns x page_size rows; rows of q, boxes of 64 columns

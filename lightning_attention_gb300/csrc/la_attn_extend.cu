@@ -768,30 +768,15 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p, int 
         const int row = r % kRowTile;
         const int tok = it.tok0 + (r / kRowTile) * row_tok + row / p.group;
         if (row >= row_tok * p.group || tok >= it.r.n) continue;
-        float m = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = blockIdx.x; c < ctas; ++c) {
-            const long long lo = work * c / ctas, hi = work * (c + 1) / ctas;
-            if (lo >= it.at + it.size) break;
-            const int j0 = it.cut(lo), j1 = it.cut(hi);
-            if (j0 == j1) continue;
-            if (j0 == 0 && j1 == it.tiles) break;  // one CTA had all of it, and has written it
-            const float *at = ws + ((2ll * c + (j0 == 0)) * kItemRows + r) * kRowFloats;
-            const float2 ml = *reinterpret_cast<const float2 *>(at + kHeadDim);
-            const float4 x = reinterpret_cast<const float4 *>(at)[lane];
-            if (ml.x == -INFINITY) continue;  // none of its keys is seen by the row
-            const float top = fmaxf(m, ml.x), f = ex2z(m - top), g = ex2z(ml.x - top);
-            m = top;
-            l = l * f + ml.y * g;
-            o.x = o.x * f + x.x * g;
-            o.y = o.y * f + x.y * g;
-            o.z = o.z * f + x.z * g;
-            o.w = o.w * f + x.w * g;
-        }
-        if (l == 0.f) continue;
-        const float inv = 1.f / l;
+        auto behind = [&](int c) { return work * c / ctas >= it.at + it.size; };
+        auto piece = [&](int c, const float *&at) {
+            const int j0 = it.cut(work * c / ctas), j1 = it.cut(work * (c + 1) / ctas);
+            at = ws + ((2ll * c + (j0 == 0)) * kItemRows + r) * kRowFloats;
+            return j0 < j1 && j1 - j0 < it.tiles;
+        };
+        uint2 w;
+        if (!join_row(blockIdx.x, ctas, kHeadDim, lane, w, piece, behind)) return;
         const int h = it.kvh * p.group + row % p.group;
-        const uint2 w = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
         reinterpret_cast<uint2 *>(p.out + ((long long)(it.r.t0 + tok) * p.H + h) * kHeadDim)[lane] = w;
     }
 }

@@ -827,32 +827,15 @@ __global__ void __launch_bounds__(256) attn_verify_join_kernel(const AttnParams 
     const long long stride = (long long)rp * (kHeadDim + 2);
     const float *ws = static_cast<const float *>(p.ws);
     for (int r = blockIdx.y * 8 + warp; r < rows; r += gridDim.y * 8) {
-        float m = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        bool whole = false;
-        for (int c = blockIdx.x; c < runs; ++c) {
-            const long long lo = all * c / runs, hi = all * (c + 1) / runs;
-            if (lo >= at + work) break;
-            const int j0 = cut(lo - at, tiles, extra), j1 = cut(hi - at, tiles, extra);
-            if (j0 == j1) continue;
-            whole = j0 == 0 && j1 == tiles;  // one CTA had all of it, and has written it
-            if (whole) break;
-            const float *piece = ws + (2ll * c + (j0 == 0)) * stride;
-            const float2 ml = reinterpret_cast<const float2 *>(piece + rp * kHeadDim)[r];
-            const float4 x = reinterpret_cast<const float4 *>(piece + r * kHeadDim)[lane];
-            if (ml.x == -INFINITY) continue;  // none of its keys is seen by the row
-            const float top = fmaxf(m, ml.x), f = ex2z(m - top), g = ex2z(ml.x - top);
-            m = top;
-            l = l * f + ml.y * g;
-            o.x = o.x * f + x.x * g;
-            o.y = o.y * f + x.y * g;
-            o.z = o.z * f + x.z * g;
-            o.w = o.w * f + x.w * g;
-        }
-        if (whole) return;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        auto behind = [&](int c) { return all * c / runs >= at + work; };
+        auto piece = [&](int c, const float *&row) {
+            const int j0 = cut(all * c / runs - at, tiles, extra), j1 = cut(all * (c + 1) / runs - at, tiles, extra);
+            row = ws + (2ll * c + (j0 == 0)) * stride + r * kHeadDim;
+            return j0 < j1 && j1 - j0 < tiles;
+        };
+        uint2 w;
+        if (!join_row(blockIdx.x, (int)runs, (long long)rp * kHeadDim - r * (kHeadDim - 2), lane, w, piece, behind)) return;
         const int tok = r / p.group, head = kvh * p.group + r - tok * p.group;
-        const uint2 w = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
         reinterpret_cast<uint2 *>(p.out + (((long long)b * p.N + rb * tok_block + tok) * p.H + head) * kHeadDim)[lane] = w;
     }
 }
