@@ -47,6 +47,8 @@ constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffKV = kOffQ + 2 * kTileBytes;
 constexpr uint32_t kOffBars = kOffKV + kSlots * kTileBytes;
 
+constexpr int kRowFloats = kHeadDim + 4;  // of a partial result: O, m, l
+
 // What a CTA's warps have to know of an item.
 struct Rec {
     int b, t0, n, kv_len, kvh, tok0;  // request, its first row, tokens, positions; kv head; first token
@@ -191,14 +193,16 @@ struct Item {
 // The items of a CTA's run, those of which it has no tile left out.
 struct Walk {
     Item it;
-    long long lo, hi;
+    long long lo, hi, all;
     int j0, j1;
     bool live;
+    Tail tail;
     // one warp
     __device__ __forceinline__ void start(const AttnParams &p) {
-        const long long all = sum_work(p, blockIdx.x == 0);
-        lo = all * blockIdx.x / gridDim.x;
-        hi = all * (blockIdx.x + 1) / gridDim.x;
+        all = sum_work(p, blockIdx.x == 0);
+        lo = run_start(all, blockIdx.x, gridDim.x);
+        hi = run_start(all, blockIdx.x + 1, gridDim.x);
+        tail.tiles = 0;
         live = lo < hi;
         if (!live) return;
         int b = 0;
@@ -211,6 +215,8 @@ struct Walk {
         while (live) {
             j0 = it.cut(lo);
             j1 = it.cut(hi);
+            if (it.at >= lo && it.at + it.size > hi)
+                tail = {it.at, it.size, all, it.tiles, it.b, it.kvh, it.tok0, it.r.t0, it.r.n};
             if (j0 < j1) return;
             advance(p);
         }
@@ -431,7 +437,7 @@ __device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, in
             }
         } else {
             const long long piece = (2ll * blockIdx.x + (it.j0 == 0)) * kItemRows + stage * kRowTile + row;
-            float *part = static_cast<float *>(p.ws) + piece * (kHeadDim + 4);
+            float *part = reinterpret_cast<float *>(static_cast<Tail *>(p.ws) + kAttnCtas) + piece * kRowFloats;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 uint32_t o[32];
@@ -639,6 +645,7 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
             asked = item + 1;
         }
     }
+    if (p.split && lane == 0) static_cast<Tail *>(p.ws)[blockIdx.x] = wk.tail;
     Rec none = {};
     publish(none);
     // no copy may be in flight when the CTA exits
@@ -731,53 +738,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kLoadWarp) drain_ring(bars, wait);
 }
 
-// The items that several CTAs shared, o = sum_c 2^{m_c - m} O_c / sum_c 2^{m_c - m} l_c over their pieces in order.
-// Block x looks at the end of CTA x's run: the first such end inside an item joins it, a warp per row.
+// Joins the items that several CTAs shared, block x the one that CTA x has left for it, a warp per row.
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p, int ctas) {
-    __shared__ Item item;
-    __shared__ int found;
-    __shared__ long long work;
+    __shared__ int list[kAttnCtas], s_count;
     pdl_wait();
     pdl_trigger();
+    const Tail t = static_cast<const Tail *>(p.ws)[blockIdx.x];
+    if (t.tiles == 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) {
-        const long long all = sum_work(p, false);
-        const long long x = all * (blockIdx.x + 1) / ctas;
-        Item it;
-        int b;
-        long long first;
-        bool ok = find_request(p, x, b, first);
-        if (ok) {
-            it.find(p, b, first, x);
-            // ends at its start cut nothing; an earlier end inside it joins it
-            ok = x > it.at && all * blockIdx.x / ctas <= it.at;
-        }
-        if (lane == 0) {
-            found = ok;
-            work = all;
-            if (ok) item = it;
-        }
+        const int count = list_pieces(t, blockIdx.x, ctas, list, [&](long long x) {
+            return x <= t.at ? 0 : x >= t.at + t.size ? t.tiles : (int)((x - t.at) * t.tiles / t.size);
+        });
+        if (lane == 0) s_count = count;
     }
     __syncthreads();
-    if (!found) return;
-    const Item it = item;
-    const int row_tok = kRowTile / p.group;
-    const float *ws = static_cast<const float *>(p.ws);
-    constexpr int kRowFloats = kHeadDim + 4;
+    const int count = s_count, row_tok = kRowTile / p.group;
+    if (count == 0) return;
+    const float *parts = reinterpret_cast<const float *>(static_cast<const Tail *>(p.ws) + kAttnCtas);
     for (int r = blockIdx.y * 8 + warp; r < kItemRows; r += gridDim.y * 8) {
-        const int row = r % kRowTile;
-        const int tok = it.tok0 + (r / kRowTile) * row_tok + row / p.group;
-        if (row >= row_tok * p.group || tok >= it.r.n) continue;
-        auto behind = [&](int c) { return work * c / ctas >= it.at + it.size; };
-        auto piece = [&](int c, const float *&at) {
-            const int j0 = it.cut(work * c / ctas), j1 = it.cut(work * (c + 1) / ctas);
-            at = ws + ((2ll * c + (j0 == 0)) * kItemRows + r) * kRowFloats;
-            return j0 < j1 && j1 - j0 < it.tiles;
-        };
-        uint2 w;
-        if (!join_row(blockIdx.x, ctas, kHeadDim, lane, w, piece, behind)) return;
-        const int h = it.kvh * p.group + row % p.group;
-        reinterpret_cast<uint2 *>(p.out + ((long long)(it.r.t0 + tok) * p.H + h) * kHeadDim)[lane] = w;
+        const int row = r % kRowTile, tok = t.first + (r / kRowTile) * row_tok + row / p.group;
+        if (row >= row_tok * p.group || tok >= t.n) continue;
+        const uint2 w = join_row(list, count, kHeadDim, lane, [&](int piece) {
+            return parts + ((long long)piece * kItemRows + r) * kRowFloats;
+        });
+        const int h = t.kvh * p.group + row % p.group;
+        reinterpret_cast<uint2 *>(p.out + ((long long)(t.t0 + tok) * p.H + h) * kHeadDim)[lane] = w;
     }
 }
 
@@ -810,7 +796,7 @@ AttnExtendPlan plan_attn_extend(long long B, long long T, int H, int Hkv, long l
     plan.split = pieces > 1;
     plan.ctas = (int)std::min<long long>(items * std::min<long long>(pieces, kAttnCtas), kAttnCtas);
     plan.whole_ctas = (int)std::min<long long>(items, kAttnCtas);
-    plan.ws_bytes = plan.split ? 2ull * plan.ctas * kItemRows * (kHeadDim + 4) * 4 : 0;
+    plan.ws_bytes = plan.split ? kAttnCtas * sizeof(Tail) + 2ull * plan.ctas * kItemRows * kRowFloats * 4 : 0;
     return plan;
 }
 
@@ -837,7 +823,7 @@ cudaError_t launch_attn_extend(const AttnParams &p, const AttnExtendPlan &plan, 
     }
     e = launch_pdl(attn_extend_kernel, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, tq, tk, tv, p);
     if (e != cudaSuccess || !p.split || ctas == 1) return e;
-    return launch_pdl(attn_join_kernel, dim3((unsigned)(ctas - 1), 8), dim3(256), 0, stream, p, ctas);
+    return launch_pdl(attn_join_kernel, dim3((unsigned)(ctas - 1), 16), dim3(256), 0, stream, p, ctas);
 }
 
 }  // namespace la

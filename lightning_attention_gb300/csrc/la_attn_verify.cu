@@ -134,15 +134,18 @@ __device__ __forceinline__ bool find_request(const AttnParams &p, int extra, lon
 // The items of a CTA's run, those of which it has no tile left out.
 struct Walk {
     int b, kvh, rb, tiles, j0, j1, kv_len, blocks, extra;
-    long long at, lo, hi;  // where the item begins; the run
+    long long at, lo, hi, all;  // where the item begins; the run; all work
     bool live;
+    Tail tail;
     __device__ __forceinline__ void start(const AttnParams &p, int extra_, int blocks_, int b_, long long first,
-                                          long long lo_, long long hi_) {
+                                          long long lo_, long long hi_, long long all_) {
         extra = extra_;
         blocks = blocks_;
         b = b_;
         lo = lo_;
         hi = hi_;
+        all = all_;
+        tail.tiles = 0;
         live = lo < hi;
         if (!live) return;
         tiles = tiles_of(p, b);
@@ -169,6 +172,8 @@ struct Walk {
         while (live) {
             j0 = cut(lo - at, tiles, extra);
             j1 = cut(hi - at, tiles, extra);
+            if (at >= lo && at + work_of(tiles, extra) > hi)
+                tail = {at, work_of(tiles, extra), all, tiles, b, kvh, rb, 0, 0};
             if (j0 < j1) return;
             advance(p);
         }
@@ -445,7 +450,7 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
         tc_fence_after();
         const int toks = min(tok_block, p.N - w.rb * tok_block), rows = toks * p.group;
         const long long piece = 2ll * blockIdx.x + (w.j0 == 0 ? 1 : 0);
-        float *po = static_cast<float *>(p.ws) + piece * RP * (kHeadDim + 2);
+        float *po = reinterpret_cast<float *>(static_cast<Tail *>(p.ws) + kAttnCtas) + piece * RP * (kHeadDim + 2);
         if (ok) {
             float o[R], l[R];
             tmem_get<R>(tbase + lanes + S::kTmO + r0, o);
@@ -629,8 +634,8 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
     using S = Shape<RP>;
     const int per = p.Hkv * blocks;
     const long long all = sum_work(p, S::kExtra) * per;
-    const long long runs = max(1ll, min((long long)gridDim.x, all)), c = min((long long)blockIdx.x, runs);
-    const long long lo = all * c / runs, hi = c < runs ? all * (c + 1) / runs : lo;
+    const int runs = (int)max(1ll, min((long long)gridDim.x, all)), c = min((int)blockIdx.x, runs);
+    const long long lo = run_start(all, c, runs), hi = run_start(all, min(c + 1, runs), runs);
     int b = 0;
     long long first = 0;
     if (lo < hi) find_request(p, S::kExtra, lo, per, b, first);
@@ -648,7 +653,7 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
         __syncwarp();
     };
     Walk w;
-    for (w.start(p, S::kExtra, blocks, b, first, lo, hi); w.live && ok; w.next(p), ++item) {
+    for (w.start(p, S::kExtra, blocks, b, first, lo, hi, all); w.live && ok; w.next(p), ++item) {
         Pages pages;
         pages.fetch(p.cache, w.b, w.kv_len, w.j0, lane);
         publish({w.b, w.kvh, w.rb, w.kv_len, w.j0, w.j1, w.j0 == 0 && w.j1 == w.tiles});
@@ -670,6 +675,7 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
             ok = ring.load(p, bars, sm, tk, page, w.kvh, wait);
         }
     }
+    if (lane == 0) static_cast<Tail *>(p.ws)[blockIdx.x] = w.tail;
     publish({});
     // no copy may be in flight when the CTA exits
     for (int x = asked > S::kQBufs ? asked - S::kQBufs : 0; x < asked; ++x)
@@ -779,64 +785,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kLoadWarp) drain_ring<RP>(bars, wait);
 }
 
-// The items that several CTAs shared.  Block x looks at the end of CTA x's run: the first such end inside an item joins
-// it, a warp per row, in the CTAs' order.  rp: the padded rows of a partial result; ctas: the grid that left them.
+// Joins the items that several CTAs shared, block x the one that CTA x has left for it, a warp per row.  rp: the
+// padded rows of a partial result; ctas: the grid that left them.
 __global__ void __launch_bounds__(256) attn_verify_join_kernel(const AttnParams p, int rp, int extra, int ctas) {
-    __shared__ long long s_at, s_all;
-    __shared__ int s_b, s_item, s_tiles;
+    __shared__ int list[kAttnCtas], s_count;
     pdl_wait();
     pdl_trigger();
+    const Tail t = static_cast<const Tail *>(p.ws)[blockIdx.x];
+    if (t.tiles == 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tok_block = min(p.N, kMaxDrafts / p.group), blocks = (p.N + tok_block - 1) / tok_block;
-    const int per = p.Hkv * blocks;
     if (warp == 0) {
-        const long long all = sum_work(p, extra) * per, runs = min((long long)ctas, all);
-        int b = 0, tiles = 0, item = 0;
-        long long at = 0, first;
-        if (blockIdx.x + 1 < runs) {
-            const long long x = all * (blockIdx.x + 1) / runs;
-            find_request(p, extra, x, per, b, first);
-            tiles = tiles_of(p, b);
-            item = (int)((x - first) / work_of(tiles, extra));
-            at = first + (long long)item * work_of(tiles, extra);
-            // an end at its beginning cut nothing; an earlier one inside it joins it
-            if (x == at || all * blockIdx.x / runs > at) tiles = 0;
-        }
-        if (tiles > 0 && p.parents) {  // a request with a parent out of range is left as it was
+        int count = list_pieces(t, blockIdx.x, (int)min((long long)ctas, t.all), list,
+                                [&](long long x) { return cut(x - t.at, t.tiles, extra); });
+        if (p.parents) {  // a request with a parent out of range is left as it was
             bool bad = false;
-            for (int t = lane; t < p.N; t += 32) {
-                const int up = p.parents[(long long)b * p.N + t];
-                bad |= up < -1 || up >= t;
+            for (int i = lane; i < p.N; i += 32) {
+                const int up = p.parents[(long long)t.b * p.N + i];
+                bad |= up < -1 || up >= i;
             }
-            if (__any_sync(0xffffffffu, bad)) tiles = 0;
+            if (__any_sync(0xffffffffu, bad)) count = 0;
         }
-        if (lane == 0) {
-            s_at = at;
-            s_all = all;
-            s_b = b;
-            s_item = item;
-            s_tiles = tiles;
-        }
+        if (lane == 0) s_count = count;
     }
     __syncthreads();
-    const int tiles = s_tiles;
-    if (tiles == 0) return;
-    const long long at = s_at, all = s_all, runs = min((long long)ctas, all), work = work_of(tiles, extra);
-    const int b = s_b, kvh = s_item / blocks, rb = s_item - kvh * blocks;
-    const int rows = min(tok_block, p.N - rb * tok_block) * p.group;
-    const long long stride = (long long)rp * (kHeadDim + 2);
-    const float *ws = static_cast<const float *>(p.ws);
+    const int count = s_count;
+    if (count == 0) return;
+    const int tok_block = min(p.N, kMaxDrafts / p.group), tok0 = t.first * tok_block;
+    const int rows = min(tok_block, p.N - tok0) * p.group;
+    const float *parts = reinterpret_cast<const float *>(static_cast<const Tail *>(p.ws) + kAttnCtas);
     for (int r = blockIdx.y * 8 + warp; r < rows; r += gridDim.y * 8) {
-        auto behind = [&](int c) { return all * c / runs >= at + work; };
-        auto piece = [&](int c, const float *&row) {
-            const int j0 = cut(all * c / runs - at, tiles, extra), j1 = cut(all * (c + 1) / runs - at, tiles, extra);
-            row = ws + (2ll * c + (j0 == 0)) * stride + r * kHeadDim;
-            return j0 < j1 && j1 - j0 < tiles;
-        };
-        uint2 w;
-        if (!join_row(blockIdx.x, (int)runs, (long long)rp * kHeadDim - r * (kHeadDim - 2), lane, w, piece, behind)) return;
-        const int tok = r / p.group, head = kvh * p.group + r - tok * p.group;
-        reinterpret_cast<uint2 *>(p.out + (((long long)b * p.N + rb * tok_block + tok) * p.H + head) * kHeadDim)[lane] = w;
+        const uint2 w = join_row(list, count, (long long)rp * kHeadDim - r * (kHeadDim - 2), lane, [&](int piece) {
+            return parts + (long long)piece * rp * (kHeadDim + 2) + r * kHeadDim;
+        });
+        const int tok = r / p.group, head = t.kvh * p.group + r - tok * p.group;
+        reinterpret_cast<uint2 *>(p.out + (((long long)t.b * p.N + tok0 + tok) * p.H + head) * kHeadDim)[lane] = w;
     }
 }
 
@@ -871,7 +853,7 @@ int padded_rows(int N, int group) {
 }  // namespace
 
 unsigned long long attn_verify_ws_bytes(int N, int group) {
-    return 2ull * kAttnCtas * padded_rows(N, group) * (kHeadDim + 2) * 4;
+    return kAttnCtas * (sizeof(Tail) + 2ull * padded_rows(N, group) * (kHeadDim + 2) * 4);
 }
 
 cudaError_t launch_attn_verify(const AttnParams &p, cudaStream_t stream) {
@@ -889,7 +871,7 @@ cudaError_t launch_attn_verify(const AttnParams &p, cudaStream_t stream) {
         default: e = launch<128>(tq, tk, tv, p, kAttnCtas, &extra, stream); break;
     }
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_verify_join_kernel, dim3(kAttnCtas - 1, (unsigned)((rp + 31) / 32)), dim3(256), 0, stream, p, rp,
+    return launch_pdl(attn_verify_join_kernel, dim3(kAttnCtas - 1, (unsigned)(rp / 16)), dim3(256), 0, stream, p, rp,
                       extra, kAttnCtas);
 }
 
