@@ -102,30 +102,36 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
+// The work of a batch in equal runs, one per CTA, the first `more` of them one unit longer.
+struct Runs {
+    long long each;
+    int more, ctas;
+    __device__ __forceinline__ Runs(long long all, int ctas_) : each(all / ctas_), more((int)(all % ctas_)), ctas(ctas_) {}
+    __device__ __forceinline__ long long start(int c) const { return each * c + min(c, more); }
+};
+
 // The item inside which a CTA's run ends, if it is the first run that does: left for the second launch, which joins the
 // results of the CTAs that share it.
 struct Tail {
-    long long at, size, all;  // the item's work [at, at + size) of `all`
-    int tiles;                // of the item; 0: nothing to join
-    int b, kvh, first;        // request, kv head, first token
-    int t0, n;                // the request's first row and its tokens
+    Runs runs;
+    long long at, size;  // the item's work [at, at + size)
+    int tiles;           // of the item; 0: nothing to join
+    int b, kvh, first;   // request, kv head, first token
+    int t0, n;           // the request's first row and its tokens
 };
-
-// Where CTA c of `ctas` begins in `all` work.
-__device__ __forceinline__ long long run_start(long long all, int c, int ctas) { return all * c / ctas; }
 
 // The partial results of an item: a list, in the CTAs' order, of their numbers (two a CTA: 2 c + 1 from the item's first
 // tile on, 2 c from a later one).  One warp, from the CTA whose run ends first inside it; returns their count, 0 if
-// one CTA had the whole item (and has written it).  cut(x): the tile at which the work before x ends.
+// one CTA had the whole item (and has written it).  cut(x): the tile at which the item's first x of work end.
 template <class Cut>
-__device__ __forceinline__ int list_pieces(const Tail &t, int first, int ctas, int *list, Cut cut) {
+__device__ __forceinline__ int list_pieces(const Tail &t, int first, int *list, Cut cut) {
     const int lane = threadIdx.x & 31;
     int count = 0;
-    for (int c0 = first; c0 < ctas; c0 += 32) {
-        const int c = c0 + lane;
-        const long long lo = run_start(t.all, min(c, ctas), ctas), hi = run_start(t.all, min(c + 1, ctas), ctas);
-        const int j0 = cut(lo), j1 = cut(hi);
-        const bool mine = c < ctas && j0 < j1 && j1 - j0 < t.tiles;
+    for (int c0 = first; c0 < t.runs.ctas; c0 += 32) {
+        const int c = min(c0 + lane, t.runs.ctas);
+        const long long lo = t.runs.start(c), hi = t.runs.start(min(c + 1, t.runs.ctas));
+        const int j0 = cut(lo - t.at), j1 = cut(hi - t.at);
+        const bool mine = j0 < j1 && j1 - j0 < t.tiles;
         const unsigned who = __ballot_sync(0xffffffffu, mine);
         if (mine) list[count + __popc(who & ((1u << lane) - 1))] = 2 * c + (j0 == 0);
         count += __popc(who);
@@ -133,55 +139,6 @@ __device__ __forceinline__ int list_pieces(const Tail &t, int first, int ctas, i
     }
     __syncwarp();
     return count;
-}
-
-// A row's partial results joined: o = sum_i 2^{m_i - m} O_i / sum_i 2^{m_i - m} l_i over the pieces of the list, a lane per
-// piece and step, four of their rows in flight; lane l gets columns 4 l .. 4 l + 3.  row(i): where piece i's O row is;
-// m and l follow `to_ml` floats behind it.
-template <class Row>
-__device__ __forceinline__ uint2 join_row(const int *list, int count, long long to_ml, int lane, Row row) {
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < count; i0 += 32) {
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (i0 + lane < count) ml = *reinterpret_cast<const float2 *>(row(list[i0 + lane]) + to_ml);
-        float top = ml.x;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        top = fmaxf(top, m);
-        // a piece whose keys the row does not see has m = -inf and counts for nothing
-        const float w = ml.x == -INFINITY ? 0.f : ex2z(ml.x - top), f = m == -INFINITY ? 0.f : ex2z(m - top);
-        float add = w * ml.y;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) add += __shfl_xor_sync(0xffffffffu, add, d);
-        m = top;
-        l = l * f + add;
-        o.x *= f;
-        o.y *= f;
-        o.z *= f;
-        o.w *= f;
-        const int n = min(32, count - i0);
-        for (int i = 0; i < n; i += 4) {
-            float4 x[4];
-            float g[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                g[k] = __shfl_sync(0xffffffffu, w, (i + k) & 31);  // 0 past the last
-                x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i + k < n && g[k] > 0.f) x[k] = reinterpret_cast<const float4 *>(row(list[i0 + i + k]))[lane];
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (i + k >= n) break;
-                o.x += g[k] * x[k].x;
-                o.y += g[k] * x[k].y;
-                o.z += g[k] * x[k].z;
-                o.w += g[k] * x[k].w;
-            }
-        }
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    return make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
 
 }  // namespace attn

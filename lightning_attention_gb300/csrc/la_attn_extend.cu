@@ -47,7 +47,9 @@ constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffKV = kOffQ + 2 * kTileBytes;
 constexpr uint32_t kOffBars = kOffKV + kSlots * kTileBytes;
 
-constexpr int kRowFloats = kHeadDim + 4;  // of a partial result: O, m, l
+// A partial result: of every group of 32 rows (a lane each) O in pieces of four columns, lane by lane, so that stores and
+// loads of a warp are contiguous, then m and l of all rows.
+constexpr int kPieceFloats = kItemRows * (kHeadDim + 2);
 
 // What a CTA's warps have to know of an item.
 struct Rec {
@@ -85,10 +87,15 @@ __device__ __forceinline__ bool request_of(const AttnParams &p, int b, Request &
 // Work of a kv head's first `items` items of a request: the keys that they see and kItemKeys each for what an item
 // costs besides, or one each where items are not cut.
 constexpr int kItemKeys = 400;
+static_assert(kItemKeys >= kKeyTile, "an item's work covers its tiles");
 __device__ __forceinline__ long long work_of(const AttnParams &p, const Request &r, long long items) {
     if (!p.split) return items;
     const long long tok = 2 * (kRowTile / p.group);
     return items * (r.kv_len - r.n + kItemKeys) + tok * (items * (items + 1) / 2);
+}
+// The tile at which the first `done` of an item's work end; what it costs besides counts as its end.
+__device__ __forceinline__ int cut(long long done, int tiles) {
+    return done <= 0 ? 0 : (int)min((long long)tiles, done / kKeyTile);
 }
 __device__ __forceinline__ int items_of(const AttnParams &p, const Request &r) {
     const int tok = 2 * (kRowTile / p.group);
@@ -168,10 +175,6 @@ struct Item {
         tok0 = t * tok;
         tiles = (r.kv_len - r.n + min(r.n, tok0 + tok) - 1) / kKeyTile + 1;
     }
-    // the tile at which the work before place x ends
-    __device__ __forceinline__ int cut(long long x) const {
-        return x <= at ? 0 : x >= at + size ? tiles : (int)((x - at) * tiles / size);
-    }
     // the next one; false behind the last
     __device__ __forceinline__ bool next(const AttnParams &p) {
         const long long end = at + size;
@@ -193,16 +196,16 @@ struct Item {
 // The items of a CTA's run, those of which it has no tile left out.
 struct Walk {
     Item it;
-    long long lo, hi, all;
+    Runs runs;
+    long long lo, hi;
     int j0, j1;
     bool live;
-    Tail tail;
+    int tail_tiles = 0;  // the item inside which the run ends, if an earlier one does not: 0 if there is none
+    Item tail;
     // one warp
-    __device__ __forceinline__ void start(const AttnParams &p) {
-        all = sum_work(p, blockIdx.x == 0);
-        lo = run_start(all, blockIdx.x, gridDim.x);
-        hi = run_start(all, blockIdx.x + 1, gridDim.x);
-        tail.tiles = 0;
+    __device__ __forceinline__ Walk(const AttnParams &p) : runs(sum_work(p, blockIdx.x == 0), gridDim.x) {
+        lo = runs.start(blockIdx.x);
+        hi = runs.start(blockIdx.x + 1);
         live = lo < hi;
         if (!live) return;
         int b = 0;
@@ -213,10 +216,12 @@ struct Walk {
     }
     __device__ __forceinline__ void settle(const AttnParams &p) {
         while (live) {
-            j0 = it.cut(lo);
-            j1 = it.cut(hi);
-            if (it.at >= lo && it.at + it.size > hi)
-                tail = {it.at, it.size, all, it.tiles, it.b, it.kvh, it.tok0, it.r.t0, it.r.n};
+            j0 = cut(lo - it.at, it.tiles);
+            j1 = hi >= it.at + it.size ? it.tiles : cut(hi - it.at, it.tiles);
+            if (it.at >= lo && it.at + it.size > hi) {
+                tail = it;
+                tail_tiles = it.tiles;
+            }
             if (j0 < j1) return;
             advance(p);
         }
@@ -230,6 +235,11 @@ struct Walk {
 
 // A row's reference before it has seen a key: any score passes it, and -inf stays -inf against it.
 constexpr float kUnseen = 1e30f;
+
+// Columns 0 .. last of 32, a bit each.
+__device__ __forceinline__ uint32_t columns_seen(int last) {
+    return last >= 31 ? 0xffffffffu : last < 0 ? 0u : (2u << last) - 1u;
+}
 
 // Half a tile of a row: its weights against the reference as bf16 pairs in w, their sums in l (four partial ones),
 // the largest exponent returned.  Columns past `last` are not seen; lo_last and hi_last: its least and largest value in
@@ -248,12 +258,11 @@ __device__ __forceinline__ float weigh(uint32_t ts, int last, int lo_last, int h
         }
         tmem_ld32(ts + i * 32, x);
         tmem_ld_wait_regs(x);
-        if (kMask) {
-            if (lo_last < i * 32 + 31) {
+        if (kMask && lo_last < i * 32 + 31) {
+            const uint32_t seen = columns_seen(last - i * 32);
 #pragma unroll
-                for (int y = 0; y < 32; ++y)
-                    if (i * 32 + y > last) x[y] = 0xff800000u;
-            }
+            for (int y = 0; y < 32; ++y)
+                if (!(seen & (1u << y))) x[y] = 0xff800000u;
         }
 #pragma unroll
         for (int y = 0; y < 16; ++y) {
@@ -279,9 +288,10 @@ __device__ __forceinline__ float largest(uint32_t ts, int last, int lo_last, int
         tmem_ld32(ts + i * 32, x);
         tmem_ld_wait_regs(x);
         if (lo_last < i * 32 + 31) {
+            const uint32_t seen = columns_seen(last - i * 32);
 #pragma unroll
             for (int y = 0; y < 32; ++y)
-                if (i * 32 + y > last) x[y] = 0xff800000u;
+                if (!(seen & (1u << y))) x[y] = 0xff800000u;
         }
 #pragma unroll
         for (int y = 0; y < 32; y += 2)
@@ -436,21 +446,21 @@ __device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, in
                 dst[4] = w[1][k];
             }
         } else {
-            const long long piece = (2ll * blockIdx.x + (it.j0 == 0)) * kItemRows + stage * kRowTile + row;
-            float *part = reinterpret_cast<float *>(static_cast<Tail *>(p.ws) + kAttnCtas) + piece * kRowFloats;
+            float *part = reinterpret_cast<float *>(static_cast<Tail *>(p.ws) + kAttnCtas) +
+                          (2ll * blockIdx.x + (it.j0 == 0)) * kPieceFloats;
+            uint4 *dst = reinterpret_cast<uint4 *>(part) + (pair * 32 + half * 16) * 32 + lane;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 uint32_t o[32];
                 tmem_ld32(to + i * 32, o);
                 tmem_ld_wait_regs(o);
-                if (!valid) continue;
 #pragma unroll
                 for (int x = 0; x < 8; ++x)
-                    reinterpret_cast<uint4 *>(part)[half * 16 + 8 * i + x] =
-                        make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                    dst[(8 * i + x) * 32] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
             }
-            if (valid && half == 0)
-                *reinterpret_cast<float2 *>(part + kHeadDim) = make_float2(neg_m == kUnseen ? -INFINITY : -neg_m, l);
+            if (half == 0)
+                reinterpret_cast<float2 *>(part + kItemRows * kHeadDim)[pair * 32 + lane] =
+                    make_float2(neg_m == kUnseen ? -INFINITY : -neg_m, l);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->o_free[stage]);
@@ -611,8 +621,8 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
         }
         __syncwarp();
     };
-    Walk wk;
-    for (wk.start(p); wk.live && ok; wk.next(p), ++item) {
+    Walk wk(p);
+    for (; wk.live && ok; wk.next(p), ++item) {
         const Item &it = wk.it;
         Pages pages;
         pages.fetch(p.cache, it.b, it.r.kv_len, wk.j0, lane);
@@ -645,7 +655,10 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
             asked = item + 1;
         }
     }
-    if (p.split && lane == 0) static_cast<Tail *>(p.ws)[blockIdx.x] = wk.tail;
+    if (p.split && lane == 0) {
+        const Item &it = wk.tail;
+        static_cast<Tail *>(p.ws)[blockIdx.x] = {wk.runs, it.at, it.size, wk.tail_tiles, it.b, it.kvh, it.tok0, it.r.t0, it.r.n};
+    }
     Rec none = {};
     publish(none);
     // no copy may be in flight when the CTA exits
@@ -718,6 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
+    pdl_trigger();  // the join may wait for the end of this grid from here on
     const Waiter wait{p.wait_limit_ns, p.err};
     if (warp < kMmaWarp) {
         reg_inc<kRegsSoftmax>();
@@ -731,24 +745,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         else if (warp == kValueWarp)
             value_role(p, &tv, bars, sm, lane, wait);
     }
-    pdl_trigger();
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) tmem_dealloc(tbase, kTmCols);
     if (warp == kLoadWarp) drain_ring(bars, wait);
 }
 
-// Joins the items that several CTAs shared, block x the one that CTA x has left for it, a warp per row.
-__global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p, int ctas) {
+// Joins the items that several CTAs shared, block x the one that CTA x has left for it, block y 32 rows of it:
+//     o = sum_i 2^{m_i - m} O_i / sum_i 2^{m_i - m} l_i   over the pieces i, in the CTAs' order.
+// A lane has a row, a warp four pieces of four columns; rows go out through shared memory.
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
     __shared__ int list[kAttnCtas], s_count;
+    __shared__ __align__(16) uint2 rows[32][33];
     pdl_wait();
     pdl_trigger();
     const Tail t = static_cast<const Tail *>(p.ws)[blockIdx.x];
     if (t.tiles == 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) {
-        const int count = list_pieces(t, blockIdx.x, ctas, list, [&](long long x) {
-            return x <= t.at ? 0 : x >= t.at + t.size ? t.tiles : (int)((x - t.at) * t.tiles / t.size);
+        const int count = list_pieces(t, blockIdx.x, list, [&](long long done) {
+            return done >= t.size ? t.tiles : cut(done, t.tiles);
         });
         if (lane == 0) s_count = count;
     }
@@ -756,14 +772,43 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p, int 
     const int count = s_count, row_tok = kRowTile / p.group;
     if (count == 0) return;
     const float *parts = reinterpret_cast<const float *>(static_cast<const Tail *>(p.ws) + kAttnCtas);
-    for (int r = blockIdx.y * 8 + warp; r < kItemRows; r += gridDim.y * 8) {
-        const int row = r % kRowTile, tok = t.first + (r / kRowTile) * row_tok + row / p.group;
+    float m = -INFINITY, l = 0.f;
+    float4 o[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < count; ++i) {
+        const float *part = parts + (long long)list[i] * kPieceFloats;
+        const float2 ml = reinterpret_cast<const float2 *>(part + kItemRows * kHeadDim)[blockIdx.y * 32 + lane];
+        float4 in[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            in[x] = reinterpret_cast<const float4 *>(part)[(blockIdx.y * 32 + warp * 4 + x) * 32 + lane];
+        // a piece whose keys the row does not see has m = -inf and counts for nothing
+        const float top = fmaxf(m, ml.x), f = m == -INFINITY ? 0.f : ex2z(m - top);
+        const float g = ml.x == -INFINITY ? 0.f : ex2z(ml.x - top);
+        m = top;
+        l = l * f + ml.y * g;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            o[x].x = o[x].x * f + in[x].x * g;
+            o[x].y = o[x].y * f + in[x].y * g;
+            o[x].z = o[x].z * f + in[x].z * g;
+            o[x].w = o[x].w * f + in[x].w * g;
+        }
+    }
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+        rows[lane][warp * 4 + x] =
+            make_uint2(pack_bf16x2(o[x].x * inv, o[x].y * inv), pack_bf16x2(o[x].z * inv, o[x].w * inv));
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = (blockIdx.y & 3) * 32 + warp * 4 + i, stage = blockIdx.y >> 2;
+        const int tok = t.first + stage * row_tok + row / p.group;
         if (row >= row_tok * p.group || tok >= t.n) continue;
-        const uint2 w = join_row(list, count, kHeadDim, lane, [&](int piece) {
-            return parts + ((long long)piece * kItemRows + r) * kRowFloats;
-        });
         const int h = t.kvh * p.group + row % p.group;
-        reinterpret_cast<uint2 *>(p.out + ((long long)(t.t0 + tok) * p.H + h) * kHeadDim)[lane] = w;
+        reinterpret_cast<uint2 *>(p.out + ((long long)(t.t0 + tok) * p.H + h) * kHeadDim)[lane] = rows[warp * 4 + i][lane];
     }
 }
 
@@ -796,7 +841,7 @@ AttnExtendPlan plan_attn_extend(long long B, long long T, int H, int Hkv, long l
     plan.split = pieces > 1;
     plan.ctas = (int)std::min<long long>(items * std::min<long long>(pieces, kAttnCtas), kAttnCtas);
     plan.whole_ctas = (int)std::min<long long>(items, kAttnCtas);
-    plan.ws_bytes = plan.split ? kAttnCtas * sizeof(Tail) + 2ull * plan.ctas * kItemRows * kRowFloats * 4 : 0;
+    plan.ws_bytes = plan.split ? kAttnCtas * sizeof(Tail) + 2ull * plan.ctas * kPieceFloats * 4 : 0;
     return plan;
 }
 
@@ -823,7 +868,7 @@ cudaError_t launch_attn_extend(const AttnParams &p, const AttnExtendPlan &plan, 
     }
     e = launch_pdl(attn_extend_kernel, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, tq, tk, tv, p);
     if (e != cudaSuccess || !p.split || ctas == 1) return e;
-    return launch_pdl(attn_join_kernel, dim3((unsigned)(ctas - 1), 16), dim3(256), 0, stream, p, ctas);
+    return launch_pdl(attn_join_kernel, dim3((unsigned)(ctas - 1), 8), dim3(256), 0, stream, p);
 }
 
 }  // namespace la

@@ -81,9 +81,8 @@ __device__ __forceinline__ int tiles_of(const AttnParams &p, int b) {
 // An item is a (request, kv head, block of drafts); its work is its tiles and `extra` more for its beginning and end.
 __device__ __forceinline__ int work_of(int tiles, int extra) { return tiles ? tiles + extra : 0; }
 // The tile at which the first `done` of an item's work end.
-__device__ __forceinline__ int cut(long long done, int tiles, int extra) {
-    const int work = tiles + extra;
-    return done <= 0 ? 0 : done >= work ? tiles : (int)(done * tiles / work);
+__device__ __forceinline__ int cut(long long done, int tiles) {
+    return done <= 0 ? 0 : (int)min((long long)tiles, done);
 }
 
 // Work of an item of every request, summed: one warp, 256 requests at a time.
@@ -134,20 +133,20 @@ __device__ __forceinline__ bool find_request(const AttnParams &p, int extra, lon
 // The items of a CTA's run, those of which it has no tile left out.
 struct Walk {
     int b, kvh, rb, tiles, j0, j1, kv_len, blocks, extra;
-    long long at, lo, hi, all;  // where the item begins; the run; all work
+    Runs runs;
+    long long at, lo, hi;  // where the item begins; the run
     bool live;
-    Tail tail;
-    __device__ __forceinline__ void start(const AttnParams &p, int extra_, int blocks_, int b_, long long first,
-                                          long long lo_, long long hi_, long long all_) {
-        extra = extra_;
-        blocks = blocks_;
-        b = b_;
-        lo = lo_;
-        hi = hi_;
-        all = all_;
-        tail.tiles = 0;
+    int tail_tiles = 0, tail_b, tail_kvh, tail_rb;  // the item inside which the run ends, if an earlier one does not
+    long long tail_at;
+    // one warp
+    __device__ __forceinline__ Walk(const AttnParams &p, int extra_, int blocks_, long long all)
+        : blocks(blocks_), extra(extra_), runs(all, (int)max(1ll, min((long long)gridDim.x, all))) {
+        lo = runs.start(min((int)blockIdx.x, runs.ctas));
+        hi = runs.start(min((int)blockIdx.x + 1, runs.ctas));
         live = lo < hi;
         if (!live) return;
+        long long first;
+        find_request(p, extra, lo, p.Hkv * blocks, b, first);
         tiles = tiles_of(p, b);
         kv_len = p.cache.kv_lens[b];
         const int item = (int)((lo - first) / work_of(tiles, extra));
@@ -170,10 +169,15 @@ struct Walk {
     }
     __device__ __forceinline__ void settle(const AttnParams &p) {
         while (live) {
-            j0 = cut(lo - at, tiles, extra);
-            j1 = cut(hi - at, tiles, extra);
-            if (at >= lo && at + work_of(tiles, extra) > hi)
-                tail = {at, work_of(tiles, extra), all, tiles, b, kvh, rb, 0, 0};
+            j0 = cut(lo - at, tiles);
+            j1 = cut(hi - at, tiles);
+            if (at >= lo && at + work_of(tiles, extra) > hi) {
+                tail_tiles = tiles;
+                tail_b = b;
+                tail_kvh = kvh;
+                tail_rb = rb;
+                tail_at = at;
+            }
             if (j0 < j1) return;
             advance(p);
         }
@@ -632,13 +636,6 @@ template <int RP>
 __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUtensorMap *tk, Bars<RP> *bars,
                           uint8_t *sm, int lane, int blocks, int tok_block, const Waiter &wait) {
     using S = Shape<RP>;
-    const int per = p.Hkv * blocks;
-    const long long all = sum_work(p, S::kExtra) * per;
-    const int runs = (int)max(1ll, min((long long)gridDim.x, all)), c = min((int)blockIdx.x, runs);
-    const long long lo = run_start(all, c, runs), hi = run_start(all, min(c + 1, runs), runs);
-    int b = 0;
-    long long first = 0;
-    if (lo < hi) find_request(p, S::kExtra, lo, per, b, first);
     const uint32_t box = (uint32_t)(tok_block * p.group) * 128;
     int item = 0, asked = 0;
     Ring<RP> ring(0);
@@ -652,8 +649,8 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
         }
         __syncwarp();
     };
-    Walk w;
-    for (w.start(p, S::kExtra, blocks, b, first, lo, hi, all); w.live && ok; w.next(p), ++item) {
+    Walk w(p, S::kExtra, blocks, sum_work(p, S::kExtra) * p.Hkv * blocks);
+    for (; w.live && ok; w.next(p), ++item) {
         Pages pages;
         pages.fetch(p.cache, w.b, w.kv_len, w.j0, lane);
         publish({w.b, w.kvh, w.rb, w.kv_len, w.j0, w.j1, w.j0 == 0 && w.j1 == w.tiles});
@@ -675,7 +672,9 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
             ok = ring.load(p, bars, sm, tk, page, w.kvh, wait);
         }
     }
-    if (lane == 0) static_cast<Tail *>(p.ws)[blockIdx.x] = w.tail;
+    if (lane == 0)
+        static_cast<Tail *>(p.ws)[blockIdx.x] = {w.runs, w.tail_at, work_of(w.tail_tiles, w.extra), w.tail_tiles, w.tail_b,
+                                                 w.tail_kvh, w.tail_rb, 0, 0};
     publish({});
     // no copy may be in flight when the CTA exits
     for (int x = asked > S::kQBufs ? asked - S::kQBufs : 0; x < asked; ++x)
@@ -785,9 +784,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kLoadWarp) drain_ring<RP>(bars, wait);
 }
 
+// A row's partial results joined: o = sum_i 2^{m_i - m} O_i / sum_i 2^{m_i - m} l_i over the pieces of the list, a lane per
+// piece and step, four of their rows in flight; lane l gets columns 4 l .. 4 l + 3.  row(i): where piece i's O row is;
+// m and l follow `to_ml` floats behind it.
+template <class Row>
+__device__ __forceinline__ uint2 join_row(const int *list, int count, long long to_ml, int lane, Row row) {
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < count; i0 += 32) {
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (i0 + lane < count) ml = *reinterpret_cast<const float2 *>(row(list[i0 + lane]) + to_ml);
+        float top = ml.x;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        top = fmaxf(top, m);
+        // a piece whose keys the row does not see has m = -inf and counts for nothing
+        const float w = ml.x == -INFINITY ? 0.f : ex2z(ml.x - top), f = m == -INFINITY ? 0.f : ex2z(m - top);
+        float add = w * ml.y;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) add += __shfl_xor_sync(0xffffffffu, add, d);
+        m = top;
+        l = l * f + add;
+        o.x *= f;
+        o.y *= f;
+        o.z *= f;
+        o.w *= f;
+        const int n = min(32, count - i0);
+        for (int i = 0; i < n; i += 4) {
+            float4 x[4];
+            float g[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                g[k] = __shfl_sync(0xffffffffu, w, (i + k) & 31);  // 0 past the last
+                x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i + k < n && g[k] > 0.f) x[k] = reinterpret_cast<const float4 *>(row(list[i0 + i + k]))[lane];
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (i + k >= n) break;
+                o.x += g[k] * x[k].x;
+                o.y += g[k] * x[k].y;
+                o.z += g[k] * x[k].z;
+                o.w += g[k] * x[k].w;
+            }
+        }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    return make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+}
+
 // Joins the items that several CTAs shared, block x the one that CTA x has left for it, a warp per row.  rp: the
-// padded rows of a partial result; ctas: the grid that left them.
-__global__ void __launch_bounds__(256) attn_verify_join_kernel(const AttnParams p, int rp, int extra, int ctas) {
+// padded rows of a partial result.
+__global__ void __launch_bounds__(256) attn_verify_join_kernel(const AttnParams p, int rp) {
     __shared__ int list[kAttnCtas], s_count;
     pdl_wait();
     pdl_trigger();
@@ -795,8 +843,7 @@ __global__ void __launch_bounds__(256) attn_verify_join_kernel(const AttnParams 
     if (t.tiles == 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) {
-        int count = list_pieces(t, blockIdx.x, (int)min((long long)ctas, t.all), list,
-                                [&](long long x) { return cut(x - t.at, t.tiles, extra); });
+        int count = list_pieces(t, blockIdx.x, list, [&](long long done) { return cut(done, t.tiles); });
         if (p.parents) {  // a request with a parent out of range is left as it was
             bool bad = false;
             for (int i = lane; i < p.N; i += 32) {
@@ -824,8 +871,7 @@ __global__ void __launch_bounds__(256) attn_verify_join_kernel(const AttnParams 
 
 template <int RP>
 cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const AttnParams &p,
-                   int ctas, int *extra, cudaStream_t stream) {
-    *extra = Shape<RP>::kExtra;
+                   int ctas, cudaStream_t stream) {
     constexpr uint32_t smem = Shape<RP>::kOffBars + sizeof(Bars<RP>) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory");
     int dev = 0;
@@ -863,16 +909,14 @@ cudaError_t launch_attn_verify(const AttnParams &p, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     const int rp = padded_rows(p.N, p.group);
     cudaError_t e;
-    int extra;
     switch (rp) {
-        case 16: e = launch<16>(tq, tk, tv, p, kAttnCtas, &extra, stream); break;
-        case 32: e = launch<32>(tq, tk, tv, p, kAttnCtas, &extra, stream); break;
-        case 64: e = launch<64>(tq, tk, tv, p, kAttnCtas, &extra, stream); break;
-        default: e = launch<128>(tq, tk, tv, p, kAttnCtas, &extra, stream); break;
+        case 16: e = launch<16>(tq, tk, tv, p, kAttnCtas, stream); break;
+        case 32: e = launch<32>(tq, tk, tv, p, kAttnCtas, stream); break;
+        case 64: e = launch<64>(tq, tk, tv, p, kAttnCtas, stream); break;
+        default: e = launch<128>(tq, tk, tv, p, kAttnCtas, stream); break;
     }
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_verify_join_kernel, dim3(kAttnCtas - 1, (unsigned)(rp / 16)), dim3(256), 0, stream, p, rp,
-                      extra, kAttnCtas);
+    return launch_pdl(attn_verify_join_kernel, dim3(kAttnCtas - 1, (unsigned)(rp / 16)), dim3(256), 0, stream, p, rp);
 }
 
 }  // namespace la

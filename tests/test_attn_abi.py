@@ -130,7 +130,7 @@ def test_workspaces(lib):
     assert size(1, 1, 1, 128, None) == 1
     for n, H, Hkv, rows in ((1, 16, 1, 16), (1, 17, 1, 32), (8, 8, 1, 64), (8, 64, 8, 64), (13, 5, 1, 128), (128, 1, 1, 128),
                             (100, 4, 2, 128), (128, 128, 1, 128)):
-        assert la.attn_verify_workspace_size(n, H, Hkv, 128) == 152 * (48 + 2 * rows * 130 * 4)
+        assert la.attn_verify_workspace_size(n, H, Hkv, 128) == 152 * (56 + 2 * rows * 130 * 4)
     need = la.attn_verify_workspace_size(3, 2, 1, 128)
     assert tree(lib, nbytes=need - 1) == 1
     assert decode(lib, nbytes=la.attn_verify_workspace_size(1, 2, 1, 128) - 1) == 1
@@ -142,7 +142,7 @@ def test_workspaces(lib):
     assert size(1, 1, 1, 1, 128, 1, 1, None) == 1
     assert la.attn_extend_workspace_size(0, 0, 1, 1, 128, 0, 0) == 0
     # pieces of items that see more than 256 keys, two per CTA at most
-    piece, tails = 2 * 256 * 132 * 4, 152 * 48
+    piece, tails = 2 * 256 * 130 * 4, 152 * 56
     assert la.attn_extend_workspace_size(1, 16384, 32, 8, 128, 16384, 16384) == tails + 152 * piece
     assert la.attn_extend_workspace_size(1, 1, 8, 1, 128, 1, 1000) == tails + 4 * piece
     assert la.attn_extend_workspace_size(100, 25600, 8, 1, 128, 256, 256) == 0
