@@ -785,7 +785,7 @@ def _rope_args(q, k, positions, inv_freq, q_out):
         raise TypeError("inv_freq must be a float64 [rot_dim / 2] tensor")
     _need_fast(inv_freq, "inv_freq", torch.float64, dev, inv_freq.shape)
     if q_out is None:
-        q_out = torch.empty((T, H * _HEAD_DIM), dtype=torch.bfloat16, device=dev)
+        return dev, T, H, Hkv, rs, q.new_empty((T, H * _HEAD_DIM)), H * _HEAD_DIM
     return dev, T, H, Hkv, rs, q_out, _need_rows(q_out, "q_out", dev, T, H * _HEAD_DIM)
 
 
@@ -796,7 +796,7 @@ def rope(q, k, positions, inv_freq, interleaved: bool = False, mscale: float = 1
     rotate in place."""
     dev, T, H, Hkv, rs, q_out, qo = _rope_args(q, k, positions, inv_freq, q_out)
     if k_out is None:
-        k_out = torch.empty((T, Hkv * _HEAD_DIM), dtype=torch.bfloat16, device=dev)
+        k_out = k.new_empty((T, Hkv * _HEAD_DIM))
     ko = _need_rows(k_out, "k_out", dev, T, Hkv * _HEAD_DIM)
     with _on(dev):
         st = (_lib or load()).la_rope(_ptr(q), _ptr(k), *rs, _ptr(positions), _ptr(inv_freq), 2 * inv_freq.shape[0],
@@ -835,11 +835,19 @@ def _attn_args(q, k_pages, v_pages, page_table, kv_lens, out, scale):
     E, Hkv, P, stride = _need_pages(k_pages, v_pages, dev)
     B, width = _need_lists(page_table, kv_lens, dev)
     if out is None:
-        out = torch.empty((T, H * _HEAD_DIM), dtype=torch.bfloat16, device=dev)
+        out = q.new_empty((T, H * _HEAD_DIM))
     else:
         _need_fast(out, "out", torch.bfloat16, dev, (T, H * _HEAD_DIM))
     cache = (_ptr(k_pages), _ptr(v_pages), stride, E, P, _ptr(page_table), width)
     return dev, T, H, Hkv, B, q_rs, cache, out, _HEAD_DIM ** -0.5 if scale is None else scale
+
+
+def _scratch(workspace, near, nbytes: int):
+    """(tensor, bytes): the caller's uint8 scratch, or nbytes of the current stream's own next to int32 tensor `near`."""
+    if workspace is None:
+        return near.new_empty(-(-nbytes // 4)), nbytes
+    _need(workspace, "workspace", torch.uint8, near.device)
+    return workspace, workspace.numel()
 
 
 @functools.lru_cache(maxsize=1024)
@@ -865,14 +873,12 @@ def attn_extend(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, out=None, 
     _need_fast(cu_seqlens, "cu_seqlens", torch.int32, dev, (B + 1,))
     max_seqlen = T if max_seqlen is None else int(max_seqlen)
     max_kvlen = cache[4] * cache[6] if max_kvlen is None else int(max_kvlen)
-    if workspace is None:
-        nbytes = 0 if H % Hkv else attn_extend_workspace_size(B, T, H, Hkv, _HEAD_DIM, max_seqlen, max_kvlen)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _need(workspace, "workspace", torch.uint8, dev)
+    workspace, nbytes = _scratch(workspace, kv_lens, 0 if H % Hkv else attn_extend_workspace_size(
+        B, T, H, Hkv, _HEAD_DIM, max_seqlen, max_kvlen))
     with _on(dev):
         st = (_lib or load()).la_attn_extend(_ptr(q), q_rs, *cache, _ptr(cu_seqlens), _ptr(kv_lens), _ptr(out), B, T, H,
-                                             Hkv, _HEAD_DIM, max_seqlen, max_kvlen, scale, _ptr(workspace),
-                                             workspace.numel(), _stream_handle(dev))
+                                             Hkv, _HEAD_DIM, max_seqlen, max_kvlen, scale, _ptr(workspace), nbytes,
+                                             _stream_handle(dev))
     if st:
         _check("la_attn_extend", st)
     return out
@@ -886,14 +892,6 @@ def attn_verify_workspace_size(N: int, H: int, Hkv: int, D: int) -> int:
     return int(n.value)
 
 
-def _verify_workspace(workspace, N: int, H: int, Hkv: int, dev):
-    if workspace is None:
-        nbytes = 0 if H % Hkv else attn_verify_workspace_size(N, H, Hkv, _HEAD_DIM)
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _need(workspace, "workspace", torch.uint8, dev)
-    return workspace
-
-
 def attn_decode(q, k_pages, v_pages, page_table, kv_lens, out=None, scale: float | None = None, workspace=None):
     """Attention of one token per request over a paged cache (la_attn_decode): q bf16 [B, H*128], the last of kv_lens[b]
     positions; returns out bf16 [B, H*128].  The other arguments are attn_extend's; workspace: uint8 scratch of
@@ -901,10 +899,10 @@ def attn_decode(q, k_pages, v_pages, page_table, kv_lens, out=None, scale: float
     dev, T, H, Hkv, B, q_rs, cache, out, scale = _attn_args(q, k_pages, v_pages, page_table, kv_lens, out, scale)
     if T != B:
         raise ValueError(f"q must have a row per request, {B}, got {T}")
-    workspace = _verify_workspace(workspace, 1, H, Hkv, dev)
+    workspace, nbytes = _scratch(workspace, kv_lens, 0 if H % Hkv else attn_verify_workspace_size(1, H, Hkv, _HEAD_DIM))
     with _on(dev):
         st = (_lib or load()).la_attn_decode(_ptr(q), q_rs, *cache, _ptr(kv_lens), _ptr(out), B, H, Hkv, _HEAD_DIM,
-                                             scale, _ptr(workspace), workspace.numel(), _stream_handle(dev))
+                                             scale, _ptr(workspace), nbytes, _stream_handle(dev))
     if st:
         _check("la_attn_decode", st)
     return out
@@ -922,11 +920,10 @@ def attn_verify_tree(q, k_pages, v_pages, page_table, kv_lens, parents, N: int, 
     if T != B * N:
         raise ValueError(f"q must have {N} rows per request, {B * N}, got {T}")
     _need_fast(parents, "parents", torch.int32, dev, (B, N))
-    workspace = _verify_workspace(workspace, N, H, Hkv, dev)
+    workspace, nbytes = _scratch(workspace, kv_lens, 0 if H % Hkv else attn_verify_workspace_size(N, H, Hkv, _HEAD_DIM))
     with _on(dev):
         st = (_lib or load()).la_attn_verify_tree(_ptr(q), q_rs, *cache, _ptr(kv_lens), _ptr(parents), _ptr(out), B, N, H,
-                                                  Hkv, _HEAD_DIM, scale, _ptr(workspace), workspace.numel(),
-                                                  _stream_handle(dev))
+                                                  Hkv, _HEAD_DIM, scale, _ptr(workspace), nbytes, _stream_handle(dev))
     if st:
         _check("la_attn_verify_tree", st)
     return out
@@ -949,7 +946,7 @@ def kv_commit(k_pages, v_pages, page_table, kv_lens, parents, accept_idx, new_le
     _need_fast(parents, "parents", torch.int32, dev, (B, N))
     _need_fast(accept_idx, "accept_idx", torch.int32, dev, (B,))
     if new_lens is None:
-        new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+        new_lens = kv_lens.new_empty(B)
     else:
         _need_fast(new_lens, "new_lens", torch.int32, dev, (B,))
     with _on(dev):

@@ -102,6 +102,60 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
+// Sum of work(b) over the requests, and the request within whose work place x lies with the place where that begins (false
+// behind the last one's).  One warp, eight requests a lane and step, whose lengths are fetched together.
+template <class Work>
+__device__ __forceinline__ long long sum_work(int B, Work work) {
+    const int lane = threadIdx.x & 31;
+    long long all = 0;
+    for (int b0 = lane * 8; b0 < B; b0 += 256) {
+        long long w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = b0 + i < B ? work(b0 + i) : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) all += w[i];
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
+    return all;
+}
+template <class Work>
+__device__ __forceinline__ bool find_request(int B, long long x, int &b, long long &first, Work work) {
+    const int lane = threadIdx.x & 31;
+    long long before = 0;
+    for (int b0 = 0; b0 < B; b0 += 256) {
+        long long w[8], mine = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = b0 + lane * 8 + i < B ? work(b0 + lane * 8 + i) : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mine += w[i];
+        long long upto = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += y;
+        }
+        upto += before;
+        const unsigned hit = __ballot_sync(0xffffffffu, x >= upto - mine && x < upto);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            long long at = upto - mine;
+            int found = b0 + lane * 8;
+#pragma unroll
+            for (int i = 0; i < 7; ++i)
+                if (x >= at + w[i] && found == b0 + lane * 8 + i) {
+                    at += w[i];
+                    ++found;
+                }
+            b = __shfl_sync(0xffffffffu, found, src);
+            first = __shfl_sync(0xffffffffu, at, src);
+            return true;
+        }
+        before = __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return false;
+}
+
 // The work of a batch in equal runs, one per CTA, the first `more` of them one unit longer.
 struct Runs {
     long long each;

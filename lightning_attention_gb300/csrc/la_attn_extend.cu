@@ -102,46 +102,12 @@ __device__ __forceinline__ int items_of(const AttnParams &p, const Request &r) {
     return (r.n + tok - 1) / tok;
 }
 
-// Work of the whole batch; with `report` faulty requests, which have none, are reported.  One warp.
-__device__ __forceinline__ long long sum_work(const AttnParams &p, bool report) {
-    long long all = 0;
-    for (int b = threadIdx.x & 31; b < p.B; b += 32) {
-        Request r;
-        if (request_of(p, b, r))
-            all += work_of(p, r, items_of(p, r)) * p.Hkv;
-        else if (report)
-            atomicOr(p.err, ERR_BIT_SEQLENS);
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
-    return all;
-}
-
-// The request within whose work place x lies, and where that begins; false behind the last one's.  One warp.
-__device__ __forceinline__ bool find_request(const AttnParams &p, long long x, int &b, long long &first) {
-    const int lane = threadIdx.x & 31;
-    long long before = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        Request r;
-        const long long mine =
-            b0 + lane < p.B && request_of(p, b0 + lane, r) ? work_of(p, r, items_of(p, r)) * p.Hkv : 0;
-        long long upto = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, upto, d);
-            if (lane >= d) upto += y;
-        }
-        upto += before;
-        const unsigned hit = __ballot_sync(0xffffffffu, x >= upto - mine && x < upto);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            b = b0 + src;
-            first = __shfl_sync(0xffffffffu, upto - mine, src);
-            return true;
-        }
-        before = __shfl_sync(0xffffffffu, upto, 31);
-    }
-    return false;
+// Work of a request; with `report` a faulty one, which has none, is reported.
+__device__ __forceinline__ long long request_work(const AttnParams &p, int b, bool report) {
+    Request r;
+    if (request_of(p, b, r)) return work_of(p, r, items_of(p, r)) * p.Hkv;
+    if (report) atomicOr(p.err, ERR_BIT_SEQLENS);
+    return 0;
 }
 
 // An item: rows of request b from token tok0 on, kv head kvh, its work [at, at + size), its tiles of keys.
@@ -203,14 +169,14 @@ struct Walk {
     int tail_tiles = 0;  // the item inside which the run ends, if an earlier one does not: 0 if there is none
     Item tail;
     // one warp
-    __device__ __forceinline__ Walk(const AttnParams &p) : runs(sum_work(p, blockIdx.x == 0), gridDim.x) {
+    __device__ __forceinline__ Walk(const AttnParams &p) : runs(sum_work(p.B, [&](int x) { return request_work(p, x, blockIdx.x == 0); }), gridDim.x) {
         lo = runs.start(blockIdx.x);
         hi = runs.start(blockIdx.x + 1);
         live = lo < hi;
         if (!live) return;
         int b = 0;
         long long first = 0;
-        find_request(p, lo, b, first);
+        find_request(p.B, lo, b, first, [&](int x) { return request_work(p, x, false); });
         it.find(p, b, first, lo);
         settle(p);
     }

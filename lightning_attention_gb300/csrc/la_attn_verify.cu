@@ -85,49 +85,9 @@ __device__ __forceinline__ int cut(long long done, int tiles) {
     return done <= 0 ? 0 : (int)min((long long)tiles, done);
 }
 
-// Work of an item of every request, summed: one warp, 256 requests at a time.
-__device__ __forceinline__ long long sum_work(const AttnParams &p, int extra) {
-    const int lane = threadIdx.x & 31;
-    long long all = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 256) {
-        int t[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            t[i] = b0 + i * 32 + lane < p.B ? work_of(tiles_of(p, b0 + i * 32 + lane), extra) : 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) all += t[i];
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
-    return all;
-}
-
-// The request whose `per` items hold place x of the work, and the place where those begin; false behind the last.
-__device__ __forceinline__ bool find_request(const AttnParams &p, int extra, long long x, int per, int &b,
-                                             long long &first) {
-    const int lane = threadIdx.x & 31;
-    long long before = 0;
-    b = 0;
-    first = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const long long mine = b0 + lane < p.B ? (long long)work_of(tiles_of(p, b0 + lane), extra) * per : 0;
-        long long upto = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, upto, d);
-            if (lane >= d) upto += y;
-        }
-        upto += before;
-        const unsigned hit = __ballot_sync(0xffffffffu, x >= upto - mine && x < upto);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            b = b0 + src;
-            first = __shfl_sync(0xffffffffu, upto - mine, src);
-            return true;
-        }
-        before = __shfl_sync(0xffffffffu, upto, 31);
-    }
-    return false;
+// Work of a request's `per` items.
+__device__ __forceinline__ long long request_work(const AttnParams &p, int b, int extra, int per) {
+    return (long long)work_of(tiles_of(p, b), extra) * per;
 }
 
 // The items of a CTA's run, those of which it has no tile left out.
@@ -146,7 +106,7 @@ struct Walk {
         live = lo < hi;
         if (!live) return;
         long long first;
-        find_request(p, extra, lo, p.Hkv * blocks, b, first);
+        find_request(p.B, lo, b, first, [&](int x) { return request_work(p, x, extra, p.Hkv * blocks); });
         tiles = tiles_of(p, b);
         kv_len = p.cache.kv_lens[b];
         const int item = (int)((lo - first) / work_of(tiles, extra));
@@ -649,7 +609,7 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
         }
         __syncwarp();
     };
-    Walk w(p, S::kExtra, blocks, sum_work(p, S::kExtra) * p.Hkv * blocks);
+    Walk w(p, S::kExtra, blocks, sum_work(p.B, [&](int x) { return request_work(p, x, S::kExtra, p.Hkv * blocks); }));
     for (; w.live && ok; w.next(p), ++item) {
         Pages pages;
         pages.fetch(p.cache, w.b, w.kv_len, w.j0, lane);
