@@ -579,11 +579,12 @@ la_status la_attn_extend_workspace_size(int B, int T, int H, int Hkv, int D, int
 /*
  * la_attn_decode -- one token per request (row b of q and out), the request's last position.  A request with kv_lens[b]
  * 0 (a padded batch) sees nothing: its row is zero.
- *   workspace       device scratch, 16-byte aligned, of at least la_attn_verify_workspace_size() bytes with N = 1
- *                   (LA_ERR_INVALID otherwise): the keys are shared out evenly among the SMs, and a second launch
- *                   joins the requests that several of them shared.  Calls that share one must not overlap on the GPU.
- * Numerics: as la_attn_extend, with the weights as bf16 pairs hi + lo (2^-16) where at most 64 rows share a kv head's
- * keys (N * H / Hkv of a block of up to 128), as bf16 above.
+ *   workspace       device scratch, 16-byte aligned, of at least la_attn_verify_workspace_size() bytes with N = 1 and
+ *                   max_kvlen = max_pages * page_size (LA_ERR_INVALID otherwise): the keys are shared out evenly among
+ *                   the SMs, and a second launch joins the requests that several of them shared.  Calls that share one
+ *                   must not overlap on the GPU.
+ * Numerics: as la_attn_extend, with the weights as bf16 pairs hi + lo (2^-16) where N * H / Hkv, the rows that share a kv
+ * head's keys, is at most 64 (N = 1 here), as bf16 above.
  */
 la_status la_attn_decode(const la_bf16 *q, int64_t q_row_stride, const la_bf16 *k_pages, const la_bf16 *v_pages,
                          int64_t page_stride, int num_pages, int page_size, const int32_t *page_table, int max_pages,
@@ -604,10 +605,10 @@ la_status la_attn_verify_tree(const la_bf16 *q, int64_t q_row_stride, const la_b
                               la_stream stream);
 
 /*
- * la_attn_verify_workspace_size -- bytes of scratch la_attn_decode (N = 1) and la_attn_verify_tree need, whatever the
- * batch.  Host only.
+ * la_attn_verify_workspace_size -- bytes of scratch la_attn_decode (N = 1) and la_attn_verify_tree need for B requests
+ * of up to max_kvlen = max_pages * page_size positions.  Host only.
  */
-la_status la_attn_verify_workspace_size(int N, int H, int Hkv, int D, size_t *bytes);
+la_status la_attn_verify_workspace_size(int B, int N, int H, int Hkv, int D, int max_kvlen, size_t *bytes);
 
 /*
  * la_kv_commit -- after la_attn_verify_tree, the counterpart of la_commit_accepted: the keys and values of the drafts on the path to draft

@@ -124,7 +124,7 @@ def load():
                 ("la_attn_extend_workspace_size", [ip] * 7 + [ctypes.POINTER(sz)]),
                 ("la_attn_decode", [vp, i64] + cache + [vp, ip, vp, vp, ip, ip, ip, ip, f32, vp, sz, vp]),
                 ("la_attn_verify_tree", [vp, i64] + cache + [vp, ip, vp, vp, vp, ip, ip, ip, ip, ip, f32, vp, sz, vp]),
-                ("la_attn_verify_workspace_size", [ip] * 4 + [ctypes.POINTER(sz)]),
+                ("la_attn_verify_workspace_size", [ip] * 6 + [ctypes.POINTER(sz)]),
                 ("la_kv_commit", cache + [vp, ip, vp, vp, vp, vp, ip, ip, ip, ip, vp])):
             getattr(lib, name).argtypes = args
             getattr(lib, name).restype = ip
@@ -885,21 +885,24 @@ def attn_extend(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, out=None, 
 
 
 @functools.lru_cache(maxsize=1024)
-def attn_verify_workspace_size(N: int, H: int, Hkv: int, D: int) -> int:
-    """Bytes of scratch la_attn_decode (N = 1) and la_attn_verify_tree need, whatever the batch."""
+def attn_verify_workspace_size(B: int, N: int, H: int, Hkv: int, D: int, max_kvlen: int) -> int:
+    """Bytes of scratch la_attn_decode (N = 1) and la_attn_verify_tree need for B requests of up to max_kvlen (what a
+    row of the page table holds) positions."""
     n = ctypes.c_size_t(0)
-    _check("la_attn_verify_workspace_size", load().la_attn_verify_workspace_size(N, H, Hkv, D, ctypes.byref(n)))
+    _check("la_attn_verify_workspace_size",
+           load().la_attn_verify_workspace_size(B, N, H, Hkv, D, max_kvlen, ctypes.byref(n)))
     return int(n.value)
 
 
 def attn_decode(q, k_pages, v_pages, page_table, kv_lens, out=None, scale: float | None = None, workspace=None):
     """Attention of one token per request over a paged cache (la_attn_decode): q bf16 [B, H*128], the last of kv_lens[b]
     positions; returns out bf16 [B, H*128].  The other arguments are attn_extend's; workspace: uint8 scratch of
-    attn_verify_workspace_size(1, ...) bytes."""
+    attn_verify_workspace_size() bytes."""
     dev, T, H, Hkv, B, q_rs, cache, out, scale = _attn_args(q, k_pages, v_pages, page_table, kv_lens, out, scale)
     if T != B:
         raise ValueError(f"q must have a row per request, {B}, got {T}")
-    workspace, nbytes = _scratch(workspace, kv_lens, 0 if H % Hkv else attn_verify_workspace_size(1, H, Hkv, _HEAD_DIM))
+    workspace, nbytes = _scratch(workspace, kv_lens, 0 if H % Hkv else attn_verify_workspace_size(
+        B, 1, H, Hkv, _HEAD_DIM, cache[4] * cache[6]))
     with _on(dev):
         st = (_lib or load()).la_attn_decode(_ptr(q), q_rs, *cache, _ptr(kv_lens), _ptr(out), B, H, Hkv, _HEAD_DIM,
                                              scale, _ptr(workspace), nbytes, _stream_handle(dev))
@@ -920,7 +923,8 @@ def attn_verify_tree(q, k_pages, v_pages, page_table, kv_lens, parents, N: int, 
     if T != B * N:
         raise ValueError(f"q must have {N} rows per request, {B * N}, got {T}")
     _need_fast(parents, "parents", torch.int32, dev, (B, N))
-    workspace, nbytes = _scratch(workspace, kv_lens, 0 if H % Hkv else attn_verify_workspace_size(N, H, Hkv, _HEAD_DIM))
+    workspace, nbytes = _scratch(workspace, kv_lens, 0 if H % Hkv else attn_verify_workspace_size(
+        B, N, H, Hkv, _HEAD_DIM, cache[4] * cache[6]))
     with _on(dev):
         st = (_lib or load()).la_attn_verify_tree(_ptr(q), q_rs, *cache, _ptr(kv_lens), _ptr(parents), _ptr(out), B, N, H,
                                                   Hkv, _HEAD_DIM, scale, _ptr(workspace), nbytes, _stream_handle(dev))

@@ -835,14 +835,19 @@ la_status attn_verify(const la_bf16 *q, int64_t q_rs, const la_bf16 *k_pages, co
     st = attn_params(&p, &work, q, q_rs, c, out, B, (long long)B * N, H, Hkv, scale);
     if (st != LA_OK || !work) return st;
     if (tree && (!parents || !aligned4(parents))) return LA_ERR_INVALID;
-    if (!workspace || !aligned16(workspace) ||
-        (unsigned long long)workspace_bytes < la::attn_verify_ws_bytes(N, p.group))
+    const bool few = N * p.group <= la::kVerifyRows;
+    const la::AttnExtendPlan plan = la::plan_attn_extend(B, p.T, H, Hkv, N, (long long)max_pages * page_size);
+    const unsigned long long need = few ? la::attn_verify_ws_bytes(N * p.group) : plan.ws_bytes;
+    if (need > 0 && (!workspace || !aligned16(workspace) || (unsigned long long)workspace_bytes < need))
         return LA_ERR_INVALID;
     p.parents = tree ? parents : nullptr;
     p.N = N;
     p.ws = workspace;
+    p.max_seqlen = N;
+    p.split = plan.split;
     if ((st = error_word_ptr(&p.err)) != LA_OK) return st;
-    return launch_status(la::launch_attn_verify(p, static_cast<cudaStream_t>(stream)));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return launch_status(few ? la::launch_attn_verify(p, s) : la::launch_attn_extend(p, plan, s));
 }
 
 }  // namespace
@@ -953,10 +958,14 @@ la_status la_attn_extend(const la_bf16 *q, int64_t q_row_stride, const la_bf16 *
     return launch_status(la::launch_attn_extend(p, plan, static_cast<cudaStream_t>(stream)));
 }
 
-la_status la_attn_verify_workspace_size(int N, int H, int Hkv, int D, size_t *bytes) {
-    if (N < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || D < 1 || bytes == nullptr) return LA_ERR_INVALID;
+la_status la_attn_verify_workspace_size(int B, int N, int H, int Hkv, int D, int max_kvlen, size_t *bytes) {
+    if (B < 0 || N < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || D < 1 || max_kvlen < 0 || bytes == nullptr)
+        return LA_ERR_INVALID;
     if (D != la::kHeadDim || N > la::kMaxDrafts || H / Hkv > la::kMaxDrafts) return LA_ERR_UNSUPPORTED;
-    *bytes = (size_t)la::attn_verify_ws_bytes(N, H / Hkv);
+    const int rows = N * (H / Hkv);
+    *bytes = (size_t)(B == 0                      ? 0
+                      : rows <= la::kVerifyRows ? la::attn_verify_ws_bytes(rows)
+                                                  : la::plan_attn_extend(B, (long long)B * N, H, Hkv, N, max_kvlen).ws_bytes);
     return LA_OK;
 }
 

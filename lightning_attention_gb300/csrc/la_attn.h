@@ -38,7 +38,7 @@ struct AttnParams {
     const __nv_bfloat16 *q;      // rows of H heads; query head h reads kv head h / group
     long long q_rs;
     CacheParams cache;
-    const int32_t *cu_seqlens;   // [B + 1] (extend)
+    const int32_t *cu_seqlens;   // [B + 1] (extend), null: N rows per request
     const int32_t *parents;      // [B][N] (tree), null: single tokens
     __nv_bfloat16 *out;          // [T][H * 128]
     void *ws;
@@ -58,8 +58,10 @@ AttnExtendPlan plan_attn_extend(long long B, long long T, int H, int Hkv, long l
                                 long long max_kvlen);
 cudaError_t launch_attn_extend(const AttnParams &p, const AttnExtendPlan &plan, cudaStream_t stream);
 
-// N drafts (or one token) per request: the last N positions.
-unsigned long long attn_verify_ws_bytes(int N, int group);
+// N drafts (or one token) per request, the last N positions, N * group at most kVerifyRows; more go to
+// launch_attn_extend, with cu_seqlens null.
+constexpr int kVerifyRows = 64;
+unsigned long long attn_verify_ws_bytes(int rows);
 cudaError_t launch_attn_verify(const AttnParams &p, cudaStream_t stream);
 
 struct KvCommitParams {

@@ -1,7 +1,9 @@
 // la_attn_extend.cu -- softmax attention of packed prompts over a paged key/value cache (causal,
 // grouped heads): for query row i of a request, with the keys at and before its position,
 //     o_i = sum_j e^{s_ij - m_i} v_j / sum_j e^{s_ij - m_i},   s_ij = scale q_i . k_j
-// in one pass over the keys, m_i a running reference.
+// in one pass over the keys, m_i a running reference.  The same for trees of drafts (and single tokens) whose rows
+// -- drafts x query heads of a kv head -- are more than la_attn_verify.cu takes: a row sees the positions before the
+// drafts, its ancestors and itself.
 //
 // An item is two tiles of up to 128 rows -- consecutive tokens x the query heads of one kv head, so
 // that the heads of a group share its keys -- and the tiles of 128 keys that they see.  Per key tile and row
@@ -55,13 +57,17 @@ constexpr int kPieceFloats = kItemRows * (kHeadDim + 2);
 struct Rec {
     int b, t0, n, kv_len, kvh, tok0;  // request, its first row, tokens, positions; kv head; first token
     int j0, j1, whole;             // tiles of keys that the CTA takes (none: the end of its run), all that there are
+    int sound;                     // no parent out of range
 };
+
+constexpr uint8_t kNoParent = 255;
 
 struct Bars {
     uint64_t full[kSlots], empty[kSlots];
     uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], o_free[2], drain;
     uint64_t item_full[kItems], item_empty[kItems];
     Rec items[kItems];
+    uint8_t parent[kItems][kMaxDrafts];  // of a tree's drafts; kNoParent: the context
     float swap[2][2][kRowTile];  // between a row's threads: [row tile][half][row]
     int loads[2];  // of keys and of values, at the end
     uint32_t tmem_base;
@@ -76,10 +82,15 @@ struct Request {
     int t0, n, kv_len;
 };
 __device__ __forceinline__ bool request_of(const AttnParams &p, int b, Request &r) {
+    r.kv_len = p.cache.kv_lens[b];
+    if (p.cu_seqlens == nullptr) {  // N drafts each
+        r.t0 = b * p.N;
+        r.n = p.N;
+        return r.kv_len >= p.N && r.kv_len <= (long long)p.cache.max_pages * p.cache.page_size;
+    }
     r.t0 = p.cu_seqlens[b];
     const int t1 = p.cu_seqlens[b + 1];
     r.n = t1 - r.t0;
-    r.kv_len = p.cache.kv_lens[b];
     return r.t0 >= 0 && t1 >= r.t0 && t1 <= p.T && r.n <= p.max_seqlen && r.kv_len >= r.n &&
            r.kv_len <= (long long)p.cache.max_pages * p.cache.page_size;
 }
@@ -106,7 +117,7 @@ __device__ __forceinline__ int items_of(const AttnParams &p, const Request &r) {
 __device__ __forceinline__ long long request_work(const AttnParams &p, int b, bool report) {
     Request r;
     if (request_of(p, b, r)) return work_of(p, r, items_of(p, r)) * p.Hkv;
-    if (report) atomicOr(p.err, ERR_BIT_SEQLENS);
+    if (report && (p.cu_seqlens != nullptr || r.kv_len != 0)) atomicOr(p.err, ERR_BIT_SEQLENS);
     return 0;
 }
 
@@ -207,11 +218,22 @@ __device__ __forceinline__ uint32_t columns_seen(int last) {
     return last >= 31 ? 0xffffffffu : last < 0 ? 0u : (2u << last) - 1u;
 }
 
+// 32 columns of which the first is draft d (those before draft 0 are seen by every row): a bit for each that is in `up`.
+__device__ __forceinline__ uint32_t drafts_seen(const uint32_t (&up)[4], int d) {
+    if (d <= -32) return 0xffffffffu;
+    if (d < 0) return (up[0] << -d) | ((1u << -d) - 1u);
+    const int q = d >> 5;
+    const uint32_t lo = q == 0 ? up[0] : q == 1 ? up[1] : q == 2 ? up[2] : q == 3 ? up[3] : 0u;
+    const uint32_t hi = q == 0 ? up[1] : q == 1 ? up[2] : q == 2 ? up[3] : 0u;
+    return __funnelshift_r(lo, hi, d & 31);
+}
+
 // Half a tile of a row: its weights against the reference as bf16 pairs in w, their sums in l (four partial ones),
-// the largest exponent returned.  Columns past `last` are not seen; lo_last and hi_last: its least and largest value in
-// the warp.  Scalar arithmetic: a packed fma.f32x2 takes 4.3 cycles a warp, two fma.f32 2.6.
-template <bool kMask>
-__device__ __forceinline__ float weigh(uint32_t ts, int last, int lo_last, int hi_last, float c, float neg_m,
+// the largest exponent returned.  seen(i): the columns of part i (32 of them) that the row sees, a bit each; all rows of
+// the warp see columns up to lo_last, none one past hi_last.  Scalar arithmetic: a packed fma.f32x2 takes 4.3 cycles a
+// warp, two fma.f32 2.6.
+template <bool kMask, class Seen>
+__device__ __forceinline__ float weigh(uint32_t ts, Seen seen, int lo_last, int hi_last, float c, float neg_m,
                                        uint32_t (&w)[32], float (&l)[4]) {
     float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -225,10 +247,10 @@ __device__ __forceinline__ float weigh(uint32_t ts, int last, int lo_last, int h
         tmem_ld32(ts + i * 32, x);
         tmem_ld_wait_regs(x);
         if (kMask && lo_last < i * 32 + 31) {
-            const uint32_t seen = columns_seen(last - i * 32);
+            const uint32_t bits = seen(i);
 #pragma unroll
             for (int y = 0; y < 32; ++y)
-                if (!(seen & (1u << y))) x[y] = 0xff800000u;
+                if (!(bits & (1u << y))) x[y] = 0xff800000u;
         }
 #pragma unroll
         for (int y = 0; y < 16; ++y) {
@@ -245,7 +267,8 @@ __device__ __forceinline__ float weigh(uint32_t ts, int last, int lo_last, int h
 }
 
 // The largest score of half a row's tile.
-__device__ __forceinline__ float largest(uint32_t ts, int last, int lo_last, int hi_last) {
+template <class Seen>
+__device__ __forceinline__ float largest(uint32_t ts, Seen seen, int lo_last, int hi_last) {
     float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -254,10 +277,10 @@ __device__ __forceinline__ float largest(uint32_t ts, int last, int lo_last, int
         tmem_ld32(ts + i * 32, x);
         tmem_ld_wait_regs(x);
         if (lo_last < i * 32 + 31) {
-            const uint32_t seen = columns_seen(last - i * 32);
+            const uint32_t bits = seen(i);
 #pragma unroll
             for (int y = 0; y < 32; ++y)
-                if (!(seen & (1u << y))) x[y] = 0xff800000u;
+                if (!(bits & (1u << y))) x[y] = 0xff800000u;
         }
 #pragma unroll
         for (int y = 0; y < 32; y += 2)
@@ -302,6 +325,7 @@ __device__ __forceinline__ void quad_transpose(uint4 (&x)[4], int lane) {
     }
 }
 
+template <bool kTree>
 __device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, int warp, int lane, const Waiter &wait) {
     const int stage = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, pair = stage * 4 + quarter;
     const uint32_t lanes = (uint32_t)quarter << 21;  // in the address's upper half
@@ -309,32 +333,56 @@ __device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, in
     const int row = quarter * 32 + lane, row_tok = kRowTile / p.group;
     const int tok_of = stage * row_tok + row / p.group, head = row % p.group;
     const float c = p.scale_log2;
+    if (p.cu_seqlens == nullptr) {  // rows without keys: a request of no positions
+        for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+            if (p.cache.kv_lens[b] == 0)
+                for (int i = threadIdx.x; i < p.N * p.H * (kHeadDim / 8); i += kMmaWarp * 32)
+                    reinterpret_cast<uint4 *>(p.out + (long long)b * p.N * p.H * kHeadDim)[i] = make_uint4(0, 0, 0, 0);
+    }
     bool ok = true;
     uint32_t tile = 0, item = 0;
     for (;; ++item) {
         ok = ok && __all_sync(0xffffffffu, wait(&bars->item_full[item % kItems], (item / kItems) & 1));
         Rec it = bars->items[item % kItems];
         if (pair_any(pair, !ok) || it.j1 <= it.j0) return;
+        const int tok = it.tok0 + tok_of;
+        const bool inside = row < row_tok * p.group && tok < it.n, valid = inside && it.sound;
+        // Last column of this half, counted from the first key, that the row sees (rows that are not written take any),
+        // and all rows and any row of the warp do.
+        int limit = it.kv_len - it.n + (inside ? tok : it.n - 1) - half * 64, lo_limit, hi_limit;
+        uint32_t up[4] = {0, 0, 0, 0};  // drafts that it sees, a bit each
+        if constexpr (kTree) {
+            for (uint32_t a = inside ? tok : 0; a != kNoParent; a = bars->parent[item % kItems][a])
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if ((a >> 5) == i) up[i] |= 1u << (a & 31);
+            limit = it.kv_len - it.n - half * 64;  // where the drafts begin
+            lo_limit = limit - 1;
+            hi_limit = limit + it.n - 1;
+        } else {
+            lo_limit = __reduce_min_sync(0xffffffffu, limit);
+            hi_limit = __reduce_max_sync(0xffffffffu, limit);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->item_empty[item % kItems]);
-        const int tok = it.tok0 + tok_of;
-        const bool valid = row < row_tok * p.group && tok < it.n;
-        // last position that the row sees; rows that are not written take any
-        const int limit = it.kv_len - it.n + (valid ? tok : it.n - 1) - half * 64;
-        const int lo_limit = __reduce_min_sync(0xffffffffu, limit), hi_limit = __reduce_max_sync(0xffffffffu, limit);
         float neg_m = kUnseen;
         float l4[4] = {0.f, 0.f, 0.f, 0.f};
         for (int j = it.j0; j < it.j1; ++j, ++tile) {
             ok = ok && __all_sync(0xffffffffu, wait(&bars->s_full[stage], tile & 1));
             tc_fence_after();
-            // of this half's columns up to `last` are seen
             const int last = limit - j * kKeyTile, lo_last = lo_limit - j * kKeyTile, hi_last = hi_limit - j * kKeyTile;
+            auto seen = [&](int i) {
+                if constexpr (kTree)
+                    return drafts_seen(up, i * 32 - last);
+                else
+                    return columns_seen(last - i * 32);
+            };
             uint32_t w[32];
             bool behind = true;
             if (j > it.j0) {
                 float sum[4] = {l4[0], l4[1], l4[2], l4[3]};
-                const float top = lo_last < 63 ? weigh<true>(ts + half * 64, last, lo_last, hi_last, c, neg_m, w, sum)
-                                               : weigh<false>(ts + half * 64, last, lo_last, hi_last, c, neg_m, w, sum);
+                const float top = lo_last < 63 ? weigh<true>(ts + half * 64, seen, lo_last, hi_last, c, neg_m, w, sum)
+                                               : weigh<false>(ts + half * 64, seen, lo_last, hi_last, c, neg_m, w, sum);
                 behind = pair_any(pair, top > 8.f || !ok);  // S has been read by both from here on
                 if (!behind) {
 #pragma unroll
@@ -342,7 +390,7 @@ __device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, in
                 }
             }
             if (behind) {
-                float top = largest(ts + half * 64, last, lo_last, hi_last);
+                float top = largest(ts + half * 64, seen, lo_last, hi_last);
                 bars->swap[stage][half][row] = top;
                 if (pair_any(pair, !ok)) return;
                 top = fmaxf(top, bars->swap[stage][half ^ 1][row]) * c;
@@ -364,7 +412,7 @@ __device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, in
                         tmem_st32(to + i * 32, o);
                     }
                 }
-                weigh<true>(ts + half * 64, last, lo_last, hi_last, c, neg_m, w, l4);
+                weigh<true>(ts + half * 64, seen, lo_last, hi_last, c, neg_m, w, l4);
                 pair_any(pair, false);
             }
             tmem_st32(ts + half * 32, w);
@@ -571,6 +619,20 @@ __device__ void drain_ring(Bars *bars, const Waiter &wait) {
     }
 }
 
+// Parents of request b's drafts 4 lane .. 4 lane + 3, kNoParent for the context and for what is out of range; false if
+// there is any of those.
+__device__ __forceinline__ bool parents_of(const AttnParams &p, int b, int lane, int (&up)[4]) {
+    bool sound = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = 4 * lane + i, x = t < p.N ? p.parents[(long long)b * p.N + t] : -1;
+        const bool good = x >= 0 && x < t;
+        sound &= good || x == -1;
+        up[i] = good ? x : kNoParent;
+    }
+    return __all_sync(0xffffffffu, sound);
+}
+
 __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUtensorMap *tk, Bars *bars, uint8_t *sm,
                           int lane, const Waiter &wait) {
     const int row_tok = kRowTile / p.group;
@@ -602,6 +664,18 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
         r.j0 = wk.j0;
         r.j1 = wk.j1;
         r.whole = wk.j0 == 0 && wk.j1 == it.tiles;
+        r.sound = 1;
+        if (p.parents) {
+            int up[4];
+            r.sound = parents_of(p, it.b, lane, up);
+            if (!r.sound && lane == 0) atomicOr(p.err, ERR_BIT_PARENTS);
+            if (item >= kItems)  // the slot's last item has been read
+                ok = ok && __all_sync(0xffffffffu, wait(&bars->item_empty[item % kItems], (item / kItems - 1) & 1));
+            if (ok)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) bars->parent[item % kItems][4 * lane + i] = (uint8_t)up[i];
+            __syncwarp();
+        }
         publish(r);
         for (int j = wk.j0; j < wk.j1 && ok; ++j) {
             const int page = pages.check(p.cache, p.err);
@@ -621,6 +695,8 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
             asked = item + 1;
         }
     }
+    int up[4];
+    if (p.parents && wk.tail_tiles > 0 && !parents_of(p, wk.tail.b, lane, up)) wk.tail_tiles = 0;  // left as it was
     if (p.split && lane == 0) {
         const Item &it = wk.tail;
         static_cast<Tail *>(p.ws)[blockIdx.x] = {wk.runs, it.at, it.size, wk.tail_tiles, it.b, it.kvh, it.tok0, it.r.t0, it.r.n};
@@ -653,6 +729,7 @@ __device__ void value_role(const AttnParams &p, const CUtensorMap *tv, Bars *bar
     if (lane == 0) bars->loads[1] = ring.count;
 }
 
+template <bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_extend_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const AttnParams p) {
@@ -701,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Waiter wait{p.wait_limit_ns, p.err};
     if (warp < kMmaWarp) {
         reg_inc<kRegsSoftmax>();
-        softmax_role(p, bars, tbase, warp, lane, wait);
+        softmax_role<kTree>(p, bars, tbase, warp, lane, wait);
     } else {
         reg_dec<kRegsRest>();
         if (warp == kMmaWarp)
@@ -827,12 +904,14 @@ cudaError_t launch_attn_extend(const AttnParams &p, const AttnExtendPlan &plan, 
         std::lock_guard<std::mutex> lock(mu);
         if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
         if (!configured[dev]) {
-            e = cudaFuncSetAttribute(attn_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+            e = cudaFuncSetAttribute(attn_extend_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+            if (e != cudaSuccess) return e;
+            e = cudaFuncSetAttribute(attn_extend_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
             if (e != cudaSuccess) return e;
             configured[dev] = true;
         }
     }
-    e = launch_pdl(attn_extend_kernel, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, tq, tk, tv, p);
+    e = launch_pdl(p.parents ? attn_extend_kernel<true> : attn_extend_kernel<false>, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, tq, tk, tv, p);
     if (e != cudaSuccess || !p.split || ctas == 1) return e;
     return launch_pdl(attn_join_kernel, dim3((unsigned)(ctas - 1), 8), dim3(256), 0, stream, p);
 }

@@ -2,7 +2,8 @@
 // cache.  The N drafts of a request are its last N positions; draft t sees the positions before them, its
 // ancestors and itself:
 //     o_r = sum_j e^{s_rj - m_r} v_j / sum_j e^{s_rj - m_r},   s_rj = scale q_r . k_j
-// for the R = (drafts) x (query heads of a kv head) rows r that share the keys, each key read once.
+// for the R = (drafts) x (query heads of a kv head) rows r that share the keys, R at most 64 (with more, what is there to
+// compute outweighs the loads: la_attn_extend.cu), each key read once.
 //
 // Bound by HBM: 512 bytes a key and kv head.  The work is the sequence of all tiles of 128 keys, request by
 // request and head by head, cut into equal runs, one CTA per SM each: the SMs finish together whatever the
@@ -10,10 +11,10 @@
 // launch joins in a fixed order.
 //
 // With few rows the keys take the 128 lanes of the tensor cores: S^T = K Q^T and O^T += V^T P^T, both with
-// N = R (padded to 16, 32, 64 or 128), K and V as they lie in their pages.  Two threads share a key in the
-// softmax, half of the rows each, and a column of v in the result.  The reference m_r is that of the first tile and follows only
-// when a score passes it by more than 2^8, so that a tile takes no maximum, one test.  P goes into shared memory as bf16 pairs hi + lo (off by at
-// most 2^-16), which the idle tensor cores take at no cost.
+// N = R (padded to 16, 32 or 64), K and V as they lie in their pages.  Two threads share a key in the
+// softmax, half of the rows each, and a column of v in the result.  The reference m_r is that of the first tile and
+// follows only when a score passes it by more than 2^8, so that a tile takes no maximum, one test.  P goes into
+// shared memory as bf16 pairs hi + lo (off by at most 2^-16), which the idle tensor cores take at no cost.
 #include <string.h>
 
 #include <algorithm>
@@ -26,33 +27,32 @@ namespace {
 
 using namespace attn;
 
-constexpr int kThreads = 352;  // warps 0-7: softmax, 8: MMAs, 9: loads of queries and keys, 10: of values
+constexpr int kThreads = 384;  // warps 0-7: softmax, 8: MMAs, 9: loads of queries and keys, 10: of values, 11: none
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kValueWarp = 10;
+constexpr int kRegsSoftmax = 208, kRegsRest = 88;  // a thread, by warp groups, with 64 rows
+static_assert(2 * kRegsSoftmax + kRegsRest <= 3 * 168, "register split");
 constexpr int kBarSoftmax = 1;
+constexpr int kMaxRuns = 2 * kAttnCtas;
 constexpr float kUnseen = 1e30f;  // minus the reference of a row that has seen no key: any score passes it, -inf stays
 
-// What fits into 227 KB.  With 128 rows P is one bf16 (2^-9 of each weight): the products with the second
-// part would take the tensor cores as long as HBM takes for the tile.
+// Up to 16 rows two CTAs share an SM, so that one works where the other waits at an item's beginning or end.
 template <int RP>
 struct Shape {
-    static constexpr int kQBufs = RP <= 64 ? 2 : 1, kPBufs = RP <= 32 ? 2 : 1;
-    static constexpr int kSlots = RP <= 32 ? 5 : 4;       // tiles of keys and values
-    static constexpr int kParts = RP <= 64 ? 2 : 1;       // of P: hi, lo
-    static constexpr int kExtra = RP <= 32 ? 1 : 2;       // tiles' time that an item takes besides its own
-    static constexpr bool kOnes = RP > 64;                // sums of P by the tensor cores, not in registers
-    static constexpr uint32_t kQBytes = RP * 256, kPart = kKeyTile * RP * 2, kPBytes = kParts * kPart;
+    static constexpr int kPerSm = RP == 16 ? 2 : 1;
+    static constexpr int kQBufs = RP == 16 ? 1 : 2, kPBufs = RP == 32 ? 2 : 1;
+    static constexpr int kSlots = RP == 16 ? 3 : RP == 32 ? 5 : 4;  // tiles of keys and values
+    static constexpr int kExtra = RP <= 32 ? 1 : 2;  // tiles' time that an item takes besides its own
+    static constexpr uint32_t kQBytes = RP * 256, kPart = kKeyTile * RP * 2, kPBytes = 2 * kPart;
     static constexpr uint32_t kOffKV = 0;
     static constexpr uint32_t kOffQ = kOffKV + kSlots * kTileBytes;
     static constexpr uint32_t kOffP = kOffQ + kQBufs * kQBytes;
-    static constexpr uint32_t kOffOnes = kOffP + kPBufs * kPBytes;
-    static constexpr uint32_t kOffBars = kOffOnes + (kOnes ? 4096 : 0);
-    // columns of tensor memory: S twice, O, sums
-    static constexpr uint32_t kTmO = 2 * RP, kTmL = 3 * RP, kTmCols = 4 * RP;
+    static constexpr uint32_t kOffBars = kOffP + kPBufs * kPBytes;
+    static constexpr uint32_t kTmO = 2 * RP, kTmCols = 4 * RP;  // columns of tensor memory: S twice, O
 };
 
 // What a CTA's warps have to know of an item, published by the warp that loads the keys; no tiles: the run's end.
 struct Rec {
-    int b, kvh, rb, kv_len, j0, j1, whole;
+    int b, kvh, kv_len, j0, j1, whole;
 };
 constexpr int kItems = 4;  // items ahead
 
@@ -61,12 +61,12 @@ struct Bars {
     uint64_t item_full[kItems], item_empty[kItems];
     Rec items[kItems];
     uint64_t full[5], empty[5];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], p_empty[2], pv_done, o_full, o_free, drain;
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], p_empty[2], o_full, o_free, drain;
     alignas(16) float neg_m[RP];        // minus the references, in log 2
     alignas(16) float factor[RP];
     float top[4][RP];
     uint8_t tok_of[RP];
-    uint32_t below[kMaxDrafts][4];      // below[a] bit t: draft t is a or descends from it
+    uint32_t below[kVerifyRows][2];     // below[a] bit t: draft t is a or descends from it
     int loads[2];                       // of keys and of values, at the end
     uint32_t tmem_base;
 };
@@ -78,49 +78,45 @@ __device__ __forceinline__ int tiles_of(const AttnParams &p, int b) {
     return (kv + kKeyTile - 1) / kKeyTile;
 }
 
-// An item is a (request, kv head, block of drafts); its work is its tiles and `extra` more for its beginning and end.
+// An item is a (request, kv head); its work is its tiles and `extra` more for its beginning and end.
 __device__ __forceinline__ int work_of(int tiles, int extra) { return tiles ? tiles + extra : 0; }
 // The tile at which the first `done` of an item's work end.
 __device__ __forceinline__ int cut(long long done, int tiles) {
     return done <= 0 ? 0 : (int)min((long long)tiles, done);
 }
 
-// Work of a request's `per` items.
-__device__ __forceinline__ long long request_work(const AttnParams &p, int b, int extra, int per) {
-    return (long long)work_of(tiles_of(p, b), extra) * per;
+// Work of a request.
+__device__ __forceinline__ long long request_work(const AttnParams &p, int b, int extra) {
+    return (long long)work_of(tiles_of(p, b), extra) * p.Hkv;
 }
 
 // The items of a CTA's run, those of which it has no tile left out.
 struct Walk {
-    int b, kvh, rb, tiles, j0, j1, kv_len, blocks, extra;
+    int b, kvh, tiles, j0, j1, kv_len, extra;
     Runs runs;
     long long at, lo, hi;  // where the item begins; the run
     bool live;
-    int tail_tiles = 0, tail_b, tail_kvh, tail_rb;  // the item inside which the run ends, if an earlier one does not
+    int tail_tiles = 0, tail_b, tail_kvh;  // the item inside which the run ends, if an earlier one does not
     long long tail_at;
     // one warp
-    __device__ __forceinline__ Walk(const AttnParams &p, int extra_, int blocks_, long long all)
-        : blocks(blocks_), extra(extra_), runs(all, (int)max(1ll, min((long long)gridDim.x, all))) {
+    __device__ __forceinline__ Walk(const AttnParams &p, int extra_, long long all)
+        : extra(extra_), runs(all, (int)max(1ll, min((long long)gridDim.x, all))) {
         lo = runs.start(min((int)blockIdx.x, runs.ctas));
         hi = runs.start(min((int)blockIdx.x + 1, runs.ctas));
         live = lo < hi;
         if (!live) return;
         long long first;
-        find_request(p.B, lo, b, first, [&](int x) { return request_work(p, x, extra, p.Hkv * blocks); });
+        find_request(p.B, lo, b, first, [&](int x) { return request_work(p, x, extra); });
         tiles = tiles_of(p, b);
         kv_len = p.cache.kv_lens[b];
-        const int item = (int)((lo - first) / work_of(tiles, extra));
-        kvh = item / blocks;
-        rb = item - kvh * blocks;
-        at = first + (long long)item * work_of(tiles, extra);
+        kvh = (int)((lo - first) / work_of(tiles, extra));
+        at = first + (long long)kvh * work_of(tiles, extra);
         settle(p);
     }
     __device__ __forceinline__ void advance(const AttnParams &p) {
         at += work_of(tiles, extra);
         live = at < hi;
-        if (!live || ++rb < blocks) return;
-        rb = 0;
-        if (++kvh < p.Hkv) return;
+        if (!live || ++kvh < p.Hkv) return;
         kvh = 0;
         do {
             tiles = tiles_of(p, ++b);  // at < hi: a request with keys follows
@@ -135,7 +131,6 @@ struct Walk {
                 tail_tiles = tiles;
                 tail_b = b;
                 tail_kvh = kvh;
-                tail_rb = rb;
                 tail_at = at;
             }
             if (j0 < j1) return;
@@ -173,10 +168,7 @@ __device__ __forceinline__ float redux_max(float x) {
 template <int RP>
 __device__ bool build_tree(const AttnParams &p, Bars<RP> *bars, int b, int tid) {
     softmax_sync();  // the last request's table is not read any more
-    if (tid < kMaxDrafts) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) bars->below[tid][i] = 0;
-    }
+    if (tid < kVerifyRows) bars->below[tid][0] = bars->below[tid][1] = 0;
     softmax_sync();
     bool bad = false;
     if (tid < p.N) {
@@ -234,7 +226,7 @@ __device__ __forceinline__ void tmem_put(uint32_t at, const float (&x)[n]) {
 // Two threads a key: warps 0-3 have the first half of the rows, warps 4-7 the other.
 template <int RP>
 __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint32_t tbase, int warp, int lane,
-                             int tok_block, const Waiter &wait) {
+                             const Waiter &wait) {
     using S = Shape<RP>;
     constexpr int R = RP / 2;  // rows of a thread
     const int tid = warp * 32 + lane, key = tid & 127, half = warp >> 2;
@@ -253,17 +245,15 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
     }
     int tile = 0, tree_of = -1;
     bool ok = true, sound = true;
-    float sum[S::kOnes ? 1 : R];  // of this thread's key
+    float sum[R];  // of this thread's key
     for (int item = 0;; ++item) {
         ok = ok && __all_sync(0xffffffffu, wait(&bars->item_full[item % kItems], (uint32_t)(item / kItems) & 1));
         const Rec w = bars->items[item % kItems];
         if (softmax_any(!ok) || w.j1 <= w.j0) return;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->item_empty[item % kItems]);
-        if (!S::kOnes) {
 #pragma unroll
-            for (int r = 0; r < R; ++r) sum[S::kOnes ? 0 : r] = 0.f;
-        }
+        for (int r = 0; r < R; ++r) sum[r] = 0.f;
         if (p.parents && tree_of != w.b) {
             sound = build_tree(p, bars, w.b, tid);
             if (!sound && tid == 0) atomicOr(p.err, ERR_BIT_PARENTS);
@@ -284,13 +274,11 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
 #pragma unroll
                     for (int r = 0; r < R; ++r) s[r] = -INFINITY;
                 } else if (d >= 0 && p.parents) {
-                    uint32_t see[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) see[i] = bars->below[d][i];
+                    const uint32_t see[2] = {bars->below[d][0], bars->below[d][1]};
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
-                        const int t = min(w.rb * tok_block + bars->tok_of[r0 + r], kMaxDrafts - 1);
-                        const uint32_t word = t < 64 ? (t < 32 ? see[0] : see[1]) : (t < 96 ? see[2] : see[3]);
+                        const int t = min((int)bars->tok_of[r0 + r], kVerifyRows - 1);
+                        const uint32_t word = t < 32 ? see[0] : see[1];
                         if (!((word >> (t & 31)) & 1u)) s[r] = -INFINITY;
                     }
                 }
@@ -335,23 +323,18 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
                 }
                 softmax_sync();
                 exponents();
-                if (!S::kOnes) {
 #pragma unroll
-                    for (int r = 0; r < R; ++r) sum[S::kOnes ? 0 : r] *= bars->factor[r0 + r];
-                }
-                if (!first) {  // O and the sums, once the last tile is in them
-                    ok = __all_sync(0xffffffffu, wait(&bars->pv_done, (uint32_t)(tile - 1) & 1));
+                for (int r = 0; r < R; ++r) sum[r] *= bars->factor[r0 + r];
+                if (!first) {  // O, once the last tile is in it
+                    ok = __all_sync(0xffffffffu, wait(&bars->p_empty[(tile - 1) % S::kPBufs],
+                                                      (uint32_t)((tile - 1) / S::kPBufs) & 1));
                     tc_fence_after();
                     if (ok) {
+                        float o[R];
+                        tmem_get<R>(tbase + lanes + S::kTmO + r0, o);
 #pragma unroll
-                        for (int x = 0; x < (S::kOnes ? 2 : 1); ++x) {
-                            float o[R];
-                            const uint32_t at = tbase + lanes + (x ? S::kTmL : S::kTmO) + r0;
-                            tmem_get<R>(at, o);
-#pragma unroll
-                            for (int r = 0; r < R; ++r) o[r] *= bars->factor[r0 + r];
-                            tmem_put<R>(at, o);
-                        }
+                        for (int r = 0; r < R; ++r) o[r] *= bars->factor[r0 + r];
+                        tmem_put<R>(tbase + lanes + S::kTmO + r0, o);
                     }
                 }
             }
@@ -366,20 +349,16 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
 #pragma unroll
                 for (int x = 0; x < 8; x += 2) {
                     const float e0 = ex2z(s[g + x]), e1 = ex2z(s[g + x + 1]);
-                    if (!S::kOnes) {
-                        sum[S::kOnes ? 0 : g + x] += e0;
-                        sum[S::kOnes ? 0 : g + x + 1] += e1;
-                    }
+                    sum[g + x] += e0;
+                    sum[g + x + 1] += e1;
                     const uint32_t h = pack_bf16x2(e0, e1);
                     hi[x / 2] = h;
-                    if (S::kParts == 2)
-                        lo[x / 2] = pack_bf16x2(e0 - __uint_as_float(h << 16), e1 - __uint_as_float(h & 0xffff0000u));
+                    lo[x / 2] = pack_bf16x2(e0 - __uint_as_float(h << 16), e1 - __uint_as_float(h & 0xffff0000u));
                 }
                 const int row = r0 + g;
                 uint8_t *at = ph + (row >> 4) * 4096 + (turn ^ ((row & 8) ? 16u : 0u));
                 *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                if (S::kParts == 2)
-                    *reinterpret_cast<uint4 *>(at + S::kPart) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                *reinterpret_cast<uint4 *>(at + S::kPart) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
             fence_proxy_async_smem();
             tc_fence_before();
@@ -388,52 +367,47 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
         }
         if (!ok) break;
         // the item's sums: over the lanes, each step with half the rows, then over the warps
-        if (!S::kOnes) {
-            int row = r0;
+        int row = r0;
 #pragma unroll
-            for (int d = 16, n = R; d > 0; d >>= 1) {
-                if (n > 1) {
-                    n >>= 1;
-                    const bool up = (lane & d) != 0;
-                    if (up) row += n;
+        for (int d = 16, n = R; d > 0; d >>= 1) {
+            if (n > 1) {
+                n >>= 1;
+                const bool up = (lane & d) != 0;
+                if (up) row += n;
 #pragma unroll
-                    for (int i = 0; i < R / 2; ++i)
-                        if (i < n) {
-                            const float mine = up ? sum[i + n] : sum[i], other = up ? sum[i] : sum[i + n];
-                            sum[i] = mine + __shfl_xor_sync(0xffffffffu, other, d);
-                        }
-                } else {
-                    sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], d);
-                }
+                for (int i = 0; i < R / 2; ++i)
+                    if (i < n) {
+                        const float mine = up ? sum[i + n] : sum[i], other = up ? sum[i] : sum[i + n];
+                        sum[i] = mine + __shfl_xor_sync(0xffffffffu, other, d);
+                    }
+            } else {
+                sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], d);
             }
-            bars->top[warp & 3][row] = sum[0];
-            softmax_sync();
         }
+        bars->top[warp & 3][row] = sum[0];
+        softmax_sync();
         // this thread holds column `key` of v
         ok = __all_sync(0xffffffffu, wait(&bars->o_full, (uint32_t)item & 1));
         tc_fence_after();
-        const int toks = min(tok_block, p.N - w.rb * tok_block), rows = toks * p.group;
+        const int rows = p.N * p.group;
         const long long piece = 2ll * blockIdx.x + (w.j0 == 0 ? 1 : 0);
-        float *po = reinterpret_cast<float *>(static_cast<Tail *>(p.ws) + kAttnCtas) + piece * RP * (kHeadDim + 2);
+        float *po = reinterpret_cast<float *>(static_cast<Tail *>(p.ws) + kMaxRuns) + piece * RP * (kHeadDim + 2);
         if (ok) {
             float o[R], l[R];
             tmem_get<R>(tbase + lanes + S::kTmO + r0, o);
-            if (S::kOnes) tmem_get<R>(tbase + lanes + S::kTmL + r0, l);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->o_free);
-            if (!S::kOnes) {
 #pragma unroll
-                for (int r = 0; r < R; ++r)
-                    l[r] = (bars->top[0][r0 + r] + bars->top[1][r0 + r]) + (bars->top[2][r0 + r] + bars->top[3][r0 + r]);
-            }
+            for (int r = 0; r < R; ++r)
+                l[r] = (bars->top[0][r0 + r] + bars->top[1][r0 + r]) + (bars->top[2][r0 + r] + bars->top[3][r0 + r]);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 if (r0 + r >= rows || !sound) break;
                 const int tok = bars->tok_of[r0 + r];
                 if (w.whole) {
                     const int head = w.kvh * p.group + r0 + r - tok * p.group;
-                    p.out[(((long long)w.b * p.N + w.rb * tok_block + tok) * p.H + head) * kHeadDim + key] =
+                    p.out[(((long long)w.b * p.N + tok) * p.H + head) * kHeadDim + key] =
                         __float2bfloat16_rn(l[r] == 0.f ? 0.f : o[r] / l[r]);
                 } else {
                     po[(r0 + r) * kHeadDim + key] = o[r];
@@ -458,11 +432,10 @@ __device__ void mma_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint3
     using S = Shape<RP>;
     const uint32_t id_s = idesc_bf16_f32(128, RP, false, false);
     const uint32_t id_o = idesc_bf16_f32(128, RP, true, true);
-    const uint32_t id_l = idesc_bf16_f32(128, RP, false, true);
     const uint64_t high = sdesc_sw128(0, 0, 1024), high32 = sdesc_sw32(0, 0, 256);
     const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(sm), 0) >> 4;
     const uint32_t kv_base = base + (S::kOffKV >> 4), q_base = base + (S::kOffQ >> 4);
-    const uint32_t p_base = base + (S::kOffP >> 4), ones = base + (S::kOffOnes >> 4) + (1u << 16);
+    const uint32_t p_base = base + (S::kOffP >> 4);
     bool ok = true;
     int slot = 0, qb = 0, pb = 0;  // the next tile, Q and P to come, and the parities of their barriers
     uint32_t slot_par = 0, q_par = 0, p_par = 0;
@@ -487,7 +460,6 @@ __device__ void mma_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint3
                 mma_bf16(tbase + s_buf * RP, high | (a + (k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2),
                          high | (b + (k >> 2) * (S::kQBytes >> 5) + (k & 3) * 2), id_s, k > 0);
             mma_commit(&bars->s_full[s_buf]);
-            mma_commit(&bars->empty[slot]);
             if (last) mma_commit(&bars->q_empty[qb]);
         }
         __syncwarp();
@@ -512,7 +484,11 @@ __device__ void mma_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint3
     };
     int item = 0;
     read_item(0);
-    if (j0 < j1) scores(true, j1 - j0 == 1);
+    if (j0 < j1) {
+        scores(true, j1 - j0 == 1);
+        if (elect()) mma_commit(&bars->empty[0]);
+        __syncwarp();
+    }
     while (j0 < j1 && ok) {
         const int from = j0, to = j1;
         const int end = kv_len % p.cache.page_size, last = (kv_len - 1) / kKeyTile;
@@ -521,10 +497,12 @@ __device__ void mma_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint3
             const int sv = slot;  // this tile's values, then the next tile's keys
             const uint32_t sv_par = slot_par;
             next_slot();
+            const int sk = slot;
             // the next tile's scores run under this one's softmax; its S was read before the P before was full
             const bool more = j + 1 < to;
             if (!more) read_item(item + 1);
-            if (more || j0 < j1) scores(!more, more ? j + 2 == to : j1 - j0 == 1);
+            const bool follows = more || j0 < j1;
+            if (follows) scores(!more, more ? j + 2 == to : j1 - j0 == 1);
             ok = ok && __all_sync(0xffffffffu, wait(&bars->full[sv], sv_par));
             if (!ok) break;
             if (end != 0 && j == last) {  // rows of the last page behind the request's positions: zeros
@@ -544,17 +522,17 @@ __device__ void mma_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint3
             const uint32_t b = p_base + (uint32_t)pb * (S::kPBytes >> 4) + ((4096u >> 4) << 16);
             if (elect()) {
 #pragma unroll
-                for (int x = 0; x < S::kParts; ++x)
+                for (int x = 0; x < 2; ++x)  // hi, lo
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         const uint32_t bk = b + x * (S::kPart >> 4) + k * 32;
                         mma_bf16(tbase + S::kTmO, high | (a + k * 128), high32 | bk, id_o, j > from || x + k > 0);
-                        if (S::kOnes)
-                            mma_bf16(tbase + S::kTmL, high32 | ones, high32 | bk, id_l, j > from || x + k > 0);
                     }
+                // Slots go back in the ring's order, although the keys were done with first: the loading warps, which fill
+                // every other one, tell a slot's phases apart by that.
                 mma_commit(&bars->empty[sv]);
+                if (follows) mma_commit(&bars->empty[sk]);
                 mma_commit(&bars->p_empty[pb]);
-                mma_commit(&bars->pv_done);
                 if (!more) mma_commit(&bars->o_full);
             }
             __syncwarp();
@@ -594,9 +572,9 @@ struct Ring {
 
 template <int RP>
 __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUtensorMap *tk, Bars<RP> *bars,
-                          uint8_t *sm, int lane, int blocks, int tok_block, const Waiter &wait) {
+                          uint8_t *sm, int lane, const Waiter &wait) {
     using S = Shape<RP>;
-    const uint32_t box = (uint32_t)(tok_block * p.group) * 128;
+    const uint32_t box = (uint32_t)(p.N * p.group) * 128;
     int item = 0, asked = 0;
     Ring<RP> ring(0);
     bool ok = true;
@@ -609,11 +587,11 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
         }
         __syncwarp();
     };
-    Walk w(p, S::kExtra, blocks, sum_work(p.B, [&](int x) { return request_work(p, x, S::kExtra, p.Hkv * blocks); }));
+    Walk w(p, S::kExtra, sum_work(p.B, [&](int x) { return request_work(p, x, S::kExtra); }));
     for (; w.live && ok; w.next(p), ++item) {
         Pages pages;
         pages.fetch(p.cache, w.b, w.kv_len, w.j0, lane);
-        publish({w.b, w.kvh, w.rb, w.kv_len, w.j0, w.j1, w.j0 == 0 && w.j1 == w.tiles});
+        publish({w.b, w.kvh, w.kv_len, w.j0, w.j1, w.j0 == 0 && w.j1 == w.tiles});
         const int qb = item % S::kQBufs;
         // a buffer's first phase is filled at once: the wait for the one before it returns
         if (!(ok = ok && __all_sync(0xffffffffu, wait(&bars->q_empty[qb], (uint32_t)(item / S::kQBufs + 1) & 1)))) break;
@@ -622,7 +600,7 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
 #pragma unroll
             for (int x = 0; x < 2; ++x)
                 tma_load_4d(sm + S::kOffQ + qb * S::kQBytes + x * (S::kQBytes / 2), tq, &bars->q_full[qb], 0,
-                            w.kvh * p.group, w.b * p.N + w.rb * tok_block, x);
+                            w.kvh * p.group, w.b * p.N, x);
         }
         __syncwarp();
         asked = item + 1;
@@ -634,7 +612,7 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
     }
     if (lane == 0)
         static_cast<Tail *>(p.ws)[blockIdx.x] = {w.runs, w.tail_at, work_of(w.tail_tiles, w.extra), w.tail_tiles, w.tail_b,
-                                                 w.tail_kvh, w.tail_rb, 0, 0};
+                                                 w.tail_kvh, 0, w.tail_b * p.N, p.N};
     publish({});
     // no copy may be in flight when the CTA exits
     for (int x = asked > S::kQBufs ? asked - S::kQBufs : 0; x < asked; ++x)
@@ -678,7 +656,7 @@ __device__ void drain_ring(Bars<RP> *bars, const Waiter &wait) {
 }
 
 template <int RP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, Shape<RP>::kPerSm)
     attn_verify_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const AttnParams p) {
     using S = Shape<RP>;
@@ -686,14 +664,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Bars<RP> *bars = reinterpret_cast<Bars<RP> *>(sm + S::kOffBars);
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int tok_block = min(p.N, kMaxDrafts / p.group), blocks = (p.N + tok_block - 1) / tok_block;
     if (warp < kMmaWarp) {
-        // rows of Q that no box fills, and the ones
+        // rows of Q that no box fills
         for (int i = threadIdx.x; i < (int)(S::kQBufs * S::kQBytes / 16); i += 256)
             reinterpret_cast<uint4 *>(sm + S::kOffQ)[i] = make_uint4(0, 0, 0, 0);
-        for (int i = threadIdx.x; S::kOnes && i < 256; i += 256)
-            reinterpret_cast<uint4 *>(sm + S::kOffOnes)[i] =
-                make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
         for (int r = threadIdx.x; r < RP; r += 256) bars->tok_of[r] = (uint8_t)(r / p.group);
         fence_proxy_async_smem();
     } else if (warp == kMmaWarp) {
@@ -716,7 +690,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&bars->item_full[i], 1);
                 mbar_init(&bars->item_empty[i], kMmaWarp + 2);
             }
-            mbar_init(&bars->pv_done, 1);
             mbar_init(&bars->o_full, 1);
             mbar_init(&bars->o_free, 8);
             mbar_init(&bars->drain, 1);
@@ -730,14 +703,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_trigger();
     const uint32_t tbase = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
     const Waiter wait{p.wait_limit_ns, p.err};
-    if (warp < kMmaWarp)
-        softmax_role<RP>(p, bars, sm, tbase, warp, lane, tok_block, wait);
-    else if (warp == kMmaWarp)
-        mma_role<RP>(p, bars, sm, tbase, lane, wait);
-    else if (warp == kLoadWarp)
-        load_role<RP>(p, &tq, &tk, bars, sm, lane, blocks, tok_block, wait);
-    else if (warp == kValueWarp)
-        value_role<RP>(p, &tv, bars, sm, lane, wait);
+    if (warp < kMmaWarp) {
+        if (RP == 64) reg_inc<kRegsSoftmax>();
+        softmax_role<RP>(p, bars, sm, tbase, warp, lane, wait);
+    } else {
+        if (RP == 64) reg_dec<kRegsRest>();
+        if (warp == kMmaWarp)
+            mma_role<RP>(p, bars, sm, tbase, lane, wait);
+        else if (warp == kLoadWarp)
+            load_role<RP>(p, &tq, &tk, bars, sm, lane, wait);
+        else if (warp == kValueWarp)
+            value_role<RP>(p, &tv, bars, sm, lane, wait);
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) tmem_dealloc(tbase, S::kTmCols);
@@ -796,7 +773,7 @@ __device__ __forceinline__ uint2 join_row(const int *list, int count, long long 
 // Joins the items that several CTAs shared, block x the one that CTA x has left for it, a warp per row.  rp: the
 // padded rows of a partial result.
 __global__ void __launch_bounds__(256) attn_verify_join_kernel(const AttnParams p, int rp) {
-    __shared__ int list[kAttnCtas], s_count;
+    __shared__ int list[kMaxRuns], s_count;
     pdl_wait();
     pdl_trigger();
     const Tail t = static_cast<const Tail *>(p.ws)[blockIdx.x];
@@ -817,23 +794,22 @@ __global__ void __launch_bounds__(256) attn_verify_join_kernel(const AttnParams 
     __syncthreads();
     const int count = s_count;
     if (count == 0) return;
-    const int tok_block = min(p.N, kMaxDrafts / p.group), tok0 = t.first * tok_block;
-    const int rows = min(tok_block, p.N - tok0) * p.group;
-    const float *parts = reinterpret_cast<const float *>(static_cast<const Tail *>(p.ws) + kAttnCtas);
+    const int rows = p.N * p.group;
+    const float *parts = reinterpret_cast<const float *>(static_cast<const Tail *>(p.ws) + kMaxRuns);
     for (int r = blockIdx.y * 8 + warp; r < rows; r += gridDim.y * 8) {
         const uint2 w = join_row(list, count, (long long)rp * kHeadDim - r * (kHeadDim - 2), lane, [&](int piece) {
             return parts + (long long)piece * rp * (kHeadDim + 2) + r * kHeadDim;
         });
         const int tok = r / p.group, head = t.kvh * p.group + r - tok * p.group;
-        reinterpret_cast<uint2 *>(p.out + (((long long)t.b * p.N + tok0 + tok) * p.H + head) * kHeadDim)[lane] = w;
+        reinterpret_cast<uint2 *>(p.out + (((long long)t.t0 + tok) * p.H + head) * kHeadDim)[lane] = w;
     }
 }
 
 template <int RP>
 cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const AttnParams &p,
-                   int ctas, cudaStream_t stream) {
+                   cudaStream_t stream) {
     constexpr uint32_t smem = Shape<RP>::kOffBars + sizeof(Bars<RP>) + 1024;
-    static_assert(smem <= 227 * 1024, "shared memory");
+    static_assert(Shape<RP>::kPerSm * (smem + 1024) <= 228 * 1024, "shared memory");
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -848,35 +824,29 @@ cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
             configured[dev] = true;
         }
     }
-    return launch_pdl(attn_verify_kernel<RP>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, tq, tk, tv, p);
+    return launch_pdl(attn_verify_kernel<RP>, dim3(kAttnCtas * Shape<RP>::kPerSm), dim3(kThreads), smem, stream, tq, tk, tv, p);
 }
 
-int padded_rows(int N, int group) {
-    const int rows = std::min(N, kMaxDrafts / group) * group;
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-}
+int padded_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 }  // namespace
 
-unsigned long long attn_verify_ws_bytes(int N, int group) {
-    return kAttnCtas * (sizeof(Tail) + 2ull * padded_rows(N, group) * (kHeadDim + 2) * 4);
+unsigned long long attn_verify_ws_bytes(int rows) {
+    const int rp = padded_rows(rows), runs = rp == 16 ? Shape<16>::kPerSm * kAttnCtas : kAttnCtas;
+    return kMaxRuns * sizeof(Tail) + 2ull * runs * rp * (kHeadDim + 2) * 4;
 }
 
 cudaError_t launch_attn_verify(const AttnParams &p, cudaStream_t stream) {
     CUtensorMap tq, tk, tv;
-    if (!make_query_map(&tq, p.q, (long long)p.B * p.N, p.H, p.q_rs, p.group, std::min(p.N, kMaxDrafts / p.group)) ||
+    if (!make_query_map(&tq, p.q, (long long)p.B * p.N, p.H, p.q_rs, p.group, p.N) ||
         !make_pages_map(&tk, p.cache.k, p.cache, p.Hkv) || !make_pages_map(&tv, p.cache.v, p.cache, p.Hkv))
         return cudaErrorInvalidValue;
-    const int rp = padded_rows(p.N, p.group);
-    cudaError_t e;
-    switch (rp) {
-        case 16: e = launch<16>(tq, tk, tv, p, kAttnCtas, stream); break;
-        case 32: e = launch<32>(tq, tk, tv, p, kAttnCtas, stream); break;
-        case 64: e = launch<64>(tq, tk, tv, p, kAttnCtas, stream); break;
-        default: e = launch<128>(tq, tk, tv, p, kAttnCtas, stream); break;
-    }
+    const int rp = padded_rows(p.N * p.group);
+    const cudaError_t e = rp == 16   ? launch<16>(tq, tk, tv, p, stream)
+                          : rp == 32 ? launch<32>(tq, tk, tv, p, stream)
+                                     : launch<64>(tq, tk, tv, p, stream);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_verify_join_kernel, dim3(kAttnCtas - 1, (unsigned)(rp / 16)), dim3(256), 0, stream, p, rp);
+    return launch_pdl(attn_verify_join_kernel, dim3((rp == 16 ? Shape<16>::kPerSm * kAttnCtas : kAttnCtas) - 1, (unsigned)(rp / 16)), dim3(256), 0, stream, p, rp);
 }
 
 }  // namespace la

@@ -124,16 +124,23 @@ def test_null_and_misaligned_pointers(lib):
 def test_workspaces(lib):
     nb = ctypes.c_size_t(7)
     size = lib.la_attn_verify_workspace_size
-    for args, st in (((0, 1, 1, 128), 1), ((1, 0, 1, 128), 1), ((1, 3, 2, 128), 1), ((1, 1, 0, 128), 1),
-                     ((1, 1, 1, 64), 2), ((129, 1, 1, 128), 2), ((1, 129, 1, 128), 2)):
+    for args, st in (((1, 0, 1, 1, 128, 9), 1), ((1, 1, 0, 1, 128, 9), 1), ((1, 1, 3, 2, 128, 9), 1), ((1, 1, 1, 0, 128, 9), 1),
+                     ((-1, 1, 1, 1, 128, 9), 1), ((1, 1, 1, 1, 128, -1), 1), ((1, 1, 1, 1, 64, 9), 2),
+                     ((1, 129, 1, 1, 128, 9), 2), ((1, 1, 129, 1, 128, 9), 2)):
         assert size(*args, ctypes.byref(nb)) == st, args
-    assert size(1, 1, 1, 128, None) == 1
-    for n, H, Hkv, rows in ((1, 16, 1, 16), (1, 17, 1, 32), (8, 8, 1, 64), (8, 64, 8, 64), (13, 5, 1, 128), (128, 1, 1, 128),
-                            (100, 4, 2, 128), (128, 128, 1, 128)):
-        assert la.attn_verify_workspace_size(n, H, Hkv, 128) == 152 * (56 + 2 * rows * 130 * 4)
-    need = la.attn_verify_workspace_size(3, 2, 1, 128)
+    assert size(1, 1, 1, 1, 128, 9, None) == 1
+    for n, H, Hkv, rows in ((1, 16, 1, 16), (1, 17, 1, 32), (8, 8, 1, 64), (8, 64, 8, 64), (21, 3, 1, 64)):
+        assert la.attn_verify_workspace_size(3, n, H, Hkv, 128, 99999) == 304 * 56 + 152 * (2 if rows == 16 else 1) * 2 * rows * 130 * 4
+    assert la.attn_verify_workspace_size(0, 1, 16, 1, 128, 999) == 0
+    # more rows than 64 go the way of prompts
+    for n, H, Hkv in ((13, 5, 1), (128, 1, 1), (100, 4, 2), (1, 128, 1)):
+        for B, kv in ((1, 200), (3, 5000), (300, 5000)):
+            assert la.attn_verify_workspace_size(B, n, H, Hkv, 128, kv) == la.attn_extend_workspace_size(
+                B, B * n, H, Hkv, 128, n, kv)
+    need = la.attn_verify_workspace_size(2, 3, 2, 1, 128, 32)
     assert tree(lib, nbytes=need - 1) == 1
-    assert decode(lib, nbytes=la.attn_verify_workspace_size(1, 2, 1, 128) - 1) == 1
+    assert decode(lib, nbytes=la.attn_verify_workspace_size(2, 1, 2, 1, 128, 32) - 1) == 1
+    assert tree(lib, H=128, P=128, nbytes=1000, width=9) == 1
     size = lib.la_attn_extend_workspace_size
     for args, st in (((-1, 1, 1, 1, 128, 1, 1), 1), ((1, -1, 1, 1, 128, 1, 1), 1), ((1, 1, 3, 2, 128, 1, 1), 1),
                      ((1, 1, 1, 1, 128, -1, 1), 1), ((1, 1, 1, 1, 128, 1, -1), 1), ((1, 1, 1, 1, 64, 1, 1), 2),
