@@ -39,7 +39,7 @@ constexpr float kUnseen = 1e30f;  // minus the reference of a row that has seen 
 template <int RP>
 struct Shape {
     static constexpr int kPerSm = RP == 16 ? 2 : 1;
-    static constexpr int kQBufs = RP == 16 ? 1 : 2, kPBufs = RP == 32 ? 2 : 1;
+    static constexpr int kQBufs = 2, kPBufs = RP == 32 ? 2 : 1;
     static constexpr int kSlots = RP == 16 ? 3 : RP == 32 ? 5 : 4;  // tiles of keys and values
     static constexpr int kExtra = RP <= 32 ? 1 : 2;  // tiles' time that an item takes besides its own
     static constexpr uint32_t kQBytes = RP * 256, kPart = kKeyTile * RP * 2, kPBytes = 2 * kPart;
@@ -66,7 +66,7 @@ struct Bars {
     alignas(16) float factor[RP];
     float top[4][RP];
     uint8_t tok_of[RP];
-    uint32_t below[kVerifyRows][2];     // below[a] bit t: draft t is a or descends from it
+    uint32_t below[RP][2];              // below[a] bit t: draft t is a or descends from it
     int loads[2];                       // of keys and of values, at the end
     uint32_t tmem_base;
 };
@@ -168,7 +168,7 @@ __device__ __forceinline__ float redux_max(float x) {
 template <int RP>
 __device__ bool build_tree(const AttnParams &p, Bars<RP> *bars, int b, int tid) {
     softmax_sync();  // the last request's table is not read any more
-    if (tid < kVerifyRows) bars->below[tid][0] = bars->below[tid][1] = 0;
+    if (tid < RP) bars->below[tid][0] = bars->below[tid][1] = 0;
     softmax_sync();
     bool bad = false;
     if (tid < p.N) {
@@ -660,8 +660,7 @@ __global__ void __launch_bounds__(kThreads, Shape<RP>::kPerSm)
     attn_verify_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const AttnParams p) {
     using S = Shape<RP>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t sm[];  // no room to align it by hand
     Bars<RP> *bars = reinterpret_cast<Bars<RP> *>(sm + S::kOffBars);
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (warp < kMmaWarp) {
@@ -808,7 +807,7 @@ __global__ void __launch_bounds__(256) attn_verify_join_kernel(const AttnParams 
 template <int RP>
 cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const AttnParams &p,
                    cudaStream_t stream) {
-    constexpr uint32_t smem = Shape<RP>::kOffBars + sizeof(Bars<RP>) + 1024;
+    constexpr uint32_t smem = Shape<RP>::kOffBars + sizeof(Bars<RP>);
     static_assert(Shape<RP>::kPerSm * (smem + 1024) <= 228 * 1024, "shared memory");
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
