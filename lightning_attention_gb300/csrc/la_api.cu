@@ -763,7 +763,8 @@ la_status rope_params(la::RopeParams *p, const la_bf16 *q, const la_bf16 *k, int
     if (T < 0 || H < 1 || Hkv < 1 || D < 1 || rot_dim < 0 || rot_dim > D || !isfinite(mscale))
         return LA_ERR_INVALID;
     if (D != la::kHeadDim || rot_dim % 16 != 0) return LA_ERR_UNSUPPORTED;
-    if ((long long)H + 2ll * Hkv > 0x7fff0000LL / la::kHeadDim) return LA_ERR_UNSUPPORTED;
+    const long long rows = (long long)H + 2ll * Hkv;  // of a token, at most
+    if (rows > 0x7fff0000LL / la::kHeadDim || rows * T > (1ll << 37)) return LA_ERR_UNSUPPORTED;
     if (!row_stride_ok(&q_rs, T, (long long)H * D) || !row_stride_ok(&k_rs, T, (long long)Hkv * D) ||
         !row_stride_ok(&qo_rs, T, (long long)H * D))
         return LA_ERR_INVALID;
