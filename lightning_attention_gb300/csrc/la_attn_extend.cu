@@ -378,43 +378,46 @@ __device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, in
                     return columns_seen(last - i * 32);
             };
             uint32_t w[32];
-            bool behind = true;
-            if (j > it.j0) {
-                float sum[4] = {l4[0], l4[1], l4[2], l4[3]};
-                const float top = lo_last < 63 ? weigh<true>(ts + half * 64, seen, lo_last, hi_last, c, neg_m, w, sum)
-                                               : weigh<false>(ts + half * 64, seen, lo_last, hi_last, c, neg_m, w, sum);
-                behind = pair_any(pair, top > 8.f || !ok);  // S has been read by both from here on
-                if (!behind) {
+            float sum[4];
+            // Against the reference that there is; with the item's first tile, and once more where a weight passes 2^8,
+            // against a new one.  (One copy of the code: instructions that are fetched anew for every item cost more
+            // than what they do.)
+            bool fresh = j == it.j0;
+            while (true) {
+                if (fresh) {
+                    float top = largest(ts + half * 64, seen, lo_last, hi_last);
+                    bars->swap[stage][half][row] = top;
+                    if (pair_any(pair, !ok)) return;
+                    top = fmaxf(top, bars->swap[stage][half ^ 1][row]) * c;
+                    float f = 1.f;
+                    if (top > 8.f - neg_m) {
+                        f = neg_m == kUnseen ? 0.f : ex2z(-neg_m - top);
+                        neg_m = -top;
+                    }
+                    if (j > it.j0) {  // S(j) comes after O += P(j-1) V, which is complete
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) l4[i] = sum[i];
-                }
-            }
-            if (behind) {
-                float top = largest(ts + half * 64, seen, lo_last, hi_last);
-                bars->swap[stage][half][row] = top;
-                if (pair_any(pair, !ok)) return;
-                top = fmaxf(top, bars->swap[stage][half ^ 1][row]) * c;
-                float f = 1.f;
-                if (top > 8.f - neg_m) {
-                    f = neg_m == kUnseen ? 0.f : ex2z(-neg_m - top);
-                    neg_m = -top;
-                }
-                if (j > it.j0) {  // S(j) comes after O += P(j-1) V, which is complete
+                        for (int i = 0; i < 4; ++i) l4[i] *= f;
+#pragma unroll 1
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t o[32];
+                            tmem_ld32(to + i * 32, o);
+                            tmem_ld_wait_regs(o);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) l4[i] *= f;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t o[32];
-                        tmem_ld32(to + i * 32, o);
-                        tmem_ld_wait_regs(o);
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                        tmem_st32(to + i * 32, o);
+                            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                            tmem_st32(to + i * 32, o);
+                        }
                     }
                 }
-                weigh<true>(ts + half * 64, seen, lo_last, hi_last, c, neg_m, w, l4);
-                pair_any(pair, false);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[i] = l4[i];
+                const float top = lo_last < 63 ? weigh<true>(ts + half * 64, seen, lo_last, hi_last, c, neg_m, w, sum)
+                                               : weigh<false>(ts + half * 64, seen, lo_last, hi_last, c, neg_m, w, sum);
+                // S has been read by both from here on
+                if (!pair_any(pair, (!fresh && top > 8.f) || !ok)) break;
+                fresh = true;
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) l4[i] = sum[i];
             tmem_st32(ts + half * 32, w);
             tmem_st_wait();
             tc_fence_before();
