@@ -482,13 +482,13 @@ la_status la_unpack_states(const int8_t *codes, const uint8_t *scales, int entri
  *                 packed; a multiple of 8, at least H * D; ignored for a single row), out packed
  *   H, Hkv        query heads and kv heads; query head h reads kv head h / (H / Hkv).  H must be a multiple of Hkv
  *                 (LA_ERR_INVALID), H / Hkv at most 128 (LA_ERR_UNSUPPORTED)
- *   scale         factor on the scores q . k, finite and positive (LA_ERR_INVALID otherwise); usually D^-0.5
+ *   scale         factor on the scores q . k, positive, at most 2e38 (LA_ERR_INVALID otherwise); usually D^-0.5
  * Rows of pages behind a request's positions, and pages that no table names, may hold anything.  Requests may share
  * pages that no call writes.  A kv_lens entry that is negative, larger than max_pages * page_size, or smaller than the
  * call's tokens skips its request (its rows of out are left as they were); a page outside [0, num_pages) reads as
  * zeros, and the rows of its request are undefined; la_poll_error reports both as LA_ERR_DEVICE_INPUT.  A NaN or an infinity in
  * q reaches its own row and head; one in a request's keys or values may reach all of that request's rows, and nothing
- * of any other request.  Scores (times scale) beyond fp32 are not supported.
+ * of any other request.  Scores (times scale) may be up to 1e29 in magnitude.
  */
 
 /* la_rope_scaling -- how the frequencies of rotary positions are stretched for long contexts. */

@@ -764,7 +764,7 @@ la_status rope_params(la::RopeParams *p, const la_bf16 *q, const la_bf16 *k, int
         return LA_ERR_INVALID;
     if (D != la::kHeadDim || rot_dim % 16 != 0) return LA_ERR_UNSUPPORTED;
     const long long rows = (long long)H + 2ll * Hkv;  // of a token, at most
-    if (rows > 0x7fff0000LL / la::kHeadDim || rows * T > (1ll << 37)) return LA_ERR_UNSUPPORTED;
+    if (rows > 0x7fff0000LL / la::kHeadDim || rows * T > (1ll << 36)) return LA_ERR_UNSUPPORTED;
     if (!row_stride_ok(&q_rs, T, (long long)H * D) || !row_stride_ok(&k_rs, T, (long long)Hkv * D) ||
         !row_stride_ok(&qo_rs, T, (long long)H * D))
         return LA_ERR_INVALID;
@@ -792,11 +792,14 @@ bool rope_pointers_ok(const la::RopeParams &p) {
            (reinterpret_cast<uintptr_t>(p.inv_freq) & 7u) == 0;
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 // Checks shared by the attention calls, of `tokens` rows; work == false: nothing to launch.
 la_status attn_params(la::AttnParams *p, bool *work, const la_bf16 *q, int64_t q_rs, const la::CacheParams &c,
                       la_bf16 *out, int B, long long tokens, int H, int Hkv, float scale) {
     *work = false;
-    if (B < 0 || tokens < 0 || H < 1 || H % Hkv != 0 || !(scale > 0.f) || !isfinite(scale)) return LA_ERR_INVALID;
+    if (B < 0 || tokens < 0 || H < 1 || H % Hkv != 0 || !(scale > 0.f) || !isfinite(scale * kLog2e))
+        return LA_ERR_INVALID;
     if (tokens > 0x7fffffffLL) return LA_ERR_INVALID;
     if (H / Hkv > la::kMaxDrafts) return LA_ERR_UNSUPPORTED;
     if (!row_stride_ok(&q_rs, tokens, (long long)H * la::kHeadDim)) return LA_ERR_INVALID;
@@ -808,7 +811,7 @@ la_status attn_params(la::AttnParams *p, bool *work, const la_bf16 *q, int64_t q
     p->q_rs = q_rs;
     p->cache = c;
     p->out = reinterpret_cast<__nv_bfloat16 *>(out);
-    p->scale_log2 = scale * 1.4426950408889634f;
+    p->scale_log2 = scale * kLog2e;
     p->B = B;
     p->T = (int)tokens;
     p->H = H;

@@ -65,7 +65,7 @@ def test_sizes_and_heads(lib):
         assert call(lib, D=64) == 2 and call(lib, rot=24) == 2 and call(lib, H=1 << 24) == 2
     for call in ATTN:
         for kw in ({"B": -1}, {"H": 0}, {"Hkv": 0}, {"H": 3, "Hkv": 2}, {"H": 1, "Hkv": 2}, {"D": 0}, {"scale": 0.0},
-                   {"scale": -1.0}, {"scale": math.nan}, {"scale": math.inf}):
+                   {"scale": -1.0}, {"scale": math.nan}, {"scale": math.inf}, {"scale": 3e38}):
             assert call(lib, **kw) == 1, (call, kw)
         assert call(lib, D=64) == 2 and call(lib, H=129) == 2
     assert extend(lib, T=-1) == 1 and extend(lib, ms=-1) == 1 and extend(lib, mk=-1) == 1
