@@ -841,7 +841,7 @@ la_status attn_verify(const la_bf16 *q, int64_t q_rs, const la_bf16 *k_pages, co
     if (tree && (!parents || !aligned4(parents))) return LA_ERR_INVALID;
     const bool few = N * p.group <= la::kVerifyRows;
     const la::AttnExtendPlan plan = la::plan_attn_extend(B, p.T, H, Hkv, N, (long long)max_pages * page_size);
-    const unsigned long long need = few ? la::attn_verify_ws_bytes(N * p.group) : plan.ws_bytes;
+    const unsigned long long need = few ? la::attn_verify_ws_bytes(N * p.group, (long long)max_pages * page_size) : plan.ws_bytes;
     if (need > 0 && (!workspace || !aligned16(workspace) || (unsigned long long)workspace_bytes < need))
         return LA_ERR_INVALID;
     p.parents = tree ? parents : nullptr;
@@ -968,7 +968,7 @@ la_status la_attn_verify_workspace_size(int B, int N, int H, int Hkv, int D, int
     if (D != la::kHeadDim || N > la::kMaxDrafts || H / Hkv > la::kMaxDrafts) return LA_ERR_UNSUPPORTED;
     const int rows = N * (H / Hkv);
     *bytes = (size_t)(B == 0                      ? 0
-                      : rows <= la::kVerifyRows ? la::attn_verify_ws_bytes(rows)
+                      : rows <= la::kVerifyRows ? la::attn_verify_ws_bytes(rows, max_kvlen)
                                                   : la::plan_attn_extend(B, (long long)B * N, H, Hkv, N, max_kvlen).ws_bytes);
     return LA_OK;
 }

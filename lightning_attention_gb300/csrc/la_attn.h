@@ -61,7 +61,7 @@ cudaError_t launch_attn_extend(const AttnParams &p, const AttnExtendPlan &plan, 
 // N drafts (or one token) per request, the last N positions, N * group at most kVerifyRows; more go to
 // launch_attn_extend, with cu_seqlens null.
 constexpr int kVerifyRows = 64;
-unsigned long long attn_verify_ws_bytes(int rows);
+unsigned long long attn_verify_ws_bytes(int rows, long long max_kvlen);
 cudaError_t launch_attn_verify(const AttnParams &p, cudaStream_t stream);
 
 struct KvCommitParams {

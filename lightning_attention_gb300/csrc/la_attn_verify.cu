@@ -35,12 +35,12 @@ constexpr int kBarSoftmax = 1;
 constexpr int kMaxRuns = 2 * kAttnCtas;
 constexpr float kUnseen = 1e30f;  // minus the reference of a row that has seen no key: any score passes it, -inf stays
 
-// Up to 16 rows two CTAs share an SM, so that one works where the other waits at an item's beginning or end.
-template <int RP>
+// Two CTAs share an SM where contexts are short, so that one works where the other waits at an item's beginning or end.
+template <int RP, int PER_SM>
 struct Shape {
-    static constexpr int kPerSm = RP == 16 ? 2 : 1;
-    static constexpr int kQBufs = 2, kPBufs = RP == 32 ? 2 : 1;
-    static constexpr int kSlots = RP == 16 ? 3 : RP == 32 ? 5 : 4;  // tiles of keys and values
+    static constexpr int kPerSm = PER_SM;
+    static constexpr int kQBufs = 2, kPBufs = RP <= 32 && PER_SM == 1 ? 2 : 1;
+    static constexpr int kSlots = PER_SM == 2 ? 3 : RP <= 32 ? 5 : 4;  // tiles of keys and values
     static constexpr int kExtra = RP <= 32 ? 1 : 2;  // tiles' time that an item takes besides its own
     static constexpr uint32_t kQBytes = RP * 256, kPart = kKeyTile * RP * 2, kPBytes = 2 * kPart;
     static constexpr uint32_t kOffKV = 0;
@@ -224,10 +224,10 @@ __device__ __forceinline__ void tmem_put(uint32_t at, const float (&x)[n]) {
 }
 
 // Two threads a key: warps 0-3 have the first half of the rows, warps 4-7 the other.
-template <int RP>
+template <int RP, int PER_SM>
 __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint32_t tbase, int warp, int lane,
                              const Waiter &wait) {
-    using S = Shape<RP>;
+    using S = Shape<RP, PER_SM>;
     constexpr int R = RP / 2;  // rows of a thread
     const int tid = warp * 32 + lane, key = tid & 127, half = warp >> 2;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
@@ -426,10 +426,10 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
 // What feeds an MMA is the same in every lane and known to be (values from shared memory through a shuffle,
 // slots counted instead of divided), so that the uniform datapath forms the operands: otherwise an issue takes 100
 // cycles, several times the MMA (128 requests of 500-8000 positions, 32 heads on 4: 304 us).
-template <int RP>
+template <int RP, int PER_SM>
 __device__ void mma_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint32_t tbase, int lane,
                          const Waiter &wait) {
-    using S = Shape<RP>;
+    using S = Shape<RP, PER_SM>;
     const uint32_t id_s = idesc_bf16_f32(128, RP, false, false);
     const uint32_t id_o = idesc_bf16_f32(128, RP, true, true);
     const uint64_t high = sdesc_sw128(0, 0, 1024), high32 = sdesc_sw32(0, 0, 256);
@@ -549,9 +549,9 @@ __device__ void mma_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint3
 }
 
 // The tiles that a loading warp fills, every other one of the ring: keys (kv 0) and values (1).
-template <int RP>
+template <int RP, int PER_SM>
 struct Ring {
-    using S = Shape<RP>;
+    using S = Shape<RP, PER_SM>;
     int slot, count = 0;
     uint32_t phase = 0;
     __device__ __forceinline__ Ring(int kv) : slot(kv) {}
@@ -570,13 +570,13 @@ struct Ring {
     }
 };
 
-template <int RP>
+template <int RP, int PER_SM>
 __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUtensorMap *tk, Bars<RP> *bars,
                           uint8_t *sm, int lane, const Waiter &wait) {
-    using S = Shape<RP>;
+    using S = Shape<RP, PER_SM>;
     const uint32_t box = (uint32_t)(p.N * p.group) * 128;
     int item = 0, asked = 0;
-    Ring<RP> ring(0);
+    Ring<RP, PER_SM> ring(0);
     bool ok = true;
     auto publish = [&](const Rec &r) {
         if (item >= kItems)
@@ -620,10 +620,10 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
     if (lane == 0) bars->loads[0] = ring.count;
 }
 
-template <int RP>
+template <int RP, int PER_SM>
 __device__ void value_role(const AttnParams &p, const CUtensorMap *tv, Bars<RP> *bars, uint8_t *sm, int lane,
                            const Waiter &wait) {
-    Ring<RP> ring(1);
+    Ring<RP, PER_SM> ring(1);
     bool ok = true;
     for (int item = 0; ok; ++item) {
         if (!__all_sync(0xffffffffu, wait(&bars->item_full[item % kItems], (uint32_t)(item / kItems) & 1))) break;
@@ -643,9 +643,9 @@ __device__ void value_role(const AttnParams &p, const CUtensorMap *tv, Bars<RP> 
 }
 
 // The last load into every slot, of those that the two warps made.
-template <int RP>
+template <int RP, int PER_SM>
 __device__ void drain_ring(Bars<RP> *bars, const Waiter &wait) {
-    constexpr int n_slots = Shape<RP>::kSlots;
+    constexpr int n_slots = Shape<RP, PER_SM>::kSlots;
     for (int s = 0; s < n_slots; ++s) {
         int last = -1;
         for (int kv = 0; kv < 2; ++kv)  // load n of warp kv is number 2 n + kv of the ring
@@ -655,11 +655,11 @@ __device__ void drain_ring(Bars<RP> *bars, const Waiter &wait) {
     }
 }
 
-template <int RP>
-__global__ void __launch_bounds__(kThreads, Shape<RP>::kPerSm)
+template <int RP, int PER_SM>
+__global__ void __launch_bounds__(kThreads, Shape<RP, PER_SM>::kPerSm)
     attn_verify_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const AttnParams p) {
-    using S = Shape<RP>;
+    using S = Shape<RP, PER_SM>;
     extern __shared__ __align__(1024) uint8_t sm[];  // no room to align it by hand
     Bars<RP> *bars = reinterpret_cast<Bars<RP> *>(sm + S::kOffBars);
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -704,20 +704,20 @@ __global__ void __launch_bounds__(kThreads, Shape<RP>::kPerSm)
     const Waiter wait{p.wait_limit_ns, p.err};
     if (warp < kMmaWarp) {
         if (RP == 64) reg_inc<kRegsSoftmax>();
-        softmax_role<RP>(p, bars, sm, tbase, warp, lane, wait);
+        softmax_role<RP, PER_SM>(p, bars, sm, tbase, warp, lane, wait);
     } else {
         if (RP == 64) reg_dec<kRegsRest>();
         if (warp == kMmaWarp)
-            mma_role<RP>(p, bars, sm, tbase, lane, wait);
+            mma_role<RP, PER_SM>(p, bars, sm, tbase, lane, wait);
         else if (warp == kLoadWarp)
-            load_role<RP>(p, &tq, &tk, bars, sm, lane, wait);
+            load_role<RP, PER_SM>(p, &tq, &tk, bars, sm, lane, wait);
         else if (warp == kValueWarp)
-            value_role<RP>(p, &tv, bars, sm, lane, wait);
+            value_role<RP, PER_SM>(p, &tv, bars, sm, lane, wait);
     }
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) tmem_dealloc(tbase, S::kTmCols);
-    if (warp == kLoadWarp) drain_ring<RP>(bars, wait);
+    if (warp == kLoadWarp) drain_ring<RP, PER_SM>(bars, wait);
 }
 
 // A row's partial results joined: o = sum_i 2^{m_i - m} O_i / sum_i 2^{m_i - m} l_i over the pieces of the list, a lane per
@@ -804,11 +804,11 @@ __global__ void __launch_bounds__(256) attn_verify_join_kernel(const AttnParams 
     }
 }
 
-template <int RP>
+template <int RP, int PER_SM>
 cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const AttnParams &p,
                    cudaStream_t stream) {
-    constexpr uint32_t smem = Shape<RP>::kOffBars + sizeof(Bars<RP>);
-    static_assert(Shape<RP>::kPerSm * (smem + 1024) <= 228 * 1024, "shared memory");
+    constexpr uint32_t smem = Shape<RP, PER_SM>::kOffBars + sizeof(Bars<RP>);
+    static_assert(Shape<RP, PER_SM>::kPerSm * (smem + 1024) <= 228 * 1024, "shared memory");
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -818,21 +818,27 @@ cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
         std::lock_guard<std::mutex> lock(mu);
         if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
         if (!configured[dev]) {
-            e = cudaFuncSetAttribute(attn_verify_kernel<RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            e = cudaFuncSetAttribute(attn_verify_kernel<RP, PER_SM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
             if (e != cudaSuccess) return e;
             configured[dev] = true;
         }
     }
-    return launch_pdl(attn_verify_kernel<RP>, dim3(kAttnCtas * Shape<RP>::kPerSm), dim3(kThreads), smem, stream, tq, tk, tv, p);
+    return launch_pdl(attn_verify_kernel<RP, PER_SM>, dim3(kAttnCtas * Shape<RP, PER_SM>::kPerSm), dim3(kThreads), smem, stream, tq, tk, tv, p);
 }
 
 int padded_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
+// One CTA an SM or two, by what a row of the page table can hold.  One / two, us, 32 heads on 4, 262,144 positions in requests of
+// 64 (the first 1024): 95 / 68, 128: 122 / 104, 256: 149 / 135, 384: 129 / 118, 512: 119 / 112, 768: 108 / 106,
+// 1024: 103.3 / 102.7, 2048: 98.4 / 99.6; 128 requests of 500-8000: 187 / 189, 2 of 115,000 on 8 heads: 146 / 151.
+constexpr long long kShortKeys = 1280;
+int per_sm(int rows, long long max_kvlen) { return rows <= 16 && max_kvlen <= kShortKeys ? 2 : 1; }
+
 }  // namespace
 
-unsigned long long attn_verify_ws_bytes(int rows) {
-    const int rp = padded_rows(rows), runs = rp == 16 ? Shape<16>::kPerSm * kAttnCtas : kAttnCtas;
-    return kMaxRuns * sizeof(Tail) + 2ull * runs * rp * (kHeadDim + 2) * 4;
+unsigned long long attn_verify_ws_bytes(int rows, long long max_kvlen) {
+    return kMaxRuns * sizeof(Tail) +
+           2ull * per_sm(rows, max_kvlen) * kAttnCtas * padded_rows(rows) * (kHeadDim + 2) * 4;
 }
 
 cudaError_t launch_attn_verify(const AttnParams &p, cudaStream_t stream) {
@@ -840,12 +846,14 @@ cudaError_t launch_attn_verify(const AttnParams &p, cudaStream_t stream) {
     if (!make_query_map(&tq, p.q, (long long)p.B * p.N, p.H, p.q_rs, p.group, p.N) ||
         !make_pages_map(&tk, p.cache.k, p.cache, p.Hkv) || !make_pages_map(&tv, p.cache.v, p.cache, p.Hkv))
         return cudaErrorInvalidValue;
-    const int rp = padded_rows(p.N * p.group);
-    const cudaError_t e = rp == 16   ? launch<16>(tq, tk, tv, p, stream)
-                          : rp == 32 ? launch<32>(tq, tk, tv, p, stream)
-                                     : launch<64>(tq, tk, tv, p, stream);
+    const int rows = p.N * p.group, rp = padded_rows(rows);
+    const int ctas = kAttnCtas * per_sm(rows, (long long)p.cache.max_pages * p.cache.page_size);
+    const cudaError_t e = ctas > kAttnCtas ? launch<16, 2>(tq, tk, tv, p, stream)
+                          : rp == 16       ? launch<16, 1>(tq, tk, tv, p, stream)
+                          : rp == 32       ? launch<32, 1>(tq, tk, tv, p, stream)
+                                           : launch<64, 1>(tq, tk, tv, p, stream);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_verify_join_kernel, dim3((rp == 16 ? Shape<16>::kPerSm * kAttnCtas : kAttnCtas) - 1, (unsigned)(rp / 16)), dim3(256), 0, stream, p, rp);
+    return launch_pdl(attn_verify_join_kernel, dim3((unsigned)(ctas - 1), (unsigned)(rp / 16)), dim3(256), 0, stream, p, rp);
 }
 
 }  // namespace la

@@ -130,7 +130,11 @@ def test_workspaces(lib):
         assert size(*args, ctypes.byref(nb)) == st, args
     assert size(1, 1, 1, 1, 128, 9, None) == 1
     for n, H, Hkv, rows in ((1, 16, 1, 16), (1, 17, 1, 32), (8, 8, 1, 64), (8, 64, 8, 64), (21, 3, 1, 64)):
-        assert la.attn_verify_workspace_size(3, n, H, Hkv, 128, 99999) == 304 * 56 + 152 * (2 if rows == 16 else 1) * 2 * rows * 130 * 4
+        assert la.attn_verify_workspace_size(3, n, H, Hkv, 128, 99999) == 304 * 56 + 152 * 2 * rows * 130 * 4
+    # twice as many runs where few rows meet short contexts
+    assert la.attn_verify_workspace_size(3, 1, 16, 1, 128, 1280) == 304 * 56 + 304 * 2 * 16 * 130 * 4
+    assert la.attn_verify_workspace_size(3, 1, 16, 1, 128, 1281) == 304 * 56 + 152 * 2 * 16 * 130 * 4
+    assert la.attn_verify_workspace_size(3, 1, 17, 1, 128, 512) == 304 * 56 + 152 * 2 * 32 * 130 * 4
     assert la.attn_verify_workspace_size(0, 1, 16, 1, 128, 999) == 0
     # more rows than 64 go the way of prompts
     for n, H, Hkv in ((13, 5, 1), (128, 1, 1), (100, 4, 2), (1, 128, 1)):

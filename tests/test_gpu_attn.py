@@ -145,9 +145,11 @@ def test_decode_pages(P, alternate):
     check_verify([100, 257, 5, 1400], 0, 8, 2, P=P, seed=P, alternate=alternate, strided=alternate)
 
 
-@pytest.mark.parametrize("lens", [[0], [0, 0, 0], [1] * 300, [5000, 3, 0, 1, 800] * 8, [20000]])
-def test_decode_batches(lens):
-    check_verify(lens, 0, 4, 2, P=16, seed=len(lens), width=1 + max(lens) // 16 + 5)
+@pytest.mark.parametrize("lens", [[0], [0, 0, 0], [1] * 300, [5000, 3, 0, 1, 800] * 8, [20000], [200, 1, 64, 1000] * 40])
+@pytest.mark.parametrize("short", [True, False])
+def test_decode_batches(lens, short):
+    """Page tables that hold up to 1,280 positions and more: two CTAs an SM, or one."""
+    check_verify(lens, 0, 4, 2, P=16, seed=len(lens), width=max(1, -(-max(lens) // 16)) if short else 81 + max(lens) // 16)
 
 
 @pytest.mark.parametrize("N", [1, 2, 5, 8, 16, 17, 33, 64, 100, 128])
