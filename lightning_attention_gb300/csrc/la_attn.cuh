@@ -45,6 +45,9 @@ __device__ __forceinline__ bool elect() {
     return r != 0;
 }
 
+// log2 of the page size, one of 16 to 128.
+__device__ __forceinline__ int page_shift(const CacheParams &c) { return 31 - __clz(c.page_size); }
+
 // Pages of a tile: lane l < 128 / page_size has the one that holds positions tile * 128 + l * page_size and on.
 // fetch() asks the table ahead of time (a load that nothing waits for), check() takes its word where the pages are
 // needed: num_pages, whose rows a tiled load fills with zeros, where the request has no such position or the
@@ -53,9 +56,9 @@ struct Pages {
     int raw;
     bool there;
     __device__ __forceinline__ void fetch(const CacheParams &c, int b, int kv_len, int tile, int lane) {
-        const long long pos = (long long)tile * kKeyTile + (long long)lane * c.page_size;
-        there = lane < kKeyTile / c.page_size && pos < kv_len;
-        raw = there ? c.page_table[(long long)b * c.max_pages + pos / c.page_size] : 0;
+        const int per_tile = kKeyTile >> page_shift(c), at = tile * per_tile + lane;
+        there = lane < per_tile && (uint32_t)at << page_shift(c) < (uint32_t)kv_len;
+        raw = there ? c.page_table[(long long)b * c.max_pages + at] : 0;
     }
     __device__ __forceinline__ int check(const CacheParams &c, unsigned int *err) const {
         if (!there) return c.num_pages;
@@ -69,11 +72,12 @@ struct Pages {
 __device__ __forceinline__ void load_tile(const CUtensorMap *map, uint8_t *dst, uint64_t *bar, int page,
                                           int page_size, int head) {
     if (elect()) mbar_arrive_expect_tx(bar, kTileBytes);
-    for (int l = 0; l < kKeyTile / page_size; ++l) {
+#pragma unroll 1
+    for (int row = 0, l = 0; row < kKeyTile; row += page_size, ++l) {
         const int at = __shfl_sync(0xffffffffu, page, l);
         if (elect()) {
-            tma_load_5d(dst + l * page_size * 128, map, bar, 0, 0, 0, head, at);
-            tma_load_5d(dst + l * page_size * 128 + kHalfBytes, map, bar, 0, 0, 1, head, at);
+            tma_load_5d(dst + row * 128, map, bar, 0, 0, 0, head, at);
+            tma_load_5d(dst + row * 128 + kHalfBytes, map, bar, 0, 0, 1, head, at);
         }
     }
     __syncwarp();
@@ -102,65 +106,64 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-// Sum of work(b) over the requests, and the request within whose work place x lies with the place where that begins (false
-// behind the last one's).  One warp, eight requests a lane and step, whose lengths are fetched together.
-template <class Work>
-__device__ __forceinline__ long long sum_work(int B, Work work) {
-    const int lane = threadIdx.x & 31;
-    long long all = 0;
-    for (int b0 = lane * 8; b0 < B; b0 += 256) {
-        long long w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = b0 + i < B ? work(b0 + i) : 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) all += w[i];
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
-    return all;
+// Requests in groups, one for each of kGroups warps.
+template <int kGroups>
+__device__ __forceinline__ uint32_t group_size(int B) {
+    return (((uint32_t)B + kGroups * 32 - 1) / (kGroups * 32)) * 32;
 }
-template <class Work>
-__device__ __forceinline__ bool find_request(int B, long long x, int &b, long long &first, Work work) {
+__device__ __forceinline__ long long scan_lanes(long long x) {
     const int lane = threadIdx.x & 31;
-    long long before = 0;
-    for (int b0 = 0; b0 < B; b0 += 256) {
-        long long w[8], mine = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = b0 + lane * 8 + i < B ? work(b0 + lane * 8 + i) : 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mine += w[i];
-        long long upto = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, upto, d);
-            if (lane >= d) upto += y;
-        }
-        upto += before;
-        const unsigned hit = __ballot_sync(0xffffffffu, x >= upto - mine && x < upto);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            long long at = upto - mine;
-            int found = b0 + lane * 8;
-#pragma unroll
-            for (int i = 0; i < 7; ++i)
-                if (x >= at + w[i] && found == b0 + lane * 8 + i) {
-                    at += w[i];
-                    ++found;
-                }
-            b = __shfl_sync(0xffffffffu, found, src);
-            first = __shfl_sync(0xffffffffu, at, src);
-            return true;
-        }
-        before = __shfl_sync(0xffffffffu, upto, 31);
+#pragma unroll 1
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
     }
-    return false;
+    return x;
 }
+// The sum of work(b) over the requests of every group, by warps 0 .. kGroups - 1.
+template <int kGroups, class Work>
+__device__ __forceinline__ void sum_groups(int B, long long *sums, Work work) {
+    const uint32_t size = group_size<kGroups>(B), begin = (threadIdx.x >> 5) * size;
+    const uint32_t end = min(begin + size, (uint32_t)B);
+    long long x = 0;
+#pragma unroll 1
+    for (uint32_t b = begin + (threadIdx.x & 31); b < end; b += 32) x += work((int)b);
+    x = scan_lanes(x);
+    if ((threadIdx.x & 31) == 31) sums[threadIdx.x >> 5] = x;
+}
+// The work of all requests, and the request within whose work place x = at(all) lies with the place where that begins (none
+// behind the last one's).  One warp.
+struct Place {
+    int b = -1;
+    long long first = 0;
+    template <int kGroups, class Work, class At>
+    __device__ __forceinline__ Place(const long long (&sums)[kGroups], int B, Work work, At at) {
+        const uint32_t lane = threadIdx.x & 31, size = group_size<kGroups>(B);
+        long long mine = lane < kGroups ? sums[lane] : 0, upto = scan_lanes(mine);
+        const long long x = at(__shfl_sync(0xffffffffu, upto, 31));
+        unsigned hit = __ballot_sync(0xffffffffu, x >= upto - mine && x < upto);
+        if (hit == 0) return;
+        int src = __ffs(hit) - 1;
+        first = __shfl_sync(0xffffffffu, upto - mine, src);
+#pragma unroll 1
+        for (uint32_t b0 = (uint32_t)src * size; b0 < (uint32_t)B; b0 += 32) {
+            mine = b0 + lane < (uint32_t)B ? work((int)(b0 + lane)) : 0;
+            upto = first + scan_lanes(mine);
+            hit = __ballot_sync(0xffffffffu, x >= upto - mine && x < upto);
+            src = hit ? __ffs(hit) - 1 : 31;
+            first = __shfl_sync(0xffffffffu, hit ? upto - mine : upto, src);
+            if (hit == 0) continue;
+            b = (int)b0 + src;
+            return;
+        }
+    }
+};
 
 // The work of a batch in equal runs, one per CTA, the first `more` of them one unit longer.
 struct Runs {
     long long each;
     int more, ctas;
-    __device__ __forceinline__ Runs(long long all, int ctas_) : each(all / ctas_), more((int)(all % ctas_)), ctas(ctas_) {}
+    __device__ __forceinline__ Runs(long long all, int ctas_) : each(all / ctas_), more((int)(all - each * ctas_)), ctas(ctas_) {}
     __device__ __forceinline__ long long start(int c) const { return each * c + min(c, more); }
 };
 

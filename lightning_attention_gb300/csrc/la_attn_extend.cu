@@ -68,7 +68,10 @@ struct Bars {
     uint64_t item_full[kItems], item_empty[kItems];
     Rec items[kItems];
     uint8_t parent[kItems][kMaxDrafts];  // of a tree's drafts; kNoParent: the context
-    float swap[2][2][kRowTile];  // between a row's threads: [row tile][half][row]
+    union {
+        float swap[2][2][kRowTile];  // between a row's threads: [row tile][half][row]
+        long long work[kMmaWarp];    // of groups of requests, until the first item is known
+    };
     int loads[2];  // of keys and of values, at the end
     uint32_t tmem_base;
 };
@@ -99,24 +102,22 @@ __device__ __forceinline__ bool request_of(const AttnParams &p, int b, Request &
 // costs besides, or one each where items are not cut.
 constexpr int kItemKeys = 400;
 static_assert(kItemKeys >= kKeyTile, "an item's work covers its tiles");
-__device__ __forceinline__ long long work_of(const AttnParams &p, const Request &r, long long items) {
+__device__ __forceinline__ long long work_of(const AttnParams &p, const Request &r, long long items, long long tok) {
     if (!p.split) return items;
-    const long long tok = 2 * (kRowTile / p.group);
     return items * (r.kv_len - r.n + kItemKeys) + tok * (items * (items + 1) / 2);
 }
 // The tile at which the first `done` of an item's work end; what it costs besides counts as its end.
 __device__ __forceinline__ int cut(long long done, int tiles) {
     return done <= 0 ? 0 : (int)min((long long)tiles, done / kKeyTile);
 }
-__device__ __forceinline__ int items_of(const AttnParams &p, const Request &r) {
-    const int tok = 2 * (kRowTile / p.group);
-    return (r.n + tok - 1) / tok;
-}
+// Tokens of an item, and a request's items of a kv head.
+__device__ __forceinline__ int tokens_of(const AttnParams &p) { return 2 * (kRowTile / p.group); }
+__device__ __forceinline__ int items_of(const Request &r, int tok) { return (int)((uint32_t)(r.n + tok - 1) / (uint32_t)tok); }
 
 // Work of a request; with `report` a faulty one, which has none, is reported.
-__device__ __forceinline__ long long request_work(const AttnParams &p, int b, bool report) {
+__device__ __forceinline__ long long request_work(const AttnParams &p, int b, int tok, bool report) {
     Request r;
-    if (request_of(p, b, r)) return work_of(p, r, items_of(p, r)) * p.Hkv;
+    if (request_of(p, b, r)) return work_of(p, r, items_of(r, tok), tok) * p.Hkv;
     if (report && (p.cu_seqlens != nullptr || r.kv_len != 0)) atomicOr(p.err, ERR_BIT_SEQLENS);
     return 0;
 }
@@ -125,88 +126,84 @@ __device__ __forceinline__ long long request_work(const AttnParams &p, int b, bo
 struct Item {
     Request r;
     int b, kvh, t, tok0, tiles;
+    int tok, count;  // tokens of an item, items of the request
     long long at, size;
     // the item whose work holds place x of request b, whose work begins at `first`
     __device__ __forceinline__ void find(const AttnParams &p, int b_, long long first, long long x) {
         b = b_;
         request_of(p, b, r);
-        const int count = items_of(p, r);
-        const long long head = work_of(p, r, count);
+        count = items_of(r, tok);
+        const long long head = work_of(p, r, count, tok);
         kvh = (int)((x - first) / head);
         const long long rem = x - first - kvh * head;
         int lo = 0, hi = count - 1;
         while (lo < hi) {  // the last t whose work begins at rem or before
             const int mid = (lo + hi + 1) >> 1;
-            if (work_of(p, r, mid) <= rem)
+            if (work_of(p, r, mid, tok) <= rem)
                 lo = mid;
             else
                 hi = mid - 1;
         }
-        set(p, lo, first + kvh * head + work_of(p, r, lo));
+        t = lo;
+        at = first + kvh * head + work_of(p, r, lo, tok);
     }
-    __device__ __forceinline__ void set(const AttnParams &p, int t_, long long at_) {
-        const int tok = 2 * (kRowTile / p.group);
-        t = t_;
-        at = at_;
-        size = work_of(p, r, t + 1) - work_of(p, r, t);
+    __device__ __forceinline__ void measure(const AttnParams &p) {
+        size = p.split ? r.kv_len - r.n + kItemKeys + (long long)tok * (t + 1) : 1;
         tok0 = t * tok;
         tiles = (r.kv_len - r.n + min(r.n, tok0 + tok) - 1) / kKeyTile + 1;
     }
     // the next one; false behind the last
     __device__ __forceinline__ bool next(const AttnParams &p) {
-        const long long end = at + size;
-        if (t + 1 < items_of(p, r)) {
-            set(p, t + 1, end);
-            return true;
-        }
-        if (++kvh == p.Hkv) {
-            kvh = 0;
-            do {
-                if (++b >= p.B) return false;
-            } while (!request_of(p, b, r) || r.n == 0);
-        }
-        set(p, 0, end);
+        at += size;
+        if (++t < count) return true;
+        t = 0;
+        if (++kvh < p.Hkv) return true;
+        kvh = 0;
+        do {
+            if (++b >= p.B) return false;
+        } while (!request_of(p, b, r) || r.n == 0);
+        count = items_of(r, tok);
         return true;
     }
 };
 
-// The items of a CTA's run, those of which it has no tile left out.
+// The items of a CTA's run, those of which it has no tile left out.  Its code is fetched anew for every item, so there is
+// one copy of each step.
 struct Walk {
     Item it;
     Runs runs;
     long long lo, hi;
     int j0, j1;
-    bool live;
+    bool begun = false;
     int tail_tiles = 0;  // the item inside which the run ends, if an earlier one does not: 0 if there is none
     Item tail;
     // one warp
-    __device__ __forceinline__ Walk(const AttnParams &p) : runs(sum_work(p.B, [&](int x) { return request_work(p, x, blockIdx.x == 0); }), gridDim.x) {
-        lo = runs.start(blockIdx.x);
-        hi = runs.start(blockIdx.x + 1);
-        live = lo < hi;
-        if (!live) return;
-        int b = 0;
-        long long first = 0;
-        find_request(p.B, lo, b, first, [&](int x) { return request_work(p, x, false); });
-        it.find(p, b, first, lo);
-        settle(p);
+    __device__ __forceinline__ Walk(const AttnParams &p, const long long (&sums)[kMmaWarp]) : runs(0, 1) {
+        it.tok = tokens_of(p);
+        const Place place(
+            sums, p.B, [&](int x) { return request_work(p, x, it.tok, false); },
+            [&](long long all) {
+                runs = Runs(all, gridDim.x);
+                lo = runs.start(blockIdx.x);
+                hi = runs.start(blockIdx.x + 1);
+                return lo;
+            });
+        if (lo < hi) it.find(p, place.b, place.first, lo);
     }
-    __device__ __forceinline__ void settle(const AttnParams &p) {
-        while (live) {
+    // the next item of which a tile is the CTA's; false: there is none
+    __device__ __forceinline__ bool next(const AttnParams &p) {
+        while (true) {
+            if (begun ? !it.next(p) || it.at >= hi : lo >= hi) return false;
+            begun = true;
+            it.measure(p);
             j0 = cut(lo - it.at, it.tiles);
             j1 = hi >= it.at + it.size ? it.tiles : cut(hi - it.at, it.tiles);
             if (it.at >= lo && it.at + it.size > hi) {
                 tail = it;
                 tail_tiles = it.tiles;
             }
-            if (j0 < j1) return;
-            advance(p);
+            if (j0 < j1) return true;
         }
-    }
-    __device__ __forceinline__ void advance(const AttnParams &p) { live = it.next(p) && it.at < hi; }
-    __device__ __forceinline__ void next(const AttnParams &p) {
-        advance(p);
-        settle(p);
     }
 };
 
@@ -530,7 +527,7 @@ __device__ void mma_role(const AttnParams &p, Bars *bars, uint8_t *sm, uint32_t 
         const Rec &it = bars->items[item % kItems];
         const int j0 = __shfl_sync(0xffffffffu, it.j0, 0), nt = __shfl_sync(0xffffffffu, it.j1, 0) - j0;
         const int kv_len = __shfl_sync(0xffffffffu, it.kv_len, 0);
-        const int end = kv_len % p.cache.page_size;
+        const int end = kv_len & (p.cache.page_size - 1);
         if (nt <= 0) break;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->item_empty[item % kItems]);
@@ -613,9 +610,12 @@ struct Ring {
 
 // No copy may be in flight when the CTA exits: the last load into every slot, of those that the two warps made.
 __device__ void drain_ring(Bars *bars, const Waiter &wait) {
+#pragma unroll 1
     for (int s = 0; s < kSlots; ++s) {
         int last = -1;
+#pragma unroll 1
         for (int kv = 0; kv < 2; ++kv)  // load n of warp kv is number 2 n + kv of the ring
+#pragma unroll 1
             for (int n = max(0, bars->loads[kv] - kSlots); n < bars->loads[kv]; ++n)
                 if ((2 * n + kv) % kSlots == s) last = max(last, 2 * n + kv);
         if (last >= 0) wait(&bars->full[s], (uint32_t)(last / kSlots) & 1);
@@ -636,6 +636,7 @@ __device__ __forceinline__ bool parents_of(const AttnParams &p, int b, int lane,
     return __all_sync(0xffffffffu, sound);
 }
 
+template <bool kTree>
 __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUtensorMap *tk, Bars *bars, uint8_t *sm,
                           int lane, const Waiter &wait) {
     const int row_tok = kRowTile / p.group;
@@ -652,8 +653,8 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
         }
         __syncwarp();
     };
-    Walk wk(p);
-    for (; wk.live && ok; wk.next(p), ++item) {
+    Walk wk(p, bars->work);
+    for (; ok && wk.next(p); ++item) {
         const Item &it = wk.it;
         Pages pages;
         pages.fetch(p.cache, it.b, it.r.kv_len, wk.j0, lane);
@@ -668,7 +669,7 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
         r.j1 = wk.j1;
         r.whole = wk.j0 == 0 && wk.j1 == it.tiles;
         r.sound = 1;
-        if (p.parents) {
+        if constexpr (kTree) {
             int up[4];
             r.sound = parents_of(p, it.b, lane, up);
             if (!r.sound && lane == 0) atomicOr(p.err, ERR_BIT_PARENTS);
@@ -698,8 +699,10 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
             asked = item + 1;
         }
     }
-    int up[4];
-    if (p.parents && wk.tail_tiles > 0 && !parents_of(p, wk.tail.b, lane, up)) wk.tail_tiles = 0;  // left as it was
+    if constexpr (kTree) {
+        int up[4];
+        if (wk.tail_tiles > 0 && !parents_of(p, wk.tail.b, lane, up)) wk.tail_tiles = 0;  // left as it was
+    }
     if (p.split && lane == 0) {
         const Item &it = wk.tail;
         static_cast<Tail *>(p.ws)[blockIdx.x] = {wk.runs, it.at, it.size, wk.tail_tiles, it.b, it.kvh, it.tok0, it.r.t0, it.r.n};
@@ -773,6 +776,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
     }
     pdl_wait();
+    if (warp < kMmaWarp)
+        sum_groups<kMmaWarp>(p.B, bars->work, [&](int x) { return request_work(p, x, tokens_of(p), blockIdx.x == 0); });
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -787,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kMmaWarp)
             mma_role(p, bars, sm, tbase, lane, wait);
         else if (warp == kLoadWarp)
-            load_role(p, &tq, &tk, bars, sm, lane, wait);
+            load_role<kTree>(p, &tq, &tk, bars, sm, lane, wait);
         else if (warp == kValueWarp)
             value_role(p, &tv, bars, sm, lane, wait);
     }

@@ -64,7 +64,10 @@ struct Bars {
     uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], p_empty[2], o_full, o_free, drain;
     alignas(16) float neg_m[RP];        // minus the references, in log 2
     alignas(16) float factor[RP];
-    float top[4][RP];
+    union {
+        float top[4][RP];
+        long long work[kMmaWarp];  // of groups of requests, until the first item is known
+    };
     uint8_t tok_of[RP];
     uint32_t below[RP][2];              // below[a] bit t: draft t is a or descends from it
     int loads[2];                       // of keys and of values, at the end
@@ -95,36 +98,42 @@ struct Walk {
     int b, kvh, tiles, j0, j1, kv_len, extra;
     Runs runs;
     long long at, lo, hi;  // where the item begins; the run
-    bool live;
+    bool begun = false;
     int tail_tiles = 0, tail_b, tail_kvh;  // the item inside which the run ends, if an earlier one does not
     long long tail_at;
     // one warp
-    __device__ __forceinline__ Walk(const AttnParams &p, int extra_, long long all)
-        : extra(extra_), runs(all, (int)max(1ll, min((long long)gridDim.x, all))) {
-        lo = runs.start(min((int)blockIdx.x, runs.ctas));
-        hi = runs.start(min((int)blockIdx.x + 1, runs.ctas));
-        live = lo < hi;
-        if (!live) return;
-        long long first;
-        find_request(p.B, lo, b, first, [&](int x) { return request_work(p, x, extra); });
+    __device__ __forceinline__ Walk(const AttnParams &p, int extra_, const long long (&sums)[kMmaWarp]) : extra(extra_), runs(0, 1) {
+        const Place place(
+            sums, p.B, [&](int x) { return request_work(p, x, extra); },
+            [&](long long all) {
+                runs = Runs(all, (int)max(1ll, min((long long)gridDim.x, all)));
+                lo = runs.start(min((int)blockIdx.x, runs.ctas));
+                hi = runs.start(min((int)blockIdx.x + 1, runs.ctas));
+                return lo;
+            });
+        if (lo >= hi) return;
+        b = place.b;
         tiles = tiles_of(p, b);
         kv_len = p.cache.kv_lens[b];
-        kvh = (int)((lo - first) / work_of(tiles, extra));
-        at = first + (long long)kvh * work_of(tiles, extra);
-        settle(p);
+        kvh = (int)((lo - place.first) / work_of(tiles, extra));
+        at = place.first + (long long)kvh * work_of(tiles, extra);
     }
-    __device__ __forceinline__ void advance(const AttnParams &p) {
+    __device__ __forceinline__ bool advance(const AttnParams &p) {
         at += work_of(tiles, extra);
-        live = at < hi;
-        if (!live || ++kvh < p.Hkv) return;
+        if (at >= hi) return false;
+        if (++kvh < p.Hkv) return true;
         kvh = 0;
         do {
             tiles = tiles_of(p, ++b);  // at < hi: a request with keys follows
         } while (tiles == 0);
         kv_len = p.cache.kv_lens[b];
+        return true;
     }
-    __device__ __forceinline__ void settle(const AttnParams &p) {
-        while (live) {
+    // the next item of which a tile is the CTA's; false: there is none
+    __device__ __forceinline__ bool next(const AttnParams &p) {
+        while (true) {
+            if (begun ? !advance(p) : lo >= hi) return false;
+            begun = true;
             j0 = cut(lo - at, tiles);
             j1 = cut(hi - at, tiles);
             if (at >= lo && at + work_of(tiles, extra) > hi) {
@@ -133,13 +142,8 @@ struct Walk {
                 tail_kvh = kvh;
                 tail_at = at;
             }
-            if (j0 < j1) return;
-            advance(p);
+            if (j0 < j1) return true;
         }
-    }
-    __device__ __forceinline__ void next(const AttnParams &p) {
-        advance(p);
-        settle(p);
     }
 };
 
@@ -491,7 +495,7 @@ __device__ void mma_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint3
     }
     while (j0 < j1 && ok) {
         const int from = j0, to = j1;
-        const int end = kv_len % p.cache.page_size, last = (kv_len - 1) / kKeyTile;
+        const int end = kv_len & (p.cache.page_size - 1), last = (kv_len - 1) / kKeyTile;
         const int r0 = kv_len - last * kKeyTile, r1 = r0 - end + p.cache.page_size;
         for (int j = from; j < to && ok; ++j) {
             const int sv = slot;  // this tile's values, then the next tile's keys
@@ -587,8 +591,8 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
         }
         __syncwarp();
     };
-    Walk w(p, S::kExtra, sum_work(p.B, [&](int x) { return request_work(p, x, S::kExtra); }));
-    for (; w.live && ok; w.next(p), ++item) {
+    Walk w(p, S::kExtra, bars->work);
+    for (; ok && w.next(p); ++item) {
         Pages pages;
         pages.fetch(p.cache, w.b, w.kv_len, w.j0, lane);
         publish({w.b, w.kvh, w.kv_len, w.j0, w.j1, w.j0 == 0 && w.j1 == w.tiles});
@@ -646,9 +650,12 @@ __device__ void value_role(const AttnParams &p, const CUtensorMap *tv, Bars<RP> 
 template <int RP, int PER_SM>
 __device__ void drain_ring(Bars<RP> *bars, const Waiter &wait) {
     constexpr int n_slots = Shape<RP, PER_SM>::kSlots;
+#pragma unroll 1
     for (int s = 0; s < n_slots; ++s) {
         int last = -1;
+#pragma unroll 1
         for (int kv = 0; kv < 2; ++kv)  // load n of warp kv is number 2 n + kv of the ring
+#pragma unroll 1
             for (int n = max(0, bars->loads[kv] - n_slots); n < bars->loads[kv]; ++n)
                 if ((2 * n + kv) % n_slots == s) last = max(last, 2 * n + kv);
         if (last >= 0) wait(&bars->full[s], (uint32_t)(last / n_slots) & 1);
@@ -696,6 +703,7 @@ __global__ void __launch_bounds__(kThreads, Shape<RP, PER_SM>::kPerSm)
         }
     }
     pdl_wait();
+    if (warp < kMmaWarp) sum_groups<kMmaWarp>(p.B, bars->work, [&](int x) { return request_work(p, x, S::kExtra); });
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
