@@ -163,7 +163,8 @@ struct Place {
 struct Runs {
     long long each;
     int more, ctas;
-    __device__ __forceinline__ Runs(long long all, int ctas_) : each(all / ctas_), more((int)(all - each * ctas_)), ctas(ctas_) {}
+    __device__ __forceinline__ Runs(long long all, int ctas_)
+        : each(all / ctas_), more((int)(all - each * ctas_)), ctas(ctas_) {}
     __device__ __forceinline__ long long start(int c) const { return each * c + min(c, more); }
 };
 

@@ -12,11 +12,12 @@
 // tile's softmax runs, the tensor cores work on the other tile:
 //     S0(j) S1(j) | O0 += P0 V, S0(j+1) | O1 += P1 V, S1(j+1) | ...
 // Warps 0-7 and 8-15: softmax of tile 0 and 1, two threads a row, one for each half of the keys (one thread took
-// 1400 cycles a tile: with the row's MMAs 2850 in place of 2048); warp 16 issues the MMAs; warp 17 works out the
+// 1400 cycles a tile, which with the row's MMAs made 2850 of 2048); warp 16 issues the MMAs; warp 17 works out the
 // items and loads queries and keys, warp 18 the values (TMA, a box per page and half of the columns).
 //
-// Bound by the tensor cores: 32 MMAs of 64 cycles per item and key tile, 65 measured.  That leaves a row's threads 1024
-// cycles from S to P, so they go over S once: weights against the reference they have, and the largest of them beside.
+// Long prompts are bound by the tensor cores: 32 MMAs of 64 cycles per item and key tile, 65 measured (16,384 tokens, 32
+// heads on 8: 1300 to 1400 us as the clock goes, 1145 with the MMAs alone; floor 1139).  That leaves a row's threads
+// 1024 cycles from S to P, so they go over S once: weights against the reference they have, and the largest of them beside.
 // The reference follows only when a weight passes 2^8 (then, and for an item's first tile, S is read twice, and O,
 // which lies in tensor memory, is rescaled): sums stay far inside fp32.
 // P is rounded to bf16 (2^-9 of each weight, independent errors: as much as out's own rounding), the sums
@@ -24,7 +25,10 @@
 //
 // Items differ in length by orders of magnitude, so a CTA per SM takes an equal run of the whole batch's work,
 // item by item, and may begin and end inside one; what it leaves of those, unnormalised, a second launch joins in a
-// fixed order.
+// fixed order.  Between two items nothing hides what they need once: an item's rows go out behind the next one's first
+// weights, while the tensor cores go on (eight prompts of 512 to 4096 tokens, 32 heads on 4: 437 -> 426 us), and the
+// code of all roles is kept small, as 16 to 20 warps at different places of it fetch it anew for every item (with
+// 184 KB, two thirds of it the walk over the items, 64 prompts of 200 to 400 tokens took 151 us, with 71 KB 114).
 #include <string.h>
 
 #include <algorithm>
@@ -99,8 +103,9 @@ __device__ __forceinline__ bool request_of(const AttnParams &p, int b, Request &
 }
 
 // Work of a kv head's first `items` items of a request: the keys that they see and kItemKeys each for what an item
-// costs besides, or one each where items are not cut.
-constexpr int kItemKeys = 400;
+// costs besides, or one each where items are not cut.  (Eight prompts of 512 to 4096 tokens: 430 us with 200, 414 with
+// 260, 417 with 320, 422 with 400.)
+constexpr int kItemKeys = 260;
 static_assert(kItemKeys >= kKeyTile, "an item's work covers its tiles");
 __device__ __forceinline__ long long work_of(const AttnParams &p, const Request &r, long long items, long long tok) {
     if (!p.split) return items;
@@ -112,7 +117,9 @@ __device__ __forceinline__ int cut(long long done, int tiles) {
 }
 // Tokens of an item, and a request's items of a kv head.
 __device__ __forceinline__ int tokens_of(const AttnParams &p) { return 2 * (kRowTile / p.group); }
-__device__ __forceinline__ int items_of(const Request &r, int tok) { return (int)((uint32_t)(r.n + tok - 1) / (uint32_t)tok); }
+__device__ __forceinline__ int items_of(const Request &r, int tok) {
+    return (int)(((uint32_t)r.n + tok - 1) / (uint32_t)tok);
+}
 
 // Work of a request; with `report` a faulty one, which has none, is reported.
 __device__ __forceinline__ long long request_work(const AttnParams &p, int b, int tok, bool report) {
@@ -124,10 +131,10 @@ __device__ __forceinline__ long long request_work(const AttnParams &p, int b, in
 
 // An item: rows of request b from token tok0 on, kv head kvh, its work [at, at + size), its tiles of keys.
 struct Item {
-    Request r;
-    int b, kvh, t, tok0, tiles;
-    int tok, count;  // tokens of an item, items of the request
-    long long at, size;
+    Request r = {};
+    int b = 0, kvh = 0, t = 0, tok0 = 0, tiles = 0;
+    int tok = 1, count = 0;  // tokens of an item, items of the request
+    long long at = 0, size = 0;
     // the item whose work holds place x of request b, whose work begins at `first`
     __device__ __forceinline__ void find(const AttnParams &p, int b_, long long first, long long x) {
         b = b_;
@@ -175,8 +182,6 @@ struct Walk {
     long long lo, hi;
     int j0, j1;
     bool begun = false;
-    int tail_tiles = 0;  // the item inside which the run ends, if an earlier one does not: 0 if there is none
-    Item tail;
     // one warp
     __device__ __forceinline__ Walk(const AttnParams &p, const long long (&sums)[kMmaWarp]) : runs(0, 1) {
         it.tok = tokens_of(p);
@@ -190,18 +195,17 @@ struct Walk {
             });
         if (lo < hi) it.find(p, place.b, place.first, lo);
     }
-    // the next item of which a tile is the CTA's; false: there is none
-    __device__ __forceinline__ bool next(const AttnParams &p) {
+    // The next item of which a tile is the CTA's; false: there is none.  tail(): the item is the one inside which the run
+    // ends, and no earlier run does.
+    template <class TailOf>
+    __device__ __forceinline__ bool next(const AttnParams &p, TailOf tail) {
         while (true) {
             if (begun ? !it.next(p) || it.at >= hi : lo >= hi) return false;
             begun = true;
             it.measure(p);
             j0 = cut(lo - it.at, it.tiles);
             j1 = hi >= it.at + it.size ? it.tiles : cut(hi - it.at, it.tiles);
-            if (it.at >= lo && it.at + it.size > hi) {
-                tail = it;
-                tail_tiles = it.tiles;
-            }
+            if (it.at >= lo && it.at + it.size > hi) tail();
             if (j0 < j1) return true;
         }
     }
@@ -327,8 +331,10 @@ __device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, in
     const int stage = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, pair = stage * 4 + quarter;
     const uint32_t lanes = (uint32_t)quarter << 21;  // in the address's upper half
     const uint32_t ts = tbase + kTmS + stage * 128 + lanes, to = tbase + kTmO + stage * 128 + half * 64 + lanes;
-    const int row = quarter * 32 + lane, row_tok = kRowTile / p.group;
-    const int tok_of = stage * row_tok + row / p.group, head = row % p.group;
+    const int row = quarter * 32 + lane;
+    // the row's token and head of an item, 8 bits each; -1: it has none
+    int mine = kRowTile / p.group;
+    mine = row < mine * p.group ? (stage * mine + row / p.group) << 8 | row % p.group : -1;
     const float c = p.scale_log2;
     if (p.cu_seqlens == nullptr) {  // rows without keys: a request of no positions
         for (int b = blockIdx.x; b < p.B; b += gridDim.x)
@@ -338,18 +344,20 @@ __device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, in
     }
     bool ok = true;
     uint32_t tile = 0, item = 0;
+    float done_l = 0.f, done_m = 0.f;  // the item before: the row's sum and minus its reference
     for (;; ++item) {
         ok = ok && __all_sync(0xffffffffu, wait(&bars->item_full[item % kItems], (item / kItems) & 1));
-        Rec it = bars->items[item % kItems];
-        if (pair_any(pair, !ok) || it.j1 <= it.j0) return;
-        const int tok = it.tok0 + tok_of;
-        const bool inside = row < row_tok * p.group && tok < it.n, valid = inside && it.sound;
+        const Rec it = bars->items[item % kItems];
+        const bool live = it.j1 > it.j0;
+        if (pair_any(pair, !ok)) return;
+        const int tok = it.tok0 + (mine >> 8);
+        const bool inside = mine >= 0 && tok < it.n;
         // Last column of this half, counted from the first key, that the row sees (rows that are not written take any),
         // and all rows and any row of the warp do.
         int limit = it.kv_len - it.n + (inside ? tok : it.n - 1) - half * 64, lo_limit, hi_limit;
         uint32_t up[4] = {0, 0, 0, 0};  // drafts that it sees, a bit each
         if constexpr (kTree) {
-            for (uint32_t a = inside ? tok : 0; a != kNoParent; a = bars->parent[item % kItems][a])
+            for (uint32_t a = inside ? tok : live ? 0 : kNoParent; a != kNoParent; a = bars->parent[item % kItems][a])
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if ((a >> 5) == i) up[i] |= 1u << (a & 31);
@@ -360,125 +368,138 @@ __device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, in
             lo_limit = __reduce_min_sync(0xffffffffu, limit);
             hi_limit = __reduce_max_sync(0xffffffffu, limit);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->item_empty[item % kItems]);
         float neg_m = kUnseen;
         float l4[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int j = it.j0; j < it.j1; ++j, ++tile) {
-            ok = ok && __all_sync(0xffffffffu, wait(&bars->s_full[stage], tile & 1));
-            tc_fence_after();
-            const int last = limit - j * kKeyTile, lo_last = lo_limit - j * kKeyTile, hi_last = hi_limit - j * kKeyTile;
-            auto seen = [&](int i) {
-                if constexpr (kTree)
-                    return drafts_seen(up, i * 32 - last);
-                else
-                    return columns_seen(last - i * 32);
-            };
-            uint32_t w[32];
-            float sum[4];
-            // Against the reference that there is; with the item's first tile, and once more where a weight passes 2^8,
-            // against a new one.  (One copy of the code: instructions that are fetched anew for every item cost more
-            // than what they do.)
-            bool fresh = j == it.j0;
-            while (true) {
-                if (fresh) {
-                    float top = largest(ts + half * 64, seen, lo_last, hi_last);
-                    bars->swap[stage][half][row] = top;
-                    if (pair_any(pair, !ok)) return;
-                    top = fmaxf(top, bars->swap[stage][half ^ 1][row]) * c;
-                    float f = 1.f;
-                    if (top > 8.f - neg_m) {
-                        f = neg_m == kUnseen ? 0.f : ex2z(-neg_m - top);
-                        neg_m = -top;
-                    }
-                    if (j > it.j0) {  // S(j) comes after O += P(j-1) V, which is complete
+        for (int j = it.j0; j == it.j0 || j < it.j1; ++j) {
+            if (live) {
+                ok = ok && __all_sync(0xffffffffu, wait(&bars->s_full[stage], tile & 1));
+                tc_fence_after();
+                const int last = limit - j * kKeyTile, lo_last = lo_limit - j * kKeyTile, hi_last = hi_limit - j * kKeyTile;
+                auto seen = [&](int i) {
+                    if constexpr (kTree)
+                        return drafts_seen(up, i * 32 - last);
+                    else
+                        return columns_seen(last - i * 32);
+                };
+                uint32_t w[32];
+                float sum[4];
+                // Against the reference that there is; with the item's first tile, and once more where a weight passes 2^8,
+                // against a new one.
+                bool fresh = j == it.j0;
+                while (true) {
+                    if (fresh) {
+                        float top = largest(ts + half * 64, seen, lo_last, hi_last);
+                        bars->swap[stage][half][row] = top;
+                        if (pair_any(pair, !ok)) return;
+                        top = fmaxf(top, bars->swap[stage][half ^ 1][row]) * c;
+                        float f = 1.f;
+                        if (top > 8.f - neg_m) {
+                            f = neg_m == kUnseen ? 0.f : ex2z(-neg_m - top);
+                            neg_m = -top;
+                        }
+                        if (j > it.j0) {  // S(j) was issued behind O += P(j-1) V, which is complete
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) l4[i] *= f;
+                            for (int i = 0; i < 4; ++i) l4[i] *= f;
 #pragma unroll 1
-                        for (int i = 0; i < 2; ++i) {
-                            uint32_t o[32];
-                            tmem_ld32(to + i * 32, o);
-                            tmem_ld_wait_regs(o);
+                            for (int i = 0; i < 2; ++i) {
+                                uint32_t o[32];
+                                tmem_ld32(to + i * 32, o);
+                                tmem_ld_wait_regs(o);
 #pragma unroll
-                            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                            tmem_st32(to + i * 32, o);
+                                for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                                tmem_st32(to + i * 32, o);
+                            }
                         }
                     }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sum[i] = l4[i];
+                    const float top = lo_last < 63 ? weigh<true>(ts + half * 64, seen, lo_last, hi_last, c, neg_m, w, sum)
+                                                   : weigh<false>(ts + half * 64, seen, lo_last, hi_last, c, neg_m, w, sum);
+                    // S has been read by both from here on
+                    if (!pair_any(pair, (!fresh && top > 8.f) || !ok)) break;
+                    fresh = true;
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sum[i] = l4[i];
-                const float top = lo_last < 63 ? weigh<true>(ts + half * 64, seen, lo_last, hi_last, c, neg_m, w, sum)
-                                               : weigh<false>(ts + half * 64, seen, lo_last, hi_last, c, neg_m, w, sum);
-                // S has been read by both from here on
-                if (!pair_any(pair, (!fresh && top > 8.f) || !ok)) break;
-                fresh = true;
+                for (int i = 0; i < 4; ++i) l4[i] = sum[i];
+                tmem_st32(ts + half * 32, w);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (elect()) mbar_arrive(&bars->p_full[stage]);
+                ++tile;
             }
+            // the rows of the item before, whose O is complete or about to be
+            if (j == it.j0 && item > 0) {
+                const Rec &was = bars->items[(item - 1) % kItems];
+                ok = ok && __all_sync(0xffffffffu, wait(&bars->o_full[stage], (item - 1) & 1));
+                if (pair_any(pair, !ok)) return;
+                tc_fence_after();
+                const int wtok = was.tok0 + (mine >> 8);
+                const bool valid = mine >= 0 && wtok < was.n && was.sound;
+                const long long out_row = (long long)(was.t0 + wtok) * p.H + was.kvh * p.group + (mine & 255);
+                const long long at = out_row * kHeadDim + half * 64;
+                if (was.whole) {
+                    const float f = 1.f / done_l;
+                    uint4 w[2][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) l4[i] = sum[i];
-            tmem_st32(ts + half * 32, w);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->p_full[stage]);
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t o[32];
+                        tmem_ld32(to + i * 32, o);
+                        tmem_ld_wait_regs(o);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            uint32_t y[4];
+#pragma unroll
+                            for (int z = 0; z < 4; ++z)
+                                y[z] = pack_bf16x2(__uint_as_float(o[8 * x + 2 * z]) * f,
+                                                   __uint_as_float(o[8 * x + 2 * z + 1]) * f);
+                            w[i][x] = make_uint4(y[0], y[1], y[2], y[3]);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (elect()) mbar_arrive(&bars->o_free[stage]);
+                    quad_transpose(w[0], lane);
+                    quad_transpose(w[1], lane);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int src = (lane & ~3) | k;
+                        const long long to_row = __shfl_sync(0xffffffffu, at, src);
+                        if (!__shfl_sync(0xffffffffu, (int)valid, src)) continue;
+                        uint4 *dst = reinterpret_cast<uint4 *>(p.out + to_row) + (lane & 3);
+                        dst[0] = w[0][k];
+                        dst[4] = w[1][k];
+                    }
+                } else {
+                    float *part = reinterpret_cast<float *>(static_cast<Tail *>(p.ws) + kAttnCtas) +
+                                  (2ll * blockIdx.x + (was.j0 == 0)) * kPieceFloats;
+                    uint4 *dst = reinterpret_cast<uint4 *>(part) + (pair * 32 + half * 16) * 32 + lane;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t o[32];
+                        tmem_ld32(to + i * 32, o);
+                        tmem_ld_wait_regs(o);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            dst[(8 * i + x) * 32] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                    }
+                    if (half == 0)
+                        reinterpret_cast<float2 *>(part + kItemRows * kHeadDim)[pair * 32 + lane] =
+                            make_float2(done_m == kUnseen ? -INFINITY : -done_m, done_l);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (elect()) mbar_arrive(&bars->o_free[stage]);
+                }
+                __syncwarp();
+                if (elect()) mbar_arrive(&bars->item_empty[(item - 1) % kItems]);
+            }
         }
-        float l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
-        bars->swap[stage][half][row] = l;
-        ok = ok && __all_sync(0xffffffffu, wait(&bars->o_full[stage], item & 1));
+        if (!live) return;
+        done_l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        done_m = neg_m;
+        bars->swap[stage][half][row] = done_l;
         if (pair_any(pair, !ok)) return;
-        l += bars->swap[stage][half ^ 1][row];
-        tc_fence_after();
-        const long long at = ((long long)(it.t0 + tok) * p.H + it.kvh * p.group + head) * kHeadDim + half * 64;
-        if (it.whole) {
-            const float f = 1.f / l;
-            uint4 w[2][4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t o[32];
-                tmem_ld32(to + i * 32, o);
-                tmem_ld_wait_regs(o);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    uint32_t y[4];
-#pragma unroll
-                    for (int z = 0; z < 4; ++z)
-                        y[z] = pack_bf16x2(__uint_as_float(o[8 * x + 2 * z]) * f, __uint_as_float(o[8 * x + 2 * z + 1]) * f);
-                    w[i][x] = make_uint4(y[0], y[1], y[2], y[3]);
-                }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->o_free[stage]);
-            quad_transpose(w[0], lane);
-            quad_transpose(w[1], lane);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int src = (lane & ~3) | k;
-                const long long to_row = __shfl_sync(0xffffffffu, at, src);
-                if (!__shfl_sync(0xffffffffu, (int)valid, src)) continue;
-                uint4 *dst = reinterpret_cast<uint4 *>(p.out + to_row) + (lane & 3);
-                dst[0] = w[0][k];
-                dst[4] = w[1][k];
-            }
-        } else {
-            float *part = reinterpret_cast<float *>(static_cast<Tail *>(p.ws) + kAttnCtas) +
-                          (2ll * blockIdx.x + (it.j0 == 0)) * kPieceFloats;
-            uint4 *dst = reinterpret_cast<uint4 *>(part) + (pair * 32 + half * 16) * 32 + lane;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t o[32];
-                tmem_ld32(to + i * 32, o);
-                tmem_ld_wait_regs(o);
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    dst[(8 * i + x) * 32] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-            }
-            if (half == 0)
-                reinterpret_cast<float2 *>(part + kItemRows * kHeadDim)[pair * 32 + lane] =
-                    make_float2(neg_m == kUnseen ? -INFINITY : -neg_m, l);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->o_free[stage]);
-        }
+        done_l += bars->swap[stage][half ^ 1][row];
     }
 }
 
@@ -654,7 +675,20 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
         __syncwarp();
     };
     Walk wk(p, bars->work);
-    for (; ok && wk.next(p); ++item) {
+    auto leave = [&](int tiles) {
+        const Item &it = wk.it;
+        if (p.split && lane == 0)
+            static_cast<Tail *>(p.ws)[blockIdx.x] = {wk.runs, it.at, it.size, tiles, it.b, it.kvh, it.tok0, it.r.t0, it.r.n};
+    };
+    auto tail = [&]() {
+        if constexpr (kTree) {
+            int up[4];
+            if (!parents_of(p, wk.it.b, lane, up)) return;  // left as it was
+        }
+        leave(wk.it.tiles);
+    };
+    leave(0);
+    for (; ok && wk.next(p, tail); ++item) {
         const Item &it = wk.it;
         Pages pages;
         pages.fetch(p.cache, it.b, it.r.kv_len, wk.j0, lane);
@@ -698,14 +732,6 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
             __syncwarp();
             asked = item + 1;
         }
-    }
-    if constexpr (kTree) {
-        int up[4];
-        if (wk.tail_tiles > 0 && !parents_of(p, wk.tail.b, lane, up)) wk.tail_tiles = 0;  // left as it was
-    }
-    if (p.split && lane == 0) {
-        const Item &it = wk.tail;
-        static_cast<Tail *>(p.ws)[blockIdx.x] = {wk.runs, it.at, it.size, wk.tail_tiles, it.b, it.kvh, it.tok0, it.r.t0, it.r.n};
     }
     Rec none = {};
     publish(none);
@@ -919,7 +945,8 @@ cudaError_t launch_attn_extend(const AttnParams &p, const AttnExtendPlan &plan, 
             configured[dev] = true;
         }
     }
-    e = launch_pdl(p.parents ? attn_extend_kernel<true> : attn_extend_kernel<false>, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, tq, tk, tv, p);
+    e = launch_pdl(p.parents ? attn_extend_kernel<true> : attn_extend_kernel<false>, dim3((unsigned)ctas), dim3(kThreads),
+                   kSmemBytes, stream, tq, tk, tv, p);
     if (e != cudaSuccess || !p.split || ctas == 1) return e;
     return launch_pdl(attn_join_kernel, dim3((unsigned)(ctas - 1), 8), dim3(256), 0, stream, p);
 }

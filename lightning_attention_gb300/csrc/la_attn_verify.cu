@@ -6,7 +6,7 @@
 // compute outweighs the loads: la_attn_extend.cu), each key read once.
 //
 // Bound by HBM: 512 bytes a key and kv head.  The work is the sequence of all tiles of 128 keys, request by
-// request and head by head, cut into equal runs, one CTA per SM each: the SMs finish together whatever the
+// request and head by head, cut into equal runs, one for each CTA: the SMs finish together whatever the
 // lengths.  A run may begin or end inside a (request, head); those leave unnormalised sums, which a second
 // launch joins in a fixed order.
 //
@@ -102,7 +102,8 @@ struct Walk {
     int tail_tiles = 0, tail_b, tail_kvh;  // the item inside which the run ends, if an earlier one does not
     long long tail_at;
     // one warp
-    __device__ __forceinline__ Walk(const AttnParams &p, int extra_, const long long (&sums)[kMmaWarp]) : extra(extra_), runs(0, 1) {
+    __device__ __forceinline__ Walk(const AttnParams &p, int extra_, const long long (&sums)[kMmaWarp])
+        : extra(extra_), runs(0, 1) {
         const Place place(
             sums, p.B, [&](int x) { return request_work(p, x, extra); },
             [&](long long all) {
@@ -405,21 +406,26 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
 #pragma unroll
             for (int r = 0; r < R; ++r)
                 l[r] = (bars->top[0][r0 + r] + bars->top[1][r0 + r]) + (bars->top[2][r0 + r] + bars->top[3][r0 + r]);
+            if (!sound) {
+            } else if (w.whole) {
+                __nv_bfloat16 *to = p.out + ((long long)w.b * p.N * p.H + w.kvh * p.group) * kHeadDim + key;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                if (r0 + r >= rows || !sound) break;
-                const int tok = bars->tok_of[r0 + r];
-                if (w.whole) {
-                    const int head = w.kvh * p.group + r0 + r - tok * p.group;
-                    p.out[(((long long)w.b * p.N + tok) * p.H + head) * kHeadDim + key] =
+                for (int r = 0; r < R; ++r) {
+                    if (r0 + r >= rows) break;
+                    to[(r0 + r + (int)bars->tok_of[r0 + r] * (p.H - p.group)) * kHeadDim] =
                         __float2bfloat16_rn(l[r] == 0.f ? 0.f : o[r] / l[r]);
-                } else {
+                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    if (r0 + r >= rows) break;
                     po[(r0 + r) * kHeadDim + key] = o[r];
-                    if (key == 0) {
-                        const float m = bars->neg_m[r0 + r];
-                        reinterpret_cast<float2 *>(po + RP * kHeadDim)[r0 + r] =
-                            make_float2(m == kUnseen ? -INFINITY : -m, l[r]);
-                    }
+                }
+                if (tid < rows) {
+                    const float m = bars->neg_m[tid];
+                    reinterpret_cast<float2 *>(po + RP * kHeadDim)[tid] =
+                        make_float2(m == kUnseen ? -INFINITY : -m,
+                                    (bars->top[0][tid] + bars->top[1][tid]) + (bars->top[2][tid] + bars->top[3][tid]));
                 }
             }
         }
