@@ -7,19 +7,20 @@
 //
 // An item is two tiles of up to 128 rows -- consecutive tokens x the query heads of one kv head, so
 // that the heads of a group share its keys -- and the tiles of 128 keys that they see.  Per key tile and row
-// tile, S = Q K^T (tcgen05, fp32 in tensor memory), P = exp2(S scale log2 e - m) by one thread per row
+// tile, S = Q K^T (tcgen05, fp32 in tensor memory), P = exp2(S scale log2 e - m) by two threads per row
 // (bf16, back into S's columns), O += P V (P from tensor memory, V as it lies in its page).  While one
 // tile's softmax runs, the tensor cores work on the other tile:
 //     S0(j) S1(j) | O0 += P0 V, S0(j+1) | O1 += P1 V, S1(j+1) | ...
-// Warps 0-7 and 8-15: softmax of tile 0 and 1, two threads a row, one for each half of the keys (one thread took
-// 1400 cycles a tile, which with the row's MMAs made 2850 of 2048); warp 16 issues the MMAs; warp 17 works out the
-// items and loads queries and keys, warp 18 the values (TMA, a box per page and half of the columns).
+// Warps 0-7 and 8-15: softmax of tile 0 and 1, a thread for each half of a row's keys (one thread took 1400 cycles
+// a tile, which with the row's MMAs made 2850 of 2048), its weights in two parts, so that O += P V begins with the first;
+// warp 16 issues the MMAs; warp 17 works out the items and loads queries and keys, warp 18 the values (TMA, a box per
+// page and half of the columns).
 //
 // Long prompts are bound by the tensor cores: 32 MMAs of 64 cycles per item and key tile, 65 measured (16,384 tokens, 32
 // heads on 8: 1300 to 1400 us as the clock goes, 1145 with the MMAs alone; floor 1139).  That leaves a row's threads
-// 1024 cycles from S to P, so they go over S once: weights against the reference they have, and the largest of them beside.
-// The reference follows only when a weight passes 2^8 (then, and for an item's first tile, S is read twice, and O,
-// which lies in tensor memory, is rescaled): sums stay far inside fp32.
+// 1024 cycles from S to P, so they do not look for the row's largest score first: exponents against the reference they
+// have, which follows only when a weight would pass 2^8 (S is then read again, and O, which lies in tensor memory,
+// rescaled): sums stay far inside fp32.
 // P is rounded to bf16 (2^-9 of each weight, independent errors: as much as out's own rounding), the sums
 // of its values are formed in fp32 before that.
 //
@@ -28,7 +29,7 @@
 // fixed order.  Between two items nothing hides what they need once: an item's rows go out behind the next one's first
 // weights, while the tensor cores go on (eight prompts of 512 to 4096 tokens, 32 heads on 4: 437 -> 426 us), and the
 // code of all roles is kept small, as 16 to 20 warps at different places of it fetch it anew for every item (with
-// 184 KB, two thirds of it the walk over the items, 64 prompts of 200 to 400 tokens took 151 us, with 71 KB 114).
+// 184 KB, two thirds of it the walk over the items, 64 prompts of 200 to 400 tokens took 151 us; with 64 KB 113).
 #include <string.h>
 
 #include <algorithm>
@@ -68,7 +69,7 @@ constexpr uint8_t kNoParent = 255;
 
 struct Bars {
     uint64_t full[kSlots], empty[kSlots];
-    uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], o_free[2], drain;
+    uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_full[2], o_free[2], drain;
     uint64_t item_full[kItems], item_empty[kItems];
     Rec items[kItems];
     uint8_t parent[kItems][kMaxDrafts];  // of a tree's drafts; kNoParent: the context
@@ -229,65 +230,34 @@ __device__ __forceinline__ uint32_t drafts_seen(const uint32_t (&up)[4], int d) 
     return __funnelshift_r(lo, hi, d & 31);
 }
 
-// Half a tile of a row: its weights against the reference as bf16 pairs in w, their sums in l (four partial ones),
-// the largest exponent returned.  seen(i): the columns of part i (32 of them) that the row sees, a bit each; all rows of
-// the warp see columns up to lo_last, none one past hi_last.  Scalar arithmetic: a packed fma.f32x2 takes 4.3 cycles a
-// warp, two fma.f32 2.6.
-template <bool kMask, class Seen>
-__device__ __forceinline__ float weigh(uint32_t ts, Seen seen, int lo_last, int hi_last, float c, float neg_m,
-                                       uint32_t (&w)[32], float (&l)[4]) {
-    float top[2] = {-INFINITY, -INFINITY};
+// 32 scores of a row of which it sees those with a bit in `bits`.
+__device__ __forceinline__ void mask_scores(uint32_t (&x)[32], uint32_t bits) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint32_t x[32];
-        if (kMask && hi_last < i * 32) {
-#pragma unroll
-            for (int y = 0; y < 16; ++y) w[i * 16 + y] = 0;
-            continue;
-        }
-        tmem_ld32(ts + i * 32, x);
-        tmem_ld_wait_regs(x);
-        if (kMask && lo_last < i * 32 + 31) {
-            const uint32_t bits = seen(i);
-#pragma unroll
-            for (int y = 0; y < 32; ++y)
-                if (!(bits & (1u << y))) x[y] = 0xff800000u;
-        }
-#pragma unroll
-        for (int y = 0; y < 16; ++y) {
-            float lo = fmaf(__uint_as_float(x[2 * y]), c, neg_m), hi = fmaf(__uint_as_float(x[2 * y + 1]), c, neg_m);
-            top[y & 1] = max3(top[y & 1], lo, hi);
-            lo = ex2z(lo);
-            hi = ex2z(hi);
-            l[(2 * y) & 3] += lo;
-            l[(2 * y + 1) & 3] += hi;
-            w[i * 16 + y] = pack_bf16x2(lo, hi);
-        }
-    }
-    return fmaxf(top[0], top[1]);
+    for (int y = 0; y < 32; ++y)
+        if (!(bits & (1u << y))) x[y] = 0xff800000u;
 }
-
-// The largest score of half a row's tile.
-template <class Seen>
-__device__ __forceinline__ float largest(uint32_t ts, Seen seen, int lo_last, int hi_last) {
-    float top[2] = {-INFINITY, -INFINITY};
+__device__ __forceinline__ float largest(const uint32_t (&x)[32], float top) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (hi_last < i * 32) continue;
-        uint32_t x[32];
-        tmem_ld32(ts + i * 32, x);
-        tmem_ld_wait_regs(x);
-        if (lo_last < i * 32 + 31) {
-            const uint32_t bits = seen(i);
+    for (int y = 0; y < 32; y += 2) top = max3(top, __uint_as_float(x[y]), __uint_as_float(x[y + 1]));
+    return top;
+}
+// The scores as exponents against the reference.  Scalar arithmetic: a packed fma.f32x2 takes 4.3 cycles a warp, two
+// fma.f32 2.6.
+__device__ __forceinline__ void exponents(uint32_t (&x)[32], float c, float neg_m) {
 #pragma unroll
-            for (int y = 0; y < 32; ++y)
-                if (!(bits & (1u << y))) x[y] = 0xff800000u;
-        }
+    for (int y = 0; y < 32; ++y) x[y] = __float_as_uint(fmaf(__uint_as_float(x[y]), c, neg_m));
+}
+// Their weights, to tensor memory as bf16 pairs, and added to four partial sums.
+__device__ __forceinline__ void weigh(const uint32_t (&x)[32], uint32_t tp, float (&l)[4]) {
+    uint32_t w[16];
 #pragma unroll
-        for (int y = 0; y < 32; y += 2)
-            top[(y >> 1) & 1] = max3(top[(y >> 1) & 1], __uint_as_float(x[y]), __uint_as_float(x[y + 1]));
+    for (int y = 0; y < 16; ++y) {
+        const float lo = ex2z(__uint_as_float(x[2 * y])), hi = ex2z(__uint_as_float(x[2 * y + 1]));
+        l[(2 * y) & 3] += lo;
+        l[(2 * y + 1) & 3] += hi;
+        w[y] = pack_bf16x2(lo, hi);
     }
-    return fmaxf(top[0], top[1]);
+    tmem_st16(tp, w);
 }
 
 // The two warps that share 32 rows; whether any of their threads says so.
@@ -330,7 +300,7 @@ template <bool kTree>
 __device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, int warp, int lane, const Waiter &wait) {
     const int stage = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, pair = stage * 4 + quarter;
     const uint32_t lanes = (uint32_t)quarter << 21;  // in the address's upper half
-    const uint32_t ts = tbase + kTmS + stage * 128 + lanes, to = tbase + kTmO + stage * 128 + half * 64 + lanes;
+    const uint32_t ts = tbase + kTmS + stage * 128 + half * 64 + lanes, to = tbase + kTmO + stage * 128 + half * 64 + lanes;
     const int row = quarter * 32 + lane;
     // the row's token and head of an item, 8 bits each; -1: it has none
     int mine = kRowTile / p.group;
@@ -353,8 +323,8 @@ __device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, in
         const int tok = it.tok0 + (mine >> 8);
         const bool inside = mine >= 0 && tok < it.n;
         // Last column of this half, counted from the first key, that the row sees (rows that are not written take any),
-        // and all rows and any row of the warp do.
-        int limit = it.kv_len - it.n + (inside ? tok : it.n - 1) - half * 64, lo_limit, hi_limit;
+        // and that all rows of the warp do.
+        int limit = it.kv_len - it.n + (inside ? tok : it.n - 1) - half * 64, lo_limit;
         uint32_t up[4] = {0, 0, 0, 0};  // drafts that it sees, a bit each
         if constexpr (kTree) {
             for (uint32_t a = inside ? tok : live ? 0 : kNoParent; a != kNoParent; a = bars->parent[item % kItems][a])
@@ -363,10 +333,8 @@ __device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, in
                     if ((a >> 5) == i) up[i] |= 1u << (a & 31);
             limit = it.kv_len - it.n - half * 64;  // where the drafts begin
             lo_limit = limit - 1;
-            hi_limit = limit + it.n - 1;
         } else {
             lo_limit = __reduce_min_sync(0xffffffffu, limit);
-            hi_limit = __reduce_max_sync(0xffffffffu, limit);
         }
         float neg_m = kUnseen;
         float l4[4] = {0.f, 0.f, 0.f, 0.f};
@@ -374,21 +342,27 @@ __device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, in
             if (live) {
                 ok = ok && __all_sync(0xffffffffu, wait(&bars->s_full[stage], tile & 1));
                 tc_fence_after();
-                const int last = limit - j * kKeyTile, lo_last = lo_limit - j * kKeyTile, hi_last = hi_limit - j * kKeyTile;
+                const int last = limit - j * kKeyTile, lo_last = lo_limit - j * kKeyTile;
                 auto seen = [&](int i) {
                     if constexpr (kTree)
                         return drafts_seen(up, i * 32 - last);
                     else
                         return columns_seen(last - i * 32);
                 };
-                uint32_t w[32];
-                float sum[4];
                 // Against the reference that there is; with the item's first tile, and once more where a weight passes 2^8,
                 // against a new one.
-                bool fresh = j == it.j0;
+                uint32_t x[2][32];
+                int state = j == it.j0;  // 1: a new reference is to be found, 2: it has been
                 while (true) {
-                    if (fresh) {
-                        float top = largest(ts + half * 64, seen, lo_last, hi_last);
+                    tmem_ld32(ts, x[0]);
+                    tmem_ld32(ts + 32, x[1]);
+                    tmem_ld_wait_regs2(x[0], x[1]);
+                    if (lo_last < 63) {
+                        mask_scores(x[0], seen(0));
+                        mask_scores(x[1], seen(1));
+                    }
+                    if (state == 1) {
+                        float top = fmaxf(largest(x[0], -INFINITY), largest(x[1], -INFINITY));
                         bars->swap[stage][half][row] = top;
                         if (pair_any(pair, !ok)) return;
                         top = fmaxf(top, bars->swap[stage][half ^ 1][row]) * c;
@@ -406,26 +380,29 @@ __device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, in
                                 tmem_ld32(to + i * 32, o);
                                 tmem_ld_wait_regs(o);
 #pragma unroll
-                                for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                                for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
                                 tmem_st32(to + i * 32, o);
                             }
+                            state = 2;
+                            continue;
                         }
                     }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sum[i] = l4[i];
-                    const float top = lo_last < 63 ? weigh<true>(ts + half * 64, seen, lo_last, hi_last, c, neg_m, w, sum)
-                                                   : weigh<false>(ts + half * 64, seen, lo_last, hi_last, c, neg_m, w, sum);
-                    // S has been read by both from here on
-                    if (!pair_any(pair, (!fresh && top > 8.f) || !ok)) break;
-                    fresh = true;
+                    exponents(x[0], c, neg_m);
+                    exponents(x[1], c, neg_m);
+                    if (state) break;
+                    const float top = fmaxf(largest(x[0], -INFINITY), largest(x[1], -INFINITY));
+                    if (!pair_any(pair, top > 8.f || !ok)) break;
+                    state = 1;
                 }
+                // a part of 32 keys at a time, so that the tensor cores begin with the first while the second is weighed
 #pragma unroll
-                for (int i = 0; i < 4; ++i) l4[i] = sum[i];
-                tmem_st32(ts + half * 32, w);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (elect()) mbar_arrive(&bars->p_full[stage]);
+                for (int i = 0; i < 2; ++i) {
+                    weigh(x[i], ts + i * 16, l4);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (elect()) mbar_arrive(&bars->p_full[stage][i]);
+                }
                 ++tile;
             }
             // the rows of the item before, whose O is complete or about to be
@@ -577,21 +554,30 @@ __device__ void mma_role(const AttnParams &p, Bars *bars, uint8_t *sm, uint32_t 
             const bool more = j + 1 < nt;
 #pragma unroll
             for (int stage = 0; stage < 2; ++stage) {
-                ok = ok && __all_sync(0xffffffffu, wait(&bars->p_full[stage], tile & 1));
+                const uint32_t b = kv_base + (uint32_t)sv * (kTileBytes >> 4) + ((uint32_t)(kHalfBytes >> 4) << 16);
                 if (ok && j == 0 && item > 0)  // the last item's O has been read
                     ok = __all_sync(0xffffffffu, wait(&bars->o_free[stage], (item - 1) & 1));
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t b = kv_base + (uint32_t)sv * (kTileBytes >> 4) + ((uint32_t)(kHalfBytes >> 4) << 16);
-                if (elect()) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_f16_tmem_a(tbase + kTmO + stage * 128, tbase + kTmS + stage * 128 + k * 8,
-                                       high | (b + k * 128), id_o, j > 0 || k > 0);
-                    if (stage == 1) mma_commit(&bars->empty[sv]);
-                    if (!more) mma_commit(&bars->o_full[stage]);
+                for (int part = 0; part < 2; ++part) {  // keys 0-31 and 64-95, then the others
+                    ok = ok && __all_sync(0xffffffffu, wait(&bars->p_full[stage][part], tile & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect()) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int k = (x >> 1) * 4 + part * 2 + (x & 1);
+                            const uint32_t weights = tbase + kTmS + stage * 128 + (k >> 2) * 64 + (k & 3) * 8;
+                            mma_f16_tmem_a(tbase + kTmO + stage * 128, weights, high | (b + k * 128), id_o,
+                                           j > 0 || part > 0 || x > 0);
+                        }
+                        if (part == 1) {
+                            if (stage == 1) mma_commit(&bars->empty[sv]);
+                            if (!more) mma_commit(&bars->o_full[stage]);
+                        }
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (!ok) break;
                 if (more) {
                     if (stage == 0) ok = full();
                     if (!ok) break;
@@ -678,7 +664,8 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
     auto leave = [&](int tiles) {
         const Item &it = wk.it;
         if (p.split && lane == 0)
-            static_cast<Tail *>(p.ws)[blockIdx.x] = {wk.runs, it.at, it.size, tiles, it.b, it.kvh, it.tok0, it.r.t0, it.r.n};
+            static_cast<Tail *>(p.ws)[blockIdx.x] = {wk.runs, it.at,   it.size,   tiles, it.b,
+                                                     it.kvh,  it.tok0, it.r.t0, it.r.n};
     };
     auto tail = [&]() {
         if constexpr (kTree) {
@@ -781,7 +768,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars->q_empty, 1);
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&bars->s_full[i], 1);
-                mbar_init(&bars->p_full[i], 8);
+                mbar_init(&bars->p_full[i][0], 8);
+                mbar_init(&bars->p_full[i][1], 8);
                 mbar_init(&bars->o_full[i], 1);
                 mbar_init(&bars->o_free[i], 8);
             }
