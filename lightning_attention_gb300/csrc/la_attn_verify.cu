@@ -5,7 +5,9 @@
 // for the R = (drafts) x (query heads of a kv head) rows r that share the keys, R at most 64 (with more, what is there to
 // compute outweighs the loads: la_attn_extend.cu), each key read once.
 //
-// Bound by HBM: 512 bytes a key and kv head.  The work is the sequence of all tiles of 128 keys, request by
+// Bound by HBM: 512 bytes a key and kv head (128 requests of 500 to 8000 positions, 32 heads on 4: 181 to 187 us, 0.93 to
+// 0.96 of the copy bandwidth; trees of 8 drafts, 64 requests of 1000 to 8000, 64 heads on 8: 189 to 196 us, 0.85 to
+// 0.88, as an item's first tile has to find the references of 64 rows).  The work is the sequence of all tiles of 128 keys, request by
 // request and head by head, cut into equal runs, one for each CTA: the SMs finish together whatever the
 // lengths.  A run may begin or end inside a (request, head); those leave unnormalised sums, which a second
 // launch joins in a fixed order.
