@@ -562,7 +562,7 @@ la_status la_kv_store(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, int6
  *                   la_attn_extend_workspace_size() bytes.  With NULL or less the call runs without it (same
  *                   results up to rounding).  Calls that share one must not overlap on the GPU.
  * Numerics: scores, running references and sums in fp32; weights as bf16 for their product with the values
- * (2^-9 of each weight, at random), accumulated in fp32; out is rounded to bf16 once.
+ * (at most 2^-8 of each weight, either way), accumulated in fp32; out is rounded to bf16 once.
  */
 la_status la_attn_extend(const la_bf16 *q, int64_t q_row_stride, const la_bf16 *k_pages, const la_bf16 *v_pages,
                          int64_t page_stride, int num_pages, int page_size, const int32_t *page_table, int max_pages,

@@ -17,11 +17,11 @@
 // page and half of the columns).
 //
 // Long prompts are bound by the tensor cores: 32 MMAs of 64 cycles per item and key tile, 65 measured (16,384 tokens, 32
-// heads on 8: 1300 to 1400 us as the clock goes, 1145 with the MMAs alone; floor 1139).  That leaves a row's threads
-// 1024 cycles from S to P, so they do not look for the row's largest score first: exponents against the reference they
-// have, which follows only when a weight would pass 2^8 (S is then read again, and O, which lies in tensor memory,
-// rescaled): sums stay far inside fp32.
-// P is rounded to bf16 (2^-9 of each weight, independent errors: as much as out's own rounding), the sums
+// heads on 8: 1300 to 1410 us as the power limit lets the clock go, 1145 with the MMAs alone; floor 1139, or 1279 at the
+// rate that large products sustain).  That leaves a row's threads 1024 cycles from S to P, so they do not look for the
+// row's largest score first: exponents against the reference they have, which follows only when a weight would pass 2^8
+// (S is then read again, and O, which lies in tensor memory, rescaled): sums stay far inside fp32.
+// P is rounded to bf16 (at most 2^-8 of each weight, either way: together about out's own rounding), the sums
 // of its values are formed in fp32 before that.
 //
 // Items differ in length by orders of magnitude, so a CTA per SM takes an equal run of the whole batch's work,

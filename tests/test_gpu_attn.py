@@ -89,7 +89,7 @@ def test_extend_runs(new, old, H, Hkv):
 def test_extend_split_and_whole():
     """Few rows over many keys run split; without scratch for that the same call runs whole."""
     new, old = [3, 40], [3000, 1200]
-    assert la.attn_extend_workspace_size(2, 43, 8, 2, D, 40, 3072) > 0
+    assert la.attn_extend_workspace_size(2, 43, 8, 2, D, 40, 3040) > 0
     a = check_extend(new, old, 8, 2, seed=9)
     none = torch.empty(0, dtype=torch.uint8, device=DEV)
     b = check_extend(new, old, 8, 2, seed=9, workspace=none)
@@ -194,6 +194,35 @@ def test_rising_scores():
     room = 2 * 138 * 2.0 ** -16
     check(f64(o1), want, size, room + TOL_PAIR, "decode")
     check(f64(o2), want, size, room + TOL_BF16, "extend")
+
+
+def test_rising_scores_of_a_prompt():
+    """The same for the rows of a prompt, whose references follow at different tiles; the second head sees none rise."""
+    P, L, n, H = 64, 900, 300, 2
+    cache = Cache([L], 1, P, 4)
+    at = torch.arange(L)
+    ramp = torch.exp(torch.linspace(-4, 2.5, L))[:, None]
+    pages = cache.table[0].long()[at // P]
+    cache.both[pages, 0, 0, at % P] = (torch.ones(L, D) * ramp).bfloat16()
+    q = torch.ones(n, H, D)
+    q[:, 1] = -1.0
+    q = q.reshape(n, H * D).bfloat16()
+    kp, vp, table, kv = cache.to(DEV)
+    out = la.attn_extend(q.to(DEV), kp, vp, table, i32([0, n]).to(DEV), kv)
+    la.poll_error()
+    kk, vv = cache.rows(0)
+    want, size = attn.attend(f64(q).reshape(n, H, D), kk, vv, attn.causal(n, L), SCALE)
+    check(f64(out), want, size, 2 * 138 * 2.0 ** -16 + TOL_BF16, "extend")
+
+
+@pytest.mark.parametrize("B", [31, 32, 33, 511, 512, 513, 1100])
+def test_many_requests(B):
+    """Batches that end before, at and behind the groups in which the requests' work is summed."""
+    rng = np.random.default_rng(B)
+    new, old = rng.integers(0, 6, B).tolist(), rng.integers(0, 40, B).tolist()
+    check_extend(new, old, 4, 2, P=16, seed=B, tail=2)
+    check_verify([int(x) for x in rng.integers(0, 60, B)], 0, 4, 2, P=16, seed=B)
+    check_verify([int(x) if x > 5 else 0 for x in rng.integers(0, 60, B)], 5, 32, 2, P=16, seed=B)
 
 
 def check_commit(lens, N, Hkv, P, accept, seed=0, in_place=False):
