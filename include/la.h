@@ -582,7 +582,7 @@ la_status la_attn_extend_workspace_size(int B, int T, int H, int Hkv, int D, int
  *   workspace       device scratch, 16-byte aligned, of at least la_attn_verify_workspace_size() bytes with N = 1 and
  *                   max_kvlen = max_pages * page_size (LA_ERR_INVALID otherwise): the keys are shared out evenly among
  *                   the SMs, and a second launch joins the requests that several of them shared.  Calls that share one
- *                   must not overlap on the GPU.
+ *                   must not overlap on the GPU.  Short contexts are not shared out and take none (0 bytes, NULL).
  * Numerics: as la_attn_extend, with the weights as bf16 pairs hi + lo (2^-16) where N * H / Hkv, the rows that share a kv
  * head's keys, is at most 64 (N = 1 here), as bf16 above.
  */

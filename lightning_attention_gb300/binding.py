@@ -848,9 +848,9 @@ def _attn_args(q, k_pages, v_pages, page_table, kv_lens, out, scale):
 
 
 def _scratch(workspace, dev, nbytes: int):
-    """(tensor, bytes): the caller's uint8 scratch, or nbytes of the current stream's own."""
+    """(tensor, bytes): the caller's uint8 scratch, or nbytes of the current stream's own (None: no bytes)."""
     if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev), nbytes
+        return (torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None), nbytes
     _need(workspace, "workspace", torch.uint8, dev)
     return workspace, workspace.numel()
 

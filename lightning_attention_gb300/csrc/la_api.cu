@@ -841,14 +841,15 @@ la_status attn_verify(const la_bf16 *q, int64_t q_rs, const la_bf16 *k_pages, co
     if (tree && (!parents || !aligned4(parents))) return LA_ERR_INVALID;
     const bool few = N * p.group <= la::kVerifyRows;
     const la::AttnExtendPlan plan = la::plan_attn_extend(B, p.T, H, Hkv, N, (long long)max_pages * page_size);
-    const unsigned long long need = few ? la::attn_verify_ws_bytes(N * p.group, (long long)max_pages * page_size) : plan.ws_bytes;
-    if (need > 0 && (!workspace || !aligned16(workspace) || (unsigned long long)workspace_bytes < need))
+    const unsigned long long need =
+        few ? la::attn_verify_ws_bytes(N * p.group, (long long)max_pages * page_size) : plan.ws_bytes;
+    if (!aligned16(workspace) || (need > 0 && (!workspace || (unsigned long long)workspace_bytes < need)))
         return LA_ERR_INVALID;
     p.parents = tree ? parents : nullptr;
     p.N = N;
     p.ws = workspace;
     p.max_seqlen = N;
-    p.split = plan.split;
+    p.split = need > 0;
     if ((st = error_word_ptr(&p.err)) != LA_OK) return st;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return launch_status(few ? la::launch_attn_verify(p, s) : la::launch_attn_extend(p, plan, s));

@@ -45,7 +45,7 @@ struct AttnParams {
     unsigned int *err;
     float scale_log2;            // scale * log2 e, positive
     int B, T, H, Hkv, group, N, max_seqlen;
-    int split;                   // extend: whether CTAs may share the keys of a tile of rows
+    int split;                   // whether CTAs may share the keys of a tile of rows, or of a request and kv head
     unsigned long long wait_limit_ns;
 };
 // Prompts: the tokens of a request are its last positions, each sees those at and before it.
@@ -59,7 +59,7 @@ AttnExtendPlan plan_attn_extend(long long B, long long T, int H, int Hkv, long l
 cudaError_t launch_attn_extend(const AttnParams &p, const AttnExtendPlan &plan, cudaStream_t stream);
 
 // N drafts (or one token) per request, the last N positions, N * group at most kVerifyRows; more go to
-// launch_attn_extend, with cu_seqlens null.
+// launch_attn_extend, with cu_seqlens null.  split: where there is a workspace to have (attn_verify_ws_bytes, 0: none).
 constexpr int kVerifyRows = 64;
 unsigned long long attn_verify_ws_bytes(int rows, long long max_kvlen);
 cudaError_t launch_attn_verify(const AttnParams &p, cudaStream_t stream);

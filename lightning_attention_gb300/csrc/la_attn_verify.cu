@@ -10,7 +10,7 @@
 // 0.88, as an item's first tile has to find the references of 64 rows).  The work is the sequence of all tiles of 128 keys, request by
 // request and head by head, cut into equal runs, one for each CTA: the SMs finish together whatever the
 // lengths.  A run may begin or end inside a (request, head); those leave unnormalised sums, which a second
-// launch joins in a fixed order.
+// launch joins in a fixed order.  Where contexts are short a (request, head) stays with the CTA in whose run it begins.
 //
 // With few rows the keys take the 128 lanes of the tensor cores: S^T = K Q^T and O^T += V^T P^T, both with
 // N = R (padded to 16, 32 or 64), K and V as they lie in their pages.  Two threads share a key in the
@@ -137,8 +137,8 @@ struct Walk {
         while (true) {
             if (begun ? !advance(p) : lo >= hi) return false;
             begun = true;
-            j0 = cut(lo - at, tiles);
-            j1 = cut(hi - at, tiles);
+            j0 = p.split ? cut(lo - at, tiles) : at < lo ? tiles : 0;
+            j1 = p.split ? cut(hi - at, tiles) : tiles;
             if (at >= lo && at + work_of(tiles, extra) > hi) {
                 tail_tiles = tiles;
                 tail_b = b;
@@ -622,7 +622,7 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
             ok = ring.load(p, bars, sm, tk, page, w.kvh, wait);
         }
     }
-    if (lane == 0)
+    if (p.split && lane == 0)
         static_cast<Tail *>(p.ws)[blockIdx.x] = {w.runs, w.tail_at, work_of(w.tail_tiles, w.extra), w.tail_tiles, w.tail_b,
                                                  w.tail_kvh, 0, w.tail_b * p.N, p.N};
     publish({});
@@ -839,20 +839,27 @@ cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
             configured[dev] = true;
         }
     }
-    return launch_pdl(attn_verify_kernel<RP, PER_SM>, dim3(kAttnCtas * Shape<RP, PER_SM>::kPerSm), dim3(kThreads), smem, stream, tq, tk, tv, p);
+    return launch_pdl(attn_verify_kernel<RP, PER_SM>, dim3(kAttnCtas * Shape<RP, PER_SM>::kPerSm), dim3(kThreads), smem,
+                      stream, tq, tk, tv, p);
 }
 
 int padded_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
-// One CTA an SM or two, by what a row of the page table can hold.  One / two, us, 32 heads on 4, 262,144 positions in requests of
-// 64 (the first 1024): 95 / 68, 128: 122 / 104, 256: 149 / 135, 384: 129 / 118, 512: 119 / 112, 768: 108 / 106,
+// One CTA an SM or two, by what a row of the page table can hold.  One / two, us, 32 heads on 4, 262,144 positions in
+// requests of 64 (the first 1024): 95 / 68, 128: 122 / 104, 256: 149 / 135, 384: 129 / 118, 512: 119 / 112, 768: 108 / 106,
 // 1024: 103.3 / 102.7, 2048: 98.4 / 99.6; 128 requests of 500-8000: 187 / 189, 2 of 115,000 on 8 heads: 146 / 151.
 constexpr long long kShortKeys = 1280;
 int per_sm(int rows, long long max_kvlen) { return rows <= 16 && max_kvlen <= kShortKeys ? 2 : 1; }
 
+// Whole (request, head)s, and no second launch, by the same.  Shared out / whole, us in a graph, 32 heads on 8: 1 request of 100
+// positions 7.9 / 6.2, of 256 9.0 / 8.8, of 512 9.7 / 11.4, 8 requests 8.4 / 6.7, 10.6 / 10.5, 12.1 / 13.4, 2 trees of 8
+// drafts 10.4 / 8.1, 12.2 / 10.3, 13.8 / 12.6; 1024 requests of 128, 32 heads on 4, 89 / 87.
+constexpr long long kWholeKeys = 256;
+
 }  // namespace
 
 unsigned long long attn_verify_ws_bytes(int rows, long long max_kvlen) {
+    if (max_kvlen <= kWholeKeys) return 0;
     return kMaxRuns * sizeof(Tail) +
            2ull * per_sm(rows, max_kvlen) * kAttnCtas * padded_rows(rows) * (kHeadDim + 2) * 4;
 }
@@ -868,8 +875,9 @@ cudaError_t launch_attn_verify(const AttnParams &p, cudaStream_t stream) {
                           : rp == 16       ? launch<16, 1>(tq, tk, tv, p, stream)
                           : rp == 32       ? launch<32, 1>(tq, tk, tv, p, stream)
                                            : launch<64, 1>(tq, tk, tv, p, stream);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(attn_verify_join_kernel, dim3((unsigned)(ctas - 1), (unsigned)(rp / 16)), dim3(256), 0, stream, p, rp);
+    if (e != cudaSuccess || !p.split) return e;
+    return launch_pdl(attn_verify_join_kernel, dim3((unsigned)(ctas - 1), (unsigned)(rp / 16)), dim3(256), 0, stream, p,
+                      rp);
 }
 
 }  // namespace la

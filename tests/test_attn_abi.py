@@ -113,9 +113,10 @@ def test_null_and_misaligned_pointers(lib):
               tree: ("table", "kv", "parents"), commit: ("table", "kv", "parents", "acc", "lens")}
     for wants, bad in ((wants16, BAD16), (wants4, BAD4)):
         for call, names in wants.items():
+            more = {"width": 17} if call in (decode, tree) else {}  # contexts that take scratch
             for name in names:
-                assert call(lib, **{name: bad}) == 1, (call, name)
-                assert call(lib, **{name: N}) == 1, (call, name)
+                assert call(lib, **more, **{name: bad}) == 1, (call, name)
+                assert call(lib, **more, **{name: N}) == 1, (call, name)
     for call in (rope, store):
         assert call(lib, freq=N) == 1 and call(lib, freq=ctypes.c_void_p(4096 + 4)) == 1
     assert extend(lib, ws=BAD16) == 1
@@ -141,9 +142,14 @@ def test_workspaces(lib):
         for B, kv in ((1, 200), (3, 5000), (300, 5000)):
             assert la.attn_verify_workspace_size(B, n, H, Hkv, 128, kv) == la.attn_extend_workspace_size(
                 B, B * n, H, Hkv, 128, n, kv)
-    need = la.attn_verify_workspace_size(2, 3, 2, 1, 128, 32)
-    assert tree(lib, nbytes=need - 1) == 1
-    assert decode(lib, nbytes=la.attn_verify_workspace_size(2, 1, 2, 1, 128, 32) - 1) == 1
+    need = la.attn_verify_workspace_size(2, 3, 2, 1, 128, 272)
+    assert tree(lib, width=17, nbytes=need - 1) == 1 and tree(lib, width=17, ws=N) == 1
+    assert decode(lib, width=17, nbytes=la.attn_verify_workspace_size(2, 1, 2, 1, 128, 272) - 1) == 1
+    # short contexts stay whole
+    for n, H, Hkv in ((1, 16, 1), (8, 8, 1), (3, 40, 2)):
+        assert la.attn_verify_workspace_size(3, n, H, Hkv, 128, 256) == 0
+        assert la.attn_verify_workspace_size(3, n, H, Hkv, 128, 257) > 0
+    assert tree(lib, ws=BAD16) == 1 and decode(lib, ws=BAD16) == 1
     assert tree(lib, H=128, P=128, nbytes=1000, width=9) == 1
     size = lib.la_attn_extend_workspace_size
     for args, st in (((-1, 1, 1, 1, 128, 1, 1), 1), ((1, -1, 1, 1, 128, 1, 1), 1), ((1, 1, 3, 2, 128, 1, 1), 1),
