@@ -194,6 +194,7 @@ struct Walk {
                 hi = runs.start(blockIdx.x + 1);
                 return lo;
             });
+        if (place.b < 0) hi = lo;  // none behind the last (nor where somebody changes the lengths meanwhile)
         if (lo < hi) it.find(p, place.b, place.first, lo);
     }
     // The next item of which a tile is the CTA's; false: there is none.  tail(): the item is the one inside which the run

@@ -114,6 +114,7 @@ struct Walk {
                 hi = runs.start(min((int)blockIdx.x + 1, runs.ctas));
                 return lo;
             });
+        if (place.b < 0) hi = lo;  // none behind the last (nor where somebody changes the lengths meanwhile)
         if (lo >= hi) return;
         b = place.b;
         tiles = tiles_of(p, b);
@@ -127,7 +128,8 @@ struct Walk {
         if (++kvh < p.Hkv) return true;
         kvh = 0;
         do {
-            tiles = tiles_of(p, ++b);  // at < hi: a request with keys follows
+            if (++b >= p.B) return false;
+            tiles = tiles_of(p, b);
         } while (tiles == 0);
         kv_len = p.cache.kv_lens[b];
         return true;
