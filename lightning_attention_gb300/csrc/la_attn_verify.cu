@@ -374,8 +374,8 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->p_full[pbuf]);
         }
-        if (!ok) break;
-        // the item's sums: over the lanes, each step with half the rows, then over the warps
+        // Where a wait ran out in some warps only, all go on to the next vote: the barriers until there count every thread.
+        // The item's sums: over the lanes, each step with half the rows, then over the warps.
         int row = r0;
 #pragma unroll
         for (int d = 16, n = R; d > 0; d >>= 1) {
@@ -396,7 +396,7 @@ __device__ void softmax_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, u
         bars->top[warp & 3][row] = sum[0];
         softmax_sync();
         // this thread holds column `key` of v
-        ok = __all_sync(0xffffffffu, wait(&bars->o_full, (uint32_t)item & 1));
+        ok = ok && __all_sync(0xffffffffu, wait(&bars->o_full, (uint32_t)item & 1));
         tc_fence_after();
         const int rows = p.N * p.group;
         const long long piece = 2ll * blockIdx.x + (w.j0 == 0 ? 1 : 0);

@@ -1,0 +1,147 @@
+"""The softmax roles of the attention kernels on the host: their source, cut out of the kernels' files and compiled with
+a fiber per thread (attn_roles_host.h).  Whichever wait of whichever warp runs out, all threads come to their end; and
+between a thread's write of a shared entry and another's access to it there is a barrier that both pass."""
+import os
+import re
+import shutil
+import subprocess
+
+import pytest
+
+from lightning_attention_gb300 import _build
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+pytestmark = pytest.mark.skipif(shutil.which("g++") is None, reason="no host compiler")
+
+
+def source(name):
+    with open(os.path.join(_build.CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def cut(text, pattern):
+    """The definition that begins with `pattern` at the start of a line, with the template line before it."""
+    m = re.search(r"^(?:template <[^\n]*>\n)?" + pattern, text, re.M)
+    assert m, pattern
+    depth, i = 0, text.index("{", m.end())
+    while True:
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        i += 1
+        if depth == 0:
+            break
+    return text[m.start():i] + (";" if pattern.startswith("struct") else "") + "\n"
+
+
+def constants(text, *names):
+    return "\n".join(re.search(rf"^constexpr [^;]*\b{n} = [^;]*;", text, re.M).group(0) for n in names) + "\n"
+
+
+def function(name):
+    return rf"[^\n(]*\b{name}\("
+
+
+def build(tmp_path, parts):
+    src, exe = tmp_path / "roles.cc", tmp_path / "roles"
+    src.write_text('#include "attn_roles_host.h"\n' + "\n".join(parts))
+    subprocess.run(["g++", "-std=c++17", "-O1", "-w", "-I", HERE, str(src), "-o", str(exe)], check=True)
+    return str(exe)
+
+
+def runs(exe, *args):
+    r = subprocess.run([exe, *map(str, args)], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+def common():
+    h = source("la_attn.h")
+    internal = source("la_internal.h")
+    return [constants(internal, "kHeadDim"), "typedef int cudaStream_t;\n", cut(internal, r"enum : unsigned int"), ";",
+            constants(h, "kVerifyRows", "kAttnCtas", "kMaxDrafts", "kKeyTile"), cut(h, "struct CacheParams"),
+            cut(h, "struct AttnParams"), "constexpr int kTileBytes = kKeyTile * kHeadDim * 2;\n",
+            "struct Tail { char bytes[56]; };\n"]
+
+
+MAIN = r"""
+static uint8_t *page(size_t n) { return static_cast<uint8_t *>(calloc(n, 1)); }
+int main(int argc, char **argv) {
+    rising = atoi(argv[2]);
+    const int lens[] = {300};
+    const int32_t parents[] = {-1, 0, 0, -1};
+    AttnParams p = {};
+    p.cache.kv_lens = lens;
+    p.cache.page_size = 16;
+    p.cache.max_pages = 100;
+    p.out = reinterpret_cast<__nv_bfloat16 *>(page(1 << 20));
+    p.ws = page(4 << 20);
+    unsigned err = 0;
+    p.err = &err;
+    p.scale_log2 = 1.f;
+    p.B = 1;
+    p.H = 4;
+    p.Hkv = 2;
+    p.group = 2;
+    p.N = 4;
+    p.T = 300;
+    p.split = 1;
+    const bool tree = atoi(argv[3]);
+    if (tree) p.parents = parents;
+    Bars_ *bars = reinterpret_cast<Bars_ *>(page(sizeof(Bars_)));
+    // items by the tiles that each has, at most three
+    static const int items[][3] = {{1}, {3}, {1, 2, 1}, {2, 2}};
+    for (const auto &tiles : items) {
+        char name[64];
+        snprintf(name, sizeof name, "items of %d, %d, %d tiles", tiles[0], tiles[1], tiles[2]);
+        scenario = name;
+        every_wait(WARPS, RUN_OUT, [&]() {
+            if (self == &fibers[0]) {
+                memset(bars, 0, sizeof *bars);
+                for (int i = 0; i < 3; ++i) set_item(bars, i, tiles[i], parents);
+            }
+            role(p, bars);
+        });
+    }
+    return 0;
+}
+"""
+
+
+@pytest.fixture(scope="module", params=[16, 64])
+def few_rows(request, tmp_path_factory):
+    t = source("la_attn_verify.cu")
+    bars = cut(t, "struct Bars")
+    for entry in ("float neg_m", "float factor", "float top"):
+        assert entry in bars
+        bars = bars.replace(entry, entry.replace("float", "Cell"))
+    role = cut(t, function("softmax_role"))
+    vector = "*reinterpret_cast<const float4 *>(&bars->neg_m[r0 + r])"
+    assert role.count(vector) == 1
+    parts = common() + [constants(t, "kMmaWarp", "kMaxRuns", "kUnseen"), cut(t, "struct Shape"), cut(t, "struct Rec"),
+                        constants(t, "kItems"), bars, cut(t, function("tiles_of")), r"""
+static int named_place(int id) { return threadIdx.x; }
+static int named_count(int id) { return 256; }
+static bool softmax_any(bool x) { return named_any(1, x); }
+static void softmax_sync() { named_any(1, false); }
+""", cut(t, function("build_tree")), role.replace(vector, "load4(&bars->neg_m[r0 + r])"), r"""
+constexpr int RP = %d;
+using Bars_ = Bars<RP>;
+#define WARPS {0, 1, 2, 3, 4, 5, 6, 7}
+#define RUN_OUT {0, 6}
+static uint8_t smem[1 << 18];
+static void set_item(Bars_ *bars, int i, int tiles, const int32_t *) {
+    Rec &r = bars->items[i];
+    r.kv_len = 300;
+    r.j1 = tiles;
+    r.whole = i != 1;
+}
+static void role(const AttnParams &p, Bars_ *bars) {
+    for (int r = lane_of(); r < RP; r += 32) bars->tok_of[r] = (uint8_t)(r / p.group);
+    softmax_role<RP, 1>(p, bars, smem, 0, threadIdx.x >> 5, lane_of(), Waiter());
+}
+""" % request.param, MAIN]
+    return build(tmp_path_factory.mktemp("few"), parts)
+
+
+@pytest.mark.parametrize("rising", [0, 1])
+@pytest.mark.parametrize("tree", [0, 1])
+def test_role_of_few_rows(few_rows, rising, tree):
+    runs(few_rows, "few", rising, tree)
