@@ -74,7 +74,9 @@ struct Bars {
     Rec items[kItems];
     uint8_t parent[kItems][kMaxDrafts];  // of a tree's drafts; kNoParent: the context
     union {
-        float swap[2][2][kRowTile];  // between a row's threads: [row tile][half][row]
+        // Between a row's threads: [row tile][half][row].  Largest scores, then sums; between a thread's read and the other's
+        // next write there is a barrier of the pair.
+        float swap[2][2][kRowTile];
         long long work[kMmaWarp];    // of groups of requests, until the first item is known
     };
     int loads[2];  // of keys and of values, at the end
@@ -339,6 +341,7 @@ __device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, in
         }
         float neg_m = kUnseen;
         float l4[4] = {0.f, 0.f, 0.f, 0.f};
+        int state = 0;  // of the last tile
         for (int j = it.j0; j == it.j0 || j < it.j1; ++j) {
             if (live) {
                 ok = ok && __all_sync(0xffffffffu, wait(&bars->s_full[stage], tile & 1));
@@ -353,7 +356,7 @@ __device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, in
                 // Against the reference that there is; with the item's first tile, and once more where a weight passes 2^8,
                 // against a new one.
                 uint32_t x[2][32];
-                int state = j == it.j0;  // 1: a new reference is to be found, 2: it has been
+                state = j == it.j0;  // 1: a new reference is to be found, 2: it has been
                 while (true) {
                     tmem_ld32(ts, x[0]);
                     tmem_ld32(ts + 32, x[1]);
@@ -475,6 +478,9 @@ __device__ void softmax_role(const AttnParams &p, Bars *bars, uint32_t tbase, in
         if (!live) return;
         done_l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
         done_m = neg_m;
+        // The sums take the entries of the largest scores: where those were exchanged for the last tile, the other thread
+        // has to have read them.  (For an earlier tile, the votes of the tiles behind it say so.)
+        if (state && pair_any(pair, !ok)) return;
         bars->swap[stage][half][row] = done_l;
         if (pair_any(pair, !ok)) return;
         done_l += bars->swap[stage][half ^ 1][row];

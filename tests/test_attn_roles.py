@@ -105,6 +105,46 @@ int main(int argc, char **argv) {
 """
 
 
+@pytest.fixture(scope="module")
+def prompts(tmp_path_factory):
+    t = source("la_attn_extend.cu")
+    bars = cut(t, "struct Bars").replace("float swap", "Cell swap")
+    assert "Cell swap" in bars
+    parts = common() + [constants(t, "kRowTile", "kItemRows", "kSlots", "kMmaWarp", "kItems", "kPieceFloats"),
+                        cut(t, "struct Rec"), constants(t, "kNoParent"), bars, constants(t, "kTmS", "kUnseen")]
+    parts += [cut(t, function(n)) for n in ("columns_seen", "drafts_seen", "mask_scores", "largest", "exponents", "weigh")]
+    parts += [r"""
+static int named_place(int id) { return (threadIdx.x >> 7 & 1) * 32 + lane_of(); }
+static int named_count(int id) { return 64; }
+static bool pair_any(int pair, bool x) { return named_any(pair + 1, x); }
+""", cut(t, function("quad_transpose")), cut(t, function("softmax_role")), r"""
+using Bars_ = Bars;
+#define WARPS {1, 5}
+#define RUN_OUT WARPS
+static void set_item(Bars *bars, int i, int tiles, const int32_t *parents) {
+    Rec &r = bars->items[i];
+    memset(bars->parent[i], kNoParent, kMaxDrafts);
+    for (int t = 0; t < 4; ++t)
+        if (parents[t] >= 0) bars->parent[i][t] = (uint8_t)parents[t];
+    r.n = 4;
+    r.kv_len = 300;
+    r.j1 = tiles;
+    r.whole = i != 1;
+    r.sound = 1;
+}
+static void role(const AttnParams &p0, Bars *bars) {
+    AttnParams p = p0;
+    static const int32_t cu[] = {0, 300};
+    if (!p.parents) p.cu_seqlens = cu;
+    if (p.parents)
+        softmax_role<true>(p, bars, 0, threadIdx.x >> 5, lane_of(), Waiter());
+    else
+        softmax_role<false>(p, bars, 0, threadIdx.x >> 5, lane_of(), Waiter());
+}
+""", MAIN]
+    return build(tmp_path_factory.mktemp("prompts"), parts)
+
+
 @pytest.fixture(scope="module", params=[16, 64])
 def few_rows(request, tmp_path_factory):
     t = source("la_attn_verify.cu")
@@ -139,6 +179,12 @@ static void role(const AttnParams &p, Bars_ *bars) {
 }
 """ % request.param, MAIN]
     return build(tmp_path_factory.mktemp("few"), parts)
+
+
+@pytest.mark.parametrize("rising", [0, 1])
+@pytest.mark.parametrize("tree", [0, 1])
+def test_prompt_role(prompts, rising, tree):
+    runs(prompts, "prompts", rising, tree)
 
 
 @pytest.mark.parametrize("rising", [0, 1])
