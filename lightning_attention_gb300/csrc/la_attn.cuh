@@ -83,7 +83,10 @@ __device__ __forceinline__ void load_tile(const CUtensorMap *map, uint8_t *dst, 
     __syncwarp();
 }
 
-// A bounded wait; the first to give up reports it.
+// A bounded wait; the first to give up reports it.  What a role has under way when it ends (copies into shared memory,
+// MMAs) is waited for with a limit of its own, however short the one on other waits is set: a CTA that left before
+// would have its shared or tensor memory written under the next one.
+constexpr uint64_t kDrainLimitNs = 2000000000ull;
 struct Waiter {
     uint64_t limit_ns;
     unsigned int *err;
@@ -92,6 +95,7 @@ struct Waiter {
         atomicOr(err, ERR_BIT_TIMEOUT);
         return false;
     }
+    __device__ __forceinline__ Waiter to_the_end() const { return {kDrainLimitNs, err}; }
 };
 
 // 2^x, what is below the normal range as 0: one instruction, 4 cycles a warp (without .ftz three, 4.6 to 6.5).

@@ -599,7 +599,7 @@ __device__ void mma_role(const AttnParams &p, Bars *bars, uint8_t *sm, uint32_t 
     // everything issued is complete before tensor memory is freed
     __syncwarp();
     if (elect()) mma_commit(&bars->drain);
-    wait(&bars->drain, 0);
+    wait.to_the_end()(&bars->drain, 0);
 }
 
 // The tiles that a loading warp fills, every other one of the ring: keys and values in turn.
@@ -632,7 +632,7 @@ __device__ void drain_ring(Bars *bars, const Waiter &wait) {
 #pragma unroll 1
             for (int n = max(0, bars->loads[kv] - kSlots); n < bars->loads[kv]; ++n)
                 if ((2 * n + kv) % kSlots == s) last = max(last, 2 * n + kv);
-        if (last >= 0) wait(&bars->full[s], (uint32_t)(last / kSlots) & 1);
+        if (last >= 0) wait.to_the_end()(&bars->full[s], (uint32_t)(last / kSlots) & 1);
     }
 }
 
@@ -730,7 +730,7 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
     Rec none = {};
     publish(none);
     // no copy may be in flight when the CTA exits
-    if (asked > 0) wait(&bars->q_full, (asked - 1) & 1);
+    if (asked > 0) wait.to_the_end()(&bars->q_full, (asked - 1) & 1);
     if (lane == 0) bars->loads[0] = ring.count;
 }
 

@@ -559,7 +559,7 @@ __device__ void mma_role(const AttnParams &p, Bars<RP> *bars, uint8_t *sm, uint3
     }
     __syncwarp();
     if (elect()) mma_commit(&bars->drain);
-    wait(&bars->drain, 0);
+    wait.to_the_end()(&bars->drain, 0);
 }
 
 // The tiles that a loading warp fills, every other one of the ring: keys (kv 0) and values (1).
@@ -630,7 +630,7 @@ __device__ void load_role(const AttnParams &p, const CUtensorMap *tq, const CUte
     publish({});
     // no copy may be in flight when the CTA exits
     for (int x = asked > S::kQBufs ? asked - S::kQBufs : 0; x < asked; ++x)
-        wait(&bars->q_full[x % S::kQBufs], (uint32_t)(x / S::kQBufs) & 1);
+        wait.to_the_end()(&bars->q_full[x % S::kQBufs], (uint32_t)(x / S::kQBufs) & 1);
     if (lane == 0) bars->loads[0] = ring.count;
 }
 
@@ -668,7 +668,7 @@ __device__ void drain_ring(Bars<RP> *bars, const Waiter &wait) {
 #pragma unroll 1
             for (int n = max(0, bars->loads[kv] - n_slots); n < bars->loads[kv]; ++n)
                 if ((2 * n + kv) % n_slots == s) last = max(last, 2 * n + kv);
-        if (last >= 0) wait(&bars->full[s], (uint32_t)(last / n_slots) & 1);
+        if (last >= 0) wait.to_the_end()(&bars->full[s], (uint32_t)(last / n_slots) & 1);
     }
 }
 

@@ -1,6 +1,7 @@
-// What the softmax roles of the attention kernels call, for the host: a fiber per thread, and barriers that count.
+// What the roles of the attention kernels call, for the host: a fiber per thread, and barriers that count.
 // Shared entries that threads exchange are Cells: they know who touched them since which barrier.  A barrier that
-// can never be complete, and accesses of two threads with no barrier between them, end the program with a message.
+// can never be complete, accesses of two threads with no barrier between them, and copies or MMAs that are under way
+// when all roles have ended and that nobody has waited for to the end, end the program with a message.
 #include <math.h>
 #include <stdint.h>
 #include <stdio.h>
@@ -10,6 +11,7 @@
 
 #include <algorithm>
 #include <functional>
+#include <set>
 #include <vector>
 
 #define __device__
@@ -114,6 +116,16 @@ static int __reduce_min_sync(unsigned, int x) {
     for (uint64_t y : lanes((uint64_t)(int64_t)x)) least = min(least, (int)(int64_t)y);
     return least;
 }
+static unsigned __ballot_sync(unsigned, bool x) {
+    const std::vector<uint64_t> &v = lanes(x);
+    unsigned bits = 0;
+    for (int i = 0; i < 32; ++i) bits |= (unsigned)(v[i] != 0) << i;
+    return bits;
+}
+template <class T>
+static T __shfl_up_sync(unsigned, T x, int d) { return lane_value(x, lane_of() < d ? lane_of() : lane_of() - d); }
+static int __clz(unsigned x) { return x ? __builtin_clz(x) : 32; }
+static int __ffs(unsigned x) { return __builtin_ffs((int)x); }
 static void __syncwarp() { lanes(0); }
 static bool elect() { return lane_of() == 0; }
 static unsigned __funnelshift_r(unsigned lo, unsigned hi, int d) {
@@ -154,14 +166,38 @@ static void tc_fence_before() {}
 static void fence_proxy_async_smem() {}
 static void mbar_arrive(uint64_t *) {}
 
-// What a wait is for is there at once, or never comes.
-struct Waiter {
-    bool operator()(uint64_t *, uint32_t) const {
-        const bool out = (int)(threadIdx.x >> 5) == fail_warp && self->waits++ == fail_at;
-        failed |= out;
-        return !out;
+// What a wait is for is there at once, or never comes; copies and MMAs are waited for to the end with a limit that
+// nobody has set (a second and more).
+static std::set<uint64_t *> copies;  // barriers of those under way
+static uint64_t *committed;          // that of the last MMAs
+static bool mmas;
+static bool mbar_wait(uint64_t *bar, uint32_t, uint64_t limit_ns) {
+    if (limit_ns < 1000000000ull && (int)(threadIdx.x >> 5) == fail_warp && self->waits++ == fail_at) {
+        failed = 1;
+        return false;
     }
-};
+    copies.erase(bar);
+    if (bar == committed) mmas = false;
+    return true;
+}
+static void mbar_arrive_expect_tx(uint64_t *bar, uint32_t) { copies.insert(bar); }
+static void mma_commit(uint64_t *bar) { committed = bar; }
+template <class... A>
+static void mma_bf16(A...) { mmas = true; committed = nullptr; }
+template <class... A>
+static void mma_f16_tmem_a(A...) { mmas = true; committed = nullptr; }
+struct CUtensorMap {};
+template <class... A>
+static void tma_load_4d(A...) {}
+template <class... A>
+static void tma_load_5d(A...) {}
+template <class... A>
+static uint32_t idesc_bf16_f32(A...) { return 0; }
+template <class... A>
+static uint64_t sdesc_sw128(A...) { return 0; }
+template <class... A>
+static uint64_t sdesc_sw32(A...) { return 0; }
+static uint32_t smem_u32(const void *) { return 0; }
 
 // Writes of one thread and accesses of another need a barrier between them; lanes of a warp may write the same value.
 struct Cell {
@@ -197,6 +233,8 @@ static void enter() {
 static void run(const std::vector<int> &which, std::function<void()> f) {
     body = f;
     failed = 0;
+    copies.clear();
+    mmas = false;
     for (auto &w : warps) w = Meeting();
     for (auto &b : named) b = Meeting();
     fibers.resize(which.size() * 32);
@@ -221,6 +259,7 @@ static void run(const std::vector<int> &which, std::function<void()> f) {
             self = &x;
             swapcontext(&scheduler, &x.ctx);
         }
+        if (left == 0 && (mmas || !copies.empty())) broken("under way at the end: MMAs, copies", mmas, (int)copies.size());
         if (left == 0) return;
         if (progress == before) broken("threads wait for others that have left", (int)left, (int)fibers.size());
     }
