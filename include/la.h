@@ -481,7 +481,7 @@ la_status la_unpack_states(const int8_t *codes, const uint8_t *scales, int entri
  *   q, out        device, bf16 rows of H * D elements, 16-byte aligned; q rows q_row_stride elements apart (0:
  *                 packed; a multiple of 8, at least H * D; ignored for a single row), out packed
  *   H, Hkv        query heads and kv heads; query head h reads kv head h / (H / Hkv).  H must be a multiple of Hkv
- *                 (LA_ERR_INVALID), H / Hkv at most 128 (LA_ERR_UNSUPPORTED)
+ *                 (LA_ERR_INVALID), at most 65536, H / Hkv at most 128 (LA_ERR_UNSUPPORTED)
  *   scale         factor on the scores q . k, positive, at most 2e38 (LA_ERR_INVALID otherwise); usually D^-0.5
  * Rows of pages behind a request's positions, and pages that no table names, may hold anything.  Requests may share
  * pages that no call writes.  A kv_lens entry that is negative, larger than max_pages * page_size, or smaller than the

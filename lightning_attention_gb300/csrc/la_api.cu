@@ -801,7 +801,7 @@ la_status attn_params(la::AttnParams *p, bool *work, const la_bf16 *q, int64_t q
     if (B < 0 || tokens < 0 || H < 1 || H % Hkv != 0 || !(scale > 0.f) || !isfinite(scale * kLog2e))
         return LA_ERR_INVALID;
     if (tokens > 0x7fffffffLL) return LA_ERR_INVALID;
-    if (H / Hkv > la::kMaxDrafts) return LA_ERR_UNSUPPORTED;
+    if (H > la::kMaxHeads || H / Hkv > la::kMaxDrafts) return LA_ERR_UNSUPPORTED;
     if (!row_stride_ok(&q_rs, tokens, (long long)H * la::kHeadDim)) return LA_ERR_INVALID;
     if (q_rs >= (1ll << 38)) return LA_ERR_UNSUPPORTED;
     if (B == 0 || tokens == 0) return LA_OK;
@@ -934,7 +934,7 @@ la_status la_attn_extend_workspace_size(int B, int T, int H, int Hkv, int D, int
     if (B < 0 || T < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || D < 1 || max_seqlen < 0 || max_kvlen < 0 ||
         bytes == nullptr)
         return LA_ERR_INVALID;
-    if (D != la::kHeadDim || H / Hkv > la::kMaxDrafts) return LA_ERR_UNSUPPORTED;
+    if (D != la::kHeadDim || H > la::kMaxHeads || H / Hkv > la::kMaxDrafts) return LA_ERR_UNSUPPORTED;
     *bytes = (size_t)la::plan_attn_extend(B, T, H, Hkv, max_seqlen, max_kvlen).ws_bytes;
     return LA_OK;
 }
@@ -966,7 +966,8 @@ la_status la_attn_extend(const la_bf16 *q, int64_t q_row_stride, const la_bf16 *
 la_status la_attn_verify_workspace_size(int B, int N, int H, int Hkv, int D, int max_kvlen, size_t *bytes) {
     if (B < 0 || N < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || D < 1 || max_kvlen < 0 || bytes == nullptr)
         return LA_ERR_INVALID;
-    if (D != la::kHeadDim || N > la::kMaxDrafts || H / Hkv > la::kMaxDrafts) return LA_ERR_UNSUPPORTED;
+    if (D != la::kHeadDim || N > la::kMaxDrafts || H > la::kMaxHeads || H / Hkv > la::kMaxDrafts)
+        return LA_ERR_UNSUPPORTED;
     const int rows = N * (H / Hkv);
     *bytes = (size_t)(B == 0                      ? 0
                       : rows <= la::kVerifyRows ? la::attn_verify_ws_bytes(rows, max_kvlen)

@@ -77,5 +77,6 @@ cudaError_t launch_kv_commit(const KvCommitParams &p, cudaStream_t stream);
 constexpr int kAttnCtas = 152;       // SMs of a GB300: what schedules and workspaces go by
 constexpr int kMaxDrafts = 128;      // drafts of a tree, and query heads that share a kv head
 constexpr int kKeyTile = 128;        // keys of a tile
+constexpr int kMaxHeads = 1 << 16;   // query heads: 32 bits hold a place among the rows of a request's drafts
 
 }  // namespace la

@@ -1,0 +1,42 @@
+"""Bounds of the attention entry points, on the host: what a call refuses before anything is launched."""
+import ctypes
+
+import pytest
+
+from lightning_attention_gb300 import _build, binding
+
+OK = ctypes.c_void_p(4096)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return binding.load()
+
+
+def extend(lib, H, Hkv, out=OK):
+    return lib.la_attn_extend(OK, 0, OK, OK, 0, 4, 16, OK, 2, OK, OK, out, 1, 8, H, Hkv, 128, 8, 32, 0.1, OK, 1 << 40, None)
+
+
+def decode(lib, H, Hkv, out=OK):
+    return lib.la_attn_decode(OK, 0, OK, OK, 0, 4, 16, OK, 2, OK, out, 2, H, Hkv, 128, 0.1, OK, 1 << 40, None)
+
+
+def tree(lib, H, Hkv, out=OK):
+    return lib.la_attn_verify_tree(OK, 0, OK, OK, 0, 4, 16, OK, 2, OK, OK, out, 2, 3, H, Hkv, 128, 0.1, OK, 1 << 40, None)
+
+
+@pytest.mark.parametrize("call", [extend, decode, tree])
+def test_number_of_heads(lib, call):
+    """The kernels hold a place among a request's rows, up to 128 * H * 128 / 8 pieces and 64 * H * 128 values, in 32 bits."""
+    for H, Hkv in ((65537, 65537), (1 << 17, 1 << 10), (1 << 24, 1 << 24), ((1 << 31) - 1, (1 << 31) - 1)):
+        assert call(lib, H, Hkv) == 2, (H, Hkv)
+    # the largest number gets as far as its pointers
+    assert call(lib, 65536, 512, out=None) == 1
+
+
+def test_number_of_heads_of_a_workspace(lib):
+    n = ctypes.c_size_t(0)
+    for H, st in ((65536, 0), (65537, 2), (1 << 24, 2)):
+        assert lib.la_attn_verify_workspace_size(2, 1, H, H, 128, 1000, ctypes.byref(n)) == st
+        assert lib.la_attn_extend_workspace_size(2, 9, H, H, 128, 9, 1000, ctypes.byref(n)) == st
