@@ -907,7 +907,8 @@ AttnExtendPlan plan_attn_extend(long long B, long long T, int H, int Hkv, long l
                                 long long max_kvlen) {
     const long long tok = 2 * (kRowTile / (H / Hkv));
     const long long longest = std::min(max_seqlen, T);
-    const long long items = std::min(T / tok + std::min(B, T), B * ((longest + tok - 1) / tok)) * Hkv;
+    // one at least: where no request may have tokens, a CTA still finds and reports those that have
+    const long long items = std::max(std::min(T / tok + std::min(B, T), B * ((longest + tok - 1) / tok)) * Hkv, 1ll);
     const long long pieces = (std::max(max_kvlen, longest) + 2 * kKeyTile - 1) / (2 * kKeyTile);  // of an item
     AttnExtendPlan plan;
     plan.split = pieces > 1;
@@ -919,7 +920,6 @@ AttnExtendPlan plan_attn_extend(long long B, long long T, int H, int Hkv, long l
 
 cudaError_t launch_attn_extend(const AttnParams &p, const AttnExtendPlan &plan, cudaStream_t stream) {
     const int ctas = p.split ? plan.ctas : plan.whole_ctas;
-    if (ctas <= 0) return cudaSuccess;
     CUtensorMap tq, tk, tv;
     if (!make_query_map(&tq, p.q, p.T, p.H, p.q_rs, p.group, kRowTile / p.group) ||
         !make_pages_map(&tk, p.cache.k, p.cache, p.Hkv) || !make_pages_map(&tv, p.cache.v, p.cache, p.Hkv))

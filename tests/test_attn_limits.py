@@ -35,6 +35,14 @@ def test_number_of_heads(lib, call):
     assert call(lib, 65536, 512, out=None) == 1
 
 
+def test_a_bound_of_no_tokens_leaves_a_cta(lib):
+    """It reports the requests that have tokens all the same (and would have a partial result of two items)."""
+    n = ctypes.c_size_t(0)
+    assert lib.la_attn_extend_workspace_size(1, 8, 2, 1, 128, 0, 256, ctypes.byref(n)) == 0 and n.value == 0
+    assert lib.la_attn_extend_workspace_size(1, 8, 2, 1, 128, 0, 300, ctypes.byref(n)) == 0
+    assert n.value == 152 * 56 + 2 * (2 * 256 * 130 * 4)
+
+
 def test_number_of_heads_of_a_workspace(lib):
     n = ctypes.c_size_t(0)
     for H, st in ((65536, 0), (65537, 2), (1 << 24, 2)):
