@@ -616,7 +616,7 @@ la_status la_attn_verify_workspace_size(int B, int N, int H, int Hkv, int D, int
  * new_lens[b] is the length of what is kept, kv_lens[b] - N + (drafts on the path).  Rows behind it are what they
  * happen to be.
  *   accept_idx      device, int32 [B], each in [-1, N-1]
- *   new_lens        device, int32 [B], written; may be kv_lens
+ *   new_lens        device, int32 [B], written but for the requests that are skipped; may be kv_lens
  * The pages of the N drafts' positions must belong to one request.  A request with kv_lens[b] 0 is left alone (new_lens[b]
  * 0).  An index out of range, a parent on the path outside [-1, t-1], a bad page of the path or a length that does
  * not fit skips the request (nothing of it is written) and is reported by la_poll_error.

@@ -941,7 +941,8 @@ def attn_verify_tree(q, k_pages, v_pages, page_table, kv_lens, parents, N: int, 
 def kv_commit(k_pages, v_pages, page_table, kv_lens, parents, accept_idx, new_lens=None):
     """Keep the accepted drafts of a tree (la_kv_commit): the rows of the drafts on the path to accept_idx[b] (-1: none) move
     to the positions behind the context, in place in the pages; returns new_lens int32 [B], the lengths of what is
-    kept (new_lens=kv_lens updates those)."""
+    kept (new_lens=kv_lens updates those and saves a copy).  A request that is skipped for a fault keeps the length that
+    it has in kv_lens, or in the new_lens given."""
     if not isinstance(k_pages, torch.Tensor):
         raise TypeError(f"k_pages must be a bf16 [pages, Hkv, P, {_HEAD_DIM}] tensor")
     dev = k_pages.device
@@ -955,7 +956,7 @@ def kv_commit(k_pages, v_pages, page_table, kv_lens, parents, accept_idx, new_le
     _need_fast(parents, "parents", torch.int32, dev, (B, N))
     _need_fast(accept_idx, "accept_idx", torch.int32, dev, (B,))
     if new_lens is None:
-        new_lens = torch.empty_like(kv_lens)
+        new_lens = kv_lens.clone()  # the call writes nothing for a request that it skips
     else:
         _need_fast(new_lens, "new_lens", torch.int32, dev, (B,))
     with _on(dev):
