@@ -101,8 +101,8 @@ struct Walk {
     Runs runs;
     long long at, lo, hi;  // where the item begins; the run
     bool begun = false;
-    int tail_tiles = 0, tail_b, tail_kvh;  // the item inside which the run ends, if an earlier one does not
-    long long tail_at;
+    int tail_tiles = 0, tail_b = 0, tail_kvh = 0;  // the item inside which the run ends, if an earlier one does not
+    long long tail_at = 0;
     // one warp
     __device__ __forceinline__ Walk(const AttnParams &p, int extra_, const long long (&sums)[kMmaWarp])
         : extra(extra_), runs(0, 1) {

@@ -44,7 +44,8 @@ def function(name):
 def build(tmp_path, parts):
     src, exe = tmp_path / "roles.cc", tmp_path / "roles"
     src.write_text('#include "attn_roles_host.h"\n' + "\n".join(parts))
-    subprocess.run(["g++", "-std=c++17", "-O1", "-w", "-I", HERE, str(src), "-o", str(exe)], check=True)
+    # what nobody has set holds a pattern
+    subprocess.run(["g++", "-std=c++17", "-O1", "-w", "-ftrivial-auto-var-init=pattern", "-I", HERE, str(src), "-o", str(exe)], check=True)
     return str(exe)
 
 
@@ -211,6 +212,8 @@ static void role(const AttnParams &p, Bars_ *bars) {
     if (part == LOADS) {
         if (self == &fibers[0]) bars->work[0] = request_work(p, 0, Shape<RP, 1>::kExtra);
         load_role<RP, 1>(p, nullptr, nullptr, bars, smem, lane_of(), wait);
+        const Tail &t = *static_cast<Tail *>(p.ws);
+        if (t.tiles == 0 && (t.at || t.size || t.b || t.kvh)) broken("a record of no item holds something", t.b, t.kvh);
         drain_ring<RP, 1>(bars, wait);
         return;
     }
