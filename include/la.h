@@ -627,6 +627,15 @@ la_status la_kv_commit(la_bf16 *k_pages, la_bf16 *v_pages, int64_t page_stride, 
                        la_stream stream);
 
 /*
+ * la_kv_commit_ex -- la_kv_commit, with the lengths of the requests that it skips: where keep_lens is nonzero, new_lens[b] of
+ * such a request becomes kv_lens[b], so that new_lens needs to hold nothing before.
+ */
+la_status la_kv_commit_ex(la_bf16 *k_pages, la_bf16 *v_pages, int64_t page_stride, int num_pages, int page_size,
+                          const int32_t *page_table, int max_pages, const int32_t *kv_lens, const int32_t *parents,
+                          const int32_t *accept_idx, int32_t *new_lens, int keep_lens, int B, int N, int Hkv, int D,
+                          la_stream stream);
+
+/*
  * la_poll_error -- synchronise `stream` and then the whole current device (every stream on it),
  * then read and clear the device's error word.  The word is shared by all of the library's
  * kernels on the device, whatever stream they run on, so the device-wide synchronisation makes

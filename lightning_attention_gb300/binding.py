@@ -32,7 +32,7 @@ EXPORTS = ("la_slopes", "la_extend", "la_extend_ex", "la_extend_workspace_size",
            "la_delta_extend_workspace_size", "la_delta_decode",
            "la_delta_verify_chain", "la_pack_states", "la_unpack_states", "la_rope_freqs", "la_rope",
            "la_kv_store", "la_attn_extend", "la_attn_extend_workspace_size", "la_attn_decode",
-           "la_attn_verify_tree", "la_attn_verify_workspace_size", "la_kv_commit")
+           "la_attn_verify_tree", "la_attn_verify_workspace_size", "la_kv_commit", "la_kv_commit_ex")
 
 
 class LAError(RuntimeError):
@@ -125,7 +125,8 @@ def load():
                 ("la_attn_decode", [vp, i64] + cache + [vp, ip, vp, vp, ip, ip, ip, ip, f32, vp, sz, vp]),
                 ("la_attn_verify_tree", [vp, i64] + cache + [vp, ip, vp, vp, vp, ip, ip, ip, ip, ip, f32, vp, sz, vp]),
                 ("la_attn_verify_workspace_size", [ip] * 6 + [ctypes.POINTER(sz)]),
-                ("la_kv_commit", cache + [vp, ip, vp, vp, vp, vp, ip, ip, ip, ip, vp])):
+                ("la_kv_commit", cache + [vp, ip, vp, vp, vp, vp, ip, ip, ip, ip, vp]),
+                ("la_kv_commit_ex", cache + [vp, ip, vp, vp, vp, vp, ip, ip, ip, ip, ip, vp])):
             getattr(lib, name).argtypes = args
             getattr(lib, name).restype = ip
         _lib = lib
@@ -939,9 +940,9 @@ def attn_verify_tree(q, k_pages, v_pages, page_table, kv_lens, parents, N: int, 
 
 
 def kv_commit(k_pages, v_pages, page_table, kv_lens, parents, accept_idx, new_lens=None):
-    """Keep the accepted drafts of a tree (la_kv_commit): the rows of the drafts on the path to accept_idx[b] (-1: none) move
+    """Keep the accepted drafts of a tree (la_kv_commit_ex): the rows of the drafts on the path to accept_idx[b] (-1: none) move
     to the positions behind the context, in place in the pages; returns new_lens int32 [B], the lengths of what is
-    kept (new_lens=kv_lens updates those and saves a copy).  A request that is skipped for a fault keeps the length that
+    kept (new_lens=kv_lens updates those).  A request that is skipped for a fault keeps the length that
     it has in kv_lens, or in the new_lens given."""
     if not isinstance(k_pages, torch.Tensor):
         raise TypeError(f"k_pages must be a bf16 [pages, Hkv, P, {_HEAD_DIM}] tensor")
@@ -955,14 +956,15 @@ def kv_commit(k_pages, v_pages, page_table, kv_lens, parents, accept_idx, new_le
     N = parents.shape[1]
     _need_fast(parents, "parents", torch.int32, dev, (B, N))
     _need_fast(accept_idx, "accept_idx", torch.int32, dev, (B,))
-    if new_lens is None:
-        new_lens = kv_lens.clone()  # the call writes nothing for a request that it skips
+    keep = new_lens is None
+    if keep:
+        new_lens = torch.empty_like(kv_lens)
     else:
         _need_fast(new_lens, "new_lens", torch.int32, dev, (B,))
     with _on(dev):
-        st = (_lib or load()).la_kv_commit(_ptr(k_pages), _ptr(v_pages), stride, E, P, _ptr(page_table), width,
-                                           _ptr(kv_lens), _ptr(parents), _ptr(accept_idx), _ptr(new_lens), B, N, Hkv,
-                                           _HEAD_DIM, _stream_handle(dev))
+        st = (_lib or load()).la_kv_commit_ex(_ptr(k_pages), _ptr(v_pages), stride, E, P, _ptr(page_table), width,
+                                              _ptr(kv_lens), _ptr(parents), _ptr(accept_idx), _ptr(new_lens),
+                                              1 if keep else 0, B, N, Hkv, _HEAD_DIM, _stream_handle(dev))
     if st:
-        _check("la_kv_commit", st)
+        _check("la_kv_commit_ex", st)
     return new_lens

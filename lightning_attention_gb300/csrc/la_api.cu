@@ -996,6 +996,14 @@ la_status la_kv_commit(la_bf16 *k_pages, la_bf16 *v_pages, int64_t page_stride, 
                        const int32_t *page_table, int max_pages, const int32_t *kv_lens, const int32_t *parents,
                        const int32_t *accept_idx, int32_t *new_lens, int B, int N, int Hkv, int D,
                        la_stream stream) {
+    return la_kv_commit_ex(k_pages, v_pages, page_stride, num_pages, page_size, page_table, max_pages, kv_lens, parents,
+                           accept_idx, new_lens, 0, B, N, Hkv, D, stream);
+}
+
+la_status la_kv_commit_ex(la_bf16 *k_pages, la_bf16 *v_pages, int64_t page_stride, int num_pages, int page_size,
+                          const int32_t *page_table, int max_pages, const int32_t *kv_lens, const int32_t *parents,
+                          const int32_t *accept_idx, int32_t *new_lens, int keep_lens, int B, int N, int Hkv, int D,
+                          la_stream stream) {
     la::KvCommitParams p = la::KvCommitParams{};
     la_status st = cache_params(&p.cache, k_pages, v_pages, page_stride, num_pages, page_size, page_table, max_pages,
                                 kv_lens, Hkv, D, true);
@@ -1012,6 +1020,7 @@ la_status la_kv_commit(la_bf16 *k_pages, la_bf16 *v_pages, int64_t page_stride, 
     p.B = B;
     p.N = N;
     p.Hkv = Hkv;
+    p.keep_lens = keep_lens != 0;
     if ((st = error_word_ptr(&p.err)) != LA_OK) return st;
     return launch_status(la::launch_kv_commit(p, static_cast<cudaStream_t>(stream)));
 }

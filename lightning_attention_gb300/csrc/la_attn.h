@@ -71,6 +71,7 @@ struct KvCommitParams {
     int32_t *new_lens;           // [B]
     unsigned int *err;
     int B, N, Hkv;
+    int keep_lens;               // a skipped request's new_lens is its kv_lens; 0: not written
 };
 cudaError_t launch_kv_commit(const KvCommitParams &p, cudaStream_t stream);
 

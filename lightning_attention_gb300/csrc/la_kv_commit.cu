@@ -22,16 +22,21 @@ __global__ void __launch_bounds__(kThreads) kv_commit_kernel(const KvCommitParam
     const CacheParams &c = p.cache;
     const int kv = c.kv_lens[b], last = p.accept_idx[b];
     const bool report = tid == 0;  // writes new_lens, which may be kv_lens, once all threads have read them
+    auto skip = [&](unsigned int fault) {
+        if (!report) return;
+        atomicOr(p.err, fault);
+        if (p.keep_lens) p.new_lens[b] = kv;
+    };
     if (kv == 0) {  // a request without positions; new_lens may hold that already
         if (report) p.new_lens[b] = 0;
         return;
     }
     if (kv < p.N || kv > (long long)c.max_pages * c.page_size) {
-        if (report) atomicOr(p.err, ERR_BIT_PAGE);
+        skip(ERR_BIT_PAGE);
         return;
     }
     if (last < -1 || last >= p.N) {
-        if (report) atomicOr(p.err, ERR_BIT_ACCEPT);
+        skip(ERR_BIT_ACCEPT);
         return;
     }
     if (tid < p.N) parent[tid] = p.parents[(long long)b * p.N + tid];
@@ -52,7 +57,7 @@ __global__ void __launch_bounds__(kThreads) kv_commit_kernel(const KvCommitParam
     __syncthreads();
     const int n = count;
     if (n < 0) {
-        if (report) atomicOr(p.err, ERR_BIT_PARENTS);
+        skip(ERR_BIT_PARENTS);
         return;
     }
     const int ctx = kv - p.N;
@@ -66,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) kv_commit_kernel(const KvCommitParam
         to[tid] = py * c.page_stride + (long long)(y % c.page_size) * kHeadDim;
     }
     if (__syncthreads_or(bad)) {
-        if (report) atomicOr(p.err, ERR_BIT_PAGE);
+        skip(ERR_BIT_PAGE);
         return;
     }
     if (report) p.new_lens[b] = ctx + n;

@@ -48,3 +48,13 @@ def test_number_of_heads_of_a_workspace(lib):
     for H, st in ((65536, 0), (65537, 2), (1 << 24, 2)):
         assert lib.la_attn_verify_workspace_size(2, 1, H, H, 128, 1000, ctypes.byref(n)) == st
         assert lib.la_attn_extend_workspace_size(2, 9, H, H, 128, 9, 1000, ctypes.byref(n)) == st
+
+
+@pytest.mark.parametrize("keep", [0, 1])
+def test_commit_with_options(lib, keep):
+    def commit(kp=OK, lens=OK, B=2, n=3, Hkv=1, D=128, P=16):
+        return lib.la_kv_commit_ex(kp, OK, 0, 4, P, OK, 2, OK, OK, OK, lens, keep, B, n, Hkv, D, None)
+
+    for kw, st in (({"B": -1}, 1), ({"n": 0}, 1), ({"n": 129}, 2), ({"Hkv": 0}, 1), ({"D": 64}, 2), ({"P": 48}, 2),
+                   ({"kp": None}, 1), ({"lens": None}, 1), ({"lens": ctypes.c_void_p(4098)}, 1), ({"B": 0, "lens": None}, 0)):
+        assert commit(**kw) == st, kw

@@ -167,3 +167,22 @@ def test_wide_calls_captured_and_replayed_with_other_lengths(N, H, width):
                 expect(cache, b, hq[r], N, H, attn.tree(parents[b], lens[b]), TOL_BF16, first[r], f"{s}, request {b}")
         graph.replay()
         assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("bad", ["page", "long", "negative", "short", "accept_high", "accept_low", "parent"])
+def test_commit_keeps_the_length_of_a_skipped_request(bad):
+    lens, N = [60, 61, 0], 5
+    cache = Cache(lens, 2, 16, 6)
+    kp, vp, table, kv = cache.to(DEV)
+    parents, accept = i32([[-1, -1, 1, 2, 2]] * 3).to(DEV), i32([4, 4, 4]).to(DEV)
+    if bad == "page":
+        table[1, 3] = -1
+    elif bad == "parent":
+        parents[1, 2] = 2
+    elif bad.startswith("accept"):
+        accept[1] = N if bad == "accept_high" else -2
+    else:
+        kv[1] = {"long": table.shape[1] * 16 + 1, "negative": -1, "short": N - 1}[bad]
+    before = kv.tolist()
+    assert la.kv_commit(kp, vp, table, kv, parents, accept).tolist() == [58, before[1], 0]
+    faulty()
