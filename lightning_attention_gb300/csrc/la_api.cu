@@ -882,7 +882,8 @@ la_status la_rope_freqs(int rot_dim, double base, la_rope_scaling scaling, doubl
         double f = pow(base, -2.0 * i / rot_dim);
         if (scaling == LA_ROPE_LINEAR) f /= factor;
         if (scaling == LA_ROPE_YARN) {
-            const double ramp = std::min(std::max((i - lo) / std::max(hi - lo, 1e-3), 0.0), 1.0);
+            // behind the ramp everything is interpolated, where it ends before pair 0 too
+            const double ramp = i >= hi ? 1.0 : std::max((i - lo) / std::max(hi - lo, 1e-3), 0.0);
             f = f / factor * ramp + f * (1.0 - ramp);
         }
         host_inv_freq[i] = f;

@@ -1,8 +1,10 @@
 """Bounds of the attention entry points, on the host: what a call refuses before anything is launched."""
 import ctypes
 
+import numpy as np
 import pytest
 
+import lightning_attention_gb300 as la
 from lightning_attention_gb300 import _build, binding
 
 OK = ctypes.c_void_p(4096)
@@ -58,3 +60,20 @@ def test_commit_with_options(lib, keep):
     for kw, st in (({"B": -1}, 1), ({"n": 0}, 1), ({"n": 129}, 2), ({"Hkv": 0}, 1), ({"D": 64}, 2), ({"P": 48}, 2),
                    ({"kp": None}, 1), ({"lens": None}, 1), ({"lens": ctypes.c_void_p(4098)}, 1), ({"B": 0, "lens": None}, 0)):
         assert commit(**kw) == st, kw
+
+
+@pytest.mark.parametrize("orig_len", [1, 5, 6, 7, 40, 4096])
+@pytest.mark.parametrize("beta_slow", [1.0, 20.0])
+def test_yarn_keeps_to_its_bounds(orig_len, beta_slow):
+    """Pairs that turn less than beta_slow times over the original length are interpolated in full, and those that turn
+    more than beta_fast times not at all, however short that length (the ramp's ends are whole pair numbers, so that
+    a pair beside an end may be on it)."""
+    R, base, factor, fast = 64, 10000.0, 4.0, 32.0
+    f = base ** (-2 * np.arange(R // 2) / R)
+    g, _ = la.rope_freqs(R, base, "yarn", factor, orig_len, fast, beta_slow)
+    turns, step = orig_len * f / (2 * np.pi), base ** (2 / R)  # from one pair to the next
+    few, many = turns * step < beta_slow, turns > fast * step
+    few[0] = turns[0] < beta_slow  # no pair before it
+    assert np.allclose(g.numpy()[few], f[few] / factor, rtol=1e-14, atol=0)
+    assert np.allclose(g.numpy()[many], f[many], rtol=1e-14, atol=0)
+    assert (g.numpy() <= f * (1 + 1e-15)).all() and (g.numpy() >= f / factor * (1 - 1e-15)).all()
