@@ -479,7 +479,8 @@ la_status la_unpack_states(const int8_t *codes, const uint8_t *scales, int entri
  *   kv_lens       device, int32 [B]: the positions that request b has in the cache, the call's own tokens among
  *                 them as the last ones (la_kv_store put them there before)
  *   q, out        device, bf16 rows of H * D elements, 16-byte aligned; q rows q_row_stride elements apart (0:
- *                 packed; a multiple of 8, at least H * D; ignored for a single row), out packed
+ *                 packed; a multiple of 8, at least H * D; ignored for a single row), out packed; out overlaps nothing
+ *                 that the call reads
  *   H, Hkv        query heads and kv heads; query head h reads kv head h / (H / Hkv).  H must be a multiple of Hkv
  *                 (LA_ERR_INVALID), at most 65536, H / Hkv at most 128 (LA_ERR_UNSUPPORTED)
  *   scale         factor on the scores q . k, positive, at most 2e38 (LA_ERR_INVALID otherwise); usually D^-0.5
@@ -557,10 +558,12 @@ la_status la_kv_store(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, int6
  * of out that belong to no request are left as they were.
  *   max_kvlen       an upper bound on kv_lens that decides the schedule (any value is right; max_pages * page_size if
  *                   nothing better is known)
- *   workspace       device scratch, 16-byte aligned, or NULL.  Where the batch's rows are too few to fill the GPU, the
- *                   keys of a row are shared out among several CTAs and a second launch joins them; that takes
- *                   la_attn_extend_workspace_size() bytes.  With NULL or less the call runs without it (same
- *                   results up to rounding).  Calls that share one must not overlap on the GPU.
+ *   workspace       device scratch, 16-byte aligned, or NULL.  Where a row may see more than 256 keys (max_kvlen, or
+ *                   max_seqlen and T if they are larger), whatever the number of rows, each CTA takes an equal share of the
+ *                   batch's work, and a second launch joins the rows whose keys several of them shared; that takes
+ *                   la_attn_extend_workspace_size() bytes, two partial results a CTA (about 40 MB).  With NULL or less
+ *                   the call runs without it: same results up to rounding, but a CTA keeps each of its tiles of rows to
+ *                   its end, which leaves SMs idle.  Calls that share one must not overlap on the GPU.
  * Numerics: scores, running references and sums in fp32; weights as bf16 for their product with the values
  * (at most 2^-8 of each weight, either way), accumulated in fp32; out is rounded to bf16 once.
  */
@@ -571,7 +574,8 @@ la_status la_attn_extend(const la_bf16 *q, int64_t q_row_stride, const la_bf16 *
                          size_t workspace_bytes, la_stream stream);
 
 /*
- * la_attn_extend_workspace_size -- bytes of scratch la_attn_extend uses for a batch of this shape (0: none).  Host only.
+ * la_attn_extend_workspace_size -- bytes of scratch la_attn_extend uses for a batch of this shape (0: none, where no row sees
+ * more than 256 keys by the bounds given).  Host only.
  */
 la_status la_attn_extend_workspace_size(int B, int T, int H, int Hkv, int D, int max_seqlen, int max_kvlen,
                                         size_t *bytes);
@@ -583,6 +587,8 @@ la_status la_attn_extend_workspace_size(int B, int T, int H, int Hkv, int D, int
  *                   max_kvlen = max_pages * page_size (LA_ERR_INVALID otherwise): the keys are shared out evenly among
  *                   the SMs, and a second launch joins the requests that several of them shared.  Calls that share one
  *                   must not overlap on the GPU.  Short contexts are not shared out and take none (0 bytes, NULL).
+ *                   What a row of the table can hold, max_pages * page_size, not kv_lens, decides: short contexts run
+ *                   faster with a table no wider than they need (1280 positions at most, 256 at most).
  * Numerics: as la_attn_extend, with the weights as bf16 pairs hi + lo (2^-16) where N * H / Hkv, the rows that share a kv
  * head's keys, is at most 64 (N = 1 here), as bf16 above.
  */

@@ -858,7 +858,8 @@ def _scratch(workspace, dev, nbytes: int):
 
 @functools.lru_cache(maxsize=1024)
 def attn_extend_workspace_size(B: int, T: int, H: int, Hkv: int, D: int, max_seqlen: int, max_kvlen: int) -> int:
-    """Bytes of scratch la_attn_extend uses for a batch of this shape: 0 where its rows fill the GPU."""
+    """Bytes of scratch la_attn_extend uses for a batch of this shape: 0 where no row sees more than 256 keys by these
+    bounds."""
     n = ctypes.c_size_t(0)
     _check("la_attn_extend_workspace_size",
            load().la_attn_extend_workspace_size(B, T, H, Hkv, D, max_seqlen, max_kvlen, ctypes.byref(n)))
