@@ -17,7 +17,7 @@
 // page and half of the columns).
 //
 // Long prompts are bound by the tensor cores: 32 MMAs of 64 cycles per item and key tile, 65 measured (16,384 tokens, 32
-// heads on 8: 1300 to 1415 us as the power limit lets the clock go, 1145 with the MMAs alone; floor 1139, or 1279 at the
+// heads on 8: 1300 to 1430 us as the power limit lets the clock go, 1145 with the MMAs alone; floor 1139, or 1279 at the
 // rate that large products sustain).  That leaves a row's threads 1024 cycles from S to P, so they do not look for the
 // row's largest score first: exponents against the reference they have, which follows only when a weight would pass 2^8
 // (S is then read again, and O, which lies in tensor memory, rescaled): sums stay far inside fp32.
