@@ -558,8 +558,8 @@ la_status la_kv_store(const la_bf16 *q, const la_bf16 *k, const la_bf16 *v, int6
  * of out that belong to no request are left as they were.
  *   max_kvlen       an upper bound on kv_lens that decides the schedule (any value is right; max_pages * page_size if
  *                   nothing better is known)
- *   workspace       device scratch, 16-byte aligned, or NULL.  Where a row may see more than 256 keys (max_kvlen, or
- *                   max_seqlen and T if they are larger), whatever the number of rows, each CTA takes an equal share of the
+ *   workspace       device scratch, 16-byte aligned, or NULL.  Where a row may see more than 256 keys (by max_kvlen, or by
+ *                   the smaller of max_seqlen and T), whatever the number of rows, each CTA takes an equal share of the
  *                   batch's work, and a second launch joins the rows whose keys several of them shared; that takes
  *                   la_attn_extend_workspace_size() bytes, two partial results a CTA (about 40 MB).  With NULL or less
  *                   the call runs without it: same results up to rounding, but a CTA keeps each of its tiles of rows to

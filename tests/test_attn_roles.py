@@ -45,7 +45,8 @@ def build(tmp_path, parts):
     src, exe = tmp_path / "roles.cc", tmp_path / "roles"
     src.write_text('#include "attn_roles_host.h"\n' + "\n".join(parts))
     # what nobody has set holds a pattern
-    subprocess.run(["g++", "-std=c++17", "-O1", "-w", "-ftrivial-auto-var-init=pattern", "-I", HERE, str(src), "-o", str(exe)], check=True)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-w", "-ftrivial-auto-var-init=pattern", "-I", HERE, str(src),
+                    "-o", str(exe)], check=True)
     return str(exe)
 
 
